@@ -32,7 +32,9 @@
  *    set a bit in a per-device error word, read with pkv_device_error().
  *
  * Element types: PKV_F16 (IEEE binary16), PKV_BF16 (bfloat16), PKV_E4M3
- * (OCP FP8 E4M3, cache only; per-tensor float32 scales, value = code*scale).
+ * (OCP FP8 E4M3, cache only; value = code*scale with float32 scales, one per
+ * tensor or, in the calls named *_scaled and in paged_rope_append, one for
+ * each (block, kv head): "a block-scaled cache").
  */
 #ifndef PAGEDKV_H
 #define PAGEDKV_H
@@ -60,8 +62,9 @@ enum pkv_device_error_bits {
     PKV_DEV_BAD_BLOCK = 1,       /* decode: block table entry outside [0, num_blocks) */
     PKV_DEV_BAD_CONTEXT_LEN = 2, /* decode: context length outside 1..max_blocks_per_seq*block_size */
     PKV_DEV_BAD_SLOT = 4,        /* append: slot >= num_blocks*block_size */
-    PKV_DEV_BAD_PAIR = 8,        /* block copy: src or dst outside [0, num_blocks) */
-    PKV_DEV_WAIT_TIMEOUT = 16    /* a kernel gave up waiting on an on-chip barrier (about 2 s) */
+    PKV_DEV_BAD_PAIR = 8,        /* block copy or swap: an id outside [0, num_blocks) */
+    PKV_DEV_WAIT_TIMEOUT = 16,   /* a kernel gave up waiting on an on-chip barrier (about 2 s) */
+    PKV_DEV_NO_SPACE = 32        /* extend: the free list or the token buffers cannot hold the step */
 };
 
 /* Partition-size selectors for paged_attention_decode. */
@@ -379,6 +382,136 @@ int paged_attention_decode_sparse(const void* q, const void* k_cache, const void
                                   float scale, void* out, int act_dtype, int cache_dtype,
                                   const float* k_scale, const float* v_scale, int partition_size,
                                   void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A step over a block-scaled E4M3 cache (Ultralytics glossary "PagedAttention",
+ * section "Related techniques": an 8-bit cache).  k_scales and v_scales are
+ * float32 [num_blocks][num_kv_heads] (device): the element of code c in block
+ * b, kv head h stands for c * scales[b][h].  With one scale for each block of
+ * tokens and head, a few large keys cost precision only in their own block.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * paged_extend_tables -- block tables, slots and positions of a step's tokens,
+ * built on the GPU from request lengths: the device counterpart of
+ * pkv_bm_append_slots / pkv_bm_add_sequence for callers whose lengths are on
+ * the device (accepted drafts, captured loops).  Request b has
+ * c = context_lens[b] tokens in the cache and n = new_lens[b] new ones (c, n
+ * >= 0).  It keeps its ceil(c/block_size) blocks and takes
+ * ceil((c+n)/block_size) - ceil(c/block_size) more; the requests take them in
+ * order, logical blocks ascending, from free_blocks[free_head],
+ * free_blocks[free_head + 1], ... -- the order in which the host block manager
+ * pops its free list, so a host manager given the same requests later holds
+ * the same tables.  The last block of a request must not be shared
+ * (copy-on-write is the host manager's part).
+ *  block_tables   int32 [num_seqs][max_blocks_per_seq] (read, and written at
+ *                 the new entries).
+ *  free_blocks    int32 [num_free]; free_head int32 [1]: the first one not yet
+ *                 taken.  Entries from free_head on are available.
+ *  num_tokens     rows of slot_mapping and positions; the step's tokens, all
+ *                 requests' in order, fill the first of them, and the rest get
+ *                 slot -1 and position -1 (padding to the other calls).
+ *  slot_mapping   int64 [num_tokens] (written; 16-byte aligned).
+ *  positions      int32 [num_tokens] (written; 16-byte aligned).
+ *  seq_starts     int32 [num_seqs + 1] (written): first token of each request.
+ *  block_starts   int32 [num_seqs + 1] (written): new blocks before each request.
+ *  context_lens_out int32 [num_seqs] (written): c + n; may be context_lens.
+ *  free_head_out  int32 [1] (written): free_head + blocks taken; may be free_head.
+ * All or nothing, decided on the device: when a length is negative or c + n
+ * passes max_blocks_per_seq*block_size (PKV_DEV_BAD_CONTEXT_LEN), or when the
+ * free list or the token rows are too few (PKV_DEV_NO_SPACE), no block is
+ * taken, tables stay as they were, every slot and position is -1, seq_starts
+ * and block_starts are 0, and lengths and head come out unchanged.  A table or
+ * free-list entry outside [0, num_blocks) flags PKV_DEV_BAD_BLOCK and gives its
+ * tokens slot -1.
+ */
+int paged_extend_tables(int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* new_lens, int num_seqs, int block_size, const int32_t* free_blocks,
+                        int num_free, const int32_t* free_head, int num_blocks, int num_tokens,
+                        int64_t* slot_mapping, int32_t* positions, int32_t* seq_starts, int32_t* block_starts,
+                        int32_t* context_lens_out, int32_t* free_head_out, void* stream);
+
+/*
+ * paged_kv_append_scaled -- paged_kv_append into a block-scaled cache.
+ *  k, v           [num_tokens] rows of [num_kv_heads][head_dim] of act_dtype,
+ *                 k_stride / v_stride elements apart (multiples of 8).
+ * A run is a maximal stretch of consecutive tokens with consecutive slots in
+ * one block.  For each run, kv head, and K and V by itself:
+ *     need = the least power of two 2^e, -64 <= e <= 120, with max|x| <= 448 * 2^e
+ *            over the run's finite elements (2^-64 if all are 0)
+ *     new  = need if the run starts at offset 0 of its block (the block starts
+ *            afresh), else max(scale, need)
+ * The scale becomes new and the run's elements are stored as e4m3(x / new)
+ * (round to nearest even, saturating; NaN stays NaN).  Where new > scale, the
+ * block's other codes become e4m3(code * (scale / new)), so they keep their
+ * values (power-of-two scales: exactly, but for codes that turn subnormal).
+ * A scale that is not positive counts as none: the other codes stay.
+ * Tokens of one block must be neighbours in the call, in slot order; two runs
+ * of one block in one call race.  Negative slots are skipped, slots outside
+ * the pool are skipped and flag PKV_DEV_BAD_SLOT.  head_dim: a multiple of 8,
+ * at most 256; any block_size >= 1.
+ */
+int paged_kv_append_scaled(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int64_t* slot_mapping, int num_tokens, void* k_cache, void* v_cache,
+                           float* k_scales, float* v_scales, int num_blocks, int num_kv_heads, int block_size,
+                           int head_dim, int act_dtype, void* stream);
+
+/*
+ * paged_rope_append -- rotary positions of queries and keys, and the append of
+ * the rotated keys and of the values, in one launch.  Channels e < rotary_dim
+ * of a head form pairs (a, b): (i, i + rotary_dim/2), or (2i, 2i + 1) if
+ * interleaved != 0, i < rotary_dim/2.  At position pos a pair becomes
+ *     (a cos t - b sin t, b cos t + a sin t) * attention_factor,  t = pos * inv_freq[i]
+ * with t taken exactly (64-bit fixed-point turns), the rest in float32; other
+ * channels pass unchanged.  Results are rounded once, to act_dtype or to the
+ * cache's type.
+ *  q, k, v        [num_tokens] rows of [heads][head_dim] of act_dtype, their
+ *                 strides apart (elements, multiples of 8), e.g. the three
+ *                 parts of one projection's output.
+ *  positions      int32 [num_tokens]; a negative one marks a padding row: its
+ *                 q_out row and the cache stay as they are.
+ *  slot_mapping   int64 [num_tokens] as for paged_kv_append (negative: q_out
+ *                 alone is written).
+ *  inv_freq       float32 [rotary_dim/2] (device), finite.
+ *  q_out          [num_tokens] rows of [num_q_heads][head_dim], q_out_stride
+ *                 apart; may be q itself (same stride).  num_q_heads may be 0.
+ *  cache_dtype    act_dtype; or PKV_E4M3 with k_scale and v_scale (one each, as
+ *                 paged_kv_append), or with k_scales and v_scales (block-scaled,
+ *                 as paged_kv_append_scaled).  The other two are NULL.
+ *  head_dim a multiple of 8, at most 256; rotary_dim even, at most head_dim.
+ */
+int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping, int num_tokens,
+                      const float* inv_freq, int rotary_dim, int interleaved, float attention_factor, void* q_out,
+                      int64_t q_out_stride, void* k_cache, void* v_cache, int num_blocks, int num_q_heads,
+                      int num_kv_heads, int block_size, int head_dim, int act_dtype, int cache_dtype,
+                      const float* k_scale, const float* v_scale, float* k_scales, float* v_scales, void* stream);
+
+/*
+ * paged_attention_decode_scaled -- paged_attention_decode over a block-scaled
+ * E4M3 cache: K_b[j] = code * k_scales[block][kvh], likewise V, block =
+ * block_tables[b][j / block_size].  Scales may be any finite float32 (a power of
+ * two or not, 0, negative); products and sums as paged_attention_decode.  A
+ * context length of 0 (a padding row) gives a row of zeros and no error bit.
+ * The workspace is pkv_workspace_size(...); other arguments as there.
+ */
+int paged_attention_decode_scaled(const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+                                  const float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+                                  const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                  int block_size, int head_dim, int num_blocks, float scale, void* out,
+                                  int act_dtype, int partition_size, void* workspace, size_t workspace_bytes,
+                                  void* stream);
+
+/* paged_block_copy of a block-scaled cache: the blocks and their scales. */
+int paged_block_copy_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                            const int32_t* src_dst_pairs, int num_pairs, int num_blocks, int num_kv_heads,
+                            size_t block_bytes, void* stream);
+
+/* The scales of swapped blocks, beside paged_block_swap (same block_ids and
+ * direction): staging float32 [num_ids][2][num_kv_heads], K then V scales, in
+ * pinned host or device memory. */
+int paged_block_scales_swap(float* k_scales, float* v_scales, const int32_t* block_ids, int num_ids,
+                            int num_blocks, int num_kv_heads, float* staging, int direction, void* stream);
 
 /* Message of the last failing call on this host thread ("" if none). */
 const char* pkv_last_error(void);

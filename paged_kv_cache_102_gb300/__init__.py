@@ -10,16 +10,23 @@ library's C++ host code.  There is no CPU fallback: a missing library raises.
     paged_attention_decode_append(q, k_new, v_new, slot_mapping, k_cache, v_cache, ...)
     DecodePlan(...).run()   # either of the two above, marshalled once for fixed buffers
     paged_block_copy(k_cache, v_cache, src_dst_pairs, ...)
+    paged_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_head, ...)
+    paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache, ...)
+    paged_kv_append_scaled(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales)
+    paged_attention_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, ...)
     BlockManager(num_blocks, block_size, free_list=None)
 
 Cache tensors are [num_blocks, num_kv_heads, block_size, head_dim], float16 or
-bfloat16, or uint8 / float8_e4m3fn holding E4M3 codes with float32 per-tensor
-scales (1-element CUDA tensors).
+bfloat16, or uint8 / float8_e4m3fn holding E4M3 codes with float32 scales:
+per tensor (1-element CUDA tensors k_scale, v_scale) or, block-scaled, one for
+each block and kv head (k_scales, v_scales [num_blocks, num_kv_heads]).
 """
 from __future__ import annotations
 
 import ctypes
+import math
 import threading
+from typing import NamedTuple
 
 import numpy as np
 import torch
@@ -33,13 +40,15 @@ PARTITION_AUTO = -1
 
 ERR_INVALID, ERR_SHAPE, ERR_CUDA, ERR_NO_SPACE, ERR_NOT_FOUND = 1, 2, 3, 4, 5
 DEV_BAD_BLOCK, DEV_BAD_CONTEXT_LEN, DEV_BAD_SLOT, DEV_BAD_PAIR, DEV_WAIT_TIMEOUT = 1, 2, 4, 8, 16
+DEV_NO_SPACE = 32
 PATH_AUTO, PATH_CUDA_CORE, PATH_TENSOR, PATH_TENSOR_2CTA = 0, 1, 2, 3
 SWAP_OUT, SWAP_IN = 0, 1
 
 __all__ = ["paged_kv_append", "paged_attention_decode", "paged_attention_decode_append", "DecodePlan",
            "paged_block_copy",
            "paged_block_swap", "paged_attention_decode_sparse", "quest_block_minmax", "quest_append_minmax",
-           "quest_select", "workspace_size",
+           "quest_select", "paged_extend_tables", "ExtendedTables", "rope_inv_freq", "paged_rope_append",
+           "paged_kv_append_scaled", "paged_attention_decode_scaled", "workspace_size",
            "resolve_partition_size", "device_error", "set_kernel_path", "BlockManager", "OutOfBlocks", "PagedKVError",
            "F16", "BF16", "E4M3", "PARTITION_SINGLE", "PARTITION_AUTO", "load"]
 
@@ -230,7 +239,8 @@ class DecodePlan:
     """One decode step for fixed tensors, validated and marshalled once.
 
     With k_new, v_new and slot_mapping it is paged_attention_decode_append,
-    else paged_attention_decode; the arguments mean the same.  run() issues
+    with k_scales and v_scales paged_attention_decode_scaled, else
+    paged_attention_decode; the arguments mean the same.  run() issues
     the step with a single C call and returns `out`.  Between runs the
     tensors' contents may change (new queries, tables, lengths), their
     storage, shapes and types may not.  Every run goes on the stream given
@@ -238,11 +248,17 @@ class DecodePlan:
 
     def __init__(self, q, k_cache, v_cache, block_tables, context_lens, scale, out=None, k_scale=None, v_scale=None,
                  partition_size=PARTITION_AUTO, workspace=None, stream=None, k_new=None, v_new=None,
-                 slot_mapping=None):
+                 slot_mapping=None, k_scales=None, v_scales=None):
         given = [t is not None for t in (k_new, v_new, slot_mapping)]
         if any(given) and not all(given):
             raise ValueError("DecodePlan: k_new, v_new and slot_mapping go together")
-        if all(given):
+        if k_scales is not None or v_scales is not None:
+            if any(given) or k_scale is not None or v_scale is not None:
+                raise ValueError("DecodePlan: k_scales and v_scales go with neither an append nor k_scale, v_scale")
+            self.func = "paged_attention_decode_scaled"
+            self._args, self.out, ws = _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables,
+                                                           context_lens, scale, out, partition_size, workspace, stream)
+        elif all(given):
             self.func = "paged_attention_decode_append"
             self._args, self.out, ws = _decode_append_args(q, k_new, v_new, slot_mapping, k_cache, v_cache,
                                                            block_tables, context_lens, scale, out, k_scale, v_scale,
@@ -253,7 +269,7 @@ class DecodePlan:
                                                     k_scale, v_scale, partition_size, workspace, stream)
         # the plan holds its tensors so that their storage outlives it
         self._tensors = (q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, ws, k_new, v_new,
-                         slot_mapping)
+                         slot_mapping, k_scales, v_scales)
         self._fn = _native.function(self.func)
 
     def run(self):
@@ -335,21 +351,269 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, sel_tables, sel_lens, sca
     return out
 
 
-def paged_block_copy(k_cache, v_cache, src_dst_pairs, stream=None):
-    """Copy whole blocks (K and V) for each (src, dst) row of int32 [P, 2]."""
+def _require_scales(name, k_cache, v_cache, k_scales, v_scales):
+    """Checks of a block-scaled cache: E4M3 codes and float32 scales [num_blocks, num_kv_heads]."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+        raise ValueError(f"{name}: k_cache and v_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
+    if _code(k_cache) != E4M3 or _code(v_cache) != E4M3:
+        raise ValueError(f"{name}: a block-scaled cache holds E4M3 codes (uint8 or float8_e4m3fn)")
+    if k_scales is None or v_scales is None:
+        raise ValueError(f"{name}: k_scales and v_scales go together")
+    want = k_cache.shape[:2]
+    if (k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or k_scales.shape != want
+            or v_scales.shape != want):
+        raise ValueError(f"{name}: k_scales and v_scales must be float32 [num_blocks, num_kv_heads]")
+    _require_cuda(k_cache.device, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales)
+
+
+def _rows(name, what, t, device):
+    """Token stride, in elements, of t [T, heads, head_dim] whose rows are contiguous."""
+    if not t.is_cuda or t.device != device:
+        raise ValueError(f"{name}: {what} must be a CUDA tensor on {device}")
+    T, H, D = t.shape
+    st = t.stride()
+    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+        raise ValueError(f"{name}: {what} must have contiguous rows [heads, head_dim]")
+    return st[0] if T > 1 else H * D
+
+
+class _on:
+    """Makes a tensor's device current for the C call."""
+
+    def __init__(self, device):
+        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
+
+    def __enter__(self):
+        if self._guard is not None:
+            self._guard.__enter__()
+
+    def __exit__(self, *exc):
+        if self._guard is not None:
+            self._guard.__exit__(*exc)
+
+
+class ExtendedTables(NamedTuple):
+    """What paged_extend_tables writes (block_tables is updated in place)."""
+    slot_mapping: torch.Tensor
+    positions: torch.Tensor
+    seq_starts: torch.Tensor
+    block_starts: torch.Tensor
+    context_lens: torch.Tensor
+    free_head: torch.Tensor
+
+
+def paged_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_head, block_size, num_blocks,
+                        num_tokens=None, slot_mapping=None, positions=None, seq_starts=None, block_starts=None,
+                        context_lens_out=None, free_head_out=None, stream=None) -> ExtendedTables:
+    """Blocks, slots and positions of a step's tokens from request lengths, on the GPU.
+
+    block_tables int32 [B, max_blocks] (new entries are written), context_lens and new_lens int32 [B],
+    free_blocks int32 [F] with free_head int32 [1] the first one not taken, num_blocks the pool's size.  num_tokens
+    rows of slots and positions come out, the step's tokens first, -1 behind them (default: the given slot_mapping's
+    rows).  context_lens_out and free_head_out may be context_lens and free_head: a captured step can then be
+    replayed.  All or nothing on the device: a step that does not fit sets DEV_NO_SPACE or DEV_BAD_CONTEXT_LEN
+    and takes nothing."""
+    name = "paged_extend_tables"
+    device = block_tables.device
+    if block_tables.dim() != 2:
+        raise ValueError(f"{name}: block_tables must be [B, max_blocks]")
+    B = block_tables.shape[0]
+    if context_lens.shape != (B,) or new_lens.shape != (B,) or free_blocks.dim() != 1 or free_head.shape != (1,):
+        raise ValueError(f"{name}: context_lens and new_lens [B], free_blocks [F], free_head [1]")
+    if num_tokens is None:
+        if slot_mapping is None:
+            raise ValueError(f"{name}: num_tokens (rows of slots to make) or slot_mapping is needed")
+        num_tokens = slot_mapping.shape[0]
+    i32 = torch.int32
+
+    def output(t, n, dtype, what):
+        if t is None:
+            return torch.empty(n, dtype=dtype, device=device)
+        if t.dtype != dtype or t.shape != (n,):
+            raise ValueError(f"{name}: {what} must be {dtype} [{n}]")
+        return t
+
+    slot_mapping = output(slot_mapping, num_tokens, torch.int64, "slot_mapping")
+    positions = output(positions, num_tokens, i32, "positions")
+    seq_starts = output(seq_starts, B + 1, i32, "seq_starts")
+    block_starts = output(block_starts, B + 1, i32, "block_starts")
+    lens_out = output(context_lens_out, B, i32, "context_lens_out")
+    head_out = output(free_head_out, 1, i32, "free_head_out")
+    for what, t in (("block_tables", block_tables), ("context_lens", context_lens), ("new_lens", new_lens),
+                    ("free_blocks", free_blocks), ("free_head", free_head)):
+        if t.dtype != i32:
+            raise ValueError(f"{name}: {what} must be int32")
+    _require_cuda(device, block_tables=block_tables, context_lens=context_lens, new_lens=new_lens,
+                  free_blocks=free_blocks, free_head=free_head, slot_mapping=slot_mapping, positions=positions,
+                  seq_starts=seq_starts, block_starts=block_starts, context_lens_out=lens_out, free_head_out=head_out)
+    with _on(device):
+        _native.call(name, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), _ptr(new_lens), B,
+                     int(block_size), _ptr(free_blocks), free_blocks.shape[0], _ptr(free_head), int(num_blocks),
+                     num_tokens, _ptr(slot_mapping), _ptr(positions), _ptr(seq_starts), _ptr(block_starts),
+                     _ptr(lens_out), _ptr(head_out), _stream(stream, device))
+    return ExtendedTables(slot_mapping, positions, seq_starts, block_starts, lens_out, head_out)
+
+
+def rope_inv_freq(rotary_dim, base=10000.0, scaling=None, factor=1.0, original_context=None, slow_turns=1.0,
+                  fast_turns=32.0, device="cuda"):
+    """Inverse frequencies float32 [rotary_dim / 2] for paged_rope_append, and the attention factor to pass with them.
+
+    scaling stretches a model trained on original_context tokens to factor times as many:
+      None      base ** (-2i / rotary_dim)
+      "linear"  every frequency divided by factor (positions interpolated)
+      "ntk"     the base raised so that the slowest pair is divided by factor and the fastest is kept
+      "yarn"    pairs that turn fewer than slow_turns times over original_context are divided by factor, those that
+                turn more than fast_turns times are kept, a linear ramp (over the turns' logarithm, that is over the
+                pair's index) between; attention factor 0.1 ln(factor) + 1
+      "smooth"  the same bands with a ramp linear in the turns; attention factor 1"""
+    if rotary_dim <= 0 or rotary_dim % 2:
+        raise ValueError("rope_inv_freq: rotary_dim must be even and positive")
+    if scaling not in (None, "linear", "ntk", "yarn", "smooth"):
+        raise ValueError(f"rope_inv_freq: unknown scaling {scaling!r}")
+    if not (factor >= 1.0 and math.isfinite(factor) and base > 1.0 and math.isfinite(base)):
+        raise ValueError("rope_inv_freq: factor must be at least 1 and base above 1")
+    half = rotary_dim // 2
+    if scaling == "ntk" and rotary_dim > 2:
+        base = base * factor ** (rotary_dim / (rotary_dim - 2))
+    f = base ** (-np.arange(half, dtype=np.float64) * 2.0 / rotary_dim)
+    attention = 1.0
+    if scaling == "linear":
+        f = f / factor
+    elif scaling in ("yarn", "smooth"):
+        if not original_context or not 0 < slow_turns < fast_turns:
+            raise ValueError(f"rope_inv_freq: {scaling!r} needs original_context and 0 < slow_turns < fast_turns")
+        turns = original_context * f / (2.0 * math.pi)
+        if scaling == "yarn":
+            ramp = np.log(turns / slow_turns) / math.log(fast_turns / slow_turns)
+            attention = 0.1 * math.log(factor) + 1.0
+        else:
+            ramp = (turns - slow_turns) / (fast_turns - slow_turns)
+        keep = np.clip(ramp, 0.0, 1.0)
+        f = f * keep + f / factor * (1.0 - keep)
+    return torch.from_numpy(f.astype(np.float32)).to(device), attention
+
+
+def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache, interleaved=False,
+                      attention_factor=1.0, q_out=None, k_scale=None, v_scale=None, k_scales=None, v_scales=None,
+                      stream=None):
+    """Rotate q [T, Hq, D] and k [T, Hkv, D] at positions int32 [T] and append the rotated keys and the values at
+    slot_mapping int64 [T], in one launch; returns the rotated queries (q_out, new by default, may be q).
+
+    The first 2 * len(inv_freq) channels turn, paired (i, i + half) or interleaved (2i, 2i + 1).  q, k, v may be
+    parts of one projection's output (rows contiguous, token strides of their own).  The cache is of q's type, or
+    E4M3 with k_scale, v_scale (one each) or k_scales, v_scales (block-scaled).  A negative position marks a padding
+    row, a negative slot a token that is not stored.  q may be None (keys alone)."""
+    name = "paged_rope_append"
+    T, Hkv, D = k.shape
+    device = k.device
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v.shape != k.shape:
+        raise ValueError(f"{name}: shape mismatch")
+    NB, Hkv2, bs, D2 = k_cache.shape
+    if Hkv2 != Hkv or D2 != D:
+        raise ValueError(f"{name}: shape mismatch")
+    if positions.dtype != torch.int32 or positions.shape != (T,):
+        raise ValueError(f"{name}: positions must be int32 [num_tokens]")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError(f"{name}: slot_mapping must be int64 [num_tokens]")
+    if inv_freq.dtype != torch.float32 or inv_freq.dim() != 1:
+        raise ValueError(f"{name}: inv_freq must be float32 [rotary_dim / 2]")
+    if v.dtype != k.dtype or v_cache.dtype != k_cache.dtype:
+        raise ValueError(f"{name}: k and v, and the two caches, must have one type")
+    if k_scales is not None or v_scales is not None:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError(f"{name}: k_scale, v_scale or k_scales, v_scales, not both")
+        _require_scales(name, k_cache, v_cache, k_scales, v_scales)
+    Hq = qs = os = 0
+    if q is not None:
+        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
+            raise ValueError(f"{name}: q must be [num_tokens, num_q_heads, head_dim] of k's type")
+        Hq = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
+        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+            raise ValueError(f"{name}: q_out must match q")
+        qs, os = _rows(name, "q", q, device), _rows(name, "q_out", q_out, device)
+    elif q_out is not None:
+        raise ValueError(f"{name}: q_out without q")
+    ks, vs = _rows(name, "k", k, device), _rows(name, "v", v, device)
+    _require_cuda(device, positions=positions, slot_mapping=slot_mapping, inv_freq=inv_freq, k_cache=k_cache,
+                  v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
+    with _on(device):
+        _native.call(name, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions), _ptr(slot_mapping), T,
+                     _ptr(inv_freq), 2 * inv_freq.shape[0], int(bool(interleaved)), float(attention_factor),
+                     _ptr(q_out), os, _ptr(k_cache), _ptr(v_cache), NB, Hq, Hkv, bs, D, _code(k), _code(k_cache),
+                     _ptr(k_scale), _ptr(v_scale), _ptr(k_scales), _ptr(v_scales), _stream(stream, device))
+    return q_out
+
+
+def paged_kv_append_scaled(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales, stream=None):
+    """Quantise k, v [T, Hkv, D] into their slots (int64 [T], negative = skip) of a block-scaled E4M3 cache.
+
+    The scale of a (block, kv head) is the least power of two that holds its largest element; a later token that
+    needs a larger one moves the block's codes along.  A token at offset 0 starts its block afresh.  Tokens of one
+    block must be neighbours in the call, in slot order."""
+    name = "paged_kv_append_scaled"
+    T, Hkv, D = k.shape
+    device = k_cache.device
+    _require_scales(name, k_cache, v_cache, k_scales, v_scales)
+    NB, Hkv2, bs, D2 = k_cache.shape
+    if v.shape != k.shape or v.dtype != k.dtype or Hkv2 != Hkv or D2 != D:
+        raise ValueError(f"{name}: shape or type mismatch")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
+        raise ValueError(f"{name}: slot_mapping must be int64 [num_tokens]")
+    ks, vs = _rows(name, "k", k, device), _rows(name, "v", v, device)
+    _require_cuda(device, slot_mapping=slot_mapping)
+    with _on(device):
+        _native.call(name, _ptr(k), ks, _ptr(v), vs, _ptr(slot_mapping), T, _ptr(k_cache), _ptr(v_cache),
+                     _ptr(k_scales), _ptr(v_scales), NB, Hkv, bs, D, _code(k), _stream(stream, device))
+
+
+def paged_attention_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out=None,
+                                  partition_size=PARTITION_AUTO, workspace=None, stream=None):
+    """Decode attention for q [B, Hq, D] over a block-scaled E4M3 cache; returns out [B, Hq, D].  A context length
+    of 0 (a padding row) gives zeros."""
+    args, out, _ = _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
+                                       partition_size, workspace, stream)
+    with _on(q.device):
+        _native.call("paged_attention_decode_scaled", *args)
+    return out
+
+
+def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
+                        partition_size, workspace, stream):
+    """Validated C arguments of paged_attention_decode_scaled, the output and the workspace."""
+    _require_scales("paged_attention_decode_scaled", k_cache, v_cache, k_scales, v_scales)
+    a, out, workspace = _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_scales, v_scales,
+                                     partition_size, workspace, stream)
+    # (q, k_cache, v_cache | tables .. scale, out, act | cache_dtype, k_scale, v_scale dropped | partition ..)
+    return (*a[:3], a[16], a[17], *a[3:15], *a[18:]), out, workspace
+
+
+def paged_block_copy(k_cache, v_cache, src_dst_pairs, stream=None, k_scales=None, v_scales=None):
+    """Copy whole blocks (K and V) for each (src, dst) row of int32 [P, 2], with their scales for a block-scaled
+    cache (k_scales, v_scales float32 [num_blocks, num_kv_heads])."""
     if src_dst_pairs.dtype != torch.int32 or src_dst_pairs.dim() != 2 or src_dst_pairs.shape[1] != 2:
         raise ValueError("paged_block_copy: src_dst_pairs must be int32 [P, 2]")
     if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
         raise ValueError("paged_block_copy: k_cache and v_cache must match")
     _require_cuda(k_cache.device, k_cache=k_cache, v_cache=v_cache, src_dst_pairs=src_dst_pairs)
     block_bytes = k_cache[0].numel() * k_cache.element_size()
+    if k_scales is not None or v_scales is not None:
+        _require_scales("paged_block_copy", k_cache, v_cache, k_scales, v_scales)
+        _native.call("paged_block_copy_scaled", _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+                     _ptr(src_dst_pairs), src_dst_pairs.shape[0], k_cache.shape[0], k_cache.shape[1], block_bytes,
+                     _stream(stream, k_cache.device))
+        return
     _native.call("paged_block_copy", _ptr(k_cache), _ptr(v_cache), _ptr(src_dst_pairs), src_dst_pairs.shape[0],
                  k_cache.shape[0], block_bytes, _stream(stream, k_cache.device))
 
 
-def paged_block_swap(k_cache, v_cache, block_ids, staging, direction, stream=None):
+def paged_block_swap(k_cache, v_cache, block_ids, staging, direction, stream=None, k_scales=None, v_scales=None,
+                     scale_staging=None):
     """Copy whole blocks between the pools and staging [n, 2, block_bytes] (uint8,
-    pinned host or device).  direction: SWAP_OUT (pools -> staging) or SWAP_IN."""
+    pinned host or device).  direction: SWAP_OUT (pools -> staging) or SWAP_IN.
+    A block-scaled cache moves its scales along, between k_scales, v_scales and
+    scale_staging (float32 [n, 2, num_kv_heads], pinned host or device)."""
     if block_ids.dtype != torch.int32 or block_ids.dim() != 1:
         raise ValueError("paged_block_swap: block_ids must be int32 [n]")
     if v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
@@ -360,8 +624,19 @@ def paged_block_swap(k_cache, v_cache, block_ids, staging, direction, stream=Non
         raise ValueError("paged_block_swap: staging must be contiguous with room for [n, 2, block_bytes]")
     if not staging.is_cuda and not staging.is_pinned():
         raise ValueError("paged_block_swap: host staging must be pinned memory")
+    if k_scales is not None or v_scales is not None or scale_staging is not None:
+        _require_scales("paged_block_swap", k_cache, v_cache, k_scales, v_scales)
+        if (scale_staging is None or scale_staging.dtype != torch.float32 or not scale_staging.is_contiguous()
+                or scale_staging.numel() < block_ids.numel() * 2 * k_cache.shape[1]):
+            raise ValueError("paged_block_swap: scale_staging must be contiguous float32 [n, 2, num_kv_heads]")
+        if not scale_staging.is_cuda and not scale_staging.is_pinned():
+            raise ValueError("paged_block_swap: host scale_staging must be pinned memory")
     _native.call("paged_block_swap", _ptr(k_cache), _ptr(v_cache), _ptr(block_ids), block_ids.numel(),
                  k_cache.shape[0], block_bytes, _ptr(staging), int(direction), _stream(stream, k_cache.device))
+    if k_scales is not None:
+        _native.call("paged_block_scales_swap", _ptr(k_scales), _ptr(v_scales), _ptr(block_ids), block_ids.numel(),
+                     k_cache.shape[0], k_cache.shape[1], _ptr(scale_staging), int(direction),
+                     _stream(stream, k_cache.device))
 
 
 def device_error(reset: bool = True, stream=None, device=None) -> int:

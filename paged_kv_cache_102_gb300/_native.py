@@ -40,6 +40,14 @@ SIGNATURES = {
     "pkv_resolve_partition_size": (I32, [I32, I32, I32, I32, I32, I32, I32]),
     "paged_block_copy": (I32, [P, P, P, I32, I32, SZ, P]),
     "paged_block_swap": (I32, [P, P, P, I32, I32, SZ, P, I32, P]),
+    "paged_extend_tables": (I32, [P, I32, P, P, I32, I32, P, I32, P, I32, I32, P, P, P, P, P, P, P]),
+    "paged_kv_append_scaled": (I32, [P, I64, P, I64, P, I32, P, P, P, P, I32, I32, I32, I32, I32, P]),
+    "paged_rope_append": (I32, [P, I64, P, I64, P, I64, P, P, I32, P, I32, I32, F32, P, I64, P, P, I32, I32, I32,
+                                I32, I32, I32, I32, P, P, P, P, P]),
+    "paged_attention_decode_scaled": (I32, [P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, F32, P, I32, I32,
+                                            P, SZ, P]),
+    "paged_block_copy_scaled": (I32, [P, P, P, P, P, I32, I32, I32, SZ, P]),
+    "paged_block_scales_swap": (I32, [P, P, P, I32, I32, I32, P, I32, P]),
     "pkv_last_error": (ctypes.c_char_p, []),
     "pkv_device_error": (I32, [P, I32, P]),
     "pkv_version": (I32, []),

@@ -184,7 +184,7 @@ int paged_block_copy(void* k_cache, void* v_cache, const int32_t* src_dst_pairs,
         return fail(PKV_ERR_INVALID, "paged_block_copy: caches must be 16-byte aligned");
     int* err = device_error_word();
     if (!err) return fail(PKV_ERR_CUDA, "paged_block_copy: cannot resolve the device error word");
-    CopyParams p{k_cache, v_cache, src_dst_pairs, err, block_bytes, num_blocks};
+    CopyParams p{k_cache, v_cache, src_dst_pairs, err, block_bytes, num_blocks, nullptr, nullptr, 0};
     cudaError_t e = launch_block_copy(p, num_pairs, static_cast<cudaStream_t>(stream));
     if (e != cudaSuccess) return cuda_fail("paged_block_copy: launch", e);
     return PKV_OK;
@@ -222,7 +222,8 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
                        int num_q_heads, int num_kv_heads, int block_size, int head_dim, int num_blocks, float scale,
                        void* out, int act_dtype, int cache_dtype, const float* k_scale, const float* v_scale,
                        int partition_size, void* workspace, size_t workspace_bytes, void* stream, const void* k_new,
-                       const void* v_new, const int64_t* new_slots, bool per_kvh_tables = false) {
+                       const void* v_new, const int64_t* new_slots, bool per_kvh_tables = false,
+                       bool block_scales = false) {
     const std::string F(fn);
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
         return fail(PKV_ERR_INVALID, F + ": " + "sizes must be positive");
@@ -244,7 +245,10 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !out)
         return fail(PKV_ERR_INVALID, F + ": " + "null pointer");
     if (cache_dtype == PKV_E4M3 && (!k_scale || !v_scale))
-        return fail(PKV_ERR_INVALID, F + ": " + "an E4M3 cache needs k_scale and v_scale");
+        return fail(PKV_ERR_INVALID, F + ": " + (block_scales ? "the cache needs k_scales and v_scales"
+                                                              : "an E4M3 cache needs k_scale and v_scale"));
+    if (block_scales && (!aligned(k_scale, 4) || !aligned(v_scale, 4)))
+        return fail(PKV_ERR_INVALID, F + ": " + "k_scales and v_scales must be 4-byte aligned");
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
         !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(workspace, 16))
         return fail(PKV_ERR_INVALID, F + ": " + "q, caches, out, workspace must be 16-byte aligned");
@@ -304,6 +308,8 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         p.lens_kvh_stride = 0;
     }
 
+    // the kernels' cache kind: E4M3 codes with one scale, or one per (block, kv head)
+    const int kind = block_scales ? kCacheE4M3Blocks : cache_dtype;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e;
     const int path = g_kernel_path.load();
@@ -311,7 +317,7 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     // batches run as several launches over consecutive sequences
     const int rows_per_seq = per_kvh_tables ? num_kv_heads : 1;
     const bool tc_ok = rows_per_seq <= decode_tc_max_rows() &&
-                       decode_tc_supported(head_dim, block_size, G, act_dtype, cache_dtype, P, num_kv_heads,
+                       decode_tc_supported(head_dim, block_size, G, act_dtype, kind, P, num_kv_heads,
                                            per_kvh_tables);
     if ((path == PKV_PATH_TENSOR || path == PKV_PATH_TENSOR_2CTA) && !tc_ok)
         return fail(PKV_ERR_INVALID, F + ": " + "the tensor-core path needs head_dim 128 (16-bit or E4M3 "
@@ -340,10 +346,13 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
                 c.ws_ml = p.ws_ml + hrow0 * 2;
                 c.ws_o = p.ws_o + hrow0 * head_dim;
             }
-            e = launch_decode_tc(c, act_dtype, cache_dtype, head_dim, block_size, G, path == PKV_PATH_TENSOR ? 0 : 1,
+            e = launch_decode_tc(c, act_dtype, kind, head_dim, block_size, G, path == PKV_PATH_TENSOR ? 0 : 1,
                                  s);
         }
-    } else if (act_dtype == PKV_F16)
+    } else if (block_scales)
+        e = act_dtype == PKV_F16 ? launch_decode_f16_e4m3b(p, head_dim, block_size, G, s)
+                                 : launch_decode_bf16_e4m3b(p, head_dim, block_size, G, s);
+    else if (act_dtype == PKV_F16)
         e = cache_dtype == PKV_E4M3 ? launch_decode_f16_e4m3(p, head_dim, block_size, G, s)
                                     : launch_decode_f16_f16(p, head_dim, block_size, G, s);
     else
@@ -411,6 +420,211 @@ int paged_attention_decode_sparse(const void* q, const void* k_cache, const void
                        num_seqs, num_q_heads, num_kv_heads, block_size, head_dim, num_blocks, scale, out, act_dtype,
                        cache_dtype, k_scale, v_scale, partition_size, workspace, workspace_bytes, stream, nullptr,
                        nullptr, nullptr, true);
+}
+
+int paged_attention_decode_scaled(const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+                                  const float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
+                                  const int32_t* context_lens, int num_seqs, int num_q_heads, int num_kv_heads,
+                                  int block_size, int head_dim, int num_blocks, float scale, void* out, int act_dtype,
+                                  int partition_size, void* workspace, size_t workspace_bytes, void* stream) {
+    return decode_impl("paged_attention_decode_scaled", q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                       context_lens, num_seqs, num_q_heads, num_kv_heads, block_size, head_dim, num_blocks, scale, out,
+                       act_dtype, PKV_E4M3, k_scales, v_scales, partition_size, workspace, workspace_bytes, stream,
+                       nullptr, nullptr, nullptr, false, true);
+}
+
+int paged_extend_tables(int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                        const int32_t* new_lens, int num_seqs, int block_size, const int32_t* free_blocks, int num_free,
+                        const int32_t* free_head, int num_blocks, int num_tokens, int64_t* slot_mapping,
+                        int32_t* positions, int32_t* seq_starts, int32_t* block_starts, int32_t* context_lens_out,
+                        int32_t* free_head_out, void* stream) {
+    const std::string F("paged_extend_tables: ");
+    if (num_seqs < 0 || max_blocks_per_seq <= 0 || block_size <= 0 || num_free < 0 || num_blocks <= 0 || num_tokens < 0)
+        return fail(PKV_ERR_INVALID, F + "sizes must be positive (num_seqs, num_free and num_tokens may be 0)");
+    if (static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
+        return fail(PKV_ERR_INVALID, F + "table too long");
+    if (num_tokens > 0x7fffffff - 4) return fail(PKV_ERR_INVALID, F + "too many tokens");
+    if (num_seqs == 0 && num_tokens == 0) return PKV_OK;
+    if (!free_head || !seq_starts || !block_starts || !free_head_out)
+        return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (num_seqs > 0 && (!block_tables || !context_lens || !new_lens || !context_lens_out))
+        return fail(PKV_ERR_INVALID, F + "null pointer");
+    if ((num_free > 0 && !free_blocks) || (num_tokens > 0 && (!slot_mapping || !positions)))
+        return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (!aligned(slot_mapping, 16) || !aligned(positions, 16))
+        return fail(PKV_ERR_INVALID, F + "slot_mapping and positions must be 16-byte aligned");
+    if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(new_lens, 4) || !aligned(free_blocks, 4) ||
+        !aligned(free_head, 4) || !aligned(seq_starts, 4) || !aligned(block_starts, 4) ||
+        !aligned(context_lens_out, 4) || !aligned(free_head_out, 4))
+        return fail(PKV_ERR_INVALID, F + "int32 buffers must be 4-byte aligned");
+    if ((num_seqs > 0 && context_lens_out == new_lens) || free_head_out == seq_starts || free_head_out == block_starts ||
+        seq_starts == block_starts)
+        return fail(PKV_ERR_INVALID, F + "outputs must be buffers of their own (context_lens_out may be context_lens, "
+                                         "free_head_out may be free_head)");
+    int* err = device_error_word();
+    if (!err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
+    ExtendParams p{block_tables, context_lens, new_lens, free_blocks, free_head, slot_mapping, positions, seq_starts,
+                   block_starts, context_lens_out, free_head_out, err, num_seqs, max_blocks_per_seq, block_size,
+                   num_free, num_blocks, num_tokens};
+    const cudaError_t e = launch_extend_tables(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail("paged_extend_tables: launch", e);
+}
+
+// Checks shared by the strided appends; returns PKV_OK or the status to return.
+static int append_checks(const std::string& F, const RopeAppendParams& p, int act_dtype) {
+    if (p.num_tokens < 0 || p.num_kv_heads <= 0 || p.block_size <= 0 || p.num_blocks <= 0 || p.head_dim <= 0 ||
+        p.head_dim % 8 != 0 || p.head_dim > 256)
+        return fail(PKV_ERR_INVALID, F + "sizes must be positive and head_dim a multiple of 8 up to 256");
+    if (act_dtype != PKV_F16 && act_dtype != PKV_BF16)
+        return fail(PKV_ERR_INVALID, F + "act_dtype must be PKV_F16 or PKV_BF16");
+    if (p.k_stride % 8 != 0 || p.v_stride % 8 != 0 || p.k_stride < 0 || p.v_stride < 0)
+        return fail(PKV_ERR_INVALID, F + "token strides must be multiples of 8 elements and not negative");
+    return PKV_OK;
+}
+
+int paged_kv_append_scaled(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                           const int64_t* slot_mapping, int num_tokens, void* k_cache, void* v_cache, float* k_scales,
+                           float* v_scales, int num_blocks, int num_kv_heads, int block_size, int head_dim,
+                           int act_dtype, void* stream) {
+    const std::string F("paged_kv_append_scaled: ");
+    RopeAppendParams p{};
+    p.k = k;
+    p.v = v;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.slot_mapping = slot_mapping;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.num_tokens = num_tokens;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    const int c = append_checks(F, p, act_dtype);
+    if (c != PKV_OK) return c;
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !slot_mapping || !k_cache || !v_cache || !k_scales || !v_scales)
+        return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(slot_mapping, 8) || !aligned(k_scales, 4) || !aligned(v_scales, 4))
+        return fail(PKV_ERR_INVALID, F + "buffers must be 16-byte aligned (slot_mapping 8, scales 4)");
+    p.err = device_error_word();
+    if (!p.err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
+    const cudaError_t e = launch_rope_append(p, act_dtype, kCacheE4M3Blocks, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail("paged_kv_append_scaled: launch", e);
+}
+
+int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                      int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping, int num_tokens,
+                      const float* inv_freq, int rotary_dim, int interleaved, float attention_factor, void* q_out,
+                      int64_t q_out_stride, void* k_cache, void* v_cache, int num_blocks, int num_q_heads,
+                      int num_kv_heads, int block_size, int head_dim, int act_dtype, int cache_dtype,
+                      const float* k_scale, const float* v_scale, float* k_scales, float* v_scales, void* stream) {
+    const std::string F("paged_rope_append: ");
+    RopeAppendParams p{};
+    p.q = q;
+    p.k = k;
+    p.v = v;
+    p.q_stride = q_stride;
+    p.k_stride = k_stride;
+    p.v_stride = v_stride;
+    p.positions = positions;
+    p.slot_mapping = slot_mapping;
+    p.inv_freq = inv_freq;
+    p.q_out = q_out;
+    p.q_out_stride = q_out_stride;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.k_scale = k_scale;
+    p.v_scale = v_scale;
+    p.k_scales = k_scales;
+    p.v_scales = v_scales;
+    p.factor = attention_factor;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.head_dim = head_dim;
+    p.rotary_dim = rotary_dim;
+    p.interleaved = interleaved ? 1 : 0;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    const int c = append_checks(F, p, act_dtype);
+    if (c != PKV_OK) return c;
+    if (num_q_heads < 0 || num_q_heads > 65535 || num_kv_heads > 65535)
+        return fail(PKV_ERR_INVALID, F + "head counts must be in 0 .. 65535 (kv heads from 1)");
+    if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_dim > head_dim)
+        return fail(PKV_ERR_INVALID, F + "rotary_dim must be even, positive and at most head_dim");
+    if (!std::isfinite(attention_factor)) return fail(PKV_ERR_INVALID, F + "attention_factor must be finite");
+    if (cache_dtype != act_dtype && cache_dtype != PKV_E4M3)
+        return fail(PKV_ERR_INVALID, F + "cache_dtype must equal act_dtype or be PKV_E4M3");
+    if (num_q_heads > 0 && (q_stride % 8 != 0 || q_stride < 0 || q_out_stride % 8 != 0 ||
+                            (num_tokens > 1 && q_out_stride < static_cast<int64_t>(num_q_heads) * head_dim)))
+        return fail(PKV_ERR_INVALID, F + "q token strides must be multiples of 8 elements, and q_out's rows apart");
+    const bool blocks = k_scales || v_scales;
+    if (cache_dtype == PKV_E4M3 && blocks == (k_scale || v_scale))
+        return fail(PKV_ERR_INVALID, F + "an E4M3 cache needs either k_scale and v_scale or k_scales and v_scales");
+    if (cache_dtype == PKV_E4M3 && (blocks ? (!k_scales || !v_scales) : (!k_scale || !v_scale)))
+        return fail(PKV_ERR_INVALID, F + "an E4M3 cache needs scales for both K and V");
+    if (num_tokens == 0) return PKV_OK;
+    if (!k || !v || !positions || !slot_mapping || !inv_freq || !k_cache || !v_cache ||
+        (num_q_heads > 0 && (!q || !q_out)))
+        return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
+        !aligned(v_cache, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(k_scales, 4) || !aligned(v_scales, 4))
+        return fail(PKV_ERR_INVALID, F + "buffers must be 16-byte aligned (slot_mapping 8; positions, inv_freq, "
+                                         "scales 4)");
+    p.err = device_error_word();
+    if (!p.err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
+    const cudaError_t e = launch_rope_append(p, act_dtype, cache_dtype == PKV_E4M3 && blocks ? kCacheE4M3Blocks : cache_dtype,
+                                             static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail("paged_rope_append: launch", e);
+}
+
+int paged_block_copy_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,
+                            const int32_t* src_dst_pairs, int num_pairs, int num_blocks, int num_kv_heads,
+                            size_t block_bytes, void* stream) {
+    const std::string F("paged_block_copy_scaled: ");
+    if (num_pairs < 0 || num_blocks <= 0 || num_kv_heads <= 0 || block_bytes == 0 || block_bytes % 16 != 0)
+        return fail(PKV_ERR_INVALID, F + "num_pairs >= 0, num_blocks and num_kv_heads > 0, block_bytes a positive multiple of 16");
+    if (num_pairs == 0) return PKV_OK;
+    if (num_pairs > 65535 * 64) return fail(PKV_ERR_INVALID, F + "too many pairs in one call");
+    if (!k_cache || !v_cache || !k_scales || !v_scales || !src_dst_pairs) return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(src_dst_pairs, 4) || !aligned(k_scales, 4) ||
+        !aligned(v_scales, 4))
+        return fail(PKV_ERR_INVALID, F + "caches must be 16-byte aligned (pairs and scales 4)");
+    int* err = device_error_word();
+    if (!err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
+    CopyParams p{k_cache, v_cache, src_dst_pairs, err, block_bytes, num_blocks, k_scales, v_scales, num_kv_heads};
+    const cudaError_t e = launch_block_copy(p, num_pairs, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail("paged_block_copy_scaled: launch", e);
+}
+
+int paged_block_scales_swap(float* k_scales, float* v_scales, const int32_t* block_ids, int num_ids, int num_blocks,
+                            int num_kv_heads, float* staging, int direction, void* stream) {
+    const std::string F("paged_block_scales_swap: ");
+    if (num_ids < 0 || num_blocks <= 0 || num_kv_heads <= 0 || (direction != PKV_SWAP_OUT && direction != PKV_SWAP_IN))
+        return fail(PKV_ERR_INVALID, F + "bad sizes or direction");
+    if (num_ids == 0) return PKV_OK;
+    if (num_ids > 0x7fffffff / 2) return fail(PKV_ERR_INVALID, F + "too many blocks");
+    if (!k_scales || !v_scales || !block_ids || !staging) return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (!aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(staging, 4) || !aligned(block_ids, 4))
+        return fail(PKV_ERR_INVALID, F + "buffers must be 4-byte aligned");
+    cudaPointerAttributes attr{};
+    cudaError_t e = cudaPointerGetAttributes(&attr, staging);
+    if (e != cudaSuccess) return cuda_fail("paged_block_scales_swap: staging pointer", e);
+    if (attr.type == cudaMemoryTypeUnregistered)
+        return fail(PKV_ERR_INVALID, F + "staging must be device memory or pinned/registered host memory");
+    int* err = device_error_word();
+    if (!err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
+    float* dev_staging = attr.type == cudaMemoryTypeHost && attr.devicePointer
+                             ? static_cast<float*>(attr.devicePointer) : staging;
+    e = launch_scales_swap(ScalesSwapParams{k_scales, v_scales, block_ids, dev_staging, err, num_ids, num_blocks,
+                                            num_kv_heads, direction == PKV_SWAP_OUT ? 1 : 0},
+                           static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail("paged_block_scales_swap: launch", e);
 }
 
 int quest_block_minmax(const void* k_cache, const int32_t* block_tables, int max_blocks_per_seq,

@@ -24,6 +24,14 @@
 // four warps' states are merged in shared memory (log-sum-exp weights) and
 // either written as the output (one partition) or as a partial
 // (m, l, o = acc/l) for the split-K merge kernel.
+//
+// Block-scaled E4M3 cache: the producer reads each block's K and V scale with
+// its table entry and leaves them beside the stage.  A warp's 8 tokens of a
+// stage lie in one block, so both scales are warp-uniform: the K scale joins
+// the factor of the reduced dot product, the V scale the weights.  Weights are
+// kept relative to a power of two 2^mv near the V scales seen, moved (with acc)
+// when a block's scale is more than 2^7 away from it, so that p * vs / 2^mv
+// stays within binary16 whatever the scales are.
 #pragma once
 
 #include <type_traits>
@@ -36,11 +44,17 @@ namespace pkv {
 constexpr int kStageTokens = 32;
 constexpr float kRescaleLog2 = 8.0f;  // largest log2 growth of the running max left unrescaled
 constexpr int kConsumerWarps = 4;
+constexpr int kNoRef = -1000;  // no V scale seen yet
 constexpr int kDecodeThreads = (kConsumerWarps + 1) * 32;
+
+// 2^e for |e| <= 126, the nearest of those powers beyond.
+__device__ __forceinline__ float pow2_clamped(int e) {
+    return __uint_as_float(static_cast<uint32_t>(min(126, max(-126, e)) + 127) << 23);
+}
 
 template <int CACHE, int D, int BS, int G>
 struct DecodeCfg {
-    static constexpr int E = CACHE == kE4M3 ? 1 : 2;  // bytes per cache element
+    static constexpr int E = is_e4m3(CACHE) ? 1 : 2;  // bytes per cache element
     static constexpr int VEC = 16 / E;                // elements per 16-byte vector
     static constexpr int LPR = D / VEC;               // lanes per token row
     static constexpr int TPP = 32 / LPR;              // token rows per warp-wide load
@@ -52,7 +66,9 @@ struct DecodeCfg {
     static constexpr int STAGES_RAW = 65536 / (2 * STAGE_BYTES);
     static constexpr int STAGES = STAGES_RAW < 2 ? 2 : (STAGES_RAW > 8 ? 8 : STAGES_RAW);
     static constexpr int RED_FLOATS = kConsumerWarps * G * (D + 2);
-    static constexpr int SMEM_BYTES = 2 * STAGES * STAGE_BYTES + 2 * STAGES * 8 + RED_FLOATS * 4;
+    static constexpr bool SCALED = CACHE == kE4M3B;
+    static constexpr int SCALE_FLOATS = SCALED ? 2 * STAGES * BPS : 0;  // K, then V scales of each stage's blocks
+    static constexpr int SMEM_BYTES = 2 * STAGES * STAGE_BYTES + 2 * STAGES * 8 + (RED_FLOATS + SCALE_FLOATS) * 4;
     static_assert(LPR >= 1 && LPR <= 32 && 32 % LPR == 0, "row layout");
     static_assert(TW % TPP == 0, "tokens per warp must be a multiple of rows per load");
     static_assert(kStageTokens % BS == 0, "block size must divide the stage");
@@ -73,6 +89,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     float* red_m = red;                                     // [NW][G]
     float* red_l = red + kConsumerWarps * G;                // [NW][G]
     float* red_acc = red + 2 * kConsumerWarps * G;          // [NW][G][D]
+    [[maybe_unused]] float* sk = red + C::RED_FLOATS;       // [STAGES][BPS]
+    [[maybe_unused]] float* sv = sk + C::STAGES * C::BPS;   // [STAGES][BPS]
 
     // the merge kernel may be scheduled once every CTA got here; it waits for
     // this grid to finish
@@ -85,6 +103,14 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
 
     const int L = p.context_lens[static_cast<int64_t>(seq) * p.lens_seq_stride + kvh * p.lens_kvh_stride];
     if (L < 1 || L > p.max_blocks_per_seq * BS) {
+        if (C::SCALED && L == 0) {  // an empty row of a padded batch: zeros
+            if (part == 0)
+                for (int i = threadIdx.x; i < G * D / 8; i += kDecodeThreads)
+                    reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                             (static_cast<size_t>(seq) * p.num_q_heads + kvh * G) * D)[i] =
+                        make_uint4(0u, 0u, 0u, 0u);
+            return;
+        }
         if (part == 0 && kvh == 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadLen);
         return;
     }
@@ -129,12 +155,25 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                 atomicOr(p.err, kErrBadBlock);
                 phys = -1;
             }
+            [[maybe_unused]] float ksc = 0.f, vsc = 0.f;
+            if (C::SCALED && have && phys >= 0) {
+                ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + kvh];
+                vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + kvh];
+            }
             const int chunk_blocks = min(32, n_blk - chunk);
             for (int j = 0; j < chunk_blocks; j += C::BPS) {
                 int pb[C::BPS];
 #pragma unroll
                 for (int bi = 0; bi < C::BPS; ++bi) pb[bi] = __shfl_sync(0xffffffffu, phys, (j + bi) & 31);
                 const int st = (chunk + j) / C::BPS;
+                [[maybe_unused]] float pk[C::BPS], pv[C::BPS];
+                if constexpr (C::SCALED) {
+#pragma unroll
+                    for (int bi = 0; bi < C::BPS; ++bi) {
+                        pk[bi] = __shfl_sync(0xffffffffu, ksc, (j + bi) & 31);
+                        pv[bi] = __shfl_sync(0xffffffffu, vsc, (j + bi) & 31);
+                    }
+                }
                 if (lane == 0) {
                     const int s = st % C::STAGES;
                     if (st >= C::STAGES && !mbar_wait(&empty[s], ((st / C::STAGES) - 1) & 1)) {
@@ -143,6 +182,13 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                     }
                     if (ok) {
                         uint32_t bytes = 0;
+                        if constexpr (C::SCALED) {  // before the arrive that publishes the stage
+#pragma unroll
+                            for (int bi = 0; bi < C::BPS; ++bi) {
+                                sk[s * C::BPS + bi] = pk[bi];
+                                sv[s * C::BPS + bi] = pv[bi];
+                            }
+                        }
 #pragma unroll
                         for (int bi = 0; bi < C::BPS; ++bi)
                             if (j + bi < chunk_blocks && pb[bi] >= 0) bytes += 2 * C::TILE_BYTES;
@@ -183,7 +229,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     const int c = lane % C::LPR;  // 16-byte chunk within the row
     const int h0 = kvh * G;
 
-    const float kmul = CACHE == kE4M3 ? *p.k_scale : 1.0f;
+    const float kmul = CACHE == kE4M3 ? *p.k_scale : 1.0f;  // block scales come with their stage
     const float qscale = p.scale_log2 * kmul;
     const uint16_t* qsrc = static_cast<const uint16_t*>(p.q) + (static_cast<size_t>(seq) * p.num_q_heads + h0) * D;
 
@@ -193,7 +239,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     // binary32 with fma.rn.f32.f16, and the scale multiplies the reduced dot
     // product.  P·V takes the probability rounded to binary16.
     bool mixed = false;
-    if constexpr (CACHE == kE4M3) {
+    if constexpr (is_e4m3(CACHE)) {
         bool fits = true;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -208,6 +254,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
         mixed = __all_sync(0xffffffffu, fits);
     }
 
+    [[maybe_unused]] int mv = kNoRef;  // block-scaled: acc is in units of 2^mv
     float m[G], l[G], acc[G][C::VEC];
 #pragma unroll
     for (int g = 0; g < G; ++g) {
@@ -255,6 +302,26 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
             const unsigned char* kb = kbuf + s * C::STAGE_BYTES;
             const unsigned char* vb = vbuf + s * C::STAGE_BYTES;
             const int tok0 = tok_begin + st * kStageTokens;
+            [[maybe_unused]] float ks = 1.f, vf = 1.f;
+            if constexpr (C::SCALED) {
+                const int bi = warp * C::TW / BS;  // the block of this warp's tokens
+                ks = sk[s * C::BPS + bi];
+                vf = sv[s * C::BPS + bi];
+                // exponent of the V scale; 0 (and subnormal scales) leave the reference alone
+                const int ev = static_cast<int>((__float_as_uint(vf) >> 23) & 0xffu) - 127;
+                if (ev > -127 && tok0 + warp * C::TW < tok_end && (ev > mv + 7 || ev < mv - 7)) {
+                    const int to = mv == kNoRef ? ev : max(ev, mv - 80);  // acc stays finite
+                    if (mv != kNoRef) {
+                        const float a = pow2_clamped(mv - to);
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+#pragma unroll
+                            for (int v = 0; v < C::VEC; ++v) acc[g][v] *= a;
+                    }
+                    mv = to;
+                }
+                vf *= mv == kNoRef ? 0.f : pow2_clamped(-mv);
+            }
 
             float sc[C::PASSES][G];
 #pragma unroll
@@ -276,7 +343,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                         float d = d0 + d1;
 #pragma unroll
                         for (int off = C::LPR / 2; off >= 1; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-                        sc[pp][g] = valid ? d * qscale : -INFINITY;
+                        sc[pp][g] = valid ? d * (C::SCALED ? qscale * ks : qscale) : -INFINITY;
                     }
                 } else {
                     float kf[C::VEC];
@@ -288,7 +355,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                         for (int v = 0; v < C::VEC; ++v) d = fmaf(qf[g][v], kf[v], d);
 #pragma unroll
                         for (int off = C::LPR / 2; off >= 1; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
-                        sc[pp][g] = valid ? d : -INFINITY;
+                        sc[pp][g] = valid ? (C::SCALED ? d * ks : d) : -INFINITY;
                     }
                 }
             }
@@ -316,6 +383,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                 for (int pp = 0; pp < C::PASSES; ++pp) {
                     pr[pp][g] = sc[pp][g] == -INFINITY ? 0.f : fast_exp2(sc[pp][g] - m[g]);
                     l[g] += pr[pp][g];
+                    if constexpr (C::SCALED) pr[pp][g] *= vf;
                 }
             }
 
@@ -348,13 +416,20 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
             if (lane == 0) mbar_arrive(&empty[s]);
         }
     };
-    if constexpr (CACHE == kE4M3) {
+    if constexpr (is_e4m3(CACHE)) {
         if (mixed) consume(std::true_type{});
         else consume(std::false_type{});
     } else {
         consume(std::false_type{});
     }
 
+    if constexpr (C::SCALED) {
+        const float a = mv == kNoRef ? 0.f : pow2_clamped(mv);
+#pragma unroll
+        for (int g = 0; g < G; ++g)
+#pragma unroll
+            for (int v = 0; v < C::VEC; ++v) acc[g][v] *= a;
+    }
     // Merge the token rows of this warp: lanes of equal chunk c hold partial sums.
 #pragma unroll
     for (int g = 0; g < G; ++g) {

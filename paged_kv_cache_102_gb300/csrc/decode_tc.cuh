@@ -54,6 +54,14 @@
 // fills all 16 rows; O = V^T P is right on dimensions 0-63 in columns 0-7 and
 // on 64-127 in columns 8-15, the only ones read.  The K/V bytes per item and
 // the MMA shapes are those of head_dim 128.
+// Block-scaled E4M3 cache: the scheduler reads each block's K and V scale with
+// its table entry and passes both through the queue.  S rows are tokens, so
+// the softmax thread of a token multiplies its scores by one K scale and its
+// weights by one V scale vs.  P enters the MMA as p * vs * 2^c, 2^c the power of
+// two that puts the largest p * vs of a head just below 2^8 (from the maximum
+// of score + log2 |vs|, taken along with the maximum score), so that the two
+// E4M3 parts keep their precision for the tokens that matter, whatever the
+// scales of the others; the epilogue takes 2^c out again.
 // Every barrier wait is bounded (kWaitLimitNs); on a timeout the CTA stops
 // issuing work, drains its in-flight copies and MMAs, frees tensor memory and
 // reports kErrTimeout.
@@ -81,7 +89,7 @@ constexpr int kTcSmemPerSm = 228 * 1024;      // shared memory of one SM, includ
 constexpr int kTcQueue = 2;                   // claimed items in flight between the roles
 constexpr int kTcLenBuckets = 8;              // length buckets of the partly filled partitions
 
-template <int NS, int STG = kTcStage, bool PAIR = false>
+template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false>
 struct TcSmem {
     static constexpr int RING = 0;
     static constexpr int Q = NS * STG;
@@ -94,13 +102,15 @@ struct TcSmem {
     static constexpr int P = Q + QBUFS * QBUF;
     static constexpr int PBUF = STG == kTcStage8 ? 8192 : PAIR ? 2 * kTcMaxTiles * 2048 : kTcPBuf;  // one P buffer
     static constexpr int PBUFS = STG == kTcStage8 ? 2 : 1;           // P buffers
-    static constexpr int QUEUE = P + PBUFS * PBUF;  // item numbers, q shifts, block-table entries [32] per entry
-    static constexpr int BARS = (QUEUE + 2 * kTcQueue * 4 + kTcQueue * 32 * 4 + 7) / 8 * 8;
+    // item numbers, q shifts, block-table entries [32] (and K and V scales [32] each) per entry
+    static constexpr int QUEUE = P + PBUFS * PBUF;
+    static constexpr int BARS = (QUEUE + 2 * kTcQueue * 4 + (SCALED ? 3 : 1) * kTcQueue * 32 * 4 + 7) / 8 * 8;
     // full[NS], empty[NS], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], final,
     // item_full[kTcQueue], item_empty[kTcQueue] (a single Q or P buffer uses entry 0 of its pair)
     static constexpr int NBARS = 2 * NS + 13 + 2 * kTcQueue;
     static constexpr int RED = BARS + NBARS * 8;
-    static constexpr int RED_FLOATS = 64 + 64;  // red_max[4][8], red_sum[4][8], stats[2][2][2][8]
+    // red_max[4][8], red_sum[4][8], stats[2][2][2][8]; SCALED: red_max2[4][8], pscale[2][8]
+    static constexpr int RED_FLOATS = 64 + 64 + (SCALED ? 48 : 0);
     static constexpr int MISC = RED + RED_FLOATS * 4;
     // per row: length (int), item prefix (int, rows + 2 entries), length order (uint16)
     static constexpr int ROWS = (MISC + 16 + 15) / 16 * 16;
@@ -222,13 +232,14 @@ template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR = false>
 __global__ void __launch_bounds__(kTcThreads, 2)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const __grid_constant__ CUtensorMap qmap, const DecodeParams p) {
-    constexpr bool FP8 = CACHE == kE4M3;
+    constexpr bool FP8 = is_e4m3(CACHE);
+    constexpr bool SCALED = CACHE == kE4M3B;
     constexpr int STG = FP8 ? kTcStage8 : kTcStage;  // bytes of one ring stage
     // PAIR: head_dim 64, kv heads 2v and 2v+1 of a sequence in one item, as
     // dimensions 0-63 and 64-127 of a 128-wide head (tile halves, Q regions)
     constexpr int HD = PAIR ? 64 : kTcD;  // head_dim of the caches, queries and output
     static_assert(!PAIR || !FP8, "pairs of head_dim-64 kv heads: 16-bit caches");
-    using S = TcSmem<NS, STG, PAIR>;
+    using S = TcSmem<NS, STG, PAIR, SCALED>;
     constexpr int THREADS = kTcThreads;
     constexpr int BPT = kTcTile / BS;  // blocks per tile
     // E4M3 x E4M3 (kind::f8f6f4) has the same descriptor bits as binary16 x binary16
@@ -252,6 +263,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     volatile int* item_q = reinterpret_cast<volatile int*>(sm + S::QUEUE);
     volatile int* item_shift = item_q + kTcQueue;
     volatile int* item_phys = item_shift + kTcQueue;  // [slot][32]: the item's physical blocks
+    // [slot][K, V][32]: the scales of those blocks
+    [[maybe_unused]] volatile float* item_scales = reinterpret_cast<volatile float*>(item_phys + kTcQueue * 32);
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::BARS);
     uint64_t* full = bars;
     uint64_t* empty = bars + NS;
@@ -267,6 +280,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     float* red_max = reinterpret_cast<float*>(sm + S::RED);
     float* red_sum = red_max + 32;
     float* stats = red_max + 64;  // [buffer][kv head of a pair][max, sum][8]
+    [[maybe_unused]] float* red_max2 = stats + 64;   // [4][8]: max of score + log2 |V scale|
+    [[maybe_unused]] float* pscale = red_max2 + 32;  // [buffer][8]: 1 / the power of two that P was scaled by
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(sm + S::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 4);
 
@@ -452,7 +467,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             // sequences with a context length outside 1..max_blocks*BS are skipped; report them once
             for (int s = blockIdx.x; s < B; s += gridDim.x) {
                 const int L = s_lens[s];
+                if (SCALED && L == 0) continue;
                 if (L < 1 || L > p.max_blocks_per_seq * BS) atomicOr(p.err, kErrBadLen);
+            }
+        }
+        if constexpr (SCALED) {  // empty rows of a padded batch: zeros
+            for (int s = blockIdx.x; s < B; s += gridDim.x) {
+                if (s_lens[s] != 0) continue;
+                uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
+                                                    static_cast<size_t>(s) * p.num_q_heads * HD);
+                for (int i = lane; i < p.num_q_heads * HD / 8; i += 32) o[i] = make_uint4(0u, 0u, 0u, 0u);
             }
         }
         auto table_entry = [&](const TcItem& it) {
@@ -472,6 +496,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         // at the end of the work (the end marker is queued) or on an abort.
         auto claim = [&](TcItem& it, int& phys) {
             phys = -1;
+            [[maybe_unused]] float ksc = 0.f, vsc = 0.f;
             int ci = -1;
             if (lane == 0) {
                 ci = atomicAdd(p.work_counter, 1);
@@ -500,7 +525,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     it.qshift = m > 0.f ? min(120, max(-120, e - 7)) : 0;
                 }
                 phys = table_entry(it);
-                if (p.new_slots != nullptr && it.tok_begin + it.n_tok == s_lens[it.row]) {
+                if (SCALED && phys >= 0) {
+                    ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
+                    vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
+                }
+                if (!SCALED && p.new_slots != nullptr && it.tok_begin + it.n_tok == s_lens[it.row]) {
                     // fused append: this item holds the new (last) token; write it
                     // before the item is published, so before any copy of its block
 #pragma unroll
@@ -521,6 +550,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 return false;
             }
             item_phys[slot * 32 + lane] = phys;
+            if constexpr (SCALED) {
+                item_scales[slot * 64 + lane] = ksc;
+                item_scales[slot * 64 + 32 + lane] = vsc;
+            }
             if (lane == 0) {
                 item_q[slot] = ci;
                 item_shift[slot] = it.qshift;
@@ -834,6 +867,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int tid = threadIdx.x - 64;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         int nread = 0;
+        // block-scaled: the scales of this thread's tokens in the item read last
+        [[maybe_unused]] float ks_t[kTcMaxTiles], vs_t[kTcMaxTiles];
 
         // Every wait below is followed by a barrier that all 128 threads reach;
         // a failure is OR-reduced there so that the four warps leave together
@@ -844,6 +879,14 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 __all_sync(0xffffffffu, tc_wait(&item_full[slot], (nread / kTcQueue) & 1, abort_flag, p.err));
             const int ci = good ? item_q[slot] : -1;
             const int qshift = good ? item_shift[slot] : 0;
+            if constexpr (SCALED) {
+#pragma unroll
+                for (int t = 0; t < kTcMaxTiles; ++t) {
+                    const int i = slot * 64 + (t * kTcTile + row) / BS;
+                    ks_t[t] = item_scales[i];
+                    vs_t[t] = item_scales[i + 32];
+                }
+            }
             ++nread;
             if (named_bar_or(3, 128, !good)) return -1;
             if (tid == 0) mbar_arrive(&item_empty[slot]);
@@ -862,7 +905,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                  (k == 0 || S::PBUFS == 2 ||
                                   tc_wait(&o_full[(k - 1) & 1], ((k - 1) >> 1) & 1, abort_flag, p.err)));
             // E4M3: S was computed on the stored codes and on q x 2^-qshift
-            const float sl = FP8 ? p.scale_log2 * *p.k_scale * __uint_as_float(static_cast<uint32_t>(127 + it.qshift) << 23)
+            const float sl = FP8 ? p.scale_log2 * (SCALED ? 1.f : *p.k_scale) *
+                                       __uint_as_float(static_cast<uint32_t>(127 + it.qshift) << 23)
                                  : p.scale_log2;
             unsigned char* pb = pbuf + (S::PBUFS == 2 ? b * S::PBUF : 0);
             // PAIR: columns 0-7 (kv head 2v) and 8-15 (kv head 2v+1) in two
@@ -896,30 +940,45 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     }
                     tc::fence_before_sync();  // these reads precede the next MMA into this S buffer
                     float mx[G];
+                    [[maybe_unused]] float mx2[G];
 #pragma unroll
-                    for (int g = 0; g < G; ++g) mx[g] = -INFINITY;
+                    for (int g = 0; g < G; ++g) mx[g] = mx2[g] = -INFINITY;
 #pragma unroll
                     for (int t = 0; t < kTcMaxTiles; ++t) {
                         const bool valid = t < it.n_tiles && t * kTcTile + row < it.n_tok;
 #pragma unroll
                         for (int g = 0; g < G; ++g) {
-                            sc[t][g] = valid ? sc[t][g] * sl : -INFINITY;
+                            sc[t][g] = valid ? sc[t][g] * (SCALED ? sl * ks_t[t] : sl) : -INFINITY;
                             mx[g] = fmaxf(mx[g], sc[t][g]);
+                            if constexpr (SCALED) mx2[g] = fmaxf(mx2[g], sc[t][g] + __log2f(fabsf(vs_t[t])));
                         }
                     }
 #pragma unroll
-                    for (int g = 0; g < G; ++g) mx[g] = warp_max(mx[g]);
+                    for (int g = 0; g < G; ++g) {
+                        mx[g] = warp_max(mx[g]);
+                        if constexpr (SCALED) mx2[g] = warp_max(mx2[g]);
+                    }
                     if (lane == 0) {
 #pragma unroll
-                        for (int g = 0; g < G; ++g) red_max[q4 * 8 + g] = mx[g];
+                        for (int g = 0; g < G; ++g) {
+                            red_max[q4 * 8 + g] = mx[g];
+                            if constexpr (SCALED) red_max2[q4 * 8 + g] = mx2[g];
+                        }
                     }
                 }
                 if (named_bar_or(1, 128, !good)) return false;
                 float M[G], sum[G];
+                [[maybe_unused]] float pc[G];  // weights enter the MMA as p * vs * pc
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     M[g] = fmaxf(fmaxf(red_max[g], red_max[8 + g]), fmaxf(red_max[16 + g], red_max[24 + g]));
                     sum[g] = 0.f;
+                    if constexpr (SCALED) {
+                        const float m2 = fmaxf(fmaxf(red_max2[g], red_max2[8 + g]), fmaxf(red_max2[16 + g], red_max2[24 + g]));
+                        // every V scale 0: any factor will do
+                        const int c = static_cast<int>(fminf(100.f, fmaxf(-100.f, floorf(M[g] - m2))));
+                        pc[g] = __uint_as_float(static_cast<uint32_t>(c + 8 + 127) << 23);
+                    }
                 }
 #pragma unroll
                 for (int t = 0; t < kTcMaxTiles; ++t) {
@@ -936,7 +995,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                 sum[g] += p0;
                                 sum[g + 1] += p1;
                                 uint32_t hi, lo;
-                                split_e4m3x2(p0 * 256.f, p1 * 256.f, hi, lo);
+                                if constexpr (SCALED) split_e4m3x2(p0 * (vs_t[t] * pc[g]), p1 * (vs_t[t] * pc[g + 1]), hi, lo);
+                                else split_e4m3x2(p0 * 256.f, p1 * 256.f, hi, lo);
                                 w[g >> 2] |= hi << (8 * (g & 3));
                                 w[2 + (g >> 2)] |= lo << (8 * (g & 3));
                             }
@@ -973,6 +1033,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     for (int g = 0; g < G; ++g) {
                         st[g] = M[g];
                         st[8 + g] = red_sum[g] + red_sum[8 + g] + red_sum[16 + g] + red_sum[24 + g];
+                        if constexpr (SCALED)  // 1 / pc, exact
+                            pscale[b * 8 + g] = __uint_as_float((254u << 23) - __float_as_uint(pc[g]));
                     }
                     if (hh == NH - 1) mbar_arrive(&p_full[S::PBUFS == 2 ? b : 0]);
                 }
@@ -1006,13 +1068,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const int d = PAIR ? (row & 63) : row;
             const bool single = p.max_parts == 1 || s_lens[it.row] <= p.partition_size;
             // E4M3: O was computed on the stored codes and on P x 2^8
-            const float vmul = FP8 ? *p.v_scale * (1.0f / 256.f) : 1.0f;
+            const float vmul = SCALED ? 1.0f : FP8 ? *p.v_scale * (1.0f / 256.f) : 1.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const float Mg = stats[(b * 2 + hh) * 16 + g];
                 const float Lg = stats[(b * 2 + hh) * 16 + 8 + g];
                 // L >= 1 (the max token's weight is 1): one reciprocal per head
-                const float val = o[g] * (__frcp_rn(Lg) * vmul);
+                const float val = o[g] * (__frcp_rn(Lg) * (SCALED ? pscale[b * 8 + g] : vmul));
                 const int kvh = PAIR ? 2 * it.kvh + hh : it.kvh;
                 const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + kvh * G + g;
                 if (single) {

@@ -1,6 +1,6 @@
 // Host side of the tensor-core grouped-query decode kernel shared by its
 // translation units (16-bit caches at head_dim 128 in decode_tc.cu, E4M3
-// caches in decode_tc_e4m3.cu, head_dim-64 pairs in decode_tc_d64.cu): TMA
+// caches in decode_tc_e4m3.cu and, with block scales, decode_tc_e4m3b.cu, head_dim-64 pairs in decode_tc_d64.cu): TMA
 // tensor maps over the caches and the queries, persistent grid sizing, the
 // launch template.
 #pragma once
@@ -57,7 +57,7 @@ template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR>
 cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                    int ctas_per_sm, cudaStream_t s) {
     auto kern = paged_decode_tc_kernel<ACT, CACHE, BS, G, NS, PAIR>;
-    using Smem = TcSmem<NS, CACHE == kE4M3 ? kTcStage8 : kTcStage, PAIR>;
+    using Smem = TcSmem<NS, is_e4m3(CACHE) ? kTcStage8 : kTcStage, PAIR, CACHE == kE4M3B>;
     constexpr int threads = kTcThreads;
     const int rows = p.table_kvh_stride != 0 ? p.num_seqs * p.num_kv_heads : p.num_seqs;
     const int smem = Smem::alloc(rows);

@@ -8,6 +8,9 @@
 namespace pkv {
 
 constexpr int kMaxDevices = 64;
+// Cache kind of the launchers next to the pkv_dtype codes: E4M3 with one scale
+// per (block, kv head) (kE4M3B of the kernels).
+constexpr int kCacheE4M3Blocks = 3;
 
 struct AppendParams {
     const void* k;
@@ -25,6 +28,60 @@ struct AppendParams {
     int num_blocks;
 };
 
+// Rotary positions and the append of rotated keys (positions == nullptr: no
+// rotation and no queries).
+struct RopeAppendParams {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride;  // elements from one token's row to the next
+    int64_t k_stride;
+    int64_t v_stride;
+    const int32_t* positions;
+    const int64_t* slot_mapping;
+    const float* inv_freq;  // [rotary_dim / 2]
+    void* q_out;
+    int64_t q_out_stride;
+    void* k_cache;
+    void* v_cache;
+    const float* k_scale;  // E4M3, one scale per tensor
+    const float* v_scale;
+    float* k_scales;  // E4M3, [num_blocks][num_kv_heads]
+    float* v_scales;
+    int* err;
+    float factor;  // multiplies cos and sin
+    int num_tokens;
+    int num_q_heads;
+    int num_kv_heads;
+    int head_dim;
+    int rotary_dim;
+    int interleaved;
+    int block_size;
+    int num_blocks;
+};
+
+// Tables, slots and positions of a step's tokens (extend_tables.cu).
+struct ExtendParams {
+    int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* new_lens;
+    const int32_t* free_blocks;
+    const int32_t* free_head;
+    int64_t* slot_mapping;
+    int32_t* positions;
+    int32_t* seq_starts;    // [num_seqs + 1]
+    int32_t* block_starts;  // [num_seqs + 1]
+    int32_t* lens_out;
+    int32_t* free_head_out;
+    int* err;
+    int num_seqs;
+    int max_blocks_per_seq;
+    int block_size;
+    int num_free;
+    int num_blocks;
+    int num_tokens;
+};
+
 struct CopyParams {
     void* k_cache;
     void* v_cache;
@@ -32,6 +89,21 @@ struct CopyParams {
     int* err;
     size_t block_bytes;
     int num_blocks;
+    float* k_scales;  // [num_blocks][num_kv_heads], copied with the block; null: none
+    float* v_scales;
+    int num_kv_heads;
+};
+
+struct ScalesSwapParams {
+    float* k_scales;
+    float* v_scales;
+    const int32_t* block_ids;
+    float* staging;  // [n][2][num_kv_heads]: K then V scales of each listed block
+    int* err;
+    int n;
+    int num_blocks;
+    int num_kv_heads;
+    int to_staging;
 };
 
 struct SwapParams {
@@ -67,7 +139,7 @@ struct DecodeParams {
     int64_t table_kvh_stride;
     int lens_seq_stride;
     int lens_kvh_stride;
-    const float* k_scale;
+    const float* k_scale;  // block-scaled E4M3 cache: [num_blocks][num_kv_heads], else one value
     const float* v_scale;
     int* err;
     int max_blocks_per_seq;
@@ -147,9 +219,12 @@ cudaError_t launch_quest_minmax(const QuestMetaParams& p, int meta, int cache, c
 cudaError_t launch_quest_append_minmax(const QuestAppendParams& p, int act, int cache, cudaStream_t s);
 cudaError_t launch_quest_select(const QuestSelectParams& p, int dtype, int G, cudaStream_t s);
 
+cudaError_t launch_rope_append(const RopeAppendParams& p, int act, int cache, cudaStream_t stream);
+cudaError_t launch_extend_tables(const ExtendParams& p, cudaStream_t stream);
 cudaError_t launch_append(const AppendParams& p, int act, int cache, cudaStream_t stream);
 cudaError_t launch_block_copy(const CopyParams& p, int num_pairs, cudaStream_t stream);
 cudaError_t launch_block_swap(const SwapParams& p, int n, cudaStream_t stream);
+cudaError_t launch_scales_swap(const ScalesSwapParams& p, cudaStream_t stream);
 cudaError_t launch_merge(const MergeParams& p, int act, cudaStream_t stream);
 cudaError_t launch_selftest_wait(uint64_t limit_ns, int* err, cudaStream_t stream);
 
@@ -159,8 +234,11 @@ cudaError_t launch_decode_f16_f16(const DecodeParams& p, int D, int BS, int G, c
 cudaError_t launch_decode_bf16_bf16(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_f16_e4m3(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_bf16_e4m3(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_f16_e4m3b(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_bf16_e4m3b(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 
-// Tensor-core grouped-query path (head_dim 128 with a 16-bit or E4M3 cache,
+// Tensor-core grouped-query path (head_dim 128 with a 16-bit or E4M3 cache
+// of either scaling,
 // or head_dim 64 with a 16-bit cache, an even kv-head count and shared
 // tables; group 2/4/8; partitions of at most 512 tokens).  variant 0: one CTA
 // per SM; variant 1: two CTAs per SM.
@@ -170,6 +248,7 @@ int decode_tc_max_rows();  // table rows (sequences, or (sequence, kv head) pair
 cudaError_t launch_decode_tc(const DecodeParams& p, int act, int cache, int head_dim, int BS, int G, int variant,
                              cudaStream_t s);
 cudaError_t launch_decode_tc_e4m3(const DecodeParams& p, int act, int BS, int G, int variant, cudaStream_t s);
+cudaError_t launch_decode_tc_e4m3b(const DecodeParams& p, int act, int BS, int G, int variant, cudaStream_t s);
 cudaError_t launch_decode_tc_d64(const DecodeParams& p, int act, int BS, int G, int variant, cudaStream_t s);
 
 }  // namespace pkv

@@ -106,6 +106,14 @@ __global__ void __launch_bounds__(256) paged_block_copy_kernel(CopyParams p) {
         *reinterpret_cast<uint4*>(kd + o) = a;
         *reinterpret_cast<uint4*>(vd + o) = b;
     }
+    if (p.k_scales && blockIdx.y == 0) {  // a block-scaled cache: the block's scales go with it
+        for (int h = threadIdx.x; h < p.num_kv_heads; h += blockDim.x) {
+            const int64_t s = static_cast<int64_t>(src) * p.num_kv_heads + h;
+            const int64_t d = static_cast<int64_t>(dst) * p.num_kv_heads + h;
+            p.k_scales[d] = p.k_scales[s];
+            p.v_scales[d] = p.v_scales[s];
+        }
+    }
 }
 
 cudaError_t launch_block_copy(const CopyParams& p, int num_pairs, cudaStream_t stream) {
@@ -156,6 +164,38 @@ cudaError_t launch_block_swap(const SwapParams& p, int n, cudaStream_t stream) {
     if (n == 0) return cudaSuccess;
     const unsigned chunks = static_cast<unsigned>((p.block_bytes + kCopyChunkBytes - 1) / kCopyChunkBytes);
     paged_block_swap_kernel<<<dim3(n, chunks), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+// The scales of swapped blocks: one thread per (listed block, kv head).
+__global__ void __launch_bounds__(256) paged_block_scales_swap_kernel(ScalesSwapParams p) {
+    const int64_t total = static_cast<int64_t>(p.n) * p.num_kv_heads;
+    for (int64_t i = blockIdx.x * static_cast<int64_t>(blockDim.x) + threadIdx.x; i < total;
+         i += static_cast<int64_t>(gridDim.x) * blockDim.x) {
+        int64_t e;
+        int h;
+        divmod_u(i, p.num_kv_heads, e, h);
+        const int b = p.block_ids[e];
+        if (b < 0 || b >= p.num_blocks) {
+            if (h == 0) atomicOr(p.err, kErrBadPair);
+            continue;
+        }
+        const int64_t pool = static_cast<int64_t>(b) * p.num_kv_heads + h;
+        float* st = p.staging + e * 2 * p.num_kv_heads + h;
+        if (p.to_staging) {
+            st[0] = p.k_scales[pool];
+            st[p.num_kv_heads] = p.v_scales[pool];
+        } else {
+            p.k_scales[pool] = st[0];
+            p.v_scales[pool] = st[p.num_kv_heads];
+        }
+    }
+}
+
+cudaError_t launch_scales_swap(const ScalesSwapParams& p, cudaStream_t stream) {
+    const int64_t want = (static_cast<int64_t>(p.n) * p.num_kv_heads + 255) / 256;
+    if (want == 0) return cudaSuccess;
+    paged_block_scales_swap_kernel<<<static_cast<unsigned>(want < 152 * 8 ? want : 152 * 8), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 

@@ -10,10 +10,12 @@
 
 namespace pkv {
 
-enum : int { kF16 = 0, kBF16 = 1, kE4M3 = 2 };
+// kE4M3B: E4M3 codes with one scale per (block, kv head) instead of one per tensor.
+enum : int { kF16 = 0, kBF16 = 1, kE4M3 = 2, kE4M3B = 3 };
+__host__ __device__ constexpr bool is_e4m3(int cache) { return cache == kE4M3 || cache == kE4M3B; }
 
 // Bits of the per-device error word (mirrors pkv_device_error_bits).
-enum : int { kErrBadBlock = 1, kErrBadLen = 2, kErrBadSlot = 4, kErrBadPair = 8, kErrTimeout = 16 };
+enum : int { kErrBadBlock = 1, kErrBadLen = 2, kErrBadSlot = 4, kErrBadPair = 8, kErrTimeout = 16, kErrNoSpace = 32 };
 
 // Longest time a kernel waits on one on-chip barrier before it reports
 // kErrTimeout and stops (nanoseconds of %globaltimer).
@@ -161,8 +163,7 @@ struct Vec16<kF16> {
     }
 };
 
-template <>
-struct Vec16<kE4M3> {
+struct Vec16E4M3 {
     static constexpr int N = 16;
     __device__ __forceinline__ static void to_float(const uint4& u, float* f) {
         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -180,6 +181,11 @@ struct Vec16<kE4M3> {
         }
     }
 };
+
+template <>
+struct Vec16<kE4M3> : Vec16E4M3 {};
+template <>
+struct Vec16<kE4M3B> : Vec16E4M3 {};
 
 // E4M3 pair -> binary16 pair (exact: every E4M3 value is a binary16 value).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
