@@ -28,6 +28,8 @@
 // E4M3 code has the same relative precision at every exponent, so a scale that
 // is not a power of two would gain nothing.)  Non-finite elements do not enter
 // the maximum: an infinity saturates to 448 * new, a NaN stays a NaN code.
+#include <type_traits>
+
 #include "kernels.h"
 #include "pkv_device.cuh"
 
@@ -36,8 +38,14 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kWindow = 32;  // tokens whose runs one warp looks over at a time
+constexpr int kTable = 2048;  // (cos, sin) pairs a block keeps in shared memory
+constexpr int kGroup = 8;     // row loads a warp has in flight
 constexpr int kScaleMinExp = -64, kScaleMaxExp = 120;
+
+// How the channels of a pair lie: neighbours; R/2 apart with R/2 a multiple of
+// 8 (whole 8-channel chunks swap, by shuffle); R/2 apart otherwise (partners
+// are read from memory).
+enum : int { kPairsNext = 0, kPairsChunks = 1, kPairsApart = 2 };
 
 // w / 2pi as a 64-bit fraction of a turn.
 __device__ __forceinline__ uint64_t turn_of(float w) {
@@ -56,83 +64,70 @@ __device__ __forceinline__ uint64_t turn_of(float w) {
 }
 
 // cos and sin of a phase in 64-bit turns.
-__device__ __forceinline__ void cos_sin_turns(uint64_t phase, float& c, float& s) {
+__device__ __forceinline__ float2 cos_sin_turns(uint64_t phase) {
     const uint64_t q = (phase + (1ull << 61)) >> 62;  // nearest quarter turn
     const int64_t r = static_cast<int64_t>(phase - (q << 62));
     float s0, c0;
     sincospif(__ll2float_rn(r) * 0x1p-63f, &s0, &c0);  // r * 2^-63 half turns, at most 1/4
     const bool odd = q & 1;
     const float cc = odd ? s0 : c0, ss = odd ? c0 : s0;
-    c = (q == 1 || q == 2) ? -cc : cc;
-    s = (q & 2) ? -ss : ss;
+    return make_float2((q == 1 || q == 2) ? -cc : cc, (q & 2) ? -ss : ss);
 }
 
-// The eight channels 8c .. 8c+7 of a row, as this lane holds them: their
-// frequencies, and cos and sin at one position.
-struct RopeLane {
-    uint64_t turn[8];
-    float cs[8], sn[8];
+__device__ __forceinline__ float2 cos_sin_at(const RopeAppendParams& p, int i, int pos) {
+    const float2 cs = cos_sin_turns(turn_of(p.inv_freq[i]) * static_cast<uint64_t>(static_cast<int64_t>(pos)));
+    return make_float2(cs.x * p.factor, cs.y * p.factor);
+}
 
-    __device__ __forceinline__ void frequencies(const RopeAppendParams& p, int c) {
-        const int half = p.rotary_dim / 2;
+// cos and sin for the eight channels 8c .. 8c+7 of a row; 1 and 0 for channels
+// that do not turn.  at(i) gives the pair i's.
+template <int PAIRS, class At>
+__device__ __forceinline__ void lane_cos_sin(const RopeAppendParams& p, int c, At at, float* cs, float* sn) {
+    const int half = p.rotary_dim / 2;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int e = 8 * c + j;
-            if (p.interleaved && (j & 1)) {
-                turn[j] = turn[j - 1];
-                continue;
-            }
-            const int i = p.interleaved ? e / 2 : (e < half ? e : e - half);
-            turn[j] = e < p.rotary_dim ? turn_of(p.inv_freq[i]) : 0;
+    for (int j = 0; j < 8; ++j) {
+        const int e = 8 * c + j;
+        if (PAIRS == kPairsNext && (j & 1)) {
+            cs[j] = cs[j - 1];
+            sn[j] = sn[j - 1];
+            continue;
         }
+        const int i = PAIRS == kPairsNext ? e / 2 : (e < half ? e : e - half);
+        const float2 t = e < p.rotary_dim ? at(i) : make_float2(1.f, 0.f);
+        cs[j] = t.x;
+        sn[j] = t.y;
     }
-    __device__ __forceinline__ void at(const RopeAppendParams& p, int pos, int c) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (p.interleaved && (j & 1)) {
-                cs[j] = cs[j - 1];
-                sn[j] = sn[j - 1];
-            } else if (8 * c + j < p.rotary_dim) {
-                cos_sin_turns(turn[j] * static_cast<uint64_t>(static_cast<int64_t>(pos)), cs[j], sn[j]);
-                cs[j] *= p.factor;
-                sn[j] *= p.factor;
-            } else {
-                cs[j] = 1.f;
-                sn[j] = 0.f;
-            }
-        }
-    }
-};
-
-template <int ACT>
-__device__ __forceinline__ void unpack(const uint4& u, float* f) {
-    Vec16<ACT>::to_float(u, f);
 }
 
 template <int ACT>
 __device__ __forceinline__ uint4 pack(const float* f) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        w[i] = static_cast<uint32_t>(float_to_act<ACT>(f[2 * i])) |
-               (static_cast<uint32_t>(float_to_act<ACT>(f[2 * i + 1])) << 16);
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (ACT == kBF16) {
+            const __nv_bfloat162 h = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        } else {
+            const __half2 h = __floats2half2_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+    }
     return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
-// Rotate the eight channels x of chunk c (raw bits u) in place.  Every lane of
-// the warp calls it: the partner chunk of the half layout comes from the lane
-// that holds it when R/2 is a multiple of 8, from memory otherwise.  Products
-// and their difference are rounded one by one (no fused multiply-add), which
-// keeps the result symmetric in the two terms.
-template <int ACT>
-__device__ __forceinline__ void rotate8(const RopeAppendParams& p, const RopeLane& rl, const uint4& u,
-                                        const uint16_t* row, int c, int lane, bool live, float* x) {
+// x = the rotated channels of chunk c (raw bits u of row `row`).  Every lane of
+// the warp calls it.  The products and their sum are rounded one by one, so
+// that both terms of a channel enter alike.
+template <int ACT, int PAIRS>
+__device__ __forceinline__ void rotate8(const RopeAppendParams& p, const uint4& u, const uint16_t* row, int c, int lane,
+                                        bool live, const float* cs, const float* sn, float* x) {
     const int rot = p.rotary_dim, half = rot / 2;
     float y[8];
-    if (p.interleaved) {
+    Vec16<ACT>::to_float(u, x);
+    if (PAIRS == kPairsNext) {
 #pragma unroll
         for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
-    } else if (half % 8 == 0) {
+    } else if (PAIRS == kPairsChunks) {
         const int hc = half / 8;
         const int src = c < hc ? lane + hc : (c < 2 * hc ? lane - hc : lane);
         uint4 v;
@@ -140,22 +135,20 @@ __device__ __forceinline__ void rotate8(const RopeAppendParams& p, const RopeLan
         v.y = __shfl_sync(0xffffffffu, u.y, src);
         v.z = __shfl_sync(0xffffffffu, u.z, src);
         v.w = __shfl_sync(0xffffffffu, u.w, src);
-        unpack<ACT>(v, y);
+        Vec16<ACT>::to_float(v, y);
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int e = 8 * c + j;
             y[j] = live && e < rot ? act_to_float<ACT>(row[e < half ? e + half : e - half]) : 0.f;
         }
-        __syncwarp();
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
         const int e = 8 * c + j;
-        if (e >= rot) continue;
-        const bool first = p.interleaved ? !(j & 1) : e < half;
-        const float a = __fmul_rn(x[j], rl.cs[j]), b = __fmul_rn(y[j], rl.sn[j]);
-        x[j] = first ? __fsub_rn(a, b) : __fadd_rn(a, b);
+        const bool first = PAIRS == kPairsNext ? !(j & 1) : e < half;
+        const float a = __fmul_rn(x[j], cs[j]), b = __fmul_rn(y[j], first ? -sn[j] : sn[j]);
+        if (e < rot) x[j] = __fadd_rn(a, b);
     }
 }
 
@@ -198,112 +191,166 @@ __device__ __forceinline__ int64_t slot_of(const RopeAppendParams& p, int t, boo
 }
 
 // ---------------------------------------------------------------------------
-// Rows that do not share a scale: the queries and, for a 16-bit or
-// one-scale E4M3 cache, the keys and values.  The rows of a token are its
-// heads [q | k | v]; one warp takes rows [part * per, (part + 1) * per) of a
-// token, RP = 32 / (D / 8) of them at a time, so that cos and sin are computed
-// once for all of them.
+// Rows that do not share a scale: the queries and, for a 16-bit or one-scale
+// E4M3 cache, the keys and values.  A warp takes a range of one token's heads
+// [q | k | v], RP = 32 / (D / 8) rows at a time and kGroup / 2 such loads ahead
+// of their use, with the token's cos and sin in registers (read once from the
+// block's table).
 // ---------------------------------------------------------------------------
-template <int ACT, int CACHE>
-__device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token, int row0, int row1) {
+template <int ACT, int CACHE, int PAIRS>
+__device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token, int row0, int row1, const float2* table) {
+    constexpr int U = kGroup / 2;
     const int lane = threadIdx.x & 31;
     const int lpr = p.head_dim / 8, rp = 32 / lpr;
     const int r = lane / lpr, c = lane - r * lpr;
-    const int pos = p.positions[token];
-    if (pos < 0) return;  // padding: q_out keeps its row
     bool bad = false;
     const int64_t slot = slot_of(p, token, &bad);
-    if (bad && row0 == 0 && lane == 0) atomicOr(p.err, kErrBadSlot);
+    if (CACHE != kE4M3B && bad && row0 == 0 && lane == 0) atomicOr(p.err, kErrBadSlot);
     int64_t blk = 0;
     int off = 0;
-    if (slot >= 0) divmod_u(slot, p.block_size, blk, off);
-    RopeLane rl;
-    rl.frequencies(p, c);
-    rl.at(p, pos, c);
-    for (int h0 = row0; h0 < row1; h0 += rp) {
-        const int h = h0 + r;
-        const bool have = r < rp && h < row1;
-        const bool is_q = h < p.num_q_heads, is_k = !is_q && h < p.num_q_heads + p.num_kv_heads;
-        const int hk = is_q ? h : is_k ? h - p.num_q_heads : h - p.num_q_heads - p.num_kv_heads;
-        const uint16_t* src = is_q   ? static_cast<const uint16_t*>(p.q) + token * p.q_stride
-                              : is_k ? static_cast<const uint16_t*>(p.k) + token * p.k_stride
-                                     : static_cast<const uint16_t*>(p.v) + token * p.v_stride;
-        src += static_cast<int64_t>(hk) * p.head_dim;
-        const uint4 u = have ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-        float x[8];
-        unpack<ACT>(u, x);
-        rotate8<ACT>(p, rl, u, src, c, lane, have && (is_q || is_k), x);
-        if (!have) continue;
-        if (is_q) {
-            uint16_t* dst = static_cast<uint16_t*>(p.q_out) + token * p.q_out_stride + static_cast<int64_t>(h) * p.head_dim;
-            *reinterpret_cast<uint4*>(dst + c * 8) = 8 * c < p.rotary_dim ? pack<ACT>(x) : u;
-            continue;
+    if (CACHE != kE4M3B && slot >= 0) divmod_u(slot, p.block_size, blk, off);
+    float cs[8], sn[8];
+    lane_cos_sin<PAIRS>(p, c, [&](int i) { return table[i]; }, cs, sn);
+    const bool turns = 8 * c < p.rotary_dim;
+    // heads [a, b) of one kind: src row, rotation or not, and where the result goes
+    auto heads = [&](int a, int b, const uint16_t* src, auto turning, auto store) {
+        for (int h0 = a; h0 < b; h0 += U * rp) {
+            uint4 u[U];
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                const int h = h0 + i * rp + r;
+                u[i] = r < rp && h < b ? *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(h) * p.head_dim + c * 8)
+                                       : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int i = 0; i < U; ++i) {
+                if (h0 + i * rp >= b) break;
+                const int h = h0 + i * rp + r;
+                const bool have = r < rp && h < b;
+                float x[8];
+                if constexpr (decltype(turning)::value) {
+                    rotate8<ACT, PAIRS>(p, u[i], src + static_cast<int64_t>(h) * p.head_dim, c, lane, have, cs, sn, x);
+                    if (PAIRS == kPairsApart) __syncwarp();  // in place: partners are read before they are written
+                } else {
+                    Vec16<ACT>::to_float(u[i], x);
+                }
+                if (have) store(h, u[i], x);
+            }
         }
-        if (slot < 0) continue;
-        const int64_t dst = ((blk * p.num_kv_heads + hk) * p.block_size + off) * p.head_dim + c * 8;
-        if constexpr (CACHE == ACT) {
-            uint16_t* cache = static_cast<uint16_t*>(is_k ? p.k_cache : p.v_cache);
-            *reinterpret_cast<uint4*>(cache + dst) = is_k && 8 * c < p.rotary_dim ? pack<ACT>(x) : u;
-        } else {
-            if (!is_k) unpack<ACT>(u, x);
-            divide8(x, is_k ? *p.k_scale : *p.v_scale);
-            *reinterpret_cast<uint2*>(static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) + dst) = to_codes(x);
+    };
+    const int nq = p.num_q_heads, nk = p.num_kv_heads;
+    if (row0 < nq) {
+        uint16_t* out = static_cast<uint16_t*>(p.q_out) + token * p.q_out_stride + c * 8;
+        heads(row0, min(row1, nq), static_cast<const uint16_t*>(p.q) + token * p.q_stride, std::true_type{},
+              [&](int h, const uint4& u, const float* x) {
+                  *reinterpret_cast<uint4*>(out + static_cast<int64_t>(h) * p.head_dim) = turns ? pack<ACT>(x) : u;
+              });
+    }
+    if constexpr (CACHE != kE4M3B) {
+        if (slot < 0) return;
+        auto at = [&](int h) { return ((blk * nk + h) * p.block_size + off) * p.head_dim + c * 8; };
+        auto put = [&](void* cache, const float* scale, bool raw, int h, const uint4& u, float* x) {
+            if constexpr (CACHE == ACT) {
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + at(h)) = raw ? u : pack<ACT>(x);
+            } else {
+                divide8(x, *scale);
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at(h)) = to_codes(x);
+            }
+        };
+        const int k0 = max(row0 - nq, 0), k1 = min(row1 - nq, nk);
+        if (k0 < k1)
+            heads(k0, k1, static_cast<const uint16_t*>(p.k) + token * p.k_stride, std::true_type{},
+                  [&](int h, const uint4& u, float* x) { put(p.k_cache, p.k_scale, !turns, h, u, x); });
+        const int v0 = max(row0 - nq - nk, 0), v1 = row1 - nq - nk;
+        if (v0 < v1)
+            heads(v0, v1, static_cast<const uint16_t*>(p.v) + token * p.v_stride, std::false_type{},
+                  [&](int h, const uint4& u, float* x) { put(p.v_cache, p.v_scale, true, h, u, x); });
+    }
+}
+
+// Largest finite |x| among eight 16-bit elements and the pairwise maxima `top`
+// so far (bit patterns without the sign: both types order as integers).
+// Infinities and NaN are at or above kInf and are taken out.
+template <int ACT>
+__device__ __forceinline__ void top_bits(const uint4& u, uint32_t& top) {
+    constexpr uint32_t kInf = ACT == kBF16 ? 0x7f80u : 0x7c00u;
+    const uint32_t w[4] = {u.x & 0x7fff7fffu, u.y & 0x7fff7fffu, u.z & 0x7fff7fffu, u.w & 0x7fff7fffu};
+    const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
+    if (max(m & 0xffffu, m >> 16) < kInf) {
+        top = __vmaxu2(top, m);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t a = w[i] & 0xffffu, b = w[i] >> 16;
+            top = __vmaxu2(top, (a < kInf ? a : 0u) | (b < kInf ? b << 16 : 0u));
         }
     }
 }
 
 // ---------------------------------------------------------------------------
-// One run of tokens of one block and kv head into a block-scaled cache, K or
+// One run of n tokens of one block and kv head into a block-scaled cache, K or
 // V, by one warp: the maximum over the run, the block's new scale, its other
-// codes where the scale grew, the run's codes.
+// codes where the scale grew, the run's codes.  Up to kGroup loads a lane (a
+// whole 16-token block at head_dim 128) stay in registers between the maximum
+// and the codes; longer runs are read twice.  Rotated keys are computed twice
+// instead of being kept.
 // ---------------------------------------------------------------------------
-template <int ACT>
-__device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, int64_t slot0, int head, bool is_k) {
+template <int ACT, int PAIRS>
+__device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, int n, int64_t blk, int off0, int head,
+                                           bool is_k, const float2* table, int tabled) {
     const int lane = threadIdx.x & 31;
     const int lpr = p.head_dim / 8, rp = 32 / lpr;
     const int r = lane / lpr, c = lane - r * lpr;
-    int64_t blk;
-    int off0;
-    divmod_u(slot0, p.block_size, blk, off0);
-    // length: up to the end of the block
-    const int most = p.block_size - off0;
-    int n = 1;
-    for (int base = 1; base < most; base += 32) {
-        const int k = base + lane;
-        bool bad = false;
-        const bool in = k < most && slot_of(p, t0 + k, &bad) == slot0 + k;
-        const unsigned out = __ballot_sync(0xffffffffu, !in);
-        n = base + (out ? __ffs(out) - 1 : 32);
-        if (out) break;
-    }
+    float* scale = (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + head;
+    const float old = off0 == 0 ? 0.f : *scale;
     const bool turn = is_k && p.positions != nullptr;
-    const uint16_t* src0 = is_k ? static_cast<const uint16_t*>(p.k) + t0 * p.k_stride
-                                : static_cast<const uint16_t*>(p.v) + t0 * p.v_stride;
-    src0 += static_cast<int64_t>(head) * p.head_dim;
     const int64_t stride = is_k ? p.k_stride : p.v_stride;
-    RopeLane rl;
-    if (turn) rl.frequencies(p, c);
-    auto load = [&](int i, float* x) {  // row i of the run (every lane calls it)
-        const bool have = r < rp && i < n;
-        const uint16_t* src = src0 + (have ? i : 0) * stride;
-        const uint4 u = have ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0u, 0u, 0u, 0u);
-        unpack<ACT>(u, x);
-        if (turn) {
-            rl.at(p, have ? p.positions[t0 + i] : 0, c);
-            rotate8<ACT>(p, rl, u, src, c, lane, have, x);
+    const uint16_t* src0 = (is_k ? static_cast<const uint16_t*>(p.k) : static_cast<const uint16_t*>(p.v)) + t0 * stride +
+                           static_cast<int64_t>(head) * p.head_dim;
+    const int half = p.rotary_dim / 2;
+    uint4 u[kGroup];
+    auto load = [&](int g0) {
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            const int i = g0 + j * rp + r;
+            u[j] = r < rp && i < n ? *reinterpret_cast<const uint4*>(src0 + i * stride + c * 8)
+                                   : make_uint4(0u, 0u, 0u, 0u);
         }
-        return have;
+    };
+    auto turned = [&](int i, const uint4& raw, float* x) {  // row i of the run (every lane calls it)
+        const bool have = r < rp && i < n;
+        const int row = have ? i : 0;
+        float cs[8], sn[8];
+        if (row < tabled) {
+            lane_cos_sin<PAIRS>(p, c, [&](int k) { return table[row * half + k]; }, cs, sn);
+        } else {
+            const int pos = p.positions[t0 + row];
+            lane_cos_sin<PAIRS>(p, c, [&](int k) { return cos_sin_at(p, k, pos); }, cs, sn);
+        }
+        __syncwarp();
+        rotate8<ACT, PAIRS>(p, raw, src0 + row * stride, c, lane, have, cs, sn, x);
     };
     float top = 0.f;
-    for (int i0 = 0; i0 < n; i0 += rp) {
-        float x[8];
-        load(i0 + r, x);
+    uint32_t tops = 0;
+    for (int g0 = 0; g0 < n; g0 += kGroup * rp) {
+        load(g0);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const float a = fabsf(x[j]);
-            if (a <= 3.402823466e38f) top = fmaxf(top, a);  // false for NaN and infinity
+        for (int j = 0; j < kGroup; ++j) {
+            if (g0 + j * rp >= n) break;
+            if (turn) {
+                float x[8];
+                turned(g0 + j * rp + r, u[j], x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float a = fabsf(x[i]);
+                    if (a <= 3.402823466e38f) top = fmaxf(top, a);  // false for NaN and infinity
+                }
+            } else {
+                top_bits<ACT>(u[j], tops);
+            }
         }
     }
+    if (!turn) top = act_to_float<ACT>(static_cast<uint16_t>(max(tops & 0xffffu, tops >> 16)));
     top = warp_max(top);
     // top = 1.m * 2^e: 448 = 1.75 * 2^8
     int e = kScaleMinExp;
@@ -313,8 +360,6 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
         e = min(kScaleMaxExp, max(kScaleMinExp, e));
     }
     const float need = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-    float* scale = (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + head;
-    const float old = off0 == 0 ? 0.f : *scale;
     const float now = old > need ? old : need;  // a scale that is not positive counts as none
     uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
                     (blk * p.num_kv_heads + head) * p.block_size * p.head_dim;
@@ -336,95 +381,144 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
             }
         }
     }
-    for (int i0 = 0; i0 < n; i0 += rp) {
-        float x[8];
-        const int i = i0 + r;
-        if (!load(i, x)) continue;
-        divide8(x, now);
-        *reinterpret_cast<uint2*>(tile + (off0 + i) * p.head_dim + c * 8) = to_codes(x);
+    for (int g0 = 0; g0 < n; g0 += kGroup * rp) {
+        if (n > kGroup * rp) load(g0);
+#pragma unroll
+        for (int j = 0; j < kGroup; ++j) {
+            if (g0 + j * rp >= n) break;
+            const int i = g0 + j * rp + r;
+            float x[8];
+            if (turn) turned(i, u[j], x);
+            else Vec16<ACT>::to_float(u[j], x);
+            if (r >= rp || i >= n) continue;
+            divide8(x, now);
+            *reinterpret_cast<uint2*>(tile + (off0 + i) * p.head_dim + c * 8) = to_codes(x);
+        }
     }
 }
 
-// Grid: the first kv_ctas * kv_windows blocks (block-scaled cache only) take
-// the runs that start in a window of kWindow tokens, kv_ctas blocks a window;
-// the others take (token, part of its rows) items, one a warp.
-template <int ACT, int CACHE>
-__global__ void __launch_bounds__(kWarps * 32)
-    rope_append_kernel(const RopeAppendParams p, int kv_windows, int kv_ctas, int parts, int per, int rows) {
+// Grid: the first kv_windows * kv_split blocks (block-scaled cache only) take
+// the runs that start in a window of `window` <= 32 tokens, kv_split blocks
+// sharing the (head, K or V) items of each run; the others take (token, part of
+// its rows) items, one a warp.  cos and sin of a block's tokens are computed
+// once into shared memory.
+template <int ACT, int CACHE, int PAIRS>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+    rope_append_kernel(const RopeAppendParams p, int window, int kv_windows, int kv_split, int parts, int per, int rows) {
+    __shared__ float2 table[kTable];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int half = p.rotary_dim / 2;
     int cta = blockIdx.x;
     if constexpr (CACHE == kE4M3B) {
-        if (cta < kv_windows * kv_ctas) {
-            const int w = cta / kv_ctas;
-            const int t = w * kWindow + lane;
+        if (cta < kv_windows * kv_split) {
+            const int w = cta / kv_split, part = cta - w * kv_split;
+            const int t = w * window + lane;
             bool bad = false, unused = false;
-            const int64_t slot = slot_of(p, t, &bad);
+            const int64_t slot = lane < window ? slot_of(p, t, &bad) : -1;
             const int64_t prev = slot_of(p, t - 1, &unused);
-            if (bad && warp == 0 && cta == w * kv_ctas) atomicOr(p.err, kErrBadSlot);
-            bool first = slot >= 0;
-            if (first && prev == slot - 1) {
-                int64_t blk;
-                int off;
-                divmod_u(slot, p.block_size, blk, off);
-                first = off == 0;
-            }
-            const unsigned leaders = __ballot_sync(0xffffffffu, first);
-            const int items = __popc(leaders) * p.num_kv_heads * 2;
-            for (int it = (cta - w * kv_ctas) * kWarps + warp; it < items; it += kv_ctas * kWarps) {
-                const int run = it / (p.num_kv_heads * 2), hv = it - run * p.num_kv_heads * 2;
-                const int at = __fns(leaders, 0, run + 1);
-                scaled_run<ACT>(p, w * kWindow + at, __shfl_sync(0xffffffffu, slot, at), hv >> 1, !(hv & 1));
+            if (bad && warp == 0 && part == 0) atomicOr(p.err, kErrBadSlot);
+            int64_t blk = 0;
+            int off = 0;
+            if (slot >= 0) divmod_u(slot, p.block_size, blk, off);
+            unsigned leaders = __ballot_sync(0xffffffffu, slot >= 0 && (prev != slot - 1 || off == 0));
+            for (; leaders; leaders &= leaders - 1) {
+                const int at = __ffs(leaders) - 1;
+                const int t0 = w * window + at;
+                const int64_t s0 = __shfl_sync(0xffffffffu, slot, at), b0 = __shfl_sync(0xffffffffu, blk, at);
+                const int off0 = __shfl_sync(0xffffffffu, off, at);
+                // the run's length: up to the end of the block
+                int n = 1;
+                for (int base = 1; base < p.block_size - off0; base += 32) {
+                    const int k = base + lane;
+                    const bool in = k < p.block_size - off0 && slot_of(p, t0 + k, &unused) == s0 + k;
+                    const unsigned out = __ballot_sync(0xffffffffu, !in);
+                    n = base + (out ? __ffs(out) - 1 : 32);
+                    if (out) break;
+                }
+                int tabled = 0;
+                if (p.positions) {
+                    tabled = min(n, kTable / half);
+                    __syncthreads();  // the run before is done with the table
+                    for (int i = threadIdx.x; i < tabled * half; i += kWarps * 32) {
+                        const int k = i / half;
+                        table[i] = cos_sin_at(p, i - k * half, p.positions[t0 + k]);
+                    }
+                    __syncthreads();
+                }
+                for (int it = part * kWarps + warp; it < 2 * p.num_kv_heads; it += kv_split * kWarps) {
+                    const bool is_k = it < p.num_kv_heads;
+                    scaled_run<ACT, PAIRS>(p, t0, n, b0, off0, is_k ? it : it - p.num_kv_heads, is_k, table, tabled);
+                }
             }
             return;
         }
-        cta -= kv_windows * kv_ctas;
+        cta -= kv_windows * kv_split;
     }
-    const int64_t item = static_cast<int64_t>(cta) * kWarps + warp;
-    const int token = static_cast<int>(item / parts);
-    if (token >= p.num_tokens) return;
-    const int row0 = static_cast<int>(item - static_cast<int64_t>(token) * parts) * per;
-    plain_rows<ACT, CACHE>(p, token, row0, min(rows, row0 + per));
+    // (token, part) items of this block's warps: at most kWarps tokens
+    const int64_t item0 = static_cast<int64_t>(cta) * kWarps;
+    int64_t token0, token;
+    int unused, part;
+    divmod_u(item0, parts, token0, unused);
+    divmod_u(item0 + warp, parts, token, part);
+    int64_t last;
+    divmod_u(item0 + kWarps - 1, parts, last, unused);
+    const int tokens = static_cast<int>(min(last, static_cast<int64_t>(p.num_tokens) - 1) - token0) + 1;
+    for (int i = threadIdx.x; i < tokens * half; i += kWarps * 32) {
+        const int k = i / half;
+        table[i] = cos_sin_at(p, i - k * half, p.positions[token0 + k]);
+    }
+    __syncthreads();
+    if (token >= p.num_tokens || p.positions[token] < 0) return;  // padding: q_out keeps its row
+    plain_rows<ACT, CACHE, PAIRS>(p, static_cast<int>(token), part * per, min(rows, part * per + per),
+                                  table + static_cast<int>(token - token0) * half);
 }
 
-template <int ACT, int CACHE>
+template <int ACT, int CACHE, int PAIRS>
 cudaError_t launch(const RopeAppendParams& p, cudaStream_t stream) {
+    static_assert(kWarps * 128 <= kTable, "a block's tokens fit the table at rotary_dim 256");
+    constexpr int kFill = 152 * 4;  // blocks that keep the GPU busy
     const int rp = 32 / (p.head_dim / 8);
-    int kv_windows = 0, kv_ctas = 0;
+    int window = 32, kv_windows = 0, kv_split = 1;
     if (CACHE == kE4M3B) {
-        kv_windows = (p.num_tokens + kWindow - 1) / kWindow;
-        // few windows (a decode step): one warp an item, every token a run
-        const int64_t items = static_cast<int64_t>(kWindow) * p.num_kv_heads * 2;
-        const int64_t want = 152 * 8 / kv_windows + 1;
-        const int64_t most = (items + kWarps - 1) / kWarps;
-        kv_ctas = static_cast<int>(want < most ? want : most);
+        // prompts: a window starts a run or a few, whose heads one block works off; few tokens: one token a window
+        while (window > 1 && (p.num_tokens + window - 1) / window < kFill) window /= 2;
+        kv_windows = (p.num_tokens + window - 1) / window;
+        const int most = (2 * p.num_kv_heads + kWarps - 1) / kWarps;
+        while (kv_split < most && kv_windows * kv_split < kFill) ++kv_split;
     }
     const int rows = p.positions == nullptr ? 0 : CACHE == kE4M3B ? p.num_q_heads : p.num_q_heads + 2 * p.num_kv_heads;
     // rows of a token per warp: all of them when the tokens alone fill the GPU
     const int passes = (rows + rp - 1) / rp;
     int split = 1;
-    while (split < passes && static_cast<int64_t>(p.num_tokens) * split < 152 * 16) split *= 2;
+    while (split < passes && static_cast<int64_t>(p.num_tokens) * split < kFill * kWarps) split *= 2;
     const int per = rows ? (passes + split - 1) / split * rp : 1;
-    const int parts = rows ? (rows + per - 1) / per : 0;
-    const int64_t plain = (static_cast<int64_t>(p.num_tokens) * parts + kWarps - 1) / kWarps;
-    const int64_t grid = static_cast<int64_t>(kv_windows) * kv_ctas + plain;
+    const int parts = rows ? (rows + per - 1) / per : 1;
+    const int64_t plain = rows ? (static_cast<int64_t>(p.num_tokens) * parts + kWarps - 1) / kWarps : 0;
+    const int64_t grid = static_cast<int64_t>(kv_windows) * kv_split + plain;
     if (grid <= 0) return cudaSuccess;
     if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    rope_append_kernel<ACT, CACHE><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(
-        p, kv_windows, kv_ctas, parts > 0 ? parts : 1, per, rows);
+    rope_append_kernel<ACT, CACHE, PAIRS><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(
+        p, window, kv_windows, kv_split, parts, per, rows);
     return cudaGetLastError();
+}
+
+template <int ACT, int CACHE>
+cudaError_t by_pairs(const RopeAppendParams& p, cudaStream_t s) {
+    if (p.positions == nullptr || p.interleaved) return launch<ACT, CACHE, kPairsNext>(p, s);
+    return p.rotary_dim % 16 == 0 ? launch<ACT, CACHE, kPairsChunks>(p, s) : launch<ACT, CACHE, kPairsApart>(p, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rope_append(const RopeAppendParams& p, int act, int cache, cudaStream_t s) {
     if (act == kF16)
-        return cache == kF16     ? launch<kF16, kF16>(p, s)
-               : cache == kE4M3  ? launch<kF16, kE4M3>(p, s)
-               : cache == kE4M3B ? launch<kF16, kE4M3B>(p, s)
+        return cache == kF16     ? by_pairs<kF16, kF16>(p, s)
+               : cache == kE4M3  ? by_pairs<kF16, kE4M3>(p, s)
+               : cache == kE4M3B ? by_pairs<kF16, kE4M3B>(p, s)
                                  : cudaErrorInvalidValue;
-    return cache == kBF16    ? launch<kBF16, kBF16>(p, s)
-           : cache == kE4M3  ? launch<kBF16, kE4M3>(p, s)
-           : cache == kE4M3B ? launch<kBF16, kE4M3B>(p, s)
+    return cache == kBF16    ? by_pairs<kBF16, kBF16>(p, s)
+           : cache == kE4M3  ? by_pairs<kBF16, kE4M3>(p, s)
+           : cache == kE4M3B ? by_pairs<kBF16, kE4M3B>(p, s)
                              : cudaErrorInvalidValue;
 }
 
