@@ -54,6 +54,17 @@
 // fills all 16 rows; O = V^T P is right on dimensions 0-63 in columns 0-7 and
 // on 64-127 in columns 8-15, the only ones read.  The K/V bytes per item and
 // the MMA shapes are those of head_dim 128.
+// head_dim 64 over a block-scaled E4M3 cache (HALF): a 128-byte row of the
+// tile holds two tokens of one kv head, 2r and 2r+1, so a 16 KB stage is 256
+// tokens and every operand keeps the head_dim-128 layout.  Each tile is two
+// "virtual" ones: S of the even tokens is one product over bytes 0-63 of the
+// rows, S of the odd tokens another over bytes 64-127, each into 16 columns of
+// its own.  O = V^T P is right for the even tokens on lanes 0-63 (their
+// dimensions) and for the odd ones on lanes 64-127, again in 16 columns each;
+// the epilogue adds the two halves through shared memory.  Half of both
+// products is not used, which costs nothing (the tensor pipe is a few percent
+// busy); no pairs of heads are needed.  A partition's 512 tokens are two
+// stages each of K and V.
 // Block-scaled E4M3 cache: the scheduler reads each block's K and V scale with
 // its table entry and passes both through the queue.  S rows are tokens, so
 // the softmax thread of a token multiplies its scores by one K scale and its
@@ -82,14 +93,13 @@ constexpr int kTcStage = 2 * kTcHalf;         // 32 KB
 constexpr int kTcStage8 = kTcTile * kTcD;     // E4M3 cache: 128 tokens x 128 one-byte codes, 16 KB
 constexpr int kTcQBuf = 3 * 1024;             // Q: two 8-row halves + 1 KB that rows 8-15 of half 1 alias
 constexpr int kTcPBuf = (2 * kTcMaxTiles + 1) * 1024;  // P: tile x token-half 8-row regions + alias pad
-constexpr int kTcSlotCols = kTcMaxTiles * kTcN + kTcN;  // S (4 x 16) + O (16) per buffer
-constexpr int kTcTmemCols = 256;              // two buffers of 80 columns, rounded to a power of 2
+constexpr int kTcTmemCols = 256;              // two buffers of S (4 x 16 columns) + O (16, or 32), rounded to a power of 2
 constexpr int kTcMaxSeqs = 2048;              // sequences served (lengths and item prefix in shared memory)
 constexpr int kTcSmemPerSm = 228 * 1024;      // shared memory of one SM, including the 1 KB each CTA reserves
 constexpr int kTcQueue = 2;                   // claimed items in flight between the roles
 constexpr int kTcLenBuckets = 8;              // length buckets of the partly filled partitions
 
-template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false>
+template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false, bool HALF = false>
 struct TcSmem {
     static constexpr int RING = 0;
     static constexpr int Q = NS * STG;
@@ -109,8 +119,9 @@ struct TcSmem {
     // item_full[kTcQueue], item_empty[kTcQueue] (a single Q or P buffer uses entry 0 of its pair)
     static constexpr int NBARS = 2 * NS + 13 + 2 * kTcQueue;
     static constexpr int RED = BARS + NBARS * 8;
-    // red_max[4][8], red_sum[4][8], stats[2][2][2][8]; SCALED: red_max2[4][8], pscale[2][8]
-    static constexpr int RED_FLOATS = 64 + 64 + (SCALED ? 48 : 0);
+    // red_max[4][8], red_sum[4][8], stats[2][2][2][8]; SCALED: red_max2[4][8], pscale[2][8];
+    // HALF: the odd tokens' half of O, [8][64]
+    static constexpr int RED_FLOATS = 64 + 64 + (SCALED ? 48 : 0) + (HALF ? 512 : 0);
     static constexpr int MISC = RED + RED_FLOATS * 4;
     // per row: length (int), item prefix (int, rows + 2 entries), length order (uint16)
     static constexpr int ROWS = (MISC + 16 + 15) / 16 * 16;
@@ -138,6 +149,7 @@ __device__ __forceinline__ int tc_rows(const DecodeParams& p) {
 // partly filled last partitions of the rows listed in `order`, H per row
 // (H = the item heads a row covers: its kv heads, or at head_dim 64 the pairs
 // of kv heads, when it.kvh is the pair's index).
+template <int TILE>  // tokens per tile
 __device__ __forceinline__ void tc_decode_item(int ci, const DecodeParams& p, const int* lens, const int* prefix,
                                                const uint16_t* order, int H, TcItem& it) {
     const int rows = tc_rows(p);
@@ -174,7 +186,7 @@ __device__ __forceinline__ void tc_decode_item(int ci, const DecodeParams& p, co
     it.part = part;
     it.tok_begin = part * p.partition_size;
     it.n_tok = min(p.partition_size, L - it.tok_begin);
-    it.n_tiles = (it.n_tok + kTcTile - 1) / kTcTile;
+    it.n_tiles = (it.n_tok + TILE - 1) / TILE;
 }
 
 // Bounded wait that also gives up when another role has aborted.
@@ -228,7 +240,7 @@ __device__ __forceinline__ void split3_e4m3x2(float x0, float x1, uint32_t& hi, 
     split_e4m3x2(x0 - hv.x, x1 - hv.y, mid, lo);
 }
 
-template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR = false>
+template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR = false, bool HALF = false>
 __global__ void __launch_bounds__(kTcThreads, 2)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const __grid_constant__ CUtensorMap qmap, const DecodeParams p) {
@@ -237,11 +249,17 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     constexpr int STG = FP8 ? kTcStage8 : kTcStage;  // bytes of one ring stage
     // PAIR: head_dim 64, kv heads 2v and 2v+1 of a sequence in one item, as
     // dimensions 0-63 and 64-127 of a 128-wide head (tile halves, Q regions)
-    constexpr int HD = PAIR ? 64 : kTcD;  // head_dim of the caches, queries and output
+    constexpr int HD = PAIR || HALF ? 64 : kTcD;  // head_dim of the caches, queries and output
     static_assert(!PAIR || !FP8, "pairs of head_dim-64 kv heads: 16-bit caches");
-    using S = TcSmem<NS, STG, PAIR, SCALED>;
+    static_assert(!HALF || SCALED, "two tokens a row: block-scaled E4M3 caches");
+    using S = TcSmem<NS, STG, PAIR, SCALED, HALF>;
     constexpr int THREADS = kTcThreads;
-    constexpr int BPT = kTcTile / BS;  // blocks per tile
+    constexpr int TPR = HALF ? 2 : 1;         // tokens per tile row
+    constexpr int TILE = kTcTile * TPR;       // tokens per tile
+    constexpr int BPT = TILE / BS;            // blocks per tile
+    constexpr int O_COL = kTcMaxTiles * kTcN;  // first O column of a buffer (HALF: 16 more for the odd tokens)
+    constexpr int SLOT_COLS = O_COL + TPR * kTcN;
+    static_assert(2 * SLOT_COLS <= kTcTmemCols, "tensor memory of two buffers");
     // E4M3 x E4M3 (kind::f8f6f4) has the same descriptor bits as binary16 x binary16
     constexpr uint32_t IDESC_S = tc::idesc_f16(128, kTcN, !FP8 && ACT == kBF16, false, false);
     // E4M3: P is the B operand in the MN-major layout without swizzle (a token's
@@ -282,6 +300,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     float* stats = red_max + 64;  // [buffer][kv head of a pair][max, sum][8]
     [[maybe_unused]] float* red_max2 = stats + 64;   // [4][8]: max of score + log2 |V scale|
     [[maybe_unused]] float* pscale = red_max2 + 32;  // [buffer][8]: 1 / the power of two that P was scaled by
+    [[maybe_unused]] float* o_odd = pscale + 16;     // HALF: [head][dimension] of the odd tokens
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(sm + S::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 4);
 
@@ -434,13 +453,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         bool good = true;
         if (lane == 0) {
             if (use >= NS) good = tc_wait(&empty[s], ((use / NS) - 1) & 1, abort_flag, p.err);
-            if (good) mbar_arrive_expect_tx(&full[s], __popc(loads) * (BS * 128));
+            if (good) mbar_arrive_expect_tx(&full[s], __popc(loads) * (BS / TPR * 128));
         }
         good = __shfl_sync(0xffffffffu, good, 0);
         if (!good) return false;
         if (mine) {
-            const int y = (pbj * p.num_kv_heads + (PAIR ? 2 * it.kvh + half : it.kvh)) * BS;
-            tc::tma_load_2d(ring + s * STG + half * kTcHalf + j * BS * 128, map, PAIR ? 0 : half * 64, y, &full[s],
+            const int y = (pbj * p.num_kv_heads + (PAIR ? 2 * it.kvh + half : it.kvh)) * (BS / TPR);
+            tc::tma_load_2d(ring + s * STG + half * kTcHalf + j * (BS / TPR) * 128, map, PAIR ? 0 : half * 64, y, &full[s],
                             policy);
         }
         ++use;
@@ -505,15 +524,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             ci = __shfl_sync(0xffffffffu, ci, 0);
             it.qshift = 0;
             if (ci >= 0) {
-                tc_decode_item(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
+                tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
                 if constexpr (FP8) {
                     // q enters the MMA as E4M3 high and low parts of q x 2^-qshift:
                     // the exact power-of-2 scale puts its largest magnitude in
                     // [128, 256), below the E4M3 maximum of 448
                     const uint16_t* qg = static_cast<const uint16_t*>(p.q) +
-                                         (static_cast<int64_t>(it.seq) * p.num_q_heads + it.kvh * G) * kTcD;
+                                         (static_cast<int64_t>(it.seq) * p.num_q_heads + it.kvh * G) * HD;
                     float m = 0.f;
-                    for (int i = lane; i < G * kTcD / 8; i += 32) {
+                    for (int i = lane; i < G * HD / 8; i += 32) {
                         const uint4 u = *reinterpret_cast<const uint4*>(qg + i * 8);
                         const uint16_t* e = reinterpret_cast<const uint16_t*>(&u);
 #pragma unroll
@@ -597,7 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             if (ci < 0) return 0;
             // (an appended row of this item was written, and fenced for the copy
             // engine, by the scheduler before it published the item)
-            tc_decode_item(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
+            tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
             return 1;
         };
         auto issue_q = [&](const TcItem& it, int k) {
@@ -619,11 +638,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 unsigned char* qbuf_k = qbuf + qb * S::QBUF;
                 const float f = __uint_as_float(static_cast<uint32_t>(127 - it.qshift) << 23);  // 2^-qshift
                 const uint16_t* qg = static_cast<const uint16_t*>(p.q) +
-                                     (static_cast<int64_t>(it.seq) * p.num_q_heads + it.kvh * G) * kTcD;
-                for (int i = lane; i < G * kTcD / 16; i += 32) {
-                    const int g = i >> 3, c = i & 7;  // head, 16-column chunk
-                    const uint4 u0 = *reinterpret_cast<const uint4*>(qg + g * kTcD + c * 16);
-                    const uint4 u1 = *reinterpret_cast<const uint4*>(qg + g * kTcD + c * 16 + 8);
+                                     (static_cast<int64_t>(it.seq) * p.num_q_heads + it.kvh * G) * HD;
+                for (int i = lane; i < G * HD / 16; i += 32) {
+                    const int g = i / (HD / 16), c = i % (HD / 16);  // head, 16-column chunk
+                    const uint4 u0 = *reinterpret_cast<const uint4*>(qg + g * HD + c * 16);
+                    const uint4 u1 = *reinterpret_cast<const uint4*>(qg + g * HD + c * 16 + 8);
                     const uint32_t e[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
                     uint32_t hw[4], mw[4], lw[4];
 #pragma unroll
@@ -727,7 +746,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             ++nread;
             if (!good) return -1;
             if (ci < 0) return 0;
-            tc_decode_item(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
+            tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
             return 1;
         };
         auto mma_s = [&](const TcItem& it, int k) {
@@ -747,14 +766,27 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 tc::fence_after_sync();
                 if (lane == 0) {
                     const uint32_t kb = smem_addr(ring + s * STG);
-                    if constexpr (FP8) {
+                    if constexpr (HALF) {
+                        // even tokens: bytes 0-63 of the rows, odd tokens: 64-127
+#pragma unroll
+                        for (int par = 0; par < 2; ++par) {
+                            const uint32_t d = tmem + b * SLOT_COLS + (2 * t + par) * kTcN;
+#pragma unroll
+                            for (int kk = 0; kk < HD / 32; ++kk) {
+                                const uint64_t a = tc::desc_sw128(kb + par * 64 + kk * 32, 16, 1024);
+                                tc::mma_f8(d, a, tc::desc_sw128(qb + kk * 32, 16, 1024), IDESC_S, kk > 0);
+                                if constexpr (Q3)
+                                    tc::mma_f8(d, a, tc::desc_sw128(qb + 2048 + kk * 32, 16, 1024), IDESC_S, 1u);
+                            }
+                        }
+                    } else if constexpr (FP8) {
                         // K = 32 codes (32 bytes of the 128-byte row) per MMA
 #pragma unroll
                         for (int kk = 0; kk < kTcD / 32; ++kk) {
-                            tc::mma_f8(tmem + b * kTcSlotCols + t * kTcN, tc::desc_sw128(kb + kk * 32, 16, 1024),
+                            tc::mma_f8(tmem + b * SLOT_COLS + t * kTcN, tc::desc_sw128(kb + kk * 32, 16, 1024),
                                        tc::desc_sw128(qb + kk * 32, 16, 1024), IDESC_S, kk > 0);
                             if constexpr (Q3)  // + K lo^T into columns 0-7 (rows 8-15 of this operand are zero)
-                                tc::mma_f8(tmem + b * kTcSlotCols + t * kTcN, tc::desc_sw128(kb + kk * 32, 16, 1024),
+                                tc::mma_f8(tmem + b * SLOT_COLS + t * kTcN, tc::desc_sw128(kb + kk * 32, 16, 1024),
                                            tc::desc_sw128(qb + 2048 + kk * 32, 16, 1024), IDESC_S, 1u);
                         }
                     } else {
@@ -763,7 +795,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                             const uint32_t off = (kk >> 2) * kTcHalf + (kk & 3) * 32;
                             // PAIR: dimensions 64-127 read the operand 2 KB in (rows 0-7 zero)
                             const uint32_t qoff = (kk >> 2) * (PAIR ? 2048 : 1024) + (kk & 3) * 32;
-                            tc::mma_f16(tmem + b * kTcSlotCols + t * kTcN, tc::desc_sw128(kb + off, 16, 1024),
+                            tc::mma_f16(tmem + b * SLOT_COLS + t * kTcN, tc::desc_sw128(kb + off, 16, 1024),
                                         tc::desc_sw128(qb + qoff, 16, 1024), IDESC_S, kk > 0);
                         }
                     }
@@ -796,7 +828,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 good = __all_sync(0xffffffffu, tc_wait(&full[s], (use / NS) & 1, abort_flag, p.err));
                 if (!good) return false;
                 unsigned char* vb = ring + s * STG;
-                const int valid = min(kTcTile, it.n_tok - t * kTcTile);
+                const int tokens = min(TILE, it.n_tok - t * TILE);
+                const int valid = (tokens + TPR - 1) / TPR;  // rows with a token of the context
                 constexpr int KSTEP = FP8 ? 32 : 16;  // tokens per MMA
                 constexpr int CHUNKS = FP8 ? 8 : 16;  // 16-byte chunks per token row
                 const int ksteps = (valid + KSTEP - 1) / KSTEP;
@@ -810,6 +843,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         *reinterpret_cast<uint4*>(vb + (c >> 3) * kTcHalf + r * 128 + (c & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
+                }
+                // the odd half of a last row whose odd token is past the context
+                const bool zero_half = HALF && (tokens & 1);
+                if (zero_half && lane < 4)
+                    *reinterpret_cast<uint4*>(vb + (valid - 1) * 128 + (((4 + lane) ^ ((valid - 1) & 7)) * 16)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                if (zero_rows > 0 || zero_half) {
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -817,17 +857,24 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 if (lane == 0) {
                     const uint32_t vaddr = smem_addr(vb);
                     for (int j = 0; j < ksteps; ++j) {
-                        if constexpr (FP8) {
+                        if constexpr (HALF) {
+#pragma unroll
+                            for (int par = 0; par < 2; ++par)
+                                tc::mma_f8(tmem + b * SLOT_COLS + O_COL + par * kTcN,
+                                           tc::desc_sw128(vaddr + j * 4096, kTcStage8, 1024),
+                                           tc::desc_noswizzle(pbase + (2 * t + par) * 2048 + j * 512, 128, 2048), IDESC_O,
+                                           (t > 0 || j > 0) ? 1u : 0u);
+                        } else if constexpr (FP8) {
                             // A = V^T: the 128 codes of a token are one 128-byte row, so
                             // M = 128 is a single swizzle atom; 32 tokens = 4 KB per step
                             // B = P: core matrices of 8 tokens x 16 bytes, 128 B apart
-                            tc::mma_f8(tmem + b * kTcSlotCols + kTcMaxTiles * kTcN,
+                            tc::mma_f8(tmem + b * SLOT_COLS + O_COL,
                                        tc::desc_sw128(vaddr + j * 4096, kTcStage8, 1024),
                                        tc::desc_noswizzle(pbase + t * 2048 + j * 512, 128, 2048), IDESC_O,
                                        (t > 0 || j > 0) ? 1u : 0u);
                         } else {
                             const uint32_t poff = (2 * t + (j >> 2)) * (PAIR ? 2048 : 1024) + (j & 3) * 32;
-                            tc::mma_f16(tmem + b * kTcSlotCols + kTcMaxTiles * kTcN,
+                            tc::mma_f16(tmem + b * SLOT_COLS + O_COL,
                                         tc::desc_sw128(vaddr + j * 2048, kTcHalf, 1024),
                                         tc::desc_sw128(pbase + poff, 16, 1024), IDESC_O, (t > 0 || j > 0) ? 1u : 0u);
                         }
@@ -867,6 +914,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         const int tid = threadIdx.x - 64;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         int nread = 0;
+        // token of this thread's row in (virtual) tile t
+        auto token_of = [&](int t) { return HALF ? (t >> 1) * TILE + 2 * row + (t & 1) : t * kTcTile + row; };
         // block-scaled: the scales of this thread's tokens in the item read last
         [[maybe_unused]] float ks_t[kTcMaxTiles], vs_t[kTcMaxTiles];
 
@@ -882,7 +931,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             if constexpr (SCALED) {
 #pragma unroll
                 for (int t = 0; t < kTcMaxTiles; ++t) {
-                    const int i = slot * 64 + (t * kTcTile + row) / BS;
+                    const int i = slot * 64 + token_of(t) / BS;
                     ks_t[t] = item_scales[i];
                     vs_t[t] = item_scales[i + 32];
                 }
@@ -891,7 +940,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             if (named_bar_or(3, 128, !good)) return -1;
             if (tid == 0) mbar_arrive(&item_empty[slot]);
             if (ci < 0) return 0;
-            tc_decode_item(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
+            tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
             it.qshift = qshift;
             return 1;
         };
@@ -909,6 +958,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                        __uint_as_float(static_cast<uint32_t>(127 + it.qshift) << 23)
                                  : p.scale_log2;
             unsigned char* pb = pbuf + (S::PBUFS == 2 ? b * S::PBUF : 0);
+            const int n_tiles = TPR * it.n_tiles;  // HALF: virtual ones
             // PAIR: columns 0-7 (kv head 2v) and 8-15 (kv head 2v+1) in two
             // passes over the same scores, each as the single-head case
             constexpr int NH = PAIR ? 2 : 1;
@@ -922,9 +972,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         float lo[kTcMaxTiles][G] = {};
 #pragma unroll
                         for (int t = 0; t < kTcMaxTiles; ++t)
-                            if (t < it.n_tiles) {
-                                tc::TmemLd<G>::load(lane_addr + b * kTcSlotCols + t * kTcN, sc[t]);
-                                tc::TmemLd<G>::load(lane_addr + b * kTcSlotCols + t * kTcN + 8, lo[t]);
+                            if (t < n_tiles) {
+                                tc::TmemLd<G>::load(lane_addr + b * SLOT_COLS + t * kTcN, sc[t]);
+                                tc::TmemLd<G>::load(lane_addr + b * SLOT_COLS + t * kTcN + 8, lo[t]);
                             }
                         tc::tmem_wait_ld();
 #pragma unroll
@@ -934,8 +984,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     } else {
 #pragma unroll
                         for (int t = 0; t < kTcMaxTiles; ++t)
-                            if (t < it.n_tiles)
-                                tc::TmemLd<G>::load(lane_addr + b * kTcSlotCols + t * kTcN + hh * 8, sc[t]);
+                            if (t < n_tiles)
+                                tc::TmemLd<G>::load(lane_addr + b * SLOT_COLS + t * kTcN + hh * 8, sc[t]);
                         tc::tmem_wait_ld();
                     }
                     tc::fence_before_sync();  // these reads precede the next MMA into this S buffer
@@ -945,7 +995,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     for (int g = 0; g < G; ++g) mx[g] = mx2[g] = -INFINITY;
 #pragma unroll
                     for (int t = 0; t < kTcMaxTiles; ++t) {
-                        const bool valid = t < it.n_tiles && t * kTcTile + row < it.n_tok;
+                        const bool valid = t < n_tiles && token_of(t) < it.n_tok;
 #pragma unroll
                         for (int g = 0; g < G; ++g) {
                             sc[t][g] = valid ? sc[t][g] * (SCALED ? sl * ks_t[t] : sl) : -INFINITY;
@@ -982,7 +1032,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 }
 #pragma unroll
                 for (int t = 0; t < kTcMaxTiles; ++t) {
-                    if (t < it.n_tiles) {
+                    if (t < n_tiles) {
                         if constexpr (FP8) {
                             // P x 2^8 (at most 256) = hi + lo in E4M3; token `row` of
                             // tile t holds 16 bytes: hi of heads 0-7, then lo of heads 0-7
@@ -1050,10 +1100,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const int hh = PAIR ? (q4 >> 1) : 0;
             if (good) {
                 tc::fence_after_sync();
-                tc::TmemLd<G>::load(lane_addr + b * kTcSlotCols + kTcMaxTiles * kTcN + hh * 8, o);
+                // HALF: lanes 64-127 hold the odd tokens' product
+                const uint32_t o_addr = lane_addr + b * SLOT_COLS + O_COL + (HALF ? (q4 >> 1) * kTcN : 0);
+                tc::TmemLd<G>::load(o_addr + hh * 8, o);
                 if constexpr (FP8) {
                     float lo[G];  // O of the low parts of P
-                    tc::TmemLd<G>::load(lane_addr + b * kTcSlotCols + kTcMaxTiles * kTcN + 8, lo);
+                    tc::TmemLd<G>::load(o_addr + 8, lo);
                     tc::tmem_wait_ld();
 #pragma unroll
                     for (int g = 0; g < G; ++g) o[g] += lo[g];
@@ -1061,10 +1113,20 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     tc::tmem_wait_ld();
                 }
                 tc::fence_before_sync();
+                if (HALF && q4 >= 2) {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) o_odd[g * 64 + (row & 63)] = o[g];
+                }
             }
             // also orders the stats written by the softmax of this item before the reads below
             if (named_bar_or(1, 128, !good)) return false;
             if (tid == 0) mbar_arrive(&o_free[b]);
+            if constexpr (HALF) {
+                // the next write of o_odd comes after barriers that these reads precede
+                if (q4 >= 2) return true;
+#pragma unroll
+                for (int g = 0; g < G; ++g) o[g] += o_odd[g * 64 + row];
+            }
             const int d = PAIR ? (row & 63) : row;
             const bool single = p.max_parts == 1 || s_lens[it.row] <= p.partition_size;
             // E4M3: O was computed on the stored codes and on P x 2^8

@@ -31,7 +31,8 @@ bool make_map(CUtensorMap* m, const void* base, int act, uint64_t rows, uint32_t
 }
 
 // E4M3 cache: a [rows][128] byte matrix read in boxes of 128 bytes x
-// box_rows rows, 128-byte swizzled.
+// box_rows rows, 128-byte swizzled
+// (head_dim 64: a row is two tokens of one kv head).
 bool make_map8(CUtensorMap* m, const void* base, uint64_t rows, uint32_t box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
@@ -53,11 +54,11 @@ int sm_count() {
     return counts[dev];
 }
 
-template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR>
+template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR, bool HALF>
 cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                    int ctas_per_sm, cudaStream_t s) {
-    auto kern = paged_decode_tc_kernel<ACT, CACHE, BS, G, NS, PAIR>;
-    using Smem = TcSmem<NS, is_e4m3(CACHE) ? kTcStage8 : kTcStage, PAIR, CACHE == kE4M3B>;
+    auto kern = paged_decode_tc_kernel<ACT, CACHE, BS, G, NS, PAIR, HALF>;
+    using Smem = TcSmem<NS, is_e4m3(CACHE) ? kTcStage8 : kTcStage, PAIR, CACHE == kE4M3B, HALF>;
     constexpr int threads = kTcThreads;
     const int rows = p.table_kvh_stride != 0 ? p.num_seqs * p.num_kv_heads : p.num_seqs;
     const int smem = Smem::alloc(rows);
@@ -81,17 +82,17 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorM
     return cudaGetLastError();
 }
 
-template <int ACT, int CACHE, int NS, bool PAIR = false>
+template <int ACT, int CACHE, int NS, bool PAIR = false, bool HALF = false>
 cudaError_t by_shape(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                      int BS, int G, int ctas_per_sm, cudaStream_t s) {
     if (BS == 16) {
-        if (G == 2) return launch<ACT, CACHE, 16, 2, NS, PAIR>(p, km, vm, qm, ctas_per_sm, s);
-        if (G == 4) return launch<ACT, CACHE, 16, 4, NS, PAIR>(p, km, vm, qm, ctas_per_sm, s);
-        if (G == 8) return launch<ACT, CACHE, 16, 8, NS, PAIR>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 2) return launch<ACT, CACHE, 16, 2, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 4) return launch<ACT, CACHE, 16, 4, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 8) return launch<ACT, CACHE, 16, 8, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
     } else if (BS == 32) {
-        if (G == 2) return launch<ACT, CACHE, 32, 2, NS, PAIR>(p, km, vm, qm, ctas_per_sm, s);
-        if (G == 4) return launch<ACT, CACHE, 32, 4, NS, PAIR>(p, km, vm, qm, ctas_per_sm, s);
-        if (G == 8) return launch<ACT, CACHE, 32, 8, NS, PAIR>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 2) return launch<ACT, CACHE, 32, 2, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 4) return launch<ACT, CACHE, 32, 4, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 8) return launch<ACT, CACHE, 32, 8, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
     }
     return cudaErrorInvalidValue;
 }

@@ -248,7 +248,8 @@ int decode_tc_max_rows();  // table rows (sequences, or (sequence, kv head) pair
 cudaError_t launch_decode_tc(const DecodeParams& p, int act, int cache, int head_dim, int BS, int G, int variant,
                              cudaStream_t s);
 cudaError_t launch_decode_tc_e4m3(const DecodeParams& p, int act, int BS, int G, int variant, cudaStream_t s);
-cudaError_t launch_decode_tc_e4m3b(const DecodeParams& p, int act, int BS, int G, int variant, cudaStream_t s);
+cudaError_t launch_decode_tc_e4m3b(const DecodeParams& p, int act, int head_dim, int BS, int G, int variant,
+                                   cudaStream_t s);
 cudaError_t launch_decode_tc_d64(const DecodeParams& p, int act, int BS, int G, int variant, cudaStream_t s);
 
 }  // namespace pkv
