@@ -65,14 +65,19 @@
 // products is not used, which costs nothing (the tensor pipe is a few percent
 // busy); no pairs of heads are needed.  A partition's 512 tokens are two
 // stages each of K and V.
-// Block-scaled E4M3 cache: the scheduler reads each block's K and V scale with
-// its table entry and passes both through the queue.  S rows are tokens, so
-// the softmax thread of a token multiplies its scores by one K scale and its
-// weights by one V scale vs.  P enters the MMA as p * vs * 2^c, 2^c the power of
-// two that puts the largest p * vs of a head just below 2^8 (from the maximum
-// of score + log2 |vs|, taken along with the maximum score), so that the two
-// E4M3 parts keep their precision for the tokens that matter, whatever the
-// scales of the others; the epilogue takes 2^c out again.
+// Block-scaled E4M3 cache (SCALED).  The scheduler reads each block's K and V
+// scale with its table entry and passes through the queue, next to the item
+// itself (seq, kv head, partition, tokens: the other roles do not search for
+// it again), ks, vs * 2^-ev and log2 |vs| - ev of the item's blocks, 2^ev the power
+// of two at or above its largest |vs|.  S rows are tokens, so the softmax
+// thread of a token multiplies its scores by one ks, and its weights by one vs.
+// Weights are relative to R = max(score + log2 |vs| - ev) of the item and head
+// instead of the maximum score: w = 2^(score - R) * vs * 2^(8 - ev) is at most 2^8
+// and reaches it for the token that matters most, so the two E4M3 parts of w
+// keep their precision whatever the scales of the other blocks are.  The sum
+// of 2^(score - R) is the denominator; log2 |vs| - ev enters R at no less than
+// -100, which keeps it finite (and a row without any V scale but 0 defined).
+// The producer that converts q finds its power-of-2 scale too.
 // Every barrier wait is bounded (kWaitLimitNs); on a timeout the CTA stops
 // issuing work, drains its in-flight copies and MMAs, frees tensor memory and
 // reports kErrTimeout.
@@ -99,6 +104,10 @@ constexpr int kTcSmemPerSm = 228 * 1024;      // shared memory of one SM, includ
 constexpr int kTcQueue = 2;                   // claimed items in flight between the roles
 constexpr int kTcLenBuckets = 8;              // length buckets of the partly filled partitions
 
+// Queue entry of the block-scaled variant: TcItem fields, physical blocks [32],
+// K scales [32], V scales [32], log2 of the V scales [32].
+constexpr int kScaledEntry = 32 + 4 * 32 * 4;
+
 template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false, bool HALF = false>
 struct TcSmem {
     static constexpr int RING = 0;
@@ -112,16 +121,17 @@ struct TcSmem {
     static constexpr int P = Q + QBUFS * QBUF;
     static constexpr int PBUF = STG == kTcStage8 ? 8192 : PAIR ? 2 * kTcMaxTiles * 2048 : kTcPBuf;  // one P buffer
     static constexpr int PBUFS = STG == kTcStage8 ? 2 : 1;           // P buffers
-    // item numbers, q shifts, block-table entries [32] (and K and V scales [32] each) per entry
+    // item numbers, q shifts, block-table entries [32] per entry; SCALED: kScaledEntry bytes per entry
     static constexpr int QUEUE = P + PBUFS * PBUF;
-    static constexpr int BARS = (QUEUE + 2 * kTcQueue * 4 + (SCALED ? 3 : 1) * kTcQueue * 32 * 4 + 7) / 8 * 8;
+    static constexpr int BARS =
+        SCALED ? QUEUE + kTcQueue * kScaledEntry : (QUEUE + 2 * kTcQueue * 4 + kTcQueue * 32 * 4 + 7) / 8 * 8;
     // full[NS], empty[NS], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], final,
     // item_full[kTcQueue], item_empty[kTcQueue] (a single Q or P buffer uses entry 0 of its pair)
     static constexpr int NBARS = 2 * NS + 13 + 2 * kTcQueue;
     static constexpr int RED = BARS + NBARS * 8;
-    // red_max[4][8], red_sum[4][8], stats[2][2][2][8]; SCALED: red_max2[4][8], pscale[2][8];
+    // red_max[4][8], red_sum[4][8], stats[2][2][2][8]; SCALED: o_scale[2][8], q shifts [4] (and 4 unused);
     // HALF: the odd tokens' half of O, [8][64]
-    static constexpr int RED_FLOATS = 64 + 64 + (SCALED ? 48 : 0) + (HALF ? 512 : 0);
+    static constexpr int RED_FLOATS = 64 + 64 + (SCALED ? 24 : 0) + (HALF ? 512 : 0);
     static constexpr int MISC = RED + RED_FLOATS * 4;
     // per row: length (int), item prefix (int, rows + 2 entries), length order (uint16)
     static constexpr int ROWS = (MISC + 16 + 15) / 16 * 16;
@@ -132,6 +142,8 @@ struct TcSmem {
 struct TcItem {
     int seq, kvh, row, part, tok_begin, n_tok, n_tiles;
     int qshift;  // E4M3 cache: q enters the MMA scaled by 2^-qshift
+    int ev;      // block-scaled: 2^ev was taken out of the V scales
+    bool single; // the row's only partition (block-scaled; the others look it up)
 };
 
 // Rows: a sequence (tables shared by its kv heads) or, with per-(sequence,
@@ -281,8 +293,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     volatile int* item_q = reinterpret_cast<volatile int*>(sm + S::QUEUE);
     volatile int* item_shift = item_q + kTcQueue;
     volatile int* item_phys = item_shift + kTcQueue;  // [slot][32]: the item's physical blocks
-    // [slot][K, V][32]: the scales of those blocks
-    [[maybe_unused]] volatile float* item_scales = reinterpret_cast<volatile float*>(item_phys + kTcQueue * 32);
+    // block-scaled: the entry instead
+    auto entry_of = [&](int slot) { return sm + S::QUEUE + slot * kScaledEntry; };
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::BARS);
     uint64_t* full = bars;
     uint64_t* empty = bars + NS;
@@ -298,9 +310,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     float* red_max = reinterpret_cast<float*>(sm + S::RED);
     float* red_sum = red_max + 32;
     float* stats = red_max + 64;  // [buffer][kv head of a pair][max, sum][8]
-    [[maybe_unused]] float* red_max2 = stats + 64;   // [4][8]: max of score + log2 |V scale|
-    [[maybe_unused]] float* pscale = red_max2 + 32;  // [buffer][8]: 1 / the power of two that P was scaled by
-    [[maybe_unused]] float* o_odd = pscale + 16;     // HALF: [head][dimension] of the odd tokens
+    [[maybe_unused]] float* o_scale = stats + 64;  // block-scaled: [buffer][8], what an O column is multiplied by
+    // block-scaled: q shift of the k-th item at [k & 3] (k + 4's is found after the softmax of k + 2 has begun)
+    [[maybe_unused]] volatile int* q_shift = reinterpret_cast<volatile int*>(o_scale + 16);
+    [[maybe_unused]] float* o_odd = o_scale + 24;  // HALF: [head][dimension] of the odd tokens
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(sm + S::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 4);
 
@@ -475,6 +488,20 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         }
     };
 
+    // Block-scaled: an item as the queue holds it; false at the end of the work.
+    auto read_entry = [&](int slot, TcItem& it) {
+        const int4* e = reinterpret_cast<const int4*>(entry_of(slot));
+        const int4 a = e[0], b = e[1];
+        it.seq = a.y;
+        it.kvh = a.z;
+        it.part = a.w;
+        it.n_tok = b.x;
+        it.n_tiles = b.y;
+        it.ev = b.z;
+        it.single = b.w != 0;
+        return a.x >= 0;
+    };
+
     if (warp == 0) {
         // ------------------------------------------------------------ scheduler
         // Claims items, reads their block-table entries, performs the fused
@@ -515,7 +542,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         // at the end of the work (the end marker is queued) or on an abort.
         auto claim = [&](TcItem& it, int& phys) {
             phys = -1;
-            [[maybe_unused]] float ksc = 0.f, vsc = 0.f;
+            [[maybe_unused]] float ksc = 0.f, vsc = 0.f, lvs = -INFINITY;
             int ci = -1;
             if (lane == 0) {
                 ci = atomicAdd(p.work_counter, 1);
@@ -525,7 +552,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             it.qshift = 0;
             if (ci >= 0) {
                 tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
-                if constexpr (FP8) {
+                if constexpr (FP8 && !SCALED) {
                     // q enters the MMA as E4M3 high and low parts of q x 2^-qshift:
                     // the exact power-of-2 scale puts its largest magnitude in
                     // [128, 256), below the E4M3 maximum of 448
@@ -544,9 +571,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     it.qshift = m > 0.f ? min(120, max(-120, e - 7)) : 0;
                 }
                 phys = table_entry(it);
-                if (SCALED && phys >= 0) {
-                    ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
-                    vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
+                if constexpr (SCALED) {
+                    if (phys >= 0) {
+                        ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
+                        vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
+                    }
+                    const float top = warp_max(fabsf(vsc));
+                    const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xff) - 126;  // top < 2^e
+                    it.ev = top > 0.f ? min(126, max(-120, e)) : 0;
+                    vsc *= __uint_as_float(static_cast<uint32_t>(127 - it.ev) << 23);
+                    lvs = fmaxf(__log2f(fabsf(vsc)), -100.f);
+                    vsc *= 256.f;
+                    it.single = p.max_parts == 1 || s_lens[it.row] <= p.partition_size;
                 }
                 if (!SCALED && p.new_slots != nullptr && it.tok_begin + it.n_tok == s_lens[it.row]) {
                     // fused append: this item holds the new (last) token; write it
@@ -568,14 +604,22 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 ok = false;
                 return false;
             }
-            item_phys[slot * 32 + lane] = phys;
             if constexpr (SCALED) {
-                item_scales[slot * 64 + lane] = ksc;
-                item_scales[slot * 64 + 32 + lane] = vsc;
-            }
-            if (lane == 0) {
-                item_q[slot] = ci;
-                item_shift[slot] = it.qshift;
+                unsigned char* e = entry_of(slot);
+                reinterpret_cast<int*>(e + 32)[lane] = phys;
+                reinterpret_cast<float*>(e + 160)[lane] = ksc;
+                reinterpret_cast<float*>(e + 288)[lane] = vsc;
+                reinterpret_cast<float*>(e + 416)[lane] = lvs;
+                if (lane == 0) {
+                    reinterpret_cast<int4*>(e)[0] = make_int4(ci, it.seq, it.kvh, it.part);
+                    reinterpret_cast<int4*>(e)[1] = make_int4(it.n_tok, it.n_tiles, it.ev, it.single ? 1 : 0);
+                }
+            } else {
+                item_phys[slot * 32 + lane] = phys;
+                if (lane == 0) {
+                    item_q[slot] = ci;
+                    item_shift[slot] = it.qshift;
+                }
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_full[slot]);
@@ -608,12 +652,19 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 __all_sync(0xffffffffu, tc_wait(&item_full[slot], (nread / kTcQueue) & 1, abort_flag, p.err));
             ++nread;
             if (!good) return -1;
-            const int ci = item_q[slot];
-            it.qshift = item_shift[slot];
-            phys = item_phys[slot * 32 + lane];
+            int ci = 0;
+            if constexpr (SCALED) {
+                if (!read_entry(slot, it)) ci = -1;
+                phys = reinterpret_cast<const int*>(entry_of(slot) + 32)[lane];
+            } else {
+                ci = item_q[slot];
+                it.qshift = item_shift[slot];
+                phys = item_phys[slot * 32 + lane];
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
             if (ci < 0) return 0;
+            if constexpr (SCALED) return 1;
             // (an appended row of this item was written, and fenced for the copy
             // engine, by the scheduler before it published the item)
             tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
@@ -636,13 +687,43 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 good = __shfl_sync(0xffffffffu, good, 0);
                 if (!good) return false;
                 unsigned char* qbuf_k = qbuf + qb * S::QBUF;
-                const float f = __uint_as_float(static_cast<uint32_t>(127 - it.qshift) << 23);  // 2^-qshift
                 const uint16_t* qg = static_cast<const uint16_t*>(p.q) +
                                      (static_cast<int64_t>(it.seq) * p.num_q_heads + it.kvh * G) * HD;
-                for (int i = lane; i < G * HD / 16; i += 32) {
+                // the item's queries, 16 channels of a head each time
+                constexpr int QN = (G * HD / 16 + 31) / 32;
+                uint4 qu[QN][2];
+#pragma unroll
+                for (int n = 0; n < QN; ++n) {
+                    const int i = n * 32 + lane;
+                    if (G * HD / 16 % 32 == 0 || i < G * HD / 16) {
+                        qu[n][0] = *reinterpret_cast<const uint4*>(qg + i * 16);
+                        qu[n][1] = *reinterpret_cast<const uint4*>(qg + i * 16 + 8);
+                    } else {
+                        qu[n][0] = qu[n][1] = make_uint4(0u, 0u, 0u, 0u);
+                    }
+                }
+                int shift = it.qshift;
+                if constexpr (SCALED) {
+                    // largest magnitude in [128, 256) after the exact power-of-2 scale (see the scheduler)
+                    float m = 0.f;
+#pragma unroll
+                    for (int n = 0; n < QN; ++n) {
+                        const uint16_t* e = reinterpret_cast<const uint16_t*>(qu[n]);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(act_to_float<ACT>(e[j])));
+                    }
+                    m = warp_max(m);
+                    const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
+                    shift = m > 0.f ? min(120, max(-120, e - 7)) : 0;
+                    if (lane == 0) q_shift[k & 3] = shift;
+                }
+                const float f = __uint_as_float(static_cast<uint32_t>(127 - shift) << 23);  // 2^-shift
+#pragma unroll
+                for (int n = 0; n < QN; ++n) {
+                    const int i = n * 32 + lane;
+                    if (G * HD / 16 % 32 != 0 && i >= G * HD / 16) break;
                     const int g = i / (HD / 16), c = i % (HD / 16);  // head, 16-column chunk
-                    const uint4 u0 = *reinterpret_cast<const uint4*>(qg + g * HD + c * 16);
-                    const uint4 u1 = *reinterpret_cast<const uint4*>(qg + g * HD + c * 16 + 8);
+                    const uint4 u0 = qu[n][0], u1 = qu[n][1];
                     const uint32_t e[8] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w};
                     uint32_t hw[4], mw[4], lw[4];
 #pragma unroll
@@ -736,7 +817,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             int ci = -1;
             if (lane == 0) {
                 good = tc_wait(&item_full[slot], (nread / kTcQueue) & 1, abort_flag, p.err);
-                if (good) {
+                if constexpr (SCALED) {
+                    if (good && read_entry(slot, it)) ci = 0;
+                    if (good) mbar_arrive(&item_empty[slot]);
+                } else if (good) {
                     ci = item_q[slot];
                     mbar_arrive(&item_empty[slot]);
                 }
@@ -746,6 +830,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             ++nread;
             if (!good) return -1;
             if (ci < 0) return 0;
+            if constexpr (SCALED) {
+                it.n_tok = __shfl_sync(0xffffffffu, it.n_tok, 0);
+                it.n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
+                return 1;
+            }
             tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
             return 1;
         };
@@ -917,7 +1006,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         // token of this thread's row in (virtual) tile t
         auto token_of = [&](int t) { return HALF ? (t >> 1) * TILE + 2 * row + (t & 1) : t * kTcTile + row; };
         // block-scaled: the scales of this thread's tokens in the item read last
-        [[maybe_unused]] float ks_t[kTcMaxTiles], vs_t[kTcMaxTiles];
+        [[maybe_unused]] float ks_t[kTcMaxTiles], vs_t[kTcMaxTiles], lv_t[kTcMaxTiles];
 
         // Every wait below is followed by a barrier that all 128 threads reach;
         // a failure is OR-reduced there so that the four warps leave together
@@ -926,20 +1015,27 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const int slot = nread % kTcQueue;
             const bool good =
                 __all_sync(0xffffffffu, tc_wait(&item_full[slot], (nread / kTcQueue) & 1, abort_flag, p.err));
-            const int ci = good ? item_q[slot] : -1;
-            const int qshift = good ? item_shift[slot] : 0;
+            int ci = -1;
+            [[maybe_unused]] int qshift = 0;
             if constexpr (SCALED) {
+                if (good && read_entry(slot, it)) ci = 0;
+                const float* e = reinterpret_cast<const float*>(entry_of(slot) + 160);
 #pragma unroll
                 for (int t = 0; t < kTcMaxTiles; ++t) {
-                    const int i = slot * 64 + token_of(t) / BS;
-                    ks_t[t] = item_scales[i];
-                    vs_t[t] = item_scales[i + 32];
+                    const int i = token_of(t) / BS;
+                    ks_t[t] = e[i];
+                    vs_t[t] = e[32 + i];
+                    lv_t[t] = e[64 + i];
                 }
+            } else {
+                ci = good ? item_q[slot] : -1;
+                qshift = good ? item_shift[slot] : 0;
             }
             ++nread;
             if (named_bar_or(3, 128, !good)) return -1;
             if (tid == 0) mbar_arrive(&item_empty[slot]);
             if (ci < 0) return 0;
+            if constexpr (SCALED) return 1;
             tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
             it.qshift = qshift;
             return 1;
@@ -954,8 +1050,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                  (k == 0 || S::PBUFS == 2 ||
                                   tc_wait(&o_full[(k - 1) & 1], ((k - 1) >> 1) & 1, abort_flag, p.err)));
             // E4M3: S was computed on the stored codes and on q x 2^-qshift
+            // (q_shift: written before Q was published, so before S was complete)
+            const int qs = SCALED ? q_shift[k & 3] : it.qshift;
             const float sl = FP8 ? p.scale_log2 * (SCALED ? 1.f : *p.k_scale) *
-                                       __uint_as_float(static_cast<uint32_t>(127 + it.qshift) << 23)
+                                       __uint_as_float(static_cast<uint32_t>(127 + qs) << 23)
                                  : p.scale_log2;
             unsigned char* pb = pbuf + (S::PBUFS == 2 ? b * S::PBUF : 0);
             const int n_tiles = TPR * it.n_tiles;  // HALF: virtual ones
@@ -990,45 +1088,30 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     }
                     tc::fence_before_sync();  // these reads precede the next MMA into this S buffer
                     float mx[G];
-                    [[maybe_unused]] float mx2[G];
 #pragma unroll
-                    for (int g = 0; g < G; ++g) mx[g] = mx2[g] = -INFINITY;
+                    for (int g = 0; g < G; ++g) mx[g] = -INFINITY;
 #pragma unroll
                     for (int t = 0; t < kTcMaxTiles; ++t) {
                         const bool valid = t < n_tiles && token_of(t) < it.n_tok;
 #pragma unroll
                         for (int g = 0; g < G; ++g) {
                             sc[t][g] = valid ? sc[t][g] * (SCALED ? sl * ks_t[t] : sl) : -INFINITY;
-                            mx[g] = fmaxf(mx[g], sc[t][g]);
-                            if constexpr (SCALED) mx2[g] = fmaxf(mx2[g], sc[t][g] + __log2f(fabsf(vs_t[t])));
+                            mx[g] = fmaxf(mx[g], SCALED ? sc[t][g] + lv_t[t] : sc[t][g]);
                         }
                     }
 #pragma unroll
-                    for (int g = 0; g < G; ++g) {
-                        mx[g] = warp_max(mx[g]);
-                        if constexpr (SCALED) mx2[g] = warp_max(mx2[g]);
-                    }
+                    for (int g = 0; g < G; ++g) mx[g] = warp_max(mx[g]);
                     if (lane == 0) {
 #pragma unroll
-                        for (int g = 0; g < G; ++g) {
-                            red_max[q4 * 8 + g] = mx[g];
-                            if constexpr (SCALED) red_max2[q4 * 8 + g] = mx2[g];
-                        }
+                        for (int g = 0; g < G; ++g) red_max[q4 * 8 + g] = mx[g];
                     }
                 }
                 if (named_bar_or(1, 128, !good)) return false;
                 float M[G], sum[G];
-                [[maybe_unused]] float pc[G];  // weights enter the MMA as p * vs * pc
 #pragma unroll
                 for (int g = 0; g < G; ++g) {
                     M[g] = fmaxf(fmaxf(red_max[g], red_max[8 + g]), fmaxf(red_max[16 + g], red_max[24 + g]));
                     sum[g] = 0.f;
-                    if constexpr (SCALED) {
-                        const float m2 = fmaxf(fmaxf(red_max2[g], red_max2[8 + g]), fmaxf(red_max2[16 + g], red_max2[24 + g]));
-                        // every V scale 0: any factor will do
-                        const int c = static_cast<int>(fminf(100.f, fmaxf(-100.f, floorf(M[g] - m2))));
-                        pc[g] = __uint_as_float(static_cast<uint32_t>(c + 8 + 127) << 23);
-                    }
                 }
 #pragma unroll
                 for (int t = 0; t < kTcMaxTiles; ++t) {
@@ -1045,8 +1128,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                 sum[g] += p0;
                                 sum[g + 1] += p1;
                                 uint32_t hi, lo;
-                                if constexpr (SCALED) split_e4m3x2(p0 * (vs_t[t] * pc[g]), p1 * (vs_t[t] * pc[g + 1]), hi, lo);
-                                else split_e4m3x2(p0 * 256.f, p1 * 256.f, hi, lo);
+                                const float pm = SCALED ? vs_t[t] : 256.f;  // vs_t: times 2^(8 - ev)
+                                split_e4m3x2(p0 * pm, p1 * pm, hi, lo);
                                 w[g >> 2] |= hi << (8 * (g & 3));
                                 w[2 + (g >> 2)] |= lo << (8 * (g & 3));
                             }
@@ -1066,25 +1149,55 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         }
                     }
                 }
+                if constexpr (SCALED) {
+                    // the heads' sums over the warp, halving the heads a lane
+                    // carries at each step: lane l ends with head l / (32 / G)
+                    constexpr int SPREAD = 32 / G;
 #pragma unroll
-                for (int g = 0; g < G; ++g) {
+                    for (int n = G, off = 16; n > 1; n >>= 1, off >>= 1) {
 #pragma unroll
-                    for (int off = 16; off >= 1; off >>= 1) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
-                }
-                if (lane == 0) {
+                        for (int g = 0; g < n / 2; ++g) {
+                            const bool up = lane & off;
+                            const float mine = up ? sum[g + n / 2] : sum[g], other = up ? sum[g] : sum[g + n / 2];
+                            sum[g] = mine + __shfl_xor_sync(0xffffffffu, other, off);
+                        }
+                    }
 #pragma unroll
-                    for (int g = 0; g < G; ++g) red_sum[q4 * 8 + g] = sum[g];
+                    for (int off = SPREAD / 2; off >= 1; off >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
+                    if (lane % SPREAD == 0) red_sum[q4 * 8 + lane / SPREAD] = sum[0];
+                } else {
+#pragma unroll
+                    for (int g = 0; g < G; ++g) {
+#pragma unroll
+                        for (int off = 16; off >= 1; off >>= 1) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
+                    }
+                    if (lane == 0) {
+#pragma unroll
+                        for (int g = 0; g < G; ++g) red_sum[q4 * 8 + g] = sum[g];
+                    }
                 }
                 if (hh == NH - 1) tc::fence_proxy_async_smem();
                 asm volatile("bar.sync 2, 128;" ::: "memory");
-                if (tid == 0) {
+                if constexpr (SCALED) {
+                    if (tid == 0) mbar_arrive(&p_full[b]);
+                    if (tid < G) {  // a head each: its statistics, and what its O column is multiplied by
+                        const float m = fmaxf(fmaxf(red_max[tid], red_max[8 + tid]),
+                                              fmaxf(red_max[16 + tid], red_max[24 + tid]));
+                        const float L = red_sum[tid] + red_sum[8 + tid] + red_sum[16 + tid] + red_sum[24 + tid];
+                        // 2^(ev - 8) / L; every V scale 0: 0 / L
+                        o_scale[b * 8 + tid] = __fdiv_rn(__uint_as_float(static_cast<uint32_t>(it.ev - 8 + 135) << 23), L) *
+                                               0x1p-8f;
+                        if (!it.single) {
+                            const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G + tid;
+                            *reinterpret_cast<float2*>(p.ws_ml + (hrow * p.max_parts + it.part) * 2) = make_float2(m, L);
+                        }
+                    }
+                } else if (tid == 0) {
                     float* st = stats + (b * 2 + hh) * 16;
 #pragma unroll
                     for (int g = 0; g < G; ++g) {
                         st[g] = M[g];
                         st[8 + g] = red_sum[g] + red_sum[8 + g] + red_sum[16 + g] + red_sum[24 + g];
-                        if constexpr (SCALED)  // 1 / pc, exact
-                            pscale[b * 8 + g] = __uint_as_float((254u << 23) - __float_as_uint(pc[g]));
                     }
                     if (hh == NH - 1) mbar_arrive(&p_full[S::PBUFS == 2 ? b : 0]);
                 }
@@ -1127,16 +1240,30 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
                 for (int g = 0; g < G; ++g) o[g] += o_odd[g * 64 + row];
             }
+            if constexpr (SCALED) {
+                const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G;
+                if (it.single) {
+                    uint16_t* dst = static_cast<uint16_t*>(p.out) + hrow * HD + row;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) dst[g * HD] = float_to_act<ACT>(o[g] * o_scale[b * 8 + g]);
+                } else {
+                    const size_t step = static_cast<size_t>(p.max_parts) * HD;
+                    float* dst = p.ws_o + (hrow * p.max_parts + it.part) * HD + row;
+#pragma unroll
+                    for (int g = 0; g < G; ++g) dst[g * step] = o[g] * o_scale[b * 8 + g];
+                }
+                return true;
+            }
             const int d = PAIR ? (row & 63) : row;
             const bool single = p.max_parts == 1 || s_lens[it.row] <= p.partition_size;
             // E4M3: O was computed on the stored codes and on P x 2^8
-            const float vmul = SCALED ? 1.0f : FP8 ? *p.v_scale * (1.0f / 256.f) : 1.0f;
+            const float vmul = FP8 ? *p.v_scale * (1.0f / 256.f) : 1.0f;
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const float Mg = stats[(b * 2 + hh) * 16 + g];
                 const float Lg = stats[(b * 2 + hh) * 16 + 8 + g];
                 // L >= 1 (the max token's weight is 1): one reciprocal per head
-                const float val = o[g] * (__frcp_rn(Lg) * (SCALED ? pscale[b * 8 + g] : vmul));
+                const float val = o[g] * (__frcp_rn(Lg) * vmul);
                 const int kvh = PAIR ? 2 * it.kvh + hh : it.kvh;
                 const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + kvh * G + g;
                 if (single) {
