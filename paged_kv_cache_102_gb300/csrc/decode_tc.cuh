@@ -806,6 +806,159 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                               : mbar_wait(&q_full[0], last & 1);
             if (!landed) atomicOr(p.err, kErrTimeout);
         }
+    } else if (SCALED && warp == 1) {
+        // --------------------------------------------------- MMA (block-scaled)
+        // The role that everything else waits on: lane 0 alone waits for tiles
+        // and issues their products, with descriptors stepped by one addition;
+        // the warp meets once or twice an item (and where rows are zeroed).
+        constexpr uint32_t HI_SW = tc::desc_hi_sw128(1024), HI_NS = tc::desc_hi_noswizzle(2048);
+        const uint32_t k_lo = tc::desc_start(smem_addr(ring)) + tc::desc_lo(16);
+        const uint32_t v_lo = tc::desc_start(smem_addr(ring)) + tc::desc_lo(kTcStage8);
+        const uint32_t q_lo = tc::desc_start(smem_addr(qbuf)) + tc::desc_lo(16);
+        const uint32_t p_lo = tc::desc_start(smem_addr(pbuf)) + tc::desc_lo(128);
+        int stage = 0, nread = 0;
+        uint32_t phase = 0;
+        auto advance = [&](int n) {
+            stage += n;
+            while (stage >= NS) {
+                stage -= NS;
+                phase ^= 1u;
+            }
+        };
+        // 1: an item, 0: end of work, -1: abort
+        auto read_item = [&](TcItem& it) {
+            const int slot = nread % kTcQueue;
+            const bool good =
+                __all_sync(0xffffffffu, tc_wait(&item_full[slot], (nread / kTcQueue) & 1, abort_flag, p.err));
+            ++nread;
+            if (!good) return -1;
+            const bool any = read_entry(slot, it);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[slot]);
+            return any ? 1 : 0;
+        };
+        auto mma_s = [&](const TcItem& it, int k) {
+            bool good = true;
+            if (lane == 0) {
+                const int b = k & 1;
+                good = tc_wait(&q_full[b], (k >> 1) & 1, abort_flag, p.err);
+                const uint32_t q = q_lo + b * (S::QBUF / 16);
+                uint32_t d = tmem + b * SLOT_COLS;
+                int s = stage;
+                uint32_t ph = phase;
+                for (int t = 0; t < it.n_tiles && good; ++t) {
+                    good = tc_wait(&full[s], ph, abort_flag, p.err);
+                    if (!good) break;
+                    tc::fence_after_sync();
+                    const uint32_t a = k_lo + s * (STG / 16);
+#pragma unroll
+                    for (int par = 0; par < TPR; ++par, d += kTcN) {
+#pragma unroll
+                        for (int kk = 0; kk < HD / 32; ++kk) {
+                            // HALF: even tokens in bytes 0-63 of the rows, odd tokens in 64-127
+                            const uint32_t ak = a + par * 4 + kk * 2, qk = q + kk * 2;
+                            tc::mma_f8_words<HI_SW, HI_SW>(d, ak, qk, IDESC_S, kk > 0);
+                            if constexpr (Q3) tc::mma_f8_words<HI_SW, HI_SW>(d, ak, qk + 128, IDESC_S, true);
+                        }
+                    }
+                    tc::commit(&empty[s]);
+                    if (++s == NS) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+                if (good) {
+                    tc::commit(&q_empty[b]);
+                    tc::commit(&s_full[b]);
+                }
+            }
+            advance(it.n_tiles);
+            return __shfl_sync(0xffffffffu, good, 0) != 0;
+        };
+        auto mma_o = [&](const TcItem& it, int k) {
+            const int b = k & 1;
+            const uint32_t d = tmem + b * SLOT_COLS + O_COL;
+            // the last tile where the context ends within a step of 32 rows: rows past it (and the odd half of a
+            // last row) are zeroed, so that never-written pool slots cannot turn P = 0 into NaN
+            const int tokens = it.n_tok - (it.n_tiles - 1) * TILE;
+            const int valid = (tokens + TPR - 1) / TPR;
+            const bool ragged = valid % 32 != 0 || (HALF && (tokens & 1));
+            auto issue = [&](int s, int t, int ksteps) {
+                const uint32_t a = v_lo + s * (STG / 16);
+                const uint32_t pb = p_lo + b * (S::PBUF / 16) + t * TPR * 128;
+                if (ksteps == 4) {
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int par = 0; par < TPR; ++par)
+                            tc::mma_f8_words<HI_SW, HI_NS>(d + par * kTcN, a + j * 256, pb + par * 128 + j * 32, IDESC_O,
+                                                           t > 0 || j > 0);
+                } else {
+                    for (int j = 0; j < ksteps; ++j)
+#pragma unroll
+                        for (int par = 0; par < TPR; ++par)
+                            tc::mma_f8_words<HI_SW, HI_NS>(d + par * kTcN, a + j * 256, pb + par * 128 + j * 32, IDESC_O,
+                                                           t > 0 || j > 0);
+                }
+                tc::commit(&empty[s]);
+            };
+            bool good = true;
+            const int whole = it.n_tiles - (ragged ? 1 : 0);
+            if (lane == 0) {
+                good = tc_wait(&p_full[b], (k >> 1) & 1, abort_flag, p.err);
+                if (good && k >= 2) good = tc_wait(&o_free[b], ((k >> 1) - 1) & 1, abort_flag, p.err);
+                int s = stage;
+                uint32_t ph = phase;
+                for (int t = 0; t < whole && good; ++t) {
+                    good = tc_wait(&full[s], ph, abort_flag, p.err);
+                    if (!good) break;
+                    tc::fence_after_sync();
+                    issue(s, t, t == it.n_tiles - 1 ? (valid + 31) / 32 : 4);
+                    if (++s == NS) {
+                        s = 0;
+                        ph ^= 1u;
+                    }
+                }
+            }
+            good = __shfl_sync(0xffffffffu, good, 0) != 0;
+            if (!good) return false;
+            advance(whole);
+            if (ragged) {
+                if (!__all_sync(0xffffffffu, tc_wait(&full[stage], phase, abort_flag, p.err))) return false;
+                unsigned char* vb = ring + stage * STG;
+                const int ksteps = (valid + 31) / 32;
+                for (int i = lane; i < (ksteps * 32 - valid) * 8; i += 32)
+                    *reinterpret_cast<uint4*>(vb + valid * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
+                if (HALF && (tokens & 1) && lane < 4)
+                    *reinterpret_cast<uint4*>(vb + (valid - 1) * 128 + (((4 + lane) ^ ((valid - 1) & 7)) * 16)) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                tc::fence_after_sync();
+                if (lane == 0) issue(stage, whole, ksteps);
+                advance(1);
+            }
+            if (lane == 0) tc::commit(&o_full[b]);
+            return true;
+        };
+        TcItem cur, nxt;
+        int rc = read_item(cur);
+        bool ok = rc >= 0;
+        if (rc > 0) ok = mma_s(cur, 0);
+        for (int k = 0; rc > 0 && ok; ++k) {
+            const int rn = read_item(nxt);
+            if (rn < 0) break;
+            if (rn > 0) ok = mma_s(nxt, k + 1);
+            if (ok) ok = mma_o(cur, k);
+            rc = rn;
+            cur = nxt;
+        }
+        // every MMA this thread issued has completed before tensor memory is freed
+        if (lane == 0) {
+            tc::commit(final_bar);
+            if (!mbar_wait(final_bar, 0)) atomicOr(p.err, kErrTimeout);
+        }
+        __syncwarp();
     } else if (warp == 1) {
         // --------------------------------------------------------------------- MMA
         uint32_t use = 0;
@@ -817,10 +970,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             int ci = -1;
             if (lane == 0) {
                 good = tc_wait(&item_full[slot], (nread / kTcQueue) & 1, abort_flag, p.err);
-                if constexpr (SCALED) {
-                    if (good && read_entry(slot, it)) ci = 0;
-                    if (good) mbar_arrive(&item_empty[slot]);
-                } else if (good) {
+                if (good) {
                     ci = item_q[slot];
                     mbar_arrive(&item_empty[slot]);
                 }
@@ -830,11 +980,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             ++nread;
             if (!good) return -1;
             if (ci < 0) return 0;
-            if constexpr (SCALED) {
-                it.n_tok = __shfl_sync(0xffffffffu, it.n_tok, 0);
-                it.n_tiles = __shfl_sync(0xffffffffu, it.n_tiles, 0);
-                return 1;
-            }
             tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
             return 1;
         };
@@ -855,20 +1000,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 tc::fence_after_sync();
                 if (lane == 0) {
                     const uint32_t kb = smem_addr(ring + s * STG);
-                    if constexpr (HALF) {
-                        // even tokens: bytes 0-63 of the rows, odd tokens: 64-127
-#pragma unroll
-                        for (int par = 0; par < 2; ++par) {
-                            const uint32_t d = tmem + b * SLOT_COLS + (2 * t + par) * kTcN;
-#pragma unroll
-                            for (int kk = 0; kk < HD / 32; ++kk) {
-                                const uint64_t a = tc::desc_sw128(kb + par * 64 + kk * 32, 16, 1024);
-                                tc::mma_f8(d, a, tc::desc_sw128(qb + kk * 32, 16, 1024), IDESC_S, kk > 0);
-                                if constexpr (Q3)
-                                    tc::mma_f8(d, a, tc::desc_sw128(qb + 2048 + kk * 32, 16, 1024), IDESC_S, 1u);
-                            }
-                        }
-                    } else if constexpr (FP8) {
+                    if constexpr (FP8) {
                         // K = 32 codes (32 bytes of the 128-byte row) per MMA
 #pragma unroll
                         for (int kk = 0; kk < kTcD / 32; ++kk) {
@@ -917,8 +1049,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 good = __all_sync(0xffffffffu, tc_wait(&full[s], (use / NS) & 1, abort_flag, p.err));
                 if (!good) return false;
                 unsigned char* vb = ring + s * STG;
-                const int tokens = min(TILE, it.n_tok - t * TILE);
-                const int valid = (tokens + TPR - 1) / TPR;  // rows with a token of the context
+                const int valid = min(kTcTile, it.n_tok - t * kTcTile);
                 constexpr int KSTEP = FP8 ? 32 : 16;  // tokens per MMA
                 constexpr int CHUNKS = FP8 ? 8 : 16;  // 16-byte chunks per token row
                 const int ksteps = (valid + KSTEP - 1) / KSTEP;
@@ -932,13 +1063,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         *reinterpret_cast<uint4*>(vb + (c >> 3) * kTcHalf + r * 128 + (c & 7) * 16) =
                             make_uint4(0u, 0u, 0u, 0u);
                     }
-                }
-                // the odd half of a last row whose odd token is past the context
-                const bool zero_half = HALF && (tokens & 1);
-                if (zero_half && lane < 4)
-                    *reinterpret_cast<uint4*>(vb + (valid - 1) * 128 + (((4 + lane) ^ ((valid - 1) & 7)) * 16)) =
-                        make_uint4(0u, 0u, 0u, 0u);
-                if (zero_rows > 0 || zero_half) {
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                 }
@@ -946,14 +1070,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 if (lane == 0) {
                     const uint32_t vaddr = smem_addr(vb);
                     for (int j = 0; j < ksteps; ++j) {
-                        if constexpr (HALF) {
-#pragma unroll
-                            for (int par = 0; par < 2; ++par)
-                                tc::mma_f8(tmem + b * SLOT_COLS + O_COL + par * kTcN,
-                                           tc::desc_sw128(vaddr + j * 4096, kTcStage8, 1024),
-                                           tc::desc_noswizzle(pbase + (2 * t + par) * 2048 + j * 512, 128, 2048), IDESC_O,
-                                           (t > 0 || j > 0) ? 1u : 0u);
-                        } else if constexpr (FP8) {
+                        if constexpr (FP8) {
                             // A = V^T: the 128 codes of a token are one 128-byte row, so
                             // M = 128 is a single swizzle atom; 32 tokens = 4 KB per step
                             // B = P: core matrices of 8 tokens x 16 bytes, 128 B apart

@@ -90,6 +90,26 @@ __device__ __forceinline__ uint64_t desc_sw128(uint32_t saddr, uint32_t lbo, uin
     return d;
 }
 
+// The two descriptor layouts as a low word (start and leading byte offset) and
+// a constant high word: a loop over start addresses adds to the low word.
+__host__ __device__ constexpr uint32_t desc_lo(uint32_t lbo) { return (lbo >> 4) << 16; }
+__device__ __forceinline__ uint32_t desc_start(uint32_t saddr) { return (saddr >> 4) & 0x3FFFu; }
+__host__ __device__ constexpr uint32_t desc_hi_sw128(uint32_t sbo) { return (sbo >> 4) | (1u << 14) | (2u << 29); }
+__host__ __device__ constexpr uint32_t desc_hi_noswizzle(uint32_t sbo) { return (sbo >> 4) | (1u << 14); }
+
+// mma_f8 with descriptors given as words.
+template <uint32_t A_HI, uint32_t B_HI>
+__device__ __forceinline__ void mma_f8_words(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(A_HI), "n"(B_HI)
+        : "memory");
+}
+
 // Shared-memory matrix descriptor, no swizzle (the canonical interleaved
 // layout: 8 rows x 16 bytes form a contiguous 128-byte core matrix).  For a
 // K-major operand the leading byte offset is the distance between core
