@@ -25,9 +25,10 @@
 // either written as the output (one partition) or as a partial
 // (m, l, o = acc/l) for the split-K merge kernel.
 //
-// Block-scaled E4M3 cache: the producer reads each block's K and V scale with
-// its table entry and leaves them beside the stage.  A warp's 8 tokens of a
-// stage lie in one block, so both scales are warp-uniform: the K scale joins
+// Block-scaled E4M3 cache: each consumer warp reads the table entries and the K
+// and V scales of 32 blocks at a time, a block a lane, while the producer's
+// copies are on their way.  A warp's 8 tokens of a stage lie in one block, so
+// both scales are warp-uniform, one shuffle each: the K scale joins
 // the factor of the reduced dot product, the V scale the weights.  Weights are
 // kept relative to a power of two 2^mv near the V scales seen, moved (with acc)
 // when a block's scale is more than 2^7 away from it, so that p * vs / 2^mv
@@ -67,8 +68,7 @@ struct DecodeCfg {
     static constexpr int STAGES = STAGES_RAW < 2 ? 2 : (STAGES_RAW > 8 ? 8 : STAGES_RAW);
     static constexpr int RED_FLOATS = kConsumerWarps * G * (D + 2);
     static constexpr bool SCALED = CACHE == kE4M3B;
-    static constexpr int SCALE_FLOATS = SCALED ? 2 * STAGES * BPS : 0;  // K, then V scales of each stage's blocks
-    static constexpr int SMEM_BYTES = 2 * STAGES * STAGE_BYTES + 2 * STAGES * 8 + (RED_FLOATS + SCALE_FLOATS) * 4;
+    static constexpr int SMEM_BYTES = 2 * STAGES * STAGE_BYTES + 2 * STAGES * 8 + RED_FLOATS * 4;
     static_assert(LPR >= 1 && LPR <= 32 && 32 % LPR == 0, "row layout");
     static_assert(TW % TPP == 0, "tokens per warp must be a multiple of rows per load");
     static_assert(kStageTokens % BS == 0, "block size must divide the stage");
@@ -89,8 +89,6 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     float* red_m = red;                                     // [NW][G]
     float* red_l = red + kConsumerWarps * G;                // [NW][G]
     float* red_acc = red + 2 * kConsumerWarps * G;          // [NW][G][D]
-    [[maybe_unused]] float* sk = red + C::RED_FLOATS;       // [STAGES][BPS]
-    [[maybe_unused]] float* sv = sk + C::STAGES * C::BPS;   // [STAGES][BPS]
 
     // the merge kernel may be scheduled once every CTA got here; it waits for
     // this grid to finish
@@ -155,25 +153,12 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                 atomicOr(p.err, kErrBadBlock);
                 phys = -1;
             }
-            [[maybe_unused]] float ksc = 0.f, vsc = 0.f;
-            if (C::SCALED && have && phys >= 0) {
-                ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + kvh];
-                vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + kvh];
-            }
             const int chunk_blocks = min(32, n_blk - chunk);
             for (int j = 0; j < chunk_blocks; j += C::BPS) {
                 int pb[C::BPS];
 #pragma unroll
                 for (int bi = 0; bi < C::BPS; ++bi) pb[bi] = __shfl_sync(0xffffffffu, phys, (j + bi) & 31);
                 const int st = (chunk + j) / C::BPS;
-                [[maybe_unused]] float pk[C::BPS], pv[C::BPS];
-                if constexpr (C::SCALED) {
-#pragma unroll
-                    for (int bi = 0; bi < C::BPS; ++bi) {
-                        pk[bi] = __shfl_sync(0xffffffffu, ksc, (j + bi) & 31);
-                        pv[bi] = __shfl_sync(0xffffffffu, vsc, (j + bi) & 31);
-                    }
-                }
                 if (lane == 0) {
                     const int s = st % C::STAGES;
                     if (st >= C::STAGES && !mbar_wait(&empty[s], ((st / C::STAGES) - 1) & 1)) {
@@ -182,13 +167,6 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                     }
                     if (ok) {
                         uint32_t bytes = 0;
-                        if constexpr (C::SCALED) {  // before the arrive that publishes the stage
-#pragma unroll
-                            for (int bi = 0; bi < C::BPS; ++bi) {
-                                sk[s * C::BPS + bi] = pk[bi];
-                                sv[s * C::BPS + bi] = pv[bi];
-                            }
-                        }
 #pragma unroll
                         for (int bi = 0; bi < C::BPS; ++bi)
                             if (j + bi < chunk_blocks && pb[bi] >= 0) bytes += 2 * C::TILE_BYTES;
@@ -264,6 +242,20 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
         for (int v = 0; v < C::VEC; ++v) acc[g][v] = 0.f;
     }
 
+    // block-scaled: scales of blocks [32 c, 32 c + 32) of the partition, a block a lane
+    [[maybe_unused]] float ksc = 0.f, vsc = 0.f;
+    [[maybe_unused]] auto load_scales = [&](int first) {
+        ksc = vsc = 0.f;
+        if (first + lane < n_blk) {
+            const int phys = p.block_tables[seq * p.table_seq_stride + kvh * p.table_kvh_stride + blk_begin + first + lane];
+            if (phys >= 0 && phys < p.num_blocks) {
+                ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + kvh];
+                vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + kvh];
+            }
+        }
+    };
+    if constexpr (C::SCALED) load_scales(0);
+
     auto consume = [&](auto mixed_tag) {
         constexpr bool MIX = decltype(mixed_tag)::value;
         constexpr int QN = MIX ? C::VEC / 2 : C::VEC;
@@ -304,9 +296,10 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
             const int tok0 = tok_begin + st * kStageTokens;
             [[maybe_unused]] float ks = 1.f, vf = 1.f;
             if constexpr (C::SCALED) {
-                const int bi = warp * C::TW / BS;  // the block of this warp's tokens
-                ks = sk[s * C::BPS + bi];
-                vf = sv[s * C::BPS + bi];
+                const int bi = st * C::BPS + warp * C::TW / BS;  // the block of this warp's tokens
+                if (st > 0 && (st * C::BPS) % 32 == 0) load_scales(st * C::BPS);
+                ks = __shfl_sync(0xffffffffu, ksc, bi & 31);
+                vf = __shfl_sync(0xffffffffu, vsc, bi & 31);
                 // exponent of the V scale; 0 (and subnormal scales) leave the reference alone
                 const int ev = static_cast<int>((__float_as_uint(vf) >> 23) & 0xffu) - 127;
                 if (ev > -127 && tok0 + warp * C::TW < tok_end && (ev > mv + 7 || ev < mv - 7)) {

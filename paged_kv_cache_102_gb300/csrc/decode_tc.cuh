@@ -628,6 +628,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         };
         TcItem it;
         int phys = -1;
+        // the counter was zeroed by the kernel before, which this launch did not wait for
+        if constexpr (SCALED) asm volatile("griddepcontrol.wait;" ::: "memory");
         while (ok && claim(it, phys)) {
         }
     } else if (warp >= 6) {
@@ -670,6 +672,24 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
             return 1;
         };
+        // E4M3: the item's queries, 16 channels of a head each time, loaded before
+        // the K copies so that their latency is covered
+        constexpr int QN = FP8 ? (G * HD / 16 + 31) / 32 : 1;
+        [[maybe_unused]] uint4 qu[QN][2];
+        [[maybe_unused]] auto load_q = [&](const TcItem& it) {
+            const uint16_t* qg = static_cast<const uint16_t*>(p.q) +
+                                 (static_cast<int64_t>(it.seq) * p.num_q_heads + it.kvh * G) * HD;
+#pragma unroll
+            for (int n = 0; n < QN; ++n) {
+                const int i = n * 32 + lane;
+                if (G * HD / 16 % 32 == 0 || i < G * HD / 16) {
+                    qu[n][0] = *reinterpret_cast<const uint4*>(qg + i * 16);
+                    qu[n][1] = *reinterpret_cast<const uint4*>(qg + i * 16 + 8);
+                } else {
+                    qu[n][0] = qu[n][1] = make_uint4(0u, 0u, 0u, 0u);
+                }
+            }
+        };
         auto issue_q = [&](const TcItem& it, int k) {
             bool good = true;
             if constexpr (FP8) {
@@ -687,21 +707,6 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 good = __shfl_sync(0xffffffffu, good, 0);
                 if (!good) return false;
                 unsigned char* qbuf_k = qbuf + qb * S::QBUF;
-                const uint16_t* qg = static_cast<const uint16_t*>(p.q) +
-                                     (static_cast<int64_t>(it.seq) * p.num_q_heads + it.kvh * G) * HD;
-                // the item's queries, 16 channels of a head each time
-                constexpr int QN = (G * HD / 16 + 31) / 32;
-                uint4 qu[QN][2];
-#pragma unroll
-                for (int n = 0; n < QN; ++n) {
-                    const int i = n * 32 + lane;
-                    if (G * HD / 16 % 32 == 0 || i < G * HD / 16) {
-                        qu[n][0] = *reinterpret_cast<const uint4*>(qg + i * 16);
-                        qu[n][1] = *reinterpret_cast<const uint4*>(qg + i * 16 + 8);
-                    } else {
-                        qu[n][0] = qu[n][1] = make_uint4(0u, 0u, 0u, 0u);
-                    }
-                }
                 int shift = it.qshift;
                 if constexpr (SCALED) {
                     // largest magnitude in [128, 256) after the exact power-of-2 scale (see the scheduler)
@@ -781,6 +786,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             // 16-bit: Q first (one TMA issue); E4M3: the K copies first, so that
             // their latency covers the Q conversion
             if (!FP8 && parity == 0 && !issue_q(it, k)) return false;
+            if (FP8 && parity == 0) load_q(it);
             for (int t = 0; t < it.n_tiles; ++t)
                 if (!issue_tile(use, parity, it, phys, t, &kmap)) return false;
             return !FP8 || parity != 0 || issue_q(it, k);

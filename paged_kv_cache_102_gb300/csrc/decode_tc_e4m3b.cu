@@ -29,8 +29,6 @@ cudaError_t launch_decode_tc_e4m3b(const DecodeParams& p, int act, int head_dim,
     CUtensorMap km, vm;
     if (!make_map8(&km, p.k_cache, cache_rows, box_rows) || !make_map8(&vm, p.v_cache, cache_rows, box_rows))
         return cudaErrorInvalidValue;
-    cudaError_t e = cudaMemsetAsync(p.work_counter, 0, sizeof(int), s);
-    if (e != cudaSuccess) return e;
     if (half)
         return act == kBF16 ? launch_scaled<kBF16, true>(p, km, vm, BS, G, variant, s)
                             : launch_scaled<kF16, true>(p, km, vm, BS, G, variant, s);

@@ -54,6 +54,11 @@ int sm_count() {
     return counts[dev];
 }
 
+__global__ void zero_counter_kernel(int* counter) {
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 0) *counter = 0;
+}
+
 template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR, bool HALF>
 cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                    int ctas_per_sm, cudaStream_t s) {
@@ -78,8 +83,26 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorM
     if (sms <= 0) return cudaErrorInvalidDevice;
     const int grid = static_cast<int>(items < static_cast<long long>(sms) * ctas_per_sm ? items : sms * ctas_per_sm);
     if (grid <= 0) return cudaSuccess;
-    kern<<<grid, threads, smem, s>>>(km, vm, qm, p);
-    return cudaGetLastError();
+    if constexpr (CACHE == kE4M3B) {
+        // zero the work counter, and let the decode kernel's prologue run meanwhile
+        zero_counter_kernel<<<1, 32, 0, s>>>(p.work_counter);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(grid));
+        cfg.blockDim = dim3(threads);
+        cfg.dynamicSmemBytes = smem;
+        cfg.stream = s;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, kern, km, vm, qm, p);
+    } else {
+        kern<<<grid, threads, smem, s>>>(km, vm, qm, p);
+        return cudaGetLastError();
+    }
 }
 
 template <int ACT, int CACHE, int NS, bool PAIR = false, bool HALF = false>

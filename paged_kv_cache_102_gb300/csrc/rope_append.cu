@@ -39,7 +39,8 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kTable = 2048;  // (cos, sin) pairs a block keeps in shared memory
-constexpr int kGroup = 8;     // row loads a warp has in flight
+constexpr int kLoads = 4;     // row loads a warp has in flight where rows do not share a scale
+constexpr int kFill = 152 * 4;  // blocks that keep the GPU busy
 constexpr int kScaleMinExp = -64, kScaleMaxExp = 120;
 
 // How the channels of a pair lie: neighbours; R/2 apart with R/2 a multiple of
@@ -193,13 +194,13 @@ __device__ __forceinline__ int64_t slot_of(const RopeAppendParams& p, int t, boo
 // ---------------------------------------------------------------------------
 // Rows that do not share a scale: the queries and, for a 16-bit or one-scale
 // E4M3 cache, the keys and values.  A warp takes a range of one token's heads
-// [q | k | v], RP = 32 / (D / 8) rows at a time and kGroup / 2 such loads ahead
-// of their use, with the token's cos and sin in registers (read once from the
+// [q | k | v], RP = 32 / (D / 8) rows at a time and kLoads such loads ahead of
+// their use, with the token's cos and sin in registers (read once from the
 // block's table).
 // ---------------------------------------------------------------------------
 template <int ACT, int CACHE, int PAIRS>
 __device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token, int row0, int row1, const float2* table) {
-    constexpr int U = kGroup / 2;
+    constexpr int U = kLoads;
     const int lane = threadIdx.x & 31;
     const int lpr = p.head_dim / 8, rp = 32 / lpr;
     const int r = lane / lpr, c = lane - r * lpr;
@@ -290,12 +291,12 @@ __device__ __forceinline__ void top_bits(const uint4& u, uint32_t& top) {
 // ---------------------------------------------------------------------------
 // One run of n tokens of one block and kv head into a block-scaled cache, K or
 // V, by one warp: the maximum over the run, the block's new scale, its other
-// codes where the scale grew, the run's codes.  Up to kGroup loads a lane (a
-// whole 16-token block at head_dim 128) stay in registers between the maximum
-// and the codes; longer runs are read twice.  Rotated keys are computed twice
+// codes where the scale grew, the run's codes.  Up to GROUP loads a lane stay in
+// registers between the maximum and the codes (8 hold a whole 16-token block at
+// head_dim 128); longer runs are read twice.  Rotated keys are computed twice
 // instead of being kept.
 // ---------------------------------------------------------------------------
-template <int ACT, int PAIRS>
+template <int ACT, int PAIRS, int GROUP>
 __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, int n, int64_t blk, int off0, int head,
                                            bool is_k, const float2* table, int tabled) {
     const int lane = threadIdx.x & 31;
@@ -308,10 +309,10 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
     const uint16_t* src0 = (is_k ? static_cast<const uint16_t*>(p.k) : static_cast<const uint16_t*>(p.v)) + t0 * stride +
                            static_cast<int64_t>(head) * p.head_dim;
     const int half = p.rotary_dim / 2;
-    uint4 u[kGroup];
+    uint4 u[GROUP];
     auto load = [&](int g0) {
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
+        for (int j = 0; j < GROUP; ++j) {
             const int i = g0 + j * rp + r;
             u[j] = r < rp && i < n ? *reinterpret_cast<const uint4*>(src0 + i * stride + c * 8)
                                    : make_uint4(0u, 0u, 0u, 0u);
@@ -332,10 +333,10 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
     };
     float top = 0.f;
     uint32_t tops = 0;
-    for (int g0 = 0; g0 < n; g0 += kGroup * rp) {
+    for (int g0 = 0; g0 < n; g0 += GROUP * rp) {
         load(g0);
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
+        for (int j = 0; j < GROUP; ++j) {
             if (g0 + j * rp >= n) break;
             if (turn) {
                 float x[8];
@@ -368,23 +369,34 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
         if (lane == 0) *scale = now;
         if (old > 0.f) {
             const float ratio = __fdiv_rn(old, now);
-            for (int i = lane; i < p.block_size * lpr; i += 32) {
-                const int row = i / lpr;
-                if (row >= off0 && row < off0 + n) continue;
-                uint2* at = reinterpret_cast<uint2*>(tile) + i;
-                const uint2 codes = *at;
-                float x[16];
-                Vec16E4M3::to_float(make_uint4(codes.x, codes.y, 0u, 0u), x);
+            // 8-byte pieces of the block, loads ahead of the stores
+            constexpr int B = 8;
+            const int pieces = p.block_size * lpr;
+            uint2* at = reinterpret_cast<uint2*>(tile);
+            for (int i0 = lane; i0 < pieces; i0 += 32 * B) {
+                uint2 codes[B];
+                bool mine[B];
 #pragma unroll
-                for (int j = 0; j < 8; ++j) x[j] *= ratio;
-                *at = to_codes(x);
+                for (int k = 0; k < B; ++k) {
+                    const int i = i0 + 32 * k, row = i / lpr;
+                    mine[k] = i < pieces && (row < off0 || row >= off0 + n);
+                    codes[k] = mine[k] ? at[i] : make_uint2(0u, 0u);
+                }
+#pragma unroll
+                for (int k = 0; k < B; ++k) {
+                    float x[16];
+                    Vec16E4M3::to_float(make_uint4(codes[k].x, codes[k].y, 0u, 0u), x);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) x[j] *= ratio;
+                    if (mine[k]) at[i0 + 32 * k] = to_codes(x);
+                }
             }
         }
     }
-    for (int g0 = 0; g0 < n; g0 += kGroup * rp) {
-        if (n > kGroup * rp) load(g0);
+    for (int g0 = 0; g0 < n; g0 += GROUP * rp) {
+        if (n > GROUP * rp) load(g0);
 #pragma unroll
-        for (int j = 0; j < kGroup; ++j) {
+        for (int j = 0; j < GROUP; ++j) {
             if (g0 + j * rp >= n) break;
             const int i = g0 + j * rp + r;
             float x[8];
@@ -397,70 +409,64 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
     }
 }
 
-// Grid: the first kv_windows * kv_split blocks (block-scaled cache only) take
-// the runs that start in a window of `window` <= 32 tokens, kv_split blocks
-// sharing the (head, K or V) items of each run; the others take (token, part of
-// its rows) items, one a warp.  cos and sin of a block's tokens are computed
-// once into shared memory.
-template <int ACT, int CACHE, int PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 2)
-    rope_append_kernel(const RopeAppendParams p, int window, int kv_windows, int kv_split, int parts, int per, int rows) {
-    __shared__ float2 table[kTable];
+// Runs that start in window w of `window` <= 32 tokens: block `part` of `split`
+// takes its share of each run's (head, K or V) items, one a warp.  cos and sin
+// of the run's tokens are computed once into shared memory.
+template <int ACT, int PAIRS, int GROUP>
+__device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int window, int w, int part, int split,
+                                             float2* table) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int half = p.rotary_dim / 2;
-    int cta = blockIdx.x;
-    if constexpr (CACHE == kE4M3B) {
-        if (cta < kv_windows * kv_split) {
-            const int w = cta / kv_split, part = cta - w * kv_split;
-            const int t = w * window + lane;
-            bool bad = false, unused = false;
-            const int64_t slot = lane < window ? slot_of(p, t, &bad) : -1;
-            const int64_t prev = slot_of(p, t - 1, &unused);
-            if (bad && warp == 0 && part == 0) atomicOr(p.err, kErrBadSlot);
-            int64_t blk = 0;
-            int off = 0;
-            if (slot >= 0) divmod_u(slot, p.block_size, blk, off);
-            unsigned leaders = __ballot_sync(0xffffffffu, slot >= 0 && (prev != slot - 1 || off == 0));
-            for (; leaders; leaders &= leaders - 1) {
-                const int at = __ffs(leaders) - 1;
-                const int t0 = w * window + at;
-                const int64_t s0 = __shfl_sync(0xffffffffu, slot, at), b0 = __shfl_sync(0xffffffffu, blk, at);
-                const int off0 = __shfl_sync(0xffffffffu, off, at);
-                // the run's length: up to the end of the block
-                int n = 1;
-                for (int base = 1; base < p.block_size - off0; base += 32) {
-                    const int k = base + lane;
-                    const bool in = k < p.block_size - off0 && slot_of(p, t0 + k, &unused) == s0 + k;
-                    const unsigned out = __ballot_sync(0xffffffffu, !in);
-                    n = base + (out ? __ffs(out) - 1 : 32);
-                    if (out) break;
-                }
-                int tabled = 0;
-                if (p.positions) {
-                    tabled = min(n, kTable / half);
-                    __syncthreads();  // the run before is done with the table
-                    for (int i = threadIdx.x; i < tabled * half; i += kWarps * 32) {
-                        const int k = i / half;
-                        table[i] = cos_sin_at(p, i - k * half, p.positions[t0 + k]);
-                    }
-                    __syncthreads();
-                }
-                for (int it = part * kWarps + warp; it < 2 * p.num_kv_heads; it += kv_split * kWarps) {
-                    const bool is_k = it < p.num_kv_heads;
-                    scaled_run<ACT, PAIRS>(p, t0, n, b0, off0, is_k ? it : it - p.num_kv_heads, is_k, table, tabled);
-                }
-            }
-            return;
+    const int t = w * window + lane;
+    bool bad = false, unused = false;
+    const int64_t slot = lane < window ? slot_of(p, t, &bad) : -1;
+    const int64_t prev = slot_of(p, t - 1, &unused);
+    if (bad && warp == 0 && part == 0) atomicOr(p.err, kErrBadSlot);
+    int64_t blk = 0;
+    int off = 0;
+    if (slot >= 0) divmod_u(slot, p.block_size, blk, off);
+    unsigned leaders = __ballot_sync(0xffffffffu, slot >= 0 && (prev != slot - 1 || off == 0));
+    for (; leaders; leaders &= leaders - 1) {
+        const int at = __ffs(leaders) - 1;
+        const int t0 = w * window + at;
+        const int64_t s0 = __shfl_sync(0xffffffffu, slot, at), b0 = __shfl_sync(0xffffffffu, blk, at);
+        const int off0 = __shfl_sync(0xffffffffu, off, at);
+        // the run's length: up to the end of the block
+        int n = 1;
+        for (int base = 1; base < p.block_size - off0; base += 32) {
+            const int k = base + lane;
+            const bool in = k < p.block_size - off0 && slot_of(p, t0 + k, &unused) == s0 + k;
+            const unsigned out = __ballot_sync(0xffffffffu, !in);
+            n = base + (out ? __ffs(out) - 1 : 32);
+            if (out) break;
         }
-        cta -= kv_windows * kv_split;
+        int tabled = 0;
+        if (p.positions) {
+            tabled = min(n, kTable / half);
+            __syncthreads();  // the run before is done with the table
+            for (int i = threadIdx.x; i < tabled * half; i += kWarps * 32) {
+                const int k = i / half;
+                table[i] = cos_sin_at(p, i - k * half, p.positions[t0 + k]);
+            }
+            __syncthreads();
+        }
+        for (int it = part * kWarps + warp; it < 2 * p.num_kv_heads; it += split * kWarps) {
+            const bool is_k = it < p.num_kv_heads;
+            scaled_run<ACT, PAIRS, GROUP>(p, t0, n, b0, off0, is_k ? it : it - p.num_kv_heads, is_k, table, tabled);
+        }
     }
-    // (token, part) items of this block's warps: at most kWarps tokens
+}
+
+// Items (token, part of its rows) of block `cta`, one a warp: at most kWarps tokens.
+template <int ACT, int CACHE, int PAIRS>
+__device__ __forceinline__ void rows_block(const RopeAppendParams& p, int cta, int parts, int per, int rows, float2* table) {
+    const int warp = threadIdx.x >> 5;
+    const int half = p.rotary_dim / 2;
     const int64_t item0 = static_cast<int64_t>(cta) * kWarps;
-    int64_t token0, token;
+    int64_t token0, token, last;
     int unused, part;
     divmod_u(item0, parts, token0, unused);
     divmod_u(item0 + warp, parts, token, part);
-    int64_t last;
     divmod_u(item0 + kWarps - 1, parts, last, unused);
     const int tokens = static_cast<int>(min(last, static_cast<int64_t>(p.num_tokens) - 1) - token0) + 1;
     for (int i = threadIdx.x; i < tokens * half; i += kWarps * 32) {
@@ -473,33 +479,89 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
                                   table + static_cast<int>(token - token0) * half);
 }
 
+// How a launch divides its work.
+struct Split {
+    int window, windows, share;  // runs: tokens a window, windows, blocks a window
+    int parts, per, rows;        // rows: items a token, rows an item, rows a token
+};
+
+template <int ACT, int CACHE, int PAIRS>
+__global__ void __launch_bounds__(kWarps * 32, 3) rope_rows_kernel(const RopeAppendParams p, const Split d) {
+    __shared__ float2 table[kTable / 2];
+    rows_block<ACT, CACHE, PAIRS>(p, blockIdx.x, d.parts, d.per, d.rows, table);
+    // launched beside the kernel that stores the keys and values: done when that is done
+    if (CACHE == kE4M3B) asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+
+// Prompts: runs of many tokens.
+template <int ACT, int PAIRS>
+__global__ void __launch_bounds__(kWarps * 32, 2) scaled_runs_kernel(const RopeAppendParams p, const Split d) {
+    __shared__ float2 table[kTable];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int w = blockIdx.x / d.share;
+    scaled_block<ACT, PAIRS, 8>(p, d.window, w, blockIdx.x - w * d.share, d.share, table);
+}
+
+// Few tokens (a decode step): runs and rows in one launch, more warps at a time.
+template <int ACT, int PAIRS>
+__global__ void __launch_bounds__(kWarps * 32, 4) scaled_step_kernel(const RopeAppendParams p, const Split d) {
+    __shared__ float2 table[kTable];
+    const int cta = blockIdx.x, runs = d.windows * d.share;
+    if (cta < runs) {
+        const int w = cta / d.share;
+        scaled_block<ACT, PAIRS, 1>(p, d.window, w, cta - w * d.share, d.share, table);
+    } else {
+        rows_block<ACT, kE4M3B, PAIRS>(p, cta - runs, d.parts, d.per, d.rows, table);
+    }
+}
+
 template <int ACT, int CACHE, int PAIRS>
 cudaError_t launch(const RopeAppendParams& p, cudaStream_t stream) {
-    static_assert(kWarps * 128 <= kTable, "a block's tokens fit the table at rotary_dim 256");
-    constexpr int kFill = 152 * 4;  // blocks that keep the GPU busy
+    static_assert(kWarps * 128 <= kTable / 2, "a block's tokens fit the table at rotary_dim 256");
     const int rp = 32 / (p.head_dim / 8);
-    int window = 32, kv_windows = 0, kv_split = 1;
-    if (CACHE == kE4M3B) {
-        // prompts: a window starts a run or a few, whose heads one block works off; few tokens: one token a window
-        while (window > 1 && (p.num_tokens + window - 1) / window < kFill) window /= 2;
-        kv_windows = (p.num_tokens + window - 1) / window;
-        const int most = (2 * p.num_kv_heads + kWarps - 1) / kWarps;
-        while (kv_split < most && kv_windows * kv_split < kFill) ++kv_split;
-    }
-    const int rows = p.positions == nullptr ? 0 : CACHE == kE4M3B ? p.num_q_heads : p.num_q_heads + 2 * p.num_kv_heads;
+    Split d{};
+    d.rows = p.positions == nullptr ? 0 : CACHE == kE4M3B ? p.num_q_heads : p.num_q_heads + 2 * p.num_kv_heads;
     // rows of a token per warp: all of them when the tokens alone fill the GPU
-    const int passes = (rows + rp - 1) / rp;
+    const int passes = (d.rows + rp - 1) / rp;
     int split = 1;
     while (split < passes && static_cast<int64_t>(p.num_tokens) * split < kFill * kWarps) split *= 2;
-    const int per = rows ? (passes + split - 1) / split * rp : 1;
-    const int parts = rows ? (rows + per - 1) / per : 1;
-    const int64_t plain = rows ? (static_cast<int64_t>(p.num_tokens) * parts + kWarps - 1) / kWarps : 0;
-    const int64_t grid = static_cast<int64_t>(kv_windows) * kv_split + plain;
-    if (grid <= 0) return cudaSuccess;
-    if (grid > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    rope_append_kernel<ACT, CACHE, PAIRS><<<static_cast<unsigned>(grid), kWarps * 32, 0, stream>>>(
-        p, window, kv_windows, kv_split, parts, per, rows);
-    return cudaGetLastError();
+    d.per = d.rows ? (passes + split - 1) / split * rp : 1;
+    d.parts = d.rows ? (d.rows + d.per - 1) / d.per : 1;
+    const int64_t row_blocks = d.rows ? (static_cast<int64_t>(p.num_tokens) * d.parts + kWarps - 1) / kWarps : 0;
+    if (row_blocks > 0x3fffffff) return cudaErrorInvalidConfiguration;
+    const unsigned threads = kWarps * 32;
+    if constexpr (CACHE != kE4M3B) {
+        rope_rows_kernel<ACT, CACHE, PAIRS><<<static_cast<unsigned>(row_blocks), threads, 0, stream>>>(p, d);
+        return cudaGetLastError();
+    } else {
+        // prompts: a window starts a run or a few, whose heads one block works off; few tokens: one token a window
+        d.window = 32;
+        while (d.window > 1 && (p.num_tokens + d.window - 1) / d.window < kFill) d.window /= 2;
+        d.windows = (p.num_tokens + d.window - 1) / d.window;
+        const int most = (2 * p.num_kv_heads + kWarps - 1) / kWarps;
+        d.share = 1;
+        const int fill = d.window == 1 ? 4 * kFill : kFill;
+        while (d.share < most && static_cast<int64_t>(d.windows) * d.share < fill) ++d.share;
+        const int64_t run_blocks = static_cast<int64_t>(d.windows) * d.share;
+        if (run_blocks + row_blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+        if (d.window == 1) {
+            scaled_step_kernel<ACT, PAIRS><<<static_cast<unsigned>(run_blocks + row_blocks), threads, 0, stream>>>(p, d);
+            return cudaGetLastError();
+        }
+        scaled_runs_kernel<ACT, PAIRS><<<static_cast<unsigned>(run_blocks), threads, 0, stream>>>(p, d);
+        cudaError_t e = cudaGetLastError();
+        if (e != cudaSuccess || row_blocks == 0) return e;
+        cudaLaunchConfig_t cfg = {};
+        cfg.gridDim = dim3(static_cast<unsigned>(row_blocks));
+        cfg.blockDim = dim3(threads);
+        cfg.stream = stream;
+        cudaLaunchAttribute attr[1];
+        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        attr[0].val.programmaticStreamSerializationAllowed = 1;
+        cfg.attrs = attr;
+        cfg.numAttrs = 1;
+        return cudaLaunchKernelEx(&cfg, rope_rows_kernel<ACT, CACHE, PAIRS>, p, d);
+    }
 }
 
 template <int ACT, int CACHE>
