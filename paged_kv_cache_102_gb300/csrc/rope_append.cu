@@ -38,15 +38,15 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 8;
-constexpr int kTable = 2048;  // (cos, sin) pairs a block keeps in shared memory
+constexpr int kTable = 4096;  // floats of cos and sin a block keeps in shared memory
 constexpr int kLoads = 4;     // row loads a warp has in flight where rows do not share a scale
 constexpr int kFill = 152 * 4;  // blocks that keep the GPU busy
 constexpr int kScaleMinExp = -64, kScaleMaxExp = 120;
 
 // How the channels of a pair lie: neighbours; R/2 apart with R/2 a multiple of
 // 8 (whole 8-channel chunks swap, by shuffle); R/2 apart otherwise (partners
-// are read from memory).
-enum : int { kPairsNext = 0, kPairsChunks = 1, kPairsApart = 2 };
+// are read from memory).  kPairsNone: no rotation (the append alone).
+enum : int { kPairsNext = 0, kPairsChunks = 1, kPairsApart = 2, kPairsNone = 3 };
 
 // w / 2pi as a 64-bit fraction of a turn.
 __device__ __forceinline__ uint64_t turn_of(float w) {
@@ -80,25 +80,76 @@ __device__ __forceinline__ float2 cos_sin_at(const RopeAppendParams& p, int i, i
     return make_float2(cs.x * p.factor, cs.y * p.factor);
 }
 
-// cos and sin for the eight channels 8c .. 8c+7 of a row; 1 and 0 for channels
-// that do not turn.  at(i) gives the pair i's.
-template <int PAIRS, class At>
-__device__ __forceinline__ void lane_cos_sin(const RopeAppendParams& p, int c, At at, float* cs, float* sn) {
-    const int half = p.rotary_dim / 2;
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const int e = 8 * c + j;
-        if (PAIRS == kPairsNext && (j & 1)) {
-            cs[j] = cs[j - 1];
-            sn[j] = sn[j - 1];
-            continue;
-        }
-        const int i = PAIRS == kPairsNext ? e / 2 : (e < half ? e : e - half);
-        const float2 t = e < p.rotary_dim ? at(i) : make_float2(1.f, 0.f);
-        cs[j] = t.x;
-        sn[j] = t.y;
+// The block's table: for each of its rows, cos of the pairs that a lane's chunk
+// of 8 channels needs (J of them) in J / 4 quads, then sin, quad q of chunk c at
+// float4 index (row * J / 2 + q) * C + c, so that the lanes of a quarter warp
+// read 128 consecutive bytes.  Chunks c and c + C of the half layout share
+// their pairs.
+template <int PAIRS>
+struct Table {
+    static constexpr int J = PAIRS == kPairsNext ? 4 : 8;
+    int C;  // chunks with entries
+    __device__ __forceinline__ explicit Table(const RopeAppendParams& p)
+        : C(PAIRS == kPairsChunks ? p.rotary_dim / 16 : (p.rotary_dim + 7) / 8) {}
+    __device__ __forceinline__ int row_floats() const { return 2 * J * C; }
+    // Pair of entry j of chunk c (past the end: any).
+    __device__ __forceinline__ static int pair(const RopeAppendParams& p, int c, int j) {
+        const int half = p.rotary_dim / 2;
+        const int e = PAIRS == kPairsNext ? 4 * c + j : 8 * c + j;
+        return PAIRS == kPairsApart ? (e < half ? e : min(e - half, half - 1)) : min(e, half - 1);
     }
-}
+    // All threads of the block: rows [0, rows) for tokens t0, t0 + 1, ...
+    __device__ __forceinline__ void fill(const RopeAppendParams& p, float* table, int64_t t0, int rows) const {
+        const int n = J * C;
+        for (int i = threadIdx.x; i < rows * n; i += kWarps * 32) {
+            const int row = i / n, k = i - row * n, c = k / J, j = k - c * J;
+            const float2 cs = cos_sin_at(p, pair(p, c, j), p.positions[t0 + row]);
+            float* at = table + row * 2 * n + ((j >> 2) * C + c) * 4 + (j & 3);
+            at[0] = cs.x;
+            at[n] = cs.y;
+        }
+    }
+    // cos and sin of the 8 channels of chunk c; 1 and 0 for a chunk that does not turn.
+    __device__ __forceinline__ void read(const RopeAppendParams& p, const float* table, int row, int c, float* cs,
+                                         float* sn) const {
+        if (8 * c >= p.rotary_dim) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                cs[j] = 1.f;
+                sn[j] = 0.f;
+            }
+            return;
+        }
+        const int cc = PAIRS == kPairsChunks && c >= C ? c - C : c;
+        const float4* at = reinterpret_cast<const float4*>(table) + row * (J / 2) * C + cc;
+#pragma unroll
+        for (int q = 0; q < J / 4; ++q) {
+            const float4 a = at[q * C], b = at[(J / 4 + q) * C];
+            const float ca[4] = {a.x, a.y, a.z, a.w}, sa[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                if constexpr (PAIRS == kPairsNext) {
+                    cs[2 * j] = cs[2 * j + 1] = ca[j];
+                    sn[2 * j] = sn[2 * j + 1] = sa[j];
+                } else {
+                    cs[4 * q + j] = ca[j];
+                    sn[4 * q + j] = sa[j];
+                }
+            }
+        }
+    }
+    // The same without the table, for a row that it does not hold.
+    __device__ __forceinline__ void compute(const RopeAppendParams& p, int pos, int c, float* cs, float* sn) const {
+        const int cc = PAIRS == kPairsChunks && c >= C ? c - C : c;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float2 t = 8 * c < p.rotary_dim ? cos_sin_at(p, pair(p, cc, PAIRS == kPairsNext ? j / 2 : j), pos)
+                                                  : make_float2(1.f, 0.f);
+            cs[j] = t.x;
+            sn[j] = t.y;
+        }
+    }
+};
 
 template <int ACT>
 __device__ __forceinline__ uint4 pack(const float* f) {
@@ -199,7 +250,7 @@ __device__ __forceinline__ int64_t slot_of(const RopeAppendParams& p, int t, boo
 // block's table).
 // ---------------------------------------------------------------------------
 template <int ACT, int CACHE, int PAIRS>
-__device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token, int row0, int row1, const float2* table) {
+__device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token, int row0, int row1, const float* table, int table_row) {
     constexpr int U = kLoads;
     const int lane = threadIdx.x & 31;
     const int lpr = p.head_dim / 8, rp = 32 / lpr;
@@ -211,7 +262,7 @@ __device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token,
     int off = 0;
     if (CACHE != kE4M3B && slot >= 0) divmod_u(slot, p.block_size, blk, off);
     float cs[8], sn[8];
-    lane_cos_sin<PAIRS>(p, c, [&](int i) { return table[i]; }, cs, sn);
+    Table<PAIRS>(p).read(p, table, table_row, c, cs, sn);
     const bool turns = 8 * c < p.rotary_dim;
     // heads [a, b) of one kind: src row, rotation or not, and where the result goes
     auto heads = [&](int a, int b, const uint16_t* src, auto turning, auto store) {
@@ -288,71 +339,9 @@ __device__ __forceinline__ void top_bits(const uint4& u, uint32_t& top) {
     }
 }
 
-// ---------------------------------------------------------------------------
-// One run of n tokens of one block and kv head into a block-scaled cache, K or
-// V, by one warp: the maximum over the run, the block's new scale, its other
-// codes where the scale grew, the run's codes.  Up to GROUP loads a lane stay in
-// registers between the maximum and the codes (8 hold a whole 16-token block at
-// head_dim 128); longer runs are read twice.  Rotated keys are computed twice
-// instead of being kept.
-// ---------------------------------------------------------------------------
-template <int ACT, int PAIRS, int GROUP>
-__device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, int n, int64_t blk, int off0, int head,
-                                           bool is_k, const float2* table, int tabled) {
-    const int lane = threadIdx.x & 31;
-    const int lpr = p.head_dim / 8, rp = 32 / lpr;
-    const int r = lane / lpr, c = lane - r * lpr;
-    float* scale = (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + head;
-    const float old = off0 == 0 ? 0.f : *scale;
-    const bool turn = is_k && p.positions != nullptr;
-    const int64_t stride = is_k ? p.k_stride : p.v_stride;
-    const uint16_t* src0 = (is_k ? static_cast<const uint16_t*>(p.k) : static_cast<const uint16_t*>(p.v)) + t0 * stride +
-                           static_cast<int64_t>(head) * p.head_dim;
-    const int half = p.rotary_dim / 2;
-    uint4 u[GROUP];
-    auto load = [&](int g0) {
-#pragma unroll
-        for (int j = 0; j < GROUP; ++j) {
-            const int i = g0 + j * rp + r;
-            u[j] = r < rp && i < n ? *reinterpret_cast<const uint4*>(src0 + i * stride + c * 8)
-                                   : make_uint4(0u, 0u, 0u, 0u);
-        }
-    };
-    auto turned = [&](int i, const uint4& raw, float* x) {  // row i of the run (every lane calls it)
-        const bool have = r < rp && i < n;
-        const int row = have ? i : 0;
-        float cs[8], sn[8];
-        if (row < tabled) {
-            lane_cos_sin<PAIRS>(p, c, [&](int k) { return table[row * half + k]; }, cs, sn);
-        } else {
-            const int pos = p.positions[t0 + row];
-            lane_cos_sin<PAIRS>(p, c, [&](int k) { return cos_sin_at(p, k, pos); }, cs, sn);
-        }
-        __syncwarp();
-        rotate8<ACT, PAIRS>(p, raw, src0 + row * stride, c, lane, have, cs, sn, x);
-    };
-    float top = 0.f;
-    uint32_t tops = 0;
-    for (int g0 = 0; g0 < n; g0 += GROUP * rp) {
-        load(g0);
-#pragma unroll
-        for (int j = 0; j < GROUP; ++j) {
-            if (g0 + j * rp >= n) break;
-            if (turn) {
-                float x[8];
-                turned(g0 + j * rp + r, u[j], x);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float a = fabsf(x[i]);
-                    if (a <= 3.402823466e38f) top = fmaxf(top, a);  // false for NaN and infinity
-                }
-            } else {
-                top_bits<ACT>(u[j], tops);
-            }
-        }
-    }
-    if (!turn) top = act_to_float<ACT>(static_cast<uint16_t>(max(tops & 0xffffu, tops >> 16)));
-    top = warp_max(top);
+// The block's new scale (see the head of the file) for the run's largest
+// element `top`, its old scale being `old` (0: starts afresh).
+__device__ __forceinline__ float new_scale(float top, float old) {
     // top = 1.m * 2^e: 448 = 1.75 * 2^8
     int e = kScaleMinExp;
     if (top > 0.f) {
@@ -361,37 +350,111 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
         e = min(kScaleMaxExp, max(kScaleMinExp, e));
     }
     const float need = __uint_as_float(static_cast<uint32_t>(e + 127) << 23);
-    const float now = old > need ? old : need;  // a scale that is not positive counts as none
+    return old > need ? old : need;  // a scale that is not positive counts as none
+}
+
+// Codes of the block's rows outside [off0, off0 + n) times ratio, by `lanes`
+// lanes of which this is number `first`; 8-byte pieces, loads ahead of stores.
+// (A call: it is rare, and inlined it costs the common path registers.)
+__device__ __noinline__ void requantise(uint8_t* tile, int rows, int lpr, int off0, int n, float ratio, int first,
+                                           int lanes) {
+    constexpr int B = 8;
+    const int pieces = rows * lpr;
+    uint2* at = reinterpret_cast<uint2*>(tile);
+    for (int i0 = first; i0 < pieces; i0 += lanes * B) {
+        uint2 codes[B];
+        bool mine[B];
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            const int i = i0 + lanes * k, row = i / lpr;
+            mine[k] = i < pieces && (row < off0 || row >= off0 + n);
+            codes[k] = mine[k] ? at[i] : make_uint2(0u, 0u);
+        }
+#pragma unroll
+        for (int k = 0; k < B; ++k) {
+            float x[16];
+            Vec16E4M3::to_float(make_uint4(codes[k].x, codes[k].y, 0u, 0u), x);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= ratio;
+            if (mine[k]) at[i0 + lanes * k] = to_codes(x);
+        }
+    }
+}
+
+__device__ __forceinline__ void finite_top(const float* x, float& top) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float a = fabsf(x[j]);
+        if (a <= 3.402823466e38f) top = fmaxf(top, a);  // false for NaN and infinity
+    }
+}
+
+// ---------------------------------------------------------------------------
+// One run of n tokens of one block and kv head into a block-scaled cache, K
+// (TURN: rotated) or V, by one warp: the maximum over the run, the block's new
+// scale, its other codes where the scale grew, the run's codes.  GROUP rows a
+// lane stay in registers between the maximum and the codes, rotated if they
+// turn; runs longer than GROUP passes are read (and rotated) twice.
+// ---------------------------------------------------------------------------
+template <int ACT, int PAIRS, int GROUP, bool TURN>
+__device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, int n, int64_t blk, int off0, int head,
+                                           bool is_k, const float* table, int tabled) {
+    const int lane = threadIdx.x & 31;
+    const int lpr = p.head_dim / 8, rp = 32 / lpr;
+    const int r = lane / lpr, c = lane - r * lpr;
+    float* scale = (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + head;
+    const float old = off0 == 0 ? 0.f : *scale;
+    const int64_t stride = is_k ? p.k_stride : p.v_stride;
+    const uint16_t* src0 = (is_k ? static_cast<const uint16_t*>(p.k) : static_cast<const uint16_t*>(p.v)) + t0 * stride +
+                           static_cast<int64_t>(head) * p.head_dim;
+    constexpr int AHEAD = TURN && GROUP > 4 ? 4 : GROUP;  // loads in flight (rotated rows take the registers)
+    uint4 u[TURN ? AHEAD : GROUP];
+    float x[TURN ? GROUP : 1][8];
+    auto load = [&](int g0) {
+#pragma unroll
+        for (int a = 0; a < GROUP; a += AHEAD) {
+            if (g0 + a * rp >= n) break;
+#pragma unroll
+            for (int j = 0; j < AHEAD; ++j) {
+                const int i = g0 + (a + j) * rp + r;
+                u[j] = r < rp && i < n ? *reinterpret_cast<const uint4*>(src0 + i * stride + c * 8)
+                                       : make_uint4(0u, 0u, 0u, 0u);
+            }
+            if constexpr (TURN) {
+#pragma unroll
+                for (int j = 0; j < AHEAD; ++j) {
+                    if (g0 + (a + j) * rp >= n) break;
+                    const int i = g0 + (a + j) * rp + r;
+                    const bool have = r < rp && i < n;
+                    const int row = have ? i : 0;
+                    float cs[8], sn[8];
+                    if (row < tabled) Table<PAIRS>(p).read(p, table, row, c, cs, sn);
+                    else Table<PAIRS>(p).compute(p, p.positions[t0 + row], c, cs, sn);
+                    __syncwarp();
+                    rotate8<ACT, PAIRS>(p, u[j], src0 + row * stride, c, lane, have, cs, sn, x[a + j]);
+                }
+            }
+        }
+    };
+    float top = 0.f;
+    uint32_t tops = 0;
+    for (int g0 = 0; g0 < n; g0 += GROUP * rp) {
+        load(g0);
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+            if (g0 + j * rp >= n) break;
+            if constexpr (TURN) finite_top(x[j], top);
+            else top_bits<ACT>(u[j], tops);
+        }
+    }
+    if (!TURN) top = act_to_float<ACT>(static_cast<uint16_t>(max(tops & 0xffffu, tops >> 16)));
+    const float now = new_scale(warp_max(top), old);
     uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
                     (blk * p.num_kv_heads + head) * p.block_size * p.head_dim;
     if (now != old) {
         __syncwarp();  // every lane has read the old scale
         if (lane == 0) *scale = now;
-        if (old > 0.f) {
-            const float ratio = __fdiv_rn(old, now);
-            // 8-byte pieces of the block, loads ahead of the stores
-            constexpr int B = 8;
-            const int pieces = p.block_size * lpr;
-            uint2* at = reinterpret_cast<uint2*>(tile);
-            for (int i0 = lane; i0 < pieces; i0 += 32 * B) {
-                uint2 codes[B];
-                bool mine[B];
-#pragma unroll
-                for (int k = 0; k < B; ++k) {
-                    const int i = i0 + 32 * k, row = i / lpr;
-                    mine[k] = i < pieces && (row < off0 || row >= off0 + n);
-                    codes[k] = mine[k] ? at[i] : make_uint2(0u, 0u);
-                }
-#pragma unroll
-                for (int k = 0; k < B; ++k) {
-                    float x[16];
-                    Vec16E4M3::to_float(make_uint4(codes[k].x, codes[k].y, 0u, 0u), x);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[j] *= ratio;
-                    if (mine[k]) at[i0 + 32 * k] = to_codes(x);
-                }
-            }
-        }
+        if (old > 0.f) requantise(tile, p.block_size, lpr, off0, n, __fdiv_rn(old, now), lane, 32);
     }
     for (int g0 = 0; g0 < n; g0 += GROUP * rp) {
         if (n > GROUP * rp) load(g0);
@@ -399,69 +462,128 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
         for (int j = 0; j < GROUP; ++j) {
             if (g0 + j * rp >= n) break;
             const int i = g0 + j * rp + r;
-            float x[8];
-            if (turn) turned(i, u[j], x);
-            else Vec16<ACT>::to_float(u[j], x);
+            float y[8];
+            if constexpr (TURN) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = x[j][k];
+            } else {
+                Vec16<ACT>::to_float(u[j], y);
+            }
             if (r >= rp || i >= n) continue;
-            divide8(x, now);
-            *reinterpret_cast<uint2*>(tile + (off0 + i) * p.head_dim + c * 8) = to_codes(x);
+            divide8(y, now);
+            *reinterpret_cast<uint2*>(tile + (off0 + i) * p.head_dim + c * 8) = to_codes(y);
         }
     }
 }
 
-// Runs that start in window w of `window` <= 32 tokens: block `part` of `split`
-// takes its share of each run's (head, K or V) items, one a warp.  cos and sin
-// of the run's tokens are computed once into shared memory.
+// The same for a run of one token (a decode step), where a row takes lpr lanes
+// (a power of two): a warp takes 32 / lpr (head, K or V) items from item0 on.
+template <int ACT, int PAIRS>
+__device__ __forceinline__ void single_rows(const RopeAppendParams& p, int t0, int64_t blk, int off0, int item0,
+                                            const float* table) {
+    const int lane = threadIdx.x & 31;
+    const int lpr = p.head_dim / 8;
+    const int r = lane / lpr, c = lane - r * lpr;
+    const int it = item0 + r;
+    const bool have = it < 2 * p.num_kv_heads, is_k = it < p.num_kv_heads;
+    const int head = !have ? 0 : is_k ? it : it - p.num_kv_heads;
+    float* scale = (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + head;
+    const float old = off0 == 0 || !have ? 0.f : *scale;
+    const uint16_t* src = (is_k ? static_cast<const uint16_t*>(p.k) + t0 * p.k_stride
+                                : static_cast<const uint16_t*>(p.v) + t0 * p.v_stride) +
+                          static_cast<int64_t>(head) * p.head_dim;
+    const uint4 u = have ? *reinterpret_cast<const uint4*>(src + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+    float x[8];
+    if constexpr (PAIRS != kPairsNone) {
+        float cs[8], sn[8];
+        Table<PAIRS>(p).read(p, table, 0, c, cs, sn);
+        rotate8<ACT, PAIRS>(p, u, src, c, lane, have && is_k, cs, sn, x);
+        if (!is_k) Vec16<ACT>::to_float(u, x);
+    } else {
+        Vec16<ACT>::to_float(u, x);
+    }
+    float top = 0.f;
+    finite_top(x, top);
+    for (int off = lpr / 2; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    if (!have) return;
+    const float now = new_scale(top, old);
+    uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
+                    (blk * p.num_kv_heads + head) * p.block_size * p.head_dim;
+    if (now != old) {
+        if (c == 0) *scale = now;  // (every lane read the old one before the shuffles)
+        if (old > 0.f) requantise(tile, p.block_size, lpr, off0, 1, __fdiv_rn(old, now), c, lpr);
+    }
+    divide8(x, now);
+    *reinterpret_cast<uint2*>(tile + off0 * p.head_dim + c * 8) = to_codes(x);
+}
+
+// Runs that start in window w of `window` < 32 tokens: block `part` of `split`
+// takes its share of each run's (head, K or V) items.  cos and sin of the run's
+// tokens are computed once into shared memory.
 template <int ACT, int PAIRS, int GROUP>
 __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int window, int w, int part, int split,
-                                             float2* table) {
+                                             float* table) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int half = p.rotary_dim / 2;
-    const int t = w * window + lane;
-    bool bad = false, unused = false;
-    const int64_t slot = lane < window ? slot_of(p, t, &bad) : -1;
-    const int64_t prev = slot_of(p, t - 1, &unused);
-    if (bad && warp == 0 && part == 0) atomicOr(p.err, kErrBadSlot);
+    const int lpr = p.head_dim / 8;
+    // lane l holds token first - 1 + l: the window's tokens, the one before and some after
+    const int first = w * window;
+    bool bad = false;
+    const int64_t slot = slot_of(p, first - 1 + lane, &bad);
+    if (bad && lane >= 1 && lane <= window && warp == 0 && part == 0) atomicOr(p.err, kErrBadSlot);
     int64_t blk = 0;
     int off = 0;
     if (slot >= 0) divmod_u(slot, p.block_size, blk, off);
-    unsigned leaders = __ballot_sync(0xffffffffu, slot >= 0 && (prev != slot - 1 || off == 0));
-    for (; leaders; leaders &= leaders - 1) {
+    // joined: the token continues the run of the one before it
+    const int64_t prev = __shfl_up_sync(0xffffffffu, slot, 1);
+    const unsigned joined = __ballot_sync(0xffffffffu, lane > 0 && slot >= 0 && prev == slot - 1 && off != 0);
+    const unsigned in_window = __ballot_sync(0xffffffffu, lane >= 1 && lane <= window && slot >= 0);
+    for (unsigned leaders = in_window & ~joined; leaders; leaders &= leaders - 1) {
         const int at = __ffs(leaders) - 1;
-        const int t0 = w * window + at;
+        const int t0 = first - 1 + at;
         const int64_t s0 = __shfl_sync(0xffffffffu, slot, at), b0 = __shfl_sync(0xffffffffu, blk, at);
         const int off0 = __shfl_sync(0xffffffffu, off, at);
-        // the run's length: up to the end of the block
-        int n = 1;
-        for (int base = 1; base < p.block_size - off0; base += 32) {
-            const int k = base + lane;
-            const bool in = k < p.block_size - off0 && slot_of(p, t0 + k, &unused) == s0 + k;
-            const unsigned out = __ballot_sync(0xffffffffu, !in);
-            n = base + (out ? __ffs(out) - 1 : 32);
-            if (out) break;
+        // the run's length: the lanes joined after it, and further where it reaches the last lane
+        const unsigned after = at < 31 ? ~(joined >> (at + 1)) : ~0u;
+        int n = 1 + min(__ffs(after) - 1, 31 - at);
+        if (at + n == 32) {
+            for (bool more = n < p.block_size - off0; more;) {
+                bool unused = false;
+                const bool in = n + lane < p.block_size - off0 && slot_of(p, t0 + n + lane, &unused) == s0 + n + lane;
+                const unsigned out = __ballot_sync(0xffffffffu, !in);
+                n += out ? __ffs(out) - 1 : 32;
+                more = out == 0;
+            }
         }
         int tabled = 0;
-        if (p.positions) {
-            tabled = min(n, kTable / half);
+        if constexpr (PAIRS != kPairsNone) {
+            const Table<PAIRS> tab(p);
+            tabled = min(n, kTable / tab.row_floats());
             __syncthreads();  // the run before is done with the table
-            for (int i = threadIdx.x; i < tabled * half; i += kWarps * 32) {
-                const int k = i / half;
-                table[i] = cos_sin_at(p, i - k * half, p.positions[t0 + k]);
-            }
+            tab.fill(p, table, t0, tabled);
             __syncthreads();
         }
-        for (int it = part * kWarps + warp; it < 2 * p.num_kv_heads; it += split * kWarps) {
+        const int items = 2 * p.num_kv_heads;
+        if (GROUP == 1 && n == 1 && (lpr & (lpr - 1)) == 0) {
+            const int rp = 32 / lpr;
+            for (int it = (part * kWarps + warp) * rp; it < items; it += split * kWarps * rp)
+                single_rows<ACT, PAIRS>(p, t0, b0, off0, it, table);
+            continue;
+        }
+        for (int it = part * kWarps + warp; it < items; it += split * kWarps) {
             const bool is_k = it < p.num_kv_heads;
-            scaled_run<ACT, PAIRS, GROUP>(p, t0, n, b0, off0, is_k ? it : it - p.num_kv_heads, is_k, table, tabled);
+            const int head = is_k ? it : it - p.num_kv_heads;
+            if (PAIRS != kPairsNone && is_k)
+                scaled_run<ACT, PAIRS, GROUP, PAIRS != kPairsNone>(p, t0, n, b0, off0, head, true, table, tabled);
+            else
+                scaled_run<ACT, PAIRS, GROUP, false>(p, t0, n, b0, off0, head, is_k, table, tabled);
         }
     }
 }
 
 // Items (token, part of its rows) of block `cta`, one a warp: at most kWarps tokens.
 template <int ACT, int CACHE, int PAIRS>
-__device__ __forceinline__ void rows_block(const RopeAppendParams& p, int cta, int parts, int per, int rows, float2* table) {
+__device__ __forceinline__ void rows_block(const RopeAppendParams& p, int cta, int parts, int per, int rows, float* table) {
     const int warp = threadIdx.x >> 5;
-    const int half = p.rotary_dim / 2;
     const int64_t item0 = static_cast<int64_t>(cta) * kWarps;
     int64_t token0, token, last;
     int unused, part;
@@ -469,14 +591,11 @@ __device__ __forceinline__ void rows_block(const RopeAppendParams& p, int cta, i
     divmod_u(item0 + warp, parts, token, part);
     divmod_u(item0 + kWarps - 1, parts, last, unused);
     const int tokens = static_cast<int>(min(last, static_cast<int64_t>(p.num_tokens) - 1) - token0) + 1;
-    for (int i = threadIdx.x; i < tokens * half; i += kWarps * 32) {
-        const int k = i / half;
-        table[i] = cos_sin_at(p, i - k * half, p.positions[token0 + k]);
-    }
+    Table<PAIRS>(p).fill(p, table, token0, tokens);
     __syncthreads();
     if (token >= p.num_tokens || p.positions[token] < 0) return;  // padding: q_out keeps its row
     plain_rows<ACT, CACHE, PAIRS>(p, static_cast<int>(token), part * per, min(rows, part * per + per),
-                                  table + static_cast<int>(token - token0) * half);
+                                  table, static_cast<int>(token - token0));
 }
 
 // How a launch divides its work.
@@ -487,7 +606,7 @@ struct Split {
 
 template <int ACT, int CACHE, int PAIRS>
 __global__ void __launch_bounds__(kWarps * 32, 3) rope_rows_kernel(const RopeAppendParams p, const Split d) {
-    __shared__ float2 table[kTable / 2];
+    __shared__ __align__(16) float table[kTable];
     rows_block<ACT, CACHE, PAIRS>(p, blockIdx.x, d.parts, d.per, d.rows, table);
     // launched beside the kernel that stores the keys and values: done when that is done
     if (CACHE == kE4M3B) asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -496,28 +615,28 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_rows_kernel(const RopeApp
 // Prompts: runs of many tokens.
 template <int ACT, int PAIRS>
 __global__ void __launch_bounds__(kWarps * 32, 2) scaled_runs_kernel(const RopeAppendParams p, const Split d) {
-    __shared__ float2 table[kTable];
+    __shared__ __align__(16) float table[PAIRS == kPairsNone ? 4 : kTable];
     asm volatile("griddepcontrol.launch_dependents;");
     const int w = blockIdx.x / d.share;
-    scaled_block<ACT, PAIRS, 8>(p, d.window, w, blockIdx.x - w * d.share, d.share, table);
+    scaled_block<ACT, PAIRS, PAIRS == kPairsNone ? 16 : 8>(p, d.window, w, blockIdx.x - w * d.share, d.share, table);
 }
 
 // Few tokens (a decode step): runs and rows in one launch, more warps at a time.
 template <int ACT, int PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 4) scaled_step_kernel(const RopeAppendParams p, const Split d) {
-    __shared__ float2 table[kTable];
+__global__ void __launch_bounds__(kWarps * 32, 3) scaled_step_kernel(const RopeAppendParams p, const Split d) {
+    __shared__ __align__(16) float table[PAIRS == kPairsNone ? 4 : kTable];
     const int cta = blockIdx.x, runs = d.windows * d.share;
     if (cta < runs) {
         const int w = cta / d.share;
         scaled_block<ACT, PAIRS, 1>(p, d.window, w, cta - w * d.share, d.share, table);
     } else {
-        rows_block<ACT, kE4M3B, PAIRS>(p, cta - runs, d.parts, d.per, d.rows, table);
+        if constexpr (PAIRS != kPairsNone) rows_block<ACT, kE4M3B, PAIRS>(p, cta - runs, d.parts, d.per, d.rows, table);
     }
 }
 
 template <int ACT, int CACHE, int PAIRS>
 cudaError_t launch(const RopeAppendParams& p, cudaStream_t stream) {
-    static_assert(kWarps * 128 <= kTable / 2, "a block's tokens fit the table at rotary_dim 256");
+    static_assert(kWarps * 2 * 8 * 32 <= kTable, "a block's tokens fit the table at rotary_dim 256");
     const int rp = 32 / (p.head_dim / 8);
     Split d{};
     d.rows = p.positions == nullptr ? 0 : CACHE == kE4M3B ? p.num_q_heads : p.num_q_heads + 2 * p.num_kv_heads;
@@ -535,10 +654,11 @@ cudaError_t launch(const RopeAppendParams& p, cudaStream_t stream) {
         return cudaGetLastError();
     } else {
         // prompts: a window starts a run or a few, whose heads one block works off; few tokens: one token a window
-        d.window = 32;
+        d.window = 16;
         while (d.window > 1 && (p.num_tokens + d.window - 1) / d.window < kFill) d.window /= 2;
         d.windows = (p.num_tokens + d.window - 1) / d.window;
-        const int most = (2 * p.num_kv_heads + kWarps - 1) / kWarps;
+        const int per_block = d.window == 1 && (rp & (rp - 1)) == 0 ? kWarps * rp : kWarps;
+        const int most = (2 * p.num_kv_heads + per_block - 1) / per_block;
         d.share = 1;
         const int fill = d.window == 1 ? 4 * kFill : kFill;
         while (d.share < most && static_cast<int64_t>(d.windows) * d.share < fill) ++d.share;
@@ -550,23 +670,30 @@ cudaError_t launch(const RopeAppendParams& p, cudaStream_t stream) {
         }
         scaled_runs_kernel<ACT, PAIRS><<<static_cast<unsigned>(run_blocks), threads, 0, stream>>>(p, d);
         cudaError_t e = cudaGetLastError();
-        if (e != cudaSuccess || row_blocks == 0) return e;
-        cudaLaunchConfig_t cfg = {};
-        cfg.gridDim = dim3(static_cast<unsigned>(row_blocks));
-        cfg.blockDim = dim3(threads);
-        cfg.stream = stream;
-        cudaLaunchAttribute attr[1];
-        attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-        attr[0].val.programmaticStreamSerializationAllowed = 1;
-        cfg.attrs = attr;
-        cfg.numAttrs = 1;
-        return cudaLaunchKernelEx(&cfg, rope_rows_kernel<ACT, CACHE, PAIRS>, p, d);
+        if constexpr (PAIRS != kPairsNone) {
+            if (e != cudaSuccess || row_blocks == 0) return e;
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(static_cast<unsigned>(row_blocks));
+            cfg.blockDim = dim3(threads);
+            cfg.stream = stream;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+            attr[0].val.programmaticStreamSerializationAllowed = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            e = cudaLaunchKernelEx(&cfg, rope_rows_kernel<ACT, CACHE, PAIRS>, p, d);
+        }
+        return e;
     }
 }
 
 template <int ACT, int CACHE>
 cudaError_t by_pairs(const RopeAppendParams& p, cudaStream_t s) {
-    if (p.positions == nullptr || p.interleaved) return launch<ACT, CACHE, kPairsNext>(p, s);
+    if (p.positions == nullptr) {
+        if constexpr (CACHE == kE4M3B) return launch<ACT, CACHE, kPairsNone>(p, s);
+        else return cudaErrorInvalidValue;
+    }
+    if (p.interleaved) return launch<ACT, CACHE, kPairsNext>(p, s);
     return p.rotary_dim % 16 == 0 ? launch<ACT, CACHE, kPairsChunks>(p, s) : launch<ACT, CACHE, kPairsApart>(p, s);
 }
 
