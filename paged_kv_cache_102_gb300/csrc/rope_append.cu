@@ -391,17 +391,21 @@ __device__ __forceinline__ void finite_top(const float* x, float& top) {
 
 // ---------------------------------------------------------------------------
 // One run of n tokens of one block and kv head into a block-scaled cache, K
-// (TURN: rotated) or V, by one warp: the maximum over the run, the block's new
-// scale, its other codes where the scale grew, the run's codes.  GROUP rows a
-// lane stay in registers between the maximum and the codes, rotated if they
-// turn; runs longer than GROUP passes are read (and rotated) twice.
+// (TURN: rotated) or V, by W warps (one, or two that take every other pass and
+// meet for the maximum): the maximum over the run, the block's new scale, its
+// other codes where the scale grew, the run's codes.  GROUP rows a lane stay in
+// registers between the maximum and the codes, rotated if they turn; runs
+// longer than GROUP passes are read (and rotated) twice.
 // ---------------------------------------------------------------------------
-template <int ACT, int PAIRS, int GROUP, bool TURN>
+template <int ACT, int PAIRS, int GROUP, int W, bool TURN>
 __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, int n, int64_t blk, int off0, int head,
-                                           bool is_k, const float* table, int tabled) {
-    const int lane = threadIdx.x & 31;
-    const int lpr = p.head_dim / 8, rp = 32 / lpr;
-    const int r = lane / lpr, c = lane - r * lpr;
+                                           bool is_k, const float* table, int tabled, float* tops2) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lpr = p.head_dim / 8, rows = 32 / lpr;  // rows a warp's pass
+    const int rp = W * rows;                          // rows a pass of all W warps
+    const int lane_row = lane / lpr, c = lane - lane_row * lpr;
+    const bool idle = lane_row >= rows;
+    const int r = (W == 2 ? (warp & 1) * rows : 0) + lane_row;
     float* scale = (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + head;
     const float old = off0 == 0 ? 0.f : *scale;
     const int64_t stride = is_k ? p.k_stride : p.v_stride;
@@ -417,7 +421,7 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
 #pragma unroll
             for (int j = 0; j < AHEAD; ++j) {
                 const int i = g0 + (a + j) * rp + r;
-                u[j] = r < rp && i < n ? *reinterpret_cast<const uint4*>(src0 + i * stride + c * 8)
+                u[j] = !idle && i < n ? *reinterpret_cast<const uint4*>(src0 + i * stride + c * 8)
                                        : make_uint4(0u, 0u, 0u, 0u);
             }
             if constexpr (TURN) {
@@ -425,7 +429,7 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
                 for (int j = 0; j < AHEAD; ++j) {
                     if (g0 + (a + j) * rp >= n) break;
                     const int i = g0 + (a + j) * rp + r;
-                    const bool have = r < rp && i < n;
+                    const bool have = !idle && i < n;
                     const int row = have ? i : 0;
                     float cs[8], sn[8];
                     if (row < tabled) Table<PAIRS>(p).read(p, table, row, c, cs, sn);
@@ -448,13 +452,20 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
         }
     }
     if (!TURN) top = act_to_float<ACT>(static_cast<uint16_t>(max(tops & 0xffffu, tops >> 16)));
-    const float now = new_scale(warp_max(top), old);
+    top = warp_max(top);
+    if constexpr (W == 2) {  // the pair's other half (also: both have read the old scale)
+        if (lane == 0) tops2[warp] = top;
+        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+        top = fmaxf(top, tops2[warp ^ 1]);
+    }
+    const float now = new_scale(top, old);
     uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
                     (blk * p.num_kv_heads + head) * p.block_size * p.head_dim;
     if (now != old) {
         __syncwarp();  // every lane has read the old scale
-        if (lane == 0) *scale = now;
-        if (old > 0.f) requantise(tile, p.block_size, lpr, off0, n, __fdiv_rn(old, now), lane, 32);
+        if (lane == 0 && (W == 1 || !(warp & 1))) *scale = now;
+        if (old > 0.f)
+            requantise(tile, p.block_size, lpr, off0, n, __fdiv_rn(old, now), W == 2 ? (warp & 1) * 32 + lane : lane, 32 * W);
     }
     for (int g0 = 0; g0 < n; g0 += GROUP * rp) {
         if (n > GROUP * rp) load(g0);
@@ -469,7 +480,7 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, in
             } else {
                 Vec16<ACT>::to_float(u[j], y);
             }
-            if (r >= rp || i >= n) continue;
+            if (idle || i >= n) continue;
             divide8(y, now);
             *reinterpret_cast<uint2*>(tile + (off0 + i) * p.head_dim + c * 8) = to_codes(y);
         }
@@ -520,9 +531,10 @@ __device__ __forceinline__ void single_rows(const RopeAppendParams& p, int t0, i
 // Runs that start in window w of `window` < 32 tokens: block `part` of `split`
 // takes its share of each run's (head, K or V) items.  cos and sin of the run's
 // tokens are computed once into shared memory.
-template <int ACT, int PAIRS, int GROUP>
+template <int ACT, int PAIRS, int GROUP, int W>
 __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int window, int w, int part, int split,
                                              float* table) {
+    __shared__ float tops2[2 * kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lpr = p.head_dim / 8;
     // lane l holds token first - 1 + l: the window's tokens, the one before and some after
@@ -569,14 +581,18 @@ __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int wind
                 single_rows<ACT, PAIRS>(p, t0, b0, off0, it, table);
             continue;
         }
-        for (int it = part * kWarps + warp; it < items; it += split * kWarps) {
+        constexpr int TEAMS = kWarps / W;
+        int flip = 0;  // the pair's maxima alternate between two places
+        for (int it = part * TEAMS + warp / W; it < items; it += split * TEAMS, flip ^= kWarps) {
             const bool is_k = it < p.num_kv_heads;
             const int head = is_k ? it : it - p.num_kv_heads;
             if (PAIRS != kPairsNone && is_k)
-                scaled_run<ACT, PAIRS, GROUP, PAIRS != kPairsNone>(p, t0, n, b0, off0, head, true, table, tabled);
+                scaled_run<ACT, PAIRS, GROUP, W, PAIRS != kPairsNone>(p, t0, n, b0, off0, head, true, table, tabled,
+                                                                      tops2 + flip);
             else
-                scaled_run<ACT, PAIRS, GROUP, false>(p, t0, n, b0, off0, head, is_k, table, tabled);
+                scaled_run<ACT, PAIRS, GROUP, W, false>(p, t0, n, b0, off0, head, is_k, table, tabled, tops2 + flip);
         }
+        if (W == 2) __syncthreads();  // the places of the last maxima
     }
 }
 
@@ -614,11 +630,11 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_rows_kernel(const RopeApp
 
 // Prompts: runs of many tokens.
 template <int ACT, int PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 2) scaled_runs_kernel(const RopeAppendParams p, const Split d) {
+__global__ void __launch_bounds__(kWarps * 32, 3) scaled_runs_kernel(const RopeAppendParams p, const Split d) {
     __shared__ __align__(16) float table[PAIRS == kPairsNone ? 4 : kTable];
     asm volatile("griddepcontrol.launch_dependents;");
     const int w = blockIdx.x / d.share;
-    scaled_block<ACT, PAIRS, PAIRS == kPairsNone ? 16 : 8>(p, d.window, w, blockIdx.x - w * d.share, d.share, table);
+    scaled_block<ACT, PAIRS, PAIRS == kPairsNone ? 8 : 4, 2>(p, d.window, w, blockIdx.x - w * d.share, d.share, table);
 }
 
 // Few tokens (a decode step): runs and rows in one launch, more warps at a time.
@@ -628,7 +644,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) scaled_step_kernel(const RopeA
     const int cta = blockIdx.x, runs = d.windows * d.share;
     if (cta < runs) {
         const int w = cta / d.share;
-        scaled_block<ACT, PAIRS, 1>(p, d.window, w, cta - w * d.share, d.share, table);
+        scaled_block<ACT, PAIRS, 1, 1>(p, d.window, w, cta - w * d.share, d.share, table);
     } else {
         if constexpr (PAIRS != kPairsNone) rows_block<ACT, kE4M3B, PAIRS>(p, cta - runs, d.parts, d.per, d.rows, table);
     }
