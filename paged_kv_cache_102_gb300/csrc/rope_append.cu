@@ -66,10 +66,11 @@ __device__ __forceinline__ uint64_t turn_of(float w) {
 
 // cos and sin of a phase in 64-bit turns.
 __device__ __forceinline__ float2 cos_sin_turns(uint64_t phase) {
-    const uint64_t q = (phase + (1ull << 61)) >> 62;  // nearest quarter turn
-    const int64_t r = static_cast<int64_t>(phase - (q << 62));
+    const uint32_t q = static_cast<uint32_t>((phase + (1ull << 61)) >> 62);  // nearest quarter turn
+    // the rest, to 2^-32 turns (7e-10 of the pair's magnitude, a hundredth of binary32's rounding)
+    const int r = static_cast<int>((static_cast<uint32_t>(phase >> 32) - (q << 30)));
     float s0, c0;
-    sincospif(__ll2float_rn(r) * 0x1p-63f, &s0, &c0);  // r * 2^-63 half turns, at most 1/4
+    sincospif(static_cast<float>(r) * 0x1p-31f, &s0, &c0);  // half turns, at most 1/4
     const bool odd = q & 1;
     const float cc = odd ? s0 : c0, ss = odd ? c0 : s0;
     return make_float2((q == 1 || q == 2) ? -cc : cc, (q & 2) ? -ss : ss);
@@ -100,13 +101,16 @@ struct Table {
     }
     // All threads of the block: rows [0, rows) for tokens t0, t0 + 1, ...
     __device__ __forceinline__ void fill(const RopeAppendParams& p, float* table, int64_t t0, int rows) const {
-        const int n = J * C;
-        for (int i = threadIdx.x; i < rows * n; i += kWarps * 32) {
-            const int row = i / n, k = i - row * n, c = k / J, j = k - c * J;
-            const float2 cs = cos_sin_at(p, pair(p, c, j), p.positions[t0 + row]);
-            float* at = table + row * 2 * n + ((j >> 2) * C + c) * 4 + (j & 3);
-            at[0] = cs.x;
-            at[n] = cs.y;
+        // a thread stays with one entry of a row (n <= 256 of them)
+        const int n = J * C, teams = kWarps * 32 / n, team = threadIdx.x / n;
+        const int k = threadIdx.x - team * n, c = k / J, j = k - c * J;
+        if (team >= teams) return;
+        const uint64_t turn = turn_of(p.inv_freq[pair(p, c, j)]);
+        float* at = table + ((j >> 2) * C + c) * 4 + (j & 3);
+        for (int row = team; row < rows; row += teams) {
+            const float2 cs = cos_sin_turns(turn * static_cast<uint64_t>(static_cast<int64_t>(p.positions[t0 + row])));
+            at[row * 2 * n] = cs.x * p.factor;
+            at[row * 2 * n + n] = cs.y * p.factor;
         }
     }
     // cos and sin of the 8 channels of chunk c; 1 and 0 for a chunk that does not turn.
@@ -169,38 +173,45 @@ __device__ __forceinline__ uint4 pack(const float* f) {
 
 // x = the rotated channels of chunk c (raw bits u of row `row`).  Every lane of
 // the warp calls it.  The products and their sum are rounded one by one, so
-// that both terms of a channel enter alike.
+// that both terms of a channel enter alike.  Half layout in whole chunks: the
+// sign of the second term is put into the partner's bits, and a chunk that
+// does not turn gets -0 for a partner (x * 1 + -0 * 0 is x, its sign too).
 template <int ACT, int PAIRS>
 __device__ __forceinline__ void rotate8(const RopeAppendParams& p, const uint4& u, const uint16_t* row, int c, int lane,
                                         bool live, const float* cs, const float* sn, float* x) {
     const int rot = p.rotary_dim, half = rot / 2;
     float y[8];
     Vec16<ACT>::to_float(u, x);
-    if (PAIRS == kPairsNext) {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) y[j] = x[j ^ 1];
-    } else if (PAIRS == kPairsChunks) {
+    if constexpr (PAIRS == kPairsChunks) {
         const int hc = half / 8;
-        const int src = c < hc ? lane + hc : (c < 2 * hc ? lane - hc : lane);
+        const bool turns = c < 2 * hc;
+        const int src = c < hc ? lane + hc : (turns ? lane - hc : lane);
+        const uint32_t keep = turns ? ~0u : 0u, flip = c < hc || !turns ? 0x80008000u : 0u;
         uint4 v;
-        v.x = __shfl_sync(0xffffffffu, u.x, src);
-        v.y = __shfl_sync(0xffffffffu, u.y, src);
-        v.z = __shfl_sync(0xffffffffu, u.z, src);
-        v.w = __shfl_sync(0xffffffffu, u.w, src);
+        v.x = (__shfl_sync(0xffffffffu, u.x, src) & keep) ^ flip;
+        v.y = (__shfl_sync(0xffffffffu, u.y, src) & keep) ^ flip;
+        v.z = (__shfl_sync(0xffffffffu, u.z, src) & keep) ^ flip;
+        v.w = (__shfl_sync(0xffffffffu, u.w, src) & keep) ^ flip;
         Vec16<ACT>::to_float(v, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[j] = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(y[j], sn[j]));
+        return;
+    }
+    if constexpr (PAIRS == kPairsNext) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) y[j] = (j & 1) ? x[j ^ 1] : -x[j ^ 1];
     } else {
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
             const int e = 8 * c + j;
             y[j] = live && e < rot ? act_to_float<ACT>(row[e < half ? e + half : e - half]) : 0.f;
+            if (e < half) y[j] = -y[j];
         }
     }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-        const int e = 8 * c + j;
-        const bool first = PAIRS == kPairsNext ? !(j & 1) : e < half;
-        const float a = __fmul_rn(x[j], cs[j]), b = __fmul_rn(y[j], first ? -sn[j] : sn[j]);
-        if (e < rot) x[j] = __fadd_rn(a, b);
+        const float a = __fadd_rn(__fmul_rn(x[j], cs[j]), __fmul_rn(y[j], sn[j]));
+        if (8 * c + j < rot) x[j] = a;
     }
 }
 
@@ -215,19 +226,26 @@ __device__ __forceinline__ uint2 to_codes(const float* x) {
     return make_uint2(w[0], w[1]);
 }
 
-// x / s: the product with an exact reciprocal when s is a power of two within
-// 2^-126 .. 2^126 (the same value, without a division), else the quotient.
-__device__ __forceinline__ void divide8(float* x, float s) {
-    const uint32_t b = __float_as_uint(s), e = b >> 23;
-    if ((b & 0x7fffffu) == 0 && e >= 1 && e <= 253) {
-        const float r = __uint_as_float((254u - e) << 23);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] *= r;
-    } else {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], s);
+// Division by s: a product with the exact reciprocal when s is a power of two
+// within 2^-126 .. 2^126 (the same value, without a division), else a quotient.
+struct Divisor {
+    float s, r;
+    bool exact;
+    __device__ __forceinline__ explicit Divisor(float scale) : s(scale) {
+        const uint32_t b = __float_as_uint(s), e = b >> 23;
+        exact = (b & 0x7fffffu) == 0 && e >= 1 && e <= 253;
+        r = __uint_as_float((254u - e) << 23);
     }
-}
+    __device__ __forceinline__ void divide8(float* x) const {
+        if (exact) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] *= r;
+        } else {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) x[j] = __fdiv_rn(x[j], s);
+        }
+    }
+};
 
 // Token t's slot: -1 for padding (negative slot or position) and for a slot
 // outside the pool (*bad is set).
@@ -305,7 +323,7 @@ __device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token,
             if constexpr (CACHE == ACT) {
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(cache) + at(h)) = raw ? u : pack<ACT>(x);
             } else {
-                divide8(x, *scale);
+                Divisor(*scale).divide8(x);
                 *reinterpret_cast<uint2*>(static_cast<uint8_t*>(cache) + at(h)) = to_codes(x);
             }
         };
@@ -320,21 +338,21 @@ __device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token,
     }
 }
 
-// Largest finite |x| among eight 16-bit elements and the pairwise maxima `top`
-// so far (bit patterns without the sign: both types order as integers).
-// Infinities and NaN are at or above kInf and are taken out.
+// tops = elementwise max(tops, |x|) of eight 16-bit elements, in pairs (a NaN
+// does not enter).
 template <int ACT>
-__device__ __forceinline__ void top_bits(const uint4& u, uint32_t& top) {
-    constexpr uint32_t kInf = ACT == kBF16 ? 0x7f80u : 0x7c00u;
-    const uint32_t w[4] = {u.x & 0x7fff7fffu, u.y & 0x7fff7fffu, u.z & 0x7fff7fffu, u.w & 0x7fff7fffu};
-    const uint32_t m = __vmaxu2(__vmaxu2(w[0], w[1]), __vmaxu2(w[2], w[3]));
-    if (max(m & 0xffffu, m >> 16) < kInf) {
-        top = __vmaxu2(top, m);
-    } else {
+__device__ __forceinline__ void top_pairs(const uint4& u, uint32_t& tops) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t a = w[i] & 0xffffu, b = w[i] >> 16;
-            top = __vmaxu2(top, (a < kInf ? a : 0u) | (b < kInf ? b << 16 : 0u));
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (ACT == kBF16) {
+            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&tops),
+                                             __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+            tops = *reinterpret_cast<const uint32_t*>(&m);
+        } else {
+            const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&tops),
+                                      __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+            tops = *reinterpret_cast<const uint32_t*>(&m);
         }
     }
 }
@@ -389,100 +407,136 @@ __device__ __forceinline__ void finite_top(const float* x, float& top) {
     }
 }
 
+// Where a run goes and comes from, for one head and K or V.
+struct RunRows {
+    const uint16_t* src;  // first row
+    int64_t stride;
+    float* scale;
+    uint8_t* tile;  // the block's codes
+    const int32_t* positions;  // of the run's tokens; null: no rotation
+};
+
+// Row i of a run in chunk c of this lane as floats, rotated if it turns (every
+// lane of the warp calls it).
+template <int ACT, int PAIRS>
+__device__ __forceinline__ void run_row(const RopeAppendParams& p, const RunRows& run, int i, int c, bool have, float* x) {
+    const uint16_t* row = run.src + (have ? i : 0) * run.stride;
+    const uint4 u = have ? *reinterpret_cast<const uint4*>(row + c * 8) : make_uint4(0u, 0u, 0u, 0u);
+    if (PAIRS != kPairsNone && run.positions) {
+        float cs[8], sn[8];
+        Table<PAIRS>(p).compute(p, run.positions[have ? i : 0], c, cs, sn);
+        rotate8<ACT, PAIRS>(p, u, row, c, threadIdx.x & 31, have, cs, sn, x);
+    } else {
+        Vec16<ACT>::to_float(u, x);
+    }
+}
+
+// The largest finite element of the rows r, r + rp, ... of a run (one warp's).
+// For runs that do not fit the registers, and those with an infinity.
+template <int ACT, int PAIRS>
+__device__ __noinline__ float run_top(const RopeAppendParams& p, const RunRows& run, int n, int r, int rp, int c, bool idle) {
+    float top = 0.f;
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += rp) {
+        float x[8];
+        run_row<ACT, PAIRS>(p, run, i0 + r, c, !idle && i0 + r < n, x);
+        finite_top(x, top);
+    }
+    return warp_max(top);
+}
+
+template <int ACT, int PAIRS>
+__device__ __noinline__ void run_codes(const RopeAppendParams& p, const RunRows& run, int n, int off0, int r, int rp, int c,
+                                       bool idle, float now) {
+    const Divisor by(now);
+#pragma unroll 1
+    for (int i0 = 0; i0 < n; i0 += rp) {
+        float x[8];
+        const bool have = !idle && i0 + r < n;
+        run_row<ACT, PAIRS>(p, run, i0 + r, c, have, x);
+        by.divide8(x);
+        if (have) *reinterpret_cast<uint2*>(run.tile + (off0 + i0 + r) * p.head_dim + c * 8) = to_codes(x);
+    }
+}
+
 // ---------------------------------------------------------------------------
 // One run of n tokens of one block and kv head into a block-scaled cache, K
 // (TURN: rotated) or V, by W warps (one, or two that take every other pass and
 // meet for the maximum): the maximum over the run, the block's new scale, its
-// other codes where the scale grew, the run's codes.  GROUP rows a lane stay in
-// registers between the maximum and the codes, rotated if they turn; runs
-// longer than GROUP passes are read (and rotated) twice.
+// other codes where the scale grew, the run's codes.  A run of up to GROUP
+// passes stays in registers between the maximum and the codes (rotated, if it
+// turns, with cos and sin from the table's rows); a longer one is read twice.
 // ---------------------------------------------------------------------------
 template <int ACT, int PAIRS, int GROUP, int W, bool TURN>
-__device__ __forceinline__ void scaled_run(const RopeAppendParams& p, int t0, int n, int64_t blk, int off0, int head,
-                                           bool is_k, const float* table, int tabled, float* tops2) {
+__device__ __forceinline__ void scaled_run(const RopeAppendParams& p, const RunRows& run, int n, int off0, int lane_row,
+                                           int c, const float* table, float* tops2) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int lpr = p.head_dim / 8, rows = 32 / lpr;  // rows a warp's pass
-    const int rp = W * rows;                          // rows a pass of all W warps
-    const int lane_row = lane / lpr, c = lane - lane_row * lpr;
+    const int lpr = p.head_dim / 8, rows = 32 / lpr;  // rows of a warp's pass
+    const int rp = W * rows;                          // rows of a pass of all W warps
     const bool idle = lane_row >= rows;
     const int r = (W == 2 ? (warp & 1) * rows : 0) + lane_row;
-    float* scale = (is_k ? p.k_scales : p.v_scales) + blk * p.num_kv_heads + head;
-    const float old = off0 == 0 ? 0.f : *scale;
-    const int64_t stride = is_k ? p.k_stride : p.v_stride;
-    const uint16_t* src0 = (is_k ? static_cast<const uint16_t*>(p.k) : static_cast<const uint16_t*>(p.v)) + t0 * stride +
-                           static_cast<int64_t>(head) * p.head_dim;
-    constexpr int AHEAD = TURN && GROUP > 4 ? 4 : GROUP;  // loads in flight (rotated rows take the registers)
-    uint4 u[TURN ? AHEAD : GROUP];
+    const float old = off0 == 0 ? 0.f : *run.scale;
+    const bool fits = n <= GROUP * rp;
+    uint4 u[GROUP];
     float x[TURN ? GROUP : 1][8];
-    auto load = [&](int g0) {
-#pragma unroll
-        for (int a = 0; a < GROUP; a += AHEAD) {
-            if (g0 + a * rp >= n) break;
-#pragma unroll
-            for (int j = 0; j < AHEAD; ++j) {
-                const int i = g0 + (a + j) * rp + r;
-                u[j] = !idle && i < n ? *reinterpret_cast<const uint4*>(src0 + i * stride + c * 8)
-                                       : make_uint4(0u, 0u, 0u, 0u);
-            }
-            if constexpr (TURN) {
-#pragma unroll
-                for (int j = 0; j < AHEAD; ++j) {
-                    if (g0 + (a + j) * rp >= n) break;
-                    const int i = g0 + (a + j) * rp + r;
-                    const bool have = !idle && i < n;
-                    const int row = have ? i : 0;
-                    float cs[8], sn[8];
-                    if (row < tabled) Table<PAIRS>(p).read(p, table, row, c, cs, sn);
-                    else Table<PAIRS>(p).compute(p, p.positions[t0 + row], c, cs, sn);
-                    __syncwarp();
-                    rotate8<ACT, PAIRS>(p, u[j], src0 + row * stride, c, lane, have, cs, sn, x[a + j]);
-                }
-            }
-        }
-    };
     float top = 0.f;
-    uint32_t tops = 0;
-    for (int g0 = 0; g0 < n; g0 += GROUP * rp) {
-        load(g0);
+    if (fits) {
+        const uint16_t* src = run.src + r * run.stride + c * 8;
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j)
+            u[j] = !idle && j * rp + r < n ? *reinterpret_cast<const uint4*>(src + j * rp * run.stride)
+                                           : make_uint4(0u, 0u, 0u, 0u);
+        [[maybe_unused]] uint32_t tops = 0;
 #pragma unroll
         for (int j = 0; j < GROUP; ++j) {
-            if (g0 + j * rp >= n) break;
-            if constexpr (TURN) finite_top(x[j], top);
-            else top_bits<ACT>(u[j], tops);
+            if (j * rp >= n) break;
+            if constexpr (TURN) {
+                const int i = j * rp + r;
+                const bool have = !idle && i < n;
+                float cs[8], sn[8];
+                Table<PAIRS>(p).read(p, table, have ? i : 0, c, cs, sn);
+                rotate8<ACT, PAIRS>(p, u[j], run.src + (have ? i : 0) * run.stride, c, lane, have, cs, sn, x[j]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fabsf(x[j][k]));
+            } else {
+                top_pairs<ACT>(u[j], tops);
+            }
         }
+        if (!TURN)
+            top = fmaxf(act_to_float<ACT>(static_cast<uint16_t>(tops)), act_to_float<ACT>(static_cast<uint16_t>(tops >> 16)));
+        top = warp_max(top);
     }
-    if (!TURN) top = act_to_float<ACT>(static_cast<uint16_t>(max(tops & 0xffffu, tops >> 16)));
-    top = warp_max(top);
+    if (!fits || !(top <= 3.402823466e38f)) top = run_top<ACT, PAIRS>(p, run, n, r, rp, c, idle);
     if constexpr (W == 2) {  // the pair's other half (also: both have read the old scale)
         if (lane == 0) tops2[warp] = top;
         asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
         top = fmaxf(top, tops2[warp ^ 1]);
     }
     const float now = new_scale(top, old);
-    uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
-                    (blk * p.num_kv_heads + head) * p.block_size * p.head_dim;
     if (now != old) {
         __syncwarp();  // every lane has read the old scale
-        if (lane == 0 && (W == 1 || !(warp & 1))) *scale = now;
+        if (lane == 0 && (W == 1 || !(warp & 1))) *run.scale = now;
         if (old > 0.f)
-            requantise(tile, p.block_size, lpr, off0, n, __fdiv_rn(old, now), W == 2 ? (warp & 1) * 32 + lane : lane, 32 * W);
+            requantise(run.tile, p.block_size, lpr, off0, n, __fdiv_rn(old, now), W == 2 ? (warp & 1) * 32 + lane : lane,
+                       32 * W);
     }
-    for (int g0 = 0; g0 < n; g0 += GROUP * rp) {
-        if (n > GROUP * rp) load(g0);
+    if (!fits) {
+        run_codes<ACT, PAIRS>(p, run, n, off0, r, rp, c, idle, now);
+        return;
+    }
+    const Divisor by(now);
+    uint8_t* dst = run.tile + (off0 + r) * p.head_dim + c * 8;
 #pragma unroll
-        for (int j = 0; j < GROUP; ++j) {
-            if (g0 + j * rp >= n) break;
-            const int i = g0 + j * rp + r;
+    for (int j = 0; j < GROUP; ++j) {
+        if (j * rp >= n) break;
+        if constexpr (!TURN) {
             float y[8];
-            if constexpr (TURN) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = x[j][k];
-            } else {
-                Vec16<ACT>::to_float(u[j], y);
-            }
-            if (idle || i >= n) continue;
-            divide8(y, now);
-            *reinterpret_cast<uint2*>(tile + (off0 + i) * p.head_dim + c * 8) = to_codes(y);
+            Vec16<ACT>::to_float(u[j], y);
+            by.divide8(y);
+            if (!idle && j * rp + r < n) *reinterpret_cast<uint2*>(dst + j * rp * p.head_dim) = to_codes(y);
+        } else {
+            by.divide8(x[j]);
+            if (!idle && j * rp + r < n) *reinterpret_cast<uint2*>(dst + j * rp * p.head_dim) = to_codes(x[j]);
         }
     }
 }
@@ -524,7 +578,7 @@ __device__ __forceinline__ void single_rows(const RopeAppendParams& p, int t0, i
         if (c == 0) *scale = now;  // (every lane read the old one before the shuffles)
         if (old > 0.f) requantise(tile, p.block_size, lpr, off0, 1, __fdiv_rn(old, now), c, lpr);
     }
-    divide8(x, now);
+    Divisor(now).divide8(x);
     *reinterpret_cast<uint2*>(tile + off0 * p.head_dim + c * 8) = to_codes(x);
 }
 
@@ -537,6 +591,7 @@ __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int wind
     __shared__ float tops2[2 * kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lpr = p.head_dim / 8;
+    const int lane_row = lane / lpr, chunk = lane - lane_row * lpr;
     // lane l holds token first - 1 + l: the window's tokens, the one before and some after
     const int first = w * window;
     bool bad = false;
@@ -566,12 +621,11 @@ __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int wind
                 more = out == 0;
             }
         }
-        int tabled = 0;
         if constexpr (PAIRS != kPairsNone) {
+            // the rows that a run of GROUP passes has (at most kTable holds them)
             const Table<PAIRS> tab(p);
-            tabled = min(n, kTable / tab.row_floats());
             __syncthreads();  // the run before is done with the table
-            tab.fill(p, table, t0, tabled);
+            tab.fill(p, table, t0, min(n, GROUP * W * (32 / lpr)));
             __syncthreads();
         }
         const int items = 2 * p.num_kv_heads;
@@ -586,11 +640,17 @@ __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int wind
         for (int it = part * TEAMS + warp / W; it < items; it += split * TEAMS, flip ^= kWarps) {
             const bool is_k = it < p.num_kv_heads;
             const int head = is_k ? it : it - p.num_kv_heads;
+            const int64_t tile = b0 * p.num_kv_heads + head;
+            RunRows run;
+            run.stride = is_k ? p.k_stride : p.v_stride;
+            run.src = static_cast<const uint16_t*>(is_k ? p.k : p.v) + t0 * run.stride + head * p.head_dim;
+            run.scale = (is_k ? p.k_scales : p.v_scales) + tile;
+            run.tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) + tile * p.block_size * p.head_dim;
+            run.positions = is_k && PAIRS != kPairsNone ? p.positions + t0 : nullptr;
             if (PAIRS != kPairsNone && is_k)
-                scaled_run<ACT, PAIRS, GROUP, W, PAIRS != kPairsNone>(p, t0, n, b0, off0, head, true, table, tabled,
-                                                                      tops2 + flip);
+                scaled_run<ACT, PAIRS, GROUP, W, PAIRS != kPairsNone>(p, run, n, off0, lane_row, chunk, table, tops2 + flip);
             else
-                scaled_run<ACT, PAIRS, GROUP, W, false>(p, t0, n, b0, off0, head, is_k, table, tabled, tops2 + flip);
+                scaled_run<ACT, PAIRS, GROUP, W, false>(p, run, n, off0, lane_row, chunk, table, tops2 + flip);
         }
         if (W == 2) __syncthreads();  // the places of the last maxima
     }
