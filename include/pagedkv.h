@@ -493,7 +493,10 @@ int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_
  * block_tables[b][j / block_size].  Scales may be any finite float32 (a power of
  * two or not, 0, negative); products and sums as paged_attention_decode.  A
  * context length of 0 (a padding row) gives a row of zeros and no error bit.
- * The workspace is pkv_workspace_size(...); other arguments as there.
+ * The workspace is at least pkv_scaled_workspace_size(...) bytes; other
+ * arguments as there.  PKV_PARTITION_AUTO gives partitions of at most 512
+ * tokens, which the tensor-core kernel serves for every group and both
+ * head_dims; pkv_set_kernel_path's two tensor-core choices are one here.
  */
 int paged_attention_decode_scaled(const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
                                   const float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,
@@ -501,6 +504,13 @@ int paged_attention_decode_scaled(const void* q, const void* k_cache, const void
                                   int block_size, int head_dim, int num_blocks, float scale, void* out,
                                   int act_dtype, int partition_size, void* workspace, size_t workspace_bytes,
                                   void* stream);
+
+/* pkv_workspace_size and pkv_resolve_partition_size of
+ * paged_attention_decode_scaled.  Host only. */
+size_t pkv_scaled_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int max_blocks_per_seq, int block_size, int partition_size);
+int pkv_scaled_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                              int max_blocks_per_seq, int block_size, int partition_size);
 
 /* paged_block_copy of a block-scaled cache: the blocks and their scales. */
 int paged_block_copy_scaled(void* k_cache, void* v_cache, float* k_scales, float* v_scales,

@@ -128,15 +128,16 @@ def set_kernel_path(path: int) -> int:
 
 
 def resolve_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
-                           partition_size=PARTITION_AUTO):
-    return int(_native.lib().pkv_resolve_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                                        max_blocks_per_seq, block_size, partition_size))
+                           partition_size=PARTITION_AUTO, block_scales=False):
+    fn = _native.lib().pkv_scaled_partition_size if block_scales else _native.lib().pkv_resolve_partition_size
+    return int(fn(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, partition_size))
 
 
 def workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
-                   partition_size=PARTITION_AUTO) -> int:
-    return int(_native.lib().pkv_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim,
-                                                max_blocks_per_seq, block_size, partition_size))
+                   partition_size=PARTITION_AUTO, block_scales=False) -> int:
+    """Bytes of workspace of paged_attention_decode (block_scales: of paged_attention_decode_scaled)."""
+    fn = _native.lib().pkv_scaled_workspace_size if block_scales else _native.lib().pkv_workspace_size
+    return int(fn(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, partition_size))
 
 
 _ws_lock = threading.Lock()
@@ -164,7 +165,7 @@ def paged_attention_decode(q, k_cache, v_cache, block_tables, context_lens, scal
 
 
 def _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_scale, v_scale, partition_size,
-                 workspace, stream):
+                 workspace, stream, block_scales=False):
     """Validated C arguments of paged_attention_decode, the output and the workspace."""
     B, Hq, D = q.shape
     NB, Hkv, bs, D2 = k_cache.shape
@@ -184,7 +185,7 @@ def _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_
     max_blocks = block_tables.shape[1]
     s = _stream(stream, q.device)
     if workspace is None:
-        need = workspace_size(B, Hq, Hkv, D, max_blocks, bs, partition_size)
+        need = workspace_size(B, Hq, Hkv, D, max_blocks, bs, partition_size, block_scales)
         if need:
             workspace = _workspace(q.device, s, need)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -584,7 +585,7 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
     """Validated C arguments of paged_attention_decode_scaled, the output and the workspace."""
     _require_scales("paged_attention_decode_scaled", k_cache, v_cache, k_scales, v_scales)
     a, out, workspace = _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_scales, v_scales,
-                                     partition_size, workspace, stream)
+                                     partition_size, workspace, stream, block_scales=True)
     # (q, k_cache, v_cache | tables .. scale, out, act | cache_dtype, k_scale, v_scale dropped | partition ..)
     return (*a[:3], a[16], a[17], *a[3:15], *a[18:]), out, workspace
 

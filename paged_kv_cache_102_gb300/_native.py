@@ -46,6 +46,8 @@ SIGNATURES = {
                                 I32, I32, I32, I32, P, P, P, P, P]),
     "paged_attention_decode_scaled": (I32, [P, P, P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, F32, P, I32, I32,
                                             P, SZ, P]),
+    "pkv_scaled_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+    "pkv_scaled_partition_size": (I32, [I32, I32, I32, I32, I32, I32, I32]),
     "paged_block_copy_scaled": (I32, [P, P, P, P, P, I32, I32, I32, SZ, P]),
     "paged_block_scales_swap": (I32, [P, P, P, I32, I32, I32, P, I32, P]),
     "pkv_last_error": (ctypes.c_char_p, []),

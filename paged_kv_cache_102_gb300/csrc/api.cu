@@ -133,10 +133,9 @@ int pkv_resolve_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, 
     return static_cast<int>(P);
 }
 
-size_t pkv_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
-                          int max_blocks_per_seq, int block_size, int partition_size) {
-    const int P = pkv_resolve_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
-                                             block_size, partition_size);
+// Workspace for partitions of P tokens.
+static size_t pkv_workspace_size_of(int num_seqs, int num_q_heads, int head_dim, int max_blocks_per_seq, int block_size,
+                                    int P) {
     if (P <= 0 || num_seqs <= 0 || num_q_heads <= 0 || head_dim <= 0) return 0;
     const long long max_ctx = static_cast<long long>(max_blocks_per_seq) * block_size;
     const long long parts = (max_ctx + P - 1) / P;
@@ -144,6 +143,36 @@ size_t pkv_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int h
     const size_t rows = static_cast<size_t>(num_seqs) * num_q_heads * static_cast<size_t>(parts);
     return kWorkspaceHeader + align_up(rows * 2 * sizeof(float), 256) +
            rows * static_cast<size_t>(head_dim) * sizeof(float);
+}
+
+size_t pkv_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                          int max_blocks_per_seq, int block_size, int partition_size) {
+    const int P = pkv_resolve_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                             block_size, partition_size);
+    return pkv_workspace_size_of(num_seqs, num_q_heads, head_dim, max_blocks_per_seq, block_size, P);
+}
+
+int pkv_scaled_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                              int block_size, int partition_size) {
+    if (partition_size != PKV_PARTITION_AUTO)
+        return pkv_resolve_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+                                          partition_size);
+    if (max_blocks_per_seq < 1 || block_size < 1 || num_kv_heads < 1 || num_q_heads < 1) return -1;
+    const long long max_ctx = static_cast<long long>(max_blocks_per_seq) * block_size;
+    const long long single = (max_ctx + kStageTokens - 1) / kStageTokens * kStageTokens;
+    // the tensor-core kernel's 512 tokens whatever the group; 256 where that leaves a few items a CTA
+    long long P = kAutoPartitionGrouped;
+    const long long items = static_cast<long long>(num_seqs) * num_kv_heads * ((max_ctx + P - 1) / P);
+    if (items >= kAutoGroupedItemsLow && items < kAutoGroupedItemsHigh && (P / 2) % block_size == 0) P /= 2;
+    if (P >= single) P = single;
+    return static_cast<int>(P);
+}
+
+size_t pkv_scaled_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int max_blocks_per_seq,
+                                 int block_size, int partition_size) {
+    const int P = pkv_scaled_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                            block_size, partition_size);
+    return P <= 0 ? 0 : pkv_workspace_size_of(num_seqs, num_q_heads, head_dim, max_blocks_per_seq, block_size, P);
 }
 
 int paged_kv_append(const void* k, const void* v, const int64_t* slot_mapping, int num_tokens, void* k_cache,
@@ -252,8 +281,8 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
         !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(workspace, 16))
         return fail(PKV_ERR_INVALID, F + ": " + "q, caches, out, workspace must be 16-byte aligned");
-    const int P = pkv_resolve_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
-                                             block_size, partition_size);
+    const int P = (block_scales ? pkv_scaled_partition_size : pkv_resolve_partition_size)(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, partition_size);
     if (P <= 0)
         return fail(PKV_ERR_INVALID, F + ": " + "partition_size must be 0, -1 or a positive multiple of 32 and of block_size");
     const long long max_ctx = static_cast<long long>(max_blocks_per_seq) * block_size;
@@ -261,11 +290,10 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     const int max_parts = static_cast<int>((max_ctx + P - 1) / P);
     if (max_parts > 65535 || num_kv_heads > 65535 || num_seqs > 65535)
         return fail(PKV_ERR_INVALID, F + ": " + "grid too large (partitions, kv heads or sequences > 65535)");
-    const size_t need = pkv_workspace_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
-                                           block_size, partition_size);
+    const size_t need = pkv_workspace_size_of(num_seqs, num_q_heads, head_dim, max_blocks_per_seq, block_size, P);
     if (!workspace || workspace_bytes < need)
-        return fail(PKV_ERR_INVALID, F + ": " + "workspace of " + std::to_string(need) +
-                                         " bytes required (pkv_workspace_size)");
+        return fail(PKV_ERR_INVALID, F + ": " + "workspace of " + std::to_string(need) + " bytes required (" +
+                                         (block_scales ? "pkv_scaled_workspace_size)" : "pkv_workspace_size)"));
     int* err = device_error_word();
     if (!err) return fail(PKV_ERR_CUDA, F + ": " + "cannot resolve the device error word");
 
@@ -324,7 +352,7 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
                                      "cache) or 64 (16-bit cache, even kv heads, shared tables), 2/4/8 query "
                                      "heads per kv head and partitions of at most 512 tokens");
     const bool use_tc = path == PKV_PATH_TENSOR || path == PKV_PATH_TENSOR_2CTA ||
-                        (path == PKV_PATH_AUTO && tc_ok && G >= 4);
+                        (path == PKV_PATH_AUTO && tc_ok && (G >= 4 || block_scales));
     if (use_tc) {
         const int chunk = decode_tc_max_rows() / rows_per_seq;
         const size_t act_bytes = 2;

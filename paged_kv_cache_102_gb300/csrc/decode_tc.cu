@@ -13,18 +13,19 @@ bool decode_tc_supported(int head_dim, int block_size, int group, int act, int c
     // kv heads with a block-scaled E4M3 cache
     const bool dims = head_dim == kTcD || (head_dim == 64 && cache == kE4M3B) ||
                       (head_dim == 64 && cache == act && num_kv_heads % 2 == 0 && !per_kvh_tables);
-    return dims && (block_size == 16 || block_size == 32) && (group == 2 || group == 4 || group == 8) &&
+    return dims && (block_size == 16 || block_size == 32) &&
+           (group == 2 || group == 4 || group == 8 || (group == 1 && cache == kE4M3B)) &&
            (act == kF16 || act == kBF16) && (cache == act || is_e4m3(cache)) &&
            partition_size <= kTcMaxTiles * kTcTile && encode_fn() != nullptr;
 }
 
 cudaError_t launch_decode_tc(const DecodeParams& p, int act, int cache, int head_dim, int BS, int G, int variant,
                              cudaStream_t s) {
-    if (head_dim == 64 && cache == kE4M3B) return launch_decode_tc_e4m3b(p, act, head_dim, BS, G, variant, s);
+    if (head_dim == 64 && cache == kE4M3B) return launch_decode_tc_e4m3b_d64(p, act, BS, G, s);
     if (head_dim == 64) return launch_decode_tc_d64(p, act, BS, G, variant, s);
     if (head_dim != kTcD) return cudaErrorInvalidValue;
     if (cache == kE4M3) return launch_decode_tc_e4m3(p, act, BS, G, variant, s);
-    if (cache == kE4M3B) return launch_decode_tc_e4m3b(p, act, head_dim, BS, G, variant, s);
+    if (cache == kE4M3B) return launch_decode_tc_e4m3b(p, act, BS, G, s);
     const int rows = p.table_kvh_stride != 0 ? p.num_seqs * p.num_kv_heads : p.num_seqs;
     const uint64_t cache_rows = static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * BS;
     CUtensorMap km, vm, qm;

@@ -279,7 +279,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     constexpr uint32_t IDESC_O = tc::idesc_f16(128, kTcN, !FP8 && ACT == kBF16, true, FP8);
     static_assert(!FP8 || G <= 8, "E4M3 cache: rows 0-7 of Q and P hold the high parts, rows 8-15 the low parts");
     constexpr bool Q3 = FP8 && ACT == kF16;  // binary16 queries: three E4M3 parts
-    static_assert(G == 2 || G == 4 || G == 8, "query heads per kv head");
+    static_assert(G == 2 || G == 4 || G == 8 || (SCALED && G == 1), "query heads per kv head");
     static_assert(kTcMaxTiles * kTcTile / BS <= 32, "one warp holds the table entries of an item");
 
     // the merge kernel may be scheduled now; it waits for this grid to finish
@@ -1246,10 +1246,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
                             for (int g = 0; g < G; g += 2) {
                                 // M is finite (every item has a token); 2^-inf = 0 for masked rows
+                                constexpr int SECOND = G > 1 ? 1 : 0;
                                 const float p0 = fast_exp2(sc[t][g] - M[g]);
-                                const float p1 = fast_exp2(sc[t][g + 1] - M[g + 1]);
+                                const float p1 = G > 1 ? fast_exp2(sc[t][g + SECOND] - M[g + SECOND]) : 0.f;
                                 sum[g] += p0;
-                                sum[g + 1] += p1;
+                                if (G > 1) sum[g + SECOND] += p1;
                                 uint32_t hi, lo;
                                 const float pm = SCALED ? vs_t[t] : 256.f;  // vs_t: times 2^(8 - ev)
                                 split_e4m3x2(p0 * pm, p1 * pm, hi, lo);

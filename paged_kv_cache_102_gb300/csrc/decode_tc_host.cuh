@@ -1,6 +1,6 @@
 // Host side of the tensor-core grouped-query decode kernel shared by its
 // translation units (16-bit caches at head_dim 128 in decode_tc.cu, E4M3
-// caches in decode_tc_e4m3.cu and, with block scales, decode_tc_e4m3b.cu, head_dim-64 pairs in decode_tc_d64.cu): TMA
+// caches in decode_tc_e4m3.cu and, with block scales, decode_tc_e4m3b.cu and decode_tc_e4m3b_d64.cu, head_dim-64 pairs in decode_tc_d64.cu): TMA
 // tensor maps over the caches and the queries, persistent grid sizing, the
 // launch template.
 #pragma once
@@ -108,6 +108,10 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorM
 template <int ACT, int CACHE, int NS, bool PAIR = false, bool HALF = false>
 cudaError_t by_shape(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                      int BS, int G, int ctas_per_sm, cudaStream_t s) {
+    if constexpr (CACHE == kE4M3B) {
+        if (BS == 16 && G == 1) return launch<ACT, CACHE, 16, 1, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+        if (BS == 32 && G == 1) return launch<ACT, CACHE, 32, 1, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+    }
     if (BS == 16) {
         if (G == 2) return launch<ACT, CACHE, 16, 2, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
         if (G == 4) return launch<ACT, CACHE, 16, 4, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);

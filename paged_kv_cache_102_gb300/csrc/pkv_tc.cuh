@@ -128,6 +128,14 @@ template <int N>
 struct TmemLd;
 
 template <>
+struct TmemLd<1> {
+    __device__ __forceinline__ static void load(uint32_t taddr, float* v) {
+        uint32_t r;
+        asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(taddr));
+        v[0] = __uint_as_float(r);
+    }
+};
+template <>
 struct TmemLd<2> {
     __device__ __forceinline__ static void load(uint32_t taddr, float* v) {
         uint32_t r[2];

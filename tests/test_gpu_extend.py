@@ -185,7 +185,7 @@ def test_a_whole_step_captured_and_replayed(pkv, hq, hkv, D):
               q=torch.zeros(B, hq, D, dtype=torch.bfloat16, **z), out=torch.zeros(B, hq, D, dtype=torch.bfloat16, **z),
               qkv=torch.zeros(B, hq + 2 * hkv, D, dtype=torch.bfloat16, **z),
               new=torch.tensor([1, 1, 1, 1, 0], dtype=I32, **z),
-              ws=torch.empty(pkv.workspace_size(B, hq, hkv, D, cols, bs), dtype=torch.uint8, **z))
+              ws=torch.empty(pkv.workspace_size(B, hq, hkv, D, cols, bs, block_scales=True), dtype=torch.uint8, **z))
     st["vc"], st["vs"] = st["kc"].clone(), st["ks"].clone()
     # prompts
     T = sum(prompts)

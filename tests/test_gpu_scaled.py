@@ -320,7 +320,8 @@ def test_decode_scaled_plan_stream_and_graph(pkv):
         q, kc, vc, ks, vs, tables, L = (t.cuda() for t in _decode_case(case, [200, 513, 77]))
         s = torch.cuda.Stream()
         s.wait_stream(torch.cuda.current_stream())
-        ws = torch.empty(pkv.workspace_size(3, case[1], case[2], case[3], tables.shape[1], case[4], case[5]),
+        ws = torch.empty(pkv.workspace_size(3, case[1], case[2], case[3], tables.shape[1], case[4], case[5],
+                                            block_scales=True),
                          dtype=torch.uint8, device="cuda")
         plan = pkv.DecodePlan(q, kc, vc, tables, L, 0.1, k_scales=ks, v_scales=vs, partition_size=case[5],
                               workspace=ws, stream=s)
