@@ -77,10 +77,9 @@
 // keep their precision whatever the scales of the other blocks are.  The sum
 // of 2^(score - R) is the denominator; log2 |vs| - ev enters R at no less than
 // -100, which keeps it finite (and a row without any V scale but 0 defined).
-// The producer that converts q finds its power-of-2 scale too.  With eight
-// query heads the softmax warps are what bounds an item (a chain of dependent
-// steps for 32 scores a thread), so two groups of four warps (2-5 and 8-11)
-// take four heads each.
+// The producer that converts q finds its power-of-2 scale too.  (Two groups of
+// softmax warps with four heads each were no faster at eight query heads: 81.3
+// against 80.3 us for 128 ragged sequences.)
 // Every barrier wait is bounded (kWaitLimitNs); on a timeout the CTA stops
 // issuing work, drains its in-flight copies and MMAs, frees tensor memory and
 // reports kErrTimeout.
@@ -255,11 +254,8 @@ __device__ __forceinline__ void split3_e4m3x2(float x0, float x1, uint32_t& hi, 
     split_e4m3x2(x0 - hv.x, x1 - hv.y, mid, lo);
 }
 
-__host__ __device__ constexpr int tc_softmax_groups(int cache, int G) { return cache == kE4M3B && G == 8 ? 2 : 1; }
-__host__ __device__ constexpr int tc_threads(int cache, int G) { return kTcThreads + (tc_softmax_groups(cache, G) - 1) * 128; }
-
 template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR = false, bool HALF = false>
-__global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
+__global__ void __launch_bounds__(kTcThreads, 2)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const __grid_constant__ CUtensorMap qmap, const DecodeParams p) {
     constexpr bool FP8 = is_e4m3(CACHE);
@@ -271,9 +267,7 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
     static_assert(!PAIR || !FP8, "pairs of head_dim-64 kv heads: 16-bit caches");
     static_assert(!HALF || SCALED, "two tokens a row: block-scaled E4M3 caches");
     using S = TcSmem<NS, STG, PAIR, SCALED, HALF>;
-    constexpr int SG = tc_softmax_groups(CACHE, G);  // groups of softmax warps
-    constexpr int GG = G / SG;                       // heads of each
-    constexpr int THREADS = tc_threads(CACHE, G);
+    constexpr int THREADS = kTcThreads;
     constexpr int TPR = HALF ? 2 : 1;         // tokens per tile row
     constexpr int TILE = kTcTile * TPR;       // tokens per tile
     constexpr int BPT = TILE / BS;            // blocks per tile
@@ -427,13 +421,10 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 1);
         }
-        for (int i = 0; i < 13; ++i) {
-            const bool groups = (i >= 6 && i < 8) || (i >= 10 && i < 12);  // p_full, o_free: every softmax group
-            mbar_init(&q_full[i], groups ? SG : 1);
-        }
+        for (int i = 0; i < 13; ++i) mbar_init(&q_full[i], 1);
         for (int i = 0; i < kTcQueue; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 3 + SG);  // the two tile producers, the MMA warp and the softmax groups
+            mbar_init(&item_empty[i], 4);  // the two tile producers, the MMA warp and the softmax warps
         }
         *abort_flag = 0;
         mbar_init_fence();
@@ -644,7 +635,7 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
         if constexpr (SCALED) asm volatile("griddepcontrol.wait;" ::: "memory");
         while (ok && claim(it, phys)) {
         }
-    } else if (warp == 6 || warp == 7) {
+    } else if (warp >= 6) {
         // ------------------------------------------------------ tile producers
         // Warp 6 arms the even stage uses and writes Q, warp 7 arms the odd
         // uses.  Both read the items from the queue and follow one tile order:
@@ -826,9 +817,10 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
         }
     } else if (SCALED && warp == 1) {
         // --------------------------------------------------- MMA (block-scaled)
-        // The role that everything else waits on: lane 0 alone waits for tiles
-        // and issues their products, with descriptors stepped by one addition;
-        // the warp meets once or twice an item (and where rows are zeroed).
+        // The role that everything else waits on.  The warp waits together and
+        // one elected lane issues a tile's products, with descriptors stepped by
+        // one addition (an elected lane instead of lane 0: decode of 128 ragged
+        // sequences 84.6 -> 81.8 us, at head_dim 64 44.1 -> 41.3 us).
         constexpr uint32_t HI_SW = tc::desc_hi_sw128(1024), HI_NS = tc::desc_hi_noswizzle(2048);
         const uint32_t k_lo = tc::desc_start(smem_addr(ring)) + tc::desc_lo(16);
         const uint32_t v_lo = tc::desc_start(smem_addr(ring)) + tc::desc_lo(kTcStage8);
@@ -856,42 +848,36 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
             return any ? 1 : 0;
         };
         auto mma_s = [&](const TcItem& it, int k) {
-            bool good = true;
-            if (lane == 0) {
-                const int b = k & 1;
-                good = tc_wait(&q_full[b], (k >> 1) & 1, abort_flag, p.err);
-                const uint32_t q = q_lo + b * (S::QBUF / 16);
-                uint32_t d = tmem + b * SLOT_COLS;
-                int s = stage;
-                uint32_t ph = phase;
-                for (int t = 0; t < it.n_tiles && good; ++t) {
-                    good = tc_wait(&full[s], ph, abort_flag, p.err);
-                    if (!good) break;
-                    tc::fence_after_sync();
-                    const uint32_t a = k_lo + s * (STG / 16);
+            const int b = k & 1;
+            if (!__all_sync(0xffffffffu, tc_wait(&q_full[b], (k >> 1) & 1, abort_flag, p.err))) return false;
+            const uint32_t q = q_lo + b * (S::QBUF / 16);
+            uint32_t d = tmem + b * SLOT_COLS;
+            for (int t = 0; t < it.n_tiles; ++t, d += TPR * kTcN) {
+                if (!__all_sync(0xffffffffu, tc_wait(&full[stage], phase, abort_flag, p.err))) return false;
+                tc::fence_after_sync();
+                if (tc::elect_one()) {
+                    const uint32_t a = k_lo + stage * (STG / 16);
 #pragma unroll
-                    for (int par = 0; par < TPR; ++par, d += kTcN) {
+                    for (int par = 0; par < TPR; ++par) {
 #pragma unroll
                         for (int kk = 0; kk < HD / 32; ++kk) {
                             // HALF: even tokens in bytes 0-63 of the rows, odd tokens in 64-127
                             const uint32_t ak = a + par * 4 + kk * 2, qk = q + kk * 2;
-                            tc::mma_f8_words<HI_SW, HI_SW>(d, ak, qk, IDESC_S, kk > 0);
-                            if constexpr (Q3) tc::mma_f8_words<HI_SW, HI_SW>(d, ak, qk + 128, IDESC_S, true);
+                            tc::mma_f8_words<HI_SW, HI_SW>(d + par * kTcN, ak, qk, IDESC_S, kk > 0);
+                            if constexpr (Q3) tc::mma_f8_words<HI_SW, HI_SW>(d + par * kTcN, ak, qk + 128, IDESC_S, true);
                         }
                     }
-                    tc::commit(&empty[s]);
-                    if (++s == NS) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
+                    tc::commit(&empty[stage]);
                 }
-                if (good) {
-                    tc::commit(&q_empty[b]);
-                    tc::commit(&s_full[b]);
-                }
+                __syncwarp();
+                advance(1);
             }
-            advance(it.n_tiles);
-            return __shfl_sync(0xffffffffu, good, 0) != 0;
+            if (tc::elect_one()) {
+                tc::commit(&q_empty[b]);
+                tc::commit(&s_full[b]);
+            }
+            __syncwarp();
+            return true;
         };
         auto mma_o = [&](const TcItem& it, int k) {
             const int b = k & 1;
@@ -914,27 +900,17 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
                 }
                 tc::commit(&empty[s]);
             };
-            bool good = true;
             const int whole = it.n_tiles - (ragged ? 1 : 0);
-            if (lane == 0) {
-                good = tc_wait(&p_full[b], (k >> 1) & 1, abort_flag, p.err);
-                if (good && k >= 2) good = tc_wait(&o_free[b], ((k >> 1) - 1) & 1, abort_flag, p.err);
-                int s = stage;
-                uint32_t ph = phase;
-                for (int t = 0; t < whole && good; ++t) {
-                    good = tc_wait(&full[s], ph, abort_flag, p.err);
-                    if (!good) break;
-                    tc::fence_after_sync();
-                    issue(s, t, t == it.n_tiles - 1 ? (valid + 31) / 32 : 4);
-                    if (++s == NS) {
-                        s = 0;
-                        ph ^= 1u;
-                    }
-                }
+            if (!__all_sync(0xffffffffu, tc_wait(&p_full[b], (k >> 1) & 1, abort_flag, p.err) &&
+                                             (k < 2 || tc_wait(&o_free[b], ((k >> 1) - 1) & 1, abort_flag, p.err))))
+                return false;
+            for (int t = 0; t < whole; ++t) {
+                if (!__all_sync(0xffffffffu, tc_wait(&full[stage], phase, abort_flag, p.err))) return false;
+                tc::fence_after_sync();
+                if (tc::elect_one()) issue(stage, t, t == it.n_tiles - 1 ? (valid + 31) / 32 : 4);
+                __syncwarp();
+                advance(1);
             }
-            good = __shfl_sync(0xffffffffu, good, 0) != 0;
-            if (!good) return false;
-            advance(whole);
             if (ragged) {
                 if (!__all_sync(0xffffffffu, tc_wait(&full[stage], phase, abort_flag, p.err))) return false;
                 unsigned char* vb = ring + stage * STG;
@@ -947,10 +923,12 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 tc::fence_after_sync();
-                if (lane == 0) issue(stage, whole, ksteps);
+                if (tc::elect_one()) issue(stage, whole, ksteps);
+                __syncwarp();
                 advance(1);
             }
-            if (lane == 0) tc::commit(&o_full[b]);
+            if (tc::elect_one()) tc::commit(&o_full[b]);
+            __syncwarp();
             return true;
         };
         TcItem cur, nxt;
@@ -966,7 +944,7 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
             cur = nxt;
         }
         // every MMA this thread issued has completed before tensor memory is freed
-        if (lane == 0) {
+        if (tc::elect_one()) {
             tc::commit(final_bar);
             if (!mbar_wait(final_bar, 0)) atomicOr(p.err, kErrTimeout);
         }
@@ -1125,14 +1103,11 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
             if (!mbar_wait(final_bar, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
-    } else {
+    } else if (warp < 6) {
         // ------------------------------------------------------ softmax + epilogue
         const int q4 = warp & 3;         // tensor-memory lane quarter of this warp
         const int row = q4 * 32 + lane;  // token of each tile (S) / dimension d (O)
-        const int grp = SG == 2 && warp >= 8 ? 1 : 0;  // heads grp * GG .. + GG
-        const int tid = threadIdx.x - (grp ? 256 : 64);
-        const int h0 = grp * GG;
-        const int bar0 = grp * 3;  // named barriers bar0 + 1, + 2, + 3
+        const int tid = threadIdx.x - 64;
         const uint32_t lane_addr = tmem + (static_cast<uint32_t>(q4 * 32) << 16);
         int nread = 0;
         // token of this thread's row in (virtual) tile t
@@ -1164,7 +1139,7 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
                 qshift = good ? item_shift[slot] : 0;
             }
             ++nread;
-            if (named_bar_or(bar0 + 3, 128, !good)) return -1;
+            if (named_bar_or(3, 128, !good)) return -1;
             if (tid == 0) mbar_arrive(&item_empty[slot]);
             if (ci < 0) return 0;
             if constexpr (SCALED) return 1;
@@ -1194,56 +1169,56 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
             constexpr int NH = PAIR ? 2 : 1;
 #pragma unroll 1
             for (int hh = 0; hh < NH; ++hh) {
-                float sc[kTcMaxTiles][GG] = {};
+                float sc[kTcMaxTiles][G] = {};
                 if (good) {
                     tc::fence_after_sync();
                     if constexpr (FP8) {
                         // column g: the high part of q, column 8 + g: the low part
-                        float lo[kTcMaxTiles][GG] = {};
+                        float lo[kTcMaxTiles][G] = {};
 #pragma unroll
                         for (int t = 0; t < kTcMaxTiles; ++t)
                             if (t < n_tiles) {
-                                tc::TmemLd<GG>::load(lane_addr + b * SLOT_COLS + t * kTcN + h0, sc[t]);
-                                tc::TmemLd<GG>::load(lane_addr + b * SLOT_COLS + t * kTcN + 8 + h0, lo[t]);
+                                tc::TmemLd<G>::load(lane_addr + b * SLOT_COLS + t * kTcN, sc[t]);
+                                tc::TmemLd<G>::load(lane_addr + b * SLOT_COLS + t * kTcN + 8, lo[t]);
                             }
                         tc::tmem_wait_ld();
 #pragma unroll
                         for (int t = 0; t < kTcMaxTiles; ++t)
 #pragma unroll
-                            for (int g = 0; g < GG; ++g) sc[t][g] += lo[t][g];
+                            for (int g = 0; g < G; ++g) sc[t][g] += lo[t][g];
                     } else {
 #pragma unroll
                         for (int t = 0; t < kTcMaxTiles; ++t)
                             if (t < n_tiles)
-                                tc::TmemLd<GG>::load(lane_addr + b * SLOT_COLS + t * kTcN + hh * 8, sc[t]);
+                                tc::TmemLd<G>::load(lane_addr + b * SLOT_COLS + t * kTcN + hh * 8, sc[t]);
                         tc::tmem_wait_ld();
                     }
                     tc::fence_before_sync();  // these reads precede the next MMA into this S buffer
-                    float mx[GG];
+                    float mx[G];
 #pragma unroll
-                    for (int g = 0; g < GG; ++g) mx[g] = -INFINITY;
+                    for (int g = 0; g < G; ++g) mx[g] = -INFINITY;
 #pragma unroll
                     for (int t = 0; t < kTcMaxTiles; ++t) {
                         const bool valid = t < n_tiles && token_of(t) < it.n_tok;
 #pragma unroll
-                        for (int g = 0; g < GG; ++g) {
+                        for (int g = 0; g < G; ++g) {
                             sc[t][g] = valid ? sc[t][g] * (SCALED ? sl * ks_t[t] : sl) : -INFINITY;
                             mx[g] = fmaxf(mx[g], SCALED ? sc[t][g] + lv_t[t] : sc[t][g]);
                         }
                     }
 #pragma unroll
-                    for (int g = 0; g < GG; ++g) mx[g] = warp_max(mx[g]);
+                    for (int g = 0; g < G; ++g) mx[g] = warp_max(mx[g]);
                     if (lane == 0) {
 #pragma unroll
-                        for (int g = 0; g < GG; ++g) red_max[q4 * 8 + h0 + g] = mx[g];
+                        for (int g = 0; g < G; ++g) red_max[q4 * 8 + g] = mx[g];
                     }
                 }
-                if (named_bar_or(bar0 + 1, 128, !good)) return false;
-                float M[GG], sum[GG];
+                if (named_bar_or(1, 128, !good)) return false;
+                float M[G], sum[G];
 #pragma unroll
-                for (int g = 0; g < GG; ++g) {
-                    M[g] = fmaxf(fmaxf(red_max[h0 + g], red_max[8 + h0 + g]),
-                                 fmaxf(red_max[16 + h0 + g], red_max[24 + h0 + g]));
+                for (int g = 0; g < G; ++g) {
+                    M[g] = fmaxf(fmaxf(red_max[g], red_max[8 + g]),
+                                 fmaxf(red_max[16 + g], red_max[24 + g]));
                     sum[g] = 0.f;
                 }
 #pragma unroll
@@ -1254,31 +1229,26 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
                             // tile t holds 16 bytes: hi of heads 0-7, then lo of heads 0-7
                             uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-                            for (int g = 0; g < GG; g += 2) {
+                            for (int g = 0; g < G; g += 2) {
                                 // M is finite (every item has a token); 2^-inf = 0 for masked rows
-                                constexpr int SECOND = GG > 1 ? 1 : 0;
+                                constexpr int SECOND = G > 1 ? 1 : 0;
                                 const float p0 = fast_exp2(sc[t][g] - M[g]);
-                                const float p1 = GG > 1 ? fast_exp2(sc[t][g + SECOND] - M[g + SECOND]) : 0.f;
+                                const float p1 = G > 1 ? fast_exp2(sc[t][g + SECOND] - M[g + SECOND]) : 0.f;
                                 sum[g] += p0;
-                                if (GG > 1) sum[g + SECOND] += p1;
+                                if (G > 1) sum[g + SECOND] += p1;
                                 uint32_t hi, lo;
                                 const float pm = SCALED ? vs_t[t] : 256.f;  // vs_t: times 2^(8 - ev)
                                 split_e4m3x2(p0 * pm, p1 * pm, hi, lo);
                                 w[g >> 2] |= hi << (8 * (g & 3));
                                 w[2 + (g >> 2)] |= lo << (8 * (g & 3));
                             }
-                            if constexpr (SG == 2) {  // the group's four heads: a word each of the parts
-                                *reinterpret_cast<uint32_t*>(pb + t * 2048 + row * 16 + h0) = w[0];
-                                *reinterpret_cast<uint32_t*>(pb + t * 2048 + row * 16 + 8 + h0) = w[2];
-                            } else {
-                                *reinterpret_cast<uint4*>(pb + t * 2048 + row * 16) = make_uint4(w[0], w[1], w[2], w[3]);
-                            }
+                            *reinterpret_cast<uint4*>(pb + t * 2048 + row * 16) = make_uint4(w[0], w[1], w[2], w[3]);
                         } else {
                             // 8-row regions of (tile, 64-token half), 1 KB apart; PAIR:
                             // 16-row regions, 2 KB apart, rows 8-15 for kv head 2v+1
                             unsigned char* pt = pb + (2 * t + (row >> 6)) * (PAIR ? 2048 : 1024) + hh * 1024;
 #pragma unroll
-                            for (int g = 0; g < GG; ++g) {
+                            for (int g = 0; g < G; ++g) {
                                 const float pv = fast_exp2(sc[t][g] - M[g]);  // 2^-inf = 0 for masked rows
                                 sum[g] += pv;
                                 const int chunk = ((row & 63) >> 3) ^ g;
@@ -1290,10 +1260,10 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
                 }
                 if constexpr (SCALED) {
                     // the heads' sums over the warp, halving the heads a lane
-                    // carries at each step: lane l ends with head l / (32 / GG)
-                    constexpr int SPREAD = 32 / GG;
+                    // carries at each step: lane l ends with head l / (32 / G)
+                    constexpr int SPREAD = 32 / G;
 #pragma unroll
-                    for (int n = GG, off = 16; n > 1; n >>= 1, off >>= 1) {
+                    for (int n = G, off = 16; n > 1; n >>= 1, off >>= 1) {
 #pragma unroll
                         for (int g = 0; g < n / 2; ++g) {
                             const bool up = lane & off;
@@ -1303,38 +1273,37 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
                     }
 #pragma unroll
                     for (int off = SPREAD / 2; off >= 1; off >>= 1) sum[0] += __shfl_xor_sync(0xffffffffu, sum[0], off);
-                    if (lane % SPREAD == 0) red_sum[q4 * 8 + h0 + lane / SPREAD] = sum[0];
+                    if (lane % SPREAD == 0) red_sum[q4 * 8 + lane / SPREAD] = sum[0];
                 } else {
 #pragma unroll
-                    for (int g = 0; g < GG; ++g) {
+                    for (int g = 0; g < G; ++g) {
 #pragma unroll
                         for (int off = 16; off >= 1; off >>= 1) sum[g] += __shfl_xor_sync(0xffffffffu, sum[g], off);
                     }
                     if (lane == 0) {
 #pragma unroll
-                        for (int g = 0; g < GG; ++g) red_sum[q4 * 8 + g] = sum[g];
+                        for (int g = 0; g < G; ++g) red_sum[q4 * 8 + g] = sum[g];
                     }
                 }
                 if (hh == NH - 1) tc::fence_proxy_async_smem();
-                asm volatile("bar.sync %0, 128;" ::"r"(bar0 + 2) : "memory");
+                asm volatile("bar.sync 2, 128;" ::: "memory");
                 if constexpr (SCALED) {
                     if (tid == 0) mbar_arrive(&p_full[b]);
-                    if (tid < GG) {  // a head each: its statistics, and what its O column is multiplied by
-                        const int h = h0 + tid;
-                        const float m = fmaxf(fmaxf(red_max[h], red_max[8 + h]), fmaxf(red_max[16 + h], red_max[24 + h]));
-                        const float L = red_sum[h] + red_sum[8 + h] + red_sum[16 + h] + red_sum[24 + h];
+                    if (tid < G) {  // a head each: its statistics, and what its O column is multiplied by
+                        const float m = fmaxf(fmaxf(red_max[tid], red_max[8 + tid]), fmaxf(red_max[16 + tid], red_max[24 + tid]));
+                        const float L = red_sum[tid] + red_sum[8 + tid] + red_sum[16 + tid] + red_sum[24 + tid];
                         // 2^(ev - 8) / L; every V scale 0: 0 / L
-                        o_scale[b * 8 + h] = __fdiv_rn(__uint_as_float(static_cast<uint32_t>(it.ev - 8 + 135) << 23), L) *
+                        o_scale[b * 8 + tid] = __fdiv_rn(__uint_as_float(static_cast<uint32_t>(it.ev - 8 + 135) << 23), L) *
                                                0x1p-8f;
                         if (!it.single) {
-                            const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G + h;
+                            const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G + tid;
                             *reinterpret_cast<float2*>(p.ws_ml + (hrow * p.max_parts + it.part) * 2) = make_float2(m, L);
                         }
                     }
                 } else if (tid == 0) {
                     float* st = stats + (b * 2 + hh) * 16;
 #pragma unroll
-                    for (int g = 0; g < GG; ++g) {
+                    for (int g = 0; g < G; ++g) {
                         st[g] = M[g];
                         st[8 + g] = red_sum[g] + red_sum[8 + g] + red_sum[16 + g] + red_sum[24 + g];
                     }
@@ -1346,7 +1315,7 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
         auto epilogue = [&](const TcItem& it, int k) {
             const int b = k & 1;
             const bool good = __all_sync(0xffffffffu, tc_wait(&o_full[b], (k >> 1) & 1, abort_flag, p.err));
-            float o[GG] = {};
+            float o[G] = {};
             // PAIR: dimensions 64-127 (warps of lane quarters 2 and 3) are kv head
             // 2v+1, whose heads are columns 8-15
             const int hh = PAIR ? (q4 >> 1) : 0;
@@ -1354,42 +1323,42 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
                 tc::fence_after_sync();
                 // HALF: lanes 64-127 hold the odd tokens' product
                 const uint32_t o_addr = lane_addr + b * SLOT_COLS + O_COL + (HALF ? (q4 >> 1) * kTcN : 0);
-                tc::TmemLd<GG>::load(o_addr + hh * 8 + h0, o);
+                tc::TmemLd<G>::load(o_addr + hh * 8, o);
                 if constexpr (FP8) {
-                    float lo[GG];  // O of the low parts of P
-                    tc::TmemLd<GG>::load(o_addr + 8 + h0, lo);
+                    float lo[G];  // O of the low parts of P
+                    tc::TmemLd<G>::load(o_addr + 8, lo);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int g = 0; g < GG; ++g) o[g] += lo[g];
+                    for (int g = 0; g < G; ++g) o[g] += lo[g];
                 } else {
                     tc::tmem_wait_ld();
                 }
                 tc::fence_before_sync();
                 if (HALF && q4 >= 2) {
 #pragma unroll
-                    for (int g = 0; g < GG; ++g) o_odd[(h0 + g) * 64 + (row & 63)] = o[g];
+                    for (int g = 0; g < G; ++g) o_odd[g * 64 + (row & 63)] = o[g];
                 }
             }
             // also orders the stats written by the softmax of this item before the reads below
-            if (named_bar_or(bar0 + 1, 128, !good)) return false;
+            if (named_bar_or(1, 128, !good)) return false;
             if (tid == 0) mbar_arrive(&o_free[b]);
             if constexpr (HALF) {
                 // the next write of o_odd comes after barriers that these reads precede
                 if (q4 >= 2) return true;
 #pragma unroll
-                for (int g = 0; g < GG; ++g) o[g] += o_odd[(h0 + g) * 64 + row];
+                for (int g = 0; g < G; ++g) o[g] += o_odd[g * 64 + row];
             }
             if constexpr (SCALED) {
-                const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G + h0;
+                const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G;
                 if (it.single) {
                     uint16_t* dst = static_cast<uint16_t*>(p.out) + hrow * HD + row;
 #pragma unroll
-                    for (int g = 0; g < GG; ++g) dst[g * HD] = float_to_act<ACT>(o[g] * o_scale[b * 8 + h0 + g]);
+                    for (int g = 0; g < G; ++g) dst[g * HD] = float_to_act<ACT>(o[g] * o_scale[b * 8 + g]);
                 } else {
                     const size_t step = static_cast<size_t>(p.max_parts) * HD;
                     float* dst = p.ws_o + (hrow * p.max_parts + it.part) * HD + row;
 #pragma unroll
-                    for (int g = 0; g < GG; ++g) dst[g * step] = o[g] * o_scale[b * 8 + h0 + g];
+                    for (int g = 0; g < G; ++g) dst[g * step] = o[g] * o_scale[b * 8 + g];
                 }
                 return true;
             }
@@ -1398,7 +1367,7 @@ __global__ void __launch_bounds__(tc_threads(CACHE, G), 2)
             // E4M3: O was computed on the stored codes and on P x 2^8
             const float vmul = FP8 ? *p.v_scale * (1.0f / 256.f) : 1.0f;
 #pragma unroll
-            for (int g = 0; g < GG; ++g) {
+            for (int g = 0; g < G; ++g) {
                 const float Mg = stats[(b * 2 + hh) * 16 + g];
                 const float Lg = stats[(b * 2 + hh) * 16 + 8 + g];
                 // L >= 1 (the max token's weight is 1): one reciprocal per head
