@@ -79,6 +79,8 @@ def _ptr(t):
 
 def _stream(stream, device) -> int:
     if stream is None:
+        if device.index is not None:
+            return torch._C._cuda_getCurrentRawStream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream
 
@@ -165,7 +167,7 @@ def paged_attention_decode(q, k_cache, v_cache, block_tables, context_lens, scal
 
 
 def _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_scale, v_scale, partition_size,
-                 workspace, stream, block_scales=False):
+                 workspace, stream):
     """Validated C arguments of paged_attention_decode, the output and the workspace."""
     B, Hq, D = q.shape
     NB, Hkv, bs, D2 = k_cache.shape
@@ -185,7 +187,7 @@ def _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_
     max_blocks = block_tables.shape[1]
     s = _stream(stream, q.device)
     if workspace is None:
-        need = workspace_size(B, Hq, Hkv, D, max_blocks, bs, partition_size, block_scales)
+        need = workspace_size(B, Hq, Hkv, D, max_blocks, bs, partition_size)
         if need:
             workspace = _workspace(q.device, s, need)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
@@ -352,45 +354,51 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, sel_tables, sel_lens, sca
     return out
 
 
+_E4M3_TYPES = (torch.uint8, torch.float8_e4m3fn)
+
+
+def _check_on(name, device, names, *tensors):
+    """Every tensor (None passes) is contiguous and on `device`; `names` are theirs, space-separated."""
+    index = device.index
+    for i, t in enumerate(tensors):
+        if t is not None and (t.get_device() != index or not t.is_contiguous()):
+            raise ValueError(f"{name}: {names.split()[i]} must be a contiguous CUDA tensor on {device}")
+
+
 def _require_scales(name, k_cache, v_cache, k_scales, v_scales):
     """Checks of a block-scaled cache: E4M3 codes and float32 scales [num_blocks, num_kv_heads]."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape:
         raise ValueError(f"{name}: k_cache and v_cache must be [num_blocks, num_kv_heads, block_size, head_dim]")
-    if _code(k_cache) != E4M3 or _code(v_cache) != E4M3:
+    if k_cache.dtype not in _E4M3_TYPES or v_cache.dtype not in _E4M3_TYPES:
         raise ValueError(f"{name}: a block-scaled cache holds E4M3 codes (uint8 or float8_e4m3fn)")
     if k_scales is None or v_scales is None:
         raise ValueError(f"{name}: k_scales and v_scales go together")
-    want = k_cache.shape[:2]
+    want = shape[:2]
     if (k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or k_scales.shape != want
             or v_scales.shape != want):
         raise ValueError(f"{name}: k_scales and v_scales must be float32 [num_blocks, num_kv_heads]")
-    _require_cuda(k_cache.device, k_cache=k_cache, v_cache=v_cache, k_scales=k_scales, v_scales=v_scales)
+    _check_on(name, k_cache.device, "k_cache v_cache k_scales v_scales", k_cache, v_cache, k_scales, v_scales)
 
 
-def _rows(name, what, t, device):
-    """Token stride, in elements, of t [T, heads, head_dim] whose rows are contiguous."""
-    if not t.is_cuda or t.device != device:
-        raise ValueError(f"{name}: {what} must be a CUDA tensor on {device}")
-    T, H, D = t.shape
+def _rows(name, what, t, index, shape):
+    """Token stride, in elements, of t [T, heads, head_dim] (its shape is given) whose rows are contiguous."""
+    T, H, D = shape
     st = t.stride()
-    if (D > 1 and st[2] != 1) or (H > 1 and st[1] != D):
+    if (st[2] != 1 and D > 1) or (st[1] != D and H > 1):
         raise ValueError(f"{name}: {what} must have contiguous rows [heads, head_dim]")
+    if t.get_device() != index:
+        raise ValueError(f"{name}: {what} must be a CUDA tensor on cuda:{index}")
     return st[0] if T > 1 else H * D
 
 
-class _on:
-    """Makes a tensor's device current for the C call."""
-
-    def __init__(self, device):
-        self._guard = None if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-    def __enter__(self):
-        if self._guard is not None:
-            self._guard.__enter__()
-
-    def __exit__(self, *exc):
-        if self._guard is not None:
-            self._guard.__exit__(*exc)
+def _call_on(device, func, *args):
+    """The C call `func` with `device` current (it launches on the current device)."""
+    if device.index == torch._C._cuda_getDevice():
+        _native.call(func, *args)
+    else:
+        with torch.cuda.device(device):
+            _native.call(func, *args)
 
 
 class ExtendedTables(NamedTuple):
@@ -416,9 +424,11 @@ def paged_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_
     and takes nothing."""
     name = "paged_extend_tables"
     device = block_tables.device
+    if not block_tables.is_cuda:
+        raise ValueError(f"{name}: block_tables must be a CUDA tensor")
     if block_tables.dim() != 2:
         raise ValueError(f"{name}: block_tables must be [B, max_blocks]")
-    B = block_tables.shape[0]
+    B, max_blocks = block_tables.shape
     if context_lens.shape != (B,) or new_lens.shape != (B,) or free_blocks.dim() != 1 or free_head.shape != (1,):
         raise ValueError(f"{name}: context_lens and new_lens [B], free_blocks [F], free_head [1]")
     if num_tokens is None:
@@ -430,7 +440,7 @@ def paged_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_
     def output(t, n, dtype, what):
         if t is None:
             return torch.empty(n, dtype=dtype, device=device)
-        if t.dtype != dtype or t.shape != (n,):
+        if t.dtype is not dtype or t.shape != (n,):
             raise ValueError(f"{name}: {what} must be {dtype} [{n}]")
         return t
 
@@ -440,18 +450,16 @@ def paged_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_
     block_starts = output(block_starts, B + 1, i32, "block_starts")
     lens_out = output(context_lens_out, B, i32, "context_lens_out")
     head_out = output(free_head_out, 1, i32, "free_head_out")
-    for what, t in (("block_tables", block_tables), ("context_lens", context_lens), ("new_lens", new_lens),
-                    ("free_blocks", free_blocks), ("free_head", free_head)):
-        if t.dtype != i32:
-            raise ValueError(f"{name}: {what} must be int32")
-    _require_cuda(device, block_tables=block_tables, context_lens=context_lens, new_lens=new_lens,
-                  free_blocks=free_blocks, free_head=free_head, slot_mapping=slot_mapping, positions=positions,
-                  seq_starts=seq_starts, block_starts=block_starts, context_lens_out=lens_out, free_head_out=head_out)
-    with _on(device):
-        _native.call(name, _ptr(block_tables), block_tables.shape[1], _ptr(context_lens), _ptr(new_lens), B,
-                     int(block_size), _ptr(free_blocks), free_blocks.shape[0], _ptr(free_head), int(num_blocks),
-                     num_tokens, _ptr(slot_mapping), _ptr(positions), _ptr(seq_starts), _ptr(block_starts),
-                     _ptr(lens_out), _ptr(head_out), _stream(stream, device))
+    if not (block_tables.dtype is i32 and context_lens.dtype is i32 and new_lens.dtype is i32
+            and free_blocks.dtype is i32 and free_head.dtype is i32):
+        raise ValueError(f"{name}: block_tables, context_lens, new_lens, free_blocks and free_head must be int32")
+    _check_on(name, device, "block_tables context_lens new_lens free_blocks free_head slot_mapping positions seq_starts "
+              "block_starts context_lens_out free_head_out", block_tables, context_lens, new_lens, free_blocks, free_head,
+              slot_mapping, positions, seq_starts, block_starts, lens_out, head_out)
+    _call_on(device, name, block_tables.data_ptr(), max_blocks, context_lens.data_ptr(), new_lens.data_ptr(), B,
+             int(block_size), free_blocks.data_ptr(), free_blocks.shape[0], free_head.data_ptr(), int(num_blocks),
+             num_tokens, slot_mapping.data_ptr(), positions.data_ptr(), seq_starts.data_ptr(),
+             block_starts.data_ptr(), lens_out.data_ptr(), head_out.data_ptr(), _stream(stream, device))
     return ExtendedTables(slot_mapping, positions, seq_starts, block_starts, lens_out, head_out)
 
 
@@ -505,11 +513,14 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
     E4M3 with k_scale, v_scale (one each) or k_scales, v_scales (block-scaled).  A negative position marks a padding
     row, a negative slot a token that is not stored.  q may be None (keys alone)."""
     name = "paged_rope_append"
-    T, Hkv, D = k.shape
+    kshape, cshape = k.shape, k_cache.shape
     device = k.device
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v.shape != k.shape:
+    if not k.is_cuda:
+        raise ValueError(f"{name}: k must be a CUDA tensor")
+    if len(kshape) != 3 or len(cshape) != 4 or v_cache.shape != cshape or v.shape != kshape:
         raise ValueError(f"{name}: shape mismatch")
-    NB, Hkv2, bs, D2 = k_cache.shape
+    T, Hkv, D = kshape
+    NB, Hkv2, bs, D2 = cshape
     if Hkv2 != Hkv or D2 != D:
         raise ValueError(f"{name}: shape mismatch")
     if positions.dtype != torch.int32 or positions.shape != (T,):
@@ -525,25 +536,27 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
             raise ValueError(f"{name}: k_scale, v_scale or k_scales, v_scales, not both")
         _require_scales(name, k_cache, v_cache, k_scales, v_scales)
     Hq = qs = os = 0
+    index = device.index
     if q is not None:
-        if q.dim() != 3 or q.shape[0] != T or q.shape[2] != D or q.dtype != k.dtype:
+        qshape = q.shape
+        if len(qshape) != 3 or qshape[0] != T or qshape[2] != D or q.dtype != k.dtype:
             raise ValueError(f"{name}: q must be [num_tokens, num_q_heads, head_dim] of k's type")
-        Hq = q.shape[1]
+        Hq = qshape[1]
         if q_out is None:
-            q_out = torch.empty(q.shape, dtype=q.dtype, device=device)
-        elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+            q_out = torch.empty(qshape, dtype=q.dtype, device=device)
+        elif q_out.shape != qshape or q_out.dtype != q.dtype:
             raise ValueError(f"{name}: q_out must match q")
-        qs, os = _rows(name, "q", q, device), _rows(name, "q_out", q_out, device)
+        qs, os = _rows(name, "q", q, index, qshape), _rows(name, "q_out", q_out, index, qshape)
     elif q_out is not None:
         raise ValueError(f"{name}: q_out without q")
-    ks, vs = _rows(name, "k", k, device), _rows(name, "v", v, device)
-    _require_cuda(device, positions=positions, slot_mapping=slot_mapping, inv_freq=inv_freq, k_cache=k_cache,
-                  v_cache=v_cache, k_scale=k_scale, v_scale=v_scale)
-    with _on(device):
-        _native.call(name, _ptr(q), qs, _ptr(k), ks, _ptr(v), vs, _ptr(positions), _ptr(slot_mapping), T,
-                     _ptr(inv_freq), 2 * inv_freq.shape[0], int(bool(interleaved)), float(attention_factor),
-                     _ptr(q_out), os, _ptr(k_cache), _ptr(v_cache), NB, Hq, Hkv, bs, D, _code(k), _code(k_cache),
-                     _ptr(k_scale), _ptr(v_scale), _ptr(k_scales), _ptr(v_scales), _stream(stream, device))
+    ks, vs = _rows(name, "k", k, index, kshape), _rows(name, "v", v, index, kshape)
+    _check_on(name, device, "positions slot_mapping inv_freq k_cache v_cache k_scale v_scale", positions, slot_mapping,
+              inv_freq, k_cache, v_cache, k_scale, v_scale)
+    _call_on(device, name, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
+             slot_mapping.data_ptr(), T, inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved)),
+             float(attention_factor), _ptr(q_out), os, k_cache.data_ptr(), v_cache.data_ptr(), NB, Hq, Hkv, bs, D,
+             _code(k), _code(k_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_scales), _ptr(v_scales),
+             _stream(stream, device))
     return q_out
 
 
@@ -554,19 +567,20 @@ def paged_kv_append_scaled(k, v, slot_mapping, k_cache, v_cache, k_scales, v_sca
     needs a larger one moves the block's codes along.  A token at offset 0 starts its block afresh.  Tokens of one
     block must be neighbours in the call, in slot order."""
     name = "paged_kv_append_scaled"
-    T, Hkv, D = k.shape
+    kshape = k.shape
     device = k_cache.device
     _require_scales(name, k_cache, v_cache, k_scales, v_scales)
     NB, Hkv2, bs, D2 = k_cache.shape
-    if v.shape != k.shape or v.dtype != k.dtype or Hkv2 != Hkv or D2 != D:
+    if len(kshape) != 3 or v.shape != kshape or v.dtype != k.dtype or Hkv2 != kshape[1] or D2 != kshape[2]:
         raise ValueError(f"{name}: shape or type mismatch")
+    T, Hkv, D = kshape
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise ValueError(f"{name}: slot_mapping must be int64 [num_tokens]")
-    ks, vs = _rows(name, "k", k, device), _rows(name, "v", v, device)
-    _require_cuda(device, slot_mapping=slot_mapping)
-    with _on(device):
-        _native.call(name, _ptr(k), ks, _ptr(v), vs, _ptr(slot_mapping), T, _ptr(k_cache), _ptr(v_cache),
-                     _ptr(k_scales), _ptr(v_scales), NB, Hkv, bs, D, _code(k), _stream(stream, device))
+    ks, vs = _rows(name, "k", k, device.index, kshape), _rows(name, "v", v, device.index, kshape)
+    _check_on(name, device, "slot_mapping", slot_mapping)
+    _call_on(device, name, k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, k_cache.data_ptr(),
+             v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), NB, Hkv, bs, D, _code(k),
+             _stream(stream, device))
 
 
 def paged_attention_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out=None,
@@ -575,19 +589,44 @@ def paged_attention_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block
     of 0 (a padding row) gives zeros."""
     args, out, _ = _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
                                        partition_size, workspace, stream)
-    with _on(q.device):
-        _native.call("paged_attention_decode_scaled", *args)
+    _call_on(q.device, "paged_attention_decode_scaled", *args)
     return out
 
 
 def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
                         partition_size, workspace, stream):
     """Validated C arguments of paged_attention_decode_scaled, the output and the workspace."""
-    _require_scales("paged_attention_decode_scaled", k_cache, v_cache, k_scales, v_scales)
-    a, out, workspace = _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_scales, v_scales,
-                                     partition_size, workspace, stream, block_scales=True)
-    # (q, k_cache, v_cache | tables .. scale, out, act | cache_dtype, k_scale, v_scale dropped | partition ..)
-    return (*a[:3], a[16], a[17], *a[3:15], *a[18:]), out, workspace
+    name = "paged_attention_decode_scaled"
+    _require_scales(name, k_cache, v_cache, k_scales, v_scales)
+    qshape = q.shape
+    NB, Hkv, bs, D = k_cache.shape
+    if len(qshape) != 3 or qshape[2] != D:
+        raise ValueError(f"{name}: shape mismatch")
+    B, Hq, _ = qshape
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError(f"{name}: block_tables and context_lens must be int32")
+    tshape = block_tables.shape
+    if len(tshape) != 2 or tshape[0] != B or context_lens.shape != (B,):
+        raise ValueError(f"{name}: block_tables [B, max_blocks], context_lens [B]")
+    device = k_cache.device
+    if out is None:
+        out = torch.empty(qshape, dtype=q.dtype, device=device)
+    elif out.shape != qshape or out.dtype != q.dtype:
+        raise ValueError(f"{name}: out must match q")
+    if not out.is_cuda:
+        _require_out(device, out)
+    _check_on(name, device, "q block_tables context_lens workspace out", q, block_tables, context_lens, workspace,
+              out if out.is_cuda else None)
+    s = _stream(stream, device)
+    if workspace is None:
+        need = workspace_size(B, Hq, Hkv, D, tshape[1], bs, partition_size, True)
+        if need:
+            workspace = _workspace(device, s, need)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+            block_tables.data_ptr(), tshape[1], context_lens.data_ptr(), B, Hq, Hkv, bs, D, NB, float(scale),
+            out.data_ptr(), _code(q), int(partition_size), _ptr(workspace), ws_bytes, s)
+    return args, out, workspace
 
 
 def paged_block_copy(k_cache, v_cache, src_dst_pairs, stream=None, k_scales=None, v_scales=None):

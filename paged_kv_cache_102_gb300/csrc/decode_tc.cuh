@@ -548,7 +548,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             [[maybe_unused]] float ksc = 0.f, vsc = 0.f, lvs = -INFINITY;
             int ci = -1;
             if (lane == 0) {
-                ci = atomicAdd(p.work_counter, 1);
+                // block-scaled without a counter: no more items than blocks, one each
+                if (SCALED && p.work_counter == nullptr) ci = nclaim == 0 ? static_cast<int>(blockIdx.x) : total;
+                else ci = atomicAdd(p.work_counter, 1);
                 if (ci >= total) ci = -1;
             }
             ci = __shfl_sync(0xffffffffu, ci, 0);
@@ -632,7 +634,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         TcItem it;
         int phys = -1;
         // the counter was zeroed by the kernel before, which this launch did not wait for
-        if constexpr (SCALED) asm volatile("griddepcontrol.wait;" ::: "memory");
+        if (SCALED && p.work_counter != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
         while (ok && claim(it, phys)) {
         }
     } else if (warp >= 6) {

@@ -84,6 +84,12 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorM
     const int grid = static_cast<int>(items < static_cast<long long>(sms) * ctas_per_sm ? items : sms * ctas_per_sm);
     if (grid <= 0) return cudaSuccess;
     if constexpr (CACHE == kE4M3B) {
+        if (items <= grid) {  // an item a block: nothing to claim, nothing to zero
+            DecodeParams one = p;
+            one.work_counter = nullptr;
+            kern<<<grid, threads, smem, s>>>(km, vm, qm, one);
+            return cudaGetLastError();
+        }
         // zero the work counter, and let the decode kernel's prologue run meanwhile
         zero_counter_kernel<<<1, 32, 0, s>>>(p.work_counter);
         e = cudaGetLastError();
