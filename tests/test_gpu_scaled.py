@@ -373,3 +373,60 @@ def test_block_copy_and_swap_take_scales_along(pkv, hkv, bs, D):
     bad = torch.tensor([nb], dtype=torch.int32).cuda()
     pkv.paged_block_swap(d[0], d[1], bad, st, pkv.SWAP_OUT, k_scales=d[2], v_scales=d[3], scale_staging=sc)
     assert pkv.device_error(reset=True) == pkv.DEV_BAD_PAIR
+
+
+# ------------------------------------------------------------- PagedKVCache ---
+@pytest.mark.parametrize("D,hq,hkv", [(128, 16, 2), (64, 4, 4)])
+def test_cache_with_block_scales_forks_and_rotates(pkv, D, hq, hkv):
+    """PagedKVCache over block-scaled pools: rotary appends, a fork in the middle of a block, copy-on-write with the
+    scales, decode against the definition over the cache as it is, and the shared tokens equal in both sequences."""
+    from paged_kv_cache_102_gb300.cache import PagedKVCache
+    g = _gen((D, hq, hkv))
+    bs = 16
+    cache = PagedKVCache(24, hkv, bs, D, block_scales=True)
+    freq, factor = pkv.rope_inv_freq(D, scaling="yarn", factor=4.0, original_context=64)
+    cache.add_sequence(0, 0)
+    rand = lambda n, h: torch.randn(n, h, D, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    for _ in range(21):
+        cache.rope_append([0], rand(1, hq), rand(1, hkv), rand(1, hkv), freq, attention_factor=factor)
+    cache.fork(0, 1)
+    shared = [t.clone() for t in (cache.k_cache, cache.v_cache, cache.k_scales, cache.v_scales)]
+    for i in range(14):
+        q = cache.rope_append([0, 1], rand(2, hq), rand(2, hkv) * 2.0 ** (i % 5), rand(2, hkv), freq,
+                              attention_factor=factor)
+        out = cache.decode([0, 1], q, 0.1)
+    torch.cuda.synchronize()
+    tables, lens = cache.blocks.tables([0, 1])
+    assert lens.tolist() == [35, 35] and tables[0, 0] == tables[1, 0] and tables[0, 1] != tables[1, 1]
+    want, bound = ref.decode_scaled(ref.f64(q), cache.k_cache.cpu().numpy(), cache.v_cache.cpu().numpy(),
+                                    cache.k_scales.cpu().numpy(), cache.v_scales.cpu().numpy(), tables, lens, 0.1, bs,
+                                    torch.bfloat16)
+    assert np.all(np.abs(ref.f64(out) - want) <= bound)
+    old_b = int(tables[0, 1]) if bool((shared[3][int(tables[0, 1])] > 0).any()) else int(tables[1, 1])
+    was = ref.VALUES[shared[1][old_b, :, :5].cpu().numpy()] * shared[3][old_b].cpu().numpy()[:, None, None]
+    for b in tables[:, 1]:  # the 5 tokens of the shared, partly filled block: values kept (V scales of N(0, 1) rows
+        s = cache.v_scales[int(b)].cpu().numpy()[:, None, None]  # move by a doubling or two at most)
+        now = ref.VALUES[cache.v_cache[int(b), :, :5].cpu().numpy()] * s
+        assert np.all(np.abs(now - was) <= 2.0 ** -9 * s)
+    # an appended token without rotation
+    cache.append([1], rand(1, hkv), rand(1, hkv))
+    assert cache.blocks.context_len(1) == 36
+
+
+def test_two_streams_with_a_workspace_each(pkv):
+    """Two decodes at once on streams of their own, default workspaces: each has its own."""
+    case = ("bf16", 32, 4, 128, 16, -1, "wide")
+    a, b = (_decode_case(case[:6] + (k,), LENS) for k in ("wide", "narrow"))
+    da, db = [t.cuda() for t in a], [t.cuda() for t in b]
+    run = lambda d: pkv.paged_attention_decode_scaled(d[0], d[1], d[2], d[3], d[4], d[5], d[6], 0.1)  # noqa: E731
+    want = run(da), run(db)
+    torch.cuda.synchronize()
+    s1, s2 = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(5):
+        for s, d in ((s1, da), (s2, db)):
+            with torch.cuda.stream(s):
+                got.append(run(d))
+    torch.cuda.synchronize()
+    for i, o in enumerate(got):
+        assert torch.equal(o, want[i % 2])
