@@ -62,14 +62,14 @@ def load():
     return _native.lib()
 
 
+_CODES = {torch.float16: F16, torch.bfloat16: BF16, torch.uint8: E4M3, torch.float8_e4m3fn: E4M3}
+
+
 def _code(t: torch.Tensor) -> int:
-    if t.dtype == torch.float16:
-        return F16
-    if t.dtype == torch.bfloat16:
-        return BF16
-    if t.dtype in (torch.uint8, torch.float8_e4m3fn):
-        return E4M3
-    raise TypeError(f"unsupported element type {t.dtype}")
+    code = _CODES.get(t.dtype)
+    if code is None:
+        raise TypeError(f"unsupported element type {t.dtype}")
+    return code
 
 
 def _ptr(t):
@@ -88,6 +88,8 @@ def _stream(stream, device) -> int:
 def _require_out(device, out):
     """`out` may be a CUDA tensor on `device` or a pinned host tensor, which the
     kernels write directly over the host link."""
+    if out.is_cuda and out.get_device() == device.index and out.is_contiguous():
+        return
     if out.is_pinned() and not out.is_cuda:
         if not out.is_contiguous():
             raise ValueError("out must be contiguous")
@@ -357,12 +359,17 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, sel_tables, sel_lens, sca
 _E4M3_TYPES = (torch.uint8, torch.float8_e4m3fn)
 
 
-def _check_on(name, device, names, *tensors):
-    """Every tensor (None passes) is contiguous and on `device`; `names` are theirs, space-separated."""
-    index = device.index
-    for i, t in enumerate(tensors):
-        if t is not None and (t.get_device() != index or not t.is_contiguous()):
-            raise ValueError(f"{name}: {names.split()[i]} must be a contiguous CUDA tensor on {device}")
+_contiguous, _device_of, _pointer = torch.Tensor.is_contiguous, torch.Tensor.get_device, torch.Tensor.data_ptr
+
+
+def _pointers(name, device, names, *tensors):
+    """Data pointers of tensors that have to be contiguous and on `device`; `names` are theirs, space-separated.
+    (Mapped builtins: these checks are most of what a small call costs on the host.)"""
+    if not all(map(_contiguous, tensors)) or set(map(_device_of, tensors)) != {device.index}:
+        for what, t in zip(names.split(), tensors):
+            if t.get_device() != device.index or not t.is_contiguous():
+                raise ValueError(f"{name}: {what} must be a contiguous CUDA tensor on {device}")
+    return map(_pointer, tensors)
 
 
 def _require_scales(name, k_cache, v_cache, k_scales, v_scales):
@@ -374,11 +381,11 @@ def _require_scales(name, k_cache, v_cache, k_scales, v_scales):
         raise ValueError(f"{name}: a block-scaled cache holds E4M3 codes (uint8 or float8_e4m3fn)")
     if k_scales is None or v_scales is None:
         raise ValueError(f"{name}: k_scales and v_scales go together")
-    want = shape[:2]
-    if (k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32 or k_scales.shape != want
-            or v_scales.shape != want):
+    sshape = k_scales.shape
+    if (k_scales.dtype is not torch.float32 or v_scales.dtype is not torch.float32 or v_scales.shape != sshape
+            or len(sshape) != 2 or sshape[0] != shape[0] or sshape[1] != shape[1]):
         raise ValueError(f"{name}: k_scales and v_scales must be float32 [num_blocks, num_kv_heads]")
-    _check_on(name, k_cache.device, "k_cache v_cache k_scales v_scales", k_cache, v_cache, k_scales, v_scales)
+    return shape
 
 
 def _rows(name, what, t, index, shape):
@@ -453,13 +460,12 @@ def paged_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_
     if not (block_tables.dtype is i32 and context_lens.dtype is i32 and new_lens.dtype is i32
             and free_blocks.dtype is i32 and free_head.dtype is i32):
         raise ValueError(f"{name}: block_tables, context_lens, new_lens, free_blocks and free_head must be int32")
-    _check_on(name, device, "block_tables context_lens new_lens free_blocks free_head slot_mapping positions seq_starts "
-              "block_starts context_lens_out free_head_out", block_tables, context_lens, new_lens, free_blocks, free_head,
-              slot_mapping, positions, seq_starts, block_starts, lens_out, head_out)
-    _call_on(device, name, block_tables.data_ptr(), max_blocks, context_lens.data_ptr(), new_lens.data_ptr(), B,
-             int(block_size), free_blocks.data_ptr(), free_blocks.shape[0], free_head.data_ptr(), int(num_blocks),
-             num_tokens, slot_mapping.data_ptr(), positions.data_ptr(), seq_starts.data_ptr(),
-             block_starts.data_ptr(), lens_out.data_ptr(), head_out.data_ptr(), _stream(stream, device))
+    tables, lens, new, free, head, *outs = _pointers(
+        name, device, "block_tables context_lens new_lens free_blocks free_head slot_mapping positions seq_starts "
+        "block_starts context_lens_out free_head_out", block_tables, context_lens, new_lens, free_blocks, free_head,
+        slot_mapping, positions, seq_starts, block_starts, lens_out, head_out)
+    _call_on(device, name, tables, max_blocks, lens, new, B, int(block_size), free, free_blocks.shape[0], head,
+             int(num_blocks), num_tokens, *outs, _stream(stream, device))
     return ExtendedTables(slot_mapping, positions, seq_starts, block_starts, lens_out, head_out)
 
 
@@ -535,6 +541,16 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
         if k_scale is not None or v_scale is not None:
             raise ValueError(f"{name}: k_scale, v_scale or k_scales, v_scales, not both")
         _require_scales(name, k_cache, v_cache, k_scales, v_scales)
+        s1 = s2 = None
+        kc, vc, pos, slots, freq, sb1, sb2 = _pointers(
+            name, device, "k_cache v_cache positions slot_mapping inv_freq k_scales v_scales", k_cache, v_cache,
+            positions, slot_mapping, inv_freq, k_scales, v_scales)
+    else:
+        sb1 = sb2 = None
+        kc, vc, pos, slots, freq = _pointers(name, device, "k_cache v_cache positions slot_mapping inv_freq", k_cache,
+                                             v_cache, positions, slot_mapping, inv_freq)
+        s1, s2 = (None if t is None else next(_pointers(name, device, what, t))
+                  for what, t in (("k_scale", k_scale), ("v_scale", v_scale)))
     Hq = qs = os = 0
     index = device.index
     if q is not None:
@@ -550,13 +566,9 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
     elif q_out is not None:
         raise ValueError(f"{name}: q_out without q")
     ks, vs = _rows(name, "k", k, index, kshape), _rows(name, "v", v, index, kshape)
-    _check_on(name, device, "positions slot_mapping inv_freq k_cache v_cache k_scale v_scale", positions, slot_mapping,
-              inv_freq, k_cache, v_cache, k_scale, v_scale)
-    _call_on(device, name, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, positions.data_ptr(),
-             slot_mapping.data_ptr(), T, inv_freq.data_ptr(), 2 * inv_freq.shape[0], int(bool(interleaved)),
-             float(attention_factor), _ptr(q_out), os, k_cache.data_ptr(), v_cache.data_ptr(), NB, Hq, Hkv, bs, D,
-             _code(k), _code(k_cache), _ptr(k_scale), _ptr(v_scale), _ptr(k_scales), _ptr(v_scales),
-             _stream(stream, device))
+    _call_on(device, name, _ptr(q), qs, k.data_ptr(), ks, v.data_ptr(), vs, pos, slots, T, freq, 2 * inv_freq.shape[0],
+             1 if interleaved else 0, attention_factor, _ptr(q_out), os, kc, vc, NB, Hq, Hkv, bs, D, _code(k),
+             _code(k_cache), s1, s2, sb1, sb2, _stream(stream, device))
     return q_out
 
 
@@ -569,17 +581,16 @@ def paged_kv_append_scaled(k, v, slot_mapping, k_cache, v_cache, k_scales, v_sca
     name = "paged_kv_append_scaled"
     kshape = k.shape
     device = k_cache.device
-    _require_scales(name, k_cache, v_cache, k_scales, v_scales)
-    NB, Hkv2, bs, D2 = k_cache.shape
+    NB, Hkv2, bs, D2 = _require_scales(name, k_cache, v_cache, k_scales, v_scales)
     if len(kshape) != 3 or v.shape != kshape or v.dtype != k.dtype or Hkv2 != kshape[1] or D2 != kshape[2]:
         raise ValueError(f"{name}: shape or type mismatch")
     T, Hkv, D = kshape
     if slot_mapping.dtype != torch.int64 or slot_mapping.shape != (T,):
         raise ValueError(f"{name}: slot_mapping must be int64 [num_tokens]")
     ks, vs = _rows(name, "k", k, device.index, kshape), _rows(name, "v", v, device.index, kshape)
-    _check_on(name, device, "slot_mapping", slot_mapping)
-    _call_on(device, name, k.data_ptr(), ks, v.data_ptr(), vs, slot_mapping.data_ptr(), T, k_cache.data_ptr(),
-             v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), NB, Hkv, bs, D, _code(k),
+    slots, kc, vc, s1, s2 = _pointers(name, device, "slot_mapping k_cache v_cache k_scales v_scales", slot_mapping,
+                                      k_cache, v_cache, k_scales, v_scales)
+    _call_on(device, name, k.data_ptr(), ks, v.data_ptr(), vs, slots, T, kc, vc, s1, s2, NB, Hkv, bs, D, _code(k),
              _stream(stream, device))
 
 
@@ -597,9 +608,8 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
                         partition_size, workspace, stream):
     """Validated C arguments of paged_attention_decode_scaled, the output and the workspace."""
     name = "paged_attention_decode_scaled"
-    _require_scales(name, k_cache, v_cache, k_scales, v_scales)
+    NB, Hkv, bs, D = _require_scales(name, k_cache, v_cache, k_scales, v_scales)
     qshape = q.shape
-    NB, Hkv, bs, D = k_cache.shape
     if len(qshape) != 3 or qshape[2] != D:
         raise ValueError(f"{name}: shape mismatch")
     B, Hq, _ = qshape
@@ -613,19 +623,18 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
         out = torch.empty(qshape, dtype=q.dtype, device=device)
     elif out.shape != qshape or out.dtype != q.dtype:
         raise ValueError(f"{name}: out must match q")
-    if not out.is_cuda:
-        _require_out(device, out)
-    _check_on(name, device, "q block_tables context_lens workspace out", q, block_tables, context_lens, workspace,
-              out if out.is_cuda else None)
+    if not q.is_cuda:
+        raise ValueError(f"{name}: q must be a CUDA tensor")
+    _require_out(device, out)
     s = _stream(stream, device)
     if workspace is None:
         need = workspace_size(B, Hq, Hkv, D, tshape[1], bs, partition_size, True)
-        if need:
-            workspace = _workspace(device, s, need)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    args = (q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
-            block_tables.data_ptr(), tshape[1], context_lens.data_ptr(), B, Hq, Hkv, bs, D, NB, float(scale),
-            out.data_ptr(), _code(q), int(partition_size), _ptr(workspace), ws_bytes, s)
+        workspace = _workspace(device, s, max(need, 1))  # (0: an argument that the library refuses)
+    qp, kc, vc, s1, s2, tables, lens, ws = _pointers(
+        name, device, "q k_cache v_cache k_scales v_scales block_tables context_lens workspace", q, k_cache, v_cache,
+        k_scales, v_scales, block_tables, context_lens, workspace)
+    args = (qp, kc, vc, s1, s2, tables, tshape[1], lens, B, Hq, Hkv, bs, D, NB, scale, out.data_ptr(), _code(q),
+            partition_size, ws, workspace.numel() * workspace.element_size(), s)
     return args, out, workspace
 
 
@@ -640,6 +649,7 @@ def paged_block_copy(k_cache, v_cache, src_dst_pairs, stream=None, k_scales=None
     block_bytes = k_cache[0].numel() * k_cache.element_size()
     if k_scales is not None or v_scales is not None:
         _require_scales("paged_block_copy", k_cache, v_cache, k_scales, v_scales)
+        _require_cuda(k_cache.device, k_scales=k_scales, v_scales=v_scales)
         _native.call("paged_block_copy_scaled", _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
                      _ptr(src_dst_pairs), src_dst_pairs.shape[0], k_cache.shape[0], k_cache.shape[1], block_bytes,
                      _stream(stream, k_cache.device))
@@ -666,6 +676,7 @@ def paged_block_swap(k_cache, v_cache, block_ids, staging, direction, stream=Non
         raise ValueError("paged_block_swap: host staging must be pinned memory")
     if k_scales is not None or v_scales is not None or scale_staging is not None:
         _require_scales("paged_block_swap", k_cache, v_cache, k_scales, v_scales)
+        _require_cuda(k_cache.device, k_scales=k_scales, v_scales=v_scales)
         if (scale_staging is None or scale_staging.dtype != torch.float32 or not scale_staging.is_contiguous()
                 or scale_staging.numel() < block_ids.numel() * 2 * k_cache.shape[1]):
             raise ValueError("paged_block_swap: scale_staging must be contiguous float32 [n, 2, num_kv_heads]")
