@@ -211,13 +211,13 @@ cudaError_t launch_scales_swap(const ScalesSwapParams& p, cudaStream_t stream) {
 // their sums through shared memory.  Rows that fit one partition were written
 // directly by the partition kernel.  The kernel is launched as a programmatic
 // dependent of the partition kernel: griddepcontrol.wait returns once that
-// grid has completed and its writes are visible.
+// grid has completed and its writes are visible.  The lengths are not its
+// writes: they are read before the wait.
 // ---------------------------------------------------------------------------
 constexpr int kMergeWarps = 8;
 
 template <int ACT, int D, int W>
 __global__ void __launch_bounds__(32 * kMergeWarps) paged_decode_merge_kernel(MergeParams p) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     constexpr int V = D / 32;  // channels per lane
     constexpr int ROWS = kMergeWarps / W;
     __shared__ float s_acc[W > 1 ? kMergeWarps : 1][D];
@@ -239,6 +239,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_decode_merge_kernel(Me
         n_parts = active ? (L + p.partition_size - 1) / p.partition_size : 0;
         active = n_parts > 1;
     }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     float acc[V] = {};
     float den = 0.f;
     if (active && W == 1 && n_parts <= 32) {
@@ -285,6 +286,54 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_decode_merge_kernel(Me
             const float* src = o + static_cast<int64_t>(k) * D;
 #pragma unroll
             for (int v = 0; v < V; ++v) acc[v] = fmaf(wk, src[v], acc[v]);
+        }
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
+    } else if (active && W > 1 && n_parts <= 8 * W) {
+        // Few partitions a warp: their vectors and the (max, sum) pairs of parts
+        // lane and 32 + lane are all loaded before any is used; sums in the
+        // order of the loop below.
+        constexpr int C = 8;
+        const float* ml = p.ws_ml + row * p.max_parts * 2;
+        const float* o = p.ws_o + row * p.max_parts * D + lane * V;
+        const float2 none = make_float2(-INFINITY, 0.f);
+        const float2 a0 = lane < n_parts ? *reinterpret_cast<const float2*>(ml + 2 * lane) : none;
+        const float2 a1 = 32 + lane < n_parts ? *reinterpret_cast<const float2*>(ml + 2 * (32 + lane)) : none;
+        float x[C][V];
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int k = sub + j * W;
+            if (k < n_parts) {
+                if constexpr (V == 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(o + static_cast<int64_t>(k) * D);
+                    x[j][0] = t.x;
+                    x[j][1] = t.y;
+                    x[j][2] = t.z;
+                    x[j][3] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2*>(o + static_cast<int64_t>(k) * D);
+                    x[j][0] = t.x;
+                    x[j][1] = t.y;
+                }
+            } else {
+#pragma unroll
+                for (int v = 0; v < V; ++v) x[j][v] = 0.f;
+            }
+        }
+        float M = fmaxf(a0.x, a1.x);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        const float w0 = lane < n_parts ? a0.y * exp2f(a0.x - M) : 0.f;
+        const float w1 = 32 + lane < n_parts ? a1.y * exp2f(a1.x - M) : 0.f;
+        if (lane % W == sub) den = w0 + w1;
+#pragma unroll
+        for (int j = 0; j < C; ++j) {
+            const int k = sub + j * W;
+            const float wk = __shfl_sync(0xffffffffu, k < 32 ? w0 : w1, k & 31);
+            if (k < n_parts) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) acc[v] = fmaf(wk, x[j][v], acc[v]);
+            }
         }
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) den += __shfl_xor_sync(0xffffffffu, den, off);
