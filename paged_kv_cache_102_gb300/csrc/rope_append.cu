@@ -434,7 +434,7 @@ __device__ __forceinline__ void run_row(const RopeAppendParams& p, const RunRows
 // The largest finite element of the rows r, r + rp, ... of a run (one warp's).
 // For runs that do not fit the registers, and those with an infinity.
 template <int ACT, int PAIRS>
-__device__ __noinline__ float run_top(const RopeAppendParams& p, const RunRows& run, int n, int r, int rp, int c, bool idle) {
+__device__ __noinline__ float run_top(const RopeAppendParams& p, const RunRows run, int n, int r, int rp, int c, bool idle) {
     float top = 0.f;
 #pragma unroll 1
     for (int i0 = 0; i0 < n; i0 += rp) {
@@ -446,7 +446,7 @@ __device__ __noinline__ float run_top(const RopeAppendParams& p, const RunRows& 
 }
 
 template <int ACT, int PAIRS>
-__device__ __noinline__ void run_codes(const RopeAppendParams& p, const RunRows& run, int n, int off0, int r, int rp, int c,
+__device__ __noinline__ void run_codes(const RopeAppendParams& p, const RunRows run, int n, int off0, int r, int rp, int c,
                                        bool idle, float now) {
     const Divisor by(now);
 #pragma unroll 1
@@ -477,10 +477,20 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, const RunR
     const int r = (W == 2 ? (warp & 1) * rows : 0) + lane_row;
     const float old = off0 == 0 ? 0.f : *run.scale;
     const bool fits = n <= GROUP * rp;
-    uint4 u[GROUP];
-    float x[TURN ? GROUP : 1][8];
-    float top = 0.f;
+    // the pair's maximum; behind its barrier both warps have read the old scale
+    auto joined_top = [&](float top) {
+        if constexpr (W == 2) {
+            if (lane == 0) tops2[warp] = top;
+            asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+            top = fmaxf(top, tops2[warp ^ 1]);
+        }
+        return top;
+    };
+    float now;
     if (fits) {
+        uint4 u[GROUP];
+        float x[TURN ? GROUP : 1][8];
+        float top = 0.f;
         const uint16_t* src = run.src + r * run.stride + c * 8;
 #pragma unroll
         for (int j = 0; j < GROUP; ++j)
@@ -505,39 +515,48 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, const RunR
         if (!TURN)
             top = fmaxf(act_to_float<ACT>(static_cast<uint16_t>(tops)), act_to_float<ACT>(static_cast<uint16_t>(tops >> 16)));
         top = warp_max(top);
+        if (!(top <= 3.402823466e38f)) {  // an infinity among them: the largest finite one instead
+            top = 0.f;
+#pragma unroll
+            for (int j = 0; j < GROUP; ++j) {
+                if (j * rp >= n) break;
+                float y[8];
+                if constexpr (TURN) {
+                    finite_top(x[j], top);
+                } else {
+                    Vec16<ACT>::to_float(u[j], y);
+                    finite_top(y, top);
+                }
+            }
+            top = warp_max(top);
+        }
+        now = new_scale(joined_top(top), old);
+        const Divisor by(now);
+        uint8_t* dst = run.tile + (off0 + r) * p.head_dim + c * 8;
+#pragma unroll
+        for (int j = 0; j < GROUP; ++j) {
+            if (j * rp >= n) break;
+            float y[8];
+            if constexpr (TURN) {
+#pragma unroll
+                for (int k = 0; k < 8; ++k) y[k] = x[j][k];
+            } else {
+                Vec16<ACT>::to_float(u[j], y);
+            }
+            by.divide8(y);
+            if (!idle && j * rp + r < n) *reinterpret_cast<uint2*>(dst + j * rp * p.head_dim) = to_codes(y);
+        }
+    } else {
+        now = new_scale(joined_top(run_top<ACT, PAIRS>(p, run, n, r, rp, c, idle)), old);
+        run_codes<ACT, PAIRS>(p, run, n, off0, r, rp, c, idle, now);
     }
-    if (!fits || !(top <= 3.402823466e38f)) top = run_top<ACT, PAIRS>(p, run, n, r, rp, c, idle);
-    if constexpr (W == 2) {  // the pair's other half (also: both have read the old scale)
-        if (lane == 0) tops2[warp] = top;
-        asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-        top = fmaxf(top, tops2[warp ^ 1]);
-    }
-    const float now = new_scale(top, old);
     if (now != old) {
         __syncwarp();  // every lane has read the old scale
         if (lane == 0 && (W == 1 || !(warp & 1))) *run.scale = now;
+        // the block's other rows (last, when nothing else needs registers)
         if (old > 0.f)
             requantise(run.tile, p.block_size, lpr, off0, n, __fdiv_rn(old, now), W == 2 ? (warp & 1) * 32 + lane : lane,
                        32 * W);
-    }
-    if (!fits) {
-        run_codes<ACT, PAIRS>(p, run, n, off0, r, rp, c, idle, now);
-        return;
-    }
-    const Divisor by(now);
-    uint8_t* dst = run.tile + (off0 + r) * p.head_dim + c * 8;
-#pragma unroll
-    for (int j = 0; j < GROUP; ++j) {
-        if (j * rp >= n) break;
-        if constexpr (!TURN) {
-            float y[8];
-            Vec16<ACT>::to_float(u[j], y);
-            by.divide8(y);
-            if (!idle && j * rp + r < n) *reinterpret_cast<uint2*>(dst + j * rp * p.head_dim) = to_codes(y);
-        } else {
-            by.divide8(x[j]);
-            if (!idle && j * rp + r < n) *reinterpret_cast<uint2*>(dst + j * rp * p.head_dim) = to_codes(x[j]);
-        }
     }
 }
 
@@ -574,12 +593,12 @@ __device__ __forceinline__ void single_rows(const RopeAppendParams& p, int t0, i
     const float now = new_scale(top, old);
     uint8_t* tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) +
                     (blk * p.num_kv_heads + head) * p.block_size * p.head_dim;
+    Divisor(now).divide8(x);
+    *reinterpret_cast<uint2*>(tile + off0 * p.head_dim + c * 8) = to_codes(x);
     if (now != old) {
         if (c == 0) *scale = now;  // (every lane read the old one before the shuffles)
         if (old > 0.f) requantise(tile, p.block_size, lpr, off0, 1, __fdiv_rn(old, now), c, lpr);
     }
-    Divisor(now).divide8(x);
-    *reinterpret_cast<uint2*>(tile + off0 * p.head_dim + c * 8) = to_codes(x);
 }
 
 // Runs that start in window w of `window` < 32 tokens: block `part` of `split`
