@@ -226,6 +226,21 @@ __device__ __forceinline__ uint2 to_codes(const float* x) {
     return make_uint2(w[0], w[1]);
 }
 
+// Binary16 elements divided by 2^e stay in binary16: for -15 <= e <= 24 the
+// factor is a binary16 value and the product exact, unless it falls among the
+// subnormals, below 2^-14, where every E4M3 result is 0 (the least code is 2^-9).
+// Half the instructions of the way through binary32.
+__device__ __forceinline__ uint2 half_codes_of(const uint4& u, uint32_t factor2) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    uint32_t q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[i]), *reinterpret_cast<const __half2*>(&factor2));
+        q[i] = __nv_cvt_halfraw2_to_fp8x2(*reinterpret_cast<const __half2_raw*>(&y), __NV_SATFINITE, __NV_E4M3);
+    }
+    return make_uint2(q[0] | (q[1] << 16), q[2] | (q[3] << 16));
+}
+
 // Division by s: a product with the exact reciprocal when s is a power of two
 // within 2^-126 .. 2^126 (the same value, without a division), else a quotient.
 struct Divisor {
@@ -235,6 +250,11 @@ struct Divisor {
         const uint32_t b = __float_as_uint(s), e = b >> 23;
         exact = (b & 0x7fffffu) == 0 && e >= 1 && e <= 253;
         r = __uint_as_float((254u - e) << 23);
+    }
+    __device__ __forceinline__ bool half_exact() const { return exact && s >= 0x1p-15f && s <= 0x1p24f; }
+    __device__ __forceinline__ uint2 half_codes(const uint4& u) const {
+        const uint32_t h = __half_as_ushort(__float2half_rn(r));
+        return half_codes_of(u, h | (h << 16));
     }
     __device__ __forceinline__ void divide8(float* x) const {
         if (exact) {
@@ -492,10 +512,11 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, const RunR
         float x[TURN ? GROUP : 1][8];
         float top = 0.f;
         const uint16_t* src = run.src + r * run.stride + c * 8;
+        const int64_t src_step = rp * run.stride;
+        const int left = idle ? 0 : n - r;  // this lane has pass j where j * rp < left
 #pragma unroll
-        for (int j = 0; j < GROUP; ++j)
-            u[j] = !idle && j * rp + r < n ? *reinterpret_cast<const uint4*>(src + j * rp * run.stride)
-                                           : make_uint4(0u, 0u, 0u, 0u);
+        for (int j = 0; j < GROUP; ++j, src += src_step)
+            u[j] = j * rp < left ? *reinterpret_cast<const uint4*>(src) : make_uint4(0u, 0u, 0u, 0u);
         [[maybe_unused]] uint32_t tops = 0;
 #pragma unroll
         for (int j = 0; j < GROUP; ++j) {
@@ -533,18 +554,27 @@ __device__ __forceinline__ void scaled_run(const RopeAppendParams& p, const RunR
         now = new_scale(joined_top(top), old);
         const Divisor by(now);
         uint8_t* dst = run.tile + (off0 + r) * p.head_dim + c * 8;
+        const int dst_step = rp * p.head_dim;
+        if (ACT == kF16 && !TURN && by.half_exact()) {
 #pragma unroll
-        for (int j = 0; j < GROUP; ++j) {
-            if (j * rp >= n) break;
-            float y[8];
-            if constexpr (TURN) {
-#pragma unroll
-                for (int k = 0; k < 8; ++k) y[k] = x[j][k];
-            } else {
-                Vec16<ACT>::to_float(u[j], y);
+            for (int j = 0; j < GROUP; ++j, dst += dst_step) {
+                if (j * rp >= n) break;
+                if (j * rp < left) *reinterpret_cast<uint2*>(dst) = by.half_codes(u[j]);
             }
-            by.divide8(y);
-            if (!idle && j * rp + r < n) *reinterpret_cast<uint2*>(dst + j * rp * p.head_dim) = to_codes(y);
+        } else {
+#pragma unroll
+            for (int j = 0; j < GROUP; ++j, dst += dst_step) {
+                if (j * rp >= n) break;
+                float y[8];
+                if constexpr (TURN) {
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) y[k] = x[j][k];
+                } else {
+                    Vec16<ACT>::to_float(u[j], y);
+                }
+                by.divide8(y);
+                if (j * rp < left) *reinterpret_cast<uint2*>(dst) = to_codes(y);
+            }
         }
     } else {
         now = new_scale(joined_top(run_top<ACT, PAIRS>(p, run, n, r, rp, c, idle)), old);
@@ -709,7 +739,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_rows_kernel(const RopeApp
 
 // Prompts: runs of many tokens.
 template <int ACT, int PAIRS>
-__global__ void __launch_bounds__(kWarps * 32, 3) scaled_runs_kernel(const RopeAppendParams p, const Split d) {
+__global__ void __launch_bounds__(kWarps * 32, PAIRS == kPairsNone ? 4 : 3) scaled_runs_kernel(const RopeAppendParams p, const Split d) {
     __shared__ __align__(16) float table[PAIRS == kPairsNone ? 4 : kTable];
     asm volatile("griddepcontrol.launch_dependents;");
     const int w = blockIdx.x / d.share;
