@@ -160,10 +160,14 @@ int pkv_scaled_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, i
     if (max_blocks_per_seq < 1 || block_size < 1 || num_kv_heads < 1 || num_q_heads < 1) return -1;
     const long long max_ctx = static_cast<long long>(max_blocks_per_seq) * block_size;
     const long long single = (max_ctx + kStageTokens - 1) / kStageTokens * kStageTokens;
-    // the tensor-core kernel's 512 tokens whatever the group; 256 where that leaves a few items a CTA
+    // The tensor-core kernel's 512 tokens whatever the group; 256 for so few
+    // items that twice as many still get an SM each.  Measured, 512 / 256 tokens,
+    // head_dim 128, one and eight query heads: 32 items 9.9 / 8.6 and 10.8 / 9.5
+    // us, 128 items 10.4 / 10.6 and 11.8 / 11.8, 256 items 12.4 / 14.6 and
+    // 13.1 / 18.2, 512 items 16.1 / 16.6 and 17.9 / 20.7.
     long long P = kAutoPartitionGrouped;
     const long long items = static_cast<long long>(num_seqs) * num_kv_heads * ((max_ctx + P - 1) / P);
-    if (items >= kAutoGroupedItemsLow && items < kAutoGroupedItemsHigh && (P / 2) % block_size == 0) P /= 2;
+    if (items <= 64 && (P / 2) % block_size == 0) P /= 2;
     if (P >= single) P = single;
     return static_cast<int>(P);
 }

@@ -85,8 +85,8 @@ def test_decode_scaled_refusals(pkv_lib):
 
 def test_scaled_partitions_and_workspace(pkv_lib):
     size, ws = pkv_lib.resolve_partition_size, pkv_lib.workspace_size
-    assert size(4, 8, 8, 128, 129, 16, block_scales=True) == 512       # whatever the group
-    assert size(16, 8, 8, 64, 129, 16, block_scales=True) == 256       # 16 * 8 * 5 = 640 items
+    assert size(4, 8, 8, 128, 129, 16, block_scales=True) == 512       # 4 * 8 * 5 = 160 items, whatever the group
+    assert size(1, 8, 8, 64, 129, 16, block_scales=True) == 256        # 8 * 5 = 40 items
     assert size(4, 8, 8, 128, 8, 16, block_scales=True) == 128         # the whole context
     assert size(4, 8, 8, 128, 129, 16, 1024, block_scales=True) == 1024
     assert size(4, 8, 8, 128, 129, 16, 48, block_scales=True) == -1
