@@ -32,7 +32,8 @@
 // the factor of the reduced dot product, the V scale the weights.  Weights are
 // kept relative to a power of two 2^mv near the V scales seen, moved (with acc)
 // when a block's scale is more than 2^7 away from it, so that p * vs / 2^mv
-// stays within binary16 whatever the scales are.
+// stays within binary16 whatever the scales are; binary16 activations, whose
+// result would show a weight's rounding to binary16, keep weights in binary32.
 #pragma once
 
 #include <type_traits>
@@ -390,6 +391,15 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
 #pragma unroll
                         for (int i = 0; i < QN; ++i) {
                             const uint32_t vh = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2))));
+                            if constexpr (C::SCALED && ACT == kF16) {
+                                const float2 vf2 = __half22float2(*reinterpret_cast<const __half2*>(&vh));
+#pragma unroll
+                                for (int g = 0; g < G; ++g) {
+                                    acc[g][2 * i] = fmaf(pr[pp][g], vf2.x, acc[g][2 * i]);
+                                    acc[g][2 * i + 1] = fmaf(pr[pp][g], vf2.y, acc[g][2 * i + 1]);
+                                }
+                                continue;
+                            }
 #pragma unroll
                             for (int g = 0; g < G; ++g)
                                 fma_f16s_f32(__half_as_ushort(__float2half_rn(pr[pp][g])), vh, acc[g][2 * i],

@@ -77,6 +77,10 @@
 // keep their precision whatever the scales of the other blocks are.  The sum
 // of 2^(score - R) is the denominator; log2 |vs| - ev enters R at no less than
 // -100, which keeps it finite (and a row without any V scale but 0 defined).
+// Two E4M3 parts of w leave up to 2^-8 of it, which the rounding of a bfloat16
+// result covers but not that of a binary16 one, so binary16 activations take a
+// third part: up to four heads fill 12 of the 16 columns, eight heads use 24 of
+// 32 (a second 16-byte column of P, with a ring of one stage less).
 // The producer that converts q finds its power-of-2 scale too.  (Two groups of
 // softmax warps with four heads each were no faster at eight query heads: 81.3
 // against 80.3 us for 128 ragged sequences.)
@@ -110,7 +114,12 @@ constexpr int kTcLenBuckets = 8;              // length buckets of the partly fi
 // K scales [32], V scales [32], log2 of the V scales [32].
 constexpr int kScaledEntry = 32 + 4 * 32 * 4;
 
-template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false, bool HALF = false>
+// 16-byte columns of P per token: a third part of eight heads' weights needs a second one.
+__host__ __device__ constexpr int tc_p_columns(int act, int cache, int G) {
+    return cache == kE4M3B && act == kF16 && G == 8 ? 2 : 1;
+}
+
+template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false, bool HALF = false, int PREG = 1>
 struct TcSmem {
     static constexpr int RING = 0;
     static constexpr int Q = NS * STG;
@@ -121,7 +130,7 @@ struct TcSmem {
     static constexpr int QBUF = STG == kTcStage8 || PAIR ? 4096 : kTcQBuf;  // one Q buffer
     static constexpr int QBUFS = STG == kTcStage8 ? 2 : 1;                  // Q buffers
     static constexpr int P = Q + QBUFS * QBUF;
-    static constexpr int PBUF = STG == kTcStage8 ? 8192 : PAIR ? 2 * kTcMaxTiles * 2048 : kTcPBuf;  // one P buffer
+    static constexpr int PBUF = STG == kTcStage8 ? 8192 * PREG : PAIR ? 2 * kTcMaxTiles * 2048 : kTcPBuf;  // one P buffer
     static constexpr int PBUFS = STG == kTcStage8 ? 2 : 1;           // P buffers
     // item numbers, q shifts, block-table entries [32] per entry; SCALED: kScaledEntry bytes per entry
     static constexpr int QUEUE = P + PBUFS * PBUF;
@@ -266,20 +275,25 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     constexpr int HD = PAIR || HALF ? 64 : kTcD;  // head_dim of the caches, queries and output
     static_assert(!PAIR || !FP8, "pairs of head_dim-64 kv heads: 16-bit caches");
     static_assert(!HALF || SCALED, "two tokens a row: block-scaled E4M3 caches");
-    using S = TcSmem<NS, STG, PAIR, SCALED, HALF>;
+    constexpr int PREG = tc_p_columns(ACT, CACHE, G);
+    constexpr bool P3 = SCALED && ACT == kF16;  // three parts of P
+    constexpr int PART = P3 && G <= 4 ? 4 : 8;  // columns from one part of P to the next
+    using S = TcSmem<NS, STG, PAIR, SCALED, HALF, PREG>;
     constexpr int THREADS = kTcThreads;
     constexpr int TPR = HALF ? 2 : 1;         // tokens per tile row
     constexpr int TILE = kTcTile * TPR;       // tokens per tile
     constexpr int BPT = TILE / BS;            // blocks per tile
-    constexpr int O_COL = kTcMaxTiles * kTcN;  // first O column of a buffer (HALF: 16 more for the odd tokens)
-    constexpr int SLOT_COLS = O_COL + TPR * kTcN;
+    constexpr int O_COL = kTcMaxTiles * kTcN;  // first O column of a buffer
+    constexpr int O_COLS = TPR * PREG * kTcN;
+    constexpr int SLOT_COLS = O_COL + O_COLS;
     static_assert(2 * SLOT_COLS <= kTcTmemCols, "tensor memory of two buffers");
     // E4M3 x E4M3 (kind::f8f6f4) has the same descriptor bits as binary16 x binary16
     constexpr uint32_t IDESC_S = tc::idesc_f16(128, kTcN, !FP8 && ACT == kBF16, false, false);
     // E4M3: P is the B operand in the MN-major layout without swizzle (a token's
     // 16 codes, 8 high and 8 low parts, are 16 contiguous bytes)
-    // (HALF: N = 32, the odd tokens' 16 codes 2 KB after the even ones')
-    constexpr uint32_t IDESC_O = tc::idesc_f16(128, kTcN * TPR, !FP8 && ACT == kBF16, true, FP8);
+    // (HALF: the odd tokens' codes 2 KB after the even ones', in columns of their
+    // own; a second 16-byte column of P 2 KB after the first)
+    constexpr uint32_t IDESC_O = tc::idesc_f16(128, O_COLS, !FP8 && ACT == kBF16, true, FP8);
     static_assert(!FP8 || G <= 8, "E4M3 cache: rows 0-7 of Q and P hold the high parts, rows 8-15 the low parts");
     constexpr bool Q3 = FP8 && ACT == kF16;  // binary16 queries: three E4M3 parts
     static_assert(G == 2 || G == 4 || G == 8 || (SCALED && G == 1), "query heads per kv head");
@@ -891,7 +905,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const bool ragged = valid % 32 != 0 || (HALF && (tokens & 1));
             auto issue = [&](int s, int t, int ksteps) {
                 const uint32_t a = v_lo + s * (STG / 16);
-                const uint32_t pb = p_lo + b * (S::PBUF / 16) + t * TPR * 128;
+                const uint32_t pb = p_lo + b * (S::PBUF / 16) + t * TPR * PREG * 128;
                 if (ksteps == 4) {
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
@@ -1230,6 +1244,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                             // P x 2^8 (at most 256) = hi + lo in E4M3; token `row` of
                             // tile t holds 16 bytes: hi of heads 0-7, then lo of heads 0-7
                             uint32_t w[4] = {0u, 0u, 0u, 0u};
+                            [[maybe_unused]] uint32_t w2[2] = {0u, 0u};
 #pragma unroll
                             for (int g = 0; g < G; g += 2) {
                                 // M is finite (every item has a token); 2^-inf = 0 for masked rows
@@ -1240,11 +1255,23 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                 if (G > 1) sum[g + SECOND] += p1;
                                 uint32_t hi, lo;
                                 const float pm = SCALED ? vs_t[t] : 256.f;  // vs_t: times 2^(8 - ev)
-                                split_e4m3x2(p0 * pm, p1 * pm, hi, lo);
-                                w[g >> 2] |= hi << (8 * (g & 3));
-                                w[2 + (g >> 2)] |= lo << (8 * (g & 3));
+                                if constexpr (P3) {
+                                    uint32_t low;
+                                    split3_e4m3x2(p0 * pm, p1 * pm, hi, lo, low);
+                                    constexpr int WORDS = PART / 4;
+                                    w[g >> 2] |= hi << (8 * (g & 3));
+                                    w[WORDS + (g >> 2)] |= lo << (8 * (g & 3));
+                                    if constexpr (PREG == 2) w2[g >> 2] |= low << (8 * (g & 3));
+                                    else w[2] |= low << (8 * g);
+                                } else {
+                                    split_e4m3x2(p0 * pm, p1 * pm, hi, lo);
+                                    w[g >> 2] |= hi << (8 * (g & 3));
+                                    w[2 + (g >> 2)] |= lo << (8 * (g & 3));
+                                }
                             }
-                            *reinterpret_cast<uint4*>(pb + t * 2048 + row * 16) = make_uint4(w[0], w[1], w[2], w[3]);
+                            unsigned char* pt = pb + t * PREG * 2048 + row * 16;
+                            *reinterpret_cast<uint4*>(pt) = make_uint4(w[0], w[1], w[2], w[3]);
+                            if constexpr (PREG == 2) *reinterpret_cast<uint4*>(pt + 2048) = make_uint4(w2[0], w2[1], 0u, 0u);
                         } else {
                             // 8-row regions of (tile, 64-token half), 1 KB apart; PAIR:
                             // 16-row regions, 2 KB apart, rows 8-15 for kv head 2v+1
@@ -1324,14 +1351,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             if (good) {
                 tc::fence_after_sync();
                 // HALF: lanes 64-127 hold the odd tokens' product
-                const uint32_t o_addr = lane_addr + b * SLOT_COLS + O_COL + (HALF ? (q4 >> 1) * kTcN : 0);
+                const uint32_t o_addr = lane_addr + b * SLOT_COLS + O_COL + (HALF ? (q4 >> 1) * (PREG * kTcN) : 0);
                 tc::TmemLd<G>::load(o_addr + hh * 8, o);
                 if constexpr (FP8) {
                     float lo[G];  // O of the low parts of P
-                    tc::TmemLd<G>::load(o_addr + 8, lo);
+                    [[maybe_unused]] float low[G];
+                    tc::TmemLd<G>::load(o_addr + PART, lo);
+                    if constexpr (P3) tc::TmemLd<G>::load(o_addr + 2 * PART, low);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int g = 0; g < G; ++g) o[g] += lo[g];
+                    for (int g = 0; g < G; ++g) o[g] += P3 ? lo[g] + low[g] : lo[g];
                 } else {
                     tc::tmem_wait_ld();
                 }

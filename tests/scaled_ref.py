@@ -103,9 +103,9 @@ def decode_scaled(q, kcodes, vcodes, ks, vs, tables, lens, scale, bs, out_dtype)
 
     bound is what the kernels' arithmetic may be off by, element by element:
       half a step of the output type, relative to the value;
-      2^-8 of sum_j p_j |v_j|: a weight enters the tensor-core product as two E4M3 parts (each leaves at most 2^-4
-      of what it rounds), the CUDA-core product as one binary16 value (2^-11);
-      2^-17 of the largest p_j |vs_j| for every code: what the second part cannot hold (its least step is 2^-9, half
+      2^-8 (bf16) or 2^-11 (fp16) of sum_j p_j |v_j|: a weight enters the tensor-core product as two or three E4M3
+      parts (each leaves at most 2^-4 of what it rounds), the CUDA-core product as a binary16 (2^-11) or float32 value;
+      2^-17 of the largest p_j |vs_j| for every code: what the last part cannot hold (its least step is 2^-9, half
       of it lost, where the largest weight is between 2^7 and 2^8);
       the scores: q enters as two (bf16) or three (fp16) E4M3 parts, 2^-12 of each element at most or 2^-17 of the
       largest, and 128 float32 additions, 2^-17 of sum |q||k|; a score off by d moves the weights by 2 d relative."""
@@ -137,6 +137,7 @@ def decode_scaled(q, kcodes, vcodes, ks, vs, tables, lens, scale, bs, out_dtype)
             move = min(1.0, 2.0 * ds[live].max())
             spread = p @ np.abs(v)
             wmax = (p * np.abs(vsc[kh])).max()
-            bound[b, h] = (torch.finfo(out_dtype).eps / 2 * np.abs(out[b, h]) + (2.0 ** -8 + move) * spread
+            parts = 2.0 ** -11 if out_dtype == torch.float16 else 2.0 ** -8
+            bound[b, h] = (torch.finfo(out_dtype).eps / 2 * np.abs(out[b, h]) + (parts + move) * spread
                            + 2.0 ** -17 * wmax * np.abs(vv[kh]).sum(0) + 2.0 ** -25)
     return out, bound
