@@ -324,7 +324,8 @@ int paged_block_swap(void* k_cache, void* v_cache, const int32_t* block_ids, int
  * glossary, section "Related techniques": an 8-bit cache) kmeta holds the
  * decoded codes without the per-tensor scale -- every E4M3 value is exact in
  * binary16 and bfloat16 -- so the bounds are the true bounds divided by
- * k_scale (> 0), which ranks the blocks identically.
+ * k_scale (> 0), which ranks the blocks identically.  (Not so with a scale for
+ * each block: these calls do not serve block-scaled caches.)
  * ---------------------------------------------------------------------- */
 
 /* Recompute kmeta (of meta_dtype: PKV_F16 or PKV_BF16; cache_dtype is
@@ -449,7 +450,7 @@ int paged_extend_tables(int32_t* block_tables, int max_blocks_per_seq, const int
  * Tokens of one block must be neighbours in the call, in slot order; two runs
  * of one block in one call race.  Negative slots are skipped, slots outside
  * the pool are skipped and flag PKV_DEV_BAD_SLOT.  head_dim: a multiple of 8,
- * at most 256; any block_size >= 1.
+ * at most 256; block_size from 1 to 2^20.
  */
 int paged_kv_append_scaled(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                            const int64_t* slot_mapping, int num_tokens, void* k_cache, void* v_cache,

@@ -149,7 +149,10 @@ _ws_cache: dict = {}
 
 
 def _workspace(device, stream_ptr: int, nbytes: int) -> torch.Tensor:
-    """A reusable workspace per (device, stream): calls on one stream are ordered."""
+    """A reusable workspace per (device, stream): calls on one stream are ordered.  A call that is being captured gets
+    one of its own, from the graph's memory: the reusable one may be replaced while the graph lives."""
+    if torch._C._cuda_isCurrentStreamCapturing():
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
     key = (device.index, stream_ptr)
     with _ws_lock:
         buf = _ws_cache.get(key)

@@ -354,7 +354,8 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     if ((path == PKV_PATH_TENSOR || path == PKV_PATH_TENSOR_2CTA) && !tc_ok)
         return fail(PKV_ERR_INVALID, F + ": " + "the tensor-core path needs head_dim 128 (16-bit or E4M3 "
                                      "cache) or 64 (16-bit cache, even kv heads, shared tables), 2/4/8 query "
-                                     "heads per kv head and partitions of at most 512 tokens");
+                                     "heads per kv head and partitions of at most 512 tokens (block-scaled "
+                                     "caches: either head_dim and any group, partitions of at most 512 tokens)");
     // Block-scaled: short contexts and few rows take the CUDA-core kernel, whose
     // one launch is over in 3 to 8 us where the tensor-core kernel's take 8 to 13
     // (head_dim 128, 128 tokens, us: 4.9 / 8.7 for 16 x 8 rows of one query head,
@@ -513,8 +514,9 @@ int paged_extend_tables(int32_t* block_tables, int max_blocks_per_seq, const int
 // Checks shared by the strided appends; returns PKV_OK or the status to return.
 static int append_checks(const std::string& F, const RopeAppendParams& p, int act_dtype) {
     if (p.num_tokens < 0 || p.num_kv_heads <= 0 || p.block_size <= 0 || p.num_blocks <= 0 || p.head_dim <= 0 ||
-        p.head_dim % 8 != 0 || p.head_dim > 256)
-        return fail(PKV_ERR_INVALID, F + "sizes must be positive and head_dim a multiple of 8 up to 256");
+        p.head_dim % 8 != 0 || p.head_dim > 256 || p.block_size > (1 << 20) || p.num_kv_heads > 65535)
+        return fail(PKV_ERR_INVALID, F + "sizes must be positive, head_dim a multiple of 8 up to 256, block_size at most "
+                                         "2^20 and num_kv_heads at most 65535");
     if (act_dtype != PKV_F16 && act_dtype != PKV_BF16)
         return fail(PKV_ERR_INVALID, F + "act_dtype must be PKV_F16 or PKV_BF16");
     if (p.k_stride % 8 != 0 || p.v_stride % 8 != 0 || p.k_stride < 0 || p.v_stride < 0)
@@ -592,8 +594,8 @@ int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_
     p.num_blocks = num_blocks;
     const int c = append_checks(F, p, act_dtype);
     if (c != PKV_OK) return c;
-    if (num_q_heads < 0 || num_q_heads > 65535 || num_kv_heads > 65535)
-        return fail(PKV_ERR_INVALID, F + "head counts must be in 0 .. 65535 (kv heads from 1)");
+    if (num_q_heads < 0 || num_q_heads > 65535)
+        return fail(PKV_ERR_INVALID, F + "num_q_heads must be in 0 .. 65535");
     if (rotary_dim <= 0 || rotary_dim % 2 != 0 || rotary_dim > head_dim)
         return fail(PKV_ERR_INVALID, F + "rotary_dim must be even, positive and at most head_dim");
     if (!std::isfinite(attention_factor)) return fail(PKV_ERR_INVALID, F + "attention_factor must be finite");
@@ -602,6 +604,8 @@ int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_
     if (num_q_heads > 0 && (q_stride % 8 != 0 || q_stride < 0 || q_out_stride % 8 != 0 ||
                             (num_tokens > 1 && q_out_stride < static_cast<int64_t>(num_q_heads) * head_dim)))
         return fail(PKV_ERR_INVALID, F + "q token strides must be multiples of 8 elements, and q_out's rows apart");
+    if (num_q_heads > 0 && q && q == q_out && num_tokens > 1 && q_stride != q_out_stride)
+        return fail(PKV_ERR_INVALID, F + "in place, q and q_out have one stride");
     const bool blocks = k_scales || v_scales;
     if (cache_dtype == PKV_E4M3 && blocks == (k_scale || v_scale))
         return fail(PKV_ERR_INVALID, F + "an E4M3 cache needs either k_scale and v_scale or k_scales and v_scales");

@@ -57,6 +57,11 @@ APPENDS = [
     ("f16", 1, 256, 64, [(0, 200), (63, 2), (10, 100)]),
     ("bf16", 40, 128, 16, [(i, 1) for i in range(70)]),
     ("f16", 1, 40, 1, [(0, 40), (3, 5)]),
+    # prompts: the kernel for runs of many tokens, whole blocks in registers or (64-token blocks) read twice
+    ("bf16", 2, 64, 16, [(i % 19, 37 + i) for i in range(40)]),
+    ("f16", 3, 128, 32, [(0, 1500), (7, 700), (31, 2), (33, 800)]),
+    ("f16", 1, 128, 64, [(0, 900), (70, 650)]),
+    ("bf16", 1, 80, 16, [(5, 1000), (0, 333)]),
 ]
 
 
@@ -108,6 +113,23 @@ def test_append_scaled_borders_and_odd_values(pkv):
     kc = _codes(g, nb, 1, bs, D)
     s = torch.exp2(torch.randint(-9, 3, (nb, 1), generator=g).float())
     _append(pkv, k, k.flip(0).contiguous(), slots, kc, kc.flip(0).contiguous(), s, s.clone())
+
+
+@pytest.mark.parametrize("act,bs", [("bf16", 16), ("f16", 32), ("bf16", 64)])
+def test_append_scaled_odd_values_in_prompts(pkv, act, bs):
+    """Infinities, NaN, zeros and tiny elements among the tokens of long runs."""
+    g = _gen((act, bs))
+    T, H, D = 1300, 2, 64
+    k = (torch.randn(T, H, D, generator=g) * torch.exp2(torch.randint(-20, 8, (T, 1, 1), generator=g).float())).to(DT[act])
+    at = torch.randint(0, T, (60,), generator=g)
+    k[at[:20], :, 5] = float("inf")
+    k[at[20:40], 0, 9] = float("nan")
+    k[at[40:50]] = 0.0
+    k[at[50:], 1] = -float("inf")
+    k[200:200 + 2 * bs] = 0.0
+    slots, nb = _requests([(3, T)], bs, g)
+    kc, s = _codes(g, nb, H, bs, D), torch.exp2(torch.randint(-8, -4, (nb, H), generator=g).float())
+    _append(pkv, k, k.flip(0).contiguous(), slots, kc, kc.clone(), s, s.clone())
 
 
 def test_append_scaled_token_by_token_equals_the_values(pkv):
@@ -430,3 +452,68 @@ def test_two_streams_with_a_workspace_each(pkv):
     torch.cuda.synchronize()
     for i, o in enumerate(got):
         assert torch.equal(o, want[i % 2])
+
+
+def test_captured_calls_keep_a_workspace_of_their_own(pkv):
+    """A captured call without a workspace, then eager calls that need a larger one on the same stream: the replay's
+    result stays, and so does that of a second graph captured on it."""
+    case = ("bf16", 32, 4, 128, 16, -1, "narrow")
+    small, large = (_decode_case(case, lens) for lens in ([700, 1025], [1500] * 12))
+    d, e = [t.cuda() for t in small], [t.cuda() for t in large]
+    run = lambda t, out=None: pkv.paged_attention_decode_scaled(*t[:7], 0.1, out=out)  # noqa: E731
+    want, out1, out2 = run(d), torch.empty_like(d[0]), torch.empty_like(d[0])
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        run(d)
+    torch.cuda.synchronize()
+    graphs = []
+    for out in (out1, out2):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1], stream=s):
+            run(d, out)
+    with torch.cuda.stream(s):
+        first = run(e)
+        junk = [torch.full((1 << 20,), 77, dtype=torch.uint8, device="cuda") for _ in range(8)]
+        graphs[0].replay()
+        second = run(e)
+        graphs[1].replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out1, want) and torch.equal(out2, want) and torch.equal(first, second)
+    assert all(bool((j == 77).all()) for j in junk)
+
+
+def test_empty_batches(pkv):
+    z = dict(device="cuda")
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, **z)
+    s = torch.zeros(4, 2, **z)
+    k = torch.zeros(0, 2, 64, dtype=torch.bfloat16, **z)
+    slots, pos = torch.zeros(0, dtype=torch.int64, **z), torch.zeros(0, dtype=torch.int32, **z)
+    pkv.paged_kv_append_scaled(k, k, slots, kc, kc.clone(), s, s.clone())
+    assert pkv.paged_rope_append(k, k, k, pos, slots, torch.ones(32, **z), kc, kc.clone(), k_scales=s,
+                                 v_scales=s.clone()).shape == k.shape
+    out = pkv.paged_attention_decode_scaled(k, kc, kc.clone(), s, s.clone(), torch.zeros(0, 3, dtype=torch.int32, **z),
+                                            pos, 0.1)
+    assert out.shape == k.shape
+    assert s.count_nonzero() == 0 and kc.count_nonzero() == 0
+
+
+def test_large_offsets_in_a_pool_past_2_31_elements(pkv):
+    """Blocks whose element offsets pass 32 bits: append and decode there equal those in a small pool."""
+    H, bs, D = 8, 16, 128
+    nb = (1 << 31) // (H * bs * D) + 9
+    g = _gen("large")
+    k = torch.randn(40, H, D, generator=g).to(torch.bfloat16).cuda()
+    q = torch.randn(1, 32, D, generator=g).to(torch.bfloat16).cuda()
+    got = []
+    for blocks, n in (([nb - 1, nb - 2, nb - 5], nb), ([2, 0, 1], 4)):
+        kc, vc = (torch.zeros(n, H, bs, D, dtype=torch.uint8, device="cuda") for _ in range(2))
+        ks, vs = (torch.zeros(n, H, device="cuda") for _ in range(2))
+        at = torch.arange(40)
+        slots = (torch.tensor(blocks)[at // bs] * bs + at % bs).cuda()
+        pkv.paged_kv_append_scaled(k, -k, slots, kc, vc, ks, vs)
+        tables = torch.tensor([blocks], dtype=torch.int32).cuda()
+        got.append((kc[blocks].cpu(), ks[blocks].cpu(), vc[blocks].cpu(), pkv.paged_attention_decode_scaled(
+            q, kc, vc, ks, vs, tables, torch.tensor([40], dtype=torch.int32).cuda(), 0.1).cpu()))
+        del kc, vc
+    assert all(torch.equal(a, b) for a, b in zip(*got))

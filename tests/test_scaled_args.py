@@ -36,6 +36,7 @@ def test_append_scaled_refusals(pkv_lib):
     lib = pkv_lib._native.lib()
     assert _append(lib, D=100) == 1 and _append(lib, D=264) == 1 and _append(lib, D=0) == 1
     assert _append(lib, act=2) == 1 and _append(lib, T=-1) == 1 and _append(lib, bs=0) == 1
+    assert _append(lib, bs=(1 << 20) + 1) == 1 and _append(lib, hkv=65536) == 1
     assert _append(lib, ks=1028) == 1 and _append(lib, vs=-8) == 1
     for name in ("k", "v", "slots", "kc", "vc", "ksc", "vsc"):
         assert _append(lib, **{name: None}) == 1, name
@@ -60,6 +61,7 @@ def test_rope_append_refusals(pkv_lib):
     assert _rope(lib, cache=2, k1=A) == 1 and _rope(lib, cache=2, kb=A) == 1
     assert _rope(lib, cache=2, k1=A, v1=A, kb=A, vb=A) == 1         # both kinds
     assert _rope(lib, qs=1020) == 1 and _rope(lib, qos=512) == 1    # rows of q_out overlap
+    assert _rope(lib, qs=2048) == 1                                 # in place with another stride
     assert _rope(lib, hq=-1) == 1 and _rope(lib, D=512, rot=128) == 1
     for name in ("q", "k", "v", "pos", "slots", "f", "qo", "kc", "vc"):
         assert _rope(lib, **{name: None}) == 1, name
