@@ -492,7 +492,8 @@ int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_
  * paged_attention_decode_scaled -- paged_attention_decode over a block-scaled
  * E4M3 cache: K_b[j] = code * k_scales[block][kvh], likewise V, block =
  * block_tables[b][j / block_size].  Scales may be any finite float32 (a power of
- * two or not, 0, negative); products and sums as paged_attention_decode.  A
+ * two or not, 0, negative; V scales of one sequence within a factor 2^100 of
+ * one another, else the smaller ones' part of the sum may be lost); products and sums as paged_attention_decode.  A
  * context length of 0 (a padding row) gives a row of zeros and no error bit.
  * The workspace is at least pkv_scaled_workspace_size(...) bytes; other
  * arguments as there.  PKV_PARTITION_AUTO gives partitions of at most 512

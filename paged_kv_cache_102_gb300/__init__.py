@@ -252,7 +252,9 @@ class DecodePlan:
     the step with a single C call and returns `out`.  Between runs the
     tensors' contents may change (new queries, tables, lengths), their
     storage, shapes and types may not.  Every run goes on the stream given
-    here (default: the current stream at construction)."""
+    here (default: the current stream at construction).  Plans that may run
+    at the same time need a workspace each (with k_scales and v_scales the
+    default one is the plan's own)."""
 
     def __init__(self, q, k_cache, v_cache, block_tables, context_lens, scale, out=None, k_scale=None, v_scale=None,
                  partition_size=PARTITION_AUTO, workspace=None, stream=None, k_new=None, v_new=None,
@@ -264,6 +266,12 @@ class DecodePlan:
             if any(given) or k_scale is not None or v_scale is not None:
                 raise ValueError("DecodePlan: k_scales and v_scales go with neither an append nor k_scale, v_scale")
             self.func = "paged_attention_decode_scaled"
+            if workspace is None:  # the plan's own, so that graphs of two plans may run at once
+                need = workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], block_tables.shape[1],
+                                      k_cache.shape[2], partition_size, True)
+                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=k_cache.device)
+                if isinstance(stream, torch.cuda.Stream) and not torch.cuda.is_current_stream_capturing():
+                    workspace.record_stream(stream)
             self._args, self.out, ws = _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables,
                                                            context_lens, scale, out, partition_size, workspace, stream)
         elif all(given):
@@ -519,8 +527,9 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
 
     The first 2 * len(inv_freq) channels turn, paired (i, i + half) or interleaved (2i, 2i + 1).  q, k, v may be
     parts of one projection's output (rows contiguous, token strides of their own).  The cache is of q's type, or
-    E4M3 with k_scale, v_scale (one each) or k_scales, v_scales (block-scaled).  A negative position marks a padding
-    row, a negative slot a token that is not stored.  q may be None (keys alone)."""
+    E4M3 with k_scale, v_scale (one each) or k_scales, v_scales (block-scaled: tokens of one block must be neighbours
+    in the call, in slot order).  A negative position marks a padding row, a negative slot a token that is not stored.
+    q may be None (keys alone)."""
     name = "paged_rope_append"
     kshape, cshape = k.shape, k_cache.shape
     device = k.device
@@ -550,6 +559,9 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
             positions, slot_mapping, inv_freq, k_scales, v_scales)
     else:
         sb1 = sb2 = None
+        for t in (k_scale, v_scale):
+            if t is not None and (t.dtype is not torch.float32 or t.numel() != 1):
+                raise ValueError(f"{name}: k_scale and v_scale must be float32 with one element")
         kc, vc, pos, slots, freq = _pointers(name, device, "k_cache v_cache positions slot_mapping inv_freq", k_cache,
                                              v_cache, positions, slot_mapping, inv_freq)
         s1, s2 = (None if t is None else next(_pointers(name, device, what, t))
@@ -653,9 +665,9 @@ def paged_block_copy(k_cache, v_cache, src_dst_pairs, stream=None, k_scales=None
     if k_scales is not None or v_scales is not None:
         _require_scales("paged_block_copy", k_cache, v_cache, k_scales, v_scales)
         _require_cuda(k_cache.device, k_scales=k_scales, v_scales=v_scales)
-        _native.call("paged_block_copy_scaled", _ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-                     _ptr(src_dst_pairs), src_dst_pairs.shape[0], k_cache.shape[0], k_cache.shape[1], block_bytes,
-                     _stream(stream, k_cache.device))
+        _call_on(k_cache.device, "paged_block_copy_scaled", _ptr(k_cache), _ptr(v_cache), _ptr(k_scales),
+                 _ptr(v_scales), _ptr(src_dst_pairs), src_dst_pairs.shape[0], k_cache.shape[0], k_cache.shape[1],
+                 block_bytes, _stream(stream, k_cache.device))
         return
     _native.call("paged_block_copy", _ptr(k_cache), _ptr(v_cache), _ptr(src_dst_pairs), src_dst_pairs.shape[0],
                  k_cache.shape[0], block_bytes, _stream(stream, k_cache.device))
@@ -688,9 +700,9 @@ def paged_block_swap(k_cache, v_cache, block_ids, staging, direction, stream=Non
     _native.call("paged_block_swap", _ptr(k_cache), _ptr(v_cache), _ptr(block_ids), block_ids.numel(),
                  k_cache.shape[0], block_bytes, _ptr(staging), int(direction), _stream(stream, k_cache.device))
     if k_scales is not None:
-        _native.call("paged_block_scales_swap", _ptr(k_scales), _ptr(v_scales), _ptr(block_ids), block_ids.numel(),
-                     k_cache.shape[0], k_cache.shape[1], _ptr(scale_staging), int(direction),
-                     _stream(stream, k_cache.device))
+        _call_on(k_cache.device, "paged_block_scales_swap", _ptr(k_scales), _ptr(v_scales), _ptr(block_ids),
+                 block_ids.numel(), k_cache.shape[0], k_cache.shape[1], _ptr(scale_staging), int(direction),
+                 _stream(stream, k_cache.device))
 
 
 def device_error(reset: bool = True, stream=None, device=None) -> int:

@@ -485,7 +485,6 @@ int paged_extend_tables(int32_t* block_tables, int max_blocks_per_seq, const int
     if (static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
         return fail(PKV_ERR_INVALID, F + "table too long");
     if (num_tokens > 0x7fffffff - 4) return fail(PKV_ERR_INVALID, F + "too many tokens");
-    if (num_seqs == 0 && num_tokens == 0) return PKV_OK;
     if (!free_head || !seq_starts || !block_starts || !free_head_out)
         return fail(PKV_ERR_INVALID, F + "null pointer");
     if (num_seqs > 0 && (!block_tables || !context_lens || !new_lens || !context_lens_out))

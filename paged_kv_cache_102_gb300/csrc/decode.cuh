@@ -302,15 +302,24 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                 ks = __shfl_sync(0xffffffffu, ksc, bi & 31);
                 vf = __shfl_sync(0xffffffffu, vsc, bi & 31);
                 // exponent of the V scale; 0 (and subnormal scales) leave the reference alone
-                const int ev = static_cast<int>((__float_as_uint(vf) >> 23) & 0xffu) - 127;
+                const int ev = min(126, static_cast<int>((__float_as_uint(vf) >> 23) & 0xffu) - 127);
                 if (ev > -127 && tok0 + warp * C::TW < tok_end && (ev > mv + 7 || ev < mv - 7)) {
-                    const int to = mv == kNoRef ? ev : max(ev, mv - 80);  // acc stays finite
+                    int to = ev;
                     if (mv != kNoRef) {
-                        const float a = pow2_clamped(mv - to);
+                        // down no further than acc stays below 2^100
+                        float top = 0.f;
 #pragma unroll
                         for (int g = 0; g < G; ++g)
 #pragma unroll
-                            for (int v = 0; v < C::VEC; ++v) acc[g][v] *= a;
+                            for (int v = 0; v < C::VEC; ++v) top = fmaxf(top, fabsf(acc[g][v]));
+                        const int room = 100 - (static_cast<int>(__float_as_uint(warp_max(top)) >> 23) - 127);
+                        to = max(ev, mv - min(126, max(0, room)));
+                        // (up by more than 126: in two factors)
+                        const float a = pow2_clamped(mv - to), b = mv - to < -126 ? pow2_clamped(mv - to + 126) : 1.f;
+#pragma unroll
+                        for (int g = 0; g < G; ++g)
+#pragma unroll
+                            for (int v = 0; v < C::VEC; ++v) acc[g][v] = acc[g][v] * a * b;
                     }
                     mv = to;
                 }

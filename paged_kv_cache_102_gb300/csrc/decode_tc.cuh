@@ -737,6 +737,21 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(act_to_float<ACT>(e[j])));
                     }
                     m = warp_max(m);
+                    if (m == INFINITY) {
+                        // an infinite query: NaN, as its head's result is, and a scale for the other heads
+                        m = 0.f;
+#pragma unroll
+                        for (int n = 0; n < QN; ++n) {
+                            uint16_t* e = reinterpret_cast<uint16_t*>(qu[n]);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                const float a = fabsf(act_to_float<ACT>(e[j]));
+                                if (a == INFINITY) e[j] = 0x7fffu;
+                                else m = fmaxf(m, a);
+                            }
+                        }
+                        m = warp_max(m);
+                    }
                     const int e = static_cast<int>(__float_as_uint(m) >> 23) - 127;
                     shift = m > 0.f ? min(120, max(-120, e - 7)) : 0;
                     if (lane == 0) q_shift[k & 3] = shift;

@@ -86,6 +86,8 @@ def test_extend_without_tokens_or_requests(pkv):
     assert r.block_starts.tolist() == [0] * 4
     _, r = _run(pkv, np.zeros((0, 4), np.int32), [], [], [1], 0, 16, 8, 5)
     assert r.slot_mapping.tolist() == [-1] * 5 and r.seq_starts.tolist() == [0]
+    _, r = _run(pkv, np.zeros((0, 4), np.int32), [], [], [1, 2, 3], 2, 16, 8, 0)  # nothing at all: the head stays
+    assert r.free_head.tolist() == [2] and r.seq_starts.tolist() == [0] and r.block_starts.tolist() == [0]
 
 
 @pytest.mark.parametrize("rows", [40, 9000])  # one launch, two launches

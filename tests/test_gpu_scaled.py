@@ -483,6 +483,70 @@ def test_captured_calls_keep_a_workspace_of_their_own(pkv):
     assert all(bool((j == 77).all()) for j in junk)
 
 
+def test_graphs_of_two_plans_at_once(pkv):
+    """Two plans made on one stream, their graphs replayed on two: neither reads the other's partial results."""
+    case = ("bf16", 32, 4, 128, 16, -1, "wide")
+    s = torch.cuda.Stream()
+    data, graphs, plans = [], [], []
+    for kind in ("wide", "narrow"):
+        d = [t.cuda() for t in _decode_case(case[:6] + (kind,), LENS)]
+        torch.cuda.synchronize()
+        plan = pkv.DecodePlan(d[0], d[1], d[2], d[5], d[6], 0.1, k_scales=d[3], v_scales=d[4], stream=s)
+        plan.run()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            plan.run()
+        data.append(d), graphs.append(graph), plans.append(plan)
+    want = [pkv.paged_attention_decode_scaled(*d[:7], 0.1) for d in data]
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    for _ in range(20):
+        for stream, graph in zip(streams, graphs):
+            with torch.cuda.stream(stream):
+                graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(p.out, w) for p, w in zip(plans, want))
+
+
+@pytest.mark.parametrize("case", [("bf16", 16, 2, 128, 16, -1, "narrow"), ("f16", 8, 2, 128, 16, -1, "narrow"),
+                                  ("bf16", 8, 1, 64, 16, -1, "narrow"), ("bf16", 4, 2, 128, 16, -1, "narrow")],
+                         ids=lambda c: "-".join(map(str, c)))
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf"), float("nan")])
+def test_decode_scaled_infinite_query(pkv, case, bad):
+    """A head whose query holds an infinity or a NaN comes out NaN; the heads of its group are not touched."""
+    lens = [256, 41, 200] if case[1] == 4 else [700, 41, 200]  # (at most 256: the CUDA-core kernel)
+    host = _decode_case(case, lens)
+    q, kc, vc, ks, vs, tables, L = (t.cuda() for t in host[:5] + (host[5][:, :-1].contiguous(), host[6]))
+    run = lambda q: pkv.paged_attention_decode_scaled(q, kc, vc, ks, vs, tables, L, 0.1)  # noqa: E731
+    want = run(q)
+    q[0, 1, 3] = bad
+    got = run(q)
+    assert bool(torch.isnan(got[0, 1]).all())
+    got[0, 1] = want[0, 1]
+    if case[1] != 4:
+        assert torch.equal(got, want)
+    else:  # binary32 instead of binary16 products for this group: not the same bits
+        exact, bound = ref.decode_scaled(*map(ref.f64, host[:1]), *(t.numpy() for t in host[1:6]), lens, 0.1, case[4],
+                                         q.dtype)
+        assert (np.abs(ref.f64(got) - exact) <= bound).all()
+
+
+def test_decode_scaled_v_scales_far_apart(pkv):
+    """V scales that fall by more than 2^118 over the blocks, and that rise by as much: the largest dominate."""
+    for hq, hkv in ((2, 2), (16, 2)):
+        for falling in (True, False):
+            case = ("bf16", hq, hkv, 128, 16, -1, "narrow")
+            q, kc, vc, ks, vs, tables, L = _decode_case(case, [96])
+            steps = torch.exp2(torch.tensor([60., 60., -20., -20., -64., -64.]))
+            vs[tables[0, :6].long()] = (steps if falling else steps.flip(0))[:, None].expand(6, hkv).contiguous()
+            host = (q, kc, vc, ks, vs, tables, L)
+            out = pkv.paged_attention_decode_scaled(*(t.cuda() for t in host), 128 ** -0.5)
+            want, bound = ref.decode_scaled(ref.f64(q), kc.numpy(), vc.numpy(), ks.numpy(), vs.numpy(), tables.numpy(),
+                                            [96], 128 ** -0.5, 16, q.dtype)
+            assert (np.abs(ref.f64(out) - want) <= bound).all()
+
+
 def test_empty_batches(pkv):
     z = dict(device="cuda")
     kc = torch.zeros(4, 2, 16, 64, dtype=torch.uint8, **z)

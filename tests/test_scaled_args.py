@@ -22,7 +22,6 @@ def test_extend_refusals(pkv_lib):
     assert _extend(lib, slots=A + 8) == 1 and _extend(lib, pos=A + 4) == 1 and _extend(lib, ctx=A + 2) == 1
     assert _extend(lib, bst=A) == 1                 # seq_starts and block_starts are one buffer
     assert _extend(lib, lens=A) == 1                # lengths over new_lens (new is A too)
-    assert _extend(lib, B=0, T=0) == 0
 
 
 def _append(lib, **kw):
