@@ -24,6 +24,7 @@ each block and kv head (k_scales, v_scales [num_blocks, num_kv_heads]).
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import threading
 from typing import NamedTuple
@@ -619,6 +620,11 @@ def paged_attention_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _scaled_workspace_size(*sizes):  # a function of the sizes alone
+    return workspace_size(*sizes, True)
+
+
 def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
                         partition_size, workspace, stream):
     """Validated C arguments of paged_attention_decode_scaled, the output and the workspace."""
@@ -643,7 +649,7 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
     _require_out(device, out)
     s = _stream(stream, device)
     if workspace is None:
-        need = workspace_size(B, Hq, Hkv, D, tshape[1], bs, partition_size, True)
+        need = _scaled_workspace_size(B, Hq, Hkv, D, tshape[1], bs, partition_size)
         workspace = _workspace(device, s, max(need, 1))  # (0: an argument that the library refuses)
     qp, kc, vc, s1, s2, tables, lens, ws = _pointers(
         name, device, "q k_cache v_cache k_scales v_scales block_tables context_lens workspace", q, k_cache, v_cache,
