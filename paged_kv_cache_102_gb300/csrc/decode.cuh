@@ -34,6 +34,9 @@
 // when a block's scale is more than 2^7 away from it, so that p * vs / 2^mv
 // stays within binary16 whatever the scales are; binary16 activations, whose
 // result would show a weight's rounding to binary16, keep weights in binary32.
+// It serves what is over in one launch (4 x 8 rows of up to 64 tokens 3.8 us,
+// bound by that launch and four dependent round trips to memory) and the shapes
+// that the tensor-core kernel does not take.
 #pragma once
 
 #include <type_traits>

@@ -84,6 +84,12 @@
 // The producer that converts q finds its power-of-2 scale too.  (Two groups of
 // softmax warps with four heads each were no faster at eight query heads: 81.3
 // against 80.3 us for 128 ragged sequences.)
+// Measured, of the 6.7 TB/s that a copy reaches: 64 sequences of 40 heads of
+// their own, 1.43 GB of codes, 210 us (101 %, the memory is the bound); 8 of 32K
+// tokens, four query heads, 87 us (92 %, the merge is the rest); 128 ragged ones,
+// eight query heads, 80 us (81 %) and at head_dim 64, binary16, 43 us (58 %): the
+// launch's ramp, its tail and the merge, about 14 us, and at head_dim 64 an
+// item's 64 KB, which pass faster than the softmax warps' 3 us for it.
 // Every barrier wait is bounded (kWaitLimitNs); on a timeout the CTA stops
 // issuing work, drains its in-flight copies and MMAs, frees tensor memory and
 // reports kErrTimeout.
