@@ -496,9 +496,9 @@ int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_
  * one another, else the smaller ones' part of the sum may be lost); products and sums as paged_attention_decode.  A
  * context length of 0 (a padding row) gives a row of zeros and no error bit.
  * The workspace is at least pkv_scaled_workspace_size(...) bytes; other
- * arguments as there.  PKV_PARTITION_AUTO gives partitions of at most 512
- * tokens, which the tensor-core kernel serves for every group and both
- * head_dims; pkv_set_kernel_path's two tensor-core choices are one here.
+ * arguments as there.  The tensor-core kernel serves every group, both head_dims
+ * and partitions of up to 2^20 tokens (PKV_PARTITION_AUTO: at most 2048);
+ * pkv_set_kernel_path's two tensor-core choices are one here.
  */
 int paged_attention_decode_scaled(const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
                                   const float* v_scales, const int32_t* block_tables, int max_blocks_per_seq,

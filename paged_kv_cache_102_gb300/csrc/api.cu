@@ -45,6 +45,7 @@ size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
 constexpr int kStageTokens = 32;  // tokens per shared-memory stage of the decode kernel
 constexpr int kAutoPartition = 1024;
 constexpr int kAutoPartitionGrouped = 512;
+constexpr int kScaledLongItems = 2048;
 // Grouped shapes with a few hundred (sequence, kv head, partition) items get
 // 256-token partitions, so that the persistent grid's CTAs each get several
 // to balance.  Below 256 items every CTA has at most about one, and smaller
@@ -160,14 +161,19 @@ int pkv_scaled_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, i
     if (max_blocks_per_seq < 1 || block_size < 1 || num_kv_heads < 1 || num_q_heads < 1) return -1;
     const long long max_ctx = static_cast<long long>(max_blocks_per_seq) * block_size;
     const long long single = (max_ctx + kStageTokens - 1) / kStageTokens * kStageTokens;
-    // The tensor-core kernel's 512 tokens whatever the group; 256 for so few
-    // items that twice as many still get an SM each.  Measured, 512 / 256 tokens,
+    // The tensor-core kernel's segment of 512 tokens whatever the group; 256 for so
+    // few items that twice as many still get an SM each.  Measured, 512 / 256 tokens,
     // head_dim 128, one and eight query heads: 32 items 9.9 / 8.6 and 10.8 / 9.5
     // us, 128 items 10.4 / 10.6 and 11.8 / 11.8, 256 items 12.4 / 14.6 and
-    // 13.1 / 18.2, 512 items 16.1 / 16.6 and 17.9 / 20.7.
+    // 13.1 / 18.2, 512 items 16.1 / 16.6 and 17.9 / 20.7.  Four segments when there
+    // are items enough for every SM all the same; 512 / 2048 tokens, eight query
+    // heads, sequences of equal and of ragged lengths: 1024 items 25.8 / 24.8 and
+    // 18.0 / 22.4 us, 2048 items 42.1 / 41.4 and 29.9 / 26.0, 4096 items 76.2 / 78.7
+    // and 46.7 / 42.8, 4096 items of at most 2048 tokens, ragged, 52.7 / 43.2.
     long long P = kAutoPartitionGrouped;
     const long long items = static_cast<long long>(num_seqs) * num_kv_heads * ((max_ctx + P - 1) / P);
     if (items <= 64 && (P / 2) % block_size == 0) P /= 2;
+    else if (items >= kScaledLongItems) P *= 4;
     if (P >= single) P = single;
     return static_cast<int>(P);
 }
@@ -355,7 +361,7 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         return fail(PKV_ERR_INVALID, F + ": " + "the tensor-core path needs head_dim 128 (16-bit or E4M3 "
                                      "cache) or 64 (16-bit cache, even kv heads, shared tables), 2/4/8 query "
                                      "heads per kv head and partitions of at most 512 tokens (block-scaled "
-                                     "caches: either head_dim and any group, partitions of at most 512 tokens)");
+                                     "caches: either head_dim, any group and partitions of at most 2^20 tokens)");
     // Block-scaled: short contexts and few rows take the CUDA-core kernel, whose
     // one launch is over in 3 to 8 us where the tensor-core kernel's take 8 to 13
     // (head_dim 128, 128 tokens, us: 4.9 / 8.7 for 16 x 8 rows of one query head,

@@ -16,7 +16,7 @@ bool decode_tc_supported(int head_dim, int block_size, int group, int act, int c
     return dims && (block_size == 16 || block_size == 32) &&
            (group == 2 || group == 4 || group == 8 || (group == 1 && cache == kE4M3B)) &&
            (act == kF16 || act == kBF16) && (cache == act || is_e4m3(cache)) &&
-           partition_size <= kTcMaxTiles * kTcTile && encode_fn() != nullptr;
+           partition_size <= (cache == kE4M3B ? kTcMaxSegments : 1) * kTcMaxTiles * kTcTile && encode_fn() != nullptr;
 }
 
 cudaError_t launch_decode_tc(const DecodeParams& p, int act, int cache, int head_dim, int BS, int G, int variant,

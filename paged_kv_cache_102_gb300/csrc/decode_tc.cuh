@@ -81,15 +81,21 @@
 // result covers but not that of a binary16 one, so binary16 activations take a
 // third part: up to four heads fill 12 of the 16 columns, eight heads use 24 of
 // 32 (a second 16-byte column of P, with a ring of one stage less).
+// An item may be longer than the 512 tokens whose scores tensor memory holds: the
+// scheduler passes it on as segments of 512, which the other roles take for items;
+// the softmax keeps each head's running maximum and sum, the epilogue the output
+// so far (in spare tensor-memory columns) and joins them, and only the last segment
+// writes.  Long items leave fewer partial results to write and merge: 2048 tokens
+// instead of 512, 128 ragged sequences 80.0 -> 75.3 us, 64 of 40 heads 211 -> 205.
 // The producer that converts q finds its power-of-2 scale too.  (Two groups of
 // softmax warps with four heads each were no faster at eight query heads: 81.3
 // against 80.3 us for 128 ragged sequences.)
 // Measured, of the 6.7 TB/s that a copy reaches: 64 sequences of 40 heads of
-// their own, 1.43 GB of codes, 210 us (101 %, the memory is the bound); 8 of 32K
-// tokens, four query heads, 87 us (92 %, the merge is the rest); 128 ragged ones,
-// eight query heads, 80 us (81 %) and at head_dim 64, binary16, 43 us (58 %): the
-// launch's ramp, its tail and the merge, about 14 us, and at head_dim 64 an
-// item's 64 KB, which pass faster than the softmax warps' 3 us for it.
+// their own, 1.43 GB of codes, 205 us (104 %, the memory is the bound); 8 of 32K
+// tokens, four query heads, 87 us (92 %); 128 ragged ones, eight query heads, 75 us
+// (86 %) and at head_dim 64, binary16, 43 us (58 %): the launch's ramp, its tail
+// and the merge, and at head_dim 64 a segment's 64 KB, which pass faster than the
+// softmax warps' 3 us for it.
 // Every barrier wait is bounded (kWaitLimitNs); on a timeout the CTA stops
 // issuing work, drains its in-flight copies and MMAs, frees tensor memory and
 // reports kErrTimeout.
@@ -103,6 +109,7 @@ namespace pkv {
 constexpr int kTcThreads = 256;
 constexpr int kTcTile = 128;                  // tokens per tile (MMA M of S = K Q^T)
 constexpr int kTcMaxTiles = 4;                // partitions of at most 512 tokens
+constexpr int kTcMaxSegments = 2048;          // segments of an item (32-bit arithmetic of the length buckets)
 constexpr int kTcD = 128;                     // head_dim served by this kernel
 constexpr int kTcN = 16;                      // MMA N: query heads padded to 16
 constexpr int kTcHalf = kTcTile * 128;        // one 64-column half of a tile: 128 rows x 128 B
@@ -146,9 +153,10 @@ struct TcSmem {
     // item_full[kTcQueue], item_empty[kTcQueue] (a single Q or P buffer uses entry 0 of its pair)
     static constexpr int NBARS = 2 * NS + 13 + 2 * kTcQueue;
     static constexpr int RED = BARS + NBARS * 8;
-    // red_max[4][8], red_sum[4][8], stats[2][2][2][8]; SCALED: o_scale[2][8], q shifts [4] (and 4 unused);
-    // HALF: the odd tokens' half of O, [8][64]
-    static constexpr int RED_FLOATS = 64 + 64 + (SCALED ? 24 : 0) + (HALF ? 512 : 0);
+    // red_max[4][8], red_sum[4][8], stats[2][2][2][8]; SCALED: o_scale[2][8], o_keep[2][8], q shifts [4] (and 4
+    // unused), (max, sum) [8] so far; HALF: the odd tokens' half of O, [8][64], and where O fills tensor memory the
+    // output so far, [8][64]
+    static constexpr int RED_FLOATS = 64 + 64 + (SCALED ? 56 : 0) + (HALF ? 512 * PREG : 0);
     static constexpr int MISC = RED + RED_FLOATS * 4;
     // per row: length (int), item prefix (int, rows + 2 entries), length order (uint16)
     static constexpr int ROWS = (MISC + 16 + 15) / 16 * 16;
@@ -156,11 +164,14 @@ struct TcSmem {
     __host__ __device__ static constexpr int alloc(int rows) { return bytes(rows) + 1024; }  // room to align the base
 };
 
+// Block-scaled items: the row's only partition, the first and the last of its segments.
+enum : int { kItemSingle = 1, kItemFirst = 2, kItemLast = 4 };
+
 struct TcItem {
     int seq, kvh, row, part, tok_begin, n_tok, n_tiles;
     int qshift;  // E4M3 cache: q enters the MMA scaled by 2^-qshift
     int ev;      // block-scaled: 2^ev was taken out of the V scales
-    bool single; // the row's only partition (block-scaled; the others look it up)
+    int flags;   // block-scaled: kItemSingle, ...
 };
 
 // Rows: a sequence (tables shared by its kv heads) or, with per-(sequence,
@@ -334,9 +345,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     float* red_sum = red_max + 32;
     float* stats = red_max + 64;  // [buffer][kv head of a pair][max, sum][8]
     [[maybe_unused]] float* o_scale = stats + 64;  // block-scaled: [buffer][8], what an O column is multiplied by
+    [[maybe_unused]] float* o_keep = o_scale + 16;  // and the output of the segments before
     // block-scaled: q shift of the k-th item at [k & 3] (k + 4's is found after the softmax of k + 2 has begun)
-    [[maybe_unused]] volatile int* q_shift = reinterpret_cast<volatile int*>(o_scale + 16);
-    [[maybe_unused]] float* o_odd = o_scale + 24;  // HALF: [head][dimension] of the odd tokens
+    [[maybe_unused]] volatile int* q_shift = reinterpret_cast<volatile int*>(o_scale + 32);
+    [[maybe_unused]] float2* ml_run = reinterpret_cast<float2*>(o_scale + 40);  // [head] (max, sum) of them
+    [[maybe_unused]] float* o_odd = o_scale + 56;      // HALF: [head][dimension] of the odd tokens
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(sm + S::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 4);
 
@@ -521,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         it.n_tok = b.x;
         it.n_tiles = b.y;
         it.ev = b.z;
-        it.single = b.w != 0;
+        it.flags = b.w;
         return a.x >= 0;
     };
 
@@ -565,19 +578,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         // at the end of the work (the end marker is queued) or on an abort.
         auto claim = [&](TcItem& it, int& phys) {
             phys = -1;
-            [[maybe_unused]] float ksc = 0.f, vsc = 0.f, lvs = -INFINITY;
             int ci = -1;
             if (lane == 0) {
-                // block-scaled without a counter: no more items than blocks, one each
-                if (SCALED && p.work_counter == nullptr) ci = nclaim == 0 ? static_cast<int>(blockIdx.x) : total;
-                else ci = atomicAdd(p.work_counter, 1);
+                ci = atomicAdd(p.work_counter, 1);
                 if (ci >= total) ci = -1;
             }
             ci = __shfl_sync(0xffffffffu, ci, 0);
             it.qshift = 0;
             if (ci >= 0) {
                 tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
-                if constexpr (FP8 && !SCALED) {
+                if constexpr (FP8) {
                     // q enters the MMA as E4M3 high and low parts of q x 2^-qshift:
                     // the exact power-of-2 scale puts its largest magnitude in
                     // [128, 256), below the E4M3 maximum of 448
@@ -596,20 +606,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     it.qshift = m > 0.f ? min(120, max(-120, e - 7)) : 0;
                 }
                 phys = table_entry(it);
-                if constexpr (SCALED) {
-                    if (phys >= 0) {
-                        ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
-                        vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
-                    }
-                    const float top = warp_max(fabsf(vsc));
-                    const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xff) - 126;  // top < 2^e
-                    it.ev = top > 0.f ? min(126, max(-120, e)) : 0;
-                    vsc *= __uint_as_float(static_cast<uint32_t>(127 - it.ev) << 23);
-                    lvs = fmaxf(__log2f(fabsf(vsc)), -100.f);
-                    vsc *= 256.f;
-                    it.single = p.max_parts == 1 || s_lens[it.row] <= p.partition_size;
-                }
-                if (!SCALED && p.new_slots != nullptr && it.tok_begin + it.n_tok == s_lens[it.row]) {
+                if (p.new_slots != nullptr && it.tok_begin + it.n_tok == s_lens[it.row]) {
                     // fused append: this item holds the new (last) token; write it
                     // before the item is published, so before any copy of its block
 #pragma unroll
@@ -629,33 +626,87 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 ok = false;
                 return false;
             }
-            if constexpr (SCALED) {
-                unsigned char* e = entry_of(slot);
-                reinterpret_cast<int*>(e + 32)[lane] = phys;
-                reinterpret_cast<float*>(e + 160)[lane] = ksc;
-                reinterpret_cast<float*>(e + 288)[lane] = vsc;
-                reinterpret_cast<float*>(e + 416)[lane] = lvs;
-                if (lane == 0) {
-                    reinterpret_cast<int4*>(e)[0] = make_int4(ci, it.seq, it.kvh, it.part);
-                    reinterpret_cast<int4*>(e)[1] = make_int4(it.n_tok, it.n_tiles, it.ev, it.single ? 1 : 0);
-                }
-            } else {
-                item_phys[slot * 32 + lane] = phys;
-                if (lane == 0) {
-                    item_q[slot] = ci;
-                    item_shift[slot] = it.qshift;
-                }
+            item_phys[slot * 32 + lane] = phys;
+            if (lane == 0) {
+                item_q[slot] = ci;
+                item_shift[slot] = it.qshift;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_full[slot]);
             ++nclaim;
             return ci >= 0;
         };
-        TcItem it;
+        TcItem it{};
         int phys = -1;
-        // the counter was zeroed by the kernel before, which this launch did not wait for
-        if (SCALED && p.work_counter != nullptr) asm volatile("griddepcontrol.wait;" ::: "memory");
-        while (ok && claim(it, phys)) {
+        if constexpr (SCALED) {
+            // (A claim on its way while the item before is passed on was slower: 76.8
+            // against 75.3 us for 128 ragged sequences, with more work held at the end.)
+            // Without a counter: no more items than blocks, one each.
+            const bool counted = p.work_counter != nullptr;
+            int next = blockIdx.x;
+            if (counted) {
+                // the counter was zeroed by the kernel before, which this launch did not wait for
+                asm volatile("griddepcontrol.wait;" ::: "memory");
+                if (lane == 0) next = atomicAdd(p.work_counter, 1);
+            }
+            while (true) {
+                int ci = __shfl_sync(0xffffffffu, next, 0);
+                if (ci >= total) ci = -1;
+                next = total;
+                int left = 1;
+                if (ci >= 0) {
+                    tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
+                    left = it.n_tok;
+                    it.flags = kItemFirst | (p.max_parts == 1 || s_lens[it.row] <= p.partition_size ? kItemSingle : 0);
+                }
+                while (left > 0) {  // its segments; the end of the work: one without tokens
+                    float ksc = 0.f, vsc = 0.f, lvs = -INFINITY;
+                    phys = -1;
+                    if (ci >= 0) {
+                        it.n_tok = min(left, kTcMaxTiles * kTcTile);
+                        it.n_tiles = (it.n_tok + TILE - 1) / TILE;
+                        phys = table_entry(it);
+                        if (phys >= 0) {
+                            ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
+                            vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
+                        }
+                        const float top = warp_max(fabsf(vsc));
+                        const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xff) - 126;  // top < 2^e
+                        it.ev = top > 0.f ? min(126, max(-120, e)) : 0;
+                        vsc *= __uint_as_float(static_cast<uint32_t>(127 - it.ev) << 23);
+                        lvs = fmaxf(__log2f(fabsf(vsc)), -100.f);
+                        vsc *= 256.f;
+                        if (left == it.n_tok) it.flags |= kItemLast;
+                    }
+                    const int slot = nclaim % kTcQueue;
+                    bool good = true;
+                    if (lane == 0 && nclaim >= kTcQueue)
+                        good = tc_wait(&item_empty[slot], ((nclaim / kTcQueue) - 1) & 1, abort_flag, p.err);
+                    ok = __shfl_sync(0xffffffffu, good, 0);
+                    if (!ok) break;
+                    unsigned char* e = entry_of(slot);
+                    reinterpret_cast<int*>(e + 32)[lane] = phys;
+                    reinterpret_cast<float*>(e + 160)[lane] = ksc;
+                    reinterpret_cast<float*>(e + 288)[lane] = vsc;
+                    reinterpret_cast<float*>(e + 416)[lane] = lvs;
+                    if (lane == 0) {
+                        reinterpret_cast<int4*>(e)[0] = make_int4(ci, it.seq, it.kvh, it.part);
+                        reinterpret_cast<int4*>(e)[1] = make_int4(it.n_tok, it.n_tiles, it.ev, it.flags);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&item_full[slot]);
+                    ++nclaim;
+                    if (ci < 0) break;
+                    left -= it.n_tok;
+                    it.tok_begin += it.n_tok;
+                    it.flags &= ~kItemFirst;
+                }
+                if (!ok || ci < 0) break;
+                if (counted && lane == 0) next = atomicAdd(p.work_counter, 1);
+            }
+        } else {
+            while (ok && claim(it, phys)) {
+            }
         }
     } else if (warp >= 6) {
         // ------------------------------------------------------ tile producers
@@ -733,28 +784,26 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 if (!good) return false;
                 unsigned char* qbuf_k = qbuf + qb * S::QBUF;
                 int shift = it.qshift;
+                [[maybe_unused]] bool infinite = false;
+                [[maybe_unused]] const uint16_t* qg = static_cast<const uint16_t*>(p.q) +
+                                                      (static_cast<int64_t>(it.seq) * p.num_q_heads + it.kvh * G) * HD;
                 if constexpr (SCALED) {
                     // largest magnitude in [128, 256) after the exact power-of-2 scale (see the scheduler)
-                    float m = 0.f;
+                    uint32_t tops = 0;
 #pragma unroll
                     for (int n = 0; n < QN; ++n) {
-                        const uint16_t* e = reinterpret_cast<const uint16_t*>(qu[n]);
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) m = fmaxf(m, fabsf(act_to_float<ACT>(e[j])));
+                        top_pairs<ACT>(qu[n][0], tops);
+                        top_pairs<ACT>(qu[n][1], tops);
                     }
-                    m = warp_max(m);
-                    if (m == INFINITY) {
-                        // an infinite query: NaN, as its head's result is, and a scale for the other heads
+                    float m = warp_max(fmaxf(act_to_float<ACT>(static_cast<uint16_t>(tops)),
+                                             act_to_float<ACT>(static_cast<uint16_t>(tops >> 16))));
+                    infinite = m == INFINITY;
+                    if (__builtin_expect(infinite, 0)) {  // the largest finite one
                         m = 0.f;
-#pragma unroll
-                        for (int n = 0; n < QN; ++n) {
-                            uint16_t* e = reinterpret_cast<uint16_t*>(qu[n]);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                const float a = fabsf(act_to_float<ACT>(e[j]));
-                                if (a == INFINITY) e[j] = 0x7fffu;
-                                else m = fmaxf(m, a);
-                            }
+#pragma unroll 1
+                        for (int i = lane; i < G * HD; i += 32) {
+                            const float a = fabsf(act_to_float<ACT>(qg[i]));
+                            if (a < INFINITY) m = fmaxf(m, a);
                         }
                         m = warp_max(m);
                     }
@@ -791,6 +840,13 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     *reinterpret_cast<uint4*>(qbuf_k + 1024 + off) = make_uint4(mw[0], mw[1], mw[2], mw[3]);
                     if constexpr (Q3)
                         *reinterpret_cast<uint4*>(qbuf_k + 2048 + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                }
+                if (SCALED && __builtin_expect(infinite, 0)) {  // an infinite element: a NaN, as its head's result is
+                    __syncwarp();
+#pragma unroll 1
+                    for (int i = lane; i < G * HD; i += 32)
+                        if (fabsf(act_to_float<ACT>(qg[i])) == INFINITY)
+                            qbuf_k[i / HD * 128 + ((i % HD / 16) ^ (i / HD)) * 16 + i % 16] = 0x7f;
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -1340,14 +1396,28 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 if constexpr (SCALED) {
                     if (tid == 0) mbar_arrive(&p_full[b]);
                     if (tid < G) {  // a head each: its statistics, and what its O column is multiplied by
-                        const float m = fmaxf(fmaxf(red_max[tid], red_max[8 + tid]), fmaxf(red_max[16 + tid], red_max[24 + tid]));
-                        const float L = red_sum[tid] + red_sum[8 + tid] + red_sum[16 + tid] + red_sum[24 + tid];
-                        // 2^(ev - 8) / L; every V scale 0: 0 / L
-                        o_scale[b * 8 + tid] = __fdiv_rn(__uint_as_float(static_cast<uint32_t>(it.ev - 8 + 135) << 23), L) *
-                                               0x1p-8f;
-                        if (!it.single) {
+                        float m = fmaxf(fmaxf(red_max[tid], red_max[8 + tid]), fmaxf(red_max[16 + tid], red_max[24 + tid]));
+                        float L = red_sum[tid] + red_sum[8 + tid] + red_sum[16 + tid] + red_sum[24 + tid];
+                        float f = 0x1p-8f, kept = 0.f;
+                        if (__builtin_expect(!(it.flags & kItemFirst), 0)) {  // joined with the item's segments before
+                            const float2 run = ml_run[tid];
+                            const float top = fmaxf(m, run.x);
+                            kept = run.y * fast_exp2(run.x - top);
+                            const float w = fast_exp2(m - top);
+                            m = top;
+                            L = fmaf(L, w, kept);
+                            f *= w;
+                        }
+                        // 2^(ev - 8) / L (times the segment's weight); every V scale 0: 0 / L
+                        const float r = __frcp_rn(L);
+                        o_scale[b * 8 + tid] = __uint_as_float(static_cast<uint32_t>(it.ev + 127) << 23) * f * r;
+                        o_keep[b * 8 + tid] = kept * r;
+                        if (!(it.flags & kItemLast)) {
+                            ml_run[tid] = make_float2(m, L);
+                        } else if (!(it.flags & kItemSingle)) {
                             const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G + tid;
-                            *reinterpret_cast<float2*>(p.ws_ml + (hrow * p.max_parts + it.part) * 2) = make_float2(m, L);
+                            *reinterpret_cast<float2*>(p.ws_ml + (hrow * p.max_parts + it.part) * 2) =
+                                make_float2(m, L);
                         }
                     }
                 } else if (tid == 0) {
@@ -1402,15 +1472,43 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             }
             if constexpr (SCALED) {
                 const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G;
-                if (it.single) {
+#pragma unroll
+                for (int g = 0; g < G; ++g) o[g] *= o_scale[b * 8 + g];
+                // the output of the item's segments so far (each thread its own values) waits in the columns behind
+                // the two buffers, or in shared memory where they fill tensor memory
+                constexpr bool SPARE = 2 * SLOT_COLS + 8 <= kTcTmemCols;
+                static_assert(SPARE || (HALF && PREG == 2), "room for the output so far");
+                const uint32_t acc_addr = lane_addr + 2 * SLOT_COLS;
+                float* acc_smem = o_odd + 512;
+                if (!(it.flags & kItemFirst)) {
+                    float acc[G];
+                    if constexpr (SPARE) {
+                        tc::TmemLd<G>::load(acc_addr, acc);
+                        tc::tmem_wait_ld();
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < G; ++g) acc[g] = acc_smem[g * 64 + row];
+                    }
+#pragma unroll
+                    for (int g = 0; g < G; ++g) o[g] = fmaf(acc[g], o_keep[b * 8 + g], o[g]);
+                }
+                if (!(it.flags & kItemLast)) {
+                    if constexpr (SPARE) {
+                        tc::tmem_st<G>(acc_addr, o);
+                        tc::tmem_wait_st();
+                    } else {
+#pragma unroll
+                        for (int g = 0; g < G; ++g) acc_smem[g * 64 + row] = o[g];
+                    }
+                } else if (it.flags & kItemSingle) {
                     uint16_t* dst = static_cast<uint16_t*>(p.out) + hrow * HD + row;
 #pragma unroll
-                    for (int g = 0; g < G; ++g) dst[g * HD] = float_to_act<ACT>(o[g] * o_scale[b * 8 + g]);
+                    for (int g = 0; g < G; ++g) dst[g * HD] = float_to_act<ACT>(o[g]);
                 } else {
                     const size_t step = static_cast<size_t>(p.max_parts) * HD;
                     float* dst = p.ws_o + (hrow * p.max_parts + it.part) * HD + row;
 #pragma unroll
-                    for (int g = 0; g < G; ++g) dst[g * step] = o[g] * o_scale[b * 8 + g];
+                    for (int g = 0; g < G; ++g) dst[g * step] = o[g];
                 }
                 return true;
             }

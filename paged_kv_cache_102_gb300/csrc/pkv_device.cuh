@@ -187,6 +187,25 @@ struct Vec16<kE4M3> : Vec16E4M3 {};
 template <>
 struct Vec16<kE4M3B> : Vec16E4M3 {};
 
+// tops = elementwise max(tops, |x|) of eight 16-bit elements, in pairs (a NaN
+// does not enter).
+template <int ACT>
+__device__ __forceinline__ void top_pairs(const uint4& u, uint32_t& tops) {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if constexpr (ACT == kBF16) {
+            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&tops),
+                                             __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+            tops = *reinterpret_cast<const uint32_t*>(&m);
+        } else {
+            const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&tops),
+                                      __habs2(*reinterpret_cast<const __half2*>(&w[i])));
+            tops = *reinterpret_cast<const uint32_t*>(&m);
+        }
+    }
+}
+
 // E4M3 pair -> binary16 pair (exact: every E4M3 value is a binary16 value).
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t v) {
     uint32_t d;

@@ -360,25 +360,6 @@ __device__ __forceinline__ void plain_rows(const RopeAppendParams& p, int token,
     }
 }
 
-// tops = elementwise max(tops, |x|) of eight 16-bit elements, in pairs (a NaN
-// does not enter).
-template <int ACT>
-__device__ __forceinline__ void top_pairs(const uint4& u, uint32_t& tops) {
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if constexpr (ACT == kBF16) {
-            const __nv_bfloat162 m = __hmax2(*reinterpret_cast<const __nv_bfloat162*>(&tops),
-                                             __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
-            tops = *reinterpret_cast<const uint32_t*>(&m);
-        } else {
-            const __half2 m = __hmax2(*reinterpret_cast<const __half2*>(&tops),
-                                      __habs2(*reinterpret_cast<const __half2*>(&w[i])));
-            tops = *reinterpret_cast<const uint32_t*>(&m);
-        }
-    }
-}
-
 // The block's new scale (see the head of the file) for the run's largest
 // element `top`, its old scale being `old` (0: starts afresh).
 __device__ __forceinline__ float new_scale(float top, float old) {

@@ -214,6 +214,13 @@ DECODES = [
     ("f16", 64, 8, 64, 32, -1, "narrow"),
     ("bf16", 16, 2, 64, 16, 128, "odd"),
     ("f16", 24, 3, 64, 16, -1, "wide"),
+    # partitions of several 512-token segments
+    ("bf16", 16, 2, 128, 16, 1024, "wide"),
+    ("f16", 16, 2, 64, 32, 608, "narrow"),
+    ("bf16", 3, 3, 128, 16, 0, "odd"),
+    ("f16", 8, 1, 128, 32, 0, "narrow"),
+    ("bf16", 32, 4, 64, 16, 0, "wide"),
+    ("f16", 4, 1, 128, 16, 1024, "odd"),
 ]
 
 
@@ -302,6 +309,16 @@ def test_decode_scaled_more_rows_than_one_launch(pkv):
 def test_decode_scaled_long_context(pkv):
     _check_decode(pkv, ("bf16", 4, 1, 128, 16, -1, "wide"), [20011, 1])
     _check_decode(pkv, ("bf16", 2, 2, 128, 32, -1, "narrow"), [9001])
+    _check_decode(pkv, ("bf16", 8, 1, 128, 16, 2048, "odd"), [20011, 2049, 7])
+    _check_decode(pkv, ("f16", 8, 1, 64, 16, 0, "narrow"), [9001, 1])
+
+
+@pytest.mark.parametrize("case", [("bf16", 16, 8, 128, 16, -1, "odd"), ("f16", 8, 8, 64, 32, -1, "narrow")],
+                         ids=lambda c: "-".join(map(str, c)))
+def test_decode_scaled_many_sequences(pkv, case):
+    """Enough items for partitions of four segments; lengths at the segments' and the partitions' borders."""
+    lens = [2049, 0, 512, 513, 1024, 1025, 1536, 1537, 2047, 2048, 1, 2100] + [(i * 37) % 200 for i in range(52)]
+    _check_decode(pkv, case, lens)
 
 
 def test_decode_scaled_all_rows_empty(pkv):

@@ -89,6 +89,8 @@ def test_scaled_partitions_and_workspace(pkv_lib):
     assert size(4, 8, 8, 128, 129, 16, block_scales=True) == 512       # 4 * 8 * 5 = 160 items, whatever the group
     assert size(1, 8, 8, 64, 129, 16, block_scales=True) == 256        # 8 * 5 = 40 items
     assert size(4, 8, 8, 128, 8, 16, block_scales=True) == 128         # the whole context
+    assert size(64, 8, 8, 128, 129, 16, block_scales=True) == 2048     # 64 * 8 * 5 = 2560 items
+    assert size(64, 8, 8, 128, 100, 16, block_scales=True) == 1600     # 64 * 8 * 4 = 2048, the whole context
     assert size(4, 8, 8, 128, 129, 16, 1024, block_scales=True) == 1024
     assert size(4, 8, 8, 128, 129, 16, 48, block_scales=True) == -1
     rows = 4 * 8 * 5
