@@ -77,10 +77,14 @@
 // keep their precision whatever the scales of the other blocks are.  The sum
 // of 2^(score - R) is the denominator; log2 |vs| - ev enters R at no less than
 // -100, which keeps it finite (and a row without any V scale but 0 defined).
-// Two E4M3 parts of w leave up to 2^-8 of it, which the rounding of a bfloat16
-// result covers but not that of a binary16 one, so binary16 activations take a
-// third part: up to four heads fill 12 of the 16 columns, eight heads use 24 of
-// 32 (a second 16-byte column of P, with a ring of one stage less).
+// w enters as three E4M3 parts, each 2^5 times what the part before left, in O columns
+// of their own that the epilogue adds up with 2^-5 and 2^-10: at most 2^-14 of a
+// weight is lost, or 2^-28 of the largest, below what either 16-bit result rounds away
+// even where one token dominates.  Up to four heads fill 12 of the 16 columns, eight
+// heads use 24 of 32 (a second 16-byte column of P, with a ring of one stage less).
+// Against parts on one scale, two for bfloat16, whose outputs were 7e-4 (rms) off the
+// binary32 form's and are 1.1e-4 off it now: 128 ragged sequences of eight query heads
+// 75.2 -> 76.9 us, at head_dim 64 42.5 -> 44.4; a fourth part would make it 78.4 and 46.8.
 // An item may be longer than the 512 tokens whose scores tensor memory holds: the
 // scheduler passes it on as segments of 512, which the other roles take for items;
 // the softmax keeps each head's running maximum and sum, the epilogue the output
@@ -92,8 +96,8 @@
 // against 80.3 us for 128 ragged sequences.)
 // Measured, of the 6.7 TB/s that a copy reaches: 64 sequences of 40 heads of
 // their own, 1.43 GB of codes, 205 us (104 %, the memory is the bound); 8 of 32K
-// tokens, four query heads, 87 us (92 %); 128 ragged ones, eight query heads, 75 us
-// (86 %) and at head_dim 64, binary16, 43 us (58 %): the launch's ramp, its tail
+// tokens, four query heads, 87 us (92 %); 128 ragged ones, eight query heads, 77 us
+// (85 %) and at head_dim 64, binary16, 44 us (56 %): the launch's ramp, its tail
 // and the merge, and at head_dim 64 a segment's 64 KB, which pass faster than the
 // softmax warps' 3 us for it.
 // Every barrier wait is bounded (kWaitLimitNs); on a timeout the CTA stops
@@ -127,10 +131,13 @@ constexpr int kTcLenBuckets = 8;              // length buckets of the partly fi
 // K scales [32], V scales [32], log2 of the V scales [32].
 constexpr int kScaledEntry = 32 + 4 * 32 * 4;
 
-// 16-byte columns of P per token: a third part of eight heads' weights needs a second one.
-__host__ __device__ constexpr int tc_p_columns(int act, int cache, int G) {
-    return cache == kE4M3B && act == kF16 && G == 8 ? 2 : 1;
-}
+// Block-scaled: E4M3 parts of a weight, and the power of two by which each part is
+// larger than the part before it counts (see take_e4m3x2).
+constexpr int kScaledParts = 3;
+constexpr float kPartScale = 32.f;
+
+// 16-byte columns of P per token: more than two parts of eight heads' weights need a second one.
+__host__ __device__ constexpr int tc_p_columns(int cache, int G) { return cache == kE4M3B && G == 8 ? 2 : 1; }
 
 template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false, bool HALF = false, int PREG = 1>
 struct TcSmem {
@@ -280,6 +287,22 @@ __device__ __forceinline__ void split3_e4m3x2(float x0, float x1, uint32_t& hi, 
     split_e4m3x2(x0 - hv.x, x1 - hv.y, mid, lo);
 }
 
+// One part of x0 and x1: the nearest E4M3 codes, returned; then x = kPartScale *
+// (x - code), exact in binary32.  A code leaves at most 2^(e-4) of an x in [2^e,
+// 2^(e+1)), so the rest times 32 is at most 2^(e+1) again: the next part has the type's
+// whole range before it, and its least code counts 2^-5 of the one before.  Three parts
+// leave at most 2^-14 of x, or 2^-20 (half the last part's least code) if that is more.
+// Parts on one scale would all end at the least code, 2^-9, which is about what weights
+// beside one that dominates amount to.
+__device__ __forceinline__ uint32_t take_e4m3x2(float& x0, float& x1) {
+    const __nv_fp8x2_storage_t h = __nv_cvt_float2_to_fp8x2(make_float2(x0, x1), __NV_SATFINITE, __NV_E4M3);
+    __half2_raw hr = __nv_cvt_fp8x2_to_halfraw2(h, __NV_E4M3);
+    const float2 hv = __half22float2(*reinterpret_cast<__half2*>(&hr));
+    x0 = (x0 - hv.x) * kPartScale;
+    x1 = (x1 - hv.y) * kPartScale;
+    return h;
+}
+
 template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR = false, bool HALF = false>
 __global__ void __launch_bounds__(kTcThreads, 2)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
@@ -292,9 +315,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     constexpr int HD = PAIR || HALF ? 64 : kTcD;  // head_dim of the caches, queries and output
     static_assert(!PAIR || !FP8, "pairs of head_dim-64 kv heads: 16-bit caches");
     static_assert(!HALF || SCALED, "two tokens a row: block-scaled E4M3 caches");
-    constexpr int PREG = tc_p_columns(ACT, CACHE, G);
-    constexpr bool P3 = SCALED && ACT == kF16;  // three parts of P
-    constexpr int PART = P3 && G <= 4 ? 4 : 8;  // columns from one part of P to the next
+    constexpr int PREG = tc_p_columns(CACHE, G);
+    constexpr int PARTS = SCALED ? kScaledParts : 2;  // of P
+    constexpr int PART = SCALED && G <= 4 ? 4 : 8;    // columns from one part of P to the next
+    static_assert(PARTS * PART <= 16 * PREG, "columns of P");
     using S = TcSmem<NS, STG, PAIR, SCALED, HALF, PREG>;
     constexpr int THREADS = kTcThreads;
     constexpr int TPR = HALF ? 2 : 1;         // tokens per tile row
@@ -718,11 +742,12 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         int nq = 0;        // Q tiles written so far
         int nread = 0;
         if constexpr (Q3) {
-            // rows 8-15 of the low-part operand stay zero (made visible to the
+            // rows 8-15 (SCALED: 0-7) of the low-part operand stay zero (made visible to the
             // MMA by the fence before the first Q is published)
             if (parity == 0)
                 for (int i = lane; i < 64 * S::QBUFS; i += 32)
-                    reinterpret_cast<uint4*>(qbuf + (i >> 6) * S::QBUF + 3072)[i & 63] = make_uint4(0u, 0u, 0u, 0u);
+                    reinterpret_cast<uint4*>(qbuf + (i >> 6) * S::QBUF + (SCALED ? 2048 : 3072))[i & 63] =
+                        make_uint4(0u, 0u, 0u, 0u);
         }
         auto read_item = [&](TcItem& it, int& phys) {
             const int slot = nread % kTcQueue;
@@ -776,7 +801,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 // g, row 8 + g lo (1 KB further).  Binary16 queries (11 bits) take
                 // a third part: rows 8 + g hold the middle part and the low part
                 // sits in a second operand 2 KB further, over 8 zero rows, so that a
-                // second MMA adds K lo^T into the same accumulator columns.
+                // second MMA adds K lo^T into the same accumulator columns.  SCALED:
+                // the remainder enters times kPartScale, so that elements far below the
+                // largest keep their bits (half the least step left is 2^-22 of the largest
+                // element instead of 2^-17), and the low part, of the same scale, in rows
+                // 8-15 of its operand, under the zero rows.
                 // two Q buffers: item k's Q goes in once the S MMAs of item k-2 have read it
                 const int qb = k & 1;
                 if (lane == 0 && k >= 2) good = tc_wait(&q_empty[qb], ((k >> 1) - 1) & 1, abort_flag, p.err);
@@ -828,8 +857,16 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                             const uint32_t w = e[2 * j + h2];
                             const float x0 = act_to_float<ACT>(static_cast<uint16_t>(w & 0xffffu)) * f;
                             const float x1 = act_to_float<ACT>(static_cast<uint16_t>(w >> 16)) * f;
-                            if constexpr (Q3) split3_e4m3x2(x0, x1, hb[h2], mb[h2], lb[h2]);
-                            else split_e4m3x2(x0, x1, hb[h2], mb[h2]);
+                            if constexpr (SCALED) {
+                                float r0 = x0, r1 = x1;
+                                hb[h2] = take_e4m3x2(r0, r1);
+                                if constexpr (Q3) split_e4m3x2(r0, r1, mb[h2], lb[h2]);
+                                else mb[h2] = take_e4m3x2(r0, r1);
+                            } else if constexpr (Q3) {
+                                split3_e4m3x2(x0, x1, hb[h2], mb[h2], lb[h2]);
+                            } else {
+                                split_e4m3x2(x0, x1, hb[h2], mb[h2]);
+                            }
                         }
                         hw[j] = hb[0] | (hb[1] << 16);
                         mw[j] = mb[0] | (mb[1] << 16);
@@ -839,7 +876,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     *reinterpret_cast<uint4*>(qbuf_k + off) = make_uint4(hw[0], hw[1], hw[2], hw[3]);
                     *reinterpret_cast<uint4*>(qbuf_k + 1024 + off) = make_uint4(mw[0], mw[1], mw[2], mw[3]);
                     if constexpr (Q3)
-                        *reinterpret_cast<uint4*>(qbuf_k + 2048 + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
+                        *reinterpret_cast<uint4*>(qbuf_k + (SCALED ? 3072 : 2048) + off) = make_uint4(lw[0], lw[1], lw[2], lw[3]);
                 }
                 if (SCALED && __builtin_expect(infinite, 0)) {  // an infinite element: a NaN, as its head's result is
                     __syncwarp();
@@ -1278,7 +1315,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
                         for (int t = 0; t < kTcMaxTiles; ++t)
 #pragma unroll
-                            for (int g = 0; g < G; ++g) sc[t][g] += lo[t][g];
+                            for (int g = 0; g < G; ++g)
+                                sc[t][g] = SCALED ? fmaf(lo[t][g], 1.f / kPartScale, sc[t][g]) : sc[t][g] + lo[t][g];
                     } else {
 #pragma unroll
                         for (int t = 0; t < kTcMaxTiles; ++t)
@@ -1318,10 +1356,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 for (int t = 0; t < kTcMaxTiles; ++t) {
                     if (t < n_tiles) {
                         if constexpr (FP8) {
-                            // P x 2^8 (at most 256) = hi + lo in E4M3; token `row` of
-                            // tile t holds 16 bytes: hi of heads 0-7, then lo of heads 0-7
-                            uint32_t w[4] = {0u, 0u, 0u, 0u};
-                            [[maybe_unused]] uint32_t w2[2] = {0u, 0u};
+                            // P x 2^8 (at most 256) in E4M3 parts; token `row` of tile t
+                            // holds 16 bytes (two times 16): the first part of heads
+                            // 0 .. PART-1, then the second, then the third
+                            uint32_t w[4 * PREG] = {};
 #pragma unroll
                             for (int g = 0; g < G; g += 2) {
                                 // M is finite (every item has a token); 2^-inf = 0 for masked rows
@@ -1330,25 +1368,22 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                                 const float p1 = G > 1 ? fast_exp2(sc[t][g + SECOND] - M[g + SECOND]) : 0.f;
                                 sum[g] += p0;
                                 if (G > 1) sum[g + SECOND] += p1;
-                                uint32_t hi, lo;
-                                const float pm = SCALED ? vs_t[t] : 256.f;  // vs_t: times 2^(8 - ev)
-                                if constexpr (P3) {
-                                    uint32_t low;
-                                    split3_e4m3x2(p0 * pm, p1 * pm, hi, lo, low);
-                                    constexpr int WORDS = PART / 4;
-                                    w[g >> 2] |= hi << (8 * (g & 3));
-                                    w[WORDS + (g >> 2)] |= lo << (8 * (g & 3));
-                                    if constexpr (PREG == 2) w2[g >> 2] |= low << (8 * (g & 3));
-                                    else w[2] |= low << (8 * g);
+                                if constexpr (SCALED) {
+                                    float x0 = p0 * vs_t[t], x1 = p1 * vs_t[t];  // vs_t: times 2^(8 - ev)
+#pragma unroll
+                                    for (int part = 0; part < PARTS; ++part)
+                                        w[part * (PART / 4) + (g >> 2)] |= take_e4m3x2(x0, x1) << (8 * (g & 3));
                                 } else {
-                                    split_e4m3x2(p0 * pm, p1 * pm, hi, lo);
+                                    uint32_t hi, lo;
+                                    split_e4m3x2(p0 * 256.f, p1 * 256.f, hi, lo);
                                     w[g >> 2] |= hi << (8 * (g & 3));
                                     w[2 + (g >> 2)] |= lo << (8 * (g & 3));
                                 }
                             }
                             unsigned char* pt = pb + t * PREG * 2048 + row * 16;
                             *reinterpret_cast<uint4*>(pt) = make_uint4(w[0], w[1], w[2], w[3]);
-                            if constexpr (PREG == 2) *reinterpret_cast<uint4*>(pt + 2048) = make_uint4(w2[0], w2[1], 0u, 0u);
+                            if constexpr (PREG == 2)
+                                *reinterpret_cast<uint4*>(pt + 2048) = make_uint4(w[4], w[5], w[6], w[7]);
                         } else {
                             // 8-row regions of (tile, 64-token half), 1 KB apart; PAIR:
                             // 16-row regions, 2 KB apart, rows 8-15 for kv head 2v+1
@@ -1445,13 +1480,22 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 const uint32_t o_addr = lane_addr + b * SLOT_COLS + O_COL + (HALF ? (q4 >> 1) * (PREG * kTcN) : 0);
                 tc::TmemLd<G>::load(o_addr + hh * 8, o);
                 if constexpr (FP8) {
-                    float lo[G];  // O of the low parts of P
-                    [[maybe_unused]] float low[G];
-                    tc::TmemLd<G>::load(o_addr + PART, lo);
-                    if constexpr (P3) tc::TmemLd<G>::load(o_addr + 2 * PART, low);
+                    float lo[PARTS - 1][G];  // O of the other parts of P
+#pragma unroll
+                    for (int part = 1; part < PARTS; ++part) tc::TmemLd<G>::load(o_addr + part * PART, lo[part - 1]);
                     tc::tmem_wait_ld();
 #pragma unroll
-                    for (int g = 0; g < G; ++g) o[g] += P3 ? lo[g] + low[g] : lo[g];
+                    for (int g = 0; g < G; ++g) {
+                        if constexpr (SCALED) {
+                            float rest = lo[PARTS - 2][g];
+#pragma unroll
+                            for (int part = PARTS - 2; part >= 1; --part)
+                                rest = fmaf(rest, 1.f / kPartScale, lo[part - 1][g]);
+                            o[g] = fmaf(rest, 1.f / kPartScale, o[g]);
+                        } else {
+                            o[g] += lo[0][g];
+                        }
+                    }
                 } else {
                     tc::tmem_wait_ld();
                 }

@@ -8,12 +8,12 @@ namespace pkv {
 namespace {
 
 // 16 KB stages at two CTAs per SM: five, or four when the per-row tables (or the
-// larger P of binary16 activations with eight heads) leave no room, then three.
+// larger P of eight heads) leave no room, then three.
 template <int ACT>
 cudaError_t launch_scaled(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, int BS, int G,
                           cudaStream_t s) {
     const int rows = p.table_kvh_stride != 0 ? p.num_seqs * p.num_kv_heads : p.num_seqs;
-    const bool wide = tc_p_columns(ACT, kE4M3B, G) == 2;
+    const bool wide = tc_p_columns(kE4M3B, G) == 2;
     auto fits = [](int bytes) { return 2 * (bytes + 1024) <= kTcSmemPerSm; };
     if (wide)
         return fits(TcSmem<4, kTcStage8, false, true, true, 2>::alloc(rows))

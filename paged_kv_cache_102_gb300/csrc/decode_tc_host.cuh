@@ -63,7 +63,7 @@ template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR, bool HALF>
 cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                    int ctas_per_sm, cudaStream_t s) {
     auto kern = paged_decode_tc_kernel<ACT, CACHE, BS, G, NS, PAIR, HALF>;
-    using Smem = TcSmem<NS, is_e4m3(CACHE) ? kTcStage8 : kTcStage, PAIR, CACHE == kE4M3B, HALF, tc_p_columns(ACT, CACHE, G)>;
+    using Smem = TcSmem<NS, is_e4m3(CACHE) ? kTcStage8 : kTcStage, PAIR, CACHE == kE4M3B, HALF, tc_p_columns(CACHE, G)>;
     constexpr int threads = kTcThreads;
     const int rows = p.table_kvh_stride != 0 ? p.num_seqs * p.num_kv_heads : p.num_seqs;
     const int smem = Smem::alloc(rows);
