@@ -31,9 +31,10 @@
 // both scales are warp-uniform, one shuffle each: the K scale joins
 // the factor of the reduced dot product, the V scale the weights.  Weights are
 // kept relative to a power of two 2^mv near the V scales seen, moved (with acc)
-// when a block's scale is more than 2^7 away from it, so that p * vs / 2^mv
-// stays within binary16 whatever the scales are; binary16 activations, whose
-// result would show a weight's rounding to binary16, keep weights in binary32.
+// when a block's scale is more than 2^7 away from it, so that p * vs / 2^mv, at
+// most 2^16, and its sums stay within binary32 whatever the scales are.  It is
+// a binary32 value: as a binary16 one it could pass that type's range, and the
+// result would show its rounding.
 // It serves what is over in one launch (4 x 8 rows of up to 64 tokens 3.8 us,
 // bound by that launch and four dependent round trips to memory) and the shapes
 // that the tensor-core kernel does not take.
@@ -219,7 +220,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     // binary16 pairs (exact), q is held in binary16 (exact for a 16-bit value
     // of magnitude <= 65504, checked per warp), products accumulate in
     // binary32 with fma.rn.f32.f16, and the scale multiplies the reduced dot
-    // product.  P·V takes the probability rounded to binary16.
+    // product.  P·V takes the probability rounded to binary16, or with block
+    // scales in binary32.
     bool mixed = false;
     if constexpr (is_e4m3(CACHE)) {
         bool fits = true;
@@ -403,7 +405,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
 #pragma unroll
                         for (int i = 0; i < QN; ++i) {
                             const uint32_t vh = e4m3x2_to_f16x2(static_cast<uint16_t>(w[i / 2] >> (16 * (i % 2))));
-                            if constexpr (C::SCALED && ACT == kF16) {
+                            if constexpr (C::SCALED) {
                                 const float2 vf2 = __half22float2(*reinterpret_cast<const __half2*>(&vh));
 #pragma unroll
                                 for (int g = 0; g < G; ++g) {

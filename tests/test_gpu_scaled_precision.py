@@ -147,3 +147,26 @@ def test_queries_with_channels_far_above_the_others(pkv, act, D):
     host[0][..., 3] = 2.0 ** 9
     host[1][..., 3] = 0
     _check(pkv, host, 16, act, True, scale)
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(128, 32, 32), (64, 32, 16), (128, 16, 4)])
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+def test_cuda_core_weights(pkv, act, D, hq, hkv):
+    """Short contexts on the CUDA cores: few tokens, one of them without values, so that an output shows a weight."""
+    host, scale = _case("short", act, hq, hkv, D, 16, [2] * 12 + [3, 9, 17, 40],
+                        lambda n, h, g: torch.rand(n, h, generator=g))
+    host[2][host[5][:, 0].long(), :, 0] = 0
+    _check(pkv, host, 16, act, False, scale)
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(128, 2, 2), (64, 4, 2)])
+@pytest.mark.parametrize("act", ["f16", "bf16"])
+def test_cuda_core_weight_times_scale_near_2_16(pkv, act, D, hq, hkv):
+    """Scores just under 2^8 times the running reference's weight, on V scales just under 2^8 times the first ones."""
+    host, _ = _case("gap", act, hq, hkv, D, 16, [64], lambda n, h, g: torch.zeros(n, h))
+    host[0].fill_(1.0)
+    late = host[5][0, 2:].long()
+    host[1][late] = 0x38  # 1.0 in the last 32 tokens, 0 before
+    host[4].fill_(2.0 ** -12)
+    host[4][late] = 2.0 ** -12 * 2.0 ** 7 * 1.9999
+    _check(pkv, host, 16, act, False, 7.9999 * np.log(2.0) / (D * 2.0 ** -6))
