@@ -221,19 +221,32 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     // of magnitude <= 65504, checked per warp), products accumulate in
     // binary32 with fma.rn.f32.f16, and the scale multiplies the reduced dot
     // product.  P·V takes the probability rounded to binary16, or with block
-    // scales in binary32.
+    // scales in binary32.  A bfloat16 value below 2^-17 can lose up to 2^-25 as
+    // a binary16 one; with block scales, whose keys may be of any magnitude, a
+    // head's largest element then has to be 2^-3 at least, so that no more than
+    // 2^-22 of it is lost, or every element exact.
     bool mixed = false;
     if constexpr (is_e4m3(CACHE)) {
         bool fits = true;
 #pragma unroll
         for (int g = 0; g < G; ++g) {
+            [[maybe_unused]] float top = 0.f;
+            [[maybe_unused]] bool exact = true;
 #pragma unroll
             for (int v = 0; v < C::VEC; v += 8) {
                 const uint4 u = *reinterpret_cast<const uint4*>(qsrc + g * D + c * C::VEC + v);
                 const uint16_t* e = reinterpret_cast<const uint16_t*>(&u);
 #pragma unroll
-                for (int i = 0; i < 8; ++i) fits = fits && fabsf(act_to_float<ACT>(e[i])) <= 65504.f;
+                for (int i = 0; i < 8; ++i) {
+                    const float a = fabsf(act_to_float<ACT>(e[i]));
+                    fits = fits && a <= 65504.f;
+                    if constexpr (C::SCALED && ACT == kBF16) {
+                        top = fmaxf(top, a);
+                        exact = exact && (a >= 0x1p-17f || a == 0.f);
+                    }
+                }
             }
+            if constexpr (C::SCALED && ACT == kBF16) fits = (warp_max(top) >= 0.125f || exact) && fits;
         }
         mixed = __all_sync(0xffffffffu, fits);
     }

@@ -170,3 +170,13 @@ def test_cuda_core_weight_times_scale_near_2_16(pkv, act, D, hq, hkv):
     host[4].fill_(2.0 ** -12)
     host[4][late] = 2.0 ** -12 * 2.0 ** 7 * 1.9999
     _check(pkv, host, 16, act, False, 7.9999 * np.log(2.0) / (D * 2.0 ** -6))
+
+
+@pytest.mark.parametrize("D,hq,hkv", [(128, 8, 8), (64, 8, 4)])
+@pytest.mark.parametrize("tensor_cores", [False, True])
+def test_tiny_bfloat16_queries_over_large_keys(pkv, D, hq, hkv, tensor_cores):
+    """Queries near 2^-18, below what binary16 holds exactly, and K scales that make up for it."""
+    host, scale = _case("tiny", "bf16", hq, hkv, D, 16, [40, 64, 3], lambda n, h, g: torch.randn(n, h, generator=g) * 2)
+    host[0] = host[0][..., :1].expand(host[0].shape).contiguous() * 2.0 ** -18
+    host[3].fill_(2.0 ** 12)
+    _check(pkv, host, 16, "bf16", tensor_cores, scale)
