@@ -23,6 +23,7 @@ each block and kv head (k_scales, v_scales [num_blocks, num_kv_heads]).
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import functools
 import math
@@ -149,12 +150,22 @@ _ws_lock = threading.Lock()
 _ws_cache: dict = {}
 
 
-def _workspace(device, stream_ptr: int, nbytes: int) -> torch.Tensor:
-    """A reusable workspace per (device, stream): calls on one stream are ordered.  A call that is being captured gets
-    one of its own, from the graph's memory: the reusable one may be replaced while the graph lives."""
+def _torch_stream(stream, device) -> torch.cuda.Stream:
+    """`stream`, any object with a cuda_stream handle, as torch's own."""
+    return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream, device)
+
+
+def _workspace(device, stream, nbytes: int, kind: int = 0) -> torch.Tensor:
+    """A reusable workspace per (device, stream) and kind of call: calls on one stream are ordered.  It is allocated on
+    the stream that uses it (default: the current one), so that a smaller one that it replaces is not handed out again
+    before the calls in flight are done with it.  A call that is being captured gets one of its own, from the graph's
+    memory: the reusable one may be replaced while the graph lives."""
+    if stream is not None:
+        with torch.cuda.stream(_torch_stream(stream, device)):
+            return _workspace(device, None, nbytes, kind)
     if torch._C._cuda_isCurrentStreamCapturing():
         return torch.empty(nbytes, dtype=torch.uint8, device=device)
-    key = (device.index, stream_ptr)
+    key = (device.index, _stream(None, device), kind)
     with _ws_lock:
         buf = _ws_cache.get(key)
         if buf is None or buf.numel() < nbytes:
@@ -195,7 +206,7 @@ def _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_
     if workspace is None:
         need = workspace_size(B, Hq, Hkv, D, max_blocks, bs, partition_size)
         if need:
-            workspace = _workspace(q.device, s, need)
+            workspace = _workspace(q.device, stream, need)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables), max_blocks, _ptr(context_lens), B, Hq, Hkv,
             bs, D, NB, float(scale), _ptr(out), _code(q), _code(k_cache), _ptr(k_scale), _ptr(v_scale),
@@ -236,7 +247,7 @@ def _decode_append_args(q, k_new, v_new, slot_mapping, k_cache, v_cache, block_t
     if workspace is None:
         need = workspace_size(B, Hq, Hkv, D, max_blocks, bs, partition_size)
         if need:
-            workspace = _workspace(q.device, s, need)
+            workspace = _workspace(q.device, stream, need)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     args = (_ptr(q), _ptr(k_new), _ptr(v_new), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), _ptr(block_tables),
             max_blocks, _ptr(context_lens), B, Hq, Hkv, bs, D, NB, float(scale), _ptr(out), _code(q),
@@ -270,9 +281,9 @@ class DecodePlan:
             if workspace is None:  # the plan's own, so that graphs of two plans may run at once
                 need = workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], block_tables.shape[1],
                                       k_cache.shape[2], partition_size, True)
-                workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=k_cache.device)
-                if isinstance(stream, torch.cuda.Stream) and not torch.cuda.is_current_stream_capturing():
-                    workspace.record_stream(stream)
+                with contextlib.nullcontext() if stream is None else torch.cuda.stream(
+                        _torch_stream(stream, k_cache.device)):
+                    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=k_cache.device)
             self._args, self.out, ws = _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables,
                                                            context_lens, scale, out, partition_size, workspace, stream)
         elif all(given):
@@ -339,7 +350,7 @@ def quest_select(q, kmeta, block_tables, context_lens, block_size, budget_blocks
     s = _stream(stream, q.device)
     need = int(_native.lib().quest_workspace_size(B, Hkv, block_tables.shape[1]))
     if workspace is None:
-        workspace = _workspace(q.device, -s - 1, need)  # separate from the decode workspace
+        workspace = _workspace(q.device, stream, need, kind=1)  # separate from the decode workspace
     _native.call("quest_select", _ptr(q), _ptr(kmeta), _ptr(block_tables), block_tables.shape[1], _ptr(context_lens),
                  B, Hq, Hkv, block_size, D, NB, _code(q), int(budget_blocks), _ptr(sel_tables), _ptr(sel_lens),
                  _ptr(workspace), workspace.numel() * workspace.element_size(), s)
@@ -360,7 +371,7 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, sel_tables, sel_lens, sca
     s = _stream(stream, q.device)
     need = workspace_size(B, Hq, Hkv, D, max_sel, bs, partition_size)
     if need and workspace is None:
-        workspace = _workspace(q.device, s, need)
+        workspace = _workspace(q.device, stream, need)
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _native.call("paged_attention_decode_sparse", _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(sel_tables), max_sel,
                  _ptr(sel_lens), B, Hq, Hkv, bs, D, NB, float(scale), _ptr(out), _code(q), _code(k_cache),
@@ -650,7 +661,7 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
     s = _stream(stream, device)
     if workspace is None:
         need = _scaled_workspace_size(B, Hq, Hkv, D, tshape[1], bs, partition_size)
-        workspace = _workspace(device, s, max(need, 1))  # (0: an argument that the library refuses)
+        workspace = _workspace(device, stream, max(need, 1))  # (0: an argument that the library refuses)
     qp, kc, vc, s1, s2, tables, lens, ws = _pointers(
         name, device, "q k_cache v_cache k_scales v_scales block_tables context_lens workspace", q, k_cache, v_cache,
         k_scales, v_scales, block_tables, context_lens, workspace)

@@ -1,0 +1,72 @@
+"""The binding's own memory on streams that are not the current one, on the GPU."""
+import numpy as np
+import pytest
+import torch
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture
+def pkv(pkv_lib, cuda_device):
+    pkv_lib.device_error(reset=True)
+    yield pkv_lib
+    assert pkv_lib.device_error(reset=True) == 0
+
+
+def _case(seed, blocks, hq=32, hkv=4, D=128, bs=16):
+    """Arguments of paged_attention_decode_scaled for sequences of so many blocks."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    nb = sum(blocks)
+    at = np.cumsum([0] + blocks)
+    tables = torch.zeros(len(blocks), max(blocks), dtype=torch.int32)
+    for b, n in enumerate(blocks):
+        tables[b, :n] = torch.arange(at[b], at[b] + n)
+    codes = lambda: torch.randint(0, 0x70, (nb, hkv, bs, D), dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    scales = lambda: torch.exp2(torch.randint(-9, -4, (nb, hkv), device="cuda", generator=g).float())  # noqa: E731
+    q = torch.randn(len(blocks), hq, D, device="cuda", generator=g).to(torch.bfloat16)
+    lens = torch.tensor([n * bs - 3 for n in blocks], dtype=torch.int32, device="cuda")
+    return q, codes(), codes(), scales(), scales(), tables.cuda(), lens, 0.1
+
+
+@pytest.mark.parametrize("given", [True, False], ids=["stream argument", "current stream"])
+def test_two_decodes_of_one_capture(pkv, given):
+    """Two decodes on streams forked from a capturing one, as branches that may run at once."""
+    args = [_case(s, [120, 90, 7, 200, 64, 128]) for s in (1, 2)]
+    want = [pkv.paged_attention_decode_scaled(*a) for a in args]
+    outs = [torch.empty_like(w) for w in want]
+    main, s1, s2 = (torch.cuda.Stream() for _ in range(3))
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=main):
+        for s, a, out in ((s1, args[0], outs[0]), (s2, args[1], outs[1])):
+            s.wait_stream(main)
+            if given:
+                pkv.paged_attention_decode_scaled(*a, out=out, stream=s)
+            else:
+                with torch.cuda.stream(s):
+                    pkv.paged_attention_decode_scaled(*a, out=out)
+        main.wait_stream(s1)
+        main.wait_stream(s2)
+    for _ in range(20):
+        for out in outs:
+            out.zero_()
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_larger_call_on_a_given_stream(pkv):
+    """A call that outgrows the stream's workspace while the call before it is still waiting to run."""
+    small, large = _case(3, [100, 64]), _case(4, [150] * 10)
+    want = [pkv.paged_attention_decode_scaled(*a) for a in (small, large)]
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)  # about ten milliseconds
+    first = pkv.paged_attention_decode_scaled(*small, stream=s)
+    second = pkv.paged_attention_decode_scaled(*large, stream=s)
+    junk = [torch.full((1 << 18,), 77, dtype=torch.uint8, device="cuda") for _ in range(16)]
+    torch.cuda.synchronize()
+    assert torch.equal(first, want[0]) and torch.equal(second, want[1])
+    assert all(bool((j == 77).all()) for j in junk)
