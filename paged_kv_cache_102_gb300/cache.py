@@ -21,8 +21,8 @@ from __future__ import annotations
 import numpy as np
 import torch
 
-from . import (PARTITION_AUTO, BlockManager, paged_attention_decode, paged_attention_decode_scaled, paged_block_copy,
-               paged_kv_append, paged_kv_append_scaled, paged_rope_append)
+from . import (PARTITION_AUTO, BlockManager, _torch_stream, paged_attention_decode, paged_attention_decode_scaled,
+               paged_block_copy, paged_kv_append, paged_kv_append_scaled, paged_rope_append)
 
 
 class PagedKVCache:
@@ -60,15 +60,21 @@ class PagedKVCache:
         self.blocks.free_sequence(seq_id)
 
     def tables(self, seq_ids, max_blocks_per_seq=None):
-        t, lens = self.blocks.tables(seq_ids, max_blocks_per_seq)
-        return (torch.from_numpy(t).to(self.device, non_blocking=False),
-                torch.from_numpy(lens).to(self.device, non_blocking=False))
+        return tuple(self._upload(a, None) for a in self.blocks.tables(seq_ids, max_blocks_per_seq))
+
+    def _upload(self, array, stream) -> torch.Tensor:
+        """A device copy of a host array, which has arrived when this returns.  It belongs to the current stream;
+        where a step on another one reads it, it is not handed out again before that step is done with it."""
+        t = torch.from_numpy(array).to(self.device)
+        if stream is not None:
+            t.record_stream(_torch_stream(stream, self.device))
+        return t
 
     # -- device steps ------------------------------------------------------------
     def append(self, seq_ids, k: torch.Tensor, v: torch.Tensor, stream=None):
         """Write one new token per sequence (k, v: [n, Hkv, D]); returns (slots, cow pairs) on the host."""
         slots, pairs = self._reserve(seq_ids, stream)
-        d_slots = torch.from_numpy(slots).to(self.device)
+        d_slots = self._upload(slots, stream)
         if self.k_scales is not None:
             paged_kv_append_scaled(k, v, d_slots, self.k_cache, self.v_cache, self.k_scales, self.v_scales,
                                    stream=stream)
@@ -81,23 +87,22 @@ class PagedKVCache:
         returns the rotated queries."""
         slots, _ = self._reserve(seq_ids, stream)
         positions = np.asarray([self.blocks.context_len(s) - 1 for s in np.asarray(seq_ids)], np.int32)
-        return paged_rope_append(q, k, v, torch.from_numpy(positions).to(self.device),
-                                 torch.from_numpy(slots).to(self.device), inv_freq, self.k_cache, self.v_cache,
-                                 interleaved=interleaved, attention_factor=attention_factor, q_out=q_out,
-                                 k_scale=self.k_scale, v_scale=self.v_scale, k_scales=self.k_scales,
-                                 v_scales=self.v_scales, stream=stream)
+        return paged_rope_append(q, k, v, self._upload(positions, stream), self._upload(slots, stream), inv_freq,
+                                 self.k_cache, self.v_cache, interleaved=interleaved,
+                                 attention_factor=attention_factor, q_out=q_out, k_scale=self.k_scale,
+                                 v_scale=self.v_scale, k_scales=self.k_scales, v_scales=self.v_scales, stream=stream)
 
     def _reserve(self, seq_ids, stream):
         """Slots of one new token per sequence; the copy-on-write copies run on the stream."""
         slots, pairs = self.blocks.append_slots(seq_ids)
         if len(pairs):
-            paged_block_copy(self.k_cache, self.v_cache, torch.from_numpy(pairs).to(self.device), stream=stream,
+            paged_block_copy(self.k_cache, self.v_cache, self._upload(pairs, stream), stream=stream,
                              k_scales=self.k_scales, v_scales=self.v_scales)
         return slots, pairs
 
     def decode(self, seq_ids, q: torch.Tensor, scale: float, out=None, partition_size=PARTITION_AUTO,
                max_blocks_per_seq=None, stream=None):
-        tables, lens = self.tables(seq_ids, max_blocks_per_seq)
+        tables, lens = (self._upload(a, stream) for a in self.blocks.tables(seq_ids, max_blocks_per_seq))
         if self.k_scales is not None:
             return paged_attention_decode_scaled(q, self.k_cache, self.v_cache, self.k_scales, self.v_scales, tables,
                                                  lens, scale, out=out, partition_size=partition_size, stream=stream)

@@ -21,7 +21,9 @@ def _case(seed, blocks, hq=32, hkv=4, D=128, bs=16):
     tables = torch.zeros(len(blocks), max(blocks), dtype=torch.int32)
     for b, n in enumerate(blocks):
         tables[b, :n] = torch.arange(at[b], at[b] + n)
-    codes = lambda: torch.randint(0, 0x70, (nb, hkv, bs, D), dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    def codes():
+        return torch.randint(0, 0x70, (nb, hkv, bs, D), dtype=torch.uint8, device="cuda", generator=g)
+
     scales = lambda: torch.exp2(torch.randint(-9, -4, (nb, hkv), device="cuda", generator=g).float())  # noqa: E731
     q = torch.randn(len(blocks), hq, D, device="cuda", generator=g).to(torch.bfloat16)
     lens = torch.tensor([n * bs - 3 for n in blocks], dtype=torch.int32, device="cuda")
@@ -70,3 +72,40 @@ def test_larger_call_on_a_given_stream(pkv):
     torch.cuda.synchronize()
     assert torch.equal(first, want[0]) and torch.equal(second, want[1])
     assert all(bool((j == 77).all()) for j in junk)
+
+
+@pytest.mark.parametrize("kind", ["plain", "scaled"])
+def test_cache_steps_on_a_given_stream(pkv, kind):
+    """Many steps of a PagedKVCache queued up behind a wait on a given stream, with uploads and other allocations of
+    the current one between them, against the same steps one after the other on one stream."""
+    from paged_kv_cache_102_gb300.cache import PagedKVCache
+    g = torch.Generator(device="cuda").manual_seed(11)
+    n, hq, hkv, D, steps = 5, 8, 2, 64, 40
+    rand = lambda h: torch.randn(steps, n, h, D, device="cuda", generator=g).to(torch.bfloat16)  # noqa: E731
+    q, k, v = rand(hq), rand(hkv), rand(hkv)
+    freq, _ = pkv.rope_inv_freq(D)
+
+    def run(stream):
+        cache = PagedKVCache(64, hkv, 16, D, block_scales=kind == "scaled")
+        for i in range(n):
+            cache.add_sequence(i, 0)
+        outs, q_outs = torch.empty_like(q), torch.empty_like(q)
+        torch.cuda.synchronize()
+        if stream is not None:
+            with torch.cuda.stream(stream):
+                torch.cuda._sleep(40_000_000)  # about twenty milliseconds
+        for t in range(steps):
+            if t == 9:
+                cache.free(n - 1)
+                cache.fork(0, n - 1)  # the next step copies the shared block
+            if t % 2:
+                cache.append(range(n), k[t], v[t], stream=stream)
+            else:
+                cache.rope_append(range(n), q[t], k[t], v[t], freq, q_out=q_outs[t], stream=stream)
+            cache.decode(range(n), q[t], 0.1, out=outs[t], stream=stream)
+            torch.full((64,), -1, dtype=torch.int64, device="cuda")  # reuses what was given back too early
+        torch.cuda.synchronize()
+        return outs, q_outs[::2], cache.k_cache, cache.v_cache
+
+    for a, b in zip(run(torch.cuda.Stream()), run(None)):
+        assert torch.equal(a, b)

@@ -89,3 +89,33 @@ def test_a_replaced_workspace_belongs_to_its_stream(streams, pkv_lib, monkeypatc
     large = run(2, 4000)
     assert large != small and run(2, 40) == large and run(3, 4) != large
     assert [h for h, _ in streams.allocated] == [2, 2, 3]
+
+
+@pytest.mark.parametrize("kind", ["plain", "scaled"])
+def test_cache_steps_keep_their_uploads_for_the_given_stream(pkv_lib, monkeypatch, kind):
+    """Slots, positions, copy pairs, tables and lengths that PagedKVCache uploads for a step on a given stream are
+    marked as used there, each of them, before the step is enqueued."""
+    from paged_kv_cache_102_gb300 import cache as cache_mod
+    recorded, used = [], []
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: _at(handle))
+    monkeypatch.setattr(torch.Tensor, "record_stream", lambda t, s: recorded.append((t.data_ptr(), s.cuda_stream)))
+
+    def launched(name, *own):
+        def call(*args, stream=None, **kw):
+            used.extend((name, (args[i].data_ptr(), stream.cuda_stream) in recorded) for i in own)
+        return call
+
+    for name, own in (("paged_kv_append", (2,)), ("paged_kv_append_scaled", (2,)), ("paged_rope_append", (3, 4)),
+                      ("paged_block_copy", (2,)), ("paged_attention_decode", (3, 4)),
+                      ("paged_attention_decode_scaled", (5, 6))):
+        monkeypatch.setattr(cache_mod, name, launched(name, *own))
+    cache = cache_mod.PagedKVCache(8, 2, 16, 64, device="cpu", block_scales=kind == "scaled")
+    cache.add_sequence(0, 5)
+    cache.fork(0, 1)
+    x = torch.zeros(2, 2, 64, dtype=torch.bfloat16)
+    s = _at(7)
+    cache.append([0, 1], x, x, stream=s)  # with a copy-on-write copy
+    cache.rope_append([0, 1], x, x, x, torch.ones(32), stream=s)
+    cache.decode([0, 1], x, 0.1, stream=s)
+    assert len(used) == 6 and all(ok for _, ok in used), used
+    assert {h for _, h in recorded} == {7}
