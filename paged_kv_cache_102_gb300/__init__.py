@@ -155,6 +155,19 @@ def _torch_stream(stream, device) -> torch.cuda.Stream:
     return stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(stream.cuda_stream, device)
 
 
+def _output(stream, device, shape, dtype, zero=False) -> torch.Tensor:
+    """A new output of a call on `stream` (default: the current one).  It is allocated there, so that no work of the
+    current stream still holds its bytes, and marked as used on the current stream, where its reader may be."""
+    make = torch.zeros if zero else torch.empty
+    if stream is None:
+        return make(shape, dtype=dtype, device=device)
+    reader = torch.cuda.current_stream(device)
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        t = make(shape, dtype=dtype, device=device)
+    t.record_stream(reader)
+    return t
+
+
 def _workspace(device, stream, nbytes: int, kind: int = 0) -> torch.Tensor:
     """A reusable workspace per (device, stream) and kind of call: calls on one stream are ordered.  It is allocated on
     the stream that uses it (default: the current one), so that a smaller one that it replaces is not handed out again
@@ -195,7 +208,7 @@ def _decode_args(q, k_cache, v_cache, block_tables, context_lens, scale, out, k_
     if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
         raise ValueError("paged_attention_decode: block_tables [B, max_blocks], context_lens [B]")
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(stream, q.device, q.shape, q.dtype)
     elif out.shape != q.shape or out.dtype != q.dtype:
         raise ValueError("paged_attention_decode: out must match q")
     _require_out(q.device, out)
@@ -237,7 +250,7 @@ def _decode_append_args(q, k_new, v_new, slot_mapping, k_cache, v_cache, block_t
     if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
         raise ValueError("paged_attention_decode_append: block_tables and context_lens must be int32")
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(stream, q.device, q.shape, q.dtype)
     _require_out(q.device, out)
     _require_cuda(q.device, q=q, k_new=k_new, v_new=v_new, slot_mapping=slot_mapping, k_cache=k_cache,
                   v_cache=v_cache, block_tables=block_tables, context_lens=context_lens, k_scale=k_scale,
@@ -316,7 +329,7 @@ def quest_block_minmax(k_cache, block_tables, context_lens, kmeta=None, stream=N
         meta_dtype = kmeta.dtype if kmeta is not None else (
             torch.bfloat16 if _code(k_cache) == E4M3 else k_cache.dtype)
     if kmeta is None:
-        kmeta = torch.zeros(NB, Hkv, 2, D, dtype=meta_dtype, device=k_cache.device)
+        kmeta = _output(stream, k_cache.device, (NB, Hkv, 2, D), meta_dtype, zero=True)
     if kmeta.dtype != meta_dtype:
         raise ValueError("quest_block_minmax: kmeta must be of meta_dtype")
     _require_cuda(k_cache.device, k_cache=k_cache, block_tables=block_tables, context_lens=context_lens, kmeta=kmeta)
@@ -342,9 +355,9 @@ def quest_select(q, kmeta, block_tables, context_lens, block_size, budget_blocks
     B, Hq, D = q.shape
     NB, Hkv = kmeta.shape[0], kmeta.shape[1]
     if sel_tables is None:
-        sel_tables = torch.empty(B, Hkv, budget_blocks, dtype=torch.int32, device=q.device)
+        sel_tables = _output(stream, q.device, (B, Hkv, budget_blocks), torch.int32)
     if sel_lens is None:
-        sel_lens = torch.empty(B, Hkv, dtype=torch.int32, device=q.device)
+        sel_lens = _output(stream, q.device, (B, Hkv), torch.int32)
     _require_cuda(q.device, q=q, kmeta=kmeta, block_tables=block_tables, context_lens=context_lens,
                   sel_tables=sel_tables, sel_lens=sel_lens, workspace=workspace)
     s = _stream(stream, q.device)
@@ -363,7 +376,7 @@ def paged_attention_decode_sparse(q, k_cache, v_cache, sel_tables, sel_lens, sca
     B, Hq, D = q.shape
     NB, Hkv, bs, _ = k_cache.shape
     if out is None:
-        out = torch.empty_like(q)
+        out = _output(stream, q.device, q.shape, q.dtype)
     _require_out(q.device, out)
     _require_cuda(q.device, q=q, k_cache=k_cache, v_cache=v_cache, sel_tables=sel_tables, sel_lens=sel_lens,
                   k_scale=k_scale, v_scale=v_scale, workspace=workspace)
@@ -469,7 +482,7 @@ def paged_extend_tables(block_tables, context_lens, new_lens, free_blocks, free_
 
     def output(t, n, dtype, what):
         if t is None:
-            return torch.empty(n, dtype=dtype, device=device)
+            return _output(stream, device, (n,), dtype)
         if t.dtype is not dtype or t.shape != (n,):
             raise ValueError(f"{name}: {what} must be {dtype} [{n}]")
         return t
@@ -586,7 +599,7 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
             raise ValueError(f"{name}: q must be [num_tokens, num_q_heads, head_dim] of k's type")
         Hq = qshape[1]
         if q_out is None:
-            q_out = torch.empty(qshape, dtype=q.dtype, device=device)
+            q_out = _output(stream, device, qshape, q.dtype)
         elif q_out.shape != qshape or q_out.dtype != q.dtype:
             raise ValueError(f"{name}: q_out must match q")
         qs, os = _rows(name, "q", q, index, qshape), _rows(name, "q_out", q_out, index, qshape)
@@ -652,7 +665,7 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
         raise ValueError(f"{name}: block_tables [B, max_blocks], context_lens [B]")
     device = k_cache.device
     if out is None:
-        out = torch.empty(qshape, dtype=q.dtype, device=device)
+        out = _output(stream, device, qshape, q.dtype)
     elif out.shape != qshape or out.dtype != q.dtype:
         raise ValueError(f"{name}: out must match q")
     if not q.is_cuda:

@@ -22,16 +22,21 @@ class _Streams:
             def __exit__(self, *exc):
                 outer.current = self.before
 
-        real_empty = torch.empty
+        self.recorded = []
 
-        def empty(*size, device=None, **kw):
-            t = real_empty(*size, **kw)
-            outer.allocated.append((outer.current, t))
-            return t
+        def on_the_host(real):
+            def make(*size, device=None, **kw):
+                t = real(*size, **kw)
+                outer.allocated.append((outer.current, t))
+                return t
+            return make
 
         monkeypatch.setattr(torch.cuda, "stream", Context)
         monkeypatch.setattr(torch.cuda, "ExternalStream", lambda handle, device=None: _at(handle))
-        monkeypatch.setattr(torch, "empty", empty)
+        monkeypatch.setattr(torch, "empty", on_the_host(torch.empty))
+        monkeypatch.setattr(torch, "zeros", on_the_host(torch.zeros))
+        monkeypatch.setattr(torch.Tensor, "record_stream",
+                            lambda t, s: outer.recorded.append((t.data_ptr(), s.cuda_stream)))
         monkeypatch.setattr(torch._C, "_cuda_isCurrentStreamCapturing", lambda: self.current in self.capturing,
                             raising=False)
         monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda index: self.current, raising=False)
@@ -44,16 +49,22 @@ def streams(monkeypatch, pkv_lib):
     return _Streams(monkeypatch)
 
 
-def _sparse_decode(pkv, monkeypatch, stream, blocks=4):
-    """The workspace that a call on `stream` passes to the library: any call of the binding will do."""
+def _calls(pkv, monkeypatch):
+    """The library's calls from now on, which are not made, with CPU tensors let through."""
     seen = []
     monkeypatch.setattr(pkv._native, "call", lambda func, *args: seen.append(args))
-    monkeypatch.setattr(pkv, "_require_cuda", lambda *a, **k: None)
-    monkeypatch.setattr(pkv, "_require_out", lambda *a, **k: None)
-    q = torch.zeros(2, 8, 64, dtype=torch.bfloat16)
-    kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
-    pkv.paged_attention_decode_sparse(q, kc, kc, torch.zeros(2, 2, blocks, dtype=torch.int32),
-                                      torch.zeros(2, 2, dtype=torch.int32), 0.1, out=q, stream=stream)
+    for check in ("_require_cuda", "_require_out"):
+        monkeypatch.setattr(pkv, check, lambda *a, **k: None)
+    return seen
+
+
+def _sparse_decode(pkv, monkeypatch, stream, blocks=4):
+    """The workspace that a call on `stream` passes to the library: any call of the binding will do."""
+    seen = _calls(pkv, monkeypatch)
+    q = torch.ones(2, 8, 64, dtype=torch.bfloat16)
+    kc = torch.ones(4, 2, 16, 64, dtype=torch.bfloat16)
+    pkv.paged_attention_decode_sparse(q, kc, kc, torch.ones(2, 2, blocks, dtype=torch.int32),
+                                      torch.ones(2, 2, dtype=torch.int32), 0.1, out=q, stream=stream)
     return seen[0][-3]
 
 
@@ -89,6 +100,47 @@ def test_a_replaced_workspace_belongs_to_its_stream(streams, pkv_lib, monkeypatc
     large = run(2, 4000)
     assert large != small and run(2, 40) == large and run(3, 4) != large
     assert [h for h, _ in streams.allocated] == [2, 2, 3]
+
+
+def test_new_outputs_belong_to_the_given_stream(streams, pkv_lib, monkeypatch):
+    """Outputs that a call makes: bytes that the current stream's work may still hold are not the given stream's to
+    write, and zeros are written there too.  The current stream, which reads them, is recorded."""
+    _calls(pkv_lib, monkeypatch)
+    streams.current = 1
+    q = torch.ones(2, 8, 64, dtype=torch.bfloat16)
+    kc = torch.ones(4, 2, 16, 64, dtype=torch.bfloat16)
+    tables, lens = torch.ones(2, 4, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    outs = [pkv_lib.paged_attention_decode(q, kc, kc, tables, lens, 0.1, stream=_at(2)),
+            pkv_lib.paged_attention_decode_append(q, kc[:2, :, 0].contiguous(), kc[:2, :, 0].contiguous(), lens.long(),
+                                                  kc, kc, tables, lens, 0.1, stream=_at(2)),
+            pkv_lib.paged_attention_decode_sparse(q, kc, kc, torch.ones(2, 2, 4, dtype=torch.int32),
+                                                  torch.ones(2, 2, dtype=torch.int32), 0.1, stream=_at(2)),
+            pkv_lib.quest_block_minmax(kc, tables, lens, stream=_at(2)),
+            *pkv_lib.quest_select(q, torch.ones(4, 2, 2, 64), tables, lens, 16, 2, stream=_at(2))]
+    assert {h for h, _ in streams.allocated} == {2}
+    assert streams.recorded == [(t.data_ptr(), 1) for t in outs]
+    streams.allocated.clear()
+    pkv_lib.paged_attention_decode(q, kc, kc, tables, lens, 0.1)
+    assert {h for h, _ in streams.allocated} == {1}
+
+
+def test_new_outputs_of_the_step_calls(streams, pkv_lib, monkeypatch):
+    """The same of the calls whose checks need pointers on a device."""
+    streams.current = 1
+    monkeypatch.setattr(pkv_lib, "_pointers", lambda name, device, names, *t: [x.data_ptr() for x in t])
+    monkeypatch.setattr(pkv_lib, "_call_on", lambda *a: None)
+    monkeypatch.setattr(pkv_lib, "_rows", lambda *a: 0)
+    monkeypatch.setattr(pkv_lib, "_require_out", lambda *a: None)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda t: True))
+    q, s = torch.ones(2, 2, 64, dtype=torch.bfloat16), torch.ones(4, 2)
+    kc = torch.ones(4, 2, 16, 64, dtype=torch.uint8)
+    tables, lens = torch.ones(2, 4, dtype=torch.int32), torch.ones(2, dtype=torch.int32)
+    outs = [pkv_lib.paged_attention_decode_scaled(q, kc, kc, s, s, tables, lens, 0.1, stream=_at(2)),
+            pkv_lib.paged_rope_append(q, q, q, lens, lens.long(), torch.ones(32), kc, kc, k_scales=s, v_scales=s,
+                                      stream=_at(2)),
+            *pkv_lib.paged_extend_tables(tables, lens, lens, lens, lens[:1], 16, 4, num_tokens=2, stream=_at(2))]
+    assert {h for h, _ in streams.allocated} == {2}
+    assert streams.recorded == [(t.data_ptr(), 1) for t in outs]
 
 
 @pytest.mark.parametrize("kind", ["plain", "scaled"])
