@@ -447,10 +447,13 @@ int paged_extend_tables(int32_t* block_tables, int max_blocks_per_seq, const int
  * block's other codes become e4m3(code * (scale / new)), so they keep their
  * values (power-of-two scales: exactly, but for codes that turn subnormal).
  * A scale that is not positive counts as none: the other codes stay.
- * Tokens of one block must be neighbours in the call, in slot order; two runs
- * of one block in one call race.  Negative slots are skipped, slots outside
- * the pool are skipped and flag PKV_DEV_BAD_SLOT.  head_dim: a multiple of 8,
- * at most 256; block_size from 1 to 2^20.
+ * Negative slots are skipped, slots outside the pool are skipped and flag
+ * PKV_DEV_BAD_SLOT.  Several runs of one block (skipped tokens or slots left out
+ * between them, slots out of order or twice) apply one after the other, in the
+ * call's order.  For that the block's tokens must follow one another in the call
+ * with at most 255 skipped ones between two of them, and the one at offset 0, if
+ * any, must be the first; else the block's runs race.  head_dim: a multiple of
+ * 8, at most 256; block_size from 1 to 2^20.
  */
 int paged_kv_append_scaled(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
                            const int64_t* slot_mapping, int num_tokens, void* k_cache, void* v_cache,

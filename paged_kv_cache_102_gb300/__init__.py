@@ -553,8 +553,8 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
     The first 2 * len(inv_freq) channels turn, paired (i, i + half) or interleaved (2i, 2i + 1).  q, k, v may be
     parts of one projection's output (rows contiguous, token strides of their own).  The cache is of q's type, or
     E4M3 with k_scale, v_scale (one each) or k_scales, v_scales (block-scaled: tokens of one block must be neighbours
-    in the call, in slot order).  A negative position marks a padding row, a negative slot a token that is not stored.
-    q may be None (keys alone)."""
+    in the call, but for up to 255 skipped ones, the one at offset 0 first).  A negative position marks a padding row,
+    a negative slot a token that is not stored.  q may be None (keys alone)."""
     name = "paged_rope_append"
     kshape, cshape = k.shape, k_cache.shape
     device = k.device
@@ -617,7 +617,7 @@ def paged_kv_append_scaled(k, v, slot_mapping, k_cache, v_cache, k_scales, v_sca
 
     The scale of a (block, kv head) is the least power of two that holds its largest element; a later token that
     needs a larger one moves the block's codes along.  A token at offset 0 starts its block afresh.  Tokens of one
-    block must be neighbours in the call, in slot order."""
+    block must be neighbours in the call, but for up to 255 skipped ones, the one at offset 0 first."""
     name = "paged_kv_append_scaled"
     kshape = k.shape
     device = k_cache.device

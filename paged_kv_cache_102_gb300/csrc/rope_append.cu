@@ -16,7 +16,8 @@
 // turn is split off in integers and sincospi runs on the rest.
 //
 // Block scales: a "run" is a maximal stretch of consecutive tokens of the call
-// with consecutive slots of one block.  For a run at offset o of its block and
+// with consecutive slots of one block.  Runs of one block apply in the call's
+// order (split_runs).  For a run at offset o of its block and
 // one kv head, K and V alike:
 //   need = the least power of two 2^e, -64 <= e <= 120, with max|x| <= 448 * 2^e
 //   new  = o == 0 ? need : max(old, need)
@@ -614,12 +615,138 @@ __device__ __forceinline__ void single_rows(const RopeAppendParams& p, int t0, i
     }
 }
 
+// ---------------------------------------------------------------------------
+// Blocks whose tokens are not one run: skipped tokens between them, slots left
+// out, out of order or twice.  Their runs apply one after the other, in the
+// call's order, by the warps that have the first one; at most kReach - 1 skipped
+// tokens lie before a later one, and a token at offset 0 starts afresh.  The
+// common path only asks small functions about them (prompts, whose registers are
+// short: only sees that there may be such a run) and leaves as the last thing it
+// does: the work in its middle cost prompts 4 to 8 us of 40.  The questions cost
+// them 1 us of 39 and 2 of 125; a step of 8 tokens and 504 padding rows behind
+// them takes 4.2 us instead of 2.8, a step without padding no more than before.
+// ---------------------------------------------------------------------------
+constexpr int kReach = 256;
+
+// The nearest token that is stored among `from`, from + step, ... (kReach of
+// them); -1 if there is none.  Every lane of the warp calls it.
+__device__ __noinline__ int nearest_stored(const RopeAppendParams& p, int from, int step) {
+    constexpr int B = kReach / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t limit = static_cast<int64_t>(p.num_blocks) * p.block_size;
+    int64_t slots[B];
+#pragma unroll
+    for (int j = 0; j < B; ++j) {  // all loads on their way before any is used
+        const int t = from + step * (32 * j + lane);
+        slots[j] = t >= 0 && t < p.num_tokens ? p.slot_mapping[t] : -1;
+    }
+#pragma unroll
+    for (int j = 0; j < B; ++j) {
+        const int t = from + step * (32 * j + lane);
+        const bool stored = slots[j] >= 0 && slots[j] < limit && !(p.positions && p.positions[t] < 0);
+        const unsigned any = __ballot_sync(0xffffffffu, stored);
+        if (any) return from + step * (32 * j + __ffs(any) - 1);
+    }
+    return -1;
+}
+
+// Whether the slot is one of the block's that starts at slot b: any (first = 0)
+// or any but the first (1).
+__device__ __forceinline__ bool in_block(const RopeAppendParams& p, int64_t slot, int64_t b, int first) {
+    return slot >= b + first && slot < b + p.block_size;
+}
+
+// Whether the nearest token before t that is stored lies in the block at slot b.
+__device__ __noinline__ bool block_before(const RopeAppendParams& p, int t, int64_t b) {
+    bool unused = false;
+    t = nearest_stored(p, t - 1, -1);
+    return t >= 0 && in_block(p, slot_of(p, t, &unused), b, 0);
+}
+
+// The next run of the block at slot b at token t or after it: its first token,
+// -1 if there is none.
+__device__ __noinline__ int later_run(const RopeAppendParams& p, int t, int64_t b) {
+    bool unused = false;
+    t = t < p.num_tokens ? nearest_stored(p, t, 1) : -1;
+    return t >= 0 && in_block(p, slot_of(p, t, &unused), b, 1) ? t : -1;
+}
+
+// Slot s0 at token t0 and the n - 1 tokens after it are a run that may go on: its
+// length.  `open`: whether a later run of its block may follow, as far as the
+// tokens read here tell.
+__device__ __forceinline__ int run_length(const RopeAppendParams& p, int t0, int64_t s0, int off0, int n, bool& open) {
+    const int lane = threadIdx.x & 31;
+    while (true) {
+        bool unused = false;
+        const int64_t s = slot_of(p, t0 + n + lane, &unused);
+        const bool in = n + lane < p.block_size - off0 && s == s0 + n + lane;
+        const unsigned out = __ballot_sync(0xffffffffu, !in);
+        const unsigned closed = __ballot_sync(0xffffffffu, t0 + n + lane >= p.num_tokens ||
+                                                               (s >= 0 && !in_block(p, s, s0 - off0, 1)));
+        const int k = out ? __ffs(out) - 1 : 32;
+        n += k;
+        if (out) {
+            open = !(closed >> k & 1);
+            return n;
+        }
+    }
+}
+
+// The runs of the block whose first run starts at token t0, one after the other:
+// block `part` of `split` takes its share of the (head, K or V) items, a warp the
+// same ones of every run, so that it finds the codes and scales of the run before.
+template <int ACT, int PAIRS>
+__device__ __noinline__ void split_runs(const RopeAppendParams& p, int t0, int part, int split) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int lpr = p.head_dim / 8, rp = 32 / lpr;
+    const int r = lane / lpr, c = lane - r * lpr;
+    const bool idle = r >= rp;
+    bool unused = false;
+    int64_t s0 = slot_of(p, t0, &unused), blk;
+    int off0;
+    divmod_u(s0, p.block_size, blk, off0);
+    const int64_t b = s0 - off0;
+    while (true) {
+        const int n = run_length(p, t0, s0, off0, 1, unused);
+        for (int it = part * kWarps + warp; it < 2 * p.num_kv_heads; it += split * kWarps) {
+            const bool is_k = it < p.num_kv_heads;
+            const int head = is_k ? it : it - p.num_kv_heads;
+            const int64_t tile = blk * p.num_kv_heads + head;
+            RunRows run;
+            run.stride = is_k ? p.k_stride : p.v_stride;
+            run.src = static_cast<const uint16_t*>(is_k ? p.k : p.v) + t0 * run.stride + head * p.head_dim;
+            run.scale = (is_k ? p.k_scales : p.v_scales) + tile;
+            run.tile = static_cast<uint8_t*>(is_k ? p.k_cache : p.v_cache) + tile * p.block_size * p.head_dim;
+            run.positions = is_k && PAIRS != kPairsNone ? p.positions + t0 : nullptr;
+            const float old = off0 == 0 ? 0.f : *run.scale;
+            const float now = new_scale(run_top<ACT, PAIRS>(p, run, n, r, rp, c, idle), old);
+            run_codes<ACT, PAIRS>(p, run, n, off0, r, rp, c, idle, now);
+            __syncwarp();  // every lane has read the old scale
+            if (now != old) {
+                if (lane == 0) *run.scale = now;
+                if (old > 0.f) requantise(run.tile, p.block_size, lpr, off0, n, __fdiv_rn(old, now), lane, 32);
+            }
+        }
+        __syncwarp();  // before the next run's reads
+        t0 = later_run(p, t0 + n, b);
+        if (t0 < 0) return;
+        s0 = slot_of(p, t0, &unused);
+        off0 = static_cast<int>(s0 - b);
+    }
+}
+
+template <int ACT, int PAIRS, int GROUP, int W>
+__device__ __noinline__ void careful_block(const RopeAppendParams& p, int window, int w, int from, int part, int split,
+                                           float* table);
+
 // Runs that start in window w of `window` < 32 tokens: block `part` of `split`
 // takes its share of each run's (head, K or V) items.  cos and sin of the run's
-// tokens are computed once into shared memory.
-template <int ACT, int PAIRS, int GROUP, int W>
+// tokens are computed once into shared memory.  CAREFUL: of the tokens from
+// `from` on, where a block's tokens may be several runs.  GROUP == 1: windows of
+// one token.
+template <int ACT, int PAIRS, int GROUP, int W, bool CAREFUL = false>
 __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int window, int w, int part, int split,
-                                             float* table) {
+                                             float* table, int from = 0) {
     __shared__ float tops2[2 * kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int lpr = p.head_dim / 8;
@@ -628,30 +755,43 @@ __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int wind
     const int first = w * window;
     bool bad = false;
     const int64_t slot = slot_of(p, first - 1 + lane, &bad);
-    if (bad && lane >= 1 && lane <= window && warp == 0 && part == 0) atomicOr(p.err, kErrBadSlot);
+    if (!CAREFUL && bad && lane >= 1 && lane <= window && warp == 0 && part == 0) atomicOr(p.err, kErrBadSlot);
     int64_t blk = 0;
     int off = 0;
     if (slot >= 0) divmod_u(slot, p.block_size, blk, off);
-    // joined: the token continues the run of the one before it
+    // joined: the token continues the run of the one before it; close: it comes, inside a block, behind
+    // a token of the block or a skipped one
     const int64_t prev = __shfl_up_sync(0xffffffffu, slot, 1);
+    const int block = slot >= 0 ? static_cast<int>(blk) : -1, prev_block = __shfl_up_sync(0xffffffffu, block, 1);
     const unsigned joined = __ballot_sync(0xffffffffu, lane > 0 && slot >= 0 && prev == slot - 1 && off != 0);
-    const unsigned in_window = __ballot_sync(0xffffffffu, lane >= 1 && lane <= window && slot >= 0);
-    for (unsigned leaders = in_window & ~joined; leaders; leaders &= leaders - 1) {
-        const int at = __ffs(leaders) - 1;
+    const unsigned close = __ballot_sync(
+        0xffffffffu, off != 0 && first + lane > 1 && (prev_block == block || prev_block < 0));
+    const unsigned starts = __ballot_sync(0xffffffffu, lane > 0 && slot >= 0) & ~joined;
+    constexpr bool STEP = GROUP == 1;  // windows of one token
+    if (!CAREFUL && !STEP && (close & starts))
+        return careful_block<ACT, PAIRS, GROUP, W>(p, window, w, first, part, split, table);
+    unsigned leaders = starts & (STEP ? 2u : (2u << window) - 2);
+    if (CAREFUL) leaders &= ~0u << (from - first + 1);
+    for (; leaders; leaders = STEP ? 0u : leaders & (leaders - 1)) {
+        const int at = STEP ? 1 : __ffs(leaders) - 1;
         const int t0 = first - 1 + at;
         const int64_t s0 = __shfl_sync(0xffffffffu, slot, at), b0 = __shfl_sync(0xffffffffu, blk, at);
         const int off0 = __shfl_sync(0xffffffffu, off, at);
+        if ((CAREFUL || STEP) && (close >> at & 1) && block_before(p, t0, s0 - off0)) continue;  // a later run
         // the run's length: the lanes joined after it, and further where it reaches the last lane
         const unsigned after = at < 31 ? ~(joined >> (at + 1)) : ~0u;
         int n = 1 + min(__ffs(after) - 1, 31 - at);
-        if (at + n == 32) {
-            for (bool more = n < p.block_size - off0; more;) {
-                bool unused = false;
-                const bool in = n + lane < p.block_size - off0 && slot_of(p, t0 + n + lane, &unused) == s0 + n + lane;
-                const unsigned out = __ballot_sync(0xffffffffu, !in);
-                n += out ? __ffs(out) - 1 : 32;
-                more = out == 0;
+        bool open = !(starts >> at >> 1) && t0 + n < p.num_tokens;  // what starts next is not held
+        if (at + n == 32) n = run_length(p, t0, s0, off0, n, open);
+        if constexpr (CAREFUL) {
+            if (later_run(p, t0 + n, s0 - off0) >= 0) {
+                split_runs<ACT, PAIRS>(p, t0, part, split);
+                continue;
             }
+        } else if (STEP ? (open || (close & starts & ~3u)) && later_run(p, t0 + n, s0 - off0) >= 0 : open) {
+            // (if not a step: the window's last leader)
+            if constexpr (STEP) return split_runs<ACT, PAIRS>(p, t0, part, split);
+            else return careful_block<ACT, PAIRS, GROUP, W>(p, window, w, t0, part, split, table);
         }
         if constexpr (PAIRS != kPairsNone) {
             // the rows that a run of GROUP passes has (at most kTable holds them)
@@ -688,6 +828,12 @@ __device__ __forceinline__ void scaled_block(const RopeAppendParams& p, int wind
     }
 }
 
+template <int ACT, int PAIRS, int GROUP, int W>
+__device__ __noinline__ void careful_block(const RopeAppendParams& p, int window, int w, int from, int part, int split,
+                                           float* table) {
+    scaled_block<ACT, PAIRS, GROUP, W, true>(p, window, w, part, split, table, from);
+}
+
 // Items (token, part of its rows) of block `cta`, one a warp: at most kWarps tokens.
 template <int ACT, int CACHE, int PAIRS>
 __device__ __forceinline__ void rows_block(const RopeAppendParams& p, int cta, int parts, int per, int rows, float* table) {
@@ -721,7 +867,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_rows_kernel(const RopeApp
 }
 
 // Prompts: runs of many tokens.  What bounds it is instructions (59 % of the
-// issue slots, a quarter of the memory's rate; 42 us for 17,700 tokens of 2 x 8
+// issue slots, a quarter of the memory's rate; 44 us for 17,700 tokens of 2 x 8
 // heads, rotated).  The queries' rows follow in a launch of their own that
 // starts as these blocks drain (88 us, 6.6 TB/s): one grid that mixes both kinds
 // of blocks took 130 us instead of 125, the rows having fewer blocks a SM there.
