@@ -23,7 +23,6 @@ each block and kv head (k_scales, v_scales [num_blocks, num_kv_heads]).
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 import functools
 import math
@@ -291,14 +290,9 @@ class DecodePlan:
             if any(given) or k_scale is not None or v_scale is not None:
                 raise ValueError("DecodePlan: k_scales and v_scales go with neither an append nor k_scale, v_scale")
             self.func = "paged_attention_decode_scaled"
-            if workspace is None:  # the plan's own, so that graphs of two plans may run at once
-                need = workspace_size(q.shape[0], q.shape[1], k_cache.shape[1], q.shape[2], block_tables.shape[1],
-                                      k_cache.shape[2], partition_size, True)
-                with contextlib.nullcontext() if stream is None else torch.cuda.stream(
-                        _torch_stream(stream, k_cache.device)):
-                    workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=k_cache.device)
             self._args, self.out, ws = _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables,
-                                                           context_lens, scale, out, partition_size, workspace, stream)
+                                                           context_lens, scale, out, partition_size, workspace, stream,
+                                                           own_workspace=True)
         elif all(given):
             self.func = "paged_attention_decode_append"
             self._args, self.out, ws = _decode_append_args(q, k_new, v_new, slot_mapping, k_cache, v_cache,
@@ -650,8 +644,9 @@ def _scaled_workspace_size(*sizes):  # a function of the sizes alone
 
 
 def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, scale, out,
-                        partition_size, workspace, stream):
-    """Validated C arguments of paged_attention_decode_scaled, the output and the workspace."""
+                        partition_size, workspace, stream, own_workspace=False):
+    """Validated C arguments of paged_attention_decode_scaled, the output and the workspace (own_workspace: not the
+    stream's reusable one, so that graphs of two plans may run at once)."""
     name = "paged_attention_decode_scaled"
     NB, Hkv, bs, D = _require_scales(name, k_cache, v_cache, k_scales, v_scales)
     qshape = q.shape
@@ -674,7 +669,9 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
     s = _stream(stream, device)
     if workspace is None:
         need = _scaled_workspace_size(B, Hq, Hkv, D, tshape[1], bs, partition_size)
-        workspace = _workspace(device, stream, max(need, 1))  # (0: an argument that the library refuses)
+        need = max(need, 1)  # (0: an argument that the library refuses)
+        workspace = (_output(stream, device, (need,), torch.uint8) if own_workspace
+                     else _workspace(device, stream, need))
     qp, kc, vc, s1, s2, tables, lens, ws = _pointers(
         name, device, "q k_cache v_cache k_scales v_scales block_tables context_lens workspace", q, k_cache, v_cache,
         k_scales, v_scales, block_tables, context_lens, workspace)

@@ -1,0 +1,21 @@
+"""Refusals of the block-scaled calls' binding beside those of the library, on the CPU."""
+import pytest
+import torch
+
+
+def _tensors():
+    s, kc = torch.zeros(4, 2), torch.zeros(4, 2, 16, 64, dtype=torch.uint8)
+    return (torch.zeros(3, 2, 64, dtype=torch.bfloat16), kc, s, torch.zeros(3, 1, dtype=torch.int32),
+            torch.zeros(3, dtype=torch.int32))
+
+
+def test_plan_refuses_shapes_like_the_call(pkv_lib):
+    """Tensors of another rank: the call's own error, not one of the plan's on its way to a workspace."""
+    q, kc, s, tables, lens = _tensors()
+    for kw in (dict(q=q[0]), dict(tables=tables[:, 0]), dict(kc=kc[0]), dict(lens=lens[:2])):
+        a = dict(q=q, kc=kc, tables=tables, lens=lens)
+        a.update(kw)
+        with pytest.raises(ValueError, match="paged_attention_decode_scaled"):
+            pkv_lib.paged_attention_decode_scaled(a["q"], a["kc"], a["kc"], s, s, a["tables"], a["lens"], 0.1)
+        with pytest.raises(ValueError, match="paged_attention_decode_scaled"):
+            pkv_lib.DecodePlan(a["q"], a["kc"], a["kc"], a["tables"], a["lens"], 0.1, k_scales=s, v_scales=s)
