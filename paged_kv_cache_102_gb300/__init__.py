@@ -306,9 +306,14 @@ class DecodePlan:
         self._tensors = (q, k_cache, v_cache, block_tables, context_lens, k_scale, v_scale, ws, k_new, v_new,
                          slot_mapping, k_scales, v_scales)
         self._fn = _native.function(self.func)
+        self._device = k_cache.device
 
     def run(self):
-        code = self._fn(*self._args)
+        if self._device.index == torch._C._cuda_getDevice():
+            code = self._fn(*self._args)
+        else:  # the library launches on the current device
+            with torch.cuda.device(self._device):
+                code = self._fn(*self._args)
         if code != 0:
             _native.check(self.func, code)
         return self.out

@@ -19,3 +19,29 @@ def test_plan_refuses_shapes_like_the_call(pkv_lib):
             pkv_lib.paged_attention_decode_scaled(a["q"], a["kc"], a["kc"], s, s, a["tables"], a["lens"], 0.1)
         with pytest.raises(ValueError, match="paged_attention_decode_scaled"):
             pkv_lib.DecodePlan(a["q"], a["kc"], a["kc"], a["tables"], a["lens"], 0.1, k_scales=s, v_scales=s)
+
+
+def test_plan_runs_on_its_tensors_device(pkv_lib, monkeypatch):
+    """The device is the tensors', whichever is current; it is current again afterwards."""
+    current, at = [0], []
+
+    class Device:
+        def __init__(self, device):
+            self.index = device.index
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.index
+
+        def __exit__(self, *exc):
+            current[0] = self.before
+
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: current[0], raising=False)
+    plan = object.__new__(pkv_lib.DecodePlan)
+    plan.func, plan.out, plan._args, plan._device = "paged_attention_decode_scaled", None, (), torch.device("cuda", 1)
+    plan._fn = lambda *args: at.append(current[0]) or 0
+    plan.run()
+    assert at == [1] and current == [0]
+    current[0] = 1
+    plan.run()
+    assert at == [1, 1]
