@@ -33,6 +33,8 @@ class PagedKVCache:
         if block_scales:
             if k_scale is not None or v_scale is not None:
                 raise ValueError("PagedKVCache: k_scale, v_scale or block scales, not both")
+            if (k_scales is None) != (v_scales is None):
+                raise ValueError("PagedKVCache: k_scales and v_scales go together")
             dtype = torch.uint8
         self.num_blocks, self.num_kv_heads = num_blocks, num_kv_heads
         self.block_size, self.head_dim = block_size, head_dim

@@ -45,3 +45,11 @@ def test_plan_runs_on_its_tensors_device(pkv_lib, monkeypatch):
     current[0] = 1
     plan.run()
     assert at == [1, 1]
+
+
+def test_cache_refuses_half_a_pair_of_scales(pkv_lib):
+    """One kind of scales given: the other's pool would be read with scales of zero."""
+    from paged_kv_cache_102_gb300.cache import PagedKVCache
+    for kw in (dict(k_scales=torch.ones(4, 2)), dict(v_scales=torch.ones(4, 2), block_scales=True)):
+        with pytest.raises(ValueError, match="go together"):
+            PagedKVCache(4, 2, 16, 64, device="cpu", **kw)
