@@ -497,16 +497,28 @@ int paged_extend_tables(int32_t* block_tables, int max_blocks_per_seq, const int
         return fail(PKV_ERR_INVALID, F + "null pointer");
     if ((num_free > 0 && !free_blocks) || (num_tokens > 0 && (!slot_mapping || !positions)))
         return fail(PKV_ERR_INVALID, F + "null pointer");
+    // what is written (first) and read: written buffers share memory with no other, but for the two updated in place
+    const size_t B = num_seqs, T = num_tokens;
+    const struct { const void* at; size_t bytes; } buffers[] = {
+        {slot_mapping, 8 * T}, {positions, 4 * T}, {seq_starts, 4 * (B + 1)}, {block_starts, 4 * (B + 1)},
+        {block_tables, 4 * B * max_blocks_per_seq}, {context_lens_out, 4 * B}, {free_head_out, 4},
+        {context_lens, 4 * B}, {free_head, 4}, {new_lens, 4 * B}, {free_blocks, 4 * static_cast<size_t>(num_free)}};
+    for (int i = 0; i < 7; ++i) {
+        for (int j = i + 1; j < 11; ++j) {
+            const auto a = reinterpret_cast<uintptr_t>(buffers[i].at), b = reinterpret_cast<uintptr_t>(buffers[j].at);
+            const bool in_place = (i == 5 && j == 7) || (i == 6 && j == 8);
+            if (buffers[i].bytes && buffers[j].bytes && a < b + buffers[j].bytes && b < a + buffers[i].bytes &&
+                !(in_place && a == b))
+                return fail(PKV_ERR_INVALID, F + "outputs must be buffers of their own (context_lens_out may be "
+                                                 "context_lens, free_head_out may be free_head)");
+        }
+    }
     if (!aligned(slot_mapping, 16) || !aligned(positions, 16))
         return fail(PKV_ERR_INVALID, F + "slot_mapping and positions must be 16-byte aligned");
     if (!aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(new_lens, 4) || !aligned(free_blocks, 4) ||
         !aligned(free_head, 4) || !aligned(seq_starts, 4) || !aligned(block_starts, 4) ||
         !aligned(context_lens_out, 4) || !aligned(free_head_out, 4))
         return fail(PKV_ERR_INVALID, F + "int32 buffers must be 4-byte aligned");
-    if ((num_seqs > 0 && context_lens_out == new_lens) || free_head_out == seq_starts || free_head_out == block_starts ||
-        seq_starts == block_starts)
-        return fail(PKV_ERR_INVALID, F + "outputs must be buffers of their own (context_lens_out may be context_lens, "
-                                         "free_head_out may be free_head)");
     int* err = device_error_word();
     if (!err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
     ExtendParams p{block_tables, context_lens, new_lens, free_blocks, free_head, slot_mapping, positions, seq_starts,

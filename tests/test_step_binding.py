@@ -53,3 +53,33 @@ def test_cache_refuses_half_a_pair_of_scales(pkv_lib):
     for kw in (dict(k_scales=torch.ones(4, 2)), dict(v_scales=torch.ones(4, 2), block_scales=True)):
         with pytest.raises(ValueError, match="go together"):
             PagedKVCache(4, 2, 16, 64, device="cpu", **kw)
+
+
+def test_extend_refuses_buffers_that_overlap(pkv_lib):
+    """Every written buffer against every other one, by a few bytes; lengths and head may be updated in place.  (The
+    slots' alignment is refused after the overlaps, so that no call is enqueued.)"""
+    lib = pkv_lib._native.lib()
+    B, T, max_blocks, free = 5, 7, 3, 9
+    sizes = dict(tables=4 * B * max_blocks, ctx=4 * B, new=4 * B, free=4 * free, head=4, slots=8 * T, pos=4 * T,
+                 ss=4 * (B + 1), bst=4 * (B + 1), lens=4 * B, hout=4)
+    apart = {name: 0x10000 + 0x1000 * i + 8 * (name == "slots") for i, name in enumerate(sizes)}
+
+    def refusal(**kw):
+        a = {**apart, **kw}
+        code = lib.paged_extend_tables(a["tables"], max_blocks, a["ctx"], a["new"], B, 16, a["free"], free, a["head"], 64,
+                                       T, a["slots"], a["pos"], a["ss"], a["bst"], a["lens"], a["hout"], None)
+        assert code == pkv_lib.ERR_INVALID
+        return lib.pkv_last_error().decode()
+
+    assert "16-byte aligned" in refusal()
+    assert "16-byte aligned" in refusal(lens=apart["ctx"], hout=apart["head"])
+    assert "16-byte aligned" in refusal(ctx=apart["new"], head=apart["free"])  # both read
+    assert "16-byte aligned" in refusal(bst=apart["ss"] + sizes["ss"])         # next to one another
+    written = ("tables", "slots", "pos", "ss", "bst", "lens", "hout")
+    for w in written:
+        for other in sizes:
+            if other == w or (w, other) in (("lens", "ctx"), ("hout", "head")):
+                continue
+            assert "buffers of their own" in refusal(**{w: apart[other] + sizes[other] - 4}), (w, other)
+            assert "buffers of their own" in refusal(**{w: apart[other]}), (w, other)
+    assert "buffers of their own" in refusal(lens=apart["ctx"] + 4)
