@@ -478,7 +478,8 @@ int paged_kv_append_scaled(const void* k, int64_t k_stride, const void* v, int64
  *                 alone is written).
  *  inv_freq       float32 [rotary_dim/2] (device), finite.
  *  q_out          [num_tokens] rows of [num_q_heads][head_dim], q_out_stride
- *                 apart; may be q itself (same stride).  num_q_heads may be 0.
+ *                 apart; may be q itself (same stride), and shares no memory with
+                 other rows of q, k or v.  num_q_heads may be 0.
  *  cache_dtype    act_dtype; or PKV_E4M3 with k_scale and v_scale (one each, as
  *                 paged_kv_append), or with k_scales and v_scales (block-scaled,
  *                 as paged_kv_append_scaled).  The other two are NULL.

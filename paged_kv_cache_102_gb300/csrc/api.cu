@@ -575,6 +575,17 @@ int paged_kv_append_scaled(const void* k, int64_t k_stride, const void* v, int64
     return e == cudaSuccess ? PKV_OK : cuda_fail("paged_kv_append_scaled: launch", e);
 }
 
+// Whether two sets of num_tokens rows share memory (strides and row lengths in bytes; with different strides:
+// whether they may).
+static bool rows_overlap(const void* a, int64_t a_stride, int64_t a_row, const void* b, int64_t b_stride, int64_t b_row,
+                         int num_tokens) {
+    const auto x = reinterpret_cast<intptr_t>(a), y = reinterpret_cast<intptr_t>(b);
+    if (x >= y + (num_tokens - 1) * b_stride + b_row || y >= x + (num_tokens - 1) * a_stride + a_row) return false;
+    if (a_stride != b_stride || a_stride == 0 || num_tokens == 1) return true;
+    const intptr_t d = ((x - y) % a_stride + a_stride) % a_stride;  // a's columns behind b's
+    return d < b_row || d + a_row > a_stride;
+}
+
 int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
                       int64_t v_stride, const int32_t* positions, const int64_t* slot_mapping, int num_tokens,
                       const float* inv_freq, int rotary_dim, int interleaved, float attention_factor, void* q_out,
@@ -632,6 +643,13 @@ int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_
     if (!k || !v || !positions || !slot_mapping || !inv_freq || !k_cache || !v_cache ||
         (num_q_heads > 0 && (!q || !q_out)))
         return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (num_q_heads > 0) {
+        const int64_t q_row = 2LL * num_q_heads * head_dim, kv_row = 2LL * num_kv_heads * head_dim, qo = 2 * q_out_stride;
+        if ((q != q_out && rows_overlap(q_out, qo, q_row, q, 2 * q_stride, q_row, num_tokens)) ||
+            rows_overlap(q_out, qo, q_row, k, 2 * k_stride, kv_row, num_tokens) ||
+            rows_overlap(q_out, qo, q_row, v, 2 * v_stride, kv_row, num_tokens))
+            return fail(PKV_ERR_INVALID, F + "q_out may be q itself, but shares no memory with k, v or other rows of q");
+    }
     if (!aligned(q, 16) || !aligned(k, 16) || !aligned(v, 16) || !aligned(q_out, 16) || !aligned(k_cache, 16) ||
         !aligned(v_cache, 16) || !aligned(slot_mapping, 8) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
         !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(k_scales, 4) || !aligned(v_scales, 4))

@@ -66,8 +66,8 @@ def test_extend_refuses_buffers_that_overlap(pkv_lib):
 
     def refusal(**kw):
         a = {**apart, **kw}
-        code = lib.paged_extend_tables(a["tables"], max_blocks, a["ctx"], a["new"], B, 16, a["free"], free, a["head"], 64,
-                                       T, a["slots"], a["pos"], a["ss"], a["bst"], a["lens"], a["hout"], None)
+        code = lib.paged_extend_tables(a["tables"], max_blocks, a["ctx"], a["new"], B, 16, a["free"], free, a["head"],
+                                       64, T, a["slots"], a["pos"], a["ss"], a["bst"], a["lens"], a["hout"], None)
         assert code == pkv_lib.ERR_INVALID
         return lib.pkv_last_error().decode()
 
@@ -83,3 +83,27 @@ def test_extend_refuses_buffers_that_overlap(pkv_lib):
             assert "buffers of their own" in refusal(**{w: apart[other] + sizes[other] - 4}), (w, other)
             assert "buffers of their own" in refusal(**{w: apart[other]}), (w, other)
     assert "buffers of their own" in refusal(lens=apart["ctx"] + 4)
+
+
+def test_rope_append_refuses_queries_written_over_its_inputs(pkv_lib):
+    """q_out over other rows of q, over k or over v.  Beside them in one buffer it is let through, up to the refusal of
+    the cache's alignment, which comes last, so that no call is enqueued."""
+    lib = pkv_lib._native.lib()
+    A, T, hq, hkv, D = 1 << 20, 5, 4, 2, 64
+    row = (hq + 2 * hkv) * D  # one projection's output: [q | k | v]
+    K, V, far = A + 2 * hq * D, A + 2 * (hq + hkv) * D, A + (1 << 16)
+
+    def refusal(q=A, qs=row, k=K, ks=row, v=V, vs=row, qo=A, qos=row, T=T):
+        code = lib.paged_rope_append(q, qs, k, ks, v, vs, A, A, T, A, D, 0, 1.0, qo, qos, far + 2, far, 8, hq, hkv, 16,
+                                     D, 1, 1, None, None, None, None, None)
+        assert code == pkv_lib.ERR_INVALID
+        return lib.pkv_last_error().decode()
+
+    for ok in (dict(), dict(qo=far), dict(qo=far, qs=0, ks=0, vs=0), dict(qo=A + 2 * row * T),
+               dict(T=1, qo=K + 2 * row), dict(q=far, qo=A),
+               dict(q=A, qo=A + 2 * row, qos=2 * row, k=far, v=far, qs=2 * row)):
+        assert "16-byte aligned" in refusal(**ok), ok
+    for bad in (dict(qo=K), dict(qo=V), dict(qo=A + 16), dict(qo=A + 2 * row), dict(qo=A - 2 * row), dict(qo=K - 16),
+                dict(q=far, qo=A, qos=2 * row), dict(q=far, qo=V + 2 * hkv * D - 16), dict(q=far, qo=A, k=A, ks=0),
+                dict(T=1, qo=K), dict(T=1, qo=A + 16)):
+        assert "shares no memory" in refusal(**bad), bad
