@@ -7,6 +7,7 @@ import pytest
 import torch
 
 from tests import scaled_ref as ref
+from tests import test_gpu_rope as rope
 
 pytestmark = pytest.mark.gpu
 DT = {"f16": torch.float16, "bf16": torch.bfloat16}
@@ -108,3 +109,27 @@ def test_rotated_append_of_split_runs(pkv, case, rot, interleaved):
     torch.cuda.synchronize()
     for a, b in zip(one, many):
         assert torch.equal(a, b)
+
+
+LONG = [
+    # act, tokens, Hq, Hkv, D, rotary_dim, interleaved, bs, positions below, packed
+    ("bf16", 1400, 4, 2, 128, 128, False, 32, 9000, True),
+    ("f16", 1400, 2, 2, 128, 128, True, 32, 9000, True),
+    ("bf16", 1400, 2, 2, 128, 24, False, 32, 9000, True),
+    ("f16", 1700, 2, 1, 128, 128, False, 64, 70000, True),
+    ("bf16", 1700, 1, 1, 128, 64, True, 64, 70000, False),
+    ("f16", 1700, 1, 1, 128, 40, False, 64, 70000, False),
+    ("bf16", 1300, 2, 2, 128, 128, True, 16, 9000, True),
+    ("f16", 1300, 2, 2, 128, 72, False, 16, 9000, True),
+    ("bf16", 1300, 1, 1, 256, 256, False, 16, 9000, True),
+    ("f16", 1300, 2, 2, 80, 20, True, 32, 9000, True),
+    ("f16", 500, 4, 2, 128, 128, True, 16, 9000, True),
+    ("bf16", 800, 2, 5, 128, 56, False, 32, 9000, True),
+]
+
+
+@pytest.mark.parametrize("case", LONG, ids=lambda c: "-".join(map(str, c)))
+def test_rotated_prompts_in_every_layout(pkv, case):
+    """Prompts whose runs stay in registers and those whose rows are read twice, with two warps a run (more than about
+    1,200 tokens) and with one, for channels paired as neighbours, in whole chunks and apart."""
+    rope.test_rope_append_e4m3(pkv, case, True)
