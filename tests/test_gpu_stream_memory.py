@@ -109,3 +109,45 @@ def test_cache_steps_on_a_given_stream(pkv, kind):
 
     for a, b in zip(run(torch.cuda.Stream()), run(None)):
         assert torch.equal(a, b)
+
+
+def test_captured_calls_with_new_outputs_on_given_streams(pkv):
+    """Branches of one capture that make their own outputs and workspaces: rotation, tables and decode on streams
+    forked from the capturing one, read on the capturing one, and the same again in the next branches."""
+    a, b = _case(5, [40, 90, 7]), _case(6, [64, 3, 120])
+    freq, _ = pkv.rope_inv_freq(128)
+    q, k = (torch.randn(3, h, 128, device="cuda").to(torch.bfloat16) for h in (32, 4))
+    pos = torch.tensor([5, 70000, 3], dtype=torch.int32, device="cuda")
+    skip = torch.full((3,), -1, dtype=torch.int64, device="cuda")
+    one = torch.ones(3, dtype=torch.int32, device="cuda")
+    free, head = torch.arange(8, dtype=torch.int32, device="cuda"), torch.zeros(1, dtype=torch.int32, device="cuda")
+    tables = [torch.zeros(3, 4, dtype=torch.int32, device="cuda") for _ in range(2)]
+
+    def branch(args, t, s):
+        turned = pkv.paged_rope_append(q, k, k, pos, skip, freq, args[1], args[2], k_scales=args[3], v_scales=args[4],
+                                       stream=s)
+        out = pkv.paged_attention_decode_scaled(*args, stream=s)
+        ext = pkv.paged_extend_tables(t, one, one, free, head, 16, 8, num_tokens=5, stream=s)
+        return [turned, out, *ext]
+
+    want = [branch(x, t, None) for x, t in zip((a, b), tables)]
+    torch.cuda.synchronize()
+    main, s1, s2 = (torch.cuda.Stream() for _ in range(3))
+    graph = torch.cuda.CUDAGraph()
+    kept = []
+    with torch.cuda.graph(graph, stream=main):
+        for _ in range(2):
+            got = []
+            for s, args, t in ((s1, a, tables[0]), (s2, b, tables[1])):
+                s.wait_stream(main)
+                got.append(branch(args, t, s))
+            main.wait_stream(s1)
+            main.wait_stream(s2)
+            kept.append([[t.clone() for t in g] for g in got])
+            del got
+    for _ in range(5):
+        graph.replay()
+        torch.cuda.synchronize()
+        for pair in kept:
+            for g, w in zip(pair, want):
+                assert all(torch.equal(x, y) for x, y in zip(g, w))
