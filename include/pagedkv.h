@@ -462,7 +462,8 @@ int paged_kv_append_scaled(const void* k, int64_t k_stride, const void* v, int64
 
 /*
  * paged_rope_append -- rotary positions of queries and keys, and the append of
- * the rotated keys and of the values, in one launch.  Channels e < rotary_dim
+ * the rotated keys and of the values, in one launch (two for prompts into a
+ * block-scaled cache: the runs, then the queries).  Channels e < rotary_dim
  * of a head form pairs (a, b): (i, i + rotary_dim/2), or (2i, 2i + 1) if
  * interleaved != 0, i < rotary_dim/2.  At position pos a pair becomes
  *     (a cos t - b sin t, b cos t + a sin t) * attention_factor,  t = pos * inv_freq[i]
@@ -497,7 +498,9 @@ int paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_
  * E4M3 cache: K_b[j] = code * k_scales[block][kvh], likewise V, block =
  * block_tables[b][j / block_size].  Scales may be any finite float32 (a power of
  * two or not, 0, negative; V scales of one sequence within a factor 2^100 of
- * one another, else the smaller ones' part of the sum may be lost); products and sums as paged_attention_decode.  A
+ * one another, else the smaller ones' part of the sum may be lost).  Products are
+ * summed in float32; a softmax weight enters them with at least 14 bits (three
+ * E4M3 parts on the tensor cores), above what act_dtype's rounding keeps.  A
  * context length of 0 (a padding row) gives a row of zeros and no error bit.
  * The workspace is at least pkv_scaled_workspace_size(...) bytes; other
  * arguments as there.  The tensor-core kernel serves every group, both head_dims

@@ -547,7 +547,7 @@ def paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cac
                       attention_factor=1.0, q_out=None, k_scale=None, v_scale=None, k_scales=None, v_scales=None,
                       stream=None):
     """Rotate q [T, Hq, D] and k [T, Hkv, D] at positions int32 [T] and append the rotated keys and the values at
-    slot_mapping int64 [T], in one launch; returns the rotated queries (q_out, new by default, may be q).
+    slot_mapping int64 [T], in one call; returns the rotated queries (q_out, new by default, may be q).
 
     The first 2 * len(inv_freq) channels turn, paired (i, i + half) or interleaved (2i, 2i + 1).  q, k, v may be
     parts of one projection's output (rows contiguous, token strides of their own).  The cache is of q's type, or

@@ -363,11 +363,12 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
                                      "heads per kv head and partitions of at most 512 tokens (block-scaled "
                                      "caches: either head_dim, any group and partitions of at most 2^20 tokens)");
     // Block-scaled: short contexts and few rows take the CUDA-core kernel, whose
-    // one launch is over in 3 to 8 us where the tensor-core kernel's take 8 to 13
-    // (head_dim 128, 128 tokens, us: 4.9 / 8.7 for 16 x 8 rows of one query head,
-    // 8.1 / 9.1 for four, 11.9 / 12.1 for 16 x 32 of two; from there on the other
-    // way: 17.7 / 12.9 for 16 x 32 of four, 22.2 / 20.4 for 64 x 32 of one, and at
-    // eight query heads always: 12.7 / 8.7 for 8 rows of 32 tokens).
+    // one launch is over in 4 to 8 us where the tensor-core kernel takes 7 to 13
+    // (head_dim 128, 128 tokens, us: 5.2 / 7.5 for 16 x 8 rows of one query head,
+    // 12.0 / 12.3 for 16 x 32 of two; 8.4 / 7.8 for 16 x 8 of four, where the border
+    // could lie lower; from there on the other way: 17.7 / 12.9 for 16 x 32 of four,
+    // 22.2 / 20.4 for 64 x 32 of one, and at eight query heads always: 12.7 / 8.7 for
+    // 8 rows of 32 tokens).
     const bool small = block_scales && G <= 4 && max_ctx <= 256 &&
                        static_cast<long long>(num_seqs) * num_q_heads <= 1024;
     const bool use_tc = path == PKV_PATH_TENSOR || path == PKV_PATH_TENSOR_2CTA ||

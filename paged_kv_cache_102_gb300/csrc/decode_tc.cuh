@@ -94,9 +94,9 @@
 // The producer that converts q finds its power-of-2 scale too.  (Two groups of
 // softmax warps with four heads each were no faster at eight query heads: 81.3
 // against 80.3 us for 128 ragged sequences.)
-// Measured, of the 6.7 TB/s that a copy reaches: 64 sequences of 40 heads of
-// their own, 1.43 GB of codes, 205 us (104 %, the memory is the bound); 8 of 32K
-// tokens, four query heads, 87 us (92 %); 128 ragged ones, eight query heads, 77 us
+// Measured, of the 6.7 TB/s that a copy reaches (a kernel that only reads reaches
+// 7.3): 64 sequences of 40 heads of their own, 1.43 GB of codes, 203 to 205 us
+// (105 %, the memory is the bound); 8 of 32K tokens, four query heads, 86 us (93 %); 128 ragged ones, eight query heads, 77 us
 // (85 %) and at head_dim 64, binary16, 44 us (56 %): the launch's ramp, its tail
 // and the merge, and at head_dim 64 a segment's 64 KB, which pass faster than the
 // softmax warps' 3 us for it.

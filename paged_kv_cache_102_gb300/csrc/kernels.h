@@ -238,10 +238,9 @@ cudaError_t launch_decode_f16_e4m3b(const DecodeParams& p, int D, int BS, int G,
 cudaError_t launch_decode_bf16_e4m3b(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 
 // Tensor-core grouped-query path (head_dim 128 with a 16-bit or E4M3 cache
-// of either scaling,
-// or head_dim 64 with a 16-bit cache, an even kv-head count and shared
-// tables, or with a block-scaled cache; group 2/4/8, block-scaled also 1;
-// partitions of at most 512 tokens).  variant 0: one CTA per SM; variant 1:
+// of either scaling, or head_dim 64 with a 16-bit cache, an even kv-head count
+// and shared tables, or with a block-scaled cache; group 2/4/8, block-scaled
+// also 1; partitions of at most 512 tokens, block-scaled 2^20).  variant 0: one CTA per SM; variant 1:
 // two CTAs per SM (block-scaled: always two).
 bool decode_tc_supported(int head_dim, int block_size, int group, int act, int cache, int partition_size,
                          int num_kv_heads, bool per_kvh_tables);

@@ -436,7 +436,8 @@ __device__ __forceinline__ void run_row(const RopeAppendParams& p, const RunRows
 }
 
 // The largest finite element of the rows r, r + rp, ... of a run (one warp's).
-// For runs that do not fit the registers, and those with an infinity.
+// For runs that do not fit the registers: longer blocks, and in calls of up to about
+// 1,200 tokens (scaled_step_kernel) every run of more than a pass.
 template <int ACT, int PAIRS>
 __device__ __noinline__ float run_top(const RopeAppendParams& p, const RunRows run, int n, int r, int rp, int c, bool idle) {
     float top = 0.f;
@@ -866,7 +867,7 @@ __global__ void __launch_bounds__(kWarps * 32, 3) rope_rows_kernel(const RopeApp
     if (CACHE == kE4M3B) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
-// Prompts: runs of many tokens.  What bounds it is instructions (59 % of the
+// Prompts: runs of many tokens.  What bounds it is instructions (56 % of the
 // issue slots, a quarter of the memory's rate; 44 us for 17,700 tokens of 2 x 8
 // heads, rotated).  The queries' rows follow in a launch of their own that
 // starts as these blocks drain (88 us, 6.6 TB/s): one grid that mixes both kinds
