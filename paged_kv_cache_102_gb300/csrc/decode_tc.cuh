@@ -85,6 +85,9 @@
 // Against parts on one scale, two for bfloat16, whose outputs were 7e-4 (rms) off the
 // binary32 form's and are 1.1e-4 off it now: 128 ragged sequences of eight query heads
 // 75.2 -> 76.9 us, at head_dim 64 42.5 -> 44.4; a fourth part would make it 78.4 and 46.8.
+// (Eight heads pay most, other groups next to nothing: bfloat16, 512 sequences of four
+// kv heads at head_dim 64 44 -> 50 us; 1,024 at head_dim 128, whose lengths leave room
+// for three stages instead of four, 112 -> 125.)
 // An item may be longer than the 512 tokens whose scores tensor memory holds: the
 // scheduler passes it on as segments of 512, which the other roles take for items;
 // the softmax keeps each head's running maximum and sum, the epilogue the output
@@ -917,12 +920,18 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 
         auto issue_k = [&](const TcItem& it, int phys, int k) {
             // 16-bit: Q first (one TMA issue); E4M3: the K copies first, so that
-            // their latency covers the Q conversion
+            // their latency covers the Q conversion -- but only as many as the ring
+            // has stages: a further one waits for a stage that the S MMA of the
+            // item's own first tile frees, and that MMA waits for Q
             if (!FP8 && parity == 0 && !issue_q(it, k)) return false;
             if (FP8 && parity == 0) load_q(it);
-            for (int t = 0; t < it.n_tiles; ++t)
+            const int early = NS < kTcMaxTiles ? min(it.n_tiles, NS) : it.n_tiles;
+            for (int t = 0; t < early; ++t)
                 if (!issue_tile(use, parity, it, phys, t, &kmap)) return false;
-            return !FP8 || parity != 0 || issue_q(it, k);
+            if (FP8 && parity == 0 && !issue_q(it, k)) return false;
+            for (int t = early; t < it.n_tiles; ++t)
+                if (!issue_tile(use, parity, it, phys, t, &kmap)) return false;
+            return true;
         };
         TcItem cur, nxt;
         int phys_c = -1, phys_n = -1;
