@@ -385,6 +385,130 @@ int paged_attention_decode_sparse(const void* q, const void* k_cache, const void
                                   void* workspace, size_t workspace_bytes, void* stream);
 
 /* ------------------------------------------------------------------------
+ * Several new tokens a sequence, windows, and caches of bounded size.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * paged_attention_chunk -- attention of each sequence's new tokens over its
+ * cache, which holds them already (prompts, parts of prompts, drafted tokens,
+ * and batches of these and single tokens).  Sequence b has n = seq_starts[b + 1]
+ * - seq_starts[b] new tokens, rows seq_starts[b] .. of q and out; its
+ * context_lens[b] = L tokens count them.  Row i of the n has position p = L - n
+ * + i and sees the tokens j <= p; with a window (window > 0) only those with
+ * j > p - window or j < sinks:
+ *     out = sum_j softmax_j(scale <q, K[j]>) V[j]
+ * Weights are rounded to act_dtype for the product with V (their sum is not),
+ * everything else is held in float32, and out is rounded once.
+ *  q, out         [num_tokens] rows of [num_q_heads][head_dim] of act_dtype,
+ *                 q_stride / out_stride elements apart (multiples of 8); out
+ *                 shares no memory with q.
+ *  seq_starts     int32 [num_seqs + 1], as paged_extend_tables writes it; rows
+ *                 of out before seq_starts[0] and from seq_starts[num_seqs] on
+ *                 stay as they are.  A sequence without new tokens has no rows.
+ *  context_lens   int32 [num_seqs].
+ *  k_scale, v_scale, or k_scales, v_scales: an E4M3 cache's scales, one each or
+ *                 float32 [num_blocks][num_kv_heads].
+ *  workspace      pkv_chunk_workspace_size bytes, no initialisation needed.
+ * Up to 64 query heads per kv head; head_dim 64 or 128; block_size 16 or 32.
+ * Table entries of blocks that no row sees are not read.  Sequences with
+ * seq_starts that descend or leave 0 .. num_tokens, with fewer than n tokens or
+ * more than max_blocks_per_seq * block_size flag PKV_DEV_BAD_CONTEXT_LEN; their
+ * rows stay as they are.  Any two rows of the batch may share blocks.
+ */
+int paged_attention_chunk(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                          const int32_t* seq_starts, int num_seqs, int num_tokens, int num_q_heads,
+                          int num_kv_heads, int block_size, int head_dim, int num_blocks, float scale,
+                          int window, int sinks, void* out, int64_t out_stride, int act_dtype,
+                          int cache_dtype, const float* k_scale, const float* v_scale,
+                          const float* k_scales, const float* v_scales, void* workspace,
+                          size_t workspace_bytes, void* stream);
+
+/* Device workspace of paged_attention_chunk.  Host only. */
+size_t pkv_chunk_workspace_size(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                                int head_dim, int max_blocks_per_seq, int block_size);
+
+/*
+ * paged_attention_decode_window -- paged_attention_decode (or, with k_scales and
+ * v_scales, _scaled) of the sequence's last `window` tokens and its first
+ * `sinks` ones alone (window >= 1, the newest token among them; sinks >= 0): what
+ * a layer with a sliding window sees of a long context.  Its cost goes by window
+ * + sinks.  Table entries of blocks wholly between the two are not read, so
+ * their blocks may be freed; the hidden tokens beside visible ones in a block
+ * may hold anything.  A context length of 0 gives zeros.  The workspace is
+ * pkv_window_workspace_size bytes; partition_size counts tokens of the blocks
+ * that are left.
+ */
+int paged_attention_decode_window(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int max_blocks_per_seq,
+                                  const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                  int num_kv_heads, int block_size, int head_dim, int num_blocks,
+                                  float scale, int window, int sinks, void* out, int act_dtype,
+                                  int cache_dtype, const float* k_scale, const float* v_scale,
+                                  const float* k_scales, const float* v_scales, int partition_size,
+                                  void* workspace, size_t workspace_bytes, void* stream);
+
+/* Device workspace of paged_attention_decode_window.  Host only. */
+size_t pkv_window_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int max_blocks_per_seq, int block_size, int window, int sinks,
+                                 int block_scales, int partition_size);
+
+/*
+ * paged_attention_decode_scored -- paged_attention_decode that also adds each
+ * cached token's attention weight, summed over the query heads of its kv head,
+ * to scores (float32 [num_seqs][num_kv_heads][score_tokens], score_tokens >=
+ * max_blocks_per_seq * block_size): scores[b][h][j] += sum_g p_g[j] for j <
+ * context_lens[b], the others stay.  What paged_kv_evict goes by.  One thread
+ * adds a token's weight, in a fixed order.  A context length of 0 gives zeros
+ * and adds nothing.  Not for block-scaled caches.  The workspace,
+ * pkv_scored_workspace_size bytes, holds the step's logits (4 bytes for each
+ * query head and token of the tables).
+ */
+int paged_attention_decode_scored(const void* q, const void* k_cache, const void* v_cache,
+                                  const int32_t* block_tables, int max_blocks_per_seq,
+                                  const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                  int num_kv_heads, int block_size, int head_dim, int num_blocks,
+                                  float scale, float* scores, int64_t score_tokens, void* out,
+                                  int act_dtype, int cache_dtype, const float* k_scale,
+                                  const float* v_scale, int partition_size, void* workspace,
+                                  size_t workspace_bytes, void* stream);
+
+/* Device workspace of paged_attention_decode_scored.  Host only. */
+size_t pkv_scored_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                 int max_blocks_per_seq, int block_size, int partition_size);
+
+/*
+ * paged_kv_evict -- shrink each sequence to `budget` tokens per kv head.  Of a
+ * sequence's L tokens stay, for each kv head by itself, the first `sinks`, the
+ * last `recent` and, up to budget in all, those of the others with the largest
+ * scores (of equal ones the earliest; a NaN counts least), in their order; all
+ * of them if L <= budget.  Their K and V rows move to the blocks of dst_tables
+ * (int32 [num_seqs][max_dst_blocks]), kept token i to position i.
+ *  dst_tables     blocks that no row of either table holds otherwise (a new
+ *                 sequence's of the block manager); the old blocks stay as they
+ *                 are, shared ones too, and the old sequence can be freed.
+ *  scores_out     float32 [num_seqs][num_kv_heads][score_tokens_out], at least
+ *                 min(budget, score_tokens) wide (written): the scores that
+ *                 moved along, zeros behind them.
+ *  context_lens_out int32 [num_seqs] (written): min(L, budget).
+ *  kept           int32 [num_seqs][num_kv_heads][budget] (written): the tokens
+ *                 that stayed, -1 behind them.
+ * Written buffers share no memory with any other.  sinks + recent <= budget;
+ * head_dim 64 or 128.  Not for block-scaled caches (a token's codes mean
+ * nothing under another block's scale).  A length outside 0 ..
+ * max_blocks_per_seq * block_size or score_tokens flags PKV_DEV_BAD_CONTEXT_LEN,
+ * tokens that the new table has no blocks for PKV_DEV_NO_SPACE: such a sequence
+ * comes out with length 0 and nothing moves.  Bad table entries skip their rows
+ * and flag PKV_DEV_BAD_BLOCK.
+ */
+int paged_kv_evict(void* k_cache, void* v_cache, int num_blocks, int num_kv_heads, int block_size,
+                   int head_dim, int cache_dtype, const float* scores, int64_t score_tokens,
+                   const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                   int num_seqs, const int32_t* dst_tables, int max_dst_blocks, int budget, int recent,
+                   int sinks, float* scores_out, int64_t score_tokens_out, int32_t* context_lens_out,
+                   int32_t* kept, void* stream);
+
+/* ------------------------------------------------------------------------
  * A step over a block-scaled E4M3 cache (Ultralytics glossary "PagedAttention",
  * section "Related techniques": an 8-bit cache).  k_scales and v_scales are
  * float32 [num_blocks][num_kv_heads] (device): the element of code c in block

@@ -14,6 +14,10 @@ library's C++ host code.  There is no CPU fallback: a missing library raises.
     paged_rope_append(q, k, v, positions, slot_mapping, inv_freq, k_cache, v_cache, ...)
     paged_kv_append_scaled(k, v, slot_mapping, k_cache, v_cache, k_scales, v_scales)
     paged_attention_decode_scaled(q, k_cache, v_cache, k_scales, v_scales, block_tables, ...)
+    paged_attention_chunk(q, k_cache, v_cache, block_tables, context_lens, seq_starts, scale, window, sinks, ...)
+    paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, window, sinks, ...)
+    paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scores, ...)
+    paged_kv_evict(k_cache, v_cache, scores, block_tables, context_lens, dst_tables, budget, recent, ...)
     BlockManager(num_blocks, block_size, free_list=None)
 
 Cache tensors are [num_blocks, num_kv_heads, block_size, head_dim], float16 or
@@ -49,7 +53,8 @@ __all__ = ["paged_kv_append", "paged_attention_decode", "paged_attention_decode_
            "paged_block_copy",
            "paged_block_swap", "paged_attention_decode_sparse", "quest_block_minmax", "quest_append_minmax",
            "quest_select", "paged_extend_tables", "ExtendedTables", "rope_inv_freq", "paged_rope_append",
-           "paged_kv_append_scaled", "paged_attention_decode_scaled", "workspace_size",
+           "paged_kv_append_scaled", "paged_attention_decode_scaled", "paged_attention_chunk",
+           "paged_attention_decode_window", "paged_attention_decode_scored", "paged_kv_evict", "Evicted", "workspace_size",
            "resolve_partition_size", "device_error", "set_kernel_path", "BlockManager", "OutOfBlocks", "PagedKVError",
            "F16", "BF16", "E4M3", "PARTITION_SINGLE", "PARTITION_AUTO", "load"]
 
@@ -683,6 +688,214 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
     args = (qp, kc, vc, s1, s2, tables, tshape[1], lens, B, Hq, Hkv, bs, D, NB, scale, out.data_ptr(), _code(q),
             partition_size, ws, workspace.numel() * workspace.element_size(), s)
     return args, out, workspace
+
+
+def _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales):
+    """(cache shape, (k_scale, v_scale, k_scales, v_scales) pointers) of a cache of q's type, or of E4M3 codes with
+    either kind of scales."""
+    if len(k_cache.shape) != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError(f"{name}: k_cache and v_cache must be [num_blocks, num_kv_heads, block_size, head_dim] of one type")
+    if not k_cache.is_cuda:
+        raise ValueError(f"{name}: k_cache must be a CUDA tensor")
+    device = k_cache.device
+    if k_scales is not None or v_scales is not None:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError(f"{name}: k_scale, v_scale or k_scales, v_scales, not both")
+        shape = _require_scales(name, k_cache, v_cache, k_scales, v_scales)
+        return shape, (None, None, *_pointers(name, device, "k_scales v_scales", k_scales, v_scales))
+    if k_cache.dtype in _E4M3_TYPES:
+        if k_scale is None or v_scale is None:
+            raise ValueError(f"{name}: an E4M3 cache needs k_scale and v_scale, or k_scales and v_scales")
+    elif k_cache.dtype != q.dtype:
+        raise ValueError(f"{name}: the cache must be of q's type or hold E4M3 codes")
+    for t in (k_scale, v_scale):
+        if t is not None and (t.dtype is not torch.float32 or t.numel() != 1):
+            raise ValueError(f"{name}: k_scale and v_scale must be float32 with one element")
+    scales = [None if t is None else next(_pointers(name, device, what, t))
+              for what, t in (("k_scale", k_scale), ("v_scale", v_scale))]
+    return k_cache.shape, (*scales, None, None)
+
+
+def _row_args(name, q, block_tables, context_lens, shape):
+    """Checks of single-token queries q [B, Hq, D] and their rows' tables and lengths; returns B, Hq, max_blocks."""
+    if q.dim() != 3 or q.shape[2] != shape[3]:
+        raise ValueError(f"{name}: q must be [B, num_q_heads, head_dim]")
+    B, Hq, _ = q.shape
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+        raise ValueError(f"{name}: block_tables and context_lens must be int32")
+    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError(f"{name}: block_tables [B, max_blocks], context_lens [B]")
+    return B, Hq, block_tables.shape[1]
+
+
+def _out_like(name, q, out, stream, device):
+    if out is None:
+        return _output(stream, device, q.shape, q.dtype)
+    if out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"{name}: out must match q")
+    _require_out(device, out)
+    return out
+
+
+def _int32(name, **values):
+    for what, x in values.items():
+        if not -2 ** 31 <= int(x) < 2 ** 31:
+            raise ValueError(f"{name}: {what} out of range")
+
+
+@functools.lru_cache(maxsize=1024)
+def _size_of(func, *sizes):  # workspace sizes are functions of the sizes alone
+    return int(getattr(_native.lib(), func)(*sizes))
+
+
+def paged_attention_chunk(q, k_cache, v_cache, block_tables, context_lens, seq_starts, scale, window=None, sinks=0,
+                          out=None, k_scale=None, v_scale=None, k_scales=None, v_scales=None, workspace=None,
+                          stream=None):
+    """Attention of each sequence's new tokens, the rows seq_starts[b] .. seq_starts[b + 1] (int32 [B + 1], as
+    paged_extend_tables writes it) of q [T, Hq, D], over its cache, which holds them already; returns out [T, Hq, D].
+
+    context_lens [B] count the new tokens: the last row of a sequence is its last token and sees all of them, a row
+    before it one less.  With a window a row sees its last `window` tokens, itself among them, and the first `sinks`
+    ones.  Rows of q and out may lie apart (contiguous [Hq, D] each), rows of no sequence stay as they are (a new out
+    holds zeros there).  The cache is of q's type or E4M3 with either kind of scales."""
+    name = "paged_attention_chunk"
+    (NB, Hkv, bs, D), scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales)
+    if q.dim() != 3 or q.shape[2] != D:
+        raise ValueError(f"{name}: q must be [num_tokens, num_q_heads, head_dim]")
+    T, Hq, _ = q.shape
+    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or seq_starts.dtype != torch.int32:
+        raise ValueError(f"{name}: block_tables, context_lens and seq_starts must be int32")
+    if block_tables.dim() != 2:
+        raise ValueError(f"{name}: block_tables must be [B, max_blocks]")
+    B, max_blocks = block_tables.shape
+    if context_lens.shape != (B,) or seq_starts.shape != (B + 1,):
+        raise ValueError(f"{name}: context_lens [B], seq_starts [B + 1]")
+    if window is not None and window < 1:
+        raise ValueError(f"{name}: window must be positive (None: no window)")
+    _int32(name, window=window or 0, sinks=sinks)
+    device = k_cache.device
+    if out is None:
+        out = _output(stream, device, q.shape, q.dtype, zero=True)
+    elif out.shape != q.shape or out.dtype != q.dtype:
+        raise ValueError(f"{name}: out must match q")
+    qs, os = _rows(name, "q", q, device.index, q.shape), _rows(name, "out", out, device.index, q.shape)
+    if workspace is None:
+        need = _size_of("pkv_chunk_workspace_size", B, T, Hq, Hkv, D, max_blocks, bs)
+        workspace = _workspace(device, stream, max(need, 1), kind=2)
+    kc, vc, tables, lens, starts, ws = _pointers(
+        name, device, "k_cache v_cache block_tables context_lens seq_starts workspace", k_cache, v_cache, block_tables,
+        context_lens, seq_starts, workspace)
+    _call_on(device, name, q.data_ptr(), qs, kc, vc, tables, max_blocks, lens, starts, B, T, Hq, Hkv, bs, D, NB,
+             float(scale), window or 0, sinks, out.data_ptr(), os, _code(q), _code(k_cache), *scales, ws,
+             workspace.numel() * workspace.element_size(), _stream(stream, device))
+    return out
+
+
+def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_lens, scale, window, sinks=0, out=None,
+                                  k_scale=None, v_scale=None, k_scales=None, v_scales=None,
+                                  partition_size=PARTITION_AUTO, workspace=None, stream=None):
+    """Decode attention for q [B, Hq, D] over the last `window` tokens of each sequence, the newest among them, and
+    its first `sinks` ones; returns out [B, Hq, D].  Blocks wholly between the two are not read, nor are their table
+    entries.  A context length of 0 (a padding row) gives zeros.  The cache is of q's type or E4M3 with either kind
+    of scales."""
+    name = "paged_attention_decode_window"
+    shape, scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales)
+    NB, Hkv, bs, D = shape
+    B, Hq, max_blocks = _row_args(name, q, block_tables, context_lens, shape)
+    _int32(name, window=window, sinks=sinks)
+    device = k_cache.device
+    out = _out_like(name, q, out, stream, device)
+    if workspace is None:
+        need = _size_of("pkv_window_workspace_size", B, Hq, Hkv, D, max_blocks, bs, window, sinks,
+                        int(scales[2] is not None), int(partition_size))
+        workspace = _workspace(device, stream, max(need, 1))
+    qp, kc, vc, tables, lens, ws = _pointers(name, device, "q k_cache v_cache block_tables context_lens workspace", q,
+                                             k_cache, v_cache, block_tables, context_lens, workspace)
+    _call_on(device, name, qp, kc, vc, tables, max_blocks, lens, B, Hq, Hkv, bs, D, NB, float(scale), window, sinks,
+             out.data_ptr(), _code(q), _code(k_cache), *scales, int(partition_size), ws,
+             workspace.numel() * workspace.element_size(), _stream(stream, device))
+    return out
+
+
+def paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scores, out=None,
+                                  k_scale=None, v_scale=None, partition_size=PARTITION_AUTO, workspace=None,
+                                  stream=None):
+    """Decode attention for q [B, Hq, D] that also adds every cached token's weight, summed over the query heads of its
+    kv head, to scores float32 [B, Hkv, S], S at least max_blocks * block_size; returns out [B, Hq, D].  A context
+    length of 0 gives zeros and adds nothing."""
+    name = "paged_attention_decode_scored"
+    shape, scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, None, None)
+    NB, Hkv, bs, D = shape
+    B, Hq, max_blocks = _row_args(name, q, block_tables, context_lens, shape)
+    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (B, Hkv):
+        raise ValueError(f"{name}: scores must be float32 [B, num_kv_heads, tokens]")
+    device = k_cache.device
+    out = _out_like(name, q, out, stream, device)
+    if workspace is None:
+        need = _size_of("pkv_scored_workspace_size", B, Hq, Hkv, D, max_blocks, bs, int(partition_size))
+        workspace = _workspace(device, stream, max(need, 1), kind=3)
+    qp, kc, vc, tables, lens, sp, ws = _pointers(
+        name, device, "q k_cache v_cache block_tables context_lens scores workspace", q, k_cache, v_cache, block_tables,
+        context_lens, scores, workspace)
+    _call_on(device, name, qp, kc, vc, tables, max_blocks, lens, B, Hq, Hkv, bs, D, NB, float(scale), sp,
+             scores.shape[2], out.data_ptr(), _code(q), _code(k_cache), *scales[:2], int(partition_size), ws,
+             workspace.numel() * workspace.element_size(), _stream(stream, device))
+    return out
+
+
+class Evicted(NamedTuple):
+    """What paged_kv_evict writes (besides the caches)."""
+    context_lens: torch.Tensor
+    scores: torch.Tensor
+    kept: torch.Tensor
+
+
+def paged_kv_evict(k_cache, v_cache, scores, block_tables, context_lens, dst_tables, budget, recent, sinks=0,
+                   scores_out=None, lens_out=None, kept=None, stream=None) -> Evicted:
+    """Shrink each sequence to `budget` tokens per kv head: the first `sinks`, the last `recent` and those of the
+    others with the largest scores (float32 [B, Hkv, S], paged_attention_decode_scored's; of equal ones the earliest)
+    stay, in their order, and move to the blocks of dst_tables int32 [B, max_dst_blocks], which hold nothing else yet
+    (a new sequence's of the BlockManager; the old one can be freed after).  Returns the new lengths int32 [B], the
+    scores that moved along (as wide as the old ones, zeros behind them) and the tokens that stayed, int32
+    [B, Hkv, budget], -1 behind them.  Not for block-scaled caches."""
+    name = "paged_kv_evict"
+    if len(k_cache.shape) != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError(f"{name}: k_cache and v_cache must be [num_blocks, num_kv_heads, block_size, head_dim] of one type")
+    NB, Hkv, bs, D = k_cache.shape
+    device = k_cache.device
+    if block_tables.dim() != 2 or dst_tables.dim() != 2:
+        raise ValueError(f"{name}: block_tables [B, max_blocks], dst_tables [B, max_dst_blocks]")
+    B, max_blocks = block_tables.shape
+    if dst_tables.shape[0] != B or context_lens.shape != (B,):
+        raise ValueError(f"{name}: dst_tables [B, max_dst_blocks], context_lens [B]")
+    i32 = torch.int32
+    if block_tables.dtype is not i32 or dst_tables.dtype is not i32 or context_lens.dtype is not i32:
+        raise ValueError(f"{name}: block_tables, dst_tables and context_lens must be int32")
+    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (B, Hkv):
+        raise ValueError(f"{name}: scores must be float32 [B, num_kv_heads, tokens]")
+    if budget < 1:
+        raise ValueError(f"{name}: budget must be positive")
+    _int32(name, budget=budget, recent=recent, sinks=sinks)
+
+    def output(t, shape, dtype, what):
+        if t is None:
+            return _output(stream, device, shape, dtype)
+        if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name}: {what} must be {dtype} {list(shape)}")
+        return t
+
+    if scores_out is not None and (scores_out.dim() != 3 or scores_out.shape[:2] != (B, Hkv)):
+        raise ValueError(f"{name}: scores_out must be float32 [B, num_kv_heads, tokens]")
+    scores_out = output(scores_out, scores.shape if scores_out is None else scores_out.shape, torch.float32, "scores_out")
+    lens_out = output(lens_out, (B,), i32, "lens_out")
+    kept = output(kept, (B, Hkv, int(budget)), i32, "kept")
+    kc, vc, sp, tables, lens, dst, so, lo, kp = _pointers(
+        name, device, "k_cache v_cache scores block_tables context_lens dst_tables scores_out lens_out kept", k_cache,
+        v_cache, scores, block_tables, context_lens, dst_tables, scores_out, lens_out, kept)
+    _call_on(device, name, kc, vc, NB, Hkv, bs, D, _code(k_cache), sp, scores.shape[2], tables, max_blocks, lens, B, dst,
+             dst_tables.shape[1], int(budget), int(recent), int(sinks), so, scores_out.shape[2], lo, kp,
+             _stream(stream, device))
+    return Evicted(lens_out, scores_out, kept)
 
 
 def paged_block_copy(k_cache, v_cache, src_dst_pairs, stream=None, k_scales=None, v_scales=None):

@@ -40,6 +40,17 @@ SIGNATURES = {
     "pkv_resolve_partition_size": (I32, [I32, I32, I32, I32, I32, I32, I32]),
     "paged_block_copy": (I32, [P, P, P, I32, I32, SZ, P]),
     "paged_block_swap": (I32, [P, P, P, I32, I32, SZ, P, I32, P]),
+    "paged_attention_chunk": (I32, [P, I64, P, P, P, I32, P, P, I32, I32, I32, I32, I32, I32, I32, F32, I32, I32, P, I64,
+                                    I32, I32, P, P, P, P, P, SZ, P]),
+    "pkv_chunk_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+    "paged_attention_decode_window": (I32, [P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, F32, I32, I32, P, I32,
+                                            I32, P, P, P, P, I32, P, SZ, P]),
+    "pkv_window_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32, I32, I32, I32]),
+    "paged_attention_decode_scored": (I32, [P, P, P, P, I32, P, I32, I32, I32, I32, I32, I32, F32, P, I64, P, I32, I32,
+                                            P, P, I32, P, SZ, P]),
+    "pkv_scored_workspace_size": (SZ, [I32, I32, I32, I32, I32, I32, I32]),
+    "paged_kv_evict": (I32, [P, P, I32, I32, I32, I32, I32, P, I64, P, I32, P, I32, P, I32, I32, I32, I32, P, I64, P,
+                             P, P]),
     "paged_extend_tables": (I32, [P, I32, P, P, I32, I32, P, I32, P, I32, I32, P, P, P, P, P, P, P]),
     "paged_kv_append_scaled": (I32, [P, I64, P, I64, P, I32, P, P, P, P, I32, I32, I32, I32, I32, P]),
     "paged_rope_append": (I32, [P, I64, P, I64, P, I64, P, P, I32, P, I32, I32, F32, P, I64, P, P, I32, I32, I32,

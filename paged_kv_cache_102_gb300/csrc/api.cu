@@ -67,6 +67,10 @@ using namespace pkv;
 
 extern "C" {
 
+static bool rows_overlap(const void* a, int64_t a_stride, int64_t a_row, const void* b, int64_t b_stride, int64_t b_row,
+                         int num_tokens);
+
+
 const char* pkv_last_error(void) { return t_last_error.c_str(); }
 
 int pkv_version(void) { return 100; }
@@ -256,13 +260,59 @@ int paged_block_swap(void* k_cache, void* v_cache, const int32_t* block_ids, int
 
 }  // extern "C"
 
+// What the calls with a window or with accumulated weights add to a decode.
+struct DecodeExt {
+    int window = 0;  // 0: none
+    int sinks = 0;
+    float* scores = nullptr;
+    int64_t score_tokens = 0;
+};
+
+// Blocks that a row of max_blocks keeps under a window: those of the first tokens, those that the window may touch.
+static int window_blocks(int max_blocks, int block_size, int window, int sinks) {
+    if (window <= 0 || sinks < 0 || block_size <= 0) return max_blocks;
+    const long long n = (static_cast<long long>(sinks) + block_size - 1) / block_size +
+                        (static_cast<long long>(window) + block_size - 2) / block_size + 1;
+    return static_cast<int>(std::min<long long>(max_blocks, n));
+}
+
+// Workspace with kept logits: the statistics of every partition, then as without, then the logits.
+struct ScoredLayout {
+    size_t ml, o, logits, total;
+};
+static ScoredLayout scored_layout(int num_seqs, int num_q_heads, int head_dim, long long max_ctx, int P) {
+    const size_t parts = static_cast<size_t>((max_ctx + P - 1) / P), heads = static_cast<size_t>(num_seqs) * num_q_heads;
+    ScoredLayout w;
+    w.ml = kWorkspaceHeader;
+    w.o = w.ml + align_up(heads * parts * 2 * sizeof(float), 256);
+    w.logits = w.o + (parts > 1 ? align_up(heads * parts * head_dim * sizeof(float), 256) : 0);
+    w.total = w.logits + heads * static_cast<size_t>(max_ctx) * sizeof(float);
+    return w;
+}
+
+extern "C" size_t pkv_window_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                            int max_blocks_per_seq, int block_size, int window, int sinks,
+                                            int block_scales, int partition_size) {
+    const int n = window_blocks(max_blocks_per_seq, block_size, window, sinks);
+    return (block_scales ? pkv_scaled_workspace_size : pkv_workspace_size)(num_seqs, num_q_heads, num_kv_heads, head_dim, n,
+                                                                          block_size, partition_size);
+}
+
+extern "C" size_t pkv_scored_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
+                                            int max_blocks_per_seq, int block_size, int partition_size) {
+    const int P = pkv_resolve_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
+                                             block_size, partition_size);
+    if (P <= 0 || num_seqs <= 0 || head_dim <= 0) return 0;
+    return scored_layout(num_seqs, num_q_heads, head_dim, static_cast<long long>(max_blocks_per_seq) * block_size, P).total;
+}
+
 static int decode_impl(const char* fn, const void* q, const void* k_cache, const void* v_cache,
                        const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens, int num_seqs,
                        int num_q_heads, int num_kv_heads, int block_size, int head_dim, int num_blocks, float scale,
                        void* out, int act_dtype, int cache_dtype, const float* k_scale, const float* v_scale,
                        int partition_size, void* workspace, size_t workspace_bytes, void* stream, const void* k_new,
                        const void* v_new, const int64_t* new_slots, bool per_kvh_tables = false,
-                       bool block_scales = false) {
+                       bool block_scales = false, const DecodeExt* ext = nullptr) {
     const std::string F(fn);
     if (num_seqs < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
         return fail(PKV_ERR_INVALID, F + ": " + "sizes must be positive");
@@ -291,19 +341,26 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
         !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(workspace, 16))
         return fail(PKV_ERR_INVALID, F + ": " + "q, caches, out, workspace must be 16-byte aligned");
+    // partitions count the tokens that are left (ext: a window's)
+    const int kept_blocks = ext ? window_blocks(max_blocks_per_seq, block_size, ext->window, ext->sinks) : max_blocks_per_seq;
     const int P = (block_scales ? pkv_scaled_partition_size : pkv_resolve_partition_size)(
-        num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size, partition_size);
+        num_seqs, num_q_heads, num_kv_heads, head_dim, kept_blocks, block_size, partition_size);
     if (P <= 0)
         return fail(PKV_ERR_INVALID, F + ": " + "partition_size must be 0, -1 or a positive multiple of 32 and of block_size");
-    const long long max_ctx = static_cast<long long>(max_blocks_per_seq) * block_size;
-    if (max_ctx > 0x7fffffffLL) return fail(PKV_ERR_INVALID, F + ": " + "table too long");
+    if (static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
+        return fail(PKV_ERR_INVALID, F + ": " + "table too long");
+    const long long max_ctx = static_cast<long long>(kept_blocks) * block_size;
+    const bool scored = ext && ext->scores;
     const int max_parts = static_cast<int>((max_ctx + P - 1) / P);
     if (max_parts > 65535 || num_kv_heads > 65535 || num_seqs > 65535)
         return fail(PKV_ERR_INVALID, F + ": " + "grid too large (partitions, kv heads or sequences > 65535)");
-    const size_t need = pkv_workspace_size_of(num_seqs, num_q_heads, head_dim, max_blocks_per_seq, block_size, P);
+    const ScoredLayout layout = scored_layout(num_seqs, num_q_heads, head_dim, max_ctx, P);
+    const size_t need = scored ? layout.total
+                               : pkv_workspace_size_of(num_seqs, num_q_heads, head_dim, kept_blocks, block_size, P);
     if (!workspace || workspace_bytes < need)
         return fail(PKV_ERR_INVALID, F + ": " + "workspace of " + std::to_string(need) + " bytes required (" +
-                                         (block_scales ? "pkv_scaled_workspace_size)" : "pkv_workspace_size)"));
+                                         (scored ? "pkv_scored_workspace_size)" : ext ? "pkv_window_workspace_size)"
+                                          : block_scales ? "pkv_scaled_workspace_size)" : "pkv_workspace_size)"));
     int* err = device_error_word();
     if (!err) return fail(PKV_ERR_CUDA, F + ": " + "cannot resolve the device error word");
 
@@ -334,6 +391,16 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     p.k_new = k_new;
     p.v_new = v_new;
     p.new_slots = new_slots;
+    if (ext) {
+        p.window = ext->window;
+        p.sinks = ext->sinks;
+    }
+    if (scored) {
+        p.ws_ml = reinterpret_cast<float*>(ws + layout.ml);
+        p.ws_o = max_parts > 1 ? reinterpret_cast<float*>(ws + layout.o) : nullptr;
+        p.logits = reinterpret_cast<float*>(ws + layout.logits);
+        p.logit_tokens = max_ctx;
+    }
     if (per_kvh_tables) {  // tables [B][Hkv][max_blocks], lengths [B][Hkv]
         p.table_seq_stride = static_cast<int64_t>(num_kv_heads) * max_blocks_per_seq;
         p.table_kvh_stride = max_blocks_per_seq;
@@ -374,7 +441,7 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     const bool use_tc = path == PKV_PATH_TENSOR || path == PKV_PATH_TENSOR_2CTA ||
                         (path == PKV_PATH_AUTO && tc_ok && !small && (G >= 4 || block_scales));
     if (use_tc) {
-        const int chunk = decode_tc_max_rows() / rows_per_seq;
+        const int chunk = (ext ? decode_tc_ext_max_rows() : decode_tc_max_rows()) / rows_per_seq;
         const size_t act_bytes = 2;
         e = cudaSuccess;
         for (int s0 = 0; s0 < num_seqs && e == cudaSuccess; s0 += chunk) {
@@ -394,9 +461,19 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
                 c.ws_ml = p.ws_ml + hrow0 * 2;
                 c.ws_o = p.ws_o + hrow0 * head_dim;
             }
-            e = launch_decode_tc(c, act_dtype, kind, head_dim, block_size, G, path == PKV_PATH_TENSOR ? 0 : 1,
-                                 s);
+            if (scored) {
+                c.ws_ml = p.ws_ml + static_cast<size_t>(s0) * num_q_heads * max_parts * 2;
+                c.logits = p.logits + static_cast<int64_t>(s0) * num_q_heads * max_ctx;
+            }
+            e = ext ? launch_decode_tc_ext(c, act_dtype, kind, head_dim, block_size, G, s)
+                    : launch_decode_tc(c, act_dtype, kind, head_dim, block_size, G, path == PKV_PATH_TENSOR ? 0 : 1, s);
         }
+    } else if (ext) {
+        const bool f16 = act_dtype == PKV_F16;
+        auto launch = kind == kCacheE4M3Blocks ? (f16 ? launch_decode_ext_f16_e4m3b : launch_decode_ext_bf16_e4m3b)
+                      : kind == PKV_E4M3       ? (f16 ? launch_decode_ext_f16_e4m3 : launch_decode_ext_bf16_e4m3)
+                                               : (f16 ? launch_decode_ext_f16_f16 : launch_decode_ext_bf16_bf16);
+        e = launch(p, head_dim, block_size, G, s);
     } else if (block_scales)
         e = act_dtype == PKV_F16 ? launch_decode_f16_e4m3b(p, head_dim, block_size, G, s)
                                  : launch_decode_bf16_e4m3b(p, head_dim, block_size, G, s);
@@ -421,9 +498,18 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         m.head_dim = head_dim;
         m.partition_size = P;
         m.max_parts = max_parts;
-        m.max_context = static_cast<int>(max_ctx);
+        m.max_context = max_blocks_per_seq * block_size;
+        m.window = p.window;
+        m.sinks = p.sinks;
+        m.block_size = block_size;
         e = launch_merge(m, act_dtype, s);
         if (e != cudaSuccess) return cuda_fail((F + ": merge kernel launch").c_str(), e);
+    }
+    if (scored) {
+        const AddWeightsParams a{p.logits, p.ws_ml, context_lens, ext->scores, ext->score_tokens, p.logit_tokens,
+                                 num_seqs, num_kv_heads, G, P, max_parts, static_cast<int>(max_ctx)};
+        e = launch_add_weights(a, s);
+        if (e != cudaSuccess) return cuda_fail((F + ": weights kernel launch").c_str(), e);
     }
     return PKV_OK;
 }
@@ -479,6 +565,178 @@ int paged_attention_decode_scaled(const void* q, const void* k_cache, const void
                        context_lens, num_seqs, num_q_heads, num_kv_heads, block_size, head_dim, num_blocks, scale, out,
                        act_dtype, PKV_E4M3, k_scales, v_scales, partition_size, workspace, workspace_bytes, stream,
                        nullptr, nullptr, nullptr, false, true);
+}
+
+int paged_attention_decode_window(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                  int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                  int num_kv_heads, int block_size, int head_dim, int num_blocks, float scale,
+                                  int window, int sinks, void* out, int act_dtype, int cache_dtype, const float* k_scale,
+                                  const float* v_scale, const float* k_scales, const float* v_scales,
+                                  int partition_size, void* workspace, size_t workspace_bytes, void* stream) {
+    const char* fn = "paged_attention_decode_window";
+    if (window < 1 || sinks < 0)
+        return fail(PKV_ERR_INVALID, std::string(fn) + ": window must be positive and sinks not negative");
+    const bool blocks = k_scales || v_scales;
+    if (blocks && (cache_dtype != PKV_E4M3 || k_scale || v_scale))
+        return fail(PKV_ERR_INVALID, std::string(fn) + ": an E4M3 cache has k_scale and v_scale or k_scales and v_scales");
+    DecodeExt ext;
+    ext.window = window;
+    ext.sinks = sinks;
+    return decode_impl(fn, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                       num_kv_heads, block_size, head_dim, num_blocks, scale, out, act_dtype, cache_dtype,
+                       blocks ? k_scales : k_scale, blocks ? v_scales : v_scale, partition_size, workspace,
+                       workspace_bytes, stream, nullptr, nullptr, nullptr, false, blocks, &ext);
+}
+
+int paged_attention_decode_scored(const void* q, const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                                  int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, int num_q_heads,
+                                  int num_kv_heads, int block_size, int head_dim, int num_blocks, float scale,
+                                  float* scores, int64_t score_tokens, void* out, int act_dtype, int cache_dtype,
+                                  const float* k_scale, const float* v_scale, int partition_size, void* workspace,
+                                  size_t workspace_bytes, void* stream) {
+    const char* fn = "paged_attention_decode_scored";
+    if (score_tokens < static_cast<int64_t>(max_blocks_per_seq) * block_size)
+        return fail(PKV_ERR_INVALID, std::string(fn) + ": scores need a value for each of a row's max_blocks_per_seq * block_size tokens");
+    if (num_seqs > 0 && (!scores || !aligned(scores, 4)))
+        return fail(PKV_ERR_INVALID, std::string(fn) + ": scores must be given, 4-byte aligned");
+    DecodeExt ext;
+    ext.scores = scores;
+    ext.score_tokens = score_tokens;
+    return decode_impl(fn, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
+                       num_kv_heads, block_size, head_dim, num_blocks, scale, out, act_dtype, cache_dtype, k_scale,
+                       v_scale, partition_size, workspace, workspace_bytes, stream, nullptr, nullptr, nullptr, false,
+                       false, &ext);
+}
+
+int paged_kv_evict(void* k_cache, void* v_cache, int num_blocks, int num_kv_heads, int block_size, int head_dim,
+                   int cache_dtype, const float* scores, int64_t score_tokens, const int32_t* block_tables,
+                   int max_blocks_per_seq, const int32_t* context_lens, int num_seqs, const int32_t* dst_tables,
+                   int max_dst_blocks, int budget, int recent, int sinks, float* scores_out, int64_t score_tokens_out,
+                   int32_t* context_lens_out, int32_t* kept, void* stream) {
+    const std::string F("paged_kv_evict: ");
+    if (num_blocks <= 0 || num_kv_heads <= 0 || block_size <= 0 || head_dim <= 0 || max_blocks_per_seq <= 0 ||
+        max_dst_blocks <= 0 || num_seqs < 0 || score_tokens <= 0 || score_tokens_out <= 0)
+        return fail(PKV_ERR_INVALID, F + "sizes must be positive");
+    if (cache_dtype != PKV_F16 && cache_dtype != PKV_BF16 && cache_dtype != PKV_E4M3)
+        return fail(PKV_ERR_INVALID, F + "cache_dtype must be PKV_F16, PKV_BF16 or PKV_E4M3");
+    if (head_dim != 64 && head_dim != 128) return fail(PKV_ERR_INVALID, F + "head_dim must be 64 or 128");
+    if (budget <= 0 || recent < 0 || sinks < 0 || static_cast<int64_t>(recent) + sinks > budget)
+        return fail(PKV_ERR_INVALID, F + "budget must be positive, recent and sinks not negative and at most budget in all");
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL ||
+        static_cast<int64_t>(max_dst_blocks) * block_size > 0x7fffffffLL)
+        return fail(PKV_ERR_INVALID, F + "table too long");
+    if (score_tokens_out < std::min<int64_t>(budget, score_tokens))
+        return fail(PKV_ERR_INVALID, F + "scores_out has no room for the tokens that stay");
+    if (num_kv_heads > 65535 || num_seqs > 65535) return fail(PKV_ERR_INVALID, F + "grid too large");
+    if (num_seqs == 0) return PKV_OK;
+    if (!k_cache || !v_cache || !scores || !block_tables || !context_lens || !dst_tables || !scores_out ||
+        !context_lens_out || !kept)
+        return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(scores, 4) || !aligned(block_tables, 4) ||
+        !aligned(context_lens, 4) || !aligned(dst_tables, 4) || !aligned(scores_out, 4) || !aligned(context_lens_out, 4) ||
+        !aligned(kept, 4))
+        return fail(PKV_ERR_INVALID, F + "caches must be 16-byte aligned (others 4)");
+    // what is written (first) and read: buffers of their own
+    const size_t B = num_seqs, BH = B * num_kv_heads;
+    const struct { const void* at; size_t bytes; } buffers[] = {
+        {scores_out, 4 * BH * score_tokens_out}, {context_lens_out, 4 * B}, {kept, 4 * BH * budget},
+        {scores, 4 * BH * score_tokens}, {context_lens, 4 * B}, {block_tables, 4 * B * max_blocks_per_seq},
+        {dst_tables, 4 * B * max_dst_blocks}};
+    for (int i = 0; i < 3; ++i)
+        for (int j = i + 1; j < 7; ++j) {
+            const auto a = reinterpret_cast<uintptr_t>(buffers[i].at), b = reinterpret_cast<uintptr_t>(buffers[j].at);
+            if (a < b + buffers[j].bytes && b < a + buffers[i].bytes)
+                return fail(PKV_ERR_INVALID, F + "scores_out, context_lens_out and kept must be buffers of their own");
+        }
+    int* err = device_error_word();
+    if (!err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
+    const EvictParams p{k_cache, v_cache, scores, block_tables, context_lens, dst_tables, scores_out, context_lens_out,
+                        kept, err, score_tokens, score_tokens_out, max_blocks_per_seq, max_dst_blocks, num_seqs,
+                        num_kv_heads, block_size, num_blocks, head_dim * (cache_dtype == PKV_E4M3 ? 1 : 2), budget,
+                        recent, sinks};
+    const cudaError_t e = launch_evict(p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail("paged_kv_evict: launch", e);
+}
+
+size_t pkv_chunk_workspace_size(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
+                                int max_blocks_per_seq, int block_size) {
+    (void)num_seqs, (void)num_tokens, (void)num_q_heads, (void)num_kv_heads, (void)head_dim, (void)max_blocks_per_seq,
+        (void)block_size;
+    return kWorkspaceHeader;
+}
+
+int paged_attention_chunk(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
+                          const int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,
+                          const int32_t* seq_starts, int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads,
+                          int block_size, int head_dim, int num_blocks, float scale, int window, int sinks, void* out,
+                          int64_t out_stride, int act_dtype, int cache_dtype, const float* k_scale, const float* v_scale,
+                          const float* k_scales, const float* v_scales, void* workspace, size_t workspace_bytes,
+                          void* stream) {
+    const std::string F("paged_attention_chunk: ");
+    if (num_seqs < 0 || num_tokens < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || max_blocks_per_seq <= 0 || num_blocks <= 0)
+        return fail(PKV_ERR_INVALID, F + "sizes must be positive (num_seqs and num_tokens may be 0)");
+    if (num_q_heads % num_kv_heads != 0)
+        return fail(PKV_ERR_SHAPE, F + "num_q_heads must be a multiple of num_kv_heads");
+    if (num_q_heads / num_kv_heads > 64) return fail(PKV_ERR_INVALID, F + "at most 64 query heads per kv head");
+    if (head_dim != 64 && head_dim != 128) return fail(PKV_ERR_INVALID, F + "head_dim must be 64 or 128");
+    if (block_size != 16 && block_size != 32) return fail(PKV_ERR_INVALID, F + "block_size must be 16 or 32");
+    if (act_dtype != PKV_F16 && act_dtype != PKV_BF16)
+        return fail(PKV_ERR_INVALID, F + "act_dtype must be PKV_F16 or PKV_BF16");
+    if (cache_dtype != act_dtype && cache_dtype != PKV_E4M3)
+        return fail(PKV_ERR_INVALID, F + "cache_dtype must equal act_dtype or be PKV_E4M3");
+    if (!std::isfinite(scale)) return fail(PKV_ERR_INVALID, F + "scale must be finite");
+    if (window < 0 || sinks < 0) return fail(PKV_ERR_INVALID, F + "window and sinks must not be negative (window 0: none)");
+    const bool blocks = k_scales || v_scales;
+    if (blocks && (cache_dtype != PKV_E4M3 || k_scale || v_scale))
+        return fail(PKV_ERR_INVALID, F + "an E4M3 cache has k_scale and v_scale or k_scales and v_scales");
+    if (cache_dtype == PKV_E4M3 && (blocks ? (!k_scales || !v_scales) : (!k_scale || !v_scale)))
+        return fail(PKV_ERR_INVALID, F + "an E4M3 cache needs scales for both K and V");
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
+        return fail(PKV_ERR_INVALID, F + "table too long");
+    const int64_t row = static_cast<int64_t>(num_q_heads) * head_dim;
+    if (q_stride % 8 != 0 || out_stride % 8 != 0 || (num_tokens > 1 && (q_stride < row || out_stride < row)))
+        return fail(PKV_ERR_INVALID, F + "token strides of q and out must be multiples of 8 elements and at least a row");
+    if (num_seqs == 0 || num_tokens == 0) return PKV_OK;
+    if (!q || !k_cache || !v_cache || !block_tables || !context_lens || !seq_starts || !out)
+        return fail(PKV_ERR_INVALID, F + "null pointer");
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16) ||
+        !aligned(workspace, 16) || !aligned(block_tables, 4) || !aligned(context_lens, 4) || !aligned(seq_starts, 4) ||
+        !aligned(k_scale, 4) || !aligned(v_scale, 4) || !aligned(k_scales, 4) || !aligned(v_scales, 4))
+        return fail(PKV_ERR_INVALID, F + "q, caches, out and workspace must be 16-byte aligned (others 4)");
+    // a row's output may not be another row's query: rows are done in any order
+    if (rows_overlap(out, 2 * out_stride, 2 * row, q, 2 * q_stride, 2 * row, num_tokens))
+        return fail(PKV_ERR_INVALID, F + "out shares memory with q");
+    const size_t need = pkv_chunk_workspace_size(num_seqs, num_tokens, num_q_heads, num_kv_heads, head_dim,
+                                                 max_blocks_per_seq, block_size);
+    if (!workspace || workspace_bytes < need)
+        return fail(PKV_ERR_INVALID, F + "workspace of " + std::to_string(need) + " bytes required (pkv_chunk_workspace_size)");
+    ChunkParams p{};
+    p.q = q;
+    p.q_stride = num_tokens > 1 ? q_stride : row;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.block_tables = block_tables;
+    p.context_lens = context_lens;
+    p.seq_starts = seq_starts;
+    p.out = out;
+    p.out_stride = num_tokens > 1 ? out_stride : row;
+    p.k_scale = blocks ? k_scales : k_scale;
+    p.v_scale = blocks ? v_scales : v_scale;
+    p.err = device_error_word();
+    p.max_blocks_per_seq = max_blocks_per_seq;
+    p.num_seqs = num_seqs;
+    p.num_tokens = num_tokens;
+    p.num_q_heads = num_q_heads;
+    p.num_kv_heads = num_kv_heads;
+    p.block_size = block_size;
+    p.num_blocks = num_blocks;
+    p.window = window;
+    p.sinks = sinks;
+    p.scale_log2 = scale * 1.4426950408889634f;
+    if (!p.err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
+    const cudaError_t e = launch_chunk(p, act_dtype, blocks ? kCacheE4M3Blocks : cache_dtype, head_dim,
+                                       static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PKV_OK : cuda_fail("paged_attention_chunk: launch", e);
 }
 
 int paged_extend_tables(int32_t* block_tables, int max_blocks_per_seq, const int32_t* context_lens,

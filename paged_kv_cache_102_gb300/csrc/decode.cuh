@@ -80,7 +80,7 @@ struct DecodeCfg {
     static_assert(TILE_BYTES % 16 == 0, "bulk copies move multiples of 16 bytes");
 };
 
-template <int ACT, int CACHE, int D, int BS, int G>
+template <int ACT, int CACHE, int D, int BS, int G, bool EXT = false>
 __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     paged_decode_partition_kernel(const DecodeParams p) {
     using C = DecodeCfg<CACHE, D, BS, G>;
@@ -104,9 +104,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
 
-    const int L = p.context_lens[static_cast<int64_t>(seq) * p.lens_seq_stride + kvh * p.lens_kvh_stride];
-    if (L < 1 || L > p.max_blocks_per_seq * BS) {
-        if (C::SCALED && L == 0) {  // an empty row of a padded batch: zeros
+    const int all = p.context_lens[static_cast<int64_t>(seq) * p.lens_seq_stride + kvh * p.lens_kvh_stride];
+    if (all < 1 || all > p.max_blocks_per_seq * BS) {
+        if ((C::SCALED || EXT) && all == 0) {  // an empty row of a padded batch: zeros
             if (part == 0)
                 for (int i = threadIdx.x; i < G * D / 8; i += kDecodeThreads)
                     reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
@@ -117,12 +117,17 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
         if (part == 0 && kvh == 0 && threadIdx.x == 0) atomicOr(p.err, kErrBadLen);
         return;
     }
+    const int L = EXT ? windowed_len(all, p.window, p.sinks, BS) : all;
     const int tok_begin = part * p.partition_size;
     if (tok_begin >= L) return;
     const int tok_end = min(L, tok_begin + p.partition_size);
     const int n_stage = (tok_end - tok_begin + kStageTokens - 1) / kStageTokens;
     const int blk_begin = tok_begin / BS;
     const int n_blk = (tok_end - tok_begin + BS - 1) / BS;
+    // EXT: table entry of block i of the partition, and whether token t is hidden
+    [[maybe_unused]] const int skip_from = p.sinks / BS + (p.sinks % BS != 0), skip = (all - L) / BS;
+    auto entry = [&](int i) { return EXT && blk_begin + i >= skip_from ? i + skip : i; };
+    auto hidden = [&](int t) { return EXT && p.window != 0 && t >= p.sinks && t < L - p.window; };
 
     if (threadIdx.x == 0) {
         s_failed = 0;
@@ -152,7 +157,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
         int issued = 0;
         for (int chunk = 0; chunk < n_blk && ok; chunk += 32) {
             const bool have = chunk + lane < n_blk;
-            int phys = have ? table[chunk + lane] : 0;
+            int phys = have ? table[entry(chunk + lane)] : 0;
             const bool bad = have && (phys < 0 || phys >= p.num_blocks);
             if (bad) {
                 atomicOr(p.err, kErrBadBlock);
@@ -266,7 +271,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     [[maybe_unused]] auto load_scales = [&](int first) {
         ksc = vsc = 0.f;
         if (first + lane < n_blk) {
-            const int phys = p.block_tables[seq * p.table_seq_stride + kvh * p.table_kvh_stride + blk_begin + first + lane];
+            const int phys = p.block_tables[seq * p.table_seq_stride + kvh * p.table_kvh_stride + blk_begin +
+                                            entry(first + lane)];
             if (phys >= 0 && phys < p.num_blocks) {
                 ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + kvh];
                 vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + kvh];
@@ -348,7 +354,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
 #pragma unroll
             for (int pp = 0; pp < C::PASSES; ++pp) {
                 const int tt = warp * C::TW + pp * C::TPP + r;
-                const bool valid = tok0 + tt < tok_end;
+                const bool valid = tok0 + tt < tok_end && !hidden(tok0 + tt);
                 const uint4 u = *reinterpret_cast<const uint4*>(kb + (tt * D * C::E) + c * 16);
                 if constexpr (MIX) {
                     const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -377,6 +383,19 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
 #pragma unroll
                         for (int off = C::LPR / 2; off >= 1; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
                         sc[pp][g] = valid ? (C::SCALED ? d * ks : d) : -INFINITY;
+                    }
+                }
+            }
+
+            if constexpr (EXT) {
+                if (p.logits != nullptr && c == 0) {
+#pragma unroll
+                    for (int pp = 0; pp < C::PASSES; ++pp) {
+                        const int t = tok0 + warp * C::TW + pp * C::TPP + r;
+                        if (t >= tok_end) continue;
+                        float* dst = p.logits + ((static_cast<int64_t>(seq) * p.num_kv_heads + kvh) * p.logit_tokens + t) * G;
+#pragma unroll
+                        for (int g = 0; g < G; ++g) dst[g] = sc[pp][g];
                     }
                 }
             }
@@ -411,7 +430,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
 #pragma unroll
             for (int pp = 0; pp < C::PASSES; ++pp) {
                 const int tt = warp * C::TW + pp * C::TPP + r;
-                if (tok0 + tt < tok_end) {
+                if (tok0 + tt < tok_end && !hidden(tok0 + tt)) {
                     const uint4 u = *reinterpret_cast<const uint4*>(vb + (tt * D * C::E) + c * 16);
                     if constexpr (MIX) {
                         const uint32_t w[4] = {u.x, u.y, u.z, u.w};
@@ -506,6 +525,10 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
         }
         const float o = num / den * vmul;
         const size_t row = static_cast<size_t>(seq) * p.num_q_heads + h0 + g;
+        if (EXT && p.logits != nullptr && d == 0) {  // whoever adds the weights up needs the statistics
+            p.ws_ml[(row * p.max_parts + part) * 2] = M;
+            p.ws_ml[(row * p.max_parts + part) * 2 + 1] = den;
+        }
         if (single) {
             static_cast<uint16_t*>(p.out)[row * D + d] = float_to_act<ACT>(o);
         } else {

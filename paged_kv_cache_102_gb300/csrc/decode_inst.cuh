@@ -1,7 +1,12 @@
 // Instantiates the partition kernel for one (activation, cache) type pair
 // over head_dim {64, 128}, block_size {16, 32}, group {1, 2, 4, 8}.
-// Include after defining PKV_ACT, PKV_CACHE and PKV_LAUNCH_NAME.
+// Include after defining PKV_ACT, PKV_CACHE and PKV_LAUNCH_NAME, and PKV_EXT as
+// true for the kernels with a window and kept logits.
 #include "decode.cuh"
+
+#ifndef PKV_EXT
+#define PKV_EXT false
+#endif
 
 namespace pkv {
 
@@ -10,7 +15,7 @@ namespace {
 template <int D, int BS, int G>
 cudaError_t launch_one(const DecodeParams& p, cudaStream_t s) {
     using C = DecodeCfg<PKV_CACHE, D, BS, G>;
-    auto kern = paged_decode_partition_kernel<PKV_ACT, PKV_CACHE, D, BS, G>;
+    auto kern = paged_decode_partition_kernel<PKV_ACT, PKV_CACHE, D, BS, G, PKV_EXT>;
     static bool configured[kMaxDevices] = {};  // shared-memory attribute set once per device
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);

@@ -126,6 +126,7 @@ constexpr int kTcQBuf = 3 * 1024;             // Q: two 8-row halves + 1 KB that
 constexpr int kTcPBuf = (2 * kTcMaxTiles + 1) * 1024;  // P: tile x token-half 8-row regions + alias pad
 constexpr int kTcTmemCols = 256;              // two buffers of S (4 x 16 columns) + O (16, or 32), rounded to a power of 2
 constexpr int kTcMaxSeqs = 2048;              // sequences served (lengths and item prefix in shared memory)
+constexpr int kTcExtRows = 256;               // sequences of one launch with a window or kept logits
 constexpr int kTcSmemPerSm = 228 * 1024;      // shared memory of one SM, including the 1 KB each CTA reserves
 constexpr int kTcQueue = 2;                   // claimed items in flight between the roles
 constexpr int kTcLenBuckets = 8;              // length buckets of the partly filled partitions
@@ -142,7 +143,8 @@ constexpr float kPartScale = 32.f;
 // 16-byte columns of P per token: more than two parts of eight heads' weights need a second one.
 __host__ __device__ constexpr int tc_p_columns(int cache, int G) { return cache == kE4M3B && G == 8 ? 2 : 1; }
 
-template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false, bool HALF = false, int PREG = 1>
+template <int NS, int STG = kTcStage, bool PAIR = false, bool SCALED = false, bool HALF = false, int PREG = 1,
+          bool EXT = false>
 struct TcSmem {
     static constexpr int RING = 0;
     static constexpr int Q = NS * STG;
@@ -158,7 +160,7 @@ struct TcSmem {
     // item numbers, q shifts, block-table entries [32] per entry; SCALED: kScaledEntry bytes per entry
     static constexpr int QUEUE = P + PBUFS * PBUF;
     static constexpr int BARS =
-        SCALED ? QUEUE + kTcQueue * kScaledEntry : (QUEUE + 2 * kTcQueue * 4 + kTcQueue * 32 * 4 + 7) / 8 * 8;
+        SCALED ? QUEUE + kTcQueue * (kScaledEntry + (EXT ? 16 : 0)) : (QUEUE + 2 * kTcQueue * 4 + kTcQueue * 32 * 4 + 7) / 8 * 8;
     // full[NS], empty[NS], q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_free[2], final,
     // item_full[kTcQueue], item_empty[kTcQueue] (a single Q or P buffer uses entry 0 of its pair)
     static constexpr int NBARS = 2 * NS + 13 + 2 * kTcQueue;
@@ -306,7 +308,7 @@ __device__ __forceinline__ uint32_t take_e4m3x2(float& x0, float& x1) {
     return h;
 }
 
-template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR = false, bool HALF = false>
+template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR = false, bool HALF = false, bool EXT = false>
 __global__ void __launch_bounds__(kTcThreads, 2)
     paged_decode_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                            const __grid_constant__ CUtensorMap qmap, const DecodeParams p) {
@@ -322,7 +324,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     constexpr int PARTS = SCALED ? kScaledParts : 2;  // of P
     constexpr int PART = SCALED && G <= 4 ? 4 : 8;    // columns from one part of P to the next
     static_assert(PARTS * PART <= 16 * PREG, "columns of P");
-    using S = TcSmem<NS, STG, PAIR, SCALED, HALF, PREG>;
+    using S = TcSmem<NS, STG, PAIR, SCALED, HALF, PREG, EXT>;
     constexpr int THREADS = kTcThreads;
     constexpr int TPR = HALF ? 2 : 1;         // tokens per tile row
     constexpr int TILE = kTcTile * TPR;       // tokens per tile
@@ -355,7 +357,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     volatile int* item_shift = item_q + kTcQueue;
     volatile int* item_phys = item_shift + kTcQueue;  // [slot][32]: the item's physical blocks
     // block-scaled: the entry instead
-    auto entry_of = [&](int slot) { return sm + S::QUEUE + slot * kScaledEntry; };
+    constexpr int ENTRY = kScaledEntry + (EXT ? 16 : 0);  // EXT: and the item's first token
+    auto entry_of = [&](int slot) { return sm + S::QUEUE + slot * ENTRY; };
     uint64_t* bars = reinterpret_cast<uint64_t*>(sm + S::BARS);
     uint64_t* full = bars;
     uint64_t* empty = bars + NS;
@@ -403,7 +406,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         auto valid_len = [&](int L) { return L >= 1 && L <= p.max_blocks_per_seq * BS; };
         int cnt[NBK + 1] = {};  // [0]: full items, [1 + k]: rows in length bucket k
         for (int s = s0; s < s1; ++s) {
-            const int L = p.context_lens[s];
+            int L = p.context_lens[s];
+            if (EXT && valid_len(L)) L = windowed_len(L, p.window, p.sinks, BS);
             s_lens[s] = L;
             if (!valid_len(L)) continue;
             cnt[0] += heads_per_row * (L / p.partition_size);
@@ -562,7 +566,30 @@ __global__ void __launch_bounds__(kTcThreads, 2)
         it.n_tiles = b.y;
         it.ev = b.z;
         it.flags = b.w;
+        if constexpr (EXT) it.tok_begin = reinterpret_cast<const int*>(entry_of(slot) + kScaledEntry)[0];
         return a.x >= 0;
+    };
+
+    // EXT: the hidden tokens [lo, hi) of an item, numbered from its first
+    auto hidden_of = [&](const TcItem& it, int& lo, int& hi) {
+        lo = EXT && p.window != 0 ? p.sinks - it.tok_begin : 0;
+        hi = EXT && p.window != 0 ? s_lens[it.seq] - p.window - it.tok_begin : 0;
+    };
+    // Their V rows in tile t become zeros, as those past the context do: what is hidden may be anything.
+    // (warp-wide; true if it wrote any, before the tile's products)
+    auto clear_hidden = [&](const TcItem& it, int t, unsigned char* vb) {
+        int lo, hi;
+        hidden_of(it, lo, hi);
+        lo = max(0, lo - t * TILE);
+        hi = min(min(TILE, it.n_tok - t * TILE), hi - t * TILE);
+        if (lo >= hi) return false;
+        constexpr int CHUNKS = FP8 ? 8 / TPR : 16;  // 16-byte chunks per token
+        for (int i = lane; i < (hi - lo) * CHUNKS; i += 32) {
+            const int tok = lo + i / CHUNKS, c = i % CHUNKS + (tok % TPR) * CHUNKS, r = tok / TPR;
+            const int at = HALF ? ((c ^ (r & 7)) * 16) : (c & 7) * 16;  // (whole rows: any order of their chunks)
+            *reinterpret_cast<uint4*>(vb + (c >> 3) * kTcHalf + r * 128 + at) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        return true;
     };
 
     if (warp == 0) {
@@ -576,11 +603,11 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             // sequences with a context length outside 1..max_blocks*BS are skipped; report them once
             for (int s = blockIdx.x; s < B; s += gridDim.x) {
                 const int L = s_lens[s];
-                if (SCALED && L == 0) continue;
+                if ((SCALED || EXT) && L == 0) continue;
                 if (L < 1 || L > p.max_blocks_per_seq * BS) atomicOr(p.err, kErrBadLen);
             }
         }
-        if constexpr (SCALED) {  // empty rows of a padded batch: zeros
+        if constexpr (SCALED || EXT) {  // empty rows of a padded batch: zeros
             for (int s = blockIdx.x; s < B; s += gridDim.x) {
                 if (s_lens[s] != 0) continue;
                 uint4* o = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.out) +
@@ -592,8 +619,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             const int n_blk = (it.n_tok + BS - 1) / BS;
             int phys = -1;
             if (lane < n_blk) {
-                phys = p.block_tables[it.seq * p.table_seq_stride + it.kvh * p.table_kvh_stride + it.tok_begin / BS +
-                                      lane];
+                int i = it.tok_begin / BS + lane;
+                if (EXT && i >= p.sinks / BS + (p.sinks % BS != 0)) i += (p.context_lens[it.seq] - s_lens[it.seq]) / BS;
+                phys = p.block_tables[it.seq * p.table_seq_stride + it.kvh * p.table_kvh_stride + i];
                 if (phys < 0 || phys >= p.num_blocks) {
                     atomicOr(p.err, kErrBadBlock);
                     phys = -1;
@@ -719,6 +747,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     if (lane == 0) {
                         reinterpret_cast<int4*>(e)[0] = make_int4(ci, it.seq, it.kvh, it.part);
                         reinterpret_cast<int4*>(e)[1] = make_int4(it.n_tok, it.n_tiles, it.ev, it.flags);
+                        if constexpr (EXT) reinterpret_cast<int*>(e + kScaledEntry)[0] = it.tok_begin;
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&item_full[slot]);
@@ -1045,6 +1074,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 return false;
             for (int t = 0; t < whole; ++t) {
                 if (!__all_sync(0xffffffffu, tc_wait(&full[stage], phase, abort_flag, p.err))) return false;
+                if (EXT && clear_hidden(it, t, ring + stage * STG)) {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                }
                 tc::fence_after_sync();
                 if (tc::elect_one()) issue(stage, t, t == it.n_tiles - 1 ? (valid + 31) / 32 : 4);
                 __syncwarp();
@@ -1054,6 +1087,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 if (!__all_sync(0xffffffffu, tc_wait(&full[stage], phase, abort_flag, p.err))) return false;
                 unsigned char* vb = ring + stage * STG;
                 const int ksteps = (valid + 31) / 32;
+                if constexpr (EXT) clear_hidden(it, whole, vb);
                 for (int i = lane; i < (ksteps * 32 - valid) * 8; i += 32)
                     *reinterpret_cast<uint4*>(vb + valid * 128 + i * 16) = make_uint4(0u, 0u, 0u, 0u);
                 if (HALF && (tokens & 1) && lane < 4)
@@ -1182,6 +1216,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 constexpr int KSTEP = FP8 ? 32 : 16;  // tokens per MMA
                 constexpr int CHUNKS = FP8 ? 8 : 16;  // 16-byte chunks per token row
                 const int ksteps = (valid + KSTEP - 1) / KSTEP;
+                if (EXT && clear_hidden(it, t, vb)) {
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                }
                 // rows past the context inside the last step: zero them so that
                 // never-written pool slots cannot turn P = 0 into NaN
                 const int zero_rows = ksteps * KSTEP - valid;
@@ -1334,16 +1372,34 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         tc::tmem_wait_ld();
                     }
                     tc::fence_before_sync();  // these reads precede the next MMA into this S buffer
+                    [[maybe_unused]] int hide_lo, hide_hi;
+                    if constexpr (EXT) hidden_of(it, hide_lo, hide_hi);
                     float mx[G];
 #pragma unroll
                     for (int g = 0; g < G; ++g) mx[g] = -INFINITY;
 #pragma unroll
                     for (int t = 0; t < kTcMaxTiles; ++t) {
-                        const bool valid = t < n_tiles && token_of(t) < it.n_tok;
+                        bool valid = t < n_tiles && token_of(t) < it.n_tok;
+                        if constexpr (EXT) valid = valid && !(token_of(t) >= hide_lo && token_of(t) < hide_hi);
 #pragma unroll
                         for (int g = 0; g < G; ++g) {
                             sc[t][g] = valid ? sc[t][g] * (SCALED ? sl * ks_t[t] : sl) : -INFINITY;
                             mx[g] = fmaxf(mx[g], SCALED ? sc[t][g] + lv_t[t] : sc[t][g]);
+                        }
+                    }
+                    if constexpr (EXT && !SCALED) {
+                        if (p.logits != nullptr) {
+                            const int kvh = PAIR ? 2 * it.kvh + hh : it.kvh;
+                            float* dst = p.logits + ((static_cast<int64_t>(it.seq) * p.num_kv_heads + kvh) *
+                                                     p.logit_tokens + it.tok_begin) * G;
+#pragma unroll
+                            for (int t = 0; t < kTcMaxTiles; ++t)
+                                if (t < n_tiles && token_of(t) < it.n_tok) {
+#pragma unroll
+                                    for (int g = 0; g < G; g += 2)
+                                        *reinterpret_cast<float2*>(dst + token_of(t) * G + g) =
+                                            make_float2(sc[t][g], sc[t][g + (G > 1)]);
+                                }
                         }
                     }
 #pragma unroll
@@ -1577,6 +1633,10 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 const float val = o[g] * (__frcp_rn(Lg) * vmul);
                 const int kvh = PAIR ? 2 * it.kvh + hh : it.kvh;
                 const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + kvh * G + g;
+                if (EXT && p.logits != nullptr && d == 0) {  // whoever adds the weights up needs the statistics
+                    p.ws_ml[(hrow * p.max_parts + it.part) * 2] = Mg;
+                    p.ws_ml[(hrow * p.max_parts + it.part) * 2 + 1] = Lg;
+                }
                 if (single) {
                     static_cast<uint16_t*>(p.out)[hrow * HD + d] = float_to_act<ACT>(val);
                 } else {

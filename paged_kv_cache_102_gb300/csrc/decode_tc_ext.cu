@@ -1,0 +1,37 @@
+// Tensor-core decode with a window or kept logits over 16-bit caches: kernel
+// instantiations and their launch (E4M3 caches: decode_tc_ext_e4m3.cu and
+// decode_tc_ext_e4m3b.cu).  One ring depth each, two CTAs per SM: the API calls
+// with at most kTcExtRows sequences, whose tables leave room for it.
+#include "decode_tc_host.cuh"
+
+namespace pkv {
+
+int decode_tc_ext_max_rows() { return kTcExtRows; }
+
+namespace {
+
+template <int ACT>
+cudaError_t launch_ext(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
+                       int head_dim, int BS, int G, cudaStream_t s) {
+    return head_dim == 64 ? by_shape<ACT, ACT, 2, true, false, true>(p, km, vm, qm, BS, G, 2, s)
+                          : by_shape<ACT, ACT, 3, false, false, true>(p, km, vm, qm, BS, G, 2, s);
+}
+
+}  // namespace
+
+cudaError_t launch_decode_tc_ext(const DecodeParams& p, int act, int cache, int head_dim, int BS, int G, cudaStream_t s) {
+    if (cache == kE4M3B) return launch_decode_tc_ext_e4m3b(p, act, head_dim, BS, G, s);
+    if (cache == kE4M3) return launch_decode_tc_ext_e4m3(p, act, BS, G, s);
+    if (head_dim == 64 && p.num_kv_heads % 2 != 0) return cudaErrorInvalidValue;
+    const uint64_t cache_rows = static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * BS;
+    CUtensorMap km, vm, qm;
+    if (!make_map(&km, p.k_cache, act, cache_rows, BS, head_dim) || !make_map(&vm, p.v_cache, act, cache_rows, BS, head_dim) ||
+        !make_map(&qm, p.q, act, static_cast<uint64_t>(p.num_seqs) * p.num_q_heads, G, head_dim))
+        return cudaErrorInvalidValue;
+    const cudaError_t e = cudaMemsetAsync(p.work_counter, 0, sizeof(int), s);
+    if (e != cudaSuccess) return e;
+    return act == kBF16 ? launch_ext<kBF16>(p, km, vm, qm, head_dim, BS, G, s)
+                        : launch_ext<kF16>(p, km, vm, qm, head_dim, BS, G, s);
+}
+
+}  // namespace pkv

@@ -59,11 +59,12 @@ __global__ void zero_counter_kernel(int* counter) {
     if (threadIdx.x == 0) *counter = 0;
 }
 
-template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR, bool HALF>
+template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR, bool HALF, bool EXT>
 cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                    int ctas_per_sm, cudaStream_t s) {
-    auto kern = paged_decode_tc_kernel<ACT, CACHE, BS, G, NS, PAIR, HALF>;
-    using Smem = TcSmem<NS, is_e4m3(CACHE) ? kTcStage8 : kTcStage, PAIR, CACHE == kE4M3B, HALF, tc_p_columns(CACHE, G)>;
+    auto kern = paged_decode_tc_kernel<ACT, CACHE, BS, G, NS, PAIR, HALF, EXT>;
+    using Smem = TcSmem<NS, is_e4m3(CACHE) ? kTcStage8 : kTcStage, PAIR, CACHE == kE4M3B, HALF, tc_p_columns(CACHE, G), EXT>;
+    static_assert(!EXT || 2 * (Smem::alloc(kTcExtRows) + 1024) <= kTcSmemPerSm, "two CTAs per SM");
     constexpr int threads = kTcThreads;
     const int rows = p.table_kvh_stride != 0 ? p.num_seqs * p.num_kv_heads : p.num_seqs;
     const int smem = Smem::alloc(rows);
@@ -111,21 +112,21 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorM
     }
 }
 
-template <int ACT, int CACHE, int NS, bool PAIR = false, bool HALF = false>
+template <int ACT, int CACHE, int NS, bool PAIR = false, bool HALF = false, bool EXT = false>
 cudaError_t by_shape(const DecodeParams& p, const CUtensorMap& km, const CUtensorMap& vm, const CUtensorMap& qm,
                      int BS, int G, int ctas_per_sm, cudaStream_t s) {
     if constexpr (CACHE == kE4M3B) {
-        if (BS == 16 && G == 1) return launch<ACT, CACHE, 16, 1, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
-        if (BS == 32 && G == 1) return launch<ACT, CACHE, 32, 1, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+        if (BS == 16 && G == 1) return launch<ACT, CACHE, 16, 1, NS, PAIR, HALF, EXT>(p, km, vm, qm, ctas_per_sm, s);
+        if (BS == 32 && G == 1) return launch<ACT, CACHE, 32, 1, NS, PAIR, HALF, EXT>(p, km, vm, qm, ctas_per_sm, s);
     }
     if (BS == 16) {
-        if (G == 2) return launch<ACT, CACHE, 16, 2, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
-        if (G == 4) return launch<ACT, CACHE, 16, 4, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
-        if (G == 8) return launch<ACT, CACHE, 16, 8, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 2) return launch<ACT, CACHE, 16, 2, NS, PAIR, HALF, EXT>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 4) return launch<ACT, CACHE, 16, 4, NS, PAIR, HALF, EXT>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 8) return launch<ACT, CACHE, 16, 8, NS, PAIR, HALF, EXT>(p, km, vm, qm, ctas_per_sm, s);
     } else if (BS == 32) {
-        if (G == 2) return launch<ACT, CACHE, 32, 2, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
-        if (G == 4) return launch<ACT, CACHE, 32, 4, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
-        if (G == 8) return launch<ACT, CACHE, 32, 8, NS, PAIR, HALF>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 2) return launch<ACT, CACHE, 32, 2, NS, PAIR, HALF, EXT>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 4) return launch<ACT, CACHE, 32, 4, NS, PAIR, HALF, EXT>(p, km, vm, qm, ctas_per_sm, s);
+        if (G == 8) return launch<ACT, CACHE, 32, 8, NS, PAIR, HALF, EXT>(p, km, vm, qm, ctas_per_sm, s);
     }
     return cudaErrorInvalidValue;
 }

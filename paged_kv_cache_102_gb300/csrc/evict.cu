@@ -1,0 +1,263 @@
+// Eviction by accumulated attention weight: which tokens of a sequence stay, and
+// their move to the blocks of a smaller table; and the accumulation itself.
+//
+// Of the L tokens of (sequence b, kv head h) the first `sinks`, the last `recent`
+// and of the others those with the largest scores stay, min(L, budget) in all,
+// in their order (of equal scores the earliest; a NaN counts least).
+//
+// evict_select_kernel: one block per (b, h).  The scores become 32-bit keys of
+// the same order, kept in shared memory (up to kKeyTokens of them; longer rows
+// are read again).  The key of the last token that stays is found by radix, 11
+// bits from the top, then 11, then 10: a histogram of the keys that agree so far
+// and a scan of it from the top.  Then one ordered pass: a thread looks at 4
+// neighbouring tokens, and with g tokens above that key and e equal to it before
+// a token, its place is g + min(e, equal ones that stay); g and e come from one
+// packed scan.
+// evict_move_kernel: 16 bytes a thread, kept rows of K and V to their new
+// blocks; source and destination blocks differ, so that rows are independent.
+#include "kernels.h"
+#include "pkv_device.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kSelectThreads = 1024;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kKeyTokens = 48 * 1024;
+constexpr int kMoveThreads = 256;
+constexpr int kAddThreads = 256;
+
+// 32-bit key of the scores' order: NaN 0, then -inf .. +inf (-0 as 0).
+__device__ __forceinline__ uint32_t score_key(float x) {
+    if (x != x) return 0;
+    const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
+    return u & 0x80000000u ? ~u : u | 0x80000000u;
+}
+
+// Exclusive sum over the block of each thread's x, and the total (one sync
+// before `totals` may be written again is the caller's).
+__device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* totals, uint32_t& all) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    uint32_t incl = x;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 31) totals[warp] = incl;
+    __syncthreads();
+    const uint32_t t = totals[lane];
+    uint32_t ti = t;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const uint32_t v = __shfl_up_sync(0xffffffffu, ti, off);
+        if (lane >= off) ti += v;
+    }
+    all = __shfl_sync(0xffffffffu, ti, 31);
+    return incl - x + __shfl_sync(0xffffffffu, ti - t, warp);
+}
+
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p) {
+    extern __shared__ uint32_t keys[];
+    __shared__ uint32_t hist[kBins];
+    __shared__ uint32_t totals[2][kSelectWarps];
+    __shared__ uint32_t s_bin, s_rest;
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int64_t row = static_cast<int64_t>(b) * p.num_kv_heads + h;
+    const float* scores = p.scores + row * p.score_tokens;
+    int32_t* kept = p.kept + row * p.budget;
+    float* out = p.scores_out + row * p.score_tokens_out;
+    int L = p.context_lens[b];
+    if (L < 0 || L > static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size || L > p.score_tokens) {
+        if (h == 0 && tid == 0) atomicOr(p.err, kErrBadLen);
+        L = 0;
+    }
+    int m = min(L, p.budget);
+    if (m > static_cast<int64_t>(p.max_dst_blocks) * p.block_size) {  // no room in the new table
+        if (h == 0 && tid == 0) atomicOr(p.err, kErrNoSpace);
+        L = m = 0;
+    }
+    if (h == 0 && tid == 0) p.lens_out[b] = m;
+    for (int i = m + tid; i < p.budget; i += kSelectThreads) kept[i] = -1;
+    for (int64_t i = m + tid; i < p.score_tokens_out; i += kSelectThreads) out[i] = 0.f;
+    if (L <= p.budget) {
+        for (int i = tid; i < L; i += kSelectThreads) {
+            kept[i] = i;
+            out[i] = scores[i];
+        }
+        return;
+    }
+    // the others compete: [sinks, L - recent)
+    const int first = p.sinks, last = L - p.recent;
+    const bool cached = L <= kKeyTokens;
+    auto key_at = [&](int i) { return cached ? keys[i] : score_key(scores[i]); };
+    if (cached)
+        for (int i = tid; i < L; i += kSelectThreads) keys[i] = score_key(scores[i]);
+    uint32_t rest = p.budget - p.sinks - p.recent;  // of them this many stay
+    uint32_t found = 0, mask = 0;
+    if (rest == 0) {
+        found = 0xffffffffu;  // (no key: a NaN's is 0, +inf's 0xff800000)
+    } else {
+        for (int pass = 0; pass < 3; ++pass) {
+            const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
+            for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
+            __syncthreads();
+            for (int i = first + tid; i < last; i += kSelectThreads) {
+                const uint32_t k = key_at(i);
+                if ((k & mask) == found) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
+            }
+            __syncthreads();
+            // bins from the top, two a thread
+            const int hi = kBins - 1 - 2 * tid;
+            const uint32_t c1 = hist[hi], c0 = hist[hi - 1];
+            uint32_t all;
+            const uint32_t before = block_scan(c0 + c1, totals[pass & 1], all);
+            if (before < rest && rest <= before + c0 + c1) {
+                const bool upper = rest <= before + c1;
+                s_bin = upper ? hi : hi - 1;
+                s_rest = rest - before - (upper ? 0 : c1);
+            }
+            __syncthreads();
+            found |= s_bin << shift;
+            mask |= static_cast<uint32_t>(bins - 1) << shift;
+            rest = s_rest;
+        }
+    }
+    __syncthreads();
+    // keys above `found` stay, and the first `rest` equal to it
+    uint32_t above = 0, equal = 0;
+    for (int base = 0, turn = 0; base < L; base += 4 * kSelectThreads, ++turn) {
+        uint32_t flags = 0;  // 2 bits a token: 1 above, 2 equal
+        const int i0 = base + 4 * tid;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int i = i0 + j;
+            if (i >= L) continue;
+            const bool must = i < first || i >= last;
+            const uint32_t k = must ? 0 : key_at(i);
+            if (must || k > found) flags |= 1u << (2 * j);
+            else if (k == found) flags |= 2u << (2 * j);
+        }
+        const uint32_t mine = __popc(flags & 0x55u) | (__popc(flags & 0xaau) << 16);
+        uint32_t all;
+        const uint32_t before = block_scan(mine, totals[turn & 1], all);
+        uint32_t g = above + (before & 0xffffu), e = equal + (before >> 16);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const uint32_t f = (flags >> (2 * j)) & 3u;
+            if (f == 1 || (f == 2 && e < rest)) {
+                const uint32_t to = g + min(e, rest);
+                kept[to] = i0 + j;
+                out[to] = scores[i0 + j];
+            }
+            g += f == 1;
+            e += f == 2;
+        }
+        above += all & 0xffffu;
+        equal += all >> 16;
+    }
+}
+
+__global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
+    const int vecs = p.row_bytes / 16;  // 4, 8 or 16
+    const int rows = kMoveThreads / vecs;
+    const int b = blockIdx.z, h = blockIdx.y;
+    const int i = blockIdx.x * rows + threadIdx.x / vecs, c = threadIdx.x % vecs;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (i >= p.budget) return;
+    const int from = p.kept[(static_cast<int64_t>(b) * p.num_kv_heads + h) * p.budget + i];
+    if (from < 0) return;
+    const int src = p.block_tables[static_cast<int64_t>(b) * p.max_blocks_per_seq + from / p.block_size];
+    const int dst = p.dst_tables[static_cast<int64_t>(b) * p.max_dst_blocks + i / p.block_size];
+    if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
+        if (c == 0) atomicOr(p.err, kErrBadBlock);
+        return;
+    }
+    const int64_t s = ((static_cast<int64_t>(src) * p.num_kv_heads + h) * p.block_size + from % p.block_size) * vecs + c;
+    const int64_t d = ((static_cast<int64_t>(dst) * p.num_kv_heads + h) * p.block_size + i % p.block_size) * vecs + c;
+    const uint4 k = static_cast<const uint4*>(p.k_cache)[s], v = static_cast<const uint4*>(p.v_cache)[s];
+    static_cast<uint4*>(p.k_cache)[d] = k;
+    static_cast<uint4*>(p.v_cache)[d] = v;
+}
+
+// scores += sum over the group's heads of 2^(logit - M) / l, (M, l) the
+// statistics of the head's partitions joined.  One thread a token.
+__global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const AddWeightsParams p) {
+    __shared__ float s_max[8], s_inv[8];
+    const int seq = blockIdx.z, kvh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int L = p.context_lens[seq];
+    if (L < 1 || L > p.max_context) return;  // flagged before
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kAddThreads;
+    if (first >= L) return;
+    const int parts = (L + p.partition_size - 1) / p.partition_size;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (warp < p.group) {
+        const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) +
+                           ((static_cast<int64_t>(seq) * p.num_kv_heads + kvh) * p.group + warp) * p.max_parts;
+        float M = -INFINITY, l = 0.f;
+        for (int i = lane; i < parts; i += 32) M = fmaxf(M, ml[i].x);
+        M = warp_max(M);
+        for (int i = lane; i < parts; i += 32) l += ml[i].y * fast_exp2(ml[i].x - M);
+#pragma unroll
+        for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
+        if (lane == 0) {
+            s_max[warp] = M;
+            s_inv[warp] = 1.f / l;
+        }
+    }
+    __syncthreads();
+    const int64_t t = first + threadIdx.x;
+    if (t >= L) return;
+    const int64_t row = static_cast<int64_t>(seq) * p.num_kv_heads + kvh;
+    const float* x = p.logits + (row * p.logit_tokens + t) * p.group;
+    float sum = 0.f;
+    for (int g = 0; g < p.group; ++g) sum += fast_exp2(x[g] - s_max[g]) * s_inv[g];
+    p.scores[row * p.score_tokens + t] += sum;
+}
+
+template <class Params>
+cudaError_t launch_after(void (*kernel)(const Params), const Params& p, dim3 grid, int threads, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
+    static bool configured[kMaxDevices] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
+    if (!configured[dev]) {
+        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyTokens * 4);
+        if (e != cudaSuccess) return e;
+        configured[dev] = true;
+    }
+    const int64_t most = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
+    const int smem = static_cast<int>((most < kKeyTokens ? most : kKeyTokens) * 4);
+    evict_select_kernel<<<dim3(p.num_kv_heads, p.num_seqs), kSelectThreads, smem, stream>>>(p);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    const int rows = kMoveThreads / (p.row_bytes / 16);
+    const dim3 grid((p.budget + rows - 1) / rows, p.num_kv_heads, p.num_seqs);
+    return launch_after(evict_move_kernel, p, grid, kMoveThreads, stream);
+}
+
+cudaError_t launch_add_weights(const AddWeightsParams& p, cudaStream_t stream) {
+    const dim3 grid((p.max_context + kAddThreads - 1) / kAddThreads, p.num_kv_heads, p.num_seqs);
+    return launch_after(add_weights_kernel, p, grid, kAddThreads, stream);
+}
+
+}  // namespace pkv

@@ -150,7 +150,29 @@ struct DecodeParams {
     int partition_size;  // tokens per partition, a multiple of 32 and of the block size
     int max_parts;
     float scale_log2;  // scale * log2(e)
+    // the extended kernels (EXT) alone; lengths and partitions count the tokens of windowed_len then
+    int window;      // the last `window` tokens and the first `sinks` are seen; 0: all
+    int sinks;
+    float* logits;   // [num_seqs][num_kv_heads][logit_tokens][G], in log2 units; null: not kept
+    int64_t logit_tokens;
 };
+
+// Tokens that a sequence of L keeps when the blocks wholly between its first
+// `sinks` tokens and its last `window` ones are left out, so that the others
+// are numbered through: token v of the result is token v in the first blocks,
+// v + L - windowed_len behind them.  The hidden ones left, inside the blocks at
+// either edge, are those with sinks <= v < windowed_len - window; every block
+// left has a visible token (it holds a first token, the window's first one, or
+// one between that and the last).
+#ifdef __CUDACC__
+__host__ __device__
+#endif
+inline int windowed_len(int L, int window, int sinks, int block_size) {
+    if (window == 0 || L <= window) return L;
+    const int first = sinks / block_size + (sinks % block_size != 0);  // blocks of the first tokens
+    const int from = (L - window) / block_size;                        // the window's first block
+    return from > first ? L - (from - first) * block_size : L;
+}
 
 struct MergeParams {
     const int32_t* context_lens;
@@ -166,6 +188,77 @@ struct MergeParams {
     int partition_size;
     int max_parts;
     int max_context;
+    int window;  // as in DecodeParams, 0: none
+    int sinks;
+    int block_size;
+};
+
+// scores[seq][kvh][token] += sum over the group's heads of their weights.
+struct AddWeightsParams {
+    const float* logits;  // [num_seqs][num_kv_heads][logit_tokens][group], log2 units
+    const float* ws_ml;   // [num_seqs][num_kv_heads * group][max_parts][2]
+    const int32_t* context_lens;
+    float* scores;        // [num_seqs][num_kv_heads][score_tokens]
+    int64_t score_tokens;
+    int64_t logit_tokens;
+    int num_seqs;
+    int num_kv_heads;
+    int group;
+    int partition_size;
+    int max_parts;
+    int max_context;
+};
+
+// The tokens that stay and their move to other blocks (evict.cu).
+struct EvictParams {
+    void* k_cache;
+    void* v_cache;
+    const float* scores;  // [num_seqs][num_kv_heads][score_tokens]
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* dst_tables;
+    float* scores_out;
+    int32_t* lens_out;
+    int32_t* kept;  // [num_seqs][num_kv_heads][budget]
+    int* err;
+    int64_t score_tokens;
+    int64_t score_tokens_out;
+    int max_blocks_per_seq;
+    int max_dst_blocks;
+    int num_seqs;
+    int num_kv_heads;
+    int block_size;
+    int num_blocks;
+    int row_bytes;  // head_dim elements
+    int budget;
+    int recent;
+    int sinks;
+};
+
+// Attention of each sequence's new tokens over the cache (chunk.cu).
+struct ChunkParams {
+    const void* q;
+    int64_t q_stride;  // elements from one token's row to the next
+    const void* k_cache;
+    const void* v_cache;
+    const int32_t* block_tables;
+    const int32_t* context_lens;
+    const int32_t* seq_starts;  // [num_seqs + 1]
+    void* out;
+    int64_t out_stride;
+    const float* k_scale;  // E4M3: one, or with block scales [num_blocks][num_kv_heads]
+    const float* v_scale;
+    int* err;
+    int max_blocks_per_seq;
+    int num_seqs;
+    int num_tokens;  // rows of q and out
+    int num_q_heads;
+    int num_kv_heads;
+    int block_size;
+    int num_blocks;
+    int window;  // 0: none
+    int sinks;
+    float scale_log2;
 };
 
 struct QuestMetaParams {
@@ -231,11 +324,17 @@ cudaError_t launch_selftest_wait(uint64_t limit_ns, int* err, cudaStream_t strea
 // Partition kernel for one (act, cache) pair; returns cudaErrorInvalidValue
 // for a (head_dim, block_size, group) it was not built for.
 cudaError_t launch_decode_f16_f16(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_ext_f16_f16(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_bf16_bf16(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_ext_bf16_bf16(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_f16_e4m3(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_ext_f16_e4m3(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_bf16_e4m3(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_ext_bf16_e4m3(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_f16_e4m3b(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_ext_f16_e4m3b(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_bf16_e4m3b(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_ext_bf16_e4m3b(const DecodeParams& p, int D, int BS, int G, cudaStream_t s);
 
 // Tensor-core grouped-query path (head_dim 128 with a 16-bit or E4M3 cache
 // of either scaling, or head_dim 64 with a 16-bit cache, an even kv-head count
@@ -251,5 +350,16 @@ cudaError_t launch_decode_tc_e4m3(const DecodeParams& p, int act, int BS, int G,
 cudaError_t launch_decode_tc_e4m3b(const DecodeParams& p, int act, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_tc_e4m3b_d64(const DecodeParams& p, int act, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_tc_d64(const DecodeParams& p, int act, int BS, int G, int variant, cudaStream_t s);
+
+// The same with a window or kept logits (tables shared by a sequence's kv heads).
+int decode_tc_ext_max_rows();
+cudaError_t launch_decode_tc_ext(const DecodeParams& p, int act, int cache, int head_dim, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_tc_ext_e4m3(const DecodeParams& p, int act, int BS, int G, cudaStream_t s);
+cudaError_t launch_decode_tc_ext_e4m3b(const DecodeParams& p, int act, int head_dim, int BS, int G, cudaStream_t s);
+
+// Adds each token's weights, from kept logits and the partitions' statistics, to its scores.
+cudaError_t launch_add_weights(const AddWeightsParams& p, cudaStream_t stream);
+cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
+cudaError_t launch_chunk(const ChunkParams& p, int act, int cache, int head_dim, cudaStream_t stream);
 
 }  // namespace pkv

@@ -232,10 +232,10 @@ __global__ void __launch_bounds__(32 * kMergeWarps) paged_decode_merge_kernel(Me
         int h;
         divmod_u(row, p.num_q_heads, seq64, h);
         const int seq = static_cast<int>(seq64);
-        const int L =
-            p.context_lens[static_cast<int64_t>(seq) * p.lens_seq_stride + (h / p.group) * p.lens_kvh_stride];
+        int L = p.context_lens[static_cast<int64_t>(seq) * p.lens_seq_stride + (h / p.group) * p.lens_kvh_stride];
         // a bad length was flagged by the partition kernel; one partition was written directly
         active = L >= 1 && L <= p.max_context;
+        if (active) L = windowed_len(L, p.window, p.sinks, p.block_size);
         n_parts = active ? (L + p.partition_size - 1) / p.partition_size : 0;
         active = n_parts > 1;
     }
