@@ -660,9 +660,14 @@ int paged_kv_evict(void* k_cache, void* v_cache, int num_blocks, int num_kv_head
 
 size_t pkv_chunk_workspace_size(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int head_dim,
                                 int max_blocks_per_seq, int block_size) {
-    (void)num_seqs, (void)num_tokens, (void)num_q_heads, (void)num_kv_heads, (void)head_dim, (void)max_blocks_per_seq,
-        (void)block_size;
-    return kWorkspaceHeader;
+    if (num_seqs <= 0 || num_tokens <= 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 ||
+        max_blocks_per_seq <= 0 || block_size <= 0 || num_q_heads < num_kv_heads)
+        return kWorkspaceHeader;
+    const int splits = chunk_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                    static_cast<int64_t>(max_blocks_per_seq) * block_size);
+    if (splits == 1) return kWorkspaceHeader;
+    const size_t rows = static_cast<size_t>(splits) * num_tokens * num_q_heads;
+    return kWorkspaceHeader + align_up(rows * 2 * sizeof(float), 256) + rows * head_dim * sizeof(float);
 }
 
 int paged_attention_chunk(const void* q, int64_t q_stride, const void* k_cache, const void* v_cache,
@@ -733,6 +738,16 @@ int paged_attention_chunk(const void* q, int64_t q_stride, const void* k_cache, 
     p.window = window;
     p.sinks = sinks;
     p.scale_log2 = scale * 1.4426950408889634f;
+    // a window's tokens alone are shared out (never more shares than the workspace was sized for)
+    const int64_t context = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+    p.splits = chunk_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                            window ? std::min<int64_t>(context, static_cast<int64_t>(window) + sinks) : context);
+    if (p.splits > 1) {
+        char* ws = static_cast<char*>(workspace) + kWorkspaceHeader;
+        const size_t rows = static_cast<size_t>(p.splits) * num_tokens * num_q_heads;
+        p.ws_ml = reinterpret_cast<float*>(ws);
+        p.ws_o = reinterpret_cast<float*>(ws + align_up(rows * 2 * sizeof(float), 256));
+    }
     if (!p.err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");
     const cudaError_t e = launch_chunk(p, act_dtype, blocks ? kCacheE4M3Blocks : cache_dtype, head_dim,
                                        static_cast<cudaStream_t>(stream));

@@ -107,6 +107,7 @@ cudaError_t launch_cache(const ChunkParams& p, int cache, int D, cudaStream_t s)
 }  // namespace
 
 cudaError_t launch_chunk(const ChunkParams& p, int act, int cache, int head_dim, cudaStream_t s) {
+    if (cache == act) return launch_chunk_tc(p, act, head_dim, s);
     return act == kBF16 ? launch_cache<kBF16>(p, cache, head_dim, s) : launch_cache<kF16>(p, cache, head_dim, s);
 }
 

@@ -259,6 +259,9 @@ struct ChunkParams {
     int window;  // 0: none
     int sinks;
     float scale_log2;
+    int splits;   // shares of an item's token tiles, each a block's; 1: none
+    float* ws_ml;  // [splits][num_tokens][num_q_heads][2]: (reference maximum in log2 units, sum); null: one share
+    float* ws_o;   // [splits][num_tokens][num_q_heads][head_dim]: sums relative to the maximum
 };
 
 struct QuestMetaParams {
@@ -361,5 +364,8 @@ cudaError_t launch_decode_tc_ext_e4m3b(const DecodeParams& p, int act, int head_
 cudaError_t launch_add_weights(const AddWeightsParams& p, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 cudaError_t launch_chunk(const ChunkParams& p, int act, int cache, int head_dim, cudaStream_t stream);
+cudaError_t launch_chunk_tc(const ChunkParams& p, int act, int head_dim, cudaStream_t stream);
+// Shares that an item's token tiles are split into (a function of the sizes).
+int chunk_splits(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int64_t max_context);
 
 }  // namespace pkv
