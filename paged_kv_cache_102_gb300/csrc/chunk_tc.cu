@@ -82,28 +82,30 @@ __global__ void __launch_bounds__(kMergeThreads) paged_chunk_merge_kernel(const 
     for (int x = 0; x < W; ++x) dst[x] = float_to_act<ACT>(acc[x] / l);
 }
 
-template <int ACT, int D>
+template <int ACT, int CACHE, int D>
 cudaError_t launch_one(const ChunkParams& p, cudaStream_t s) {
-    auto kern = paged_chunk_tc_kernel<ACT, D>;
+    auto kern = paged_chunk_tc_kernel<ACT, CACHE, D>;
     static bool configured[kMaxDevices] = {};
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<D>::BYTES);
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, ChunkSmem<CACHE, D>::BYTES);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
     const uint64_t cache_rows = static_cast<uint64_t>(p.num_blocks) * p.num_kv_heads * p.block_size;
     CUtensorMap km, vm, qm;
-    if (!cache_map(&km, p.k_cache, ACT, D, cache_rows, p.block_size) ||
-        !cache_map(&vm, p.v_cache, ACT, D, cache_rows, p.block_size) || !query_map(&qm, p, ACT, D))
+    if (!query_map(&qm, p, ACT, D)) return cudaErrorInvalidValue;
+    if (is_e4m3(CACHE)) km = vm = qm;  // codes are copied without
+    else if (!cache_map(&km, p.k_cache, ACT, D, cache_rows, p.block_size) ||
+             !cache_map(&vm, p.v_cache, ACT, D, cache_rows, p.block_size))
         return cudaErrorInvalidValue;
     const int R = 2 * (kChunkTile / (p.num_q_heads / p.num_kv_heads));
     const int64_t blocks = (static_cast<int64_t>(p.num_tokens) / R + p.num_seqs) * p.num_kv_heads;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    kern<<<dim3(static_cast<unsigned>(blocks), p.splits), kChunkThreads, ChunkSmem<D>::BYTES, s>>>(km, vm, qm, p);
+    kern<<<dim3(static_cast<unsigned>(blocks), p.splits), chunk_threads(CACHE), ChunkSmem<CACHE, D>::BYTES, s>>>(km, vm, qm, p);
     e = cudaGetLastError();
     if (e != cudaSuccess || p.splits == 1) return e;
     const int64_t rows = static_cast<int64_t>(p.num_tokens) * p.num_q_heads;
@@ -129,9 +131,24 @@ int chunk_splits(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({want, max_context / kChunkSplitTokens, kChunkMaxSplits})));
 }
 
-cudaError_t launch_chunk_tc(const ChunkParams& p, int act, int head_dim, cudaStream_t s) {
-    if (head_dim == 64) return act == kBF16 ? launch_one<kBF16, 64>(p, s) : launch_one<kF16, 64>(p, s);
-    return act == kBF16 ? launch_one<kBF16, 128>(p, s) : launch_one<kF16, 128>(p, s);
+namespace {
+
+template <int ACT, int CACHE>
+cudaError_t by_dim(const ChunkParams& p, int head_dim, cudaStream_t s) {
+    return head_dim == 64 ? launch_one<ACT, CACHE, 64>(p, s) : launch_one<ACT, CACHE, 128>(p, s);
+}
+
+template <int ACT>
+cudaError_t by_cache(const ChunkParams& p, int cache, int head_dim, cudaStream_t s) {
+    if (cache == kE4M3) return by_dim<ACT, kE4M3>(p, head_dim, s);
+    if (cache == kE4M3B) return by_dim<ACT, kE4M3B>(p, head_dim, s);
+    return by_dim<ACT, ACT>(p, head_dim, s);
+}
+
+}  // namespace
+
+cudaError_t launch_chunk(const ChunkParams& p, int act, int cache, int head_dim, cudaStream_t s) {
+    return act == kBF16 ? by_cache<kBF16>(p, cache, head_dim, s) : by_cache<kF16>(p, cache, head_dim, s);
 }
 
 }  // namespace pkv

@@ -28,6 +28,16 @@
 //                  0 times it must be 0); a number that is not finite among the
 //                  others sends the item to the plain loop at the end, since a
 //                  weight of 0 would carry it to rows that do not see it.
+//  warps 12-15     E4M3 caches: conversion.  The producers copy the codes (one bulk
+//                  copy a block) into a ring of their own; these warps write them
+//                  as 16-bit elements, exactly, into the ring that the products
+//                  read, and do warp 11's work on the way.  One scale per tensor
+//                  joins the logits' factor and the output's.  Block scales: the
+//                  K producer leaves a tile's scales in shared memory; a logit is
+//                  multiplied by its block's K scale, and a weight, for the product
+//                  alone, by vs 2^(m - R), R the running maximum of a row's logits
+//                  plus log2 |vs|: O is a sum in units of 2^R whose largest term
+//                  is about 1, however far apart the scales are.
 // Every barrier wait is bounded (kWaitLimitNs); on a timeout the block stops,
 // drains its copies and products, frees tensor memory and reports kErrTimeout.
 #pragma once
@@ -37,21 +47,31 @@
 
 namespace pkv {
 
-constexpr int kChunkThreads = 384;
+__host__ __device__ constexpr int chunk_threads(int cache) { return is_e4m3(cache) ? 512 : 384; }
 constexpr int kChunkTile = 128;       // tokens of a tile
 constexpr int kChunkTmemCols = 512;   // two S (128 columns each, P over them), two O
 constexpr float kChunkRescale = 8.f;  // log2 by which a maximum may pass the reference
 
-template <int D>
+template <int CACHE, int D>
 struct ChunkSmem {
+    static constexpr bool E8 = is_e4m3(CACHE);
     static constexpr int HALVES = D / 64;
     static constexpr int STG = kChunkTile * D * 2;  // a K or V tile: per 64 channels 128 rows of 128 bytes
-    static constexpr int NS = D == 128 ? 5 : 8;
+    static constexpr int NS = E8 ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);
+    static constexpr int CSTG = kChunkTile * D;  // its codes
+    static constexpr int NC = E8 ? (D == 128 ? 4 : 6) : 0;
+    // Scales of a tile: [8] K scales, [8] V scales, [8] log2 |V scale|.  Entry i % SLOTS is written again for
+    // tile i + SLOTS, once the codes of K tile use 2 (i + SLOTS) - NC were converted, for which the stage of use
+    // 2 (i + SLOTS) - NC - NS >= 2 i + 1 was free: V tile i's, so that softmax(i) was over.
+    static constexpr int SLOTS = CACHE == kE4M3B ? (NC + NS + 2) / 2 : 0;
     static constexpr int QT = kChunkTile * D * 2;
     static constexpr int RING = 0;
     static constexpr int Q = NS * STG;
-    static constexpr int BARS = Q + 2 * QT;
-    static constexpr int NBARS = 3 * NS + 8;  // full, empty, v_ok, q_full, s_full[2], p_full[2], o_done[2], final
+    static constexpr int CODES = Q + 2 * QT;
+    static constexpr int SCALES = CODES + NC * CSTG;
+    static constexpr int BARS = SCALES + SLOTS * 24 * 4;
+    // full, empty, v_ok [NS]; c_full, c_empty [NC]; q_full, s_full[2], p_full[2], o_done[2], final
+    static constexpr int NBARS = 3 * NS + 2 * NC + 8;
     static constexpr int MISC = BARS + NBARS * 8;
     static constexpr int BYTES = MISC + 64 + 1024;  // room to align the base
     static_assert(BYTES <= 227 * 1024, "shared memory of a block");
@@ -127,12 +147,26 @@ __device__ __forceinline__ uint32_t pack_act(float a, float b) {
     }
 }
 
-template <int ACT, int D>
-__global__ void __launch_bounds__(kChunkThreads, 1)
+// One element of a cache, without its scale.
+template <int CACHE>
+__device__ __forceinline__ float cache_element(const void* base, int64_t i) {
+    if constexpr (is_e4m3(CACHE)) {
+        const __half_raw h = __nv_cvt_fp8_to_halfraw(static_cast<const uint8_t*>(base)[i], __NV_E4M3);
+        return __half2float(*reinterpret_cast<const __half*>(&h));
+    } else {
+        return act_to_float<CACHE>(static_cast<const uint16_t*>(base)[i]);
+    }
+}
+
+template <int ACT, int CACHE, int D>
+__global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     paged_chunk_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const __grid_constant__ CUtensorMap qmap, const ChunkParams p) {
-    using S = ChunkSmem<D>;
+    using S = ChunkSmem<CACHE, D>;
+    constexpr bool E8 = S::E8, SCALED = CACHE == kE4M3B;
+    constexpr int THREADS = chunk_threads(CACHE);
     constexpr int NS = S::NS, STG = S::STG, HALVES = S::HALVES, HALF = kChunkTile * 128;
+    constexpr int NP = E8 ? S::NC : NS;  // stages of the ring that the producers fill
     constexpr uint32_t IDESC_S = tc::idesc_f16(128, kChunkTile, ACT == kBF16, false, false);
     constexpr uint32_t IDESC_O = tc::idesc_f16(128, D, ACT == kBF16, false, true);
     constexpr int O_COL = 2 * kChunkTile;  // first column of O_0; O_1 D further
@@ -145,7 +179,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + S::BARS);
     uint64_t* empty = full + NS;
     uint64_t* v_ok = empty + NS;
-    uint64_t* q_full = v_ok + NS;
+    uint64_t* c_full = v_ok + NS;
+    uint64_t* c_empty = c_full + S::NC;
+    uint64_t* q_full = c_empty + S::NC;
     uint64_t* s_full = q_full + 1;
     uint64_t* p_full = s_full + 2;
     uint64_t* o_done = p_full + 2;
@@ -172,9 +208,13 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         tc::tmem_relinquish();
     } else if (threadIdx.x == 9 * 32) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], 1);
+            mbar_init(&full[i], E8 ? 4 : 1);
             mbar_init(&empty[i], 1);
             mbar_init(&v_ok[i], 1);
+        }
+        for (int i = 0; i < S::NC; ++i) {
+            mbar_init(&c_full[i], 1);
+            mbar_init(&c_empty[i], 4);
         }
         mbar_init(q_full, 1);
         for (int t = 0; t < 2; ++t) {
@@ -186,8 +226,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         *abort_flag = 0;
         *plain_flag = 0;
         mbar_init_fence();
-        tc::prefetch_tensormap(&kmap);
-        tc::prefetch_tensormap(&vmap);
+        if constexpr (!E8) {
+            tc::prefetch_tensormap(&kmap);
+            tc::prefetch_tensormap(&vmap);
+        }
         tc::prefetch_tensormap(&qmap);
     }
     tc::fence_before_sync();
@@ -239,45 +281,74 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         const int pos_lo = it.pos0 + t * TQ, pos_hi = pos_lo + rows_of(t) - 1;  // of the row tile
         const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * kChunkTile;
         const uint32_t o_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + O_COL + t * D;
-        const float c = fmaxf(fabsf(p.scale_log2), 1e-37f);  // (times -inf: never a NaN, at a scale of 0 either)
-        const bool negative = p.scale_log2 < 0.f;
-        float m = -INFINITY, l = 0.f;  // reference maximum (log2 units) and sum
+        const float factor = CACHE == kE4M3 ? p.scale_log2 * *p.k_scale : p.scale_log2;
+        const float c = SCALED ? 1.f : fmaxf(fabsf(factor), 1e-37f);  // (times -inf: never a NaN, at a factor of 0 either)
+        const bool negative = !SCALED && factor < 0.f;
+        // reference maximum (log2 units) and sum; block scales: of the logits plus log2 |vs|, the unit of O
+        float m = -INFINITY, l = 0.f;
+        [[maybe_unused]] float unit = -INFINITY;
         bool ok = true;
         for (int i = 0; i < cnt && ok; ++i) {
             ok = __all_sync(0xffffffffu, chunk_wait(&s_full[t], i & 1, abort_flag, p.err));
             if (!ok) break;
             tc::fence_after_sync();
             if (live) {
-                float s[kChunkTile];
-#pragma unroll
-                for (int k = 0; k < kChunkTile; k += 32) tc::TmemLd<32>::load(s_addr + k, s + k);
-                tc::tmem_wait_ld();
-                if (negative) {
-#pragma unroll
-                    for (int k = 0; k < kChunkTile; ++k) s[k] = -s[k];
-                }
                 const int start = chunk_tile_start(it, it.i0 + i);
-                if (start + kChunkTile - 1 > pos_lo ||
-                    (p.window != 0 && start <= pos_hi - p.window && start + kChunkTile > p.sinks)) {
-                    const int end = pos - start;                            // sees columns up to this one
-                    const int from = p.window ? end - p.window + 1 : 0;     // and from this one on,
-                    const int sink = p.sinks - start;                       // or before this one
+                const bool masked = start + kChunkTile - 1 > pos_lo ||
+                                    (p.window != 0 && start <= pos_hi - p.window && start + kChunkTile > p.sinks);
+                const int end = pos - start;                         // sees columns up to this one
+                const int from = p.window ? end - p.window + 1 : 0;  // and from this one on,
+                const int sink = p.sinks - start;                    // or before this one
+                [[maybe_unused]] const float* scales =
+                    reinterpret_cast<const float*>(sm + S::SCALES) + (SCALED ? (i % max(1, S::SLOTS)) * 24 : 0);
+                [[maybe_unused]] const int bshift = p.block_size == 32 ? 1 : 0;  // 16-column groups to blocks
+                // 32 scores from column k on, in what `c` makes log2 units
+                auto scores = [&](int k, float* s) {
+                    tc::TmemLd<32>::load(s_addr + k, s);
+                    tc::tmem_wait_ld();
+                    if constexpr (SCALED) {
 #pragma unroll
-                    for (int k = 0; k < kChunkTile; ++k)
-                        if (k > end || (k < from && k >= sink)) s[k] = -INFINITY;
+                        for (int x = 0; x < 32; x += 16) {
+                            const float f = factor * scales[((k + x) >> 4) >> bshift];
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) s[x + j] *= f;
+                        }
+                    } else if (negative) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) s[j] = -s[j];
+                    }
+                    if (masked) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (k + j > end || (k + j < from && k + j >= sink)) s[j] = -INFINITY;
+                    }
+                };
+                // 16-bit caches hold a row's scores; the others, with fewer registers a thread, read them twice
+                float s[E8 ? 32 : kChunkTile];
+                float mx = -INFINITY;
+                [[maybe_unused]] float mu = -INFINITY;
+#pragma unroll
+                for (int k = 0; k < kChunkTile; k += 32) {
+                    float* x = s + (E8 ? 0 : k);
+                    scores(k, x);
+#pragma unroll
+                    for (int y = 0; y < 32; y += 16) {
+                        float top = x[y];
+#pragma unroll
+                        for (int j = 1; j < 16; ++j) top = fmaxf(top, x[y + j]);
+                        mx = fmaxf(mx, top);
+                        if constexpr (SCALED) mu = fmaxf(mu, top + scales[16 + (((k + y) >> 4) >> bshift)]);
+                    }
                 }
-                float mx = s[0];
-#pragma unroll
-                for (int k = 1; k < kChunkTile; ++k) mx = fmaxf(mx, s[k]);
                 mx *= c;
                 const bool move = mine && mx > m + kChunkRescale;
-                if (__any_sync(0xffffffffu, move && l > 0.f)) {
+                const bool turn = SCALED ? mine && mu > unit + kChunkRescale : move;
+                if (__any_sync(0xffffffffu, turn && l > 0.f)) {
                     // O holds the tiles before: their products are done, then the row is multiplied
                     ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (i - 1) & 1, abort_flag, p.err));
                     if (!ok) break;
                     tc::fence_after_sync();
-                    const float f = move ? fast_exp2(m - mx) : 1.f;
-                    l *= f;
+                    const float f = !turn ? 1.f : SCALED ? fast_exp2(unit - mu) : fast_exp2(m - mx);
 #pragma unroll
                     for (int k = 0; k < D; k += 8) {
                         float o[8];
@@ -288,21 +359,37 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                         tc::tmem_st<8>(o_addr + k, o);
                     }
                 }
-                if (move) m = mx;
+                if (move) {
+                    l *= fast_exp2(m - mx);  // (0 times what it is at first)
+                    m = mx;
+                }
+                if (SCALED && turn) unit = mu;
                 const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of 0
+                [[maybe_unused]] const float lift = SCALED && unit != -INFINITY ? fast_exp2(ref - unit) : 0.f;
                 float sum0 = 0.f, sum1 = 0.f;
 #pragma unroll
-                for (int k = 0; k < kChunkTile; k += 64) {
-                    uint32_t w[32];
+                for (int k = 0; k < kChunkTile; k += 32) {
+                    float* x = s + (E8 ? 0 : k);
+                    if constexpr (E8) scores(k, x);
+                    uint32_t w[16];
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) {
-                        const float a = fast_exp2(fmaf(s[k + 2 * j], c, -ref));
-                        const float b = fast_exp2(fmaf(s[k + 2 * j + 1], c, -ref));
-                        sum0 += a;
-                        sum1 += b;
-                        w[j] = pack_act<ACT>(a, b);
+                    for (int y = 0; y < 32; y += 16) {
+                        [[maybe_unused]] float vf = 1.f;
+                        if constexpr (SCALED) vf = lift * scales[8 + (((k + y) >> 4) >> bshift)];
+#pragma unroll
+                        for (int j = 0; j < 16; j += 2) {
+                            float a = fast_exp2(fmaf(x[y + j], c, -ref));
+                            float b = fast_exp2(fmaf(x[y + j + 1], c, -ref));
+                            sum0 += a;
+                            sum1 += b;
+                            if constexpr (SCALED) {
+                                a *= vf;
+                                b *= vf;
+                            }
+                            w[(y + j) / 2] = pack_act<ACT>(a, b);
+                        }
                     }
-                    tc::tmem_st32(s_addr + k / 2, w);
+                    tc::tmem_st16(s_addr + k / 2, w);
                 }
                 l += sum0 + sum1;
                 tc::tmem_wait_st();
@@ -316,6 +403,10 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             tc::fence_after_sync();
         }
         if (ok && live && any) {
+            // what an element of O stands for
+            float vmul = 1.f;
+            if constexpr (CACHE == kE4M3) vmul = *p.v_scale;
+            if constexpr (SCALED) vmul = unit == -INFINITY ? 0.f : fast_exp2(unit - m);
             const int64_t at = it.row0 + t * TQ + tok;
             const int h = it.kvh * G + g;
             if (p.ws_ml != nullptr) {
@@ -331,11 +422,11 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (mine && cnt > 0) {
                         float4* dst = reinterpret_cast<float4*>(p.ws_o + slot_row * D + k);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                        for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j] * vmul, o[4 * j + 1] * vmul, o[4 * j + 2] * vmul, o[4 * j + 3] * vmul);
                     }
                 }
             } else {
-                const float inv = 1.f / l;
+                const float inv = vmul / l;
                 uint16_t* dst = static_cast<uint16_t*>(p.out) + at * p.out_stride + static_cast<int64_t>(h) * D;
 #pragma unroll
                 for (int k = 0; k < D; k += 32) {
@@ -393,7 +484,8 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
             const int uv = 2 * i + 1, uk = 2 * i + 2;
             const int sv = uv % NS, sk = uk % NS;
             const bool more = i + 1 < n_run;
-            ok = __all_sync(0xffffffffu, chunk_wait(&v_ok[i % NS], (i / NS) & 1, abort_flag, p.err));
+            ok = __all_sync(0xffffffffu, E8 ? chunk_wait(&full[sv], (uv / NS) & 1, abort_flag, p.err)
+                                            : chunk_wait(&v_ok[i % NS], (i / NS) & 1, abort_flag, p.err));
             if (!ok) break;
             if (more) ok = __all_sync(0xffffffffu, chunk_wait(&full[sk], (uk / NS) & 1, abort_flag, p.err));
             if (!ok) break;
@@ -442,7 +534,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         const int BS = p.block_size, bpt = kChunkTile / BS;
         const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
-        const int j = lane / HALVES, h = lane % HALVES;  // block of the tile and 64-channel part of this lane
+        // block of the tile and 64-channel part of this lane (codes: the whole block)
+        constexpr int PARTS = E8 ? 1 : HALVES;
+        const int j = lane / PARTS, h = lane % PARTS;
         // the lane's block in tile i: -1 past the last row's tokens, wholly hidden, or outside the pool
         auto entry = [&](int i) {
             if (i >= n_run || j >= bpt) return -1;
@@ -458,16 +552,40 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         int phys = entry(0);
         int issued = 0;
         for (int i = 0; i < n_run; ++i) {
-            const int use = 2 * i + v, s = use % NS;
+            const int use = 2 * i + v, s = use % NP;
+            uint64_t* filled = E8 ? &c_full[s] : &full[s];
             const int next = entry(i + 1);
+            [[maybe_unused]] float ks = 0.f, vs = 0.f;
+            if (SCALED && v == 0 && phys >= 0) {
+                const int64_t at = static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh;
+                ks = p.k_scale[at];
+                vs = p.v_scale[at];
+            }
             const unsigned loads = __ballot_sync(0xffffffffu, phys >= 0);
             bool good = true;
-            if (lane == 0) {
-                if (use >= NS) good = chunk_wait(&empty[s], (use / NS - 1) & 1, abort_flag, p.err);
-                if (good) mbar_arrive_expect_tx(&full[s], __popc(loads) * BS * 128);
-            }
+            if (lane == 0 && use >= NP)
+                good = chunk_wait(E8 ? &c_empty[s] : &empty[s], (use / NP - 1) & 1, abort_flag, p.err);
             if (!__shfl_sync(0xffffffffu, good, 0)) break;
-            if (phys >= 0)
+            if constexpr (SCALED) {
+                if (v == 0) {
+                    if (lane < 8) {
+                        float* dst = reinterpret_cast<float*>(sm + S::SCALES) + (i % S::SLOTS) * 24 + lane;
+                        dst[0] = ks;
+                        dst[8] = vs;
+                        dst[16] = fmaxf(__log2f(fabsf(vs)), -100.f);
+                    }
+                    __syncwarp();  // before the copies' barrier, which the softmax waits on in the end
+                }
+            }
+            if (lane == 0) mbar_arrive_expect_tx(filled, __popc(loads) * (E8 ? BS * D : BS * 128));
+            __syncwarp();
+            if constexpr (E8) {
+                if (phys >= 0)
+                    bulk_copy_g2s(sm + S::CODES + s * S::CSTG + j * BS * D,
+                                  static_cast<const unsigned char*>(v ? p.v_cache : p.k_cache) +
+                                      (static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh) * (BS * D),
+                                  BS * D, filled, policy);
+            } else if (phys >= 0)
                 tc::tma_load_2d(ring + s * STG + h * HALF + j * BS * 128, map, h * 64, (phys * p.num_kv_heads + it.kvh) * BS,
                                 &full[s], policy);
             phys = next;
@@ -475,14 +593,73 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
         }
         // leave only when every copy into this block's shared memory has landed
         if (lane == 0) {
-            for (int i = max(0, issued - NS); i < issued; ++i) {
+            for (int i = max(0, issued - NP); i < issued; ++i) {
                 const int use = 2 * i + v;
-                if (use + NS >= 2 * issued && !mbar_wait(&full[use % NS], (use / NS) & 1)) atomicOr(p.err, kErrTimeout);
+                if (use + NP >= 2 * issued && !mbar_wait(E8 ? &c_full[use % NP] : &full[use % NP], (use / NP) & 1))
+                    atomicOr(p.err, kErrTimeout);
             }
             if (v == 0 && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
-    } else {
+    } else if (E8 && warp >= 12) {
+        // --------------------------------------------------------- conversion
+        // 16 codes a lane and step.  8 neighbouring lanes, which shared memory serves at once, take 64 channels of
+        // two tokens (head_dim 128: the other half of the second), so that neither their reads nor their writes,
+        // which the swizzle moves by one 16-byte chunk from token to token, meet in a bank.
+        if constexpr (E8) {
+            for (int u = 0; u < 2 * n_run; ++u) {
+                const int cs = u % S::NC, s = u % NS;
+                bool good = chunk_wait(&c_full[cs], (u / S::NC) & 1, abort_flag, p.err);
+                if (good && u >= NS) good = chunk_wait(&empty[s], (u / NS - 1) & 1, abort_flag, p.err);
+                if (!__all_sync(0xffffffffu, good)) break;
+                const unsigned char* codes = sm + S::CODES + cs * S::CSTG;
+                unsigned char* dst = ring + s * STG;
+                const int start = chunk_tile_start(it, it.i0 + (u >> 1));
+                const int last_lo = p.window ? max(0, last - p.window + 1) : 0;
+                const bool partly = (u & 1) && (start + kChunkTile - 1 > it.pos0 || (start < last_lo && start + kChunkTile > p.sinks));
+                bool bad = false;
+                constexpr int TOKENS = 32 / (4 * HALVES);  // a warp's step
+#pragma unroll 4
+                for (int r0 = (warp - 12) * TOKENS; r0 < kChunkTile; r0 += 4 * TOKENS) {
+                    const int pair = lane & 15, second = (lane >> 2) & 1;
+                    const int r = r0 + (HALVES == 2 ? (lane >> 4) * 2 + second : lane >> 2);
+                    const int h = HALVES == 2 ? ((pair >> 3) ^ second) : 0;
+                    const int x = (lane & 3) * 2;  // first of two 8-channel chunks of the part
+                    uint4 c = *reinterpret_cast<const uint4*>(codes + r * D + h * 64 + x * 8);
+                    if (partly) {
+                        const int j = start + r;
+                        if (j > last || (j < it.first_lo && j >= p.sinks)) c = make_uint4(0u, 0u, 0u, 0u);
+                        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)  // a code of 0x7f or 0xff
+                            bad = bad || __vcmpeq4(cw[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+                    }
+                    const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+                    uint32_t w[8];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(cw[q / 2] >> (16 * (q % 2))));
+                        if constexpr (ACT == kF16) {
+                            w[q] = f;
+                        } else {
+                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                            w[q] = pack_act<kBF16>(v.x, v.y);
+                        }
+                    }
+                    unsigned char* row = dst + h * HALF + r * 128;
+                    *reinterpret_cast<uint4*>(row + ((x ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                    *reinterpret_cast<uint4*>(row + (((x + 1) ^ (r & 7)) * 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+                }
+                if (bad) *plain_flag = 1;
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(&full[s]);
+                    mbar_arrive(&c_empty[cs]);
+                }
+            }
+        }
+    } else if (!E8) {
         // ------------------------------------------------------- V tiles' check
         for (int i = 0; i < n_run; ++i) {
             const int use = 2 * i + 1, s = use % NS;
@@ -516,15 +693,15 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
     // A V that is not finite, in a tile that some row sees in part: the item's rows one by one.
     if (*plain_flag != 0 && *abort_flag == 0) {
         constexpr int W = D / 32;
-        const uint16_t *kc = static_cast<const uint16_t*>(p.k_cache), *vc = static_cast<const uint16_t*>(p.v_cache);
         const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
-        for (int r = warp; r < it.n * G; r += kChunkThreads / 32) {
+        for (int r = warp; r < it.n * G; r += THREADS / 32) {
             const int64_t at = it.row0 + r / G;
             const int pos = it.pos0 + r / G, h = it.kvh * G + r % G;
             const uint16_t* q = static_cast<const uint16_t*>(p.q) + at * p.q_stride + static_cast<int64_t>(h) * D;
             float qf[W], acc[W] = {}, m = -INFINITY, l = 0.f;
 #pragma unroll
             for (int x = 0; x < W; ++x) qf[x] = act_to_float<ACT>(q[lane + 32 * x]) * p.scale_log2;
+            const float kt = CACHE == kE4M3 ? *p.k_scale : 1.f, vt = CACHE == kE4M3 ? *p.v_scale : 1.f;
             const int lo = p.window ? max(0, pos - p.window + 1) : 0;
             for (int i = it.i0; i < it.i1; ++i) {
                 const int start = chunk_tile_start(it, i);
@@ -532,12 +709,14 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     if (j < lo && j >= p.sinks) continue;
                     const int blk = table[j / p.block_size];
                     if (blk < 0 || blk >= p.num_blocks) continue;
-                    const int64_t src = ((static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh) * p.block_size + j % p.block_size) * D;
+                    const int64_t tile = static_cast<int64_t>(blk) * p.num_kv_heads + it.kvh;
+                    const int64_t src = (tile * p.block_size + j % p.block_size) * D;
                     float d = 0.f;
 #pragma unroll
-                    for (int x = 0; x < W; ++x) d = fmaf(qf[x], act_to_float<ACT>(kc[src + lane + 32 * x]), d);
+                    for (int x = 0; x < W; ++x) d = fmaf(qf[x], cache_element<CACHE>(p.k_cache, src + lane + 32 * x), d);
 #pragma unroll
                     for (int off = 16; off >= 1; off >>= 1) d += __shfl_xor_sync(0xffffffffu, d, off);
+                    d *= SCALED ? p.k_scale[tile] : kt;
                     if (d > m) {
                         const float f = fast_exp2(m - d);
                         l *= f;
@@ -547,8 +726,9 @@ __global__ void __launch_bounds__(kChunkThreads, 1)
                     }
                     const float w = fast_exp2(d - m);
                     l += w;
+                    const float wv = w * (SCALED ? p.v_scale[tile] : vt);
 #pragma unroll
-                    for (int x = 0; x < W; ++x) acc[x] = fmaf(w, act_to_float<ACT>(vc[src + lane + 32 * x]), acc[x]);
+                    for (int x = 0; x < W; ++x) acc[x] = fmaf(wv, cache_element<CACHE>(p.v_cache, src + lane + 32 * x), acc[x]);
                 }
             }
             if (p.ws_ml != nullptr) {

@@ -364,7 +364,6 @@ cudaError_t launch_decode_tc_ext_e4m3b(const DecodeParams& p, int act, int head_
 cudaError_t launch_add_weights(const AddWeightsParams& p, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 cudaError_t launch_chunk(const ChunkParams& p, int act, int cache, int head_dim, cudaStream_t stream);
-cudaError_t launch_chunk_tc(const ChunkParams& p, int act, int head_dim, cudaStream_t stream);
 // Shares that an item's token tiles are split into (a function of the sizes).
 int chunk_splits(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int64_t max_context);
 
