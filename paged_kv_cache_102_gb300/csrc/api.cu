@@ -579,9 +579,11 @@ int paged_attention_decode_window(const void* q, const void* k_cache, const void
     const bool blocks = k_scales || v_scales;
     if (blocks && (cache_dtype != PKV_E4M3 || k_scale || v_scale))
         return fail(PKV_ERR_INVALID, std::string(fn) + ": an E4M3 cache has k_scale and v_scale or k_scales and v_scales");
+    // no row has more tokens than the tables: more than that of either changes nothing
+    const int64_t context = std::max<int64_t>(1, static_cast<int64_t>(max_blocks_per_seq) * block_size);
     DecodeExt ext;
-    ext.window = window;
-    ext.sinks = sinks;
+    ext.window = static_cast<int>(std::min<int64_t>(window, context));
+    ext.sinks = static_cast<int>(std::min<int64_t>(sinks, context));
     return decode_impl(fn, q, k_cache, v_cache, block_tables, max_blocks_per_seq, context_lens, num_seqs, num_q_heads,
                        num_kv_heads, block_size, head_dim, num_blocks, scale, out, act_dtype, cache_dtype,
                        blocks ? k_scales : k_scale, blocks ? v_scales : v_scale, partition_size, workspace,
@@ -735,13 +737,14 @@ int paged_attention_chunk(const void* q, int64_t q_stride, const void* k_cache, 
     p.num_kv_heads = num_kv_heads;
     p.block_size = block_size;
     p.num_blocks = num_blocks;
-    p.window = window;
-    p.sinks = sinks;
+    // no row has more tokens than the tables: a window of as many is none, more first tokens change nothing
+    const int64_t context = static_cast<int64_t>(max_blocks_per_seq) * block_size;
+    p.window = window < context ? window : 0;
+    p.sinks = p.window ? static_cast<int>(std::min<int64_t>(sinks, context)) : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     // a window's tokens alone are shared out (never more shares than the workspace was sized for)
-    const int64_t context = static_cast<int64_t>(max_blocks_per_seq) * block_size;
     p.splits = chunk_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads,
-                            window ? std::min<int64_t>(context, static_cast<int64_t>(window) + sinks) : context);
+                            p.window ? std::min<int64_t>(context, static_cast<int64_t>(p.window) + p.sinks) : context);
     if (p.splits > 1) {
         char* ws = static_cast<char*>(workspace) + kWorkspaceHeader;
         const size_t rows = static_cast<size_t>(p.splits) * num_tokens * num_q_heads;

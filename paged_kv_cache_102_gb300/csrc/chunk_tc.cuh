@@ -57,9 +57,13 @@ struct ChunkSmem {
     static constexpr bool E8 = is_e4m3(CACHE);
     static constexpr int HALVES = D / 64;
     static constexpr int STG = kChunkTile * D * 2;  // a K or V tile: per 64 channels 128 rows of 128 bytes
-    static constexpr int NS = E8 ? (D == 128 ? 3 : 5) : (D == 128 ? 5 : 8);
+    static constexpr int NS = E8 ? (D == 128 ? 3 : 5) : (D == 128 ? 4 : 8);
+    // A role that waits for the K or for the V tiles alone sees every use of its stages when their number is even (a
+    // parity names a phase only to whom none before it is still open).
+    static_assert(E8 || NS % 2 == 0, "K and V tiles in stages of their own");
     static constexpr int CSTG = kChunkTile * D;  // its codes
     static constexpr int NC = E8 ? (D == 128 ? 4 : 6) : 0;
+    static_assert(NC % 2 == 0, "the codes too");
     // Scales of a tile: [8] K scales, [8] V scales, [8] log2 |V scale|.  Entry i % SLOTS is written again for
     // tile i + SLOTS, once the codes of K tile use 2 (i + SLOTS) - NC were converted, for which the stage of use
     // 2 (i + SLOTS) - NC - NS >= 2 i + 1 was free: V tile i's, so that softmax(i) was over.
@@ -70,8 +74,8 @@ struct ChunkSmem {
     static constexpr int CODES = Q + 2 * QT;
     static constexpr int SCALES = CODES + NC * CSTG;
     static constexpr int BARS = SCALES + SLOTS * 24 * 4;
-    // full, empty, v_ok [NS]; c_full, c_empty [NC]; q_full, s_full[2], p_full[2], o_done[2], final
-    static constexpr int NBARS = 3 * NS + 2 * NC + 8;
+    // full, empty, v_ok [NS]; c_full, c_empty [NC]; q_full, s_full[2], p_full[2][2], o_done[2], final
+    static constexpr int NBARS = 3 * NS + 2 * NC + 10;
     static constexpr int MISC = BARS + NBARS * 8;
     static constexpr int BYTES = MISC + 64 + 1024;  // room to align the base
     static_assert(BYTES <= 227 * 1024, "shared memory of a block");
@@ -125,14 +129,8 @@ __device__ __forceinline__ int chunk_tile_start(const ChunkItem& it, int i) {
 template <int ACT>
 __device__ __forceinline__ bool any_not_finite(const uint4& u) {
     constexpr uint32_t EXP = ACT == kBF16 ? 0x7f807f80u : 0x7c007c00u;
-    bool bad = false;
-    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t e = w[i] & EXP;
-        bad = bad || (e & 0xffffu) == (EXP & 0xffffu) || (e >> 16) == (EXP >> 16);
-    }
-    return bad;
+    const uint32_t top = __vmaxu2(__vmaxu2(u.x & EXP, u.y & EXP), __vmaxu2(u.z & EXP, u.w & EXP));
+    return (top & 0xffffu) == (EXP & 0xffffu) || (top >> 16) == (EXP >> 16);
 }
 
 // Two floats -> 16-bit pair, `a` in the low half.
@@ -145,6 +143,65 @@ __device__ __forceinline__ uint32_t pack_act(float a, float b) {
         const __half2 v = __floats2half2_rn(a, b);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
+}
+
+// max(a, b, c); a NaN if one is.
+__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
+// Two binary32 values in a 64-bit register: multiply-add and add of both at once.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// 2^a, 2^b for a, b below 127 on the multiply-add pipe, which the exponential
+// unit (16 results a cycle and SM) leaves idle: x = n + f, n the nearest whole
+// number (found by adding 1.5 * 2^23, which leaves it in the low bits), 2^f by a
+// polynomial that is 1 at 0, of the least largest relative error on [-1/2, 1/2],
+// and n added to its exponent.  At most 2^-13.2 off for bfloat16 weights, 2^-18.4
+// for binary16 ones, whose rounding is 2^-9 and 2^-12.  x counts as -127 below
+// that and 2^-127 comes out as 0, so that a masked weight is 0 exactly.  Not for
+// NaN (the row's maximum tells of them).
+template <int ACT>
+__device__ __forceinline__ void exp2_pair(uint64_t x, float& a, float& b) {
+    float x0, x1;
+    unpair(x, x0, x1);
+    x = pair(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
+    const uint64_t t = add2(x, pair(12582912.f, 12582912.f));
+    const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
+    uint64_t y;
+    if constexpr (ACT == kBF16) {
+        y = fma2(f, pair(0.05500893294811249f, 0.05500893294811249f), pair(0.2422109693288803f, 0.2422109693288803f));
+        y = fma2(f, y, pair(0.6932829022407532f, 0.6932829022407532f));
+    } else {
+        y = fma2(f, pair(0.009582852944731712f, 0.009582852944731712f), pair(0.055906426161527634f, 0.055906426161527634f));
+        y = fma2(f, y, pair(0.24024099111557007f, 0.24024099111557007f));
+        y = fma2(f, y, pair(0.6931241750717163f, 0.6931241750717163f));
+    }
+    y = fma2(f, y, pair(1.f, 1.f));
+    float t0, t1;
+    unpair(t, t0, t1);
+    unpair(y, a, b);
+    a = __uint_as_float(__float_as_uint(a) + (__float_as_uint(t0) << 23));
+    b = __uint_as_float(__float_as_uint(b) + (__float_as_uint(t1) << 23));
 }
 
 // One element of a cache, without its scale.
@@ -184,7 +241,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     uint64_t* q_full = c_empty + S::NC;
     uint64_t* s_full = q_full + 1;
     uint64_t* p_full = s_full + 2;
-    uint64_t* o_done = p_full + 2;
+    uint64_t* o_done = p_full + 4;
     uint64_t* final_bar = o_done + 2;
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(sm + S::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 4);
@@ -219,7 +276,8 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         mbar_init(q_full, 1);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
-            mbar_init(&p_full[t], 4);
+            mbar_init(&p_full[2 * t], 4);
+            mbar_init(&p_full[2 * t + 1], 4);
             mbar_init(&o_done[t], 1);
         }
         mbar_init(final_bar, 1);
@@ -302,10 +360,12 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 [[maybe_unused]] const float* scales =
                     reinterpret_cast<const float*>(sm + S::SCALES) + (SCALED ? (i % max(1, S::SLOTS)) * 24 : 0);
                 [[maybe_unused]] const int bshift = p.block_size == 32 ? 1 : 0;  // 16-column groups to blocks
-                // 32 scores from column k on, in what `c` makes log2 units
+                // 32 scores from column k on, in what `c` makes log2 units (16-bit caches: they are there already)
                 auto scores = [&](int k, float* s) {
-                    tc::TmemLd<32>::load(s_addr + k, s);
-                    tc::tmem_wait_ld();
+                    if constexpr (E8) {
+                        tc::TmemLd<32>::load(s_addr + k, s);
+                        tc::tmem_wait_ld();
+                    }
                     if constexpr (SCALED) {
 #pragma unroll
                         for (int x = 0; x < 32; x += 16) {
@@ -325,7 +385,12 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 };
                 // 16-bit caches hold a row's scores; the others, with fewer registers a thread, read them twice
                 float s[E8 ? 32 : kChunkTile];
-                float mx = -INFINITY;
+                if constexpr (!E8) {
+#pragma unroll
+                    for (int k = 0; k < kChunkTile; k += 32) tc::TmemLd<32>::load(s_addr + k, s + k);
+                    tc::tmem_wait_ld();
+                }
+                float mx = -INFINITY, tops[8];
                 [[maybe_unused]] float mu = -INFINITY;
 #pragma unroll
                 for (int k = 0; k < kChunkTile; k += 32) {
@@ -333,14 +398,17 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                     scores(k, x);
 #pragma unroll
                     for (int y = 0; y < 32; y += 16) {
-                        float top = x[y];
+                        float top = max3_nan(x[y], x[y + 1], x[y + 2]);
 #pragma unroll
-                        for (int j = 1; j < 16; ++j) top = fmaxf(top, x[y + j]);
-                        mx = fmaxf(mx, top);
+                        for (int j = 3; j < 15; j += 2) top = max3_nan(top, x[y + j], x[y + j + 1]);
+                        tops[(k + y) / 16] = top = max3_nan(top, x[y + 15], x[y + 15]);
                         if constexpr (SCALED) mu = fmaxf(mu, top + scales[16 + (((k + y) >> 4) >> bshift)]);
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < 8; j += 2) mx = max3_nan(mx, tops[j], tops[j + 1]);
                 mx *= c;
+                if (!(mx < INFINITY)) l = NAN;  // an infinite logit or none at all: no weights
                 const bool move = mine && mx > m + kChunkRescale;
                 const bool turn = SCALED ? mine && mu > unit + kChunkRescale : move;
                 if (__any_sync(0xffffffffu, turn && l > 0.f)) {
@@ -366,7 +434,8 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 if (SCALED && turn) unit = mu;
                 const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of 0
                 [[maybe_unused]] const float lift = SCALED && unit != -INFINITY ? fast_exp2(ref - unit) : 0.f;
-                float sum0 = 0.f, sum1 = 0.f;
+                uint64_t sum = pair(0.f, 0.f);
+                const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
 #pragma unroll
                 for (int k = 0; k < kChunkTile; k += 32) {
                     float* x = s + (E8 ? 0 : k);
@@ -378,10 +447,16 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                         if constexpr (SCALED) vf = lift * scales[8 + (((k + y) >> 4) >> bshift)];
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            float a = fast_exp2(fmaf(x[y + j], c, -ref));
-                            float b = fast_exp2(fmaf(x[y + j + 1], c, -ref));
-                            sum0 += a;
-                            sum1 += b;
+                            const uint64_t e = fma2(pair(x[y + j], x[y + j + 1]), c2, ref2);
+                            float a, b;
+                            if (j % 8 == 6) {
+                                exp2_pair<ACT>(e, a, b);
+                            } else {
+                                unpair(e, a, b);
+                                a = fast_exp2(a);
+                                b = fast_exp2(b);
+                            }
+                            sum = add2(sum, pair(a, b));
                             if constexpr (SCALED) {
                                 a *= vf;
                                 b *= vf;
@@ -390,13 +465,23 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                         }
                     }
                     tc::tmem_st16(s_addr + k / 2, w);
+                    if (k == 32) {  // the products over the first 64 tokens may begin
+                        tc::tmem_wait_st();
+                        tc::fence_before_sync();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&p_full[2 * t]);
+                    }
                 }
+                float sum0, sum1;
+                unpair(sum, sum0, sum1);
                 l += sum0 + sum1;
                 tc::tmem_wait_st();
+            } else if (lane == 0) {
+                mbar_arrive(&p_full[2 * t]);
             }
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[t]);
+            if (lane == 0) mbar_arrive(&p_full[2 * t + 1]);
         }
         if (ok && cnt > 0) {
             ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (cnt - 1) & 1, abort_flag, p.err));
@@ -455,12 +540,12 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                             IDESC_S, kk > 0);
             }
         };
-        auto mma_o = [&](int t, int stage, bool add) {
+        auto mma_o = [&](int t, int stage, int half, bool add) {  // over 64 tokens
             const uint32_t b = k_base + stage * STG;
 #pragma unroll
-            for (int kk = 0; kk < kChunkTile / 16; ++kk)
+            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
                 tc::mma_f16_ts(tmem + O_COL + t * D, tmem + t * kChunkTile + kk * 8, tc::desc_sw128(b + kk * 2048, HALF, 1024),
-                               IDESC_O, add || kk > 0);
+                               IDESC_O, add || half > 0 || kk > 0);
         };
         bool ok = n_run > 0 && __all_sync(0xffffffffu, chunk_wait(q_full, 0, abort_flag, p.err));
         // tile i: K is stage use 2 i, V 2 i + 1
@@ -493,11 +578,16 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             for (int t = 0; t < 2; ++t) {
                 const int cnt = t == 0 ? cnt0 : cnt1;
                 if (i >= cnt) continue;
-                ok = __all_sync(0xffffffffu, chunk_wait(&p_full[t], i & 1, abort_flag, p.err));
+                ok = __all_sync(0xffffffffu, chunk_wait(&p_full[2 * t], i & 1, abort_flag, p.err));
+                if (!ok) break;
+                tc::fence_after_sync();
+                if (tc::elect_one()) mma_o(t, sv, 0, i > 0);
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, chunk_wait(&p_full[2 * t + 1], i & 1, abort_flag, p.err));
                 if (!ok) break;
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
-                    mma_o(t, sv, i > 0);
+                    mma_o(t, sv, 1, true);
                     tc::commit(&o_done[t]);
                     if (i + 1 < cnt) {
                         mma_s(t, sk);
@@ -667,17 +757,36 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             const int start = chunk_tile_start(it, it.i0 + i);
             const int last_lo = p.window ? max(0, last - p.window + 1) : 0;  // the last row's window begins here
             if (start + kChunkTile - 1 > it.pos0 || (start < last_lo && start + kChunkTile > p.sinks)) {
-                unsigned char* vb = ring + s * STG;
-                bool bad = false;
-                // a token's row is HALVES parts of 8 chunks; 4 / HALVES tokens a turn of the warp
-                constexpr int CH = 8 * HALVES;
-                for (int k = lane; k < kChunkTile * CH; k += 32) {
-                    const int r = k / CH, x = k % CH, j = start + r;
-                    uint4* at = reinterpret_cast<uint4*>(vb + (x >> 3) * HALF + r * 128 + (x & 7) * 16);
-                    if (j > last || (j < it.first_lo && j >= p.sinks)) *at = make_uint4(0u, 0u, 0u, 0u);
-                    else bad = bad || any_not_finite<ACT>(*at);
+                constexpr int CH = 8 * HALVES, STEP = 32 / CH;  // 16-byte chunks of a token, tokens of a warp's access
+                const int x = lane % CH, r0 = lane / CH;
+                unsigned char* vb = ring + s * STG + (x >> 3) * HALF + (x & 7) * 16;
+                auto clear = [&](int from, int to) {  // tokens [from, to) of the tile
+                    for (int r = min(kChunkTile, max(0, from)) + r0; r < min(kChunkTile, to); r += STEP)
+                        *reinterpret_cast<uint4*>(vb + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+                };
+                auto look = [&](int from, int to) {
+                    bool bad = false;
+                    to = min(kChunkTile, to);
+                    for (int r = min(kChunkTile, max(0, from)) + r0; r < to; r += 8 * STEP) {
+                        uint4 u[8];
+#pragma unroll
+                        for (int y = 0; y < 8; ++y)
+                            u[y] = r + y * STEP < to ? *reinterpret_cast<const uint4*>(vb + (r + y * STEP) * 128)
+                                                     : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+                        for (int y = 0; y < 8; ++y) bad = any_not_finite<ACT>(u[y]) || bad;
+                    }
+                    if (bad) *plain_flag = 1;
+                };
+                clear(last + 1 - start, kChunkTile);
+                if (p.window) {
+                    clear(p.sinks - start, it.first_lo - start);                    // hidden from every row
+                    look(max(p.sinks, it.first_lo) - start, last_lo - start);       // from the last ones
+                    look(max(it.pos0 + 1, last_lo) - start, last + 1 - start);      // from the first ones
+                    look(it.pos0 + 1 - start, min(p.sinks, last + 1) - start);
+                } else {
+                    look(it.pos0 + 1 - start, last + 1 - start);
                 }
-                if (bad) *plain_flag = 1;
                 tc::fence_proxy_async_smem();
             }
             __syncwarp();
