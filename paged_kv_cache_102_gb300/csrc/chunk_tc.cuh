@@ -12,26 +12,29 @@
 // row of the item sees; with few items a second grid axis splits their list, and
 // a merge kernel joins the partial results.  One item a block, a block an SM.
 // Roles:
-//  warps 0-3, 4-7  softmax of row tile 0, 1 (a thread a row): scores from tensor
-//                  memory, running maximum and sum, weights back to tensor memory
-//                  over the scores, at last the output.  The reference maximum
-//                  moves only when a row's maximum passes it by 2^8; then (almost
-//                  never after the first tile) the thread multiplies its row of O.
-//  warp 8          MMA: S_t = Q_t K^T (M = 128 rows, N = 128 tokens), O_t += P_t V
+//  warps 0-15      softmax: a row of a tile is two threads', 64 tokens each (row
+//                  tile (w >> 2) & 1, half w >> 3, rows 32 (w & 3) .. of warp w):
+//                  scores from tensor memory, running maximum and sum, weights
+//                  back to tensor memory over the scores, at last the output.  The
+//                  reference maximum moves only when a maximum passes it by 2^8,
+//                  so that the two need no more of each other than a vote; when it
+//                  moves (almost never after the first tile) they exchange their
+//                  maxima and multiply the row of O, half each.
+//  warp 16         MMA: S_t = Q_t K^T (M = 128 rows, N = 128 tokens), O_t += P_t V
 //                  (P from tensor memory, N = head_dim).  Order: S_0(0), S_1(0),
 //                  then for each tile i and t: O_t(i), S_t(i + 1).  While one row
 //                  tile is in the softmax, the other's products run.
-//  warps 9, 10     producers of K and of V: one TMA copy (128-byte swizzle) for
+//  warps 17, 18    producers of K and of V: one TMA copy (128-byte swizzle) for
 //                  each (block, 64 channels) of a tile, into a ring of stages.
-//  warp 11         V tiles that some row sees in part: rows that no row of the
+//  warp 19         V tiles that some row sees in part: rows that no row of the
 //                  item sees become zeros (what lies there may be anything, and
 //                  0 times it must be 0); a number that is not finite among the
 //                  others sends the item to the plain loop at the end, since a
 //                  weight of 0 would carry it to rows that do not see it.
-//  warps 12-15     E4M3 caches: conversion.  The producers copy the codes (one bulk
+//  warps 20-23     E4M3 caches: conversion.  The producers copy the codes (one bulk
 //                  copy a block) into a ring of their own; these warps write them
 //                  as 16-bit elements, exactly, into the ring that the products
-//                  read, and do warp 11's work on the way.  One scale per tensor
+//                  read, and do warp 19's work on the way.  One scale per tensor
 //                  joins the logits' factor and the output's.  Block scales: the
 //                  K producer leaves a tile's scales in shared memory; a logit is
 //                  multiplied by its block's K scale, and a weight, for the product
@@ -47,7 +50,7 @@
 
 namespace pkv {
 
-__host__ __device__ constexpr int chunk_threads(int cache) { return is_e4m3(cache) ? 512 : 384; }
+__host__ __device__ constexpr int chunk_threads(int cache) { return is_e4m3(cache) ? 768 : 640; }
 constexpr int kChunkTile = 128;       // tokens of a tile
 constexpr int kChunkTmemCols = 512;   // two S (128 columns each, P over them), two O
 constexpr float kChunkRescale = 8.f;  // log2 by which a maximum may pass the reference
@@ -73,7 +76,8 @@ struct ChunkSmem {
     static constexpr int Q = NS * STG;
     static constexpr int CODES = Q + 2 * QT;
     static constexpr int SCALES = CODES + NC * CSTG;
-    static constexpr int BARS = SCALES + SLOTS * 24 * 4;
+    static constexpr int SWAP = SCALES + SLOTS * 24 * 4;  // a value of each row, between its two threads
+    static constexpr int BARS = SWAP + 2 * kChunkTile * 4;
     // full, empty, v_ok [NS]; c_full, c_empty [NC]; q_full, s_full[2], p_full[2][2], o_done[2], final
     static constexpr int NBARS = 3 * NS + 2 * NC + 10;
     static constexpr int MISC = BARS + NBARS * 8;
@@ -145,63 +149,28 @@ __device__ __forceinline__ uint32_t pack_act(float a, float b) {
     }
 }
 
-// max(a, b, c); a NaN if one is.
-__device__ __forceinline__ float max3_nan(float a, float b, float c) {
+// Whether any of the 64 threads of named barrier `id` says so; a barrier among them.
+__device__ __forceinline__ bool pair_any(int id, bool mine) {
+    int r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.or.pred q, %2, 64, p;\n\t"
+        "selp.b32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"(mine ? 1 : 0), "r"(id)
+        : "memory");
+    return r != 0;
+}
+
+// The lowest n bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? ~0u : n <= 0 ? 0u : (1u << n) - 1u; }
+
+// max(a, b, c) in one instruction.
+__device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
-    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
-}
-
-// Two binary32 values in a 64-bit register: multiply-add and add of both at once.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
-    return r;
-}
-__device__ __forceinline__ void unpair(uint64_t x, float& a, float& b) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(x));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t r;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-    return r;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t r;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
-    return r;
-}
-
-// 2^a, 2^b for a, b below 127 on the multiply-add pipe, which the exponential
-// unit (16 results a cycle and SM) leaves idle: x = n + f, n the nearest whole
-// number (found by adding 1.5 * 2^23, which leaves it in the low bits), 2^f by a
-// polynomial that is 1 at 0, of the least largest relative error on [-1/2, 1/2],
-// and n added to its exponent.  At most 2^-13.2 off for bfloat16 weights, 2^-18.4
-// for binary16 ones, whose rounding is 2^-9 and 2^-12.  x counts as -127 below
-// that and 2^-127 comes out as 0, so that a masked weight is 0 exactly.  Not for
-// NaN (the row's maximum tells of them).
-template <int ACT>
-__device__ __forceinline__ void exp2_pair(uint64_t x, float& a, float& b) {
-    float x0, x1;
-    unpair(x, x0, x1);
-    x = pair(fmaxf(x0, -127.f), fmaxf(x1, -127.f));
-    const uint64_t t = add2(x, pair(12582912.f, 12582912.f));
-    const uint64_t f = fma2(add2(t, pair(-12582912.f, -12582912.f)), pair(-1.f, -1.f), x);
-    uint64_t y;
-    if constexpr (ACT == kBF16) {
-        y = fma2(f, pair(0.05500893294811249f, 0.05500893294811249f), pair(0.2422109693288803f, 0.2422109693288803f));
-        y = fma2(f, y, pair(0.6932829022407532f, 0.6932829022407532f));
-    } else {
-        y = fma2(f, pair(0.009582852944731712f, 0.009582852944731712f), pair(0.055906426161527634f, 0.055906426161527634f));
-        y = fma2(f, y, pair(0.24024099111557007f, 0.24024099111557007f));
-        y = fma2(f, y, pair(0.6931241750717163f, 0.6931241750717163f));
-    }
-    y = fma2(f, y, pair(1.f, 1.f));
-    float t0, t1;
-    unpair(t, t0, t1);
-    unpair(y, a, b);
-    a = __uint_as_float(__float_as_uint(a) + (__float_as_uint(t0) << 23));
-    b = __uint_as_float(__float_as_uint(b) + (__float_as_uint(t1) << 23));
 }
 
 // One element of a cache, without its scale.
@@ -251,7 +220,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.num_q_heads / p.num_kv_heads, TQ = kChunkTile / G, R = 2 * TQ;
     const int slot = (gridDim.x - 1 - blockIdx.x) / p.num_kv_heads;  // later rows, which see more, first
-    if (warp == 11) {
+    if (warp == 19) {
         const int b = chunk_find(p.seq_starts, p.num_seqs, R, slot, lane);
         if (lane == 0) *s_seq = b;
         if (blockIdx.x == 0 && blockIdx.y == 0)  // every sequence's rows and length once
@@ -260,10 +229,10 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 if (s0 < 0 || s1 < s0 || s1 > p.num_tokens || (s1 > s0 && (L < s1 - s0 || L > p.max_blocks_per_seq * p.block_size)))
                     atomicOr(p.err, kErrBadLen);
             }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         tc::tmem_alloc(tmem_base_smem, kChunkTmemCols);
         tc::tmem_relinquish();
-    } else if (threadIdx.x == 9 * 32) {
+    } else if (threadIdx.x == 17 * 32) {
         for (int i = 0; i < NS; ++i) {
             mbar_init(&full[i], E8 ? 4 : 1);
             mbar_init(&empty[i], 1);
@@ -328,135 +297,151 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     const int n_run = max(cnt0, cnt1);
     const uint64_t policy = l2_policy_evict_first();
 
-    if (warp < 8) {
+    if (warp < 16) {
         // ------------------------------------------------------------ softmax
-        const int t = warp >> 2, row = (warp & 3) * 32 + lane;
+        const int t = (warp >> 2) & 1, half = warp >> 3, row = (warp & 3) * 32 + lane;
+        const int pair = 1 + (warp & 7);  // named barrier of the two warps of these rows
         const int cnt = t == 0 ? cnt0 : cnt1;
         const int tok = row / G, g = row - tok * G;  // (rows past TQ * G and past the last token: none)
         const bool mine = tok < rows_of(t);
         const bool live = __any_sync(0xffffffffu, mine);
         const int pos = mine ? it.pos0 + t * TQ + tok : -1;
         const int pos_lo = it.pos0 + t * TQ, pos_hi = pos_lo + rows_of(t) - 1;  // of the row tile
-        const uint32_t s_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + t * kChunkTile;
-        const uint32_t o_addr = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16) + O_COL + t * D;
+        const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t s_addr = lanes + t * kChunkTile + half * 64;  // this thread's scores, then its weights, packed
+        const uint32_t o_addr = lanes + O_COL + t * D + half * (D / 2);
+        volatile float* swap = reinterpret_cast<volatile float*>(sm + S::SWAP) + t * kChunkTile + row;
         const float factor = CACHE == kE4M3 ? p.scale_log2 * *p.k_scale : p.scale_log2;
         const float c = SCALED ? 1.f : fmaxf(fabsf(factor), 1e-37f);  // (times -inf: never a NaN, at a factor of 0 either)
         const bool negative = !SCALED && factor < 0.f;
-        // reference maximum (log2 units) and sum; block scales: of the logits plus log2 |vs|, the unit of O
+        // reference maximum (log2 units) and this half's sum; block scales: of the logits plus log2 |vs|, the unit of O
         float m = -INFINITY, l = 0.f;
         [[maybe_unused]] float unit = -INFINITY;
         bool ok = true;
-        for (int i = 0; i < cnt && ok; ++i) {
+        for (int i = 0; i < cnt; ++i) {
             ok = __all_sync(0xffffffffu, chunk_wait(&s_full[t], i & 1, abort_flag, p.err));
-            if (!ok) break;
-            tc::fence_after_sync();
             if (live) {
-                const int start = chunk_tile_start(it, it.i0 + i);
-                const bool masked = start + kChunkTile - 1 > pos_lo ||
-                                    (p.window != 0 && start <= pos_hi - p.window && start + kChunkTile > p.sinks);
-                const int end = pos - start;                         // sees columns up to this one
-                const int from = p.window ? end - p.window + 1 : 0;  // and from this one on,
-                const int sink = p.sinks - start;                    // or before this one
+                tc::fence_after_sync();
+                const int start = chunk_tile_start(it, it.i0 + i) + half * 64;  // this half's first token
+                const bool masked = start + 63 > pos_lo || (p.window != 0 && start <= pos_hi - p.window && start + 64 > p.sinks);
                 [[maybe_unused]] const float* scales =
                     reinterpret_cast<const float*>(sm + S::SCALES) + (SCALED ? (i % max(1, S::SLOTS)) * 24 : 0);
-                [[maybe_unused]] const int bshift = p.block_size == 32 ? 1 : 0;  // 16-column groups to blocks
-                // 32 scores from column k on, in what `c` makes log2 units (16-bit caches: they are there already)
-                auto scores = [&](int k, float* s) {
-                    if constexpr (E8) {
-                        tc::TmemLd<32>::load(s_addr + k, s);
-                        tc::tmem_wait_ld();
-                    }
+                [[maybe_unused]] const int block0 = half * 64 / p.block_size, bshift = p.block_size == 32 ? 1 : 0;
+                // scores x[0 .. N) from column k on, as loaded, to what `c` makes log2 units
+                auto prepare = [&](int k, int n, float* x) {
                     if constexpr (SCALED) {
 #pragma unroll
-                        for (int x = 0; x < 32; x += 16) {
-                            const float f = factor * scales[((k + x) >> 4) >> bshift];
+                        for (int y = 0; y < n; y += 16) {
+                            const float f = factor * scales[block0 + (((k + y) >> 4) >> bshift)];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) s[x + j] *= f;
+                            for (int j = 0; j < 16; ++j) x[y + j] *= f;
                         }
                     } else if (negative) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) s[j] = -s[j];
+                        for (int j = 0; j < n; ++j) x[j] = -x[j];
                     }
                     if (masked) {
+                        const int end = pos - start - k;                     // sees columns up to this one
+                        const int from = p.window ? end - p.window + 1 : 0;  // and from this one on,
+                        const int sink = p.sinks - start - k;                // or before this one
 #pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (k + j > end || (k + j < from && k + j >= sink)) s[j] = -INFINITY;
+                        for (int y = 0; y < n; y += 32) {
+                            const uint32_t seen = low_bits(end + 1 - y) & (~low_bits(from - y) | low_bits(sink - y));
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!(seen & (1u << j))) x[y + j] = -INFINITY;
+                        }
                     }
                 };
-                // 16-bit caches hold a row's scores; the others, with fewer registers a thread, read them twice
-                float s[E8 ? 32 : kChunkTile];
-                if constexpr (!E8) {
-#pragma unroll
-                    for (int k = 0; k < kChunkTile; k += 32) tc::TmemLd<32>::load(s_addr + k, s + k);
-                    tc::tmem_wait_ld();
-                }
-                float mx = -INFINITY, tops[8];
+                // 16-bit caches hold a thread's scores; the others, with fewer registers a thread, read them twice
+                constexpr int HELD = E8 ? 32 : 64;
+                float s[HELD], tops[4];
                 [[maybe_unused]] float mu = -INFINITY;
 #pragma unroll
-                for (int k = 0; k < kChunkTile; k += 32) {
-                    float* x = s + (E8 ? 0 : k);
-                    scores(k, x);
+                for (int k = 0; k < 64; k += HELD) {
 #pragma unroll
-                    for (int y = 0; y < 32; y += 16) {
-                        float top = max3_nan(x[y], x[y + 1], x[y + 2]);
+                    for (int y = 0; y < HELD; y += 32) tc::TmemLd<32>::load(s_addr + k + y, s + y);
+                    tc::tmem_wait_ld();
+                    prepare(k, HELD, s);
 #pragma unroll
-                        for (int j = 3; j < 15; j += 2) top = max3_nan(top, x[y + j], x[y + j + 1]);
-                        tops[(k + y) / 16] = top = max3_nan(top, x[y + 15], x[y + 15]);
-                        if constexpr (SCALED) mu = fmaxf(mu, top + scales[16 + (((k + y) >> 4) >> bshift)]);
+                    for (int y = 0; y < HELD; y += 16) {
+                        float top = max3(s[y], s[y + 1], s[y + 2]);
+#pragma unroll
+                        for (int j = 3; j < 15; j += 2) top = max3(top, s[y + j], s[y + j + 1]);
+                        tops[(k + y) / 16] = top = fmaxf(top, s[y + 15]);
+                        if constexpr (SCALED) mu = fmaxf(mu, top + scales[16 + block0 + (((k + y) >> 4) >> bshift)]);
                     }
                 }
+                float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
+                const bool past = mine && (mx > m + kChunkRescale || (SCALED && mu > unit + kChunkRescale));
+                if (pair_any(pair, past || !ok)) {
+                    // the products of the tiles before are done before the row of O is multiplied
+                    if (ok && i > 0) {
+                        ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (i - 1) & 1, abort_flag, p.err));
+                        tc::fence_after_sync();
+                    }
+                    if (pair_any(pair, !ok)) {  // both leave
+                        ok = false;
+                        break;
+                    }
+                    // the row's maximum, and so its reference, from both threads
+                    auto agree = [&](float top, float at) {
+                        if (half == 1) *swap = top;
+                        pair_any(pair, false);
+                        float to = at;
+                        if (half == 0) {
+                            top = fmaxf(top, *swap);
+                            if (mine && top > at + kChunkRescale) to = top;
+                            *swap = to;
+                        }
+                        pair_any(pair, false);
+                        if (half == 1) to = *swap;
+                        return to;
+                    };
+                    const float to = agree(mx, m);
+                    const float down = to == m ? 1.f : fast_exp2(m - to);
+                    float f = down;
+                    if constexpr (SCALED) {
+                        const float u = agree(mu, unit);
+                        f = u == unit ? 1.f : fast_exp2(unit - u);
+                        unit = u;
+                    }
+                    l *= down;
+                    m = to;
+                    if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll
-                for (int j = 0; j < 8; j += 2) mx = max3_nan(mx, tops[j], tops[j + 1]);
-                mx *= c;
-                if (!(mx < INFINITY)) l = NAN;  // an infinite logit or none at all: no weights
-                const bool move = mine && mx > m + kChunkRescale;
-                const bool turn = SCALED ? mine && mu > unit + kChunkRescale : move;
-                if (__any_sync(0xffffffffu, turn && l > 0.f)) {
-                    // O holds the tiles before: their products are done, then the row is multiplied
-                    ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (i - 1) & 1, abort_flag, p.err));
-                    if (!ok) break;
-                    tc::fence_after_sync();
-                    const float f = !turn ? 1.f : SCALED ? fast_exp2(unit - mu) : fast_exp2(m - mx);
+                        for (int k = 0; k < D / 2; k += 8) {
+                            float o[8];
+                            tc::TmemLd<8>::load(o_addr + k, o);
+                            tc::tmem_wait_ld();
 #pragma unroll
-                    for (int k = 0; k < D; k += 8) {
-                        float o[8];
-                        tc::TmemLd<8>::load(o_addr + k, o);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) o[j] *= f;
-                        tc::tmem_st<8>(o_addr + k, o);
+                            for (int j = 0; j < 8; ++j) o[j] *= f;
+                            tc::tmem_st<8>(o_addr + k, o);
+                        }
                     }
                 }
-                if (move) {
-                    l *= fast_exp2(m - mx);  // (0 times what it is at first)
-                    m = mx;
-                }
-                if (SCALED && turn) unit = mu;
                 const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of 0
                 [[maybe_unused]] const float lift = SCALED && unit != -INFINITY ? fast_exp2(ref - unit) : 0.f;
-                uint64_t sum = pair(0.f, 0.f);
-                const uint64_t c2 = pair(c, c), ref2 = pair(-ref, -ref);
+                float sum[4] = {};
 #pragma unroll
-                for (int k = 0; k < kChunkTile; k += 32) {
+                for (int k = 0; k < 64; k += 32) {
                     float* x = s + (E8 ? 0 : k);
-                    if constexpr (E8) scores(k, x);
+                    if constexpr (E8) {
+                        tc::TmemLd<32>::load(s_addr + k, x);
+                        tc::tmem_wait_ld();
+                        prepare(k, 32, x);
+                    }
                     uint32_t w[16];
 #pragma unroll
                     for (int y = 0; y < 32; y += 16) {
                         [[maybe_unused]] float vf = 1.f;
-                        if constexpr (SCALED) vf = lift * scales[8 + (((k + y) >> 4) >> bshift)];
+                        if constexpr (SCALED) vf = lift * scales[8 + block0 + (((k + y) >> 4) >> bshift)];
 #pragma unroll
                         for (int j = 0; j < 16; j += 2) {
-                            const uint64_t e = fma2(pair(x[y + j], x[y + j + 1]), c2, ref2);
-                            float a, b;
-                            if (j % 8 == 6) {
-                                exp2_pair<ACT>(e, a, b);
-                            } else {
-                                unpair(e, a, b);
-                                a = fast_exp2(a);
-                                b = fast_exp2(b);
-                            }
-                            sum = add2(sum, pair(a, b));
+                            float a = fast_exp2(fmaf(x[y + j], c, -ref));
+                            float b = fast_exp2(fmaf(x[y + j + 1], c, -ref));
+                            sum[j & 2] += a;
+                            sum[(j & 2) + 1] += b;
                             if constexpr (SCALED) {
                                 a *= vf;
                                 b *= vf;
@@ -465,29 +450,26 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                         }
                     }
                     tc::tmem_st16(s_addr + k / 2, w);
-                    if (k == 32) {  // the products over the first 64 tokens may begin
-                        tc::tmem_wait_st();
-                        tc::fence_before_sync();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&p_full[2 * t]);
-                    }
                 }
-                float sum0, sum1;
-                unpair(sum, sum0, sum1);
-                l += sum0 + sum1;
+                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
                 tc::tmem_wait_st();
-            } else if (lane == 0) {
-                mbar_arrive(&p_full[2 * t]);
             }
+            if (!ok) break;
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * t + 1]);
+            if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
         }
         if (ok && cnt > 0) {
             ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (cnt - 1) & 1, abort_flag, p.err));
             tc::fence_after_sync();
         }
-        if (ok && live && any) {
+        if (live && any && !pair_any(pair, !ok)) {
+            // the row's sum from both threads
+            if (half == 1) *swap = l;
+            pair_any(pair, false);
+            if (half == 0) *swap = l = l + *swap;
+            pair_any(pair, false);
+            l = *swap;
             // what an element of O stands for
             float vmul = 1.f;
             if constexpr (CACHE == kE4M3) vmul = *p.v_scale;
@@ -496,25 +478,26 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             const int h = it.kvh * G + g;
             if (p.ws_ml != nullptr) {
                 const int64_t slot_row = (static_cast<int64_t>(blockIdx.y) * p.num_tokens + at) * p.num_q_heads + h;
-                if (mine) reinterpret_cast<float2*>(p.ws_ml)[slot_row] = make_float2(m, l);
+                if (mine && half == 0) reinterpret_cast<float2*>(p.ws_ml)[slot_row] = make_float2(m, l);
 #pragma unroll
-                for (int k = 0; k < D; k += 16) {
+                for (int k = 0; k < D / 2; k += 16) {
                     float o[16];
                     if (cnt > 0) {
                         tc::TmemLd<16>::load(o_addr + k, o);
                         tc::tmem_wait_ld();
                     }
                     if (mine && cnt > 0) {
-                        float4* dst = reinterpret_cast<float4*>(p.ws_o + slot_row * D + k);
+                        float4* dst = reinterpret_cast<float4*>(p.ws_o + slot_row * D + half * (D / 2) + k);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) dst[j] = make_float4(o[4 * j] * vmul, o[4 * j + 1] * vmul, o[4 * j + 2] * vmul, o[4 * j + 3] * vmul);
+                        for (int j = 0; j < 4; ++j)
+                            dst[j] = make_float4(o[4 * j] * vmul, o[4 * j + 1] * vmul, o[4 * j + 2] * vmul, o[4 * j + 3] * vmul);
                     }
                 }
             } else {
                 const float inv = vmul / l;
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + at * p.out_stride + static_cast<int64_t>(h) * D;
+                uint16_t* dst = static_cast<uint16_t*>(p.out) + at * p.out_stride + static_cast<int64_t>(h) * D + half * (D / 2);
 #pragma unroll
-                for (int k = 0; k < D; k += 32) {
+                for (int k = 0; k < D / 2; k += 32) {
                     float o[32];
                     tc::TmemLd<32>::load(o_addr + k, o);
                     tc::tmem_wait_ld();
@@ -528,7 +511,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 }
             }
         }
-    } else if (warp == 8) {
+    } else if (warp == 16) {
         // ---------------------------------------------------------------- MMA
         const uint32_t k_base = smem_addr(ring), q_base = smem_addr(qbuf);
         auto mma_s = [&](int t, int stage) {
@@ -544,7 +527,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             const uint32_t b = k_base + stage * STG;
 #pragma unroll
             for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                tc::mma_f16_ts(tmem + O_COL + t * D, tmem + t * kChunkTile + kk * 8, tc::desc_sw128(b + kk * 2048, HALF, 1024),
+                tc::mma_f16_ts(tmem + O_COL + t * D, tmem + t * kChunkTile + half * 64 + (kk & 3) * 8, tc::desc_sw128(b + kk * 2048, HALF, 1024),
                                IDESC_O, add || half > 0 || kk > 0);
         };
         bool ok = n_run > 0 && __all_sync(0xffffffffu, chunk_wait(q_full, 0, abort_flag, p.err));
@@ -609,9 +592,9 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             if (!mbar_wait(final_bar, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
-    } else if (warp < 11) {
+    } else if (warp < 19) {
         // ---------------------------------------------------------- producers
-        const int v = warp - 9;  // 0: K (and Q), 1: V
+        const int v = warp - 17;  // 0: K (and Q), 1: V
         const CUtensorMap* map = v ? &vmap : &kmap;
         if (v == 0 && lane == 0 && n_run > 0) {
             const uint32_t bytes = HALVES * G * TQ * 128;
@@ -691,7 +674,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             if (v == 0 && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
-    } else if (E8 && warp >= 12) {
+    } else if (E8 && warp >= 20) {
         // --------------------------------------------------------- conversion
         // 16 codes a lane and step.  8 neighbouring lanes, which shared memory serves at once, take 64 channels of
         // two tokens (head_dim 128: the other half of the second), so that neither their reads nor their writes,
@@ -710,7 +693,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 bool bad = false;
                 constexpr int TOKENS = 32 / (4 * HALVES);  // a warp's step
 #pragma unroll 4
-                for (int r0 = (warp - 12) * TOKENS; r0 < kChunkTile; r0 += 4 * TOKENS) {
+                for (int r0 = (warp - 20) * TOKENS; r0 < kChunkTile; r0 += 4 * TOKENS) {
                     const int pair = lane & 15, second = (lane >> 2) & 1;
                     const int r = r0 + (HALVES == 2 ? (lane >> 4) * 2 + second : lane >> 2);
                     const int h = HALVES == 2 ? ((pair >> 3) ^ second) : 0;
@@ -797,7 +780,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 8) tc::tmem_dealloc(tmem, kChunkTmemCols);
+    if (warp == 16) tc::tmem_dealloc(tmem, kChunkTmemCols);
 
     // A V that is not finite, in a tile that some row sees in part: the item's rows one by one.
     if (*plain_flag != 0 && *abort_flag == 0) {
