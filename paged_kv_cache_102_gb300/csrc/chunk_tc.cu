@@ -24,6 +24,18 @@ bool cache_map(CUtensorMap* m, const void* base, int act, int D, uint64_t rows, 
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same in boxes of all D columns, 64 of them after the other (box_rows rows of 128 bytes each).
+bool value_map(CUtensorMap* m, const void* base, int act, int D, uint64_t rows, uint32_t box_rows) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    cuuint64_t dims[3] = {64, rows, static_cast<cuuint64_t>(D / 64)};
+    cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * 2, 128};
+    cuuint32_t box[3] = {64, box_rows, static_cast<cuuint32_t>(D / 64)}, steps[3] = {1, 1, 1};
+    return fn(m, act == kBF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void*>(base), dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // q as [tokens][heads][D] in boxes of 64 channels x G heads x 128 / G tokens.
 bool query_map(CUtensorMap* m, const ChunkParams& p, int act, int D) {
     auto fn = encode_fn();
@@ -100,7 +112,7 @@ cudaError_t launch_one(const ChunkParams& p, cudaStream_t s) {
     if (!query_map(&qm, p, ACT, D)) return cudaErrorInvalidValue;
     if (is_e4m3(CACHE)) km = vm = qm;  // codes are copied without
     else if (!cache_map(&km, p.k_cache, ACT, D, cache_rows, p.block_size) ||
-             !cache_map(&vm, p.v_cache, ACT, D, cache_rows, p.block_size))
+             !value_map(&vm, p.v_cache, ACT, D, cache_rows, p.block_size))
         return cudaErrorInvalidValue;
     const int R = 2 * (kChunkTile / (p.num_q_heads / p.num_kv_heads));
     const int64_t blocks = (static_cast<int64_t>(p.num_tokens) / R + p.num_seqs) * p.num_kv_heads;

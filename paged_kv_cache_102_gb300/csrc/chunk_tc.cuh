@@ -24,8 +24,11 @@
 //                  (P from tensor memory, N = head_dim).  Order: S_0(0), S_1(0),
 //                  then for each tile i and t: O_t(i), S_t(i + 1).  While one row
 //                  tile is in the softmax, the other's products run.
-//  warps 17, 18    producers of K and of V: one TMA copy (128-byte swizzle) for
-//                  each (block, 64 channels) of a tile, into a ring of stages.
+//  warps 17, 18    producers of K and of V, into a ring of stages: TMA copies (128-byte
+//                  swizzle), for K one of each (block, 64 channels) of a tile, for V,
+//                  whose products take a block's tokens at a time, one of each block.
+//                  The copies of a warp leave one after the other, some 94 cycles
+//                  each, so that warp 18 issues a quarter of K's as well.
 //  warp 19         V tiles that some row sees in part: rows that no row of the
 //                  item sees become zeros (what lies there may be anything, and
 //                  0 times it must be 0); a number that is not finite among the
@@ -215,14 +218,14 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(sm + S::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 4);
     volatile int* plain_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 8);
-    int* s_seq = reinterpret_cast<int*>(sm + S::MISC + 12);
+    int* s_item = reinterpret_cast<int*>(sm + S::MISC + 16);  // sequence, its first row and the next one's, its length
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.num_q_heads / p.num_kv_heads, TQ = kChunkTile / G, R = 2 * TQ;
     const int slot = (gridDim.x - 1 - blockIdx.x) / p.num_kv_heads;  // later rows, which see more, first
     if (warp == 19) {
         const int b = chunk_find(p.seq_starts, p.num_seqs, R, slot, lane);
-        if (lane == 0) *s_seq = b;
+        if (lane < 4) s_item[lane] = lane == 0 ? b : lane == 3 ? p.context_lens[b] : p.seq_starts[b + lane - 1];
         if (blockIdx.x == 0 && blockIdx.y == 0)  // every sequence's rows and length once
             for (int i = lane; i < p.num_seqs; i += 32) {
                 const int s0 = p.seq_starts[i], s1 = p.seq_starts[i + 1], L = p.context_lens[i];
@@ -234,7 +237,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         tc::tmem_relinquish();
     } else if (threadIdx.x == 17 * 32) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], E8 ? 4 : 1);
+            mbar_init(&full[i], E8 ? 4 : i % 2 == 0 ? 2 : 1);  // 16-bit: K tiles in the even stages
             mbar_init(&empty[i], 1);
             mbar_init(&v_ok[i], 1);
         }
@@ -265,11 +268,11 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     const uint32_t tmem = *tmem_base_smem;
 
     ChunkItem it;
-    it.seq = *s_seq;
+    it.seq = s_item[0];
     it.kvh = (gridDim.x - 1 - blockIdx.x) % p.num_kv_heads;
     bool any;
     {
-        const int s0 = p.seq_starts[it.seq], s1 = p.seq_starts[it.seq + 1], L = p.context_lens[it.seq];
+        const int s0 = s_item[1], s1 = s_item[2], L = s_item[3];
         const int first = (slot - (s0 / R + it.seq)) * R;  // of the sequence's new tokens
         any = s0 >= 0 && s1 <= p.num_tokens && first >= 0 && first < s1 - s0 && L >= s1 - s0 &&
               L <= p.max_blocks_per_seq * p.block_size;
@@ -295,7 +298,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     };
     const int cnt0 = count_of(0), cnt1 = count_of(1);
     const int n_run = max(cnt0, cnt1);
-    const uint64_t policy = l2_policy_evict_first();
+    const uint64_t policy = l2_policy_evict_normal();  // other row tiles read them too
 
     if (warp < 16) {
         // ------------------------------------------------------------ softmax
@@ -476,44 +479,75 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             if constexpr (SCALED) vmul = unit == -INFINITY ? 0.f : fast_exp2(unit - m);
             const int64_t at = it.row0 + t * TQ + tok;
             const int h = it.kvh * G + g;
+            // Rows go out through the row tile's queries' memory, which its last scores have read: 32 rows of 128 bytes
+            // a warp and turn, chunks of 16 bytes swizzled by the row; then 8 lanes write 128 bytes of one row (a lane
+            // with a row of its own would take 32 lines an instruction).
+            unsigned char* stage = qbuf + t * S::QT + (half * 4 + (warp & 3)) * (S::QT / 8);
+            static_assert(S::QT / 8 >= 32 * 64, "room for half a turn of each warp");
+            constexpr int TURN = S::QT / 8 / 32;  // bytes of a row: 128, or 64 at head_dim 64
+            constexpr int CHUNKS = TURN / 16;
+            auto put = [&](int x, const uint4& v) {  // chunk x of this thread's row
+                *reinterpret_cast<uint4*>(stage + lane * TURN + ((x ^ (lane & (CHUNKS - 1))) * 16)) = v;
+            };
+            // the warp's rows, TURN bytes each, to `row_dst(row's index in the item) + offset`
+            auto flush = [&](auto row_dst) {
+                __syncwarp();
+#pragma unroll
+                for (int y = 0; y < CHUNKS; ++y) {
+                    const int r = y * (32 / CHUNKS) + lane / CHUNKS, x = lane % CHUNKS;
+                    const int rr = (warp & 3) * 32 + r, rt = rr / G;
+                    if (rt < rows_of(t))
+                        *reinterpret_cast<uint4*>(row_dst(it.row0 + t * TQ + rt, it.kvh * G + rr - rt * G) + x * 16) =
+                            *reinterpret_cast<const uint4*>(stage + r * TURN + ((x ^ (r & (CHUNKS - 1))) * 16));
+                }
+                __syncwarp();
+            };
             if (p.ws_ml != nullptr) {
-                const int64_t slot_row = (static_cast<int64_t>(blockIdx.y) * p.num_tokens + at) * p.num_q_heads + h;
-                if (mine && half == 0) reinterpret_cast<float2*>(p.ws_ml)[slot_row] = make_float2(m, l);
+                const int64_t share = static_cast<int64_t>(blockIdx.y) * p.num_tokens;
+                if (mine && half == 0) reinterpret_cast<float2*>(p.ws_ml)[(share + at) * p.num_q_heads + h] = make_float2(m, l);
+                if (cnt > 0) {
 #pragma unroll
-                for (int k = 0; k < D / 2; k += 16) {
-                    float o[16];
-                    if (cnt > 0) {
-                        tc::TmemLd<16>::load(o_addr + k, o);
+                    for (int k = 0; k < D / 2; k += TURN / 4) {
+                        float o[TURN / 4];
+                        tc::TmemLd<TURN / 4>::load(o_addr + k, o);
                         tc::tmem_wait_ld();
-                    }
-                    if (mine && cnt > 0) {
-                        float4* dst = reinterpret_cast<float4*>(p.ws_o + slot_row * D + half * (D / 2) + k);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
-                            dst[j] = make_float4(o[4 * j] * vmul, o[4 * j + 1] * vmul, o[4 * j + 2] * vmul, o[4 * j + 3] * vmul);
+                        for (int x = 0; x < CHUNKS; ++x)
+                            put(x, make_uint4(__float_as_uint(o[4 * x] * vmul), __float_as_uint(o[4 * x + 1] * vmul),
+                                              __float_as_uint(o[4 * x + 2] * vmul), __float_as_uint(o[4 * x + 3] * vmul)));
+                        flush([&](int64_t r, int head) {
+                            return reinterpret_cast<unsigned char*>(
+                                p.ws_o + ((share + r) * p.num_q_heads + head) * D + half * (D / 2) + k);
+                        });
                     }
                 }
             } else {
                 const float inv = vmul / l;
-                uint16_t* dst = static_cast<uint16_t*>(p.out) + at * p.out_stride + static_cast<int64_t>(h) * D + half * (D / 2);
 #pragma unroll
-                for (int k = 0; k < D / 2; k += 32) {
-                    float o[32];
-                    tc::TmemLd<32>::load(o_addr + k, o);
+                for (int k = 0; k < D / 2; k += TURN / 2) {
+                    float o[TURN / 2];
+#pragma unroll
+                    for (int y = 0; y < TURN / 2; y += 32) tc::TmemLd<32>::load(o_addr + k + y, o + y);
                     tc::tmem_wait_ld();
-                    if (mine) {
 #pragma unroll
-                        for (int j = 0; j < 32; j += 8)
-                            *reinterpret_cast<uint4*>(dst + k + j) =
-                                make_uint4(pack_act<ACT>(o[j] * inv, o[j + 1] * inv), pack_act<ACT>(o[j + 2] * inv, o[j + 3] * inv),
-                                           pack_act<ACT>(o[j + 4] * inv, o[j + 5] * inv), pack_act<ACT>(o[j + 6] * inv, o[j + 7] * inv));
-                    }
+                    for (int x = 0; x < CHUNKS; ++x)
+                        put(x, make_uint4(pack_act<ACT>(o[8 * x] * inv, o[8 * x + 1] * inv),
+                                          pack_act<ACT>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                          pack_act<ACT>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                                          pack_act<ACT>(o[8 * x + 6] * inv, o[8 * x + 7] * inv)));
+                    flush([&](int64_t r, int head) {
+                        return reinterpret_cast<unsigned char*>(static_cast<uint16_t*>(p.out) + r * p.out_stride +
+                                                                static_cast<int64_t>(head) * D + half * (D / 2) + k);
+                    });
                 }
             }
         }
     } else if (warp == 16) {
         // ---------------------------------------------------------------- MMA
         const uint32_t k_base = smem_addr(ring), q_base = smem_addr(qbuf);
+        const uint32_t v_part = p.block_size * 128;
+        const int vsh = p.block_size == 32 ? 1 : 0;
+        auto v_step = [&](int kk) { return (kk >> vsh) * v_part * HALVES + (kk & vsh) * 2048; };  // of 16 tokens
         auto mma_s = [&](int t, int stage) {
             const uint32_t a = q_base + t * S::QT, b = k_base + stage * STG;
 #pragma unroll
@@ -524,10 +558,11 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             }
         };
         auto mma_o = [&](int t, int stage, int half, bool add) {  // over 64 tokens
+            // 16-bit: a block's tokens together, its 64-channel parts v_part apart (the converted tile: as K)
             const uint32_t b = k_base + stage * STG;
 #pragma unroll
             for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                tc::mma_f16_ts(tmem + O_COL + t * D, tmem + t * kChunkTile + half * 64 + (kk & 3) * 8, tc::desc_sw128(b + kk * 2048, HALF, 1024),
+                tc::mma_f16_ts(tmem + O_COL + t * D, tmem + t * kChunkTile + half * 64 + (kk & 3) * 8, tc::desc_sw128(b + (E8 ? kk * 2048 : v_step(kk)), E8 ? HALF : v_part, 1024),
                                IDESC_O, add || half > 0 || kk > 0);
         };
         bool ok = n_run > 0 && __all_sync(0xffffffffu, chunk_wait(q_full, 0, abort_flag, p.err));
@@ -594,9 +629,8 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         __syncwarp();
     } else if (warp < 19) {
         // ---------------------------------------------------------- producers
-        const int v = warp - 17;  // 0: K (and Q), 1: V
-        const CUtensorMap* map = v ? &vmap : &kmap;
-        if (v == 0 && lane == 0 && n_run > 0) {
+        const bool second = warp == 18;  // V, and of 16-bit caches the last quarter of K; else K (the rest of it) and Q
+        if (!second && lane == 0 && n_run > 0) {
             const uint32_t bytes = HALVES * G * TQ * 128;
             mbar_arrive_expect_tx(q_full, ((cnt0 > 0) + (cnt1 > 0)) * bytes);
 #pragma unroll
@@ -607,12 +641,9 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         }
         const int BS = p.block_size, bpt = kChunkTile / BS;
         const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
-        // block of the tile and 64-channel part of this lane (codes: the whole block)
-        constexpr int PARTS = E8 ? 1 : HALVES;
-        const int j = lane / PARTS, h = lane % PARTS;
-        // the lane's block in tile i: -1 past the last row's tokens, wholly hidden, or outside the pool
-        auto entry = [&](int i) {
-            if (i >= n_run || j >= bpt) return -1;
+        // the block of tile i: -1 past the last row's tokens, wholly hidden, or outside the pool
+        auto entry = [&](int i, int j, bool take) {
+            if (i >= n_run || !take) return -1;
             const int t0 = chunk_tile_start(it, it.i0 + i) + j * BS;
             if (t0 > last || (t0 >= p.sinks && t0 + BS <= it.first_lo)) return -1;
             const int phys = table[t0 / BS];
@@ -622,14 +653,19 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             }
             return phys;
         };
-        int phys = entry(0);
-        int issued = 0;
-        for (int i = 0; i < n_run; ++i) {
-            const int use = 2 * i + v, s = use % NP;
+        // this lane's part of a K tile: block kj, channels from 64 kh on (codes: the block), and of a V tile: block lane
+        const int parts = E8 ? 1 : HALVES, k_first = !E8 && second ? bpt - bpt / 4 : 0;
+        const int k_blocks = E8 ? (second ? 0 : bpt) : second ? bpt / 4 : bpt - bpt / 4;
+        const int kj = k_first + lane / parts, kh = lane % parts;
+        const bool k_take = lane < k_blocks * parts, v_take = second && lane < bpt;
+        int k_phys = entry(0, kj, k_take), v_phys = entry(0, lane, v_take);
+        int uses = 0;  // of the ring that this warp has gone past, its own or not
+        auto step = [&](int use, int phys) {
+            const bool is_v = use & 1;
+            const int s = use % NP;
             uint64_t* filled = E8 ? &c_full[s] : &full[s];
-            const int next = entry(i + 1);
             [[maybe_unused]] float ks = 0.f, vs = 0.f;
-            if (SCALED && v == 0 && phys >= 0) {
+            if (SCALED && !is_v && phys >= 0) {
                 const int64_t at = static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh;
                 ks = p.k_scale[at];
                 vs = p.v_scale[at];
@@ -638,11 +674,11 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             bool good = true;
             if (lane == 0 && use >= NP)
                 good = chunk_wait(E8 ? &c_empty[s] : &empty[s], (use / NP - 1) & 1, abort_flag, p.err);
-            if (!__shfl_sync(0xffffffffu, good, 0)) break;
+            if (!__shfl_sync(0xffffffffu, good, 0)) return false;
             if constexpr (SCALED) {
-                if (v == 0) {
+                if (!is_v) {
                     if (lane < 8) {
-                        float* dst = reinterpret_cast<float*>(sm + S::SCALES) + (i % S::SLOTS) * 24 + lane;
+                        float* dst = reinterpret_cast<float*>(sm + S::SCALES) + ((use >> 1) % S::SLOTS) * 24 + lane;
                         dst[0] = ks;
                         dst[8] = vs;
                         dst[16] = fmaxf(__log2f(fabsf(vs)), -100.f);
@@ -650,28 +686,38 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                     __syncwarp();  // before the copies' barrier, which the softmax waits on in the end
                 }
             }
-            if (lane == 0) mbar_arrive_expect_tx(filled, __popc(loads) * (E8 ? BS * D : BS * 128));
+            if (lane == 0) mbar_arrive_expect_tx(filled, __popc(loads) * (E8 ? BS * D : is_v ? BS * D * 2 : BS * 128));
             __syncwarp();
-            if constexpr (E8) {
-                if (phys >= 0)
-                    bulk_copy_g2s(sm + S::CODES + s * S::CSTG + j * BS * D,
-                                  static_cast<const unsigned char*>(v ? p.v_cache : p.k_cache) +
+            if (phys >= 0) {
+                if constexpr (E8) {
+                    bulk_copy_g2s(sm + S::CODES + s * S::CSTG + (is_v ? lane : kj) * BS * D,
+                                  static_cast<const unsigned char*>(is_v ? p.v_cache : p.k_cache) +
                                       (static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh) * (BS * D),
                                   BS * D, filled, policy);
-            } else if (phys >= 0)
-                tc::tma_load_2d(ring + s * STG + h * HALF + j * BS * 128, map, h * 64, (phys * p.num_kv_heads + it.kvh) * BS,
-                                &full[s], policy);
-            phys = next;
-            ++issued;
+                } else {
+                    const int y = (phys * p.num_kv_heads + it.kvh) * BS;
+                    if (is_v) tc::tma_load_3d(ring + s * STG + lane * BS * D * 2, &vmap, 0, y, 0, filled, policy);
+                    else tc::tma_load_2d(ring + s * STG + kh * HALF + kj * BS * 128, &kmap, kh * 64, y, filled, policy);
+                }
+            }
+            return true;
+        };
+        for (int i = 0; i < n_run; ++i) {
+            const int k_next = entry(i + 1, kj, k_take), v_next = entry(i + 1, lane, v_take);
+            if ((!E8 || !second) && !step(2 * i, k_phys)) break;
+            uses = 2 * i + 1;
+            if (second && !step(2 * i + 1, v_phys)) break;
+            uses = 2 * i + 2;
+            k_phys = k_next;
+            v_phys = v_next;
         }
         // leave only when every copy into this block's shared memory has landed
         if (lane == 0) {
-            for (int i = max(0, issued - NP); i < issued; ++i) {
-                const int use = 2 * i + v;
-                if (use + NP >= 2 * issued && !mbar_wait(E8 ? &c_full[use % NP] : &full[use % NP], (use / NP) & 1))
-                    atomicOr(p.err, kErrTimeout);
+            for (int use = max(0, uses - NP); use < uses; ++use) {
+                const bool own = use & 1 ? second : !E8 || !second;
+                if (own && !mbar_wait(E8 ? &c_full[use % NP] : &full[use % NP], (use / NP) & 1)) atomicOr(p.err, kErrTimeout);
             }
-            if (v == 0 && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
+            if (!second && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
     } else if (E8 && warp >= 20) {
@@ -732,7 +778,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 }
             }
         }
-    } else if (!E8) {
+    } else if (!E8 && warp == 19) {
         // ------------------------------------------------------- V tiles' check
         for (int i = 0; i < n_run; ++i) {
             const int use = 2 * i + 1, s = use % NS;
@@ -742,10 +788,12 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             if (start + kChunkTile - 1 > it.pos0 || (start < last_lo && start + kChunkTile > p.sinks)) {
                 constexpr int CH = 8 * HALVES, STEP = 32 / CH;  // 16-byte chunks of a token, tokens of a warp's access
                 const int x = lane % CH, r0 = lane / CH;
-                unsigned char* vb = ring + s * STG + (x >> 3) * HALF + (x & 7) * 16;
+                const int bsh = p.block_size == 32 ? 5 : 4, part = p.block_size * 128;
+                unsigned char* vb = ring + s * STG + (x >> 3) * part + (x & 7) * 16;
+                auto row_at = [&](int r) { return vb + (r >> bsh) * (part * HALVES) + (r & (p.block_size - 1)) * 128; };
                 auto clear = [&](int from, int to) {  // tokens [from, to) of the tile
                     for (int r = min(kChunkTile, max(0, from)) + r0; r < min(kChunkTile, to); r += STEP)
-                        *reinterpret_cast<uint4*>(vb + r * 128) = make_uint4(0u, 0u, 0u, 0u);
+                        *reinterpret_cast<uint4*>(row_at(r)) = make_uint4(0u, 0u, 0u, 0u);
                 };
                 auto look = [&](int from, int to) {
                     bool bad = false;
@@ -754,7 +802,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                         uint4 u[8];
 #pragma unroll
                         for (int y = 0; y < 8; ++y)
-                            u[y] = r + y * STEP < to ? *reinterpret_cast<const uint4*>(vb + (r + y * STEP) * 128)
+                            u[y] = r + y * STEP < to ? *reinterpret_cast<const uint4*>(row_at(r + y * STEP))
                                                      : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
                         for (int y = 0; y < 8; ++y) bad = any_not_finite<ACT>(u[y]) || bad;
