@@ -28,7 +28,7 @@
 //                  swizzle), for K one of each (block, 64 channels) of a tile, for V,
 //                  whose products take a block's tokens at a time, one of each block.
 //                  The copies of a warp leave one after the other, some 94 cycles
-//                  each, so that warp 18 issues a quarter of K's as well.
+//                  each; sharing K's 16 between the two warps was no faster.
 //  warp 19         V tiles that some row sees in part: rows that no row of the
 //                  item sees become zeros (what lies there may be anything, and
 //                  0 times it must be 0); a number that is not finite among the
@@ -237,7 +237,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         tc::tmem_relinquish();
     } else if (threadIdx.x == 17 * 32) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], E8 ? 4 : i % 2 == 0 ? 2 : 1);  // 16-bit: K tiles in the even stages
+            mbar_init(&full[i], E8 ? 4 : 1);
             mbar_init(&empty[i], 1);
             mbar_init(&v_ok[i], 1);
         }
@@ -489,13 +489,14 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             auto put = [&](int x, const uint4& v) {  // chunk x of this thread's row
                 *reinterpret_cast<uint4*>(stage + lane * TURN + ((x ^ (lane & (CHUNKS - 1))) * 16)) = v;
             };
+            const int inv_g = 65536 / G + 1;  // (r inv_g) >> 16 = r / G for r < 128, G <= 64
             // the warp's rows, TURN bytes each, to `row_dst(row's index in the item) + offset`
             auto flush = [&](auto row_dst) {
                 __syncwarp();
 #pragma unroll
                 for (int y = 0; y < CHUNKS; ++y) {
                     const int r = y * (32 / CHUNKS) + lane / CHUNKS, x = lane % CHUNKS;
-                    const int rr = (warp & 3) * 32 + r, rt = rr / G;
+                    const int rr = (warp & 3) * 32 + r, rt = (rr * inv_g) >> 16;
                     if (rt < rows_of(t))
                         *reinterpret_cast<uint4*>(row_dst(it.row0 + t * TQ + rt, it.kvh * G + rr - rt * G) + x * 16) =
                             *reinterpret_cast<const uint4*>(stage + r * TURN + ((x ^ (r & (CHUNKS - 1))) * 16));
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         __syncwarp();
     } else if (warp < 19) {
         // ---------------------------------------------------------- producers
-        const bool second = warp == 18;  // V, and of 16-bit caches the last quarter of K; else K (the rest of it) and Q
+        const bool second = warp == 18;  // V; else K and Q
         if (!second && lane == 0 && n_run > 0) {
             const uint32_t bytes = HALVES * G * TQ * 128;
             mbar_arrive_expect_tx(q_full, ((cnt0 > 0) + (cnt1 > 0)) * bytes);
@@ -653,19 +654,17 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             }
             return phys;
         };
-        // this lane's part of a K tile: block kj, channels from 64 kh on (codes: the block), and of a V tile: block lane
-        const int parts = E8 ? 1 : HALVES, k_first = !E8 && second ? bpt - bpt / 4 : 0;
-        const int k_blocks = E8 ? (second ? 0 : bpt) : second ? bpt / 4 : bpt - bpt / 4;
-        const int kj = k_first + lane / parts, kh = lane % parts;
-        const bool k_take = lane < k_blocks * parts, v_take = second && lane < bpt;
-        int k_phys = entry(0, kj, k_take), v_phys = entry(0, lane, v_take);
-        int uses = 0;  // of the ring that this warp has gone past, its own or not
-        auto step = [&](int use, int phys) {
-            const bool is_v = use & 1;
+        // this lane's part of a tile: block j, of K channels from 64 kh on (codes: the block)
+        const int parts = E8 ? 1 : HALVES;
+        const int j = second ? lane : lane / parts, kh = lane % parts;
+        const bool take = lane < (second ? bpt : bpt * parts);
+        int phys = entry(0, j, take), issued = 0;
+        for (int i = 0; i < n_run; ++i) {
+            const int use = 2 * i + second, next = entry(i + 1, j, take);
             const int s = use % NP;
             uint64_t* filled = E8 ? &c_full[s] : &full[s];
             [[maybe_unused]] float ks = 0.f, vs = 0.f;
-            if (SCALED && !is_v && phys >= 0) {
+            if (SCALED && !second && phys >= 0) {
                 const int64_t at = static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh;
                 ks = p.k_scale[at];
                 vs = p.v_scale[at];
@@ -674,11 +673,11 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             bool good = true;
             if (lane == 0 && use >= NP)
                 good = chunk_wait(E8 ? &c_empty[s] : &empty[s], (use / NP - 1) & 1, abort_flag, p.err);
-            if (!__shfl_sync(0xffffffffu, good, 0)) return false;
+            if (!__shfl_sync(0xffffffffu, good, 0)) break;
             if constexpr (SCALED) {
-                if (!is_v) {
+                if (!second) {
                     if (lane < 8) {
-                        float* dst = reinterpret_cast<float*>(sm + S::SCALES) + ((use >> 1) % S::SLOTS) * 24 + lane;
+                        float* dst = reinterpret_cast<float*>(sm + S::SCALES) + (i % S::SLOTS) * 24 + lane;
                         dst[0] = ks;
                         dst[8] = vs;
                         dst[16] = fmaxf(__log2f(fabsf(vs)), -100.f);
@@ -686,36 +685,28 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                     __syncwarp();  // before the copies' barrier, which the softmax waits on in the end
                 }
             }
-            if (lane == 0) mbar_arrive_expect_tx(filled, __popc(loads) * (E8 ? BS * D : is_v ? BS * D * 2 : BS * 128));
+            if (lane == 0) mbar_arrive_expect_tx(filled, __popc(loads) * (E8 ? BS * D : second ? BS * D * 2 : BS * 128));
             __syncwarp();
             if (phys >= 0) {
                 if constexpr (E8) {
-                    bulk_copy_g2s(sm + S::CODES + s * S::CSTG + (is_v ? lane : kj) * BS * D,
-                                  static_cast<const unsigned char*>(is_v ? p.v_cache : p.k_cache) +
+                    bulk_copy_g2s(sm + S::CODES + s * S::CSTG + j * BS * D,
+                                  static_cast<const unsigned char*>(second ? p.v_cache : p.k_cache) +
                                       (static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh) * (BS * D),
                                   BS * D, filled, policy);
                 } else {
                     const int y = (phys * p.num_kv_heads + it.kvh) * BS;
-                    if (is_v) tc::tma_load_3d(ring + s * STG + lane * BS * D * 2, &vmap, 0, y, 0, filled, policy);
-                    else tc::tma_load_2d(ring + s * STG + kh * HALF + kj * BS * 128, &kmap, kh * 64, y, filled, policy);
+                    if (second) tc::tma_load_3d(ring + s * STG + j * BS * D * 2, &vmap, 0, y, 0, filled, policy);
+                    else tc::tma_load_2d(ring + s * STG + kh * HALF + j * BS * 128, &kmap, kh * 64, y, filled, policy);
                 }
             }
-            return true;
-        };
-        for (int i = 0; i < n_run; ++i) {
-            const int k_next = entry(i + 1, kj, k_take), v_next = entry(i + 1, lane, v_take);
-            if ((!E8 || !second) && !step(2 * i, k_phys)) break;
-            uses = 2 * i + 1;
-            if (second && !step(2 * i + 1, v_phys)) break;
-            uses = 2 * i + 2;
-            k_phys = k_next;
-            v_phys = v_next;
+            phys = next;
+            ++issued;
         }
         // leave only when every copy into this block's shared memory has landed
         if (lane == 0) {
-            for (int use = max(0, uses - NP); use < uses; ++use) {
-                const bool own = use & 1 ? second : !E8 || !second;
-                if (own && !mbar_wait(E8 ? &c_full[use % NP] : &full[use % NP], (use / NP) & 1)) atomicOr(p.err, kErrTimeout);
+            for (int i = max(0, issued - NP / 2); i < issued; ++i) {
+                const int use = 2 * i + second;
+                if (!mbar_wait(E8 ? &c_full[use % NP] : &full[use % NP], (use / NP) & 1)) atomicOr(p.err, kErrTimeout);
             }
             if (!second && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
         }
