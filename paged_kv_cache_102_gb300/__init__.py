@@ -690,57 +690,67 @@ def _decode_scaled_args(q, k_cache, v_cache, k_scales, v_scales, block_tables, c
     return args, out, workspace
 
 
+_NO_SCALES = (None, None, None, None)
+
+
 def _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales):
-    """(cache shape, (k_scale, v_scale, k_scales, v_scales) pointers) of a cache of q's type, or of E4M3 codes with
-    either kind of scales."""
-    if len(k_cache.shape) != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    """(cache shape, device, (k_scale, v_scale, k_scales, v_scales) pointers) of a cache of q's type, or of E4M3 codes
+    with either kind of scales."""
+    shape, dtype = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dtype:
         raise ValueError(f"{name}: k_cache and v_cache must be [num_blocks, num_kv_heads, block_size, head_dim] of one type")
-    if not k_cache.is_cuda:
-        raise ValueError(f"{name}: k_cache must be a CUDA tensor")
     device = k_cache.device
+    if device.type != "cuda":
+        raise ValueError(f"{name}: k_cache must be a CUDA tensor")
     if k_scales is not None or v_scales is not None:
         if k_scale is not None or v_scale is not None:
             raise ValueError(f"{name}: k_scale, v_scale or k_scales, v_scales, not both")
-        shape = _require_scales(name, k_cache, v_cache, k_scales, v_scales)
-        return shape, (None, None, *_pointers(name, device, "k_scales v_scales", k_scales, v_scales))
-    if k_cache.dtype in _E4M3_TYPES:
-        if k_scale is None or v_scale is None:
+        _require_scales(name, k_cache, v_cache, k_scales, v_scales)
+        return shape, device, (None, None, *_pointers(name, device, "k_scales v_scales", k_scales, v_scales))
+    if k_scale is None and v_scale is None:
+        if dtype in _E4M3_TYPES:
             raise ValueError(f"{name}: an E4M3 cache needs k_scale and v_scale, or k_scales and v_scales")
-    elif k_cache.dtype != q.dtype:
-        raise ValueError(f"{name}: the cache must be of q's type or hold E4M3 codes")
-    for t in (k_scale, v_scale):
-        if t is not None and (t.dtype is not torch.float32 or t.numel() != 1):
+        scales = _NO_SCALES
+    else:
+        if k_scale is None or v_scale is None:
+            raise ValueError(f"{name}: k_scale and v_scale go together")
+        if k_scale.dtype is not torch.float32 or v_scale.dtype is not torch.float32 or k_scale.numel() != 1 or v_scale.numel() != 1:
             raise ValueError(f"{name}: k_scale and v_scale must be float32 with one element")
-    scales = [None if t is None else next(_pointers(name, device, what, t))
-              for what, t in (("k_scale", k_scale), ("v_scale", v_scale))]
-    return k_cache.shape, (*scales, None, None)
+        scales = (*_pointers(name, device, "k_scale v_scale", k_scale, v_scale), None, None)
+    if dtype not in _E4M3_TYPES and dtype is not q.dtype:
+        raise ValueError(f"{name}: the cache must be of q's type or hold E4M3 codes")
+    return shape, device, scales
 
 
-def _row_args(name, q, block_tables, context_lens, shape):
-    """Checks of single-token queries q [B, Hq, D] and their rows' tables and lengths; returns B, Hq, max_blocks."""
-    if q.dim() != 3 or q.shape[2] != shape[3]:
+def _row_args(name, q, out, block_tables, context_lens, head_dim, stream, device):
+    """Checks of single-token queries q [B, Hq, D], their output, tables and lengths; returns (out, B, Hq, max_blocks)."""
+    qshape, tshape = q.shape, block_tables.shape
+    if len(qshape) != 3 or qshape[2] != head_dim:
         raise ValueError(f"{name}: q must be [B, num_q_heads, head_dim]")
-    B, Hq, _ = q.shape
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32:
+    if block_tables.dtype is not torch.int32 or context_lens.dtype is not torch.int32:
         raise ValueError(f"{name}: block_tables and context_lens must be int32")
-    if block_tables.dim() != 2 or block_tables.shape[0] != B or context_lens.shape != (B,):
+    B = qshape[0]
+    if len(tshape) != 2 or tshape[0] != B or context_lens.shape != (B,):
         raise ValueError(f"{name}: block_tables [B, max_blocks], context_lens [B]")
-    return B, Hq, block_tables.shape[1]
-
-
-def _out_like(name, q, out, stream, device):
     if out is None:
-        return _output(stream, device, q.shape, q.dtype)
-    if out.shape != q.shape or out.dtype != q.dtype:
-        raise ValueError(f"{name}: out must match q")
-    _require_out(device, out)
-    return out
+        out = _output(stream, device, qshape, q.dtype)
+    else:
+        if out.shape != qshape or out.dtype is not q.dtype:
+            raise ValueError(f"{name}: out must match q")
+        _require_out(device, out)
+    return out, B, qshape[1], tshape[1]
 
 
-def _int32(name, **values):
-    for what, x in values.items():
-        if not -2 ** 31 <= int(x) < 2 ** 31:
-            raise ValueError(f"{name}: {what} out of range")
+def _reused(device, stream, s, nbytes, kind):
+    """_workspace for the raw stream s of a call, with few host steps where the stream's reusable one is enough."""
+    if stream is None:
+        buf = _ws_cache.get((device.index, s, kind))
+        if buf is not None and buf.numel() >= nbytes and not torch._C._cuda_isCurrentStreamCapturing():
+            return buf
+    return _workspace(device, stream, max(nbytes, 1), kind)
+
+
+_INT_MAX = 2 ** 31 - 1
 
 
 @functools.lru_cache(maxsize=1024)
@@ -759,35 +769,38 @@ def paged_attention_chunk(q, k_cache, v_cache, block_tables, context_lens, seq_s
     ones.  Rows of q and out may lie apart (contiguous [Hq, D] each), rows of no sequence stay as they are (a new out
     holds zeros there).  The cache is of q's type or E4M3 with either kind of scales."""
     name = "paged_attention_chunk"
-    (NB, Hkv, bs, D), scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales)
-    if q.dim() != 3 or q.shape[2] != D:
+    shape, device, scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales)
+    NB, Hkv, bs, D = shape
+    qshape, tshape = q.shape, block_tables.shape
+    if len(qshape) != 3 or qshape[2] != D:
         raise ValueError(f"{name}: q must be [num_tokens, num_q_heads, head_dim]")
-    T, Hq, _ = q.shape
-    if block_tables.dtype != torch.int32 or context_lens.dtype != torch.int32 or seq_starts.dtype != torch.int32:
+    T, Hq, _ = qshape
+    i32 = torch.int32
+    if block_tables.dtype is not i32 or context_lens.dtype is not i32 or seq_starts.dtype is not i32:
         raise ValueError(f"{name}: block_tables, context_lens and seq_starts must be int32")
-    if block_tables.dim() != 2:
-        raise ValueError(f"{name}: block_tables must be [B, max_blocks]")
-    B, max_blocks = block_tables.shape
-    if context_lens.shape != (B,) or seq_starts.shape != (B + 1,):
-        raise ValueError(f"{name}: context_lens [B], seq_starts [B + 1]")
-    if window is not None and window < 1:
-        raise ValueError(f"{name}: window must be positive (None: no window)")
-    _int32(name, window=window or 0, sinks=sinks)
-    device = k_cache.device
+    if len(tshape) != 2 or context_lens.shape != (tshape[0],) or seq_starts.shape != (tshape[0] + 1,):
+        raise ValueError(f"{name}: block_tables [B, max_blocks], context_lens [B], seq_starts [B + 1]")
+    B, max_blocks = tshape
+    if window is None:
+        window = 0
+    elif not 0 < window <= _INT_MAX:
+        raise ValueError(f"{name}: window must be positive (None: no window) and below 2^31")
+    if not 0 <= sinks <= _INT_MAX:
+        raise ValueError(f"{name}: sinks must be from 0 to 2^31 - 1")
     if out is None:
-        out = _output(stream, device, q.shape, q.dtype, zero=True)
-    elif out.shape != q.shape or out.dtype != q.dtype:
+        out = _output(stream, device, qshape, q.dtype, zero=True)
+    elif out.shape != qshape or out.dtype is not q.dtype:
         raise ValueError(f"{name}: out must match q")
-    qs, os = _rows(name, "q", q, device.index, q.shape), _rows(name, "out", out, device.index, q.shape)
+    qs, os = _rows(name, "q", q, device.index, qshape), _rows(name, "out", out, device.index, qshape)
+    s = _stream(stream, device)
     if workspace is None:
-        need = _size_of("pkv_chunk_workspace_size", B, T, Hq, Hkv, D, max_blocks, bs)
-        workspace = _workspace(device, stream, max(need, 1), kind=2)
+        workspace = _reused(device, stream, s, _size_of("pkv_chunk_workspace_size", B, T, Hq, Hkv, D, max_blocks, bs), 2)
     kc, vc, tables, lens, starts, ws = _pointers(
         name, device, "k_cache v_cache block_tables context_lens seq_starts workspace", k_cache, v_cache, block_tables,
         context_lens, seq_starts, workspace)
     _call_on(device, name, q.data_ptr(), qs, kc, vc, tables, max_blocks, lens, starts, B, T, Hq, Hkv, bs, D, NB,
-             float(scale), window or 0, sinks, out.data_ptr(), os, _code(q), _code(k_cache), *scales, ws,
-             workspace.numel() * workspace.element_size(), _stream(stream, device))
+             float(scale), window, sinks, out.data_ptr(), os, _code(q), _code(k_cache), *scales, ws,
+             workspace.numel() * workspace.element_size(), s)
     return out
 
 
@@ -799,21 +812,21 @@ def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_len
     entries.  A context length of 0 (a padding row) gives zeros.  The cache is of q's type or E4M3 with either kind
     of scales."""
     name = "paged_attention_decode_window"
-    shape, scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales)
+    shape, device, scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales)
     NB, Hkv, bs, D = shape
-    B, Hq, max_blocks = _row_args(name, q, block_tables, context_lens, shape)
-    _int32(name, window=window, sinks=sinks)
-    device = k_cache.device
-    out = _out_like(name, q, out, stream, device)
+    out, B, Hq, max_blocks = _row_args(name, q, out, block_tables, context_lens, D, stream, device)
+    if not 0 < window <= _INT_MAX or not 0 <= sinks <= _INT_MAX:
+        raise ValueError(f"{name}: window must be positive, sinks not negative, both below 2^31")
+    s = _stream(stream, device)
     if workspace is None:
         need = _size_of("pkv_window_workspace_size", B, Hq, Hkv, D, max_blocks, bs, window, sinks,
-                        int(scales[2] is not None), int(partition_size))
-        workspace = _workspace(device, stream, max(need, 1))
+                        0 if scales[2] is None else 1, partition_size)
+        workspace = _reused(device, stream, s, need, 0)
     qp, kc, vc, tables, lens, ws = _pointers(name, device, "q k_cache v_cache block_tables context_lens workspace", q,
                                              k_cache, v_cache, block_tables, context_lens, workspace)
     _call_on(device, name, qp, kc, vc, tables, max_blocks, lens, B, Hq, Hkv, bs, D, NB, float(scale), window, sinks,
-             out.data_ptr(), _code(q), _code(k_cache), *scales, int(partition_size), ws,
-             workspace.numel() * workspace.element_size(), _stream(stream, device))
+             out.data_ptr(), _code(q), _code(k_cache), *scales, partition_size, ws,
+             workspace.numel() * workspace.element_size(), s)
     return out
 
 
@@ -824,22 +837,22 @@ def paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_len
     kv head, to scores float32 [B, Hkv, S], S at least max_blocks * block_size; returns out [B, Hq, D].  A context
     length of 0 gives zeros and adds nothing."""
     name = "paged_attention_decode_scored"
-    shape, scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, None, None)
+    shape, device, scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, None, None)
     NB, Hkv, bs, D = shape
-    B, Hq, max_blocks = _row_args(name, q, block_tables, context_lens, shape)
-    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (B, Hkv):
+    out, B, Hq, max_blocks = _row_args(name, q, out, block_tables, context_lens, D, stream, device)
+    sshape = scores.shape
+    if scores.dtype is not torch.float32 or len(sshape) != 3 or sshape[0] != B or sshape[1] != Hkv:
         raise ValueError(f"{name}: scores must be float32 [B, num_kv_heads, tokens]")
-    device = k_cache.device
-    out = _out_like(name, q, out, stream, device)
+    s = _stream(stream, device)
     if workspace is None:
-        need = _size_of("pkv_scored_workspace_size", B, Hq, Hkv, D, max_blocks, bs, int(partition_size))
-        workspace = _workspace(device, stream, max(need, 1), kind=3)
+        need = _size_of("pkv_scored_workspace_size", B, Hq, Hkv, D, max_blocks, bs, partition_size)
+        workspace = _reused(device, stream, s, need, 3)
     qp, kc, vc, tables, lens, sp, ws = _pointers(
         name, device, "q k_cache v_cache block_tables context_lens scores workspace", q, k_cache, v_cache, block_tables,
         context_lens, scores, workspace)
     _call_on(device, name, qp, kc, vc, tables, max_blocks, lens, B, Hq, Hkv, bs, D, NB, float(scale), sp,
-             scores.shape[2], out.data_ptr(), _code(q), _code(k_cache), *scales[:2], int(partition_size), ws,
-             workspace.numel() * workspace.element_size(), _stream(stream, device))
+             sshape[2], out.data_ptr(), _code(q), _code(k_cache), *scales[:2], partition_size, ws,
+             workspace.numel() * workspace.element_size(), s)
     return out
 
 
@@ -859,42 +872,43 @@ def paged_kv_evict(k_cache, v_cache, scores, block_tables, context_lens, dst_tab
     scores that moved along (as wide as the old ones, zeros behind them) and the tokens that stayed, int32
     [B, Hkv, budget], -1 behind them.  Not for block-scaled caches."""
     name = "paged_kv_evict"
-    if len(k_cache.shape) != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    shape = k_cache.shape
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype:
         raise ValueError(f"{name}: k_cache and v_cache must be [num_blocks, num_kv_heads, block_size, head_dim] of one type")
-    NB, Hkv, bs, D = k_cache.shape
     device = k_cache.device
-    if block_tables.dim() != 2 or dst_tables.dim() != 2:
-        raise ValueError(f"{name}: block_tables [B, max_blocks], dst_tables [B, max_dst_blocks]")
-    B, max_blocks = block_tables.shape
-    if dst_tables.shape[0] != B or context_lens.shape != (B,):
-        raise ValueError(f"{name}: dst_tables [B, max_dst_blocks], context_lens [B]")
-    i32 = torch.int32
+    if device.type != "cuda":
+        raise ValueError(f"{name}: k_cache must be a CUDA tensor")
+    NB, Hkv, bs, D = shape
+    tshape, dshape, sshape = block_tables.shape, dst_tables.shape, scores.shape
+    B = tshape[0] if len(tshape) == 2 else -1
+    if len(tshape) != 2 or len(dshape) != 2 or dshape[0] != B or context_lens.shape != (B,):
+        raise ValueError(f"{name}: block_tables [B, max_blocks], dst_tables [B, max_dst_blocks], context_lens [B]")
+    i32, f32 = torch.int32, torch.float32
     if block_tables.dtype is not i32 or dst_tables.dtype is not i32 or context_lens.dtype is not i32:
         raise ValueError(f"{name}: block_tables, dst_tables and context_lens must be int32")
-    if scores.dtype != torch.float32 or scores.dim() != 3 or scores.shape[:2] != (B, Hkv):
+    if scores.dtype is not f32 or len(sshape) != 3 or sshape[0] != B or sshape[1] != Hkv:
         raise ValueError(f"{name}: scores must be float32 [B, num_kv_heads, tokens]")
-    if budget < 1:
-        raise ValueError(f"{name}: budget must be positive")
-    _int32(name, budget=budget, recent=recent, sinks=sinks)
-
-    def output(t, shape, dtype, what):
-        if t is None:
-            return _output(stream, device, shape, dtype)
-        if t.dtype is not dtype or tuple(t.shape) != tuple(shape):
-            raise ValueError(f"{name}: {what} must be {dtype} {list(shape)}")
-        return t
-
-    if scores_out is not None and (scores_out.dim() != 3 or scores_out.shape[:2] != (B, Hkv)):
-        raise ValueError(f"{name}: scores_out must be float32 [B, num_kv_heads, tokens]")
-    scores_out = output(scores_out, scores.shape if scores_out is None else scores_out.shape, torch.float32, "scores_out")
-    lens_out = output(lens_out, (B,), i32, "lens_out")
-    kept = output(kept, (B, Hkv, int(budget)), i32, "kept")
+    if not 0 < budget <= _INT_MAX or not 0 <= recent <= _INT_MAX or not 0 <= sinks <= _INT_MAX:
+        raise ValueError(f"{name}: budget must be positive, recent and sinks not negative, all below 2^31")
+    if scores_out is None:
+        scores_out, oshape = _output(stream, device, sshape, f32), sshape
+    else:
+        oshape = scores_out.shape
+        if scores_out.dtype is not f32 or len(oshape) != 3 or oshape[0] != B or oshape[1] != Hkv:
+            raise ValueError(f"{name}: scores_out must be float32 [B, num_kv_heads, tokens]")
+    if lens_out is None:
+        lens_out = _output(stream, device, (B,), i32)
+    elif lens_out.dtype is not i32 or lens_out.shape != (B,):
+        raise ValueError(f"{name}: lens_out must be int32 [B]")
+    if kept is None:
+        kept = _output(stream, device, (B, Hkv, budget), i32)
+    elif kept.dtype is not i32 or kept.shape != (B, Hkv, budget):
+        raise ValueError(f"{name}: kept must be int32 [B, num_kv_heads, budget]")
     kc, vc, sp, tables, lens, dst, so, lo, kp = _pointers(
         name, device, "k_cache v_cache scores block_tables context_lens dst_tables scores_out lens_out kept", k_cache,
         v_cache, scores, block_tables, context_lens, dst_tables, scores_out, lens_out, kept)
-    _call_on(device, name, kc, vc, NB, Hkv, bs, D, _code(k_cache), sp, scores.shape[2], tables, max_blocks, lens, B, dst,
-             dst_tables.shape[1], int(budget), int(recent), int(sinks), so, scores_out.shape[2], lo, kp,
-             _stream(stream, device))
+    _call_on(device, name, kc, vc, NB, Hkv, bs, D, _code(k_cache), sp, sshape[2], tables, tshape[1], lens, B, dst,
+             dshape[1], budget, recent, sinks, so, oshape[2], lo, kp, _stream(stream, device))
     return Evicted(lens_out, scores_out, kept)
 
 

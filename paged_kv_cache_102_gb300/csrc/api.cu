@@ -276,6 +276,30 @@ static int window_blocks(int max_blocks, int block_size, int window, int sinks) 
     return static_cast<int>(std::min<long long>(max_blocks, n));
 }
 
+// Partitions of the calls with a window or kept logits.  Under a window most rows are as long as they can be, so
+// partitions of equal size (tensor cores: whole tiles of 128) waste none: 1072 tokens in three of 384 instead of 512,
+// 512 and 48.  The CUDA-core kernel's 1024 tokens are halved while its blocks would not fill the GPU's SMs (three
+// blocks each) twice.
+static int ext_partition_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim, int blocks, int block_size,
+                              int partition_size, bool block_scales, bool window) {
+    const int P0 = (block_scales ? pkv_scaled_partition_size : pkv_resolve_partition_size)(
+        num_seqs, num_q_heads, num_kv_heads, head_dim, blocks, block_size, partition_size);
+    if (P0 <= 0 || partition_size != PKV_PARTITION_AUTO) return P0;
+    const int64_t ctx = static_cast<int64_t>(blocks) * block_size;
+    const int G = num_q_heads / num_kv_heads;
+    const bool grouped = block_scales || (G >= 4 && (head_dim == 128 || num_kv_heads % 2 == 0));
+    int64_t P = P0;
+    if (!grouped)
+        while (P > 256 && (P / 2) % block_size == 0 && (P / 2) % kStageTokens == 0 &&
+               num_seqs * static_cast<int64_t>(num_kv_heads) * ((ctx + P - 1) / P) < 2 * 456)
+            P /= 2;
+    if (window && P < ctx) {
+        const int64_t parts = (ctx + P - 1) / P, unit = grouped ? 128 : kStageTokens;
+        P = std::min<int64_t>(P, ((ctx + parts - 1) / parts + unit - 1) / unit * unit);
+    }
+    return static_cast<int>(P);
+}
+
 // Workspace with kept logits: the statistics of every partition, then as without, then the logits.
 struct ScoredLayout {
     size_t ml, o, logits, total;
@@ -294,15 +318,20 @@ extern "C" size_t pkv_window_workspace_size(int num_seqs, int num_q_heads, int n
                                             int max_blocks_per_seq, int block_size, int window, int sinks,
                                             int block_scales, int partition_size) {
     const int n = window_blocks(max_blocks_per_seq, block_size, window, sinks);
-    return (block_scales ? pkv_scaled_workspace_size : pkv_workspace_size)(num_seqs, num_q_heads, num_kv_heads, head_dim, n,
-                                                                          block_size, partition_size);
+    if (num_seqs < 1 || num_q_heads < 1 || num_kv_heads < 1 || n < 1 || block_size < 1 || num_q_heads < num_kv_heads) return 0;
+    const int P = ext_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, n, block_size, partition_size,
+                                     block_scales != 0, true);
+    return pkv_workspace_size_of(num_seqs, num_q_heads, head_dim, n, block_size, P);
 }
 
 extern "C" size_t pkv_scored_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads, int head_dim,
                                             int max_blocks_per_seq, int block_size, int partition_size) {
-    const int P = pkv_resolve_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq,
-                                             block_size, partition_size);
-    if (P <= 0 || num_seqs <= 0 || head_dim <= 0) return 0;
+    if (num_seqs < 1 || num_q_heads < 1 || num_kv_heads < 1 || head_dim < 1 || max_blocks_per_seq < 1 || block_size < 1 ||
+        num_q_heads < num_kv_heads)
+        return 0;
+    const int P = ext_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, max_blocks_per_seq, block_size,
+                                     partition_size, false, false);
+    if (P <= 0) return 0;
     return scored_layout(num_seqs, num_q_heads, head_dim, static_cast<long long>(max_blocks_per_seq) * block_size, P).total;
 }
 
@@ -343,8 +372,10 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         return fail(PKV_ERR_INVALID, F + ": " + "q, caches, out, workspace must be 16-byte aligned");
     // partitions count the tokens that are left (ext: a window's)
     const int kept_blocks = ext ? window_blocks(max_blocks_per_seq, block_size, ext->window, ext->sinks) : max_blocks_per_seq;
-    const int P = (block_scales ? pkv_scaled_partition_size : pkv_resolve_partition_size)(
-        num_seqs, num_q_heads, num_kv_heads, head_dim, kept_blocks, block_size, partition_size);
+    const int P = ext ? ext_partition_size(num_seqs, num_q_heads, num_kv_heads, head_dim, kept_blocks, block_size,
+                                           partition_size, block_scales, ext->window > 0)
+                      : (block_scales ? pkv_scaled_partition_size : pkv_resolve_partition_size)(
+                            num_seqs, num_q_heads, num_kv_heads, head_dim, kept_blocks, block_size, partition_size);
     if (P <= 0)
         return fail(PKV_ERR_INVALID, F + ": " + "partition_size must be 0, -1 or a positive multiple of 32 and of block_size");
     if (static_cast<long long>(max_blocks_per_seq) * block_size > 0x7fffffffLL)
@@ -484,7 +515,7 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         e = cache_dtype == PKV_E4M3 ? launch_decode_bf16_e4m3(p, head_dim, block_size, G, s)
                                     : launch_decode_bf16_bf16(p, head_dim, block_size, G, s);
     if (e != cudaSuccess) return cuda_fail((F + ": partition kernel launch").c_str(), e);
-    if (max_parts > 1) {
+    if (max_parts > 1 && !scored) {
         MergeParams m{};
         m.context_lens = context_lens;
         m.num_seqs = num_seqs;
@@ -506,9 +537,9 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         if (e != cudaSuccess) return cuda_fail((F + ": merge kernel launch").c_str(), e);
     }
     if (scored) {
-        const AddWeightsParams a{p.logits, p.ws_ml, context_lens, ext->scores, ext->score_tokens, p.logit_tokens,
-                                 num_seqs, num_kv_heads, G, P, max_parts, static_cast<int>(max_ctx)};
-        e = launch_add_weights(a, s);
+        const AddWeightsParams a{p.logits, p.ws_ml, context_lens, ext->scores, p.ws_o, out, ext->score_tokens,
+                                 p.logit_tokens, num_seqs, num_kv_heads, G, P, max_parts, static_cast<int>(max_ctx)};
+        e = launch_scored_finish(a, act_dtype, head_dim, s);
         if (e != cudaSuccess) return cuda_fail((F + ": weights kernel launch").c_str(), e);
     }
     return PKV_OK;

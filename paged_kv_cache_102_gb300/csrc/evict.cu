@@ -13,6 +13,7 @@
 // neighbouring tokens, and with g tokens above that key and e equal to it before
 // a token, its place is g + min(e, equal ones that stay); g and e come from one
 // packed scan.
+// A small budget's rows move in the same kernel, by the block that chose them.
 // evict_move_kernel: 16 bytes a thread, kept rows of K and V to their new
 // blocks; source and destination blocks differ, so that rows are independent.
 #include "kernels.h"
@@ -27,6 +28,7 @@ constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kKeyTokens = 48 * 1024;
 constexpr int kMoveThreads = 256;
+constexpr int kMoveHere = 64 * 1024;  // bytes of K that the selecting block moves itself
 constexpr int kAddThreads = 256;
 
 // 32-bit key of the scores' order: NaN 0, then -inf .. +inf (-0 as 0).
@@ -59,13 +61,25 @@ __device__ __forceinline__ uint32_t block_scan(uint32_t x, uint32_t* totals, uin
     return incl - x + __shfl_sync(0xffffffffu, ti - t, warp);
 }
 
-__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p) {
-    extern __shared__ uint32_t keys[];
+// 16 bytes, chunk c of the row, of kept token `from` to place i; false if a table entry is no block.
+__device__ __forceinline__ bool move_chunk(const EvictParams& p, int b, int h, int from, int i, int c, int vecs) {
+    const int src = p.block_tables[static_cast<int64_t>(b) * p.max_blocks_per_seq + from / p.block_size];
+    const int dst = p.dst_tables[static_cast<int64_t>(b) * p.max_dst_blocks + i / p.block_size];
+    if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) return false;
+    const int64_t s = ((static_cast<int64_t>(src) * p.num_kv_heads + h) * p.block_size + from % p.block_size) * vecs + c;
+    const int64_t d = ((static_cast<int64_t>(dst) * p.num_kv_heads + h) * p.block_size + i % p.block_size) * vecs + c;
+    const uint4 k = static_cast<const uint4*>(p.k_cache)[s], v = static_cast<const uint4*>(p.v_cache)[s];
+    static_cast<uint4*>(p.k_cache)[d] = k;
+    static_cast<uint4*>(p.v_cache)[d] = v;
+    return true;
+}
+
+// The selection of one (sequence, kv head): kept tokens, their scores; returns how many stay.
+__device__ __forceinline__ int evict_select(const EvictParams& p, int h, int b, uint32_t* keys) {
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t totals[2][kSelectWarps];
     __shared__ uint32_t s_bin, s_rest;
-    asm volatile("griddepcontrol.launch_dependents;");
-    const int h = blockIdx.x, b = blockIdx.y, tid = threadIdx.x;
+    const int tid = threadIdx.x;
     const int64_t row = static_cast<int64_t>(b) * p.num_kv_heads + h;
     const float* scores = p.scores + row * p.score_tokens;
     int32_t* kept = p.kept + row * p.budget;
@@ -88,7 +102,7 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
             kept[i] = i;
             out[i] = scores[i];
         }
-        return;
+        return m;
     }
     // the others compete: [sinks, L - recent)
     const int first = p.sinks, last = L - p.recent;
@@ -159,6 +173,25 @@ __global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const Evic
         above += all & 0xffffu;
         equal += all >> 16;
     }
+    return m;
+}
+
+template <bool MOVE>
+__global__ void __launch_bounds__(kSelectThreads) evict_select_kernel(const EvictParams p) {
+    extern __shared__ uint32_t keys[];
+    asm volatile("griddepcontrol.launch_dependents;");
+    const int h = blockIdx.x, b = blockIdx.y;
+    const int m = evict_select(p, h, b, keys);
+    if constexpr (MOVE) {
+        __syncthreads();  // the list of tokens, written by this block's threads
+        const int32_t* kept = p.kept + (static_cast<int64_t>(b) * p.num_kv_heads + h) * p.budget;
+        const int vecs = p.row_bytes / 16, shift = 31 - __clz(vecs);
+        bool good = true;
+#pragma unroll 4
+        for (int x = threadIdx.x; x < m * vecs; x += kSelectThreads)
+            good = move_chunk(p, b, h, kept[x >> shift], x >> shift, x & (vecs - 1), vecs) && good;
+        if (!good) atomicOr(p.err, kErrBadBlock);
+    }
 }
 
 __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictParams p) {
@@ -169,23 +202,16 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (i >= p.budget) return;
     const int from = p.kept[(static_cast<int64_t>(b) * p.num_kv_heads + h) * p.budget + i];
-    if (from < 0) return;
-    const int src = p.block_tables[static_cast<int64_t>(b) * p.max_blocks_per_seq + from / p.block_size];
-    const int dst = p.dst_tables[static_cast<int64_t>(b) * p.max_dst_blocks + i / p.block_size];
-    if (src < 0 || src >= p.num_blocks || dst < 0 || dst >= p.num_blocks) {
-        if (c == 0) atomicOr(p.err, kErrBadBlock);
-        return;
-    }
-    const int64_t s = ((static_cast<int64_t>(src) * p.num_kv_heads + h) * p.block_size + from % p.block_size) * vecs + c;
-    const int64_t d = ((static_cast<int64_t>(dst) * p.num_kv_heads + h) * p.block_size + i % p.block_size) * vecs + c;
-    const uint4 k = static_cast<const uint4*>(p.k_cache)[s], v = static_cast<const uint4*>(p.v_cache)[s];
-    static_cast<uint4*>(p.k_cache)[d] = k;
-    static_cast<uint4*>(p.v_cache)[d] = v;
+    if (from >= 0 && !move_chunk(p, b, h, from, i, c, vecs)) atomicOr(p.err, kErrBadBlock);
 }
 
-// scores += sum over the group's heads of 2^(logit - M) / l, (M, l) the
-// statistics of the head's partitions joined.  One thread a token.
-__global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const AddWeightsParams p) {
+// What is left once every partition is there, for 256 tokens of a (sequence, kv
+// head) a block: scores += sum over the group's heads of 2^(logit - M) / l, one
+// thread a token, (M, l) the statistics of the head's partitions joined; and a
+// share of the output's elements, where there are partitions to join (as the
+// merge kernel would: sum_i w_i o_i / l with w_i = l_i 2^(m_i - M)).
+template <int ACT, int D>
+__global__ void __launch_bounds__(kAddThreads) scored_finish_kernel(const AddWeightsParams p) {
     __shared__ float s_max[8], s_inv[8];
     const int seq = blockIdx.z, kvh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = p.context_lens[seq];
@@ -193,14 +219,22 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const AddWeigh
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kAddThreads;
     if (first >= L) return;
     const int parts = (L + p.partition_size - 1) / p.partition_size;
+    const int64_t row = static_cast<int64_t>(seq) * p.num_kv_heads + kvh, t = first + threadIdx.x;
+    const float before = t < L ? p.scores[row * p.score_tokens + t] : 0.f;  // not written by the kernel before
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    const float* x = p.logits + (row * p.logit_tokens + t) * p.group;
+    float logit[8];
+#pragma unroll
+    for (int g = 0; g < 8; ++g) logit[g] = t < L && g < p.group ? x[g] : -INFINITY;
+    const float2* stats = reinterpret_cast<const float2*>(p.ws_ml) + row * p.group * p.max_parts;
     if (warp < p.group) {
-        const float2* ml = reinterpret_cast<const float2*>(p.ws_ml) +
-                           ((static_cast<int64_t>(seq) * p.num_kv_heads + kvh) * p.group + warp) * p.max_parts;
-        float M = -INFINITY, l = 0.f;
-        for (int i = lane; i < parts; i += 32) M = fmaxf(M, ml[i].x);
+        const float2* ml = stats + warp * p.max_parts;
+        const float2 mine = lane < parts ? ml[lane] : make_float2(-INFINITY, 0.f);
+        float M = mine.x;
+        for (int i = 32 + lane; i < parts; i += 32) M = fmaxf(M, ml[i].x);
         M = warp_max(M);
-        for (int i = lane; i < parts; i += 32) l += ml[i].y * fast_exp2(ml[i].x - M);
+        float l = lane < parts ? mine.y * fast_exp2(mine.x - M) : 0.f;
+        for (int i = 32 + lane; i < parts; i += 32) l += ml[i].y * fast_exp2(ml[i].x - M);
 #pragma unroll
         for (int off = 16; off >= 1; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
         if (lane == 0) {
@@ -209,13 +243,25 @@ __global__ void __launch_bounds__(kAddThreads) add_weights_kernel(const AddWeigh
         }
     }
     __syncthreads();
-    const int64_t t = first + threadIdx.x;
-    if (t >= L) return;
-    const int64_t row = static_cast<int64_t>(seq) * p.num_kv_heads + kvh;
-    const float* x = p.logits + (row * p.logit_tokens + t) * p.group;
-    float sum = 0.f;
-    for (int g = 0; g < p.group; ++g) sum += fast_exp2(x[g] - s_max[g]) * s_inv[g];
-    p.scores[row * p.score_tokens + t] += sum;
+    if (t < L) {
+        float sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < 8; ++g)
+            if (g < p.group) sum += fast_exp2(logit[g] - s_max[g]) * s_inv[g];
+        p.scores[row * p.score_tokens + t] = before + sum;
+    }
+    if (parts == 1) return;
+    const int blocks = (L + kAddThreads - 1) / kAddThreads, each = (p.group * D + blocks - 1) / blocks;
+    const int end = min(p.group * D, static_cast<int>(blockIdx.x + 1) * each);
+    for (int e = blockIdx.x * each + threadIdx.x; e < end; e += kAddThreads) {
+        const int g = e / D, d = e % D;
+        const float2* ml = stats + g * p.max_parts;
+        const float* o = p.ws_o + (row * p.group + g) * p.max_parts * D + d;
+        float acc = 0.f;
+#pragma unroll 4
+        for (int i = 0; i < parts; ++i) acc = fmaf(ml[i].y * fast_exp2(ml[i].x - s_max[g]), o[static_cast<int64_t>(i) * D], acc);
+        static_cast<uint16_t*>(p.out)[(row * p.group + g) * D + d] = float_to_act<ACT>(acc * s_inv[g]);
+    }
 }
 
 template <class Params>
@@ -241,13 +287,20 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     if (dev < 0 || dev >= kMaxDevices) return cudaErrorInvalidDevice;
     if (!configured[dev]) {
-        e = cudaFuncSetAttribute(evict_select_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyTokens * 4);
+        e = cudaFuncSetAttribute(evict_select_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyTokens * 4);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(evict_select_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize, kKeyTokens * 4);
         if (e != cudaSuccess) return e;
         configured[dev] = true;
     }
     const int64_t most = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
     const int smem = static_cast<int>((most < kKeyTokens ? most : kKeyTokens) * 4);
-    evict_select_kernel<<<dim3(p.num_kv_heads, p.num_seqs), kSelectThreads, smem, stream>>>(p);
+    const dim3 heads(p.num_kv_heads, p.num_seqs);
+    if (static_cast<int64_t>(p.budget) * p.row_bytes <= kMoveHere) {
+        evict_select_kernel<true><<<heads, kSelectThreads, smem, stream>>>(p);
+        return cudaGetLastError();
+    }
+    evict_select_kernel<false><<<heads, kSelectThreads, smem, stream>>>(p);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int rows = kMoveThreads / (p.row_bytes / 16);
@@ -255,9 +308,11 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     return launch_after(evict_move_kernel, p, grid, kMoveThreads, stream);
 }
 
-cudaError_t launch_add_weights(const AddWeightsParams& p, cudaStream_t stream) {
+cudaError_t launch_scored_finish(const AddWeightsParams& p, int act, int head_dim, cudaStream_t stream) {
     const dim3 grid((p.max_context + kAddThreads - 1) / kAddThreads, p.num_kv_heads, p.num_seqs);
-    return launch_after(add_weights_kernel, p, grid, kAddThreads, stream);
+    auto kernel = head_dim == 64 ? (act == kBF16 ? scored_finish_kernel<kBF16, 64> : scored_finish_kernel<kF16, 64>)
+                                 : (act == kBF16 ? scored_finish_kernel<kBF16, 128> : scored_finish_kernel<kF16, 128>);
+    return launch_after(kernel, p, grid, kAddThreads, stream);
 }
 
 }  // namespace pkv

@@ -199,6 +199,8 @@ struct AddWeightsParams {
     const float* ws_ml;   // [num_seqs][num_kv_heads * group][max_parts][2]
     const int32_t* context_lens;
     float* scores;        // [num_seqs][num_kv_heads][score_tokens]
+    const float* ws_o;    // [num_seqs][num_kv_heads * group][max_parts][head_dim], where there are several
+    void* out;
     int64_t score_tokens;
     int64_t logit_tokens;
     int num_seqs;
@@ -360,8 +362,8 @@ cudaError_t launch_decode_tc_ext(const DecodeParams& p, int act, int cache, int 
 cudaError_t launch_decode_tc_ext_e4m3(const DecodeParams& p, int act, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_tc_ext_e4m3b(const DecodeParams& p, int act, int head_dim, int BS, int G, cudaStream_t s);
 
-// Adds each token's weights, from kept logits and the partitions' statistics, to its scores.
-cudaError_t launch_add_weights(const AddWeightsParams& p, cudaStream_t stream);
+// Adds each token's weights, from kept logits and the partitions' statistics, to its scores, and joins the partitions.
+cudaError_t launch_scored_finish(const AddWeightsParams& p, int act, int head_dim, cudaStream_t stream);
 cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream);
 cudaError_t launch_chunk(const ChunkParams& p, int act, int cache, int head_dim, cudaStream_t stream);
 // Shares that an item's token tiles are split into (a function of the sizes).
