@@ -11,6 +11,10 @@
 // rows share every K and V tile.  Tokens come in tiles of 128, those that some
 // row of the item sees; with few items a second grid axis splits their list, and
 // a merge kernel joins the partial results.  One item a block, a block an SM.
+// An item of one row tile (up to TQ tokens: single tokens, drafts) is folded: both
+// halves of the machinery below, row tile 0's and 1's, take its rows, one the even
+// and one the odd token tiles, each with a maximum, sum and O of its own, which the
+// first joins at the end; one's products run under the other's softmax all the same.
 // Roles:
 //  warps 0-15      softmax: a row of a tile is two threads', 64 tokens each (row
 //                  tile (w >> 2) & 1, half w >> 3, rows 32 (w & 3) .. of warp w):
@@ -48,6 +52,8 @@
 // drains its copies and products, frees tensor memory and reports kErrTimeout.
 #pragma once
 
+#include <type_traits>
+
 #include "kernels.h"
 #include "pkv_tc.cuh"
 
@@ -70,10 +76,12 @@ struct ChunkSmem {
     static constexpr int CSTG = kChunkTile * D;  // its codes
     static constexpr int NC = E8 ? (D == 128 ? 4 : 6) : 0;
     static_assert(NC % 2 == 0, "the codes too");
-    // Scales of a tile: [8] K scales, [8] V scales, [8] log2 |V scale|.  Entry i % SLOTS is written again for
-    // tile i + SLOTS, once the codes of K tile use 2 (i + SLOTS) - NC were converted, for which the stage of use
-    // 2 (i + SLOTS) - NC - NS >= 2 i + 1 was free: V tile i's, so that softmax(i) was over.
-    static constexpr int SLOTS = CACHE == kE4M3B ? (NC + NS + 2) / 2 : 0;
+    // Scales of a tile: [8] K scales, [8] V scales, [8] log2 |V scale|.  Entry i % SLOTS is written again for tile
+    // i + SLOTS, once the codes of K tile i' = i + SLOTS - NC / 2 were converted, as use 2 i' at least 2 i' - 1 of the
+    // ring, for which the stage of NS uses before was free; no earlier than V tile i's (use 2 i + 2 at most), so that
+    // softmax(i) was over.
+    static constexpr int SLOTS = CACHE == kE4M3B ? (NC + NS + 4) / 2 : 0;
+    static_assert(CACHE != kE4M3B || 2 * SLOTS >= NC + NS + 3, "scales of a tile in use");
     static constexpr int QT = kChunkTile * D * 2;
     static constexpr int RING = 0;
     static constexpr int Q = NS * STG;
@@ -126,6 +134,15 @@ __device__ __forceinline__ int chunk_find(const int32_t* starts, int num_seqs, i
         hi = min(hi, lo + step);
     }
     return lo;
+}
+
+// Codes are converted in the order in which the products take the tiles: K(0), V(0), K(1), V(1), ..., folded K(0), K(1),
+// V(0), K(2), V(1), ..., K(n - 1), V(n - 2), V(n - 1).  The place of a tile in it, and the tile of a place.
+__device__ __forceinline__ int chunk_use_k(int i, bool fold) { return fold && i > 0 ? 2 * i - 1 : 2 * i; }
+__device__ __forceinline__ int chunk_use_v(int i, int n, bool fold) { return fold && i < n - 1 ? 2 * i + 2 : 2 * i + 1; }
+__device__ __forceinline__ void chunk_tile_of(int use, int n, bool fold, int& i, bool& is_v) {
+    is_v = fold ? use == 2 * n - 1 || (use > 0 && use % 2 == 0) : use % 2 == 1;
+    i = !fold || use == 0 || use == 2 * n - 1 ? use / 2 : is_v ? use / 2 - 1 : (use + 1) / 2;
 }
 
 __device__ __forceinline__ int chunk_tile_start(const ChunkItem& it, int i) {
@@ -285,19 +302,22 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     it.win_tile0 = it.first_lo / kChunkTile;
     it.sink_tiles = min(it.win_tile0, p.sinks / kChunkTile + (p.sinks % kChunkTile != 0));
     const int tiles = last / kChunkTile - it.win_tile0 + 1 + it.sink_tiles;
-    it.i0 = static_cast<int>(static_cast<int64_t>(tiles) * blockIdx.y / gridDim.y);
-    it.i1 = static_cast<int>(static_cast<int64_t>(tiles) * (blockIdx.y + 1) / gridDim.y);
+    // (at most 2^24 tiles, 32 shares)
+    it.i0 = static_cast<unsigned>(tiles) * blockIdx.y / gridDim.y;
+    it.i1 = static_cast<unsigned>(tiles) * (blockIdx.y + 1) / gridDim.y;
     const int n_list = any ? it.i1 - it.i0 : 0;
-    // row tile t's share of the list: up to the tile of its last row (none without rows)
-    auto rows_of = [&](int t) { return max(0, min(TQ, it.n - t * TQ)); };
+    const bool fold = it.n <= TQ;
+    // row tile t's first token (folded: both have the same), and its share of the list: up to the tile of its last row
+    auto first_of = [&](int t) { return fold ? 0 : t * TQ; };
+    auto rows_of = [&](int t) { return min(TQ, it.n - first_of(t)); };
     auto count_of = [&](int t) {
+        if (fold) return (n_list + 1 - t) / 2;
         const int rows = rows_of(t);
-        if (rows == 0) return 0;
         const int end = (it.pos0 + t * TQ + rows - 1) / kChunkTile - it.win_tile0 + 1 + it.sink_tiles;
         return max(0, min(n_list, end - it.i0));
     };
     const int cnt0 = count_of(0), cnt1 = count_of(1);
-    const int n_run = max(cnt0, cnt1);
+    const int n_run = fold ? n_list : max(cnt0, cnt1);
     const uint64_t policy = l2_policy_evict_normal();  // other row tiles read them too
 
     if (warp < 16) {
@@ -308,8 +328,8 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         const int tok = row / G, g = row - tok * G;  // (rows past TQ * G and past the last token: none)
         const bool mine = tok < rows_of(t);
         const bool live = __any_sync(0xffffffffu, mine);
-        const int pos = mine ? it.pos0 + t * TQ + tok : -1;
-        const int pos_lo = it.pos0 + t * TQ, pos_hi = pos_lo + rows_of(t) - 1;  // of the row tile
+        const int pos = mine ? it.pos0 + first_of(t) + tok : -1;
+        const int pos_lo = it.pos0 + first_of(t), pos_hi = pos_lo + rows_of(t) - 1;  // of the row tile
         const uint32_t lanes = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
         const uint32_t s_addr = lanes + t * kChunkTile + half * 64;  // this thread's scores, then its weights, packed
         const uint32_t o_addr = lanes + O_COL + t * D + half * (D / 2);
@@ -325,10 +345,11 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             ok = __all_sync(0xffffffffu, chunk_wait(&s_full[t], i & 1, abort_flag, p.err));
             if (live) {
                 tc::fence_after_sync();
-                const int start = chunk_tile_start(it, it.i0 + i) + half * 64;  // this half's first token
+                const int tile = fold ? 2 * i + t : i;
+                const int start = chunk_tile_start(it, it.i0 + tile) + half * 64;  // this half's first token
                 const bool masked = start + 63 > pos_lo || (p.window != 0 && start <= pos_hi - p.window && start + 64 > p.sinks);
                 [[maybe_unused]] const float* scales =
-                    reinterpret_cast<const float*>(sm + S::SCALES) + (SCALED ? (i % max(1, S::SLOTS)) * 24 : 0);
+                    reinterpret_cast<const float*>(sm + S::SCALES) + (SCALED ? (tile % max(1, S::SLOTS)) * 24 : 0);
                 [[maybe_unused]] const int block0 = half * 64 / p.block_size, bshift = p.block_size == 32 ? 1 : 0;
                 // scores x[0 .. N) from column k on, as loaded, to what `c` makes log2 units
                 auto prepare = [&](int k, int n, float* x) {
@@ -466,7 +487,23 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (cnt - 1) & 1, abort_flag, p.err));
             tc::fence_after_sync();
         }
-        if (live && any && !pair_any(pair, !ok)) {
+        // folded, slot 1: slot 0's last product too, after which nothing reads the ring (at most one of its products is
+        // still open then, so that the parity names it)
+        if (ok && fold && t == 1 && cnt0 > 0) ok = __all_sync(0xffffffffu, chunk_wait(&o_done[0], (cnt0 - 1) & 1, abort_flag, p.err));
+        // folded: both slots' threads of a quarter of the rows (128) go on or stop together
+        auto quarter_any = [&](bool say) {
+            int r;
+            asm volatile(
+                "{\n\t.reg .pred p, q;\n\t"
+                "setp.ne.b32 p, %1, 0;\n\t"
+                "bar.red.or.pred q, %2, 128, p;\n\t"
+                "selp.b32 %0, 1, 0, q;\n\t}"
+                : "=r"(r)
+                : "r"(say ? 1 : 0), "r"(9 + (warp & 3))
+                : "memory");
+            return r != 0;
+        };
+        if (live && any && !(fold ? quarter_any(!ok) : pair_any(pair, !ok))) {
             // the row's sum from both threads
             if (half == 1) *swap = l;
             pair_any(pair, false);
@@ -477,8 +514,54 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             float vmul = 1.f;
             if constexpr (CACHE == kE4M3) vmul = *p.v_scale;
             if constexpr (SCALED) vmul = unit == -INFINITY ? 0.f : fast_exp2(unit - m);
-            const int64_t at = it.row0 + t * TQ + tok;
+            // Folded: slot 1 leaves its O, in units of 2^m, with m and l in the ring (every tile was consumed: the products
+            // of both slots are done), column by column, a row a lane; slot 0 adds it to its own.
+            float keep = 1.f, other = 0.f;
+            float* join = reinterpret_cast<float*>(ring);
+            float* from_1 = join + 2 * kChunkTile + half * (D / 2) * kChunkTile + row;
+            if (fold) {
+                if (t == 1) {
+                    if (half == 0) {
+                        join[row] = m;
+                        join[kChunkTile + row] = l;
+                    }
+                    if (cnt > 0) {
+#pragma unroll
+                        for (int k = 0; k < D / 2; k += 32) {
+                            float o[32];
+                            tc::TmemLd<32>::load(o_addr + k, o);
+                            tc::tmem_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) from_1[(k + j) * kChunkTile] = o[j] * (CACHE == kE4M3 ? 1.f : vmul);
+                        }
+                    }
+                }
+                quarter_any(false);
+                if (t == 0 && cnt1 > 0) {
+                    const float m1 = join[row], l1 = join[kChunkTile + row], top = fmaxf(m, m1);
+                    keep = m == -INFINITY && l == 0.f ? 0.f : fast_exp2(m - top);
+                    other = m1 == -INFINITY && l1 == 0.f ? 0.f : fast_exp2(m1 - top);
+                    l = l * keep + l1 * other;
+                    m = top;
+                }
+            }
+            // 32 channels of the row from k on, in units of 2^m (per-tensor E4M3: without the scale)
+            auto load_o = [&](int k, float* o) {
+                tc::TmemLd<32>::load(o_addr + k, o);
+                tc::tmem_wait_ld();
+                if (fold && cnt1 > 0) {
+                    const float f = keep * (CACHE == kE4M3 ? 1.f : vmul);
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = o[j] * f + (other == 0.f ? 0.f : from_1[(k + j) * kChunkTile] * other);
+                } else if constexpr (SCALED) {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] *= vmul;
+                }
+            };
+            const int64_t at = it.row0 + first_of(t) + tok;
             const int h = it.kvh * G + g;
+            const float vt = CACHE == kE4M3 ? vmul : 1.f;
+            if (!fold || t == 0) {
             // Rows go out through the row tile's queries' memory, which its last scores have read: 32 rows of 128 bytes
             // a warp and turn, chunks of 16 bytes swizzled by the row; then 8 lanes write 128 bytes of one row (a lane
             // with a row of its own would take 32 lines an instruction).
@@ -498,7 +581,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                     const int r = y * (32 / CHUNKS) + lane / CHUNKS, x = lane % CHUNKS;
                     const int rr = (warp & 3) * 32 + r, rt = (rr * inv_g) >> 16;
                     if (rt < rows_of(t))
-                        *reinterpret_cast<uint4*>(row_dst(it.row0 + t * TQ + rt, it.kvh * G + rr - rt * G) + x * 16) =
+                        *reinterpret_cast<uint4*>(row_dst(it.row0 + first_of(t) + rt, it.kvh * G + rr - rt * G) + x * 16) =
                             *reinterpret_cast<const uint4*>(stage + r * TURN + ((x ^ (r & (CHUNKS - 1))) * 16));
                 }
                 __syncwarp();
@@ -508,119 +591,180 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 if (mine && half == 0) reinterpret_cast<float2*>(p.ws_ml)[(share + at) * p.num_q_heads + h] = make_float2(m, l);
                 if (cnt > 0) {
 #pragma unroll
-                    for (int k = 0; k < D / 2; k += TURN / 4) {
-                        float o[TURN / 4];
-                        tc::TmemLd<TURN / 4>::load(o_addr + k, o);
-                        tc::tmem_wait_ld();
+                    for (int k = 0; k < D / 2; k += 32) {
+                        float o[32];
+                        load_o(k, o);
 #pragma unroll
-                        for (int x = 0; x < CHUNKS; ++x)
-                            put(x, make_uint4(__float_as_uint(o[4 * x] * vmul), __float_as_uint(o[4 * x + 1] * vmul),
-                                              __float_as_uint(o[4 * x + 2] * vmul), __float_as_uint(o[4 * x + 3] * vmul)));
-                        flush([&](int64_t r, int head) {
-                            return reinterpret_cast<unsigned char*>(
-                                p.ws_o + ((share + r) * p.num_q_heads + head) * D + half * (D / 2) + k);
-                        });
+                        for (int y = 0; y < 32; y += TURN / 4) {
+#pragma unroll
+                            for (int x = 0; x < CHUNKS; ++x)
+                                put(x, make_uint4(__float_as_uint(o[y + 4 * x] * vt), __float_as_uint(o[y + 4 * x + 1] * vt),
+                                                  __float_as_uint(o[y + 4 * x + 2] * vt), __float_as_uint(o[y + 4 * x + 3] * vt)));
+                            flush([&](int64_t r, int head) {
+                                return reinterpret_cast<unsigned char*>(
+                                    p.ws_o + ((share + r) * p.num_q_heads + head) * D + half * (D / 2) + k + y);
+                            });
+                        }
                     }
                 }
             } else {
-                const float inv = vmul / l;
+                const float inv = vt / l;
 #pragma unroll
-                for (int k = 0; k < D / 2; k += TURN / 2) {
-                    float o[TURN / 2];
+                for (int k = 0; k < D / 2; k += 32) {
+                    float o[32];
+                    load_o(k, o);
 #pragma unroll
-                    for (int y = 0; y < TURN / 2; y += 32) tc::TmemLd<32>::load(o_addr + k + y, o + y);
-                    tc::tmem_wait_ld();
-#pragma unroll
-                    for (int x = 0; x < CHUNKS; ++x)
-                        put(x, make_uint4(pack_act<ACT>(o[8 * x] * inv, o[8 * x + 1] * inv),
-                                          pack_act<ACT>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
-                                          pack_act<ACT>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
-                                          pack_act<ACT>(o[8 * x + 6] * inv, o[8 * x + 7] * inv)));
-                    flush([&](int64_t r, int head) {
-                        return reinterpret_cast<unsigned char*>(static_cast<uint16_t*>(p.out) + r * p.out_stride +
-                                                                static_cast<int64_t>(head) * D + half * (D / 2) + k);
-                    });
+                    for (int x = 0; x < 4; ++x)
+                        put((k / 8 + x) % CHUNKS, make_uint4(pack_act<ACT>(o[8 * x] * inv, o[8 * x + 1] * inv),
+                                                             pack_act<ACT>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                                             pack_act<ACT>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                                                             pack_act<ACT>(o[8 * x + 6] * inv, o[8 * x + 7] * inv)));
+                    if ((k + 32) % (TURN / 2) == 0)
+                        flush([&](int64_t r, int head) {
+                            return reinterpret_cast<unsigned char*>(static_cast<uint16_t*>(p.out) + r * p.out_stride +
+                                                                    static_cast<int64_t>(head) * D + half * (D / 2) + (k + 32 - TURN / 2));
+                        });
                 }
+            }
             }
         }
     } else if (warp == 16) {
         // ---------------------------------------------------------------- MMA
-        const uint32_t k_base = smem_addr(ring), q_base = smem_addr(qbuf);
-        const uint32_t v_part = p.block_size * 128;
-        const int vsh = p.block_size == 32 ? 1 : 0;
-        auto v_step = [&](int kk) { return (kk >> vsh) * v_part * HALVES + (kk & vsh) * 2048; };  // of 16 tokens
+        // Descriptors as words, stepped by additions; one elected lane issues.
+        constexpr uint32_t HI = tc::desc_hi_sw128(1024);
+        const uint32_t q_lo = tc::desc_start(smem_addr(qbuf)) + tc::desc_lo(16);
+        const uint32_t k_lo = tc::desc_start(smem_addr(ring)) + tc::desc_lo(16);
+        // V: 16-bit, a block's tokens together, its 64-channel parts v_part apart (the converted tile: as K)
+        const uint32_t v_part = E8 ? HALF : p.block_size * 128;
+        const uint32_t v_lo = tc::desc_start(smem_addr(ring)) + tc::desc_lo(v_part);
+        const uint32_t v_two = E8 || p.block_size == 16 ? 2 * (E8 ? 2048 : 2048 * HALVES) : v_part * HALVES;  // 32 tokens
+        const uint32_t v_one = E8 || p.block_size == 32 ? 2048 : 2048 * HALVES;                              // 16 tokens
         auto mma_s = [&](int t, int stage) {
-            const uint32_t a = q_base + t * S::QT, b = k_base + stage * STG;
+            const uint32_t a = q_lo + (fold ? 0 : t * (S::QT / 16)), b = k_lo + stage * (STG / 16), to = tmem + t * kChunkTile;
 #pragma unroll
             for (int kk = 0; kk < D / 16; ++kk) {
-                const uint32_t off = (kk >> 2) * HALF + (kk & 3) * 32;
-                tc::mma_f16(tmem + t * kChunkTile, tc::desc_sw128(a + off, 16, 1024), tc::desc_sw128(b + off, 16, 1024),
-                            IDESC_S, kk > 0);
+                const uint32_t off = ((kk >> 2) * HALF + (kk & 3) * 32) / 16;
+                tc::mma_f16_words<HI, HI>(to, a + off, b + off, IDESC_S, kk > 0);
             }
         };
         auto mma_o = [&](int t, int stage, int half, bool add) {  // over 64 tokens
-            // 16-bit: a block's tokens together, its 64-channel parts v_part apart (the converted tile: as K)
-            const uint32_t b = k_base + stage * STG;
+            const uint32_t b = v_lo + stage * (STG / 16) + half * (v_two / 8);
+            const uint32_t a = tmem + t * kChunkTile + half * 64, to = tmem + O_COL + t * D;
 #pragma unroll
-            for (int kk = half * 4; kk < half * 4 + 4; ++kk)
-                tc::mma_f16_ts(tmem + O_COL + t * D, tmem + t * kChunkTile + half * 64 + (kk & 3) * 8, tc::desc_sw128(b + (E8 ? kk * 2048 : v_step(kk)), E8 ? HALF : v_part, 1024),
-                               IDESC_O, add || half > 0 || kk > 0);
+            for (int kk = 0; kk < 4; ++kk)
+                tc::mma_f16_ts_words<HI>(to, a + kk * 8, b + (kk >> 1) * (v_two / 16) + (kk & 1) * (v_one / 16), IDESC_O, add || kk > 0);
         };
         bool ok = n_run > 0 && __all_sync(0xffffffffu, chunk_wait(q_full, 0, abort_flag, p.err));
-        // tile i: K is stage use 2 i, V 2 i + 1
-        if (ok) ok = __all_sync(0xffffffffu, chunk_wait(&full[0], 0, abort_flag, p.err));
-        if (ok) {
+        // K and V of tile i: their stages, and whether they are there
+        auto k_use = [&](int i) { return E8 ? chunk_use_k(i, fold) : 2 * i; };
+        auto v_use = [&](int i) { return E8 ? chunk_use_v(i, n_run, fold) : 2 * i + 1; };
+        auto k_there = [&](int i) {
+            const int use = k_use(i);
+            return __all_sync(0xffffffffu, chunk_wait(&full[use % NS], (use / NS) & 1, abort_flag, p.err));
+        };
+        auto v_there = [&](int i) {
+            const int use = v_use(i);
+            return __all_sync(0xffffffffu, E8 ? chunk_wait(&full[use % NS], (use / NS) & 1, abort_flag, p.err)
+                                              : chunk_wait(&v_ok[i % NS], (i / NS) & 1, abort_flag, p.err));
+        };
+        // O_t += P_t V, the k-th of slot t, half by half as its weights come
+        auto product_o = [&](int t, int k, int stage) {
+            if (!__all_sync(0xffffffffu, chunk_wait(&p_full[2 * t], k & 1, abort_flag, p.err))) return false;
+            tc::fence_after_sync();
+            if (tc::elect_one()) mma_o(t, stage, 0, k > 0);
+            __syncwarp();
+            if (!__all_sync(0xffffffffu, chunk_wait(&p_full[2 * t + 1], k & 1, abort_flag, p.err))) return false;
             tc::fence_after_sync();
             if (tc::elect_one()) {
-                if (cnt0 > 0) {
-                    mma_s(0, 0);
-                    tc::commit(&s_full[0]);
-                }
-                if (cnt1 > 0) {
-                    mma_s(1, 0);
-                    tc::commit(&s_full[1]);
-                }
-                tc::commit(&empty[0]);
+                mma_o(t, stage, 1, true);
+                tc::commit(&o_done[t]);
             }
             __syncwarp();
-        }
-        for (int i = 0; i < n_run && ok; ++i) {
-            const int uv = 2 * i + 1, uk = 2 * i + 2;
-            const int sv = uv % NS, sk = uk % NS;
-            const bool more = i + 1 < n_run;
-            ok = __all_sync(0xffffffffu, E8 ? chunk_wait(&full[sv], (uv / NS) & 1, abort_flag, p.err)
-                                            : chunk_wait(&v_ok[i % NS], (i / NS) & 1, abort_flag, p.err));
-            if (!ok) break;
-            if (more) ok = __all_sync(0xffffffffu, chunk_wait(&full[sk], (uk / NS) & 1, abort_flag, p.err));
-            if (!ok) break;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                const int cnt = t == 0 ? cnt0 : cnt1;
-                if (i >= cnt) continue;
-                ok = __all_sync(0xffffffffu, chunk_wait(&p_full[2 * t], i & 1, abort_flag, p.err));
+            return true;
+        };
+        auto product_s = [&](int t, int stage) {
+            if (tc::elect_one()) {
+                mma_s(t, stage);
+                tc::commit(&s_full[t]);
+            }
+            __syncwarp();
+        };
+        auto release = [&](int stage) {
+            if (tc::elect_one()) tc::commit(&empty[stage]);
+            __syncwarp();
+        };
+        if (fold) {
+            for (int i = 0; i < 2 && i < n_run && ok; ++i) {
+                ok = k_there(i);
                 if (!ok) break;
                 tc::fence_after_sync();
-                if (tc::elect_one()) mma_o(t, sv, 0, i > 0);
-                __syncwarp();
-                ok = __all_sync(0xffffffffu, chunk_wait(&p_full[2 * t + 1], i & 1, abort_flag, p.err));
+                product_s(i, k_use(i) % NS);
+                release(k_use(i) % NS);
+            }
+            for (int i = 0; i < n_run && ok; ++i) {
+                const int t = i & 1;
+                ok = v_there(i) && product_o(t, i >> 1, v_use(i) % NS);
                 if (!ok) break;
+                release(v_use(i) % NS);
+                if (i + 2 < n_run) {
+                    ok = k_there(i + 2);
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    product_s(t, k_use(i + 2) % NS);
+                    release(k_use(i + 2) % NS);
+                }
+            }
+        } else {
+            if (ok) ok = k_there(0);
+            if (ok) {
                 tc::fence_after_sync();
                 if (tc::elect_one()) {
-                    mma_o(t, sv, 1, true);
-                    tc::commit(&o_done[t]);
-                    if (i + 1 < cnt) {
-                        mma_s(t, sk);
-                        tc::commit(&s_full[t]);
+                    if (cnt0 > 0) {
+                        mma_s(0, 0);
+                        tc::commit(&s_full[0]);
                     }
+                    if (cnt1 > 0) {
+                        mma_s(1, 0);
+                        tc::commit(&s_full[1]);
+                    }
+                    tc::commit(&empty[0]);
                 }
                 __syncwarp();
             }
-            if (!ok) break;
-            if (tc::elect_one()) {
-                tc::commit(&empty[sv]);
-                if (more) tc::commit(&empty[sk]);
+            for (int i = 0; i < n_run && ok; ++i) {
+                const int sv = (2 * i + 1) % NS, sk = (2 * i + 2) % NS;
+                const bool more = i + 1 < n_run;
+                ok = v_there(i) && (!more || k_there(i + 1));
+                if (!ok) break;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int cnt = t == 0 ? cnt0 : cnt1;
+                    if (i >= cnt) continue;
+                    ok = __all_sync(0xffffffffu, chunk_wait(&p_full[2 * t], i & 1, abort_flag, p.err));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) mma_o(t, sv, 0, i > 0);
+                    __syncwarp();
+                    ok = __all_sync(0xffffffffu, chunk_wait(&p_full[2 * t + 1], i & 1, abort_flag, p.err));
+                    if (!ok) break;
+                    tc::fence_after_sync();
+                    if (tc::elect_one()) {
+                        mma_o(t, sv, 1, true);
+                        tc::commit(&o_done[t]);
+                        if (i + 1 < cnt) {
+                            mma_s(t, sk);
+                            tc::commit(&s_full[t]);
+                        }
+                    }
+                    __syncwarp();
+                }
+                if (!ok) break;
+                if (tc::elect_one()) {
+                    tc::commit(&empty[sv]);
+                    if (more) tc::commit(&empty[sk]);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
         // every product issued has completed before tensor memory is freed
         if (tc::elect_one()) {
@@ -633,10 +777,11 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         const bool second = warp == 18;  // V; else K and Q
         if (!second && lane == 0 && n_run > 0) {
             const uint32_t bytes = HALVES * G * TQ * 128;
-            mbar_arrive_expect_tx(q_full, ((cnt0 > 0) + (cnt1 > 0)) * bytes);
+            const bool both = !fold && cnt1 > 0;  // (tiles of a share that are all behind row tile 0 leave its queries unused)
+            mbar_arrive_expect_tx(q_full, (both ? 2 : 1) * bytes);
 #pragma unroll
             for (int t = 0; t < 2; ++t)
-                if ((t == 0 ? cnt0 : cnt1) > 0)
+                if (t == 0 || both)
                     for (int h = 0; h < HALVES; ++h)
                         tc::tma_load_3d(qbuf + t * S::QT + h * HALF, &qmap, h * 64, it.kvh * G, it.row0 + t * TQ, q_full, policy);
         }
@@ -718,48 +863,63 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         // which the swizzle moves by one 16-byte chunk from token to token, meet in a bank.
         if constexpr (E8) {
             for (int u = 0; u < 2 * n_run; ++u) {
-                const int cs = u % S::NC, s = u % NS;
-                bool good = chunk_wait(&c_full[cs], (u / S::NC) & 1, abort_flag, p.err);
+                int tile;
+                bool is_v;
+                chunk_tile_of(u, n_run, fold, tile, is_v);
+                const int code = 2 * tile + is_v, cs = code % S::NC, s = u % NS;
+                bool good = chunk_wait(&c_full[cs], (code / S::NC) & 1, abort_flag, p.err);
                 if (good && u >= NS) good = chunk_wait(&empty[s], (u / NS - 1) & 1, abort_flag, p.err);
                 if (!__all_sync(0xffffffffu, good)) break;
                 const unsigned char* codes = sm + S::CODES + cs * S::CSTG;
                 unsigned char* dst = ring + s * STG;
-                const int start = chunk_tile_start(it, it.i0 + (u >> 1));
+                const int start = chunk_tile_start(it, it.i0 + tile);
                 const int last_lo = p.window ? max(0, last - p.window + 1) : 0;
-                const bool partly = (u & 1) && (start + kChunkTile - 1 > it.pos0 || (start < last_lo && start + kChunkTile > p.sinks));
+                const bool partly = is_v && (start + kChunkTile - 1 > it.pos0 || (start < last_lo && start + kChunkTile > p.sinks));
+                constexpr int TOKENS = 32 / (4 * HALVES);  // of a warp's step
+                const int second = (lane >> 2) & 1;
+                const int lane_r = HALVES == 2 ? (lane >> 4) * 2 + second : lane >> 2;
+                const int h = HALVES == 2 ? ((lane >> 3) & 1) ^ second : 0;
+                const int x = (lane & 3) * 2;  // first of two 8-channel chunks of the part
+                const unsigned char* src = codes + lane_r * D + h * 64 + x * 8;
                 bool bad = false;
-                constexpr int TOKENS = 32 / (4 * HALVES);  // a warp's step
-#pragma unroll 4
-                for (int r0 = (warp - 20) * TOKENS; r0 < kChunkTile; r0 += 4 * TOKENS) {
-                    const int pair = lane & 15, second = (lane >> 2) & 1;
-                    const int r = r0 + (HALVES == 2 ? (lane >> 4) * 2 + second : lane >> 2);
-                    const int h = HALVES == 2 ? ((pair >> 3) ^ second) : 0;
-                    const int x = (lane & 3) * 2;  // first of two 8-channel chunks of the part
-                    uint4 c = *reinterpret_cast<const uint4*>(codes + r * D + h * 64 + x * 8);
-                    if (partly) {
-                        const int j = start + r;
-                        if (j > last || (j < it.first_lo && j >= p.sinks)) c = make_uint4(0u, 0u, 0u, 0u);
-                        const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
+                // four steps' codes are read before the first is written; a tile that no row sees in part needs no look
+                auto convert = [&](auto look) {
 #pragma unroll
-                        for (int q = 0; q < 4; ++q)  // a code of 0x7f or 0xff
-                            bad = bad || __vcmpeq4(cw[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-                    }
-                    const uint32_t cw[4] = {c.x, c.y, c.z, c.w};
-                    uint32_t w[8];
+                    for (int r0 = (warp - 20) * TOKENS; r0 < kChunkTile + (warp - 20) * TOKENS; r0 += 16 * TOKENS) {
+                        uint4 c[4];
 #pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(cw[q / 2] >> (16 * (q % 2))));
-                        if constexpr (ACT == kF16) {
-                            w[q] = f;
-                        } else {
-                            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-                            w[q] = pack_act<kBF16>(v.x, v.y);
+                        for (int y = 0; y < 4; ++y) c[y] = *reinterpret_cast<const uint4*>(src + (r0 + 4 * y * TOKENS) * D);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            const int r = r0 + 4 * y * TOKENS + lane_r;
+                            if constexpr (decltype(look)::value) {
+                                const int j = start + r;
+                                if (j > last || (j < it.first_lo && j >= p.sinks)) c[y] = make_uint4(0u, 0u, 0u, 0u);
+                                const uint32_t cw[4] = {c[y].x, c[y].y, c[y].z, c[y].w};
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)  // a code of 0x7f or 0xff
+                                    bad = bad || __vcmpeq4(cw[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+                            }
+                            const uint32_t cw[4] = {c[y].x, c[y].y, c[y].z, c[y].w};
+                            uint32_t w[8];
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(cw[q / 2] >> (16 * (q % 2))));
+                                if constexpr (ACT == kF16) {
+                                    w[q] = f;
+                                } else {
+                                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                                    w[q] = pack_act<kBF16>(v.x, v.y);
+                                }
+                            }
+                            unsigned char* row = dst + h * HALF + r * 128;
+                            *reinterpret_cast<uint4*>(row + ((x ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(row + (((x + 1) ^ (r & 7)) * 16)) = make_uint4(w[4], w[5], w[6], w[7]);
                         }
                     }
-                    unsigned char* row = dst + h * HALF + r * 128;
-                    *reinterpret_cast<uint4*>(row + ((x ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-                    *reinterpret_cast<uint4*>(row + (((x + 1) ^ (r & 7)) * 16)) = make_uint4(w[4], w[5], w[6], w[7]);
-                }
+                };
+                if (partly) convert(std::true_type{});
+                else convert(std::false_type{});
                 if (bad) *plain_flag = 1;
                 tc::fence_proxy_async_smem();
                 __syncwarp();

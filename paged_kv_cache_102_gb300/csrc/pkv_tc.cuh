@@ -121,6 +121,29 @@ __device__ __forceinline__ void mma_f8_words(uint32_t d_tmem, uint32_t a_lo, uin
         : "memory");
 }
 
+// mma_f16 and mma_f16_ts the same way.
+template <uint32_t A_HI, uint32_t B_HI>
+__device__ __forceinline__ void mma_f16_words(uint32_t d_tmem, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5};\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_lo), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(A_HI), "n"(B_HI)
+        : "memory");
+}
+template <uint32_t B_HI>
+__device__ __forceinline__ void mma_f16_ts_words(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b_lo), "r"(idesc), "r"(accumulate ? 1u : 0u), "n"(B_HI)
+        : "memory");
+}
+
 // Shared-memory matrix descriptor, no swizzle (the canonical interleaved
 // layout: 8 rows x 16 bytes form a contiguous 128-byte core matrix).  For a
 // K-major operand the leading byte offset is the distance between core
