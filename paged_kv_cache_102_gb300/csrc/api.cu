@@ -774,8 +774,10 @@ int paged_attention_chunk(const void* q, int64_t q_stride, const void* k_cache, 
     p.sinks = p.window ? static_cast<int>(std::min<int64_t>(sinks, context)) : 0;
     p.scale_log2 = scale * 1.4426950408889634f;
     // a window's tokens alone are shared out (never more shares than the workspace was sized for)
-    p.splits = chunk_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads,
-                            p.window ? std::min<int64_t>(context, static_cast<int64_t>(p.window) + p.sinks) : context);
+    p.splits = chunk_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads, context);
+    if (p.window)
+        p.splits = std::min(p.splits, chunk_splits(num_seqs, num_tokens, num_q_heads, num_kv_heads,
+                                                   std::min<int64_t>(context, static_cast<int64_t>(p.window) + p.sinks)));
     if (p.splits > 1) {
         char* ws = static_cast<char*>(workspace) + kWorkspaceHeader;
         const size_t rows = static_cast<size_t>(p.splits) * num_tokens * num_q_heads;

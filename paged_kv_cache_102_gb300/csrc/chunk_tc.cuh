@@ -39,7 +39,8 @@
 //                  others sends the item to the plain loop at the end, since a
 //                  weight of 0 would carry it to rows that do not see it.
 //  warps 20-23     E4M3 caches: conversion.  The producers copy the codes (one bulk
-//                  copy a block) into a ring of their own; these warps write them
+//                  copy a block) into a ring of their own; these warps, and of a
+//                  folded item the softmax warps that have none of its rows, write them
 //                  as 16-bit elements, exactly, into the ring that the products
 //                  read, and do warp 19's work on the way.  One scale per tensor
 //                  joins the logits' factor and the output's.  Block scales: the
@@ -61,6 +62,7 @@ namespace pkv {
 
 __host__ __device__ constexpr int chunk_threads(int cache) { return is_e4m3(cache) ? 768 : 640; }
 constexpr int kChunkTile = 128;       // tokens of a tile
+constexpr int kConverters = 16;       // most warps that convert codes
 constexpr int kChunkTmemCols = 512;   // two S (128 columns each, P over them), two O
 constexpr float kChunkRescale = 8.f;  // log2 by which a maximum may pass the reference
 
@@ -103,7 +105,8 @@ struct ChunkItem {
     int n;         // its new tokens: at most 2 TQ
     int pos0;      // position of the first
     int first_lo;  // the first row's window begins here
-    int sink_tiles, win_tile0, i0, i1;  // tiles of the list, and this block's share [i0, i1) of it
+    int sink_tiles, win_tile0, i0, i1;  // tiles of the list, and this block's share [i0, i1) of it (0, 0: nothing to do)
+    int any;       // whether it has rows
 };
 
 __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, int* err) {
@@ -118,6 +121,10 @@ __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, volat
         }
     }
     return true;
+}
+
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(n) : "memory");
 }
 
 // The sequence of row slot `slot`: the last b with starts[b] / rows + b <= slot
@@ -235,14 +242,33 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     uint32_t* tmem_base_smem = reinterpret_cast<uint32_t*>(sm + S::MISC);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 4);
     volatile int* plain_flag = reinterpret_cast<volatile int*>(sm + S::MISC + 8);
-    int* s_item = reinterpret_cast<int*>(sm + S::MISC + 16);  // sequence, its first row and the next one's, its length
+    ChunkItem* s_item = reinterpret_cast<ChunkItem*>(sm + S::MISC + 16);
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int G = p.num_q_heads / p.num_kv_heads, TQ = kChunkTile / G, R = 2 * TQ;
-    const int slot = (gridDim.x - 1 - blockIdx.x) / p.num_kv_heads;  // later rows, which see more, first
+    const int G = p.group, TQ = p.row_tokens, R = 2 * TQ;
     if (warp == 19) {
+        // the item: found and worked out once, for the others to read
+        const int slot = (gridDim.x - 1 - blockIdx.x) / p.num_kv_heads;  // later rows, which see more, first
         const int b = chunk_find(p.seq_starts, p.num_seqs, R, slot, lane);
-        if (lane < 4) s_item[lane] = lane == 0 ? b : lane == 3 ? p.context_lens[b] : p.seq_starts[b + lane - 1];
+        if (lane == 0) {
+            const int s0 = p.seq_starts[b], s1 = p.seq_starts[b + 1], L = p.context_lens[b];
+            const int first = (slot - (s0 / R + b)) * R;  // of the sequence's new tokens
+            ChunkItem x;
+            x.seq = b;
+            x.kvh = (gridDim.x - 1 - blockIdx.x) - slot * p.num_kv_heads;
+            x.any = s0 >= 0 && s1 <= p.num_tokens && first >= 0 && first < s1 - s0 && L >= s1 - s0 &&
+                    L <= p.max_blocks_per_seq * p.block_size;
+            x.row0 = s0 + first;
+            x.n = min(R, s1 - s0 - first);
+            x.pos0 = L - (s1 - s0) + first;
+            x.first_lo = p.window ? max(0, x.pos0 - p.window + 1) : 0;
+            x.win_tile0 = x.first_lo / kChunkTile;
+            x.sink_tiles = min(x.win_tile0, p.sinks / kChunkTile + (p.sinks % kChunkTile != 0));
+            const unsigned tiles = (x.pos0 + x.n - 1) / kChunkTile - x.win_tile0 + 1 + x.sink_tiles;
+            x.i0 = x.any ? tiles * blockIdx.y / gridDim.y : 0;  // (at most 2^24 tiles, 32 shares)
+            x.i1 = x.any ? tiles * (blockIdx.y + 1) / gridDim.y : 0;
+            *s_item = x;
+        }
         if (blockIdx.x == 0 && blockIdx.y == 0)  // every sequence's rows and length once
             for (int i = lane; i < p.num_seqs; i += 32) {
                 const int s0 = p.seq_starts[i], s1 = p.seq_starts[i + 1], L = p.context_lens[i];
@@ -254,13 +280,13 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         tc::tmem_relinquish();
     } else if (threadIdx.x == 17 * 32) {
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&full[i], E8 ? 4 : 1);
+            mbar_init(&full[i], E8 ? kConverters : 1);
             mbar_init(&empty[i], 1);
             mbar_init(&v_ok[i], 1);
         }
         for (int i = 0; i < S::NC; ++i) {
             mbar_init(&c_full[i], 1);
-            mbar_init(&c_empty[i], 4);
+            mbar_init(&c_empty[i], kConverters);
         }
         mbar_init(q_full, 1);
         for (int t = 0; t < 2; ++t) {
@@ -284,28 +310,10 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     tc::fence_after_sync();
     const uint32_t tmem = *tmem_base_smem;
 
-    ChunkItem it;
-    it.seq = s_item[0];
-    it.kvh = (gridDim.x - 1 - blockIdx.x) % p.num_kv_heads;
-    bool any;
-    {
-        const int s0 = s_item[1], s1 = s_item[2], L = s_item[3];
-        const int first = (slot - (s0 / R + it.seq)) * R;  // of the sequence's new tokens
-        any = s0 >= 0 && s1 <= p.num_tokens && first >= 0 && first < s1 - s0 && L >= s1 - s0 &&
-              L <= p.max_blocks_per_seq * p.block_size;
-        it.row0 = s0 + first;
-        it.n = min(R, s1 - s0 - first);
-        it.pos0 = L - (s1 - s0) + first;
-    }
+    const ChunkItem it = *s_item;
+    const bool any = it.any;
     const int last = it.pos0 + it.n - 1;  // position of the last row
-    it.first_lo = p.window ? max(0, it.pos0 - p.window + 1) : 0;
-    it.win_tile0 = it.first_lo / kChunkTile;
-    it.sink_tiles = min(it.win_tile0, p.sinks / kChunkTile + (p.sinks % kChunkTile != 0));
-    const int tiles = last / kChunkTile - it.win_tile0 + 1 + it.sink_tiles;
-    // (at most 2^24 tiles, 32 shares)
-    it.i0 = static_cast<unsigned>(tiles) * blockIdx.y / gridDim.y;
-    it.i1 = static_cast<unsigned>(tiles) * (blockIdx.y + 1) / gridDim.y;
-    const int n_list = any ? it.i1 - it.i0 : 0;
+    const int n_list = it.i1 - it.i0;
     const bool fold = it.n <= TQ;
     // row tile t's first token (folded: both have the same), and its share of the list: up to the tile of its last row
     auto first_of = [&](int t) { return fold ? 0 : t * TQ; };
@@ -320,12 +328,96 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     const int n_run = fold ? n_list : max(cnt0, cnt1);
     const uint64_t policy = l2_policy_evict_normal();  // other row tiles read them too
 
-    if (warp < 16) {
+    // Conversion: warps 20-23, and of a folded item the softmax warps whose 32 rows it has not.
+    const int quarters = min(4, (rows_of(0) * G + 31) / 32);
+    const bool converter = E8 && (warp >= 20 || (fold && warp < 16 && (warp & 3) >= quarters));
+    [[maybe_unused]] const int team = fold ? 4 + 4 * (4 - quarters) : 4;
+    [[maybe_unused]] const int index = warp >= 20 ? warp - 20 : 4 + ((warp & 3) - quarters) * 4 + (warp >> 2);
+
+    if (converter) {
+        // --------------------------------------------------------- conversion
+        // 16 codes a lane and step.  8 neighbouring lanes, which shared memory serves at once, take 64 channels of
+        // two tokens (head_dim 128: the other half of the second), so that neither their reads nor their writes,
+        // which the swizzle moves by one 16-byte chunk from token to token, meet in a bank.
+        if constexpr (E8) {
+            // the first one arrives for the warps that are not there
+            const uint32_t arrivals = warp == 20 ? 1 + kConverters - team : 1;
+            for (int u = 0; u < 2 * n_run; ++u) {
+                int tile;
+                bool is_v;
+                chunk_tile_of(u, n_run, fold, tile, is_v);
+                const int code = 2 * tile + is_v, cs = code % S::NC, s = u % NS;
+                bool good = chunk_wait(&c_full[cs], (code / S::NC) & 1, abort_flag, p.err);
+                if (good && u >= NS) good = chunk_wait(&empty[s], (u / NS - 1) & 1, abort_flag, p.err);
+                if (!__all_sync(0xffffffffu, good)) break;
+                const unsigned char* codes = sm + S::CODES + cs * S::CSTG;
+                unsigned char* dst = ring + s * STG;
+                const int start = chunk_tile_start(it, it.i0 + tile);
+                const int last_lo = p.window ? max(0, last - p.window + 1) : 0;
+                const bool partly = is_v && (start + kChunkTile - 1 > it.pos0 || (start < last_lo && start + kChunkTile > p.sinks));
+                constexpr int TOKENS = 32 / (4 * HALVES), GROUPS = kChunkTile / TOKENS;  // tokens of a warp's step, steps
+                const int second = (lane >> 2) & 1;
+                const int lane_r = HALVES == 2 ? (lane >> 4) * 2 + second : lane >> 2;
+                const int h = HALVES == 2 ? ((lane >> 3) & 1) ^ second : 0;
+                const int x = (lane & 3) * 2;  // first of two 8-channel chunks of the part
+                const unsigned char* src = codes + lane_r * D + h * 64 + x * 8;
+                bool bad = false;
+                // four steps' codes are read before the first is written; a tile that no row sees in part needs no look
+                auto convert = [&](auto look) {
+#pragma unroll 1
+                    for (int g0 = index; g0 < GROUPS; g0 += 4 * team) {
+                        uint4 c[4];
+#pragma unroll
+                        for (int y = 0; y < 4; ++y)
+                            if (g0 + y * team < GROUPS)
+                                c[y] = *reinterpret_cast<const uint4*>(src + (g0 + y * team) * TOKENS * D);
+#pragma unroll
+                        for (int y = 0; y < 4; ++y) {
+                            if (g0 + y * team >= GROUPS) break;
+                            const int r = (g0 + y * team) * TOKENS + lane_r;
+                            if constexpr (decltype(look)::value) {
+                                const int j = start + r;
+                                if (j > last || (j < it.first_lo && j >= p.sinks)) c[y] = make_uint4(0u, 0u, 0u, 0u);
+                                const uint32_t cw[4] = {c[y].x, c[y].y, c[y].z, c[y].w};
+#pragma unroll
+                                for (int q = 0; q < 4; ++q)  // a code of 0x7f or 0xff
+                                    bad = bad || __vcmpeq4(cw[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
+                            }
+                            const uint32_t cw[4] = {c[y].x, c[y].y, c[y].z, c[y].w};
+                            uint32_t w[8];
+#pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(cw[q / 2] >> (16 * (q % 2))));
+                                if constexpr (ACT == kF16) {
+                                    w[q] = f;
+                                } else {
+                                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
+                                    w[q] = pack_act<kBF16>(v.x, v.y);
+                                }
+                            }
+                            unsigned char* row = dst + h * HALF + r * 128;
+                            *reinterpret_cast<uint4*>(row + ((x ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+                            *reinterpret_cast<uint4*>(row + (((x + 1) ^ (r & 7)) * 16)) = make_uint4(w[4], w[5], w[6], w[7]);
+                        }
+                    }
+                };
+                if (partly) convert(std::true_type{});
+                else convert(std::false_type{});
+                if (bad) *plain_flag = 1;
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive_n(&full[s], arrivals);
+                    mbar_arrive_n(&c_empty[cs], arrivals);
+                }
+            }
+        }
+    } else if (warp < 16) {
         // ------------------------------------------------------------ softmax
         const int t = (warp >> 2) & 1, half = warp >> 3, row = (warp & 3) * 32 + lane;
         const int pair = 1 + (warp & 7);  // named barrier of the two warps of these rows
         const int cnt = t == 0 ? cnt0 : cnt1;
-        const int tok = row / G, g = row - tok * G;  // (rows past TQ * G and past the last token: none)
+        const int tok = (row * p.inv_group) >> 16, g = row - tok * G;  // (rows past TQ * G and past the last token: none)
         const bool mine = tok < rows_of(t);
         const bool live = __any_sync(0xffffffffu, mine);
         const int pos = mine ? it.pos0 + first_of(t) + tok : -1;
@@ -341,9 +433,11 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         float m = -INFINITY, l = 0.f;
         [[maybe_unused]] float unit = -INFINITY;
         bool ok = true;
-        for (int i = 0; i < cnt; ++i) {
+        // Warps without a row have nothing to do; the first one, which has some if any has, arrives for them.
+        const uint32_t arrivals = (warp & 3) == 0 ? 1 + 4 - (rows_of(t) * G + 31) / 32 : 1;
+        for (int i = 0; live && i < cnt; ++i) {
             ok = __all_sync(0xffffffffu, chunk_wait(&s_full[t], i & 1, abort_flag, p.err));
-            if (live) {
+            {
                 tc::fence_after_sync();
                 const int tile = fold ? 2 * i + t : i;
                 const int start = chunk_tile_start(it, it.i0 + tile) + half * 64;  // this half's first token
@@ -481,15 +575,12 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             if (!ok) break;
             tc::fence_before_sync();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_full[2 * t + half]);
+            if (lane == 0) mbar_arrive_n(&p_full[2 * t + half], arrivals);
         }
-        if (ok && cnt > 0) {
+        if (live && ok && cnt > 0) {
             ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (cnt - 1) & 1, abort_flag, p.err));
             tc::fence_after_sync();
         }
-        // folded, slot 1: slot 0's last product too, after which nothing reads the ring (at most one of its products is
-        // still open then, so that the parity names it)
-        if (ok && fold && t == 1 && cnt0 > 0) ok = __all_sync(0xffffffffu, chunk_wait(&o_done[0], (cnt0 - 1) & 1, abort_flag, p.err));
         // folded: both slots' threads of a quarter of the rows (128) go on or stop together
         auto quarter_any = [&](bool say) {
             int r;
@@ -514,48 +605,54 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             float vmul = 1.f;
             if constexpr (CACHE == kE4M3) vmul = *p.v_scale;
             if constexpr (SCALED) vmul = unit == -INFINITY ? 0.f : fast_exp2(unit - m);
-            // Folded: slot 1 leaves its O, in units of 2^m, with m and l in the ring (every tile was consumed: the products
-            // of both slots are done), column by column, a row a lane; slot 0 adds it to its own.
+            // Folded: slot 1 leaves its maximum, sum and unit; slot 0 reads both slots' O, the same lanes of tensor memory.
             float keep = 1.f, other = 0.f;
-            float* join = reinterpret_cast<float*>(ring);
-            float* from_1 = join + 2 * kChunkTile + half * (D / 2) * kChunkTile + row;
             if (fold) {
-                if (t == 1) {
-                    if (half == 0) {
-                        join[row] = m;
-                        join[kChunkTile + row] = l;
-                    }
-                    if (cnt > 0) {
-#pragma unroll
-                        for (int k = 0; k < D / 2; k += 32) {
-                            float o[32];
-                            tc::TmemLd<32>::load(o_addr + k, o);
-                            tc::tmem_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) from_1[(k + j) * kChunkTile] = o[j] * (CACHE == kE4M3 ? 1.f : vmul);
-                        }
-                    }
+                float* join = reinterpret_cast<float*>(sm + S::SWAP);  // [m, l], then [vmul]
+                quarter_any(false);  // the sums above were read
+                if (t == 1 && half == 0) {
+                    join[row] = m;
+                    join[kChunkTile + row] = l;
                 }
+                tc::fence_before_sync();
                 quarter_any(false);
-                if (t == 0 && cnt1 > 0) {
-                    const float m1 = join[row], l1 = join[kChunkTile + row], top = fmaxf(m, m1);
+                tc::fence_after_sync();
+                const float m1 = join[row], l1 = join[kChunkTile + row], top = fmaxf(m, m1);
+                if constexpr (SCALED) {
+                    quarter_any(false);
+                    if (t == 1 && half == 0) join[row] = vmul;
+                    quarter_any(false);
+                    other = join[row];
+                } else {
+                    other = 1.f;
+                }
+                if (t == 0) {
                     keep = m == -INFINITY && l == 0.f ? 0.f : fast_exp2(m - top);
-                    other = m1 == -INFINITY && l1 == 0.f ? 0.f : fast_exp2(m1 - top);
-                    l = l * keep + l1 * other;
+                    const float f = m1 == -INFINITY && l1 == 0.f ? 0.f : fast_exp2(m1 - top);
+                    l = l * keep + l1 * f;
+                    other *= f;
                     m = top;
                 }
             }
             // 32 channels of the row from k on, in units of 2^m (per-tensor E4M3: without the scale)
             auto load_o = [&](int k, float* o) {
                 tc::TmemLd<32>::load(o_addr + k, o);
-                tc::tmem_wait_ld();
                 if (fold && cnt1 > 0) {
                     const float f = keep * (CACHE == kE4M3 ? 1.f : vmul);
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = o[j] * f + (other == 0.f ? 0.f : from_1[(k + j) * kChunkTile] * other);
-                } else if constexpr (SCALED) {
+                    for (int x = 0; x < 32; x += 16) {
+                        float o1[16];
+                        tc::TmemLd<16>::load(o_addr + D + k + x, o1);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] *= vmul;
+                        for (int j = 0; j < 16; ++j) o[x + j] = o[x + j] * f + o1[j] * other;
+                    }
+                } else {
+                    tc::tmem_wait_ld();
+                    if constexpr (SCALED) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) o[j] *= vmul;
+                    }
                 }
             };
             const int64_t at = it.row0 + first_of(t) + tok;
@@ -572,7 +669,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             auto put = [&](int x, const uint4& v) {  // chunk x of this thread's row
                 *reinterpret_cast<uint4*>(stage + lane * TURN + ((x ^ (lane & (CHUNKS - 1))) * 16)) = v;
             };
-            const int inv_g = 65536 / G + 1;  // (r inv_g) >> 16 = r / G for r < 128, G <= 64
+            const int inv_g = p.inv_group;  // (r inv_g) >> 16 = r / G for r < 128, G <= 64
             // the warp's rows, TURN bytes each, to `row_dst(row's index in the item) + offset`
             auto flush = [&](auto row_dst) {
                 __syncwarp();
@@ -856,79 +953,6 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             if (!second && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
-    } else if (E8 && warp >= 20) {
-        // --------------------------------------------------------- conversion
-        // 16 codes a lane and step.  8 neighbouring lanes, which shared memory serves at once, take 64 channels of
-        // two tokens (head_dim 128: the other half of the second), so that neither their reads nor their writes,
-        // which the swizzle moves by one 16-byte chunk from token to token, meet in a bank.
-        if constexpr (E8) {
-            for (int u = 0; u < 2 * n_run; ++u) {
-                int tile;
-                bool is_v;
-                chunk_tile_of(u, n_run, fold, tile, is_v);
-                const int code = 2 * tile + is_v, cs = code % S::NC, s = u % NS;
-                bool good = chunk_wait(&c_full[cs], (code / S::NC) & 1, abort_flag, p.err);
-                if (good && u >= NS) good = chunk_wait(&empty[s], (u / NS - 1) & 1, abort_flag, p.err);
-                if (!__all_sync(0xffffffffu, good)) break;
-                const unsigned char* codes = sm + S::CODES + cs * S::CSTG;
-                unsigned char* dst = ring + s * STG;
-                const int start = chunk_tile_start(it, it.i0 + tile);
-                const int last_lo = p.window ? max(0, last - p.window + 1) : 0;
-                const bool partly = is_v && (start + kChunkTile - 1 > it.pos0 || (start < last_lo && start + kChunkTile > p.sinks));
-                constexpr int TOKENS = 32 / (4 * HALVES);  // of a warp's step
-                const int second = (lane >> 2) & 1;
-                const int lane_r = HALVES == 2 ? (lane >> 4) * 2 + second : lane >> 2;
-                const int h = HALVES == 2 ? ((lane >> 3) & 1) ^ second : 0;
-                const int x = (lane & 3) * 2;  // first of two 8-channel chunks of the part
-                const unsigned char* src = codes + lane_r * D + h * 64 + x * 8;
-                bool bad = false;
-                // four steps' codes are read before the first is written; a tile that no row sees in part needs no look
-                auto convert = [&](auto look) {
-#pragma unroll
-                    for (int r0 = (warp - 20) * TOKENS; r0 < kChunkTile + (warp - 20) * TOKENS; r0 += 16 * TOKENS) {
-                        uint4 c[4];
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) c[y] = *reinterpret_cast<const uint4*>(src + (r0 + 4 * y * TOKENS) * D);
-#pragma unroll
-                        for (int y = 0; y < 4; ++y) {
-                            const int r = r0 + 4 * y * TOKENS + lane_r;
-                            if constexpr (decltype(look)::value) {
-                                const int j = start + r;
-                                if (j > last || (j < it.first_lo && j >= p.sinks)) c[y] = make_uint4(0u, 0u, 0u, 0u);
-                                const uint32_t cw[4] = {c[y].x, c[y].y, c[y].z, c[y].w};
-#pragma unroll
-                                for (int q = 0; q < 4; ++q)  // a code of 0x7f or 0xff
-                                    bad = bad || __vcmpeq4(cw[q] & 0x7f7f7f7fu, 0x7f7f7f7fu) != 0;
-                            }
-                            const uint32_t cw[4] = {c[y].x, c[y].y, c[y].z, c[y].w};
-                            uint32_t w[8];
-#pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const uint32_t f = e4m3x2_to_f16x2(static_cast<uint16_t>(cw[q / 2] >> (16 * (q % 2))));
-                                if constexpr (ACT == kF16) {
-                                    w[q] = f;
-                                } else {
-                                    const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&f));
-                                    w[q] = pack_act<kBF16>(v.x, v.y);
-                                }
-                            }
-                            unsigned char* row = dst + h * HALF + r * 128;
-                            *reinterpret_cast<uint4*>(row + ((x ^ (r & 7)) * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-                            *reinterpret_cast<uint4*>(row + (((x + 1) ^ (r & 7)) * 16)) = make_uint4(w[4], w[5], w[6], w[7]);
-                        }
-                    }
-                };
-                if (partly) convert(std::true_type{});
-                else convert(std::false_type{});
-                if (bad) *plain_flag = 1;
-                tc::fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&full[s]);
-                    mbar_arrive(&c_empty[cs]);
-                }
-            }
-        }
     } else if (!E8 && warp == 19) {
         // ------------------------------------------------------- V tiles' check
         for (int i = 0; i < n_run; ++i) {

@@ -261,6 +261,9 @@ struct ChunkParams {
     int window;  // 0: none
     int sinks;
     float scale_log2;
+    int group;       // query heads of a kv head, set by launch_chunk with the two below
+    int row_tokens;  // tokens of a row tile: 128 / group
+    int inv_group;   // 65536 / group + 1: (r * inv_group) >> 16 = r / group for r < 128, group <= 64
     int splits;   // shares of an item's token tiles, each a block's; 1: none
     float* ws_ml;  // [splits][num_tokens][num_q_heads][2]: (reference maximum in log2 units, sum); null: one share
     float* ws_o;   // [splits][num_tokens][num_q_heads][head_dim]: sums relative to the maximum
