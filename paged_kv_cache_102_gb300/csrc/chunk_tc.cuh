@@ -24,7 +24,7 @@
 //                  so that the two need no more of each other than a vote; when it
 //                  moves (almost never after the first tile) they exchange their
 //                  maxima and multiply the row of O, half each.
-//  warp 16         MMA: S_t = Q_t K^T (M = 128 rows, N = 128 tokens), O_t += P_t V
+//  warp 19         MMA: S_t = Q_t K^T (M = 128 rows, N = 128 tokens), O_t += P_t V
 //                  (P from tensor memory, N = head_dim).  Order: S_0(0), S_1(0),
 //                  then for each tile i and t: O_t(i), S_t(i + 1).  While one row
 //                  tile is in the softmax, the other's products run.
@@ -33,7 +33,7 @@
 //                  whose products take a block's tokens at a time, one of each block.
 //                  The copies of a warp leave one after the other, some 94 cycles
 //                  each; sharing K's 16 between the two warps was no faster.
-//  warp 19         V tiles that some row sees in part: rows that no row of the
+//  warp 16         V tiles that some row sees in part: rows that no row of the
 //                  item sees become zeros (what lies there may be anything, and
 //                  0 times it must be 0); a number that is not finite among the
 //                  others sends the item to the plain loop at the end, since a
@@ -42,7 +42,7 @@
 //                  copy a block) into a ring of their own; these warps, and of a
 //                  folded item the softmax warps that have none of its rows, write them
 //                  as 16-bit elements, exactly, into the ring that the products
-//                  read, and do warp 19's work on the way.  One scale per tensor
+//                  read, and do warp 16's work on the way.  One scale per tensor
 //                  joins the logits' factor and the output's.  Block scales: the
 //                  K producer leaves a tile's scales in shared memory; a logit is
 //                  multiplied by its block's K scale, and a weight, for the product
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int G = p.group, TQ = p.row_tokens, R = 2 * TQ;
-    if (warp == 19) {
+    if (warp == 16) {
         // the item: found and worked out once, for the others to read
         const int slot = (gridDim.x - 1 - blockIdx.x) / p.num_kv_heads;  // later rows, which see more, first
         const int b = chunk_find(p.seq_starts, p.num_seqs, R, slot, lane);
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 if (s0 < 0 || s1 < s0 || s1 > p.num_tokens || (s1 > s0 && (L < s1 - s0 || L > p.max_blocks_per_seq * p.block_size)))
                     atomicOr(p.err, kErrBadLen);
             }
-    } else if (warp == 16) {
+    } else if (warp == 19) {
         tc::tmem_alloc(tmem_base_smem, kChunkTmemCols);
         tc::tmem_relinquish();
     } else if (threadIdx.x == 17 * 32) {
@@ -725,7 +725,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             }
             }
         }
-    } else if (warp == 16) {
+    } else if (warp == 19) {
         // ---------------------------------------------------------------- MMA
         // Descriptors as words, stepped by additions; one elected lane issues.
         constexpr uint32_t HI = tc::desc_hi_sw128(1024);
@@ -869,7 +869,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             if (!mbar_wait(final_bar, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
-    } else if (warp < 19) {
+    } else if (warp == 17 || warp == 18) {
         // ---------------------------------------------------------- producers
         const bool second = warp == 18;  // V; else K and Q
         if (!second && lane == 0 && n_run > 0) {
@@ -953,7 +953,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             if (!second && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
-    } else if (!E8 && warp == 19) {
+    } else if (!E8 && warp == 16) {
         // ------------------------------------------------------- V tiles' check
         for (int i = 0; i < n_run; ++i) {
             const int use = 2 * i + 1, s = use % NS;
@@ -1003,7 +1003,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();
-    if (warp == 16) tc::tmem_dealloc(tmem, kChunkTmemCols);
+    if (warp == 19) tc::tmem_dealloc(tmem, kChunkTmemCols);
 
     // A V that is not finite, in a tile that some row sees in part: the item's rows one by one.
     if (*plain_flag != 0 && *abort_flag == 0) {
