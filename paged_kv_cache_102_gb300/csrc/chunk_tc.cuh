@@ -119,6 +119,7 @@ __device__ __forceinline__ bool chunk_wait(uint64_t* bar, uint32_t parity, volat
             atomicOr(err, kErrTimeout);
             return false;
         }
+        __nanosleep(50);  // most warps wait most of the time: their tries take issue slots from the others
     }
     return true;
 }
@@ -249,9 +250,20 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
     if (warp == 16) {
         // the item: found and worked out once, for the others to read
         const int slot = (gridDim.x - 1 - blockIdx.x) / p.num_kv_heads;  // later rows, which see more, first
-        const int b = chunk_find(p.seq_starts, p.num_seqs, R, slot, lane);
+        int b, s0, s1, L;
+        if (p.num_seqs < 32) {  // one round trip
+            const int at = lane <= p.num_seqs ? p.seq_starts[lane] : 0, len = lane < p.num_seqs ? p.context_lens[lane] : 0;
+            b = 31 - __clz(__ballot_sync(0xffffffffu, lane < p.num_seqs && at / R + lane <= slot) | 1u);
+            s0 = __shfl_sync(0xffffffffu, at, b);
+            s1 = __shfl_sync(0xffffffffu, at, b + 1);
+            L = __shfl_sync(0xffffffffu, len, b);
+        } else {
+            b = chunk_find(p.seq_starts, p.num_seqs, R, slot, lane);
+            s0 = p.seq_starts[b];
+            s1 = p.seq_starts[b + 1];
+            L = p.context_lens[b];
+        }
         if (lane == 0) {
-            const int s0 = p.seq_starts[b], s1 = p.seq_starts[b + 1], L = p.context_lens[b];
             const int first = (slot - (s0 / R + b)) * R;  // of the sequence's new tokens
             ChunkItem x;
             x.seq = b;
@@ -871,17 +883,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         __syncwarp();
     } else if (warp == 17 || warp == 18) {
         // ---------------------------------------------------------- producers
-        const bool second = warp == 18;  // V; else K and Q
-        if (!second && lane == 0 && n_run > 0) {
-            const uint32_t bytes = HALVES * G * TQ * 128;
-            const bool both = !fold && cnt1 > 0;  // (tiles of a share that are all behind row tile 0 leave its queries unused)
-            mbar_arrive_expect_tx(q_full, (both ? 2 : 1) * bytes);
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (t == 0 || both)
-                    for (int h = 0; h < HALVES; ++h)
-                        tc::tma_load_3d(qbuf + t * S::QT + h * HALF, &qmap, h * 64, it.kvh * G, it.row0 + t * TQ, q_full, policy);
-        }
+        const bool second = warp == 18;  // V and Q; else K
         const int BS = p.block_size, bpt = kChunkTile / BS;
         const int32_t* table = p.block_tables + static_cast<int64_t>(it.seq) * p.max_blocks_per_seq;
         // the block of tile i: -1 past the last row's tokens, wholly hidden, or outside the pool
@@ -901,6 +903,16 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         const int j = second ? lane : lane / parts, kh = lane % parts;
         const bool take = lane < (second ? bpt : bpt * parts);
         int phys = entry(0, j, take), issued = 0;
+        if (second && lane == 0 && n_run > 0) {
+            const uint32_t bytes = HALVES * G * TQ * 128;
+            const bool both = !fold && cnt1 > 0;  // (tiles of a share that are all behind row tile 0 leave its queries unused)
+            mbar_arrive_expect_tx(q_full, (both ? 2 : 1) * bytes);
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+                if (t == 0 || both)
+                    for (int h = 0; h < HALVES; ++h)
+                        tc::tma_load_3d(qbuf + t * S::QT + h * HALF, &qmap, h * 64, it.kvh * G, it.row0 + t * TQ, q_full, policy);
+        }
         for (int i = 0; i < n_run; ++i) {
             const int use = 2 * i + second, next = entry(i + 1, j, take);
             const int s = use % NP;
@@ -950,7 +962,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 const int use = 2 * i + second;
                 if (!mbar_wait(E8 ? &c_full[use % NP] : &full[use % NP], (use / NP) & 1)) atomicOr(p.err, kErrTimeout);
             }
-            if (!second && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
+            if (second && n_run > 0 && !mbar_wait(q_full, 0)) atomicOr(p.err, kErrTimeout);
         }
         __syncwarp();
     } else if (!E8 && warp == 16) {
