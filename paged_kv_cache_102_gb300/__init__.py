@@ -276,22 +276,32 @@ class DecodePlan:
     """One decode step for fixed tensors, validated and marshalled once.
 
     With k_new, v_new and slot_mapping it is paged_attention_decode_append,
-    with k_scales and v_scales paged_attention_decode_scaled, else
-    paged_attention_decode; the arguments mean the same.  run() issues
+    with window (and sinks) paged_attention_decode_window, with k_scales and
+    v_scales paged_attention_decode_scaled, else paged_attention_decode; the
+    arguments mean the same.  run() issues
     the step with a single C call and returns `out`.  Between runs the
     tensors' contents may change (new queries, tables, lengths), their
     storage, shapes and types may not.  Every run goes on the stream given
     here (default: the current stream at construction).  Plans that may run
-    at the same time need a workspace each (with k_scales and v_scales the
-    default one is the plan's own)."""
+    at the same time need a workspace each (with window, or with k_scales and
+    v_scales, the default one is the plan's own)."""
 
     def __init__(self, q, k_cache, v_cache, block_tables, context_lens, scale, out=None, k_scale=None, v_scale=None,
                  partition_size=PARTITION_AUTO, workspace=None, stream=None, k_new=None, v_new=None,
-                 slot_mapping=None, k_scales=None, v_scales=None):
+                 slot_mapping=None, k_scales=None, v_scales=None, window=None, sinks=0):
         given = [t is not None for t in (k_new, v_new, slot_mapping)]
         if any(given) and not all(given):
             raise ValueError("DecodePlan: k_new, v_new and slot_mapping go together")
-        if k_scales is not None or v_scales is not None:
+        if window is None and sinks != 0:
+            raise ValueError("DecodePlan: sinks without a window")
+        if window is not None:
+            if any(given):
+                raise ValueError("DecodePlan: a window does not go with an append")
+            self.func = "paged_attention_decode_window"
+            self._args, self.out, ws = _decode_window_args(q, k_cache, v_cache, block_tables, context_lens, scale, window,
+                                                           sinks, out, k_scale, v_scale, k_scales, v_scales,
+                                                           partition_size, workspace, stream, own_workspace=True)
+        elif k_scales is not None or v_scales is not None:
             if any(given) or k_scale is not None or v_scale is not None:
                 raise ValueError("DecodePlan: k_scales and v_scales go with neither an append nor k_scale, v_scale")
             self.func = "paged_attention_decode_scaled"
@@ -811,6 +821,16 @@ def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_len
     its first `sinks` ones; returns out [B, Hq, D].  Blocks wholly between the two are not read, nor are their table
     entries.  A context length of 0 (a padding row) gives zeros.  The cache is of q's type or E4M3 with either kind
     of scales."""
+    args, out, _ = _decode_window_args(q, k_cache, v_cache, block_tables, context_lens, scale, window, sinks, out, k_scale,
+                                       v_scale, k_scales, v_scales, partition_size, workspace, stream)
+    _call_on(k_cache.device, "paged_attention_decode_window", *args)
+    return out
+
+
+def _decode_window_args(q, k_cache, v_cache, block_tables, context_lens, scale, window, sinks, out, k_scale, v_scale,
+                        k_scales, v_scales, partition_size, workspace, stream, own_workspace=False):
+    """Validated C arguments of paged_attention_decode_window, the output and the workspace (own_workspace: not the
+    stream's reusable one)."""
     name = "paged_attention_decode_window"
     shape, device, scales = _cache_args(name, q, k_cache, v_cache, k_scale, v_scale, k_scales, v_scales)
     NB, Hkv, bs, D = shape
@@ -821,13 +841,13 @@ def paged_attention_decode_window(q, k_cache, v_cache, block_tables, context_len
     if workspace is None:
         need = _size_of("pkv_window_workspace_size", B, Hq, Hkv, D, max_blocks, bs, window, sinks,
                         0 if scales[2] is None else 1, partition_size)
-        workspace = _reused(device, stream, s, need, 0)
+        workspace = (_output(stream, device, (max(need, 1),), torch.uint8) if own_workspace
+                     else _reused(device, stream, s, need, 0))
     qp, kc, vc, tables, lens, ws = _pointers(name, device, "q k_cache v_cache block_tables context_lens workspace", q,
                                              k_cache, v_cache, block_tables, context_lens, workspace)
-    _call_on(device, name, qp, kc, vc, tables, max_blocks, lens, B, Hq, Hkv, bs, D, NB, float(scale), window, sinks,
-             out.data_ptr(), _code(q), _code(k_cache), *scales, partition_size, ws,
-             workspace.numel() * workspace.element_size(), s)
-    return out
+    args = (qp, kc, vc, tables, max_blocks, lens, B, Hq, Hkv, bs, D, NB, float(scale), window, sinks, out.data_ptr(),
+            _code(q), _code(k_cache), *scales, partition_size, ws, workspace.numel() * workspace.element_size(), s)
+    return args, out, workspace
 
 
 def paged_attention_decode_scored(q, k_cache, v_cache, block_tables, context_lens, scale, scores, out=None,

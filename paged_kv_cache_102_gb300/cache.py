@@ -15,14 +15,20 @@ to store the KV cache", section "Copy-on-Write").
 With block_scales=True the pools hold E4M3 codes with one scale for each block
 and kv head (k_scales, v_scales), kept by the scaled append, the copies and the
 scaled decode.  rope_append rotates queries and keys on the way in.
+
+attend is the attention of several new tokens a sequence (prompts, their parts,
+drafted tokens) once they are in the pools; with a window, attend and decode see
+the last tokens and the first ones alone.  decode_scored keeps count of what the
+cached tokens are worth, and evict moves the best of them to fewer blocks.
 """
 from __future__ import annotations
 
 import numpy as np
 import torch
 
-from . import (PARTITION_AUTO, BlockManager, _torch_stream, paged_attention_decode, paged_attention_decode_scaled,
-               paged_block_copy, paged_kv_append, paged_kv_append_scaled, paged_rope_append)
+from . import (PARTITION_AUTO, BlockManager, _torch_stream, paged_attention_chunk, paged_attention_decode,
+               paged_attention_decode_scaled, paged_attention_decode_scored, paged_attention_decode_window,
+               paged_block_copy, paged_kv_append, paged_kv_append_scaled, paged_kv_evict, paged_rope_append)
 
 
 class PagedKVCache:
@@ -103,14 +109,75 @@ class PagedKVCache:
         return slots, pairs
 
     def decode(self, seq_ids, q: torch.Tensor, scale: float, out=None, partition_size=PARTITION_AUTO,
-               max_blocks_per_seq=None, stream=None):
+               max_blocks_per_seq=None, stream=None, window=None, sinks=0):
+        if window is None and sinks:
+            raise ValueError("PagedKVCache.decode: sinks without a window")
         tables, lens = (self._upload(a, stream) for a in self.blocks.tables(seq_ids, max_blocks_per_seq))
+        if window is not None:
+            return paged_attention_decode_window(q, self.k_cache, self.v_cache, tables, lens, scale, window, sinks=sinks,
+                                                 out=out, k_scale=self.k_scale, v_scale=self.v_scale,
+                                                 k_scales=self.k_scales, v_scales=self.v_scales,
+                                                 partition_size=partition_size, stream=stream)
         if self.k_scales is not None:
             return paged_attention_decode_scaled(q, self.k_cache, self.v_cache, self.k_scales, self.v_scales, tables,
                                                  lens, scale, out=out, partition_size=partition_size, stream=stream)
         return paged_attention_decode(q, self.k_cache, self.v_cache, tables, lens, scale, out=out,
                                       k_scale=self.k_scale, v_scale=self.v_scale,
                                       partition_size=partition_size, stream=stream)
+
+    def attend(self, seq_ids, q: torch.Tensor, new_lens, scale: float, window=None, sinks=0, out=None,
+               max_blocks_per_seq=None, stream=None):
+        """Attention of each sequence's last new_lens tokens, the rows of q [sum(new_lens), Hq, D] in the order of
+        seq_ids; they are in the pools already."""
+        new = np.asarray(new_lens, np.int64)
+        if new.shape != np.asarray(seq_ids).shape or (new < 0).any() or new.sum() != q.shape[0]:
+            raise ValueError("PagedKVCache.attend: q has a row for each of the sequences' new tokens")
+        if any(n > self.blocks.context_len(s) for s, n in zip(np.asarray(seq_ids), new)):
+            raise ValueError("PagedKVCache.attend: more new tokens than a sequence has")
+        tables, lens = (self._upload(a, stream) for a in self.blocks.tables(seq_ids, max_blocks_per_seq))
+        starts = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        return paged_attention_chunk(q, self.k_cache, self.v_cache, tables, lens, self._upload(starts, stream), scale,
+                                     window=window, sinks=sinks, out=out, k_scale=self.k_scale, v_scale=self.v_scale,
+                                     k_scales=self.k_scales, v_scales=self.v_scales, stream=stream)
+
+    def decode_scored(self, seq_ids, q: torch.Tensor, scale: float, scores: torch.Tensor, out=None,
+                      partition_size=PARTITION_AUTO, max_blocks_per_seq=None, stream=None):
+        """decode that adds every cached token's weight to scores float32 [n, Hkv, tokens], a row a sequence (not for
+        block scales)."""
+        if self.k_scales is not None:
+            raise ValueError("PagedKVCache.decode_scored: not for a block-scaled cache")
+        tables, lens = (self._upload(a, stream) for a in self.blocks.tables(seq_ids, max_blocks_per_seq))
+        return paged_attention_decode_scored(q, self.k_cache, self.v_cache, tables, lens, scale, scores, out=out,
+                                             k_scale=self.k_scale, v_scale=self.v_scale, partition_size=partition_size,
+                                             stream=stream)
+
+    def evict(self, seq_ids, new_ids, scores: torch.Tensor, budget: int, recent: int, sinks=0, stream=None):
+        """Replace each sequence by one of at most budget tokens under a new id: those that paged_kv_evict keeps, whose
+        result this returns.  The old sequences are freed (blocks that they share with others stay)."""
+        if self.k_scales is not None:
+            raise ValueError("PagedKVCache.evict: not for a block-scaled cache")
+        seq_ids, new_ids = [int(s) for s in np.asarray(seq_ids)], [int(s) for s in np.asarray(new_ids)]
+        lens = [self.blocks.context_len(s) for s in seq_ids]
+        if len(new_ids) != len(seq_ids) or len(set(seq_ids)) != len(seq_ids) or budget < 1:
+            raise ValueError("PagedKVCache.evict: a new id for each sequence, each once, and a positive budget")
+        if lens and max(lens) > scores.shape[-1]:
+            raise ValueError("PagedKVCache.evict: scores for each token of the sequences")
+        added = []
+        try:
+            for s, n in zip(new_ids, lens):
+                self.blocks.add_sequence(s, min(n, int(budget)))
+                added.append(s)
+            src, length = (self._upload(a, stream) for a in self.blocks.tables(seq_ids))
+            dst = self._upload(self.blocks.tables(new_ids)[0], stream)
+            got = paged_kv_evict(self.k_cache, self.v_cache, scores, src, length, dst, budget, recent, sinks=sinks,
+                                 stream=stream)
+        except Exception:
+            for s in added:  # as before
+                self.blocks.free_sequence(s)
+            raise
+        for s in seq_ids:
+            self.blocks.free_sequence(s)
+        return got
 
     def unused_slots(self, seq_ids) -> int:
         """Slots allocated to these sequences but not yet written (tail waste)."""
