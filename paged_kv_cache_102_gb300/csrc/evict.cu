@@ -296,7 +296,8 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     const int64_t most = static_cast<int64_t>(p.max_blocks_per_seq) * p.block_size;
     const int smem = static_cast<int>((most < kKeyTokens ? most : kKeyTokens) * 4);
     const dim3 heads(p.num_kv_heads, p.num_seqs);
-    if (static_cast<int64_t>(p.budget) * p.row_bytes <= kMoveHere) {
+    const int64_t stay = p.budget < most ? p.budget : most;  // tokens of a row that may
+    if (stay * p.row_bytes <= kMoveHere) {
         evict_select_kernel<true><<<heads, kSelectThreads, smem, stream>>>(p);
         return cudaGetLastError();
     }
@@ -304,7 +305,7 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const int rows = kMoveThreads / (p.row_bytes / 16);
-    const dim3 grid((p.budget + rows - 1) / rows, p.num_kv_heads, p.num_seqs);
+    const dim3 grid(static_cast<unsigned>((stay + rows - 1) / rows), p.num_kv_heads, p.num_seqs);
     return launch_after(evict_move_kernel, p, grid, kMoveThreads, stream);
 }
 
