@@ -415,6 +415,9 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 };
                 if (partly) convert(std::true_type{});
                 else convert(std::false_type{});
+                if constexpr (SCALED)  // a V scale is a factor of weights of 0 too (K's place came first, and its scales)
+                    if (partly && lane < 8)
+                        bad = bad || !isfinite(reinterpret_cast<const float*>(sm + S::SCALES)[(tile % S::SLOTS) * 24 + 8 + lane]);
                 if (bad) *plain_flag = 1;
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -449,142 +452,139 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         const uint32_t arrivals = (warp & 3) == 0 ? 1 + 4 - (rows_of(t) * G + 31) / 32 : 1;
         for (int i = 0; live && i < cnt; ++i) {
             ok = __all_sync(0xffffffffu, chunk_wait(&s_full[t], i & 1, abort_flag, p.err));
-            {
-                tc::fence_after_sync();
-                const int tile = fold ? 2 * i + t : i;
-                const int start = chunk_tile_start(it, it.i0 + tile) + half * 64;  // this half's first token
-                const bool masked = start + 63 > pos_lo || (p.window != 0 && start <= pos_hi - p.window && start + 64 > p.sinks);
-                [[maybe_unused]] const float* scales =
-                    reinterpret_cast<const float*>(sm + S::SCALES) + (SCALED ? (tile % max(1, S::SLOTS)) * 24 : 0);
-                [[maybe_unused]] const int block0 = half * 64 / p.block_size, bshift = p.block_size == 32 ? 1 : 0;
-                // scores x[0 .. N) from column k on, as loaded, to what `c` makes log2 units
-                auto prepare = [&](int k, int n, float* x) {
-                    if constexpr (SCALED) {
+            tc::fence_after_sync();
+            const int tile = fold ? 2 * i + t : i;
+            const int start = chunk_tile_start(it, it.i0 + tile) + half * 64;  // this half's first token
+            const bool masked = start + 63 > pos_lo || (p.window != 0 && start <= pos_hi - p.window && start + 64 > p.sinks);
+            [[maybe_unused]] const float* scales =
+                reinterpret_cast<const float*>(sm + S::SCALES) + (SCALED ? (tile % max(1, S::SLOTS)) * 24 : 0);
+            [[maybe_unused]] const int block0 = half * 64 / p.block_size, bshift = p.block_size == 32 ? 1 : 0;
+            // scores x[0 .. N) from column k on, as loaded, to what `c` makes log2 units
+            auto prepare = [&](int k, int n, float* x) {
+                if constexpr (SCALED) {
 #pragma unroll
-                        for (int y = 0; y < n; y += 16) {
-                            const float f = factor * scales[block0 + (((k + y) >> 4) >> bshift)];
+                    for (int y = 0; y < n; y += 16) {
+                        const float f = factor * scales[block0 + (((k + y) >> 4) >> bshift)];
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) x[y + j] *= f;
-                        }
-                    } else if (negative) {
-#pragma unroll
-                        for (int j = 0; j < n; ++j) x[j] = -x[j];
+                        for (int j = 0; j < 16; ++j) x[y + j] *= f;
                     }
-                    if (masked) {
-                        const int end = pos - start - k;                     // sees columns up to this one
-                        const int from = p.window ? end - p.window + 1 : 0;  // and from this one on,
-                        const int sink = p.sinks - start - k;                // or before this one
+                } else if (negative) {
 #pragma unroll
-                        for (int y = 0; y < n; y += 32) {
-                            const uint32_t seen = low_bits(end + 1 - y) & (~low_bits(from - y) | low_bits(sink - y));
+                    for (int j = 0; j < n; ++j) x[j] = -x[j];
+                }
+                if (masked) {
+                    const int end = pos - start - k;                     // sees columns up to this one
+                    const int from = p.window ? end - p.window + 1 : 0;  // and from this one on,
+                    const int sink = p.sinks - start - k;                // or before this one
 #pragma unroll
-                            for (int j = 0; j < 32; ++j)
-                                if (!(seen & (1u << j))) x[y + j] = -INFINITY;
-                        }
-                    }
-                };
-                // 16-bit caches hold a thread's scores; the others, with fewer registers a thread, read them twice
-                constexpr int HELD = E8 ? 32 : 64;
-                float s[HELD], tops[4];
-                [[maybe_unused]] float mu = -INFINITY;
+                    for (int y = 0; y < n; y += 32) {
+                        const uint32_t seen = low_bits(end + 1 - y) & (~low_bits(from - y) | low_bits(sink - y));
 #pragma unroll
-                for (int k = 0; k < 64; k += HELD) {
-#pragma unroll
-                    for (int y = 0; y < HELD; y += 32) tc::TmemLd<32>::load(s_addr + k + y, s + y);
-                    tc::tmem_wait_ld();
-                    prepare(k, HELD, s);
-#pragma unroll
-                    for (int y = 0; y < HELD; y += 16) {
-                        float top = max3(s[y], s[y + 1], s[y + 2]);
-#pragma unroll
-                        for (int j = 3; j < 15; j += 2) top = max3(top, s[y + j], s[y + j + 1]);
-                        tops[(k + y) / 16] = top = fmaxf(top, s[y + 15]);
-                        if constexpr (SCALED) mu = fmaxf(mu, top + scales[16 + block0 + (((k + y) >> 4) >> bshift)]);
+                        for (int j = 0; j < 32; ++j)
+                            if (!(seen & (1u << j))) x[y + j] = -INFINITY;
                     }
                 }
-                float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
-                const bool past = mine && (mx > m + kChunkRescale || (SCALED && mu > unit + kChunkRescale));
-                if (pair_any(pair, past || !ok)) {
-                    // the products of the tiles before are done before the row of O is multiplied
-                    if (ok && i > 0) {
-                        ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (i - 1) & 1, abort_flag, p.err));
-                        tc::fence_after_sync();
-                    }
-                    if (pair_any(pair, !ok)) {  // both leave
-                        ok = false;
-                        break;
-                    }
-                    // the row's maximum, and so its reference, from both threads
-                    auto agree = [&](float top, float at) {
-                        if (half == 1) *swap = top;
-                        pair_any(pair, false);
-                        float to = at;
-                        if (half == 0) {
-                            top = fmaxf(top, *swap);
-                            if (mine && top > at + kChunkRescale) to = top;
-                            *swap = to;
-                        }
-                        pair_any(pair, false);
-                        if (half == 1) to = *swap;
-                        return to;
-                    };
-                    const float to = agree(mx, m);
-                    const float down = to == m ? 1.f : fast_exp2(m - to);
-                    float f = down;
-                    if constexpr (SCALED) {
-                        const float u = agree(mu, unit);
-                        f = u == unit ? 1.f : fast_exp2(unit - u);
-                        unit = u;
-                    }
-                    l *= down;
-                    m = to;
-                    if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            };
+            // 16-bit caches hold a thread's scores; the others, with fewer registers a thread, read them twice
+            constexpr int HELD = E8 ? 32 : 64;
+            float s[HELD], tops[4];
+            [[maybe_unused]] float mu = -INFINITY;
 #pragma unroll
-                        for (int k = 0; k < D / 2; k += 8) {
-                            float o[8];
-                            tc::TmemLd<8>::load(o_addr + k, o);
-                            tc::tmem_wait_ld();
+            for (int k = 0; k < 64; k += HELD) {
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) o[j] *= f;
-                            tc::tmem_st<8>(o_addr + k, o);
-                        }
-                    }
+                for (int y = 0; y < HELD; y += 32) tc::TmemLd<32>::load(s_addr + k + y, s + y);
+                tc::tmem_wait_ld();
+                prepare(k, HELD, s);
+#pragma unroll
+                for (int y = 0; y < HELD; y += 16) {
+                    float top = max3(s[y], s[y + 1], s[y + 2]);
+#pragma unroll
+                    for (int j = 3; j < 15; j += 2) top = max3(top, s[y + j], s[y + j + 1]);
+                    tops[(k + y) / 16] = top = fmaxf(top, s[y + 15]);
+                    if constexpr (SCALED) mu = fmaxf(mu, top + scales[16 + block0 + (((k + y) >> 4) >> bshift)]);
                 }
-                const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of 0
-                [[maybe_unused]] const float lift = SCALED && unit != -INFINITY ? fast_exp2(ref - unit) : 0.f;
-                float sum[4] = {};
-#pragma unroll
-                for (int k = 0; k < 64; k += 32) {
-                    float* x = s + (E8 ? 0 : k);
-                    if constexpr (E8) {
-                        tc::TmemLd<32>::load(s_addr + k, x);
-                        tc::tmem_wait_ld();
-                        prepare(k, 32, x);
-                    }
-                    uint32_t w[16];
-#pragma unroll
-                    for (int y = 0; y < 32; y += 16) {
-                        [[maybe_unused]] float vf = 1.f;
-                        if constexpr (SCALED) vf = lift * scales[8 + block0 + (((k + y) >> 4) >> bshift)];
-#pragma unroll
-                        for (int j = 0; j < 16; j += 2) {
-                            float a = fast_exp2(fmaf(x[y + j], c, -ref));
-                            float b = fast_exp2(fmaf(x[y + j + 1], c, -ref));
-                            sum[j & 2] += a;
-                            sum[(j & 2) + 1] += b;
-                            if constexpr (SCALED) {
-                                a *= vf;
-                                b *= vf;
-                            }
-                            w[(y + j) / 2] = pack_act<ACT>(a, b);
-                        }
-                    }
-                    tc::tmem_st16(s_addr + k / 2, w);
-                }
-                l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                tc::tmem_wait_st();
             }
-            if (!ok) break;
+            float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
+            const bool past = mine && (mx > m + kChunkRescale || (SCALED && mu > unit + kChunkRescale));
+            if (pair_any(pair, past || !ok)) {
+                // the products of the tiles before are done before the row of O is multiplied
+                if (ok && i > 0) {
+                    ok = __all_sync(0xffffffffu, chunk_wait(&o_done[t], (i - 1) & 1, abort_flag, p.err));
+                    tc::fence_after_sync();
+                }
+                if (pair_any(pair, !ok)) {  // both leave
+                    ok = false;
+                    break;
+                }
+                // the row's maximum, and so its reference, from both threads
+                auto agree = [&](float top, float at) {
+                    if (half == 1) *swap = top;
+                    pair_any(pair, false);
+                    float to = at;
+                    if (half == 0) {
+                        top = fmaxf(top, *swap);
+                        if (mine && top > at + kChunkRescale) to = top;
+                        *swap = to;
+                    }
+                    pair_any(pair, false);
+                    if (half == 1) to = *swap;
+                    return to;
+                };
+                const float to = agree(mx, m);
+                const float down = to == m ? 1.f : fast_exp2(m - to);
+                float f = down;
+                if constexpr (SCALED) {
+                    const float u = agree(mu, unit);
+                    f = u == unit ? 1.f : fast_exp2(unit - u);
+                    unit = u;
+                }
+                l *= down;
+                m = to;
+                if (i > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+#pragma unroll
+                    for (int k = 0; k < D / 2; k += 8) {
+                        float o[8];
+                        tc::TmemLd<8>::load(o_addr + k, o);
+                        tc::tmem_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) o[j] *= f;
+                        tc::tmem_st<8>(o_addr + k, o);
+                    }
+                }
+            }
+            const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of 0
+            [[maybe_unused]] const float lift = SCALED && unit != -INFINITY ? fast_exp2(ref - unit) : 0.f;
+            float sum[4] = {};
+#pragma unroll
+            for (int k = 0; k < 64; k += 32) {
+                float* x = s + (E8 ? 0 : k);
+                if constexpr (E8) {
+                    tc::TmemLd<32>::load(s_addr + k, x);
+                    tc::tmem_wait_ld();
+                    prepare(k, 32, x);
+                }
+                uint32_t w[16];
+#pragma unroll
+                for (int y = 0; y < 32; y += 16) {
+                    [[maybe_unused]] float vf = 1.f;
+                    if constexpr (SCALED) vf = lift * scales[8 + block0 + (((k + y) >> 4) >> bshift)];
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2) {
+                        float a = fast_exp2(fmaf(x[y + j], c, -ref));
+                        float b = fast_exp2(fmaf(x[y + j + 1], c, -ref));
+                        sum[j & 2] += a;
+                        sum[(j & 2) + 1] += b;
+                        if constexpr (SCALED) {
+                            a *= vf;
+                            b *= vf;
+                        }
+                        w[(y + j) / 2] = pack_act<ACT>(a, b);
+                    }
+                }
+                tc::tmem_st16(s_addr + k / 2, w);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tc::tmem_wait_st();
             tc::fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive_n(&p_full[2 * t + half], arrivals);
@@ -671,70 +671,70 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             const int h = it.kvh * G + g;
             const float vt = CACHE == kE4M3 ? vmul : 1.f;
             if (!fold || t == 0) {
-            // Rows go out through the row tile's queries' memory, which its last scores have read: 32 rows of 128 bytes
-            // a warp and turn, chunks of 16 bytes swizzled by the row; then 8 lanes write 128 bytes of one row (a lane
-            // with a row of its own would take 32 lines an instruction).
-            unsigned char* stage = qbuf + t * S::QT + (half * 4 + (warp & 3)) * (S::QT / 8);
-            static_assert(S::QT / 8 >= 32 * 64, "room for half a turn of each warp");
-            constexpr int TURN = S::QT / 8 / 32;  // bytes of a row: 128, or 64 at head_dim 64
-            constexpr int CHUNKS = TURN / 16;
-            auto put = [&](int x, const uint4& v) {  // chunk x of this thread's row
-                *reinterpret_cast<uint4*>(stage + lane * TURN + ((x ^ (lane & (CHUNKS - 1))) * 16)) = v;
-            };
-            const int inv_g = p.inv_group;  // (r inv_g) >> 16 = r / G for r < 128, G <= 64
-            // the warp's rows, TURN bytes each, to `row_dst(row's index in the item) + offset`
-            auto flush = [&](auto row_dst) {
-                __syncwarp();
+                // Rows go out through the row tile's queries' memory, which its last scores have read: 32 rows of 128 bytes
+                // a warp and turn, chunks of 16 bytes swizzled by the row; then 8 lanes write 128 bytes of one row (a lane
+                // with a row of its own would take 32 lines an instruction).
+                unsigned char* stage = qbuf + t * S::QT + (half * 4 + (warp & 3)) * (S::QT / 8);
+                static_assert(S::QT / 8 >= 32 * 64, "room for half a turn of each warp");
+                constexpr int TURN = S::QT / 8 / 32;  // bytes of a row: 128, or 64 at head_dim 64
+                constexpr int CHUNKS = TURN / 16;
+                auto put = [&](int x, const uint4& v) {  // chunk x of this thread's row
+                    *reinterpret_cast<uint4*>(stage + lane * TURN + ((x ^ (lane & (CHUNKS - 1))) * 16)) = v;
+                };
+                const int inv_g = p.inv_group;  // (r inv_g) >> 16 = r / G for r < 128, G <= 64
+                // the warp's rows, TURN bytes each, to `row_dst(row's index in the item) + offset`
+                auto flush = [&](auto row_dst) {
+                    __syncwarp();
 #pragma unroll
-                for (int y = 0; y < CHUNKS; ++y) {
-                    const int r = y * (32 / CHUNKS) + lane / CHUNKS, x = lane % CHUNKS;
-                    const int rr = (warp & 3) * 32 + r, rt = (rr * inv_g) >> 16;
-                    if (rt < rows_of(t))
-                        *reinterpret_cast<uint4*>(row_dst(it.row0 + first_of(t) + rt, it.kvh * G + rr - rt * G) + x * 16) =
-                            *reinterpret_cast<const uint4*>(stage + r * TURN + ((x ^ (r & (CHUNKS - 1))) * 16));
-                }
-                __syncwarp();
-            };
-            if (p.ws_ml != nullptr) {
-                const int64_t share = static_cast<int64_t>(blockIdx.y) * p.num_tokens;
-                if (mine && half == 0) reinterpret_cast<float2*>(p.ws_ml)[(share + at) * p.num_q_heads + h] = make_float2(m, l);
-                if (cnt > 0) {
+                    for (int y = 0; y < CHUNKS; ++y) {
+                        const int r = y * (32 / CHUNKS) + lane / CHUNKS, x = lane % CHUNKS;
+                        const int rr = (warp & 3) * 32 + r, rt = (rr * inv_g) >> 16;
+                        if (rt < rows_of(t))
+                            *reinterpret_cast<uint4*>(row_dst(it.row0 + first_of(t) + rt, it.kvh * G + rr - rt * G) + x * 16) =
+                                *reinterpret_cast<const uint4*>(stage + r * TURN + ((x ^ (r & (CHUNKS - 1))) * 16));
+                    }
+                    __syncwarp();
+                };
+                if (p.ws_ml != nullptr) {
+                    const int64_t share = static_cast<int64_t>(blockIdx.y) * p.num_tokens;
+                    if (mine && half == 0) reinterpret_cast<float2*>(p.ws_ml)[(share + at) * p.num_q_heads + h] = make_float2(m, l);
+                    if (cnt > 0) {
+#pragma unroll
+                        for (int k = 0; k < D / 2; k += 32) {
+                            float o[32];
+                            load_o(k, o);
+#pragma unroll
+                            for (int y = 0; y < 32; y += TURN / 4) {
+#pragma unroll
+                                for (int x = 0; x < CHUNKS; ++x)
+                                    put(x, make_uint4(__float_as_uint(o[y + 4 * x] * vt), __float_as_uint(o[y + 4 * x + 1] * vt),
+                                                      __float_as_uint(o[y + 4 * x + 2] * vt), __float_as_uint(o[y + 4 * x + 3] * vt)));
+                                flush([&](int64_t r, int head) {
+                                    return reinterpret_cast<unsigned char*>(
+                                        p.ws_o + ((share + r) * p.num_q_heads + head) * D + half * (D / 2) + k + y);
+                                });
+                            }
+                        }
+                    }
+                } else {
+                    const float inv = vt / l;
 #pragma unroll
                     for (int k = 0; k < D / 2; k += 32) {
                         float o[32];
                         load_o(k, o);
 #pragma unroll
-                        for (int y = 0; y < 32; y += TURN / 4) {
-#pragma unroll
-                            for (int x = 0; x < CHUNKS; ++x)
-                                put(x, make_uint4(__float_as_uint(o[y + 4 * x] * vt), __float_as_uint(o[y + 4 * x + 1] * vt),
-                                                  __float_as_uint(o[y + 4 * x + 2] * vt), __float_as_uint(o[y + 4 * x + 3] * vt)));
+                        for (int x = 0; x < 4; ++x)
+                            put((k / 8 + x) % CHUNKS, make_uint4(pack_act<ACT>(o[8 * x] * inv, o[8 * x + 1] * inv),
+                                                                 pack_act<ACT>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
+                                                                 pack_act<ACT>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
+                                                                 pack_act<ACT>(o[8 * x + 6] * inv, o[8 * x + 7] * inv)));
+                        if ((k + 32) % (TURN / 2) == 0)
                             flush([&](int64_t r, int head) {
-                                return reinterpret_cast<unsigned char*>(
-                                    p.ws_o + ((share + r) * p.num_q_heads + head) * D + half * (D / 2) + k + y);
+                                return reinterpret_cast<unsigned char*>(static_cast<uint16_t*>(p.out) + r * p.out_stride +
+                                                                        static_cast<int64_t>(head) * D + half * (D / 2) + (k + 32 - TURN / 2));
                             });
-                        }
                     }
                 }
-            } else {
-                const float inv = vt / l;
-#pragma unroll
-                for (int k = 0; k < D / 2; k += 32) {
-                    float o[32];
-                    load_o(k, o);
-#pragma unroll
-                    for (int x = 0; x < 4; ++x)
-                        put((k / 8 + x) % CHUNKS, make_uint4(pack_act<ACT>(o[8 * x] * inv, o[8 * x + 1] * inv),
-                                                             pack_act<ACT>(o[8 * x + 2] * inv, o[8 * x + 3] * inv),
-                                                             pack_act<ACT>(o[8 * x + 4] * inv, o[8 * x + 5] * inv),
-                                                             pack_act<ACT>(o[8 * x + 6] * inv, o[8 * x + 7] * inv)));
-                    if ((k + 32) % (TURN / 2) == 0)
-                        flush([&](int64_t r, int head) {
-                            return reinterpret_cast<unsigned char*>(static_cast<uint16_t*>(p.out) + r * p.out_stride +
-                                                                    static_cast<int64_t>(head) * D + half * (D / 2) + (k + 32 - TURN / 2));
-                        });
-                }
-            }
             }
         }
     } else if (warp == 19) {
@@ -1051,7 +1051,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                         for (int x = 0; x < W; ++x) acc[x] *= f;
                         m = d;
                     }
-                    const float w = fast_exp2(d - m);
+                    const float w = d == -INFINITY ? 0.f : fast_exp2(d - m);
                     l += w;
                     const float wv = w * (SCALED ? p.v_scale[tile] : vt);
 #pragma unroll

@@ -394,3 +394,132 @@ def test_bounded_cache_together(pkv_lib):
         want, _, tol = ref.attend(paged, 0, qi[0], seen, scale)
         rows = slice(h * hq // hkv, (h + 1) * hq // hkv)
         ref.check(out[0, rows], want[rows], tol[rows])
+
+
+# --------------------------------------------------------------------------- sizes and values at the edge
+@pytest.mark.parametrize("scale", [0.0, -0.11])
+@pytest.mark.parametrize("cache", ["act", "e4m3", "scaled"])
+def test_chunk_scale_of_any_sign(pkv_lib, cache, scale):
+    paged = ref.Paged([300, 20], 2, 16, 128, BF16, cache, seed=11)
+    q = torch.randn(153, 8, 128, generator=torch.Generator().manual_seed(12)).to(BF16)
+    want, tol = chunk_ref(paged, q, [0, 150, 153], scale)
+    ref.check(run_chunk(pkv_lib, paged, q, [0, 150, 153], scale), want, tol)
+
+
+@pytest.mark.parametrize("bad_v", [False, True], ids=["V finite", "V not finite"])
+def test_chunk_logits_of_minus_infinity(pkv_lib, bad_v):
+    """Tokens whose logits are -inf weigh nothing, the first ones of a row among them."""
+    paged = ref.Paged([200], 2, 16, 64, F16, seed=13)
+    q = torch.randn(170, 4, 64, generator=torch.Generator().manual_seed(14)).to(F16)
+    q[..., 3] = q[..., 3].abs() + 0.01
+    for j in list(range(20)) + [40, 100]:
+        blk, off = paged.slot(0, j)
+        paged.k[blk, :, off, 3] = -float("inf")
+    want, tol = chunk_ref(paged, q, [0, 170], 0.125)
+    tol = torch.nan_to_num(tol, nan=1.0, posinf=1.0)  # (the magnitudes' sums are infinite)
+    sums = torch.zeros_like(want)  # so they are taken over the tokens that weigh something
+    for i in range(170):
+        js = [j for j in range(30 + i + 1) if j >= 20 and j not in (40, 100)]
+        sums[i], _, tol[i] = ref.attend(paged, 0, q[i], js, 0.125)
+    assert torch.equal(torch.isfinite(want), torch.ones_like(want, dtype=torch.bool))
+    sees = torch.zeros(170, dtype=torch.bool)
+    if bad_v:
+        blk, off = paged.slot(0, 150)
+        paged.v[blk, :, off] = float("nan")
+        sees = torch.arange(170) + 30 >= 150
+    got = run_chunk(pkv_lib, paged, q, [0, 170], 0.125).cpu()
+    ref.check(got[~sees], sums[~sees], tol[~sees])
+    assert not torch.isfinite(got[sees]).any()
+
+
+def test_chunk_rows_do_not_see_later_scales(pkv_lib):
+    """A block whose scales are no numbers reaches the rows that see it alone."""
+    paged = ref.Paged([300], 2, 16, 128, BF16, "scaled", seed=5)
+    q = torch.randn(260, 4, 128, generator=torch.Generator().manual_seed(6)).to(BF16)
+    want, tol = chunk_ref(paged, q, [0, 260], 0.09)
+    blk, _ = paged.slot(0, 176)
+    sees = torch.arange(260) + 40 >= 176
+    for value in (float("inf"), float("nan")):
+        for scales in (paged.v_scales, paged.k_scales):
+            old = scales[blk].clone()
+            scales[blk] = value
+            got = run_chunk(pkv_lib, paged, q, [0, 260], 0.09).cpu()
+            scales[blk] = old
+            ref.check(got[~sees], want[~sees], tol[~sees], "rows that do not see it")
+
+
+@pytest.mark.parametrize("hq,hkv,dim", [(8, 2, 128), (8, 2, 64), (2, 2, 64)])
+def test_scored_many_rows(pkv_lib, hq, hkv, dim):
+    """More sequences than one tensor-core launch takes."""
+    lens = [(37 * i) % 200 for i in range(600)]
+    paged = ref.Paged(lens, hkv, 16, dim, BF16, seed=21)
+    q = torch.randn(600, hq, dim, generator=torch.Generator().manual_seed(22)).to(BF16)
+    args, _ = paged.cuda()
+    tokens = paged.tables.shape[1] * 16
+    scores = torch.zeros(600, hkv, tokens).cuda()
+    out = pkv_lib.paged_attention_decode_scored(q.cuda(), *args, 0.1, scores, partition_size=64)
+    want, tol = torch.zeros(q.shape, dtype=torch.float64), torch.full(q.shape, 1e-9, dtype=torch.float64)
+    sums = torch.zeros(scores.shape, dtype=torch.float64)
+    for b, n in enumerate(lens):
+        if n:
+            want[b], p, tol[b] = ref.attend(paged, b, q[b], list(range(n)), 0.1)
+            sums[b, :, :n] = p.view(hkv, hq // hkv, n).sum(1)
+    ref.check(out, want, tol, "scored")
+    ref.check(scores, sums, 2.0 ** -10 * sums + 2.0 ** -20 * (1 + sums), "scores")  # as in test_scored
+
+
+@pytest.mark.parametrize("cache", ["act", "e4m3", "scaled"])
+def test_blocks_past_32_bits(pkv_lib, cache):
+    """Pools whose last blocks lie behind 2^32 elements: what the same blocks at the front give, bit for bit."""
+    hkv, bs, dim = 8, 32, 128
+    paged = ref.Paged([700, 61], hkv, bs, dim, BF16, cache, seed=31, extra_blocks=8)
+    q = torch.randn(90, 4 * hkv, dim, generator=torch.Generator().manual_seed(32)).to(BF16).cuda()
+    (k, v, tables, lens), scales = paged.cuda()
+    blocks = 2 ** 32 // (hkv * bs * dim) + 64
+    shift = blocks - k.shape[0]
+    K, V = (torch.empty((blocks, *k.shape[1:]), dtype=k.dtype, device="cuda") for _ in range(2))
+    K[shift:], V[shift:] = k, v
+    far = torch.where(tables >= 0, tables + shift, tables)
+    Scales = dict(scales)
+    for name in ("k_scales", "v_scales"):
+        if scales[name] is not None:
+            Scales[name] = torch.ones(blocks, hkv, device="cuda")
+            Scales[name][shift:] = scales[name]
+    starts = torch.tensor([0, 80, 90], dtype=torch.int32).cuda()
+    a, b = (pkv_lib.paged_attention_chunk(q, *pools, lens, starts, 0.09, **s)
+            for pools, s in (((k, v, tables), scales), ((K, V, far), Scales)))
+    assert torch.equal(a, b)
+    a, b = (pkv_lib.paged_attention_decode_window(q[:2], *pools, lens, 0.09, 300, sinks=5, **s)
+            for pools, s in (((k, v, tables), scales), ((K, V, far), Scales)))
+    assert torch.equal(a, b)
+    if cache == "scaled":
+        return
+    one = {n: scales[n] for n in ("k_scale", "v_scale")}
+    sums = [torch.zeros(2, hkv, tables.shape[1] * bs).cuda() for _ in range(2)]
+    a, b = (pkv_lib.paged_attention_decode_scored(q[:2], *pools, lens, 0.09, s, **one)
+            for pools, s in zip(((k, v, tables), (K, V, far)), sums))
+    assert torch.equal(a, b) and torch.equal(*sums)
+    dst = paged.free[:8].view(2, 4).to(torch.int32).cuda()
+    a = pkv_lib.paged_kv_evict(k, v, sums[0], tables, lens, dst, 128, 32, sinks=4)
+    b = pkv_lib.paged_kv_evict(K, V, sums[1], far, lens, dst + shift, 128, 32, sinks=4)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    bits = torch.uint8 if cache != "act" else torch.int16
+    assert torch.equal(k.view(bits), K[shift:].view(bits)) and torch.equal(v.view(bits), V[shift:].view(bits))
+
+
+def test_no_rows(pkv_lib):
+    """Calls over no sequences and over no tokens do nothing."""
+    paged = ref.Paged([20], 2, 16, 64, F16)
+    (k, v, tables, lens), _ = paged.cuda()
+    none, empty = tables[:0], lens[:0]
+    q = torch.empty(0, 4, 64, dtype=F16, device="cuda")
+    assert pkv_lib.paged_attention_chunk(q, k, v, tables, lens, torch.zeros(2, dtype=torch.int32).cuda(), 1.0).shape == q.shape
+    assert pkv_lib.paged_attention_chunk(q, k, v, none, empty, torch.zeros(1, dtype=torch.int32).cuda(), 1.0).shape == q.shape
+    out = torch.full((3, 4, 64), 2.0, dtype=F16).cuda()
+    rows = torch.zeros(3, 4, 64, dtype=F16).cuda()
+    pkv_lib.paged_attention_chunk(rows, k, v, tables, lens, torch.zeros(2, dtype=torch.int32).cuda(), 1.0, out=out)
+    assert torch.all(out == 2.0)
+    assert pkv_lib.paged_attention_decode_window(q, k, v, none, empty, 1.0, 5).shape == q.shape
+    scores = torch.zeros(0, 2, tables.shape[1] * 16).cuda()
+    assert pkv_lib.paged_attention_decode_scored(q, k, v, none, empty, 1.0, scores).shape == q.shape
+    assert pkv_lib.paged_kv_evict(k, v, scores, none, empty, none, 4, 1).kept.shape == (0, 2, 4)
