@@ -70,7 +70,6 @@ extern "C" {
 static bool rows_overlap(const void* a, int64_t a_stride, int64_t a_row, const void* b, int64_t b_stride, int64_t b_row,
                          int num_tokens);
 
-
 const char* pkv_last_error(void) { return t_last_error.c_str(); }
 
 int pkv_version(void) { return 100; }
@@ -392,6 +391,17 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         return fail(PKV_ERR_INVALID, F + ": " + "workspace of " + std::to_string(need) + " bytes required (" +
                                          (scored ? "pkv_scored_workspace_size)" : ext ? "pkv_window_workspace_size)"
                                           : block_scales ? "pkv_scaled_workspace_size)" : "pkv_workspace_size)"));
+    if (scored) {  // written, the scores read and written by different blocks
+        const auto at = reinterpret_cast<uintptr_t>(ext->scores);
+        const size_t B = num_seqs, rows = 2 * B * num_q_heads * head_dim;
+        const uintptr_t end = at + sizeof(float) * B * num_kv_heads * ext->score_tokens;
+        const struct { const void* at; size_t bytes; } others[] = {
+            {q, rows}, {out, rows}, {context_lens, 4 * B}, {block_tables, 4 * B * max_blocks_per_seq}, {workspace, need}};
+        for (const auto& o : others) {
+            const auto x = reinterpret_cast<uintptr_t>(o.at);
+            if (x < end && at < x + o.bytes) return fail(PKV_ERR_INVALID, F + ": " + "scores must be a buffer of its own");
+        }
+    }
     int* err = device_error_word();
     if (!err) return fail(PKV_ERR_CUDA, F + ": " + "cannot resolve the device error word");
 
@@ -472,7 +482,7 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     const bool use_tc = path == PKV_PATH_TENSOR || path == PKV_PATH_TENSOR_2CTA ||
                         (path == PKV_PATH_AUTO && tc_ok && !small && (G >= 4 || block_scales));
     if (use_tc) {
-        const int chunk = (ext ? decode_tc_ext_max_rows() : decode_tc_max_rows()) / rows_per_seq;
+        const int chunk = (ext ? decode_tc_ext_max_rows(head_dim, kind) : decode_tc_max_rows()) / rows_per_seq;
         const size_t act_bytes = 2;
         e = cudaSuccess;
         for (int s0 = 0; s0 < num_seqs && e == cudaSuccess; s0 += chunk) {

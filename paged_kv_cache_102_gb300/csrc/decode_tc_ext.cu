@@ -1,12 +1,12 @@
 // Tensor-core decode with a window or kept logits over 16-bit caches: kernel
 // instantiations and their launch (E4M3 caches: decode_tc_ext_e4m3.cu and
 // decode_tc_ext_e4m3b.cu).  One ring depth each, two CTAs per SM: the API calls
-// with at most kTcExtRows sequences, whose tables leave room for it.
+// with at most decode_tc_ext_max_rows sequences, whose tables leave room for it.
 #include "decode_tc_host.cuh"
 
 namespace pkv {
 
-int decode_tc_ext_max_rows() { return kTcExtRows; }
+int decode_tc_ext_max_rows(int head_dim, int cache) { return head_dim == 64 && !is_e4m3(cache) ? kTcMaxSeqs : kTcExtRows; }
 
 namespace {
 

@@ -64,7 +64,7 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorM
                    int ctas_per_sm, cudaStream_t s) {
     auto kern = paged_decode_tc_kernel<ACT, CACHE, BS, G, NS, PAIR, HALF, EXT>;
     using Smem = TcSmem<NS, is_e4m3(CACHE) ? kTcStage8 : kTcStage, PAIR, CACHE == kE4M3B, HALF, tc_p_columns(CACHE, G), EXT>;
-    static_assert(!EXT || 2 * (Smem::alloc(kTcExtRows) + 1024) <= kTcSmemPerSm, "two CTAs per SM");
+    static_assert(!EXT || 2 * (Smem::alloc(PAIR ? kTcMaxSeqs : kTcExtRows) + 1024) <= kTcSmemPerSm, "two CTAs per SM");
     constexpr int threads = kTcThreads;
     const int rows = p.table_kvh_stride != 0 ? p.num_seqs * p.num_kv_heads : p.num_seqs;
     const int smem = Smem::alloc(rows);

@@ -360,7 +360,7 @@ cudaError_t launch_decode_tc_e4m3b_d64(const DecodeParams& p, int act, int BS, i
 cudaError_t launch_decode_tc_d64(const DecodeParams& p, int act, int BS, int G, int variant, cudaStream_t s);
 
 // The same with a window or kept logits (tables shared by a sequence's kv heads).
-int decode_tc_ext_max_rows();
+int decode_tc_ext_max_rows(int head_dim, int cache);
 cudaError_t launch_decode_tc_ext(const DecodeParams& p, int act, int cache, int head_dim, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_tc_ext_e4m3(const DecodeParams& p, int act, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_tc_ext_e4m3b(const DecodeParams& p, int act, int head_dim, int BS, int G, cudaStream_t s);

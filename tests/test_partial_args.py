@@ -66,6 +66,10 @@ def test_scored_refusals(pkv_lib):
     assert _scored(lib, n=63) == 1 and _scored(lib, scores=None) == 1 and _scored(lib, scores=A + 2) == 1
     assert _scored(lib, Hq=24) == 1 and _scored(lib, cache=2) == 1 and _scored(lib, part=48) == 1
     assert _scored(lib, B=0) == 0
+    apart = dict(q=A << 1, tables=A << 2, lens=A << 3, scores=A << 4, out=A << 5, ws=A << 6, wsb=1 << 30)
+    for name in ("q", "tables", "lens", "out", "ws"):
+        assert _scored(lib, **{**apart, name: (A << 4) + 1024}) == 1, name
+        assert "buffer of its own" in lib.pkv_last_error().decode(), name
 
 
 def _evict(lib, **kw):
