@@ -459,8 +459,8 @@ size_t pkv_window_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads
  * to scores (float32 [num_seqs][num_kv_heads][score_tokens], score_tokens >=
  * max_blocks_per_seq * block_size): scores[b][h][j] += sum_g p_g[j] for j <
  * context_lens[b], the others stay.  What paged_kv_evict goes by.  One thread
- * adds a token's weight, in a fixed order.  A context length of 0 gives zeros
- * and adds nothing.  Not for block-scaled caches.  The workspace,
+ * adds a token's weight, in a fixed order.  scores share no memory with another
+ * buffer.  A context length of 0 gives zeros and adds nothing.  Not for block-scaled caches.  The workspace,
  * pkv_scored_workspace_size bytes, holds the step's logits (4 bytes for each
  * query head and token of the tables).
  */
