@@ -550,7 +550,12 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                         for (int j = 0; j < 8; ++j) o[j] *= f;
                         tc::tmem_st<8>(o_addr + k, o);
                     }
+                    tc::tmem_wait_st();
+                    tc::fence_before_sync();
                 }
+                // The product with the first half's weights adds to all of the row, so these are not announced before
+                // both halves of it are multiplied.
+                pair_any(pair, false);
             }
             const float ref = m == -INFINITY ? 0.f : m;  // nothing seen yet: weights of 0
             [[maybe_unused]] const float lift = SCALED && unit != -INFINITY ? fast_exp2(ref - unit) : 0.f;

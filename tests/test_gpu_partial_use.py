@@ -149,6 +149,28 @@ def test_chunk_runs_again_the_same(pkv):
         assert torch.equal(pkv.paged_attention_chunk(q, *args, starts, 0.09), want)
 
 
+@pytest.mark.parametrize("cache,dim,factor", [("act", 64, 1.0), ("act", 64, 1.5), ("act", 128, 1.0), ("act", 128, 1.5),
+                                              ("scaled", 64, 1.0), ("scaled", 128, 1.0), ("act", 64, 4.0)])
+def test_chunk_references_that_move(pkv, cache, dim, factor):
+    """Rows whose first tile, four tokens in front of the window, has far smaller logits than the window, so that what
+    they summed up is multiplied when their reference moves, in few of many rows or (factor 4) in most: the same bits
+    every time, and the right ones."""
+    n, hq, hkv = 3000, 32, 32
+    paged = ref.Paged([n, n], hkv, 16, dim, F16, cache, seed=41)
+    q = (factor * torch.randn(2 * n, hq, dim, generator=torch.Generator().manual_seed(42))).to(F16)
+    args, scales = paged.cuda()
+    starts = torch.tensor([0, n, 2 * n], dtype=torch.int32).cuda()
+    dev, scale = q.cuda(), dim ** -0.5
+    run = lambda: pkv.paged_attention_chunk(dev, *args, starts, scale, window=300, sinks=4, **scales)  # noqa: E731
+    first = run()
+    differing = sum(not torch.equal(run(), first) for _ in range(300))
+    assert differing == 0
+    for r in range(310, 2 * n, 373):
+        b, pos = divmod(r, n)
+        want, _, tol = ref.attend(paged, b, q[r], ref.visible(pos, 300, 4), scale)
+        ref.check(first[r], want, tol)
+
+
 @pytest.mark.parametrize("kind", ["16-bit", "block scales"])
 def test_cache_prompts_windows_and_drafts(pkv, kind):
     """PagedKVCache: a prompt appended token by token, its chunk attention in two parts, drafts, windowed steps."""
