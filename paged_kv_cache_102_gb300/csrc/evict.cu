@@ -14,9 +14,10 @@
 // a token, its place is g + min(e, equal ones that stay); g and e come from one
 // packed scan.
 // A small budget's rows move in the same kernel, by the block that chose them.
-// Measured: 4 sequences of 270 tokens, 8 heads of 64, to 256: 8.0 us, of which a launch 2.5 and dependent passes over
-// shared memory the rest (two launches 11.4); 16 of 4096 to 8192 tokens, 8 heads of 128, to 2048: 58 us, a third of it the
-// selection (a block an SM, 128 blocks), the rest the move at about 5.5 TB/s.
+// Measured: 4 sequences of 270 tokens, 8 heads of 64, to 256: 8.0 us, a launch and a
+// dozen dependent passes over shared memory (11.4 with two launches); 16 of 4096 to
+// 8192 tokens, 8 heads of 128, to 2048: selection 13 us, bound by its passes too (a
+// block an SM, 128 blocks), the move 43, 268 MB at 6.2 TB/s.
 // evict_move_kernel: 16 bytes a thread, kept rows of K and V to their new
 // blocks; source and destination blocks differ, so that rows are independent.
 #include "kernels.h"
@@ -33,6 +34,8 @@ constexpr int kKeyTokens = 48 * 1024;
 constexpr int kMoveThreads = 256;
 constexpr int kMoveHere = 64 * 1024;  // bytes of K that the selecting block moves itself
 constexpr int kAddThreads = 256;
+constexpr int kAddEach = 2;  // tokens a thread
+constexpr int kAddTokens = kAddThreads * kAddEach;
 
 // 32-bit key of the scores' order: NaN 0, then -inf .. +inf (-0 as 0).
 __device__ __forceinline__ uint32_t score_key(float x) {
@@ -208,34 +211,45 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
     if (from >= 0 && !move_chunk(p, b, h, from, i, c, vecs)) atomicOr(p.err, kErrBadBlock);
 }
 
-// What is left once every partition is there, for 256 tokens of a (sequence, kv
+// What is left once every partition is there, for 512 tokens of a (sequence, kv
 // head) a block: scores += sum over the group's heads of 2^(logit - M) / l, one
-// thread a token, (M, l) the statistics of the head's partitions joined; and a
+// thread for every two tokens, (M, l) the statistics of the head's partitions joined; and a
 // share of the output's elements, where there are partitions to join (as the
-// merge kernel would: sum_i w_i o_i / l with w_i = l_i 2^(m_i - M)).
+// merge kernel would: sum_i w_i o_i / l with w_i = l_i 2^(m_i - M)).  Bound by
+// the chain of loads of a block; 1, 2 or 4 tokens a thread: 122.5, 119.5 and
+// 120.9 us for the call over 64 sequences of up to 4096 tokens, 64 / 8 heads (the
+// decode before it 108 by itself, its K and V 80 at the copy's rate).
 template <int ACT, int D>
 __global__ void __launch_bounds__(kAddThreads) scored_finish_kernel(const AddWeightsParams p) {
     __shared__ float s_max[8], s_inv[8];
     const int seq = blockIdx.z, kvh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int L = p.context_lens[seq];
     if (L < 1 || L > p.max_context) return;  // flagged before
-    const int64_t first = static_cast<int64_t>(blockIdx.x) * kAddThreads;
+    const int64_t first = static_cast<int64_t>(blockIdx.x) * kAddTokens;
     if (first >= L) return;
     const int parts = (L + p.partition_size - 1) / p.partition_size;
-    const int64_t row = static_cast<int64_t>(seq) * p.num_kv_heads + kvh, t = first + threadIdx.x;
-    const float before = t < L ? p.scores[row * p.score_tokens + t] : 0.f;  // not written by the kernel before
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const float* x = p.logits + (row * p.logit_tokens + t) * p.group;
-    float logit[8];
-    if (p.group % 4 == 0) {  // (a token's logits are together)
-        const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-        const float4 a = t < L ? reinterpret_cast<const float4*>(x)[0] : none;
-        const float4 b = t < L && p.group == 8 ? reinterpret_cast<const float4*>(x)[1] : none;
-        logit[0] = a.x, logit[1] = a.y, logit[2] = a.z, logit[3] = a.w;
-        logit[4] = b.x, logit[5] = b.y, logit[6] = b.z, logit[7] = b.w;
-    } else {
+    const int64_t row = static_cast<int64_t>(seq) * p.num_kv_heads + kvh;
+    float before[kAddEach], logit[kAddEach][8];
 #pragma unroll
-        for (int g = 0; g < 8; ++g) logit[g] = t < L && g < p.group ? x[g] : -INFINITY;
+    for (int y = 0; y < kAddEach; ++y) {  // not written by the kernel before
+        const int64_t t = first + y * kAddThreads + threadIdx.x;
+        before[y] = t < L ? p.scores[row * p.score_tokens + t] : 0.f;
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+#pragma unroll
+    for (int y = 0; y < kAddEach; ++y) {
+        const int64_t t = first + y * kAddThreads + threadIdx.x;
+        const float* x = p.logits + (row * p.logit_tokens + t) * p.group;
+        if (p.group % 4 == 0) {  // (a token's logits are together)
+            const float4 none = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+            const float4 a = t < L ? reinterpret_cast<const float4*>(x)[0] : none;
+            const float4 b = t < L && p.group == 8 ? reinterpret_cast<const float4*>(x)[1] : none;
+            logit[y][0] = a.x, logit[y][1] = a.y, logit[y][2] = a.z, logit[y][3] = a.w;
+            logit[y][4] = b.x, logit[y][5] = b.y, logit[y][6] = b.z, logit[y][7] = b.w;
+        } else {
+#pragma unroll
+            for (int g = 0; g < 8; ++g) logit[y][g] = t < L && g < p.group ? x[g] : -INFINITY;
+        }
     }
     const float2* stats = reinterpret_cast<const float2*>(p.ws_ml) + row * p.group * p.max_parts;
     if (warp < p.group) {
@@ -254,15 +268,18 @@ __global__ void __launch_bounds__(kAddThreads) scored_finish_kernel(const AddWei
         }
     }
     __syncthreads();
-    if (t < L) {
+#pragma unroll
+    for (int y = 0; y < kAddEach; ++y) {
+        const int64_t t = first + y * kAddThreads + threadIdx.x;
+        if (t >= L) break;
         float sum = 0.f;
 #pragma unroll
         for (int g = 0; g < 8; ++g)
-            if (g < p.group) sum += fast_exp2(logit[g] - s_max[g]) * s_inv[g];
-        p.scores[row * p.score_tokens + t] = before + sum;
+            if (g < p.group) sum += fast_exp2(logit[y][g] - s_max[g]) * s_inv[g];
+        p.scores[row * p.score_tokens + t] = before[y] + sum;
     }
     if (parts == 1) return;
-    const int blocks = (L + kAddThreads - 1) / kAddThreads, each = (p.group * D + blocks - 1) / blocks;
+    const int blocks = (L + kAddTokens - 1) / kAddTokens, each = (p.group * D + blocks - 1) / blocks;
     const int end = min(p.group * D, static_cast<int>(blockIdx.x + 1) * each);
     for (int e = blockIdx.x * each + threadIdx.x; e < end; e += kAddThreads) {
         const int g = e / D, d = e % D;
@@ -321,7 +338,7 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_scored_finish(const AddWeightsParams& p, int act, int head_dim, cudaStream_t stream) {
-    const dim3 grid((p.max_context + kAddThreads - 1) / kAddThreads, p.num_kv_heads, p.num_seqs);
+    const dim3 grid((p.max_context + kAddTokens - 1) / kAddTokens, p.num_kv_heads, p.num_seqs);
     auto kernel = head_dim == 64 ? (act == kBF16 ? scored_finish_kernel<kBF16, 64> : scored_finish_kernel<kF16, 64>)
                                  : (act == kBF16 ? scored_finish_kernel<kBF16, 128> : scored_finish_kernel<kF16, 128>);
     return launch_after(kernel, p, grid, kAddThreads, stream);
