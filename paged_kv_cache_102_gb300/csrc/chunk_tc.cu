@@ -136,8 +136,9 @@ cudaError_t launch_one(const ChunkParams& p, cudaStream_t s) {
 
 // The sequences are taken to be alike, as long as the tables: items of `tiles` token tiles in waves of an SM each, 6
 // tiles' time for the start and end of a block, and for the partial results to be written and read.  Measured, us, shares
-// 1 / 2 / 3 / 4: 16 sequences of 5 new tokens, 128 items of 1 to 32 tiles, 45.1 / 49.6 / 47.9 / 54.5; 4 of them, 32 items,
-// 32.2 / 23.4 / 19.8 / 19.4; 48 single tokens and three parts of prompts, 408 items, 147 / 194 / 224 / 255.
+// 1 / 2 / 3 / 4: 16 sequences of 5 new tokens, 128 items of 1 to 32 tiles, 41.2 / 47.1 / 47.0 / 52.4 (all of 32 tiles 51.6 /
+// 65.2 / 72.2 / 78.8); 4 of them, 32 items, 28.9 / 21.7 / 19.9 / 19.2; 509 tokens behind 32K, 64 items of 256 tiles, 443 /
+// 238 / 314 / 249; one single token there, 8 items, 235 / 125 / 88 / 70, and 41 with the 19 shares that this takes.
 int chunk_splits(int num_seqs, int num_tokens, int num_q_heads, int num_kv_heads, int64_t max_context) {
     const int R = 2 * std::max(1, kChunkTile / (num_q_heads / num_kv_heads));
     const int64_t each = (static_cast<int64_t>(num_tokens) + num_seqs - 1) / num_seqs;
