@@ -493,6 +493,9 @@ size_t pkv_scored_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads
  *  context_lens_out int32 [num_seqs] (written): min(L, budget).
  *  kept           int32 [num_seqs][num_kv_heads][budget] (written): the tokens
  *                 that stayed, -1 behind them.
+ * Keys move as they are: rotary ones keep the rotation of their old positions,
+ * so the next token's position is still L (pkv_bm_set_dropped; the caller's to
+ * count otherwise).  Lengths, tables and windows count the tokens that are held.
  * Written buffers share no memory with any other.  sinks + recent <= budget;
  * head_dim 64 or 128.  Not for block-scaled caches (a token's codes mean
  * nothing under another block's scale).  A length outside 0 ..
@@ -537,7 +540,10 @@ int paged_kv_evict(void* k_cache, void* v_cache, int num_blocks, int num_kv_head
  *                 requests' in order, fill the first of them, and the rest get
  *                 slot -1 and position -1 (padding to the other calls).
  *  slot_mapping   int64 [num_tokens] (written; 16-byte aligned).
- *  positions      int32 [num_tokens] (written; 16-byte aligned).
+ *  positions      int32 [num_tokens] (written; 16-byte aligned): places in the
+ *                 cache, c, c + 1, ...  Where tokens of a request were evicted
+ *                 (paged_kv_evict), add how many to its rows before they go to
+ *                 paged_rope_append.
  *  seq_starts     int32 [num_seqs + 1] (written): first token of each request.
  *  block_starts   int32 [num_seqs + 1] (written): new blocks before each request.
  *  context_lens_out int32 [num_seqs] (written): c + n; may be context_lens.
@@ -809,6 +815,12 @@ int pkv_bm_num_free(const pkv_block_manager* bm);
 int pkv_bm_ref_count(const pkv_block_manager* bm, int block); /* -1 if out of range */
 int pkv_bm_context_len(const pkv_block_manager* bm, int64_t seq_id); /* -1 if unknown */
 int pkv_bm_num_seq_blocks(const pkv_block_manager* bm, int64_t seq_id); /* -1 if unknown */
+/* Tokens of a sequence that came before and are no longer in the cache (0 until
+ * set; forks inherit it, -1 if unknown): after an eviction the position of its
+ * token at place i, as rotary positions count, is i + dropped for every token
+ * appended since.  PagedKVCache sets it; tables and lengths do not change. */
+int pkv_bm_set_dropped(pkv_block_manager* bm, int64_t seq_id, int num_dropped);
+int pkv_bm_num_dropped(const pkv_block_manager* bm, int64_t seq_id);
 /* Copy the free list, in pop order, into out (capacity cap); returns its length. */
 int pkv_bm_free_list(const pkv_block_manager* bm, int32_t* out, int cap);
 

@@ -890,7 +890,8 @@ def paged_kv_evict(k_cache, v_cache, scores, block_tables, context_lens, dst_tab
     stay, in their order, and move to the blocks of dst_tables int32 [B, max_dst_blocks], which hold nothing else yet
     (a new sequence's of the BlockManager; the old one can be freed after).  Returns the new lengths int32 [B], the
     scores that moved along (as wide as the old ones, zeros behind them) and the tokens that stayed, int32
-    [B, Hkv, budget], -1 behind them.  Not for block-scaled caches."""
+    [B, Hkv, budget], -1 behind them.  Keys keep the rotation of their old positions: the next token's is still the old
+    length, not the new one.  Not for block-scaled caches."""
     name = "paged_kv_evict"
     shape = k_cache.shape
     if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not k_cache.dtype:
@@ -1141,6 +1142,14 @@ class BlockManager:
 
     def num_seq_blocks(self, seq_id: int) -> int:
         return int(_native.lib().pkv_bm_num_seq_blocks(self._h, int(seq_id)))
+
+    def set_dropped(self, seq_id: int, num_dropped: int) -> None:
+        """Count num_dropped tokens before the sequence's that are no longer held (an eviction's)."""
+        self._check("pkv_bm_set_dropped", _native.lib().pkv_bm_set_dropped(self._h, int(seq_id), int(num_dropped)))
+
+    def num_dropped(self, seq_id: int) -> int:
+        """Tokens before the sequence's that are no longer held: its next token's position is context_len + num_dropped."""
+        return int(_native.lib().pkv_bm_num_dropped(self._h, int(seq_id)))
 
     def free_list(self) -> np.ndarray:
         n = int(_native.lib().pkv_bm_free_list(self._h, None, 0))

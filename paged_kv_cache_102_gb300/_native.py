@@ -84,6 +84,8 @@ SIGNATURES = {
     "pkv_bm_ref_count": (I32, [P, I32]),
     "pkv_bm_context_len": (I32, [P, I64]),
     "pkv_bm_num_seq_blocks": (I32, [P, I64]),
+    "pkv_bm_set_dropped": (I32, [P, I64, I32]),
+    "pkv_bm_num_dropped": (I32, [P, I64]),
     "pkv_bm_free_list": (I32, [P, P, I32]),
 }
 

@@ -91,10 +91,11 @@ class PagedKVCache:
         return slots, pairs
 
     def rope_append(self, seq_ids, q, k, v, inv_freq, interleaved=False, attention_factor=1.0, q_out=None, stream=None):
-        """append with rotary positions: rotate q [n, Hq, D] and k at each sequence's newest position and write k, v;
-        returns the rotated queries."""
+        """append with rotary positions: rotate q [n, Hq, D] and k at each sequence's newest position (evicted tokens
+        counted) and write k, v; returns the rotated queries."""
         slots, _ = self._reserve(seq_ids, stream)
-        positions = np.asarray([self.blocks.context_len(s) - 1 for s in np.asarray(seq_ids)], np.int32)
+        positions = np.asarray([self.blocks.context_len(s) + self.blocks.num_dropped(s) - 1 for s in np.asarray(seq_ids)],
+                               np.int32)
         return paged_rope_append(q, k, v, self._upload(positions, stream), self._upload(slots, stream), inv_freq,
                                  self.k_cache, self.v_cache, interleaved=interleaved,
                                  attention_factor=attention_factor, q_out=q_out, k_scale=self.k_scale,
@@ -153,7 +154,8 @@ class PagedKVCache:
 
     def evict(self, seq_ids, new_ids, scores: torch.Tensor, budget: int, recent: int, sinks=0, stream=None):
         """Replace each sequence by one of at most budget tokens under a new id: those that paged_kv_evict keeps, whose
-        result this returns.  The old sequences are freed (blocks that they share with others stay)."""
+        result this returns.  The old sequences are freed (blocks that they share with others stay).  Positions go on
+        from the old sequence's; a window counts the tokens that are held, not the ones between them that went."""
         if self.k_scales is not None:
             raise ValueError("PagedKVCache.evict: not for a block-scaled cache")
         seq_ids, new_ids = [int(s) for s in np.asarray(seq_ids)], [int(s) for s in np.asarray(new_ids)]
@@ -167,6 +169,8 @@ class PagedKVCache:
             for s, n in zip(new_ids, lens):
                 self.blocks.add_sequence(s, min(n, int(budget)))
                 added.append(s)
+            for s, old, n in zip(new_ids, seq_ids, lens):
+                self.blocks.set_dropped(s, self.blocks.num_dropped(old) + n - min(n, int(budget)))
             src, length = (self._upload(a, stream) for a in self.blocks.tables(seq_ids))
             dst = self._upload(self.blocks.tables(new_ids)[0], stream)
             got = paged_kv_evict(self.k_cache, self.v_cache, scores, src, length, dst, budget, recent, sinks=sinks,

@@ -47,6 +47,7 @@ namespace {
 struct Sequence {
     std::vector<int32_t> blocks;
     int64_t len = 0;
+    int64_t dropped = 0;   // tokens that came before and are no longer held: the next one's position is len + dropped
     bool swapped = false;  // contents staged outside the pool; no blocks held
     int64_t swap_group = -1;          // the group it was swapped out with
     std::vector<int32_t> staged_idx;  // while swapped: its table as positions in the group's staged list
@@ -499,6 +500,22 @@ int pkv_bm_context_len(const pkv_block_manager* bm, int64_t seq_id) {
     if (!bm) return -1;
     auto it = bm->seqs.find(seq_id);
     return it == bm->seqs.end() ? -1 : static_cast<int>(it->second.len);
+}
+
+int pkv_bm_set_dropped(pkv_block_manager* bm, int64_t seq_id, int num_dropped) {
+    if (!bm || num_dropped < 0) return pkv::fail(PKV_ERR_INVALID, "pkv_bm_set_dropped: bad arguments");
+    auto it = bm->seqs.find(seq_id);
+    if (it == bm->seqs.end()) return pkv::fail(PKV_ERR_NOT_FOUND, "pkv_bm_set_dropped: unknown id");
+    if (it->second.len + num_dropped > 0x7fffffff)
+        return pkv::fail(PKV_ERR_INVALID, "pkv_bm_set_dropped: positions past 2^31 - 1");
+    it->second.dropped = num_dropped;
+    return PKV_OK;
+}
+
+int pkv_bm_num_dropped(const pkv_block_manager* bm, int64_t seq_id) {
+    if (!bm) return -1;
+    auto it = bm->seqs.find(seq_id);
+    return it == bm->seqs.end() ? -1 : static_cast<int>(it->second.dropped);
 }
 
 int pkv_bm_num_seq_blocks(const pkv_block_manager* bm, int64_t seq_id) {

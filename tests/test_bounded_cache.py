@@ -1,0 +1,62 @@
+"""Caches of bounded size, the host's part (no GPU needed): what PagedKVCache and the block manager keep of a sequence
+whose tokens were evicted."""
+import numpy as np
+import pytest
+import torch
+
+from paged_kv_cache_102_gb300 import cache as cache_module
+
+
+@pytest.fixture
+def host_cache(pkv_lib, monkeypatch):
+    """A PagedKVCache of CPU pools whose device calls are noted instead of run."""
+    calls = []
+    for name in ("paged_kv_evict", "paged_rope_append", "paged_block_copy", "paged_kv_append"):
+        monkeypatch.setattr(cache_module, name, lambda *a, _name=name, **kw: calls.append((_name, a, kw)))
+    return cache_module.PagedKVCache(64, 1, 16, 64, dtype=torch.float16, device="cpu"), calls
+
+
+def test_manager_counts_dropped_tokens(pkv_lib):
+    bm = pkv_lib.BlockManager(16, 16)
+    bm.add_sequence(1, 20)
+    assert bm.num_dropped(1) == 0 and bm.num_dropped(9) == -1
+    bm.set_dropped(1, 5)
+    bm.fork(1, 2)
+    assert bm.num_dropped(2) == 5 and bm.context_len(2) == 20
+    bm.append_slots([1])
+    assert bm.num_dropped(1) == 5 and bm.context_len(1) == 21
+    bm.swap_out(1)
+    bm.swap_in(1, 4)
+    assert bm.num_dropped(1) == 5
+    bm.free_sequence(1)
+    bm.add_sequence(1, 3)
+    assert bm.num_dropped(1) == 0
+    for seq, n in ((7, 1), (1, -1), (1, 2 ** 31 - 3)):
+        with pytest.raises(pkv_lib.PagedKVError):
+            bm.set_dropped(seq, n)
+    bm.set_dropped(1, 2 ** 31 - 4)
+
+
+def test_positions_go_on_after_an_eviction(host_cache):
+    """Rotary positions count evicted tokens, after a second eviction and in a fork too."""
+    cache, calls = host_cache
+    cache.add_sequence(1, 100)
+    cache.add_sequence(2, 30)
+    scores = torch.zeros(2, 1, 128)
+
+    def positions(*ids):
+        calls.clear()
+        cache.rope_append(ids, None, None, None, None)
+        return [a[3].tolist() for name, a, _ in calls if name == "paged_rope_append"][0]
+
+    assert positions(1, 2) == [100, 30]
+    cache.evict([1, 2], [11, 12], scores, budget=40, recent=8)
+    assert cache.blocks.context_len(11) == 40 and cache.blocks.context_len(12) == 31
+    assert positions(11, 12) == [101, 31]
+    cache.fork(11, 21)
+    assert positions(21) == [102] and positions(11) == [102]
+    cache.evict([11], [31], scores[:1], budget=16, recent=8)
+    assert cache.blocks.context_len(31) == 16 and positions(31) == [103]
+    cache.free(31)
+    cache.add_sequence(31, 4)
+    assert positions(31) == [4]

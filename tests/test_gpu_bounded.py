@@ -1,0 +1,50 @@
+"""Caches of bounded size on the GPU: rotary positions across an eviction, and what follows a step that went wrong."""
+import numpy as np
+import pytest
+import torch
+
+from tests import partial_ref as ref
+
+pytestmark = pytest.mark.gpu
+F16, BF16 = torch.float16, torch.bfloat16
+
+
+@pytest.fixture
+def pkv(pkv_lib, cuda_device):
+    pkv_lib.device_error()
+    yield pkv_lib
+    assert pkv_lib.device_error() == 0
+
+
+def test_rotation_after_an_eviction(pkv):
+    """Tokens appended before and after an eviction are rotated by their positions in the text: the same queries and
+    attention as over a cache that holds every token and is asked for the ones that stayed."""
+    from paged_kv_cache_102_gb300.cache import PagedKVCache
+    hq, hkv, bs, dim, n, more, budget = 4, 2, 16, 64, 90, 20, 33
+    g = torch.Generator().manual_seed(5)
+    k, v, q = (torch.randn(n + more, h, dim, generator=g).to(F16).cuda() for h in (hkv, hkv, hq))
+    inv_freq, _ = pkv.rope_inv_freq(dim)
+    # every token, rotated by its position, at slot i
+    kc, vc = (torch.zeros(8, hkv, bs, dim, dtype=F16, device="cuda") for _ in range(2))
+    at = torch.arange(n + more, dtype=torch.int32, device="cuda")
+    rotated = pkv.paged_rope_append(q, k, v, at, at.long(), inv_freq, kc, vc)
+    held_k, held_v = (c.transpose(1, 2).reshape(-1, hkv, dim)[:n + more].double().cpu() for c in (kc, vc))
+
+    cache = PagedKVCache(16, hkv, bs, dim, dtype=F16)
+    cache.add_sequence(1, 0)
+    for i in range(n):
+        got = cache.rope_append([1], q[i:i + 1], k[i:i + 1], v[i:i + 1], inv_freq)
+        assert torch.equal(got[0], rotated[i])
+    scores = torch.rand(1, hkv, 96, generator=g).cuda()
+    kept = cache.evict([1], [2], scores, budget, 8, sinks=2).kept[0].cpu()
+    for i in range(n, n + more):
+        got = cache.rope_append([2], q[i:i + 1], k[i:i + 1], v[i:i + 1], inv_freq)
+        assert torch.equal(got[0], rotated[i])
+    out = cache.decode([2], got, 0.125).double().cpu()
+    for h in range(hkv):
+        stay = torch.cat([kept[h].long(), torch.arange(n, n + more)])
+        for e in range(h * hq // hkv, (h + 1) * hq // hkv):
+            p = torch.softmax(0.125 * (held_k[stay, h] @ rotated[-1, e].double().cpu()), 0)
+            want, size = p @ held_v[stay, h], p @ held_v[stay, h].abs()
+            # binary16: the output's rounding, half a step; float32 logits and sums
+            assert torch.all((out[0, e] - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -12 * size + 1e-6)
