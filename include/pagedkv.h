@@ -435,8 +435,11 @@ size_t pkv_chunk_workspace_size(int num_seqs, int num_tokens, int num_q_heads, i
  * a layer with a sliding window sees of a long context.  Its cost goes by window
  * + sinks.  Table entries of blocks wholly between the two are not read, so
  * their blocks may be freed; the hidden tokens beside visible ones in a block
- * may hold anything.  A context length of 0 gives zeros.  The workspace is
- * pkv_window_workspace_size bytes; partition_size counts tokens of the blocks
+ * may hold anything.  A context length of 0 gives zeros.  Held in float32 but
+ * for the weights: the product with V takes them rounded to act_dtype where the
+ * tensor cores serve a 16-bit cache (4 or 8 query heads a kv head), to binary16
+ * where the CUDA cores serve an E4M3 one, and with 2^-14 of themselves left out
+ * where the tensor cores do.  The workspace is pkv_window_workspace_size bytes; partition_size counts tokens of the blocks
  * that are left.
  */
 int paged_attention_decode_window(const void* q, const void* k_cache, const void* v_cache,
@@ -460,7 +463,9 @@ size_t pkv_window_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads
  * max_blocks_per_seq * block_size): scores[b][h][j] += sum_g p_g[j] for j <
  * context_lens[b], the others stay.  What paged_kv_evict goes by.  One thread
  * adds a token's weight, in a fixed order.  scores share no memory with another
- * buffer.  A context length of 0 gives zeros and adds nothing.  Not for block-scaled caches.  The workspace,
+ * buffer.  A context length of 0 gives zeros and adds nothing.  Weights are
+ * added in float32, rounded for the product with V as in
+ * paged_attention_decode_window.  Not for block-scaled caches.  The workspace,
  * pkv_scored_workspace_size bytes, holds the step's logits (4 bytes for each
  * query head and token of the tables).
  */

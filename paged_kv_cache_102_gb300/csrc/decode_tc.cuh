@@ -722,8 +722,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         it.n_tiles = (it.n_tok + TILE - 1) / TILE;
                         phys = table_entry(it);
                         if (phys >= 0) {
-                            ksc = p.k_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
-                            vsc = p.v_scale[static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh];
+                            const int64_t at = EXT && p.one_scale ? 0 : static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh;
+                            ksc = p.k_scale[at];
+                            vsc = p.v_scale[at];
                         }
                         const float top = warp_max(fabsf(vsc));
                         const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xff) - 126;  // top < 2^e
@@ -1387,7 +1388,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                             mx[g] = fmaxf(mx[g], SCALED ? sc[t][g] + lv_t[t] : sc[t][g]);
                         }
                     }
-                    if constexpr (EXT && !SCALED) {
+                    if constexpr (EXT && G > 1 && !HALF) {
                         if (p.logits != nullptr) {
                             const int kvh = PAIR ? 2 * it.kvh + hh : it.kvh;
                             float* dst = p.logits + ((static_cast<int64_t>(it.seq) * p.num_kv_heads + kvh) *
@@ -1398,7 +1399,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
 #pragma unroll
                                     for (int g = 0; g < G; g += 2)
                                         *reinterpret_cast<float2*>(dst + token_of(t) * G + g) =
-                                            make_float2(sc[t][g], sc[t][g + (G > 1)]);
+                                            make_float2(sc[t][g], sc[t][g + 1]);
                                 }
                         }
                     }
@@ -1514,7 +1515,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         o_keep[b * 8 + tid] = kept * r;
                         if (!(it.flags & kItemLast)) {
                             ml_run[tid] = make_float2(m, L);
-                        } else if (!(it.flags & kItemSingle)) {
+                        } else if (!(it.flags & kItemSingle) || (EXT && p.logits != nullptr)) {
                             const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G + tid;
                             *reinterpret_cast<float2*>(p.ws_ml + (hrow * p.max_parts + it.part) * 2) =
                                 make_float2(m, L);

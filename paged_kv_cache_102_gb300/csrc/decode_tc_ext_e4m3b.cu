@@ -1,5 +1,5 @@
-// Tensor-core decode with a window over block-scaled E4M3 caches: kernel
-// instantiations and their launch.
+// Tensor-core decode with a window or kept logits over E4M3 caches, with block
+// scales or (p.one_scale) one for all: kernel instantiations and their launch.
 #include "decode_tc_host.cuh"
 
 namespace pkv {

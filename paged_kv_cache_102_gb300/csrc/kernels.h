@@ -153,6 +153,7 @@ struct DecodeParams {
     // the extended kernels (EXT) alone; lengths and partitions count the tokens of windowed_len then
     int window;      // the last `window` tokens and the first `sinks` are seen; 0: all
     int sinks;
+    bool one_scale;  // block-scaled kernels: k_scale and v_scale hold one value, every block's
     float* logits;   // [num_seqs][num_kv_heads][logit_tokens][G], in log2 units; null: not kept
     int64_t logit_tokens;
 };
@@ -362,7 +363,6 @@ cudaError_t launch_decode_tc_d64(const DecodeParams& p, int act, int BS, int G, 
 // The same with a window or kept logits (tables shared by a sequence's kv heads).
 int decode_tc_ext_max_rows(int head_dim, int cache);
 cudaError_t launch_decode_tc_ext(const DecodeParams& p, int act, int cache, int head_dim, int BS, int G, cudaStream_t s);
-cudaError_t launch_decode_tc_ext_e4m3(const DecodeParams& p, int act, int BS, int G, cudaStream_t s);
 cudaError_t launch_decode_tc_ext_e4m3b(const DecodeParams& p, int act, int head_dim, int BS, int G, cudaStream_t s);
 
 // Adds each token's weights, from kept logits and the partitions' statistics, to its scores, and joins the partitions.
