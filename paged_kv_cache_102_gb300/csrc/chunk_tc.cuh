@@ -23,7 +23,13 @@
 //                  reference maximum moves only when a maximum passes it by 2^8,
 //                  so that the two need no more of each other than a vote; when it
 //                  moves (almost never after the first tile) they exchange their
-//                  maxima and multiply the row of O, half each.
+//                  maxima and multiply the row of O, half each.  For binary16
+//                  weights the reference lies 2^7 below the maximum: the largest
+//                  are 2^7, at most 2^15, and weights keep the type's precision
+//                  down to 2^-21 of the largest, below that 2^-32 of it.  (Beside
+//                  a first token that has nearly all the weight and a V of nearly
+//                  nothing, as such tokens do, the others' weights are the output:
+//                  with the maximum itself for a reference those of 2^-21.6 lost 5 %.)
 //  warp 19         MMA: S_t = Q_t K^T (M = 128 rows, N = 128 tokens), O_t += P_t V
 //                  (P from tensor memory, N = head_dim).  Order: S_0(0), S_1(0),
 //                  then for each tile i and t: O_t(i), S_t(i + 1).  While one row
@@ -454,6 +460,8 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
         // reference maximum (log2 units) and this half's sum; block scales: of the logits plus log2 |vs|, the unit of O
         float m = -INFINITY, l = 0.f;
         [[maybe_unused]] float unit = -INFINITY;
+        // how far below its maximum the reference (block scales: the unit, by which weights are rounded) is set
+        constexpr float LOW = ACT == kF16 ? 7.f : 0.f, LOW_M = SCALED ? 0.f : LOW;
         bool ok = true;
         // Warps without a row have nothing to do; the first one, which has some if any has, arrives for them.
         const uint32_t arrivals = (warp & 3) == 0 ? 1 + 4 - (rows_of(t) * G + 31) / 32 : 1;
@@ -512,7 +520,7 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                 }
             }
             float mx = fmaxf(max3(tops[0], tops[1], tops[2]), tops[3]) * c;
-            const bool past = mine && (mx > m + kChunkRescale || (SCALED && mu > unit + kChunkRescale));
+            const bool past = mine && (mx > m + (LOW_M + kChunkRescale) || (SCALED && mu > unit + (LOW + kChunkRescale)));
             if (pair_any(pair, past || !ok)) {
                 // the products of the tiles before are done before the row of O is multiplied
                 if (ok && i > 0) {
@@ -524,24 +532,24 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
                     break;
                 }
                 // the row's maximum, and so its reference, from both threads
-                auto agree = [&](float top, float at) {
+                auto agree = [&](float top, float at, float low) {
                     if (half == 1) *swap = top;
                     pair_any(pair, false);
                     float to = at;
                     if (half == 0) {
                         top = fmaxf(top, *swap);
-                        if (mine && top > at + kChunkRescale) to = top;
+                        if (mine && top > at + (low + kChunkRescale)) to = top - low;
                         *swap = to;
                     }
                     pair_any(pair, false);
                     if (half == 1) to = *swap;
                     return to;
                 };
-                const float to = agree(mx, m);
+                const float to = agree(mx, m, LOW_M);
                 const float down = to == m ? 1.f : fast_exp2(m - to);
                 float f = down;
                 if constexpr (SCALED) {
-                    const float u = agree(mu, unit);
+                    const float u = agree(mu, unit, LOW);
                     f = u == unit ? 1.f : fast_exp2(unit - u);
                     unit = u;
                 }

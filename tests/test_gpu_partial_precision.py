@@ -58,3 +58,45 @@ def test_weights_over_one_scale(pkv, group, dim, act):
         got = scores[b, :, :n].double().cpu()
         off = ((2 * d + 2.0 ** -20) * p).view(2, group, n).sum(1)  # the logits' errors, the exponential's
         assert torch.all((got - p.view(2, group, n).sum(1)).abs() <= off + 1e-6)
+
+
+def one_of_many(n, act, cache, gap, bs=16, dim=64, hkv=1):
+    """A sequence of n tokens: logit `gap` (log2) and V = 0 for the first, logit 0 and V = 1 for the others, for a query
+    whose first channel alone is 1.  Returns it and the call's scale."""
+    paged = ref.Paged([n], hkv, bs, dim, act, cache, extra_blocks=0)
+    k, v = torch.zeros(paged.k.shape), torch.ones(paged.v.shape)
+    blk, off = paged.slot(0, 0)
+    k[blk, :, off, 0] = 1.0
+    v[blk, :, off] = 0.0
+    paged.k, paged.v = (x.to(act) if cache == "act" else paged._codes(x) for x in (k, v))
+    if cache == "e4m3":
+        paged.k_scale, paged.v_scale = torch.ones(1), torch.ones(1)
+    if cache == "scaled":
+        paged.k_scales, paged.v_scales = torch.ones_like(paged.k_scales), torch.ones_like(paged.v_scales)
+    return paged, gap * 0.6931471805599453
+
+
+def small_weights(n, gap, u):
+    """Output of n tokens of 2^-gap beside one of weight 1 and V = 0, and what it may be off by: the output's and a weight's
+    half step (a weight below 2^-21 of the largest: 2^-32 of that), the logit of the first token in float32 (2^-17 of it),
+    and 2^-14 of the sum for float32 sums."""
+    x = n * 2.0 ** -gap
+    o = x / (1 + x)
+    return o, (2 * u + 2.0 ** -14 + 2.0 ** -16 * gap) * o + n * 2.0 ** -32
+
+
+@pytest.mark.parametrize("gap", [15.7, 19.1, 21.6, 25.2])
+@pytest.mark.parametrize("new", [1, 200], ids=["folded", "two row tiles"])
+@pytest.mark.parametrize("cache", ["act", "e4m3", "scaled"])
+@pytest.mark.parametrize("act", [F16, BF16])
+def test_chunk_small_weights(pkv, act, cache, new, gap):
+    """A first token that has nearly all the weight and no V: the output is what the others' small weights make it."""
+    n, dim = 4000, 64
+    paged, scale = one_of_many(n, act, cache, gap, dim=dim)
+    args, scales = paged.cuda()
+    q = torch.zeros(new, 1, dim, dtype=act)
+    q[..., 0] = 1.0
+    out = pkv.paged_attention_chunk(q.cuda(), *args, torch.tensor([0, new], dtype=torch.int32).cuda(), scale, **scales)
+    for i in range(new):
+        want, tol = small_weights(n - new + i, gap, ref.U[act])
+        assert torch.all((out[i].double() - want).abs() <= tol), (i, want, tol)
