@@ -51,6 +51,9 @@ constexpr int kStageTokens = 32;
 constexpr float kRescaleLog2 = 8.0f;  // largest log2 growth of the running max left unrescaled
 constexpr int kConsumerWarps = 4;
 constexpr int kNoRef = -1000;  // no V scale seen yet
+// EXT, one E4M3 scale: how far (log2) below a new maximum its reference is set.  Weights enter the product with V as
+// binary16 values, at most 2^(7 + 8) then, and keep their bits down to 2^-21 of the largest instead of 2^-14.
+constexpr float kBelowMax = 7.0f;
 constexpr int kDecodeThreads = (kConsumerWarps + 1) * 32;
 
 // 2^e for |e| <= 126, the nearest of those powers beyond.
@@ -412,9 +415,10 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
                 // stage max exceeds it by more than kRescaleLog2 (warp-uniform
                 // test), so probabilities stay below 2^kRescaleLog2 and l and
                 // acc, both relative to m, stay consistent.
-                if (mx > m[g] + kRescaleLog2) {
-                    const float alpha = m[g] == -INFINITY ? 0.f : fast_exp2(m[g] - mx);
-                    m[g] = mx;
+                constexpr float LOW = EXT && CACHE == kE4M3 ? kBelowMax : 0.f;
+                if (mx > m[g] + (LOW + kRescaleLog2)) {
+                    const float alpha = m[g] == -INFINITY ? 0.f : fast_exp2(m[g] - (mx - LOW));
+                    m[g] = mx - LOW;
                     l[g] *= alpha;
 #pragma unroll
                     for (int v = 0; v < C::VEC; ++v) acc[g][v] *= alpha;

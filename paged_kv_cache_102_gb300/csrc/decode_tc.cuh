@@ -1416,6 +1416,9 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 for (int g = 0; g < G; ++g) {
                     M[g] = fmaxf(fmaxf(red_max[g], red_max[8 + g]),
                                  fmaxf(red_max[16 + g], red_max[24 + g]));
+                    // binary16 weights of up to 2^15: small ones, all that counts beside a first token whose V is
+                    // nearly nothing, keep their bits down to 2^-29 of the largest instead of 2^-14
+                    if constexpr (EXT && !FP8 && ACT == kF16) M[g] -= 15.f;
                     sum[g] = 0.f;
                 }
 #pragma unroll
@@ -1630,7 +1633,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             for (int g = 0; g < G; ++g) {
                 const float Mg = stats[(b * 2 + hh) * 16 + g];
                 const float Lg = stats[(b * 2 + hh) * 16 + 8 + g];
-                // L >= 1 (the max token's weight is 1): one reciprocal per head
+                // L >= 1 (the max token's weight is 1, or 2^15): one reciprocal per head
                 const float val = o[g] * (__frcp_rn(Lg) * vmul);
                 const int kvh = PAIR ? 2 * it.kvh + hh : it.kvh;
                 const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + kvh * G + g;

@@ -76,13 +76,18 @@ def one_of_many(n, act, cache, gap, bs=16, dim=64, hkv=1):
     return paged, gap * 0.6931471805599453
 
 
-def small_weights(n, gap, u):
+def small_weights(n, gap, act, least=2.0 ** -32):
     """Output of n tokens of 2^-gap beside one of weight 1 and V = 0, and what it may be off by: the output's and a weight's
-    half step (a weight below 2^-21 of the largest: 2^-32 of that), the logit of the first token in float32 (2^-17 of it),
-    and 2^-14 of the sum for float32 sums."""
+    half step (a weight below 2^-21 of the largest: 2^-32 of that; an output that is a subnormal binary16 value: half of
+    2^-24), the logit of the first token in float32 (2^-17 of it), and 2^-14 of the sum for float32 sums.
+
+    Weights in three E4M3 parts, the block-scaled kernel's on the tensor cores: least = 2^-28.  A weight times 2^8 is a sum
+    of codes, 2^-5 of codes and 2^-10 of codes, each part the nearest code to 2^5 times what the part before left; codes
+    below 2^-6 are 2^-9 apart, so the last part leaves up to 2^-10, which counts 2^-10 * 2^-10 * 2^-8 of the largest."""
     x = n * 2.0 ** -gap
     o = x / (1 + x)
-    return o, (2 * u + 2.0 ** -14 + 2.0 ** -16 * gap) * o + n * 2.0 ** -32
+    u = ref.U[act]
+    return o, (2 * u + 2.0 ** -14 + 2.0 ** -16 * gap) * o + n * least + (2.0 ** -25 if act is F16 else 0.0)
 
 
 @pytest.mark.parametrize("gap", [15.7, 19.1, 21.6, 25.2])
@@ -98,5 +103,33 @@ def test_chunk_small_weights(pkv, act, cache, new, gap):
     q[..., 0] = 1.0
     out = pkv.paged_attention_chunk(q.cuda(), *args, torch.tensor([0, new], dtype=torch.int32).cuda(), scale, **scales)
     for i in range(new):
-        want, tol = small_weights(n - new + i, gap, ref.U[act])
+        want, tol = small_weights(n - new + i, gap, act)
         assert torch.all((out[i].double() - want).abs() <= tol), (i, want, tol)
+
+
+@pytest.mark.parametrize("gap", [15.7, 21.6, 25.2])
+@pytest.mark.parametrize("group,dim", [(1, 64), (2, 128), (4, 64), (8, 128)])
+@pytest.mark.parametrize("cache", ["act", "e4m3", "scaled"])
+@pytest.mark.parametrize("act", [F16, BF16])
+def test_decode_small_weights(pkv, act, cache, group, dim, gap):
+    """The same for one row, under a window with the first token in front of it and scored, and the weights added."""
+    n, hkv = 1300, 2
+    paged, scale = one_of_many(n, act, cache, gap, dim=dim, hkv=hkv)
+    args, scales = paged.cuda()
+    q = torch.zeros(1, hkv * group, dim, dtype=act).cuda()
+    q[..., 0] = 1.0
+    least = 2.0 ** -28 if cache == "scaled" or (cache == "e4m3" and group >= 4) else 2.0 ** -32
+    for part in (-1, 0):  # of the library's choice, and one
+        out = pkv.paged_attention_decode_window(q, *args, scale, 1000, sinks=1, partition_size=part, **scales)
+        want, tol = small_weights(1000, gap, act, least)
+        assert torch.all((out.double() - want).abs() <= tol), (part, want, tol)
+        if cache == "scaled":
+            continue
+        scores = torch.zeros(1, hkv, paged.tables.shape[1] * 16).cuda()
+        one = dict(k_scale=scales["k_scale"], v_scale=scales["v_scale"])
+        out = pkv.paged_attention_decode_scored(q, *args, scale, scores, partition_size=part, **one)
+        want, tol = small_weights(n - 1, gap, act, least)
+        assert torch.all((out.double() - want).abs() <= tol), (part, want, tol)
+        p = group * 2.0 ** -gap / (1 + (n - 1) * 2.0 ** -gap)
+        off = (2.0 ** -16 * gap + 2.0 ** -14) * p
+        assert torch.all((scores[0, :, 1:n].double() - p).abs() <= off)
