@@ -69,9 +69,10 @@ __global__ void __launch_bounds__(kMergeThreads) paged_chunk_merge_kernel(const 
         hi = min(hi, lo + step);
     }
     const int s0 = p.seq_starts[lo], s1 = p.seq_starts[lo + 1], L = p.context_lens[lo];
+    // (every row waits, so that this grid does not end, and what follows it on the stream begin, before the one ahead)
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     // rows of no sequence, or of one that was flagged
     if (s0 < 0 || row < s0 || row >= s1 || s1 > p.num_tokens || L < s1 - s0 || L > p.max_blocks_per_seq * p.block_size) return;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     const float2* ml = reinterpret_cast<const float2*>(p.ws_ml);
     const float2 mine = lane < p.splits ? ml[lane * rows + w] : make_float2(-INFINITY, 0.f);
     const float M = warp_max(mine.x);

@@ -223,10 +223,15 @@ template <int ACT, int D>
 __global__ void __launch_bounds__(kAddThreads) scored_finish_kernel(const AddWeightsParams p) {
     __shared__ float s_max[8], s_inv[8];
     const int seq = blockIdx.z, kvh = blockIdx.y, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int L = p.context_lens[seq];
-    if (L < 1 || L > p.max_context) return;  // flagged before
+    int L = p.context_lens[seq];
+    if (L > p.max_context) L = 0;  // flagged before
     const int64_t first = static_cast<int64_t>(blockIdx.x) * kAddTokens;
-    if (first >= L) return;
+    if (first >= L) {
+        // Nothing to do here.  Each row's first block waits all the same, so that this grid does not end, and what follows
+        // it on the stream begin, while the decode still runs.
+        if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     const int parts = (L + p.partition_size - 1) / p.partition_size;
     const int64_t row = static_cast<int64_t>(seq) * p.num_kv_heads + kvh;
     float before[kAddEach], logit[kAddEach][8];

@@ -48,3 +48,38 @@ def test_rotation_after_an_eviction(pkv):
             want, size = p @ held_v[stay, h], p @ held_v[stay, h].abs()
             # binary16: the output's rounding, half a step; float32 logits and sums
             assert torch.all((out[0, e] - want).abs() <= 2.0 ** -11 * want.abs() + 2.0 ** -12 * size + 1e-6)
+
+
+def test_nothing_to_do_is_done_in_order(pkv):
+    """Batches without a token or a row: what follows on the stream finds the call's zeros, and the call nothing of what
+    follows."""
+    B, hq, hkv, dim = 4096, 64, 8, 128
+    kc = torch.zeros(4, hkv, 16, dim, dtype=BF16, device="cuda")
+    tables = torch.zeros(B, 64, dtype=torch.int32, device="cuda")
+    q = torch.randn(B, hq, dim, device="cuda").to(BF16)
+    scores = torch.zeros(B, hkv, 64 * 16, device="cuda")
+    empty = torch.zeros(B, dtype=torch.int32, device="cuda")
+    out, seen = torch.empty_like(q), torch.empty_like(q)
+    for _ in range(10):
+        lens = empty.clone()
+        out.fill_(3.0)
+        pkv.paged_attention_decode_scored(q, kc, kc, tables, lens, 0.1, scores, out=out)
+        seen.copy_(out)
+        lens.fill_(16)
+        assert torch.all(seen == 0) and torch.all(scores == 0)
+        out.fill_(3.0)
+        lens.zero_()
+        pkv.paged_attention_decode_window(q, kc, kc, tables, lens, 0.1, 600, out=out)
+        seen.copy_(out)
+        assert torch.all(seen == 0)
+    # no new tokens, and several shares
+    tables, lens = tables[:2].repeat(1, 64).contiguous(), torch.full((2,), 60000, dtype=torch.int32, device="cuda")
+    valid = torch.tensor([0, 100, 200], dtype=torch.int32, device="cuda")
+    assert pkv._native.lib().pkv_chunk_workspace_size(2, 200, hq, hkv, dim, tables.shape[1], 16) > 256
+    for _ in range(10):
+        starts = torch.zeros_like(valid)
+        out[:200] = 3.0
+        pkv.paged_attention_chunk(q[:200], kc, kc, tables, lens, starts, 0.1, out=out[:200])
+        starts.copy_(valid)
+        torch.cuda.synchronize()
+        assert torch.all(out[:200] == 3.0)
