@@ -465,7 +465,10 @@ size_t pkv_window_workspace_size(int num_seqs, int num_q_heads, int num_kv_heads
  * adds a token's weight, in a fixed order.  scores share no memory with another
  * buffer.  A context length of 0 gives zeros and adds nothing.  Weights are
  * added in float32, rounded for the product with V as in
- * paged_attention_decode_window.  Not for block-scaled caches.  The workspace,
+ * paged_attention_decode_window.  A sequence with a table entry of its tokens'
+ * outside the pool adds nothing (PKV_DEV_BAD_BLOCK; its rows of out mean nothing),
+ * and after a wait that was given up what was not finished does not
+ * (PKV_DEV_WAIT_TIMEOUT).  Not for block-scaled caches.  The workspace,
  * pkv_scored_workspace_size bytes, holds the step's logits (4 bytes for each
  * query head and token of the tables).
  */

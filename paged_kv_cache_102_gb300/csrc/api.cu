@@ -485,6 +485,8 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         const int chunk = (ext ? decode_tc_ext_max_rows(head_dim, kind) : decode_tc_max_rows()) / rows_per_seq;
         const size_t act_bytes = 2;
         e = cudaSuccess;
+        p.zero_words = 1;
+        if (scored) p.failed = p.work_counter + 1;
         for (int s0 = 0; s0 < num_seqs && e == cudaSuccess; s0 += chunk) {
             DecodeParams c = p;
             c.num_seqs = std::min(chunk, num_seqs - s0);
@@ -505,6 +507,7 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
             if (scored) {
                 c.ws_ml = p.ws_ml + static_cast<size_t>(s0) * num_q_heads * max_parts * 2;
                 c.logits = p.logits + static_cast<int64_t>(s0) * num_q_heads * max_ctx;
+                c.zero_words = s0 == 0 ? 2 : 1;  // (the launches of a call share `failed`)
             }
             e = ext ? launch_decode_tc_ext(c, act_dtype, kind, head_dim, block_size, G, s)
                     : launch_decode_tc(c, act_dtype, kind, head_dim, block_size, G, path == PKV_PATH_TENSOR ? 0 : 1, s);
@@ -547,7 +550,7 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
         if (e != cudaSuccess) return cuda_fail((F + ": merge kernel launch").c_str(), e);
     }
     if (scored) {
-        const AddWeightsParams a{p.logits, p.ws_ml, context_lens, ext->scores, p.ws_o, out, ext->score_tokens,
+        const AddWeightsParams a{p.logits, p.ws_ml, context_lens, p.failed, ext->scores, p.ws_o, out, ext->score_tokens,
                                  p.logit_tokens, num_seqs, num_kv_heads, G, P, max_parts, static_cast<int>(max_ctx)};
         e = launch_scored_finish(a, act_dtype, head_dim, s);
         if (e != cudaSuccess) return cuda_fail((F + ": weights kernel launch").c_str(), e);

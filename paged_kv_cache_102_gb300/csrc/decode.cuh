@@ -89,6 +89,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     using C = DecodeCfg<CACHE, D, BS, G>;
     extern __shared__ __align__(1024) unsigned char smem[];
     __shared__ int s_failed;
+    [[maybe_unused]] __shared__ int s_bad;  // EXT: a table entry is no block
     unsigned char* kbuf = smem;
     unsigned char* vbuf = smem + C::STAGES * C::STAGE_BYTES;
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + 2 * C::STAGES * C::STAGE_BYTES);
@@ -134,6 +135,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
 
     if (threadIdx.x == 0) {
         s_failed = 0;
+        if constexpr (EXT) s_bad = 0;
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], kConsumerWarps);
@@ -165,7 +167,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
             if (bad) {
                 atomicOr(p.err, kErrBadBlock);
                 phys = -1;
+                if constexpr (EXT) s_bad = 1;
             }
+            if constexpr (EXT) __syncwarp();  // before lane 0 announces the stage
             const int chunk_blocks = min(32, n_blk - chunk);
             for (int j = 0; j < chunk_blocks; j += C::BPS) {
                 int pb[C::BPS];
@@ -508,7 +512,15 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
     }
     // all consumer warps (not the producer) meet here
     asm volatile("bar.sync 1, %0;" ::"n"(kConsumerWarps * 32) : "memory");
-    if (s_failed) return;
+    if (s_failed) {
+        if constexpr (EXT) {
+            if (p.logits != nullptr && threadIdx.x < G)
+                *reinterpret_cast<float2*>(
+                    p.ws_ml + ((static_cast<size_t>(seq) * p.num_q_heads + h0 + threadIdx.x) * p.max_parts + part) * 2) =
+                    make_float2(0.f, 0.f);
+        }
+        return;
+    }
 
     const float vmul = CACHE == kE4M3 ? *p.v_scale : 1.0f;
     const int tid = threadIdx.x;
@@ -529,16 +541,15 @@ __global__ void __launch_bounds__(kDecodeThreads, (G <= 2 ? 3 : 2))
         }
         const float o = num / den * vmul;
         const size_t row = static_cast<size_t>(seq) * p.num_q_heads + h0 + g;
-        if (EXT && p.logits != nullptr && d == 0) {  // whoever adds the weights up needs the statistics
-            p.ws_ml[(row * p.max_parts + part) * 2] = M;
-            p.ws_ml[(row * p.max_parts + part) * 2 + 1] = den;
-        }
+        if (EXT && p.logits != nullptr && d == 0)  // whoever adds the weights up needs the statistics
+            *reinterpret_cast<float2*>(p.ws_ml + (row * p.max_parts + part) * 2) =
+                s_bad ? make_float2(0.f, 0.f) : make_float2(M, den);
         if (single) {
             static_cast<uint16_t*>(p.out)[row * D + d] = float_to_act<ACT>(o);
         } else {
             const size_t slot = row * p.max_parts + part;
             p.ws_o[slot * D + d] = o;
-            if (d == 0) {
+            if (d == 0 && !(EXT && p.logits != nullptr)) {
                 p.ws_ml[slot * 2] = M;
                 p.ws_ml[slot * 2 + 1] = den;
             }

@@ -176,14 +176,14 @@ struct TcSmem {
     __host__ __device__ static constexpr int alloc(int rows) { return bytes(rows) + 1024; }  // room to align the base
 };
 
-// Block-scaled items: the row's only partition, the first and the last of its segments.
-enum : int { kItemSingle = 1, kItemFirst = 2, kItemLast = 4 };
+// Block-scaled items: the row's only partition, the first and the last of its segments.  EXT: a table entry is no block.
+enum : int { kItemSingle = 1, kItemFirst = 2, kItemLast = 4, kItemBad = 8 };
 
 struct TcItem {
     int seq, kvh, row, part, tok_begin, n_tok, n_tiles;
     int qshift;  // E4M3 cache: q enters the MMA scaled by 2^-qshift
     int ev;      // block-scaled: 2^ev was taken out of the V scales
-    int flags;   // block-scaled: kItemSingle, ...
+    int flags;   // block-scaled: kItemSingle, ...; EXT: kItemBad
 };
 
 // Rows: a sequence (tables shared by its kv heads) or, with per-(sequence,
@@ -342,6 +342,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     constexpr uint32_t IDESC_O = tc::idesc_f16(128, O_COLS, !FP8 && ACT == kBF16, true, FP8);
     static_assert(!FP8 || G <= 8, "E4M3 cache: rows 0-7 of Q and P hold the high parts, rows 8-15 the low parts");
     constexpr bool Q3 = FP8 && ACT == kF16;  // binary16 queries: three E4M3 parts
+    static_assert(!EXT || !FP8 || SCALED, "windows and kept logits over E4M3 caches: the block-scaled kernel");
     static_assert(G == 2 || G == 4 || G == 8 || (SCALED && G == 1), "query heads per kv head");
     static_assert(kTcMaxTiles * kTcTile / BS <= 32, "one warp holds the table entries of an item");
 
@@ -661,6 +662,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                     it.qshift = m > 0.f ? min(120, max(-120, e - 7)) : 0;
                 }
                 phys = table_entry(it);
+                if constexpr (EXT)  // (16-bit caches, which need no shift: the flag in its place)
+                    it.qshift = __any_sync(0xffffffffu, lane < (it.n_tok + BS - 1) / BS && phys < 0) ? kItemBad : 0;
                 if (p.new_slots != nullptr && it.tok_begin + it.n_tok == s_lens[it.row]) {
                     // fused append: this item holds the new (last) token; write it
                     // before the item is published, so before any copy of its block
@@ -721,6 +724,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         it.n_tok = min(left, kTcMaxTiles * kTcTile);
                         it.n_tiles = (it.n_tok + TILE - 1) / TILE;
                         phys = table_entry(it);
+                        if (EXT && __any_sync(0xffffffffu, lane < (it.n_tok + BS - 1) / BS && phys < 0)) it.flags |= kItemBad;
                         if (phys >= 0) {
                             const int64_t at = EXT && p.one_scale ? 0 : static_cast<int64_t>(phys) * p.num_kv_heads + it.kvh;
                             ksc = p.k_scale[at];
@@ -1322,7 +1326,8 @@ __global__ void __launch_bounds__(kTcThreads, 2)
             if (ci < 0) return 0;
             if constexpr (SCALED) return 1;
             tc_decode_item<TILE>(ci, p, s_lens, s_prefix, s_order, heads_per_row, it);
-            it.qshift = qshift;
+            it.qshift = EXT ? 0 : qshift;
+            it.flags = EXT ? qshift : 0;
             return 1;
         };
         auto softmax = [&](const TcItem& it, int k) {
@@ -1521,7 +1526,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                         } else if (!(it.flags & kItemSingle) || (EXT && p.logits != nullptr)) {
                             const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + it.kvh * G + tid;
                             *reinterpret_cast<float2*>(p.ws_ml + (hrow * p.max_parts + it.part) * 2) =
-                                make_float2(m, L);
+                                EXT && (it.flags & kItemBad) ? make_float2(0.f, 0.f) : make_float2(m, L);
                         }
                     }
                 } else if (tid == 0) {
@@ -1637,16 +1642,15 @@ __global__ void __launch_bounds__(kTcThreads, 2)
                 const float val = o[g] * (__frcp_rn(Lg) * vmul);
                 const int kvh = PAIR ? 2 * it.kvh + hh : it.kvh;
                 const size_t hrow = static_cast<size_t>(it.seq) * p.num_q_heads + kvh * G + g;
-                if (EXT && p.logits != nullptr && d == 0) {  // whoever adds the weights up needs the statistics
-                    p.ws_ml[(hrow * p.max_parts + it.part) * 2] = Mg;
-                    p.ws_ml[(hrow * p.max_parts + it.part) * 2 + 1] = Lg;
-                }
+                if (EXT && p.logits != nullptr && d == 0)  // whoever adds the weights up needs the statistics
+                    *reinterpret_cast<float2*>(p.ws_ml + (hrow * p.max_parts + it.part) * 2) =
+                        it.flags & kItemBad ? make_float2(0.f, 0.f) : make_float2(Mg, Lg);
                 if (single) {
                     static_cast<uint16_t*>(p.out)[hrow * HD + d] = float_to_act<ACT>(val);
                 } else {
                     const size_t slot = hrow * p.max_parts + it.part;
                     p.ws_o[slot * HD + d] = val;
-                    if (d == 0) {
+                    if (d == 0 && !(EXT && p.logits != nullptr)) {
                         p.ws_ml[slot * 2] = Mg;
                         p.ws_ml[slot * 2 + 1] = Lg;
                     }
@@ -1673,6 +1677,7 @@ __global__ void __launch_bounds__(kTcThreads, 2)
     __syncthreads();
     tc::fence_after_sync();
     if (warp == 1) tc::tmem_dealloc(tmem, kTcTmemCols);
+    if (EXT && threadIdx.x == 0 && p.failed != nullptr && *abort_flag) *p.failed = 1;
 }
 
 }  // namespace pkv

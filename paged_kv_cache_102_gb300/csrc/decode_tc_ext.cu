@@ -40,7 +40,7 @@ cudaError_t launch_decode_tc_ext(const DecodeParams& p, int act, int cache, int 
     if (!make_map(&km, p.k_cache, act, cache_rows, BS, head_dim) || !make_map(&vm, p.v_cache, act, cache_rows, BS, head_dim) ||
         !make_map(&qm, p.q, act, static_cast<uint64_t>(p.num_seqs) * p.num_q_heads, G, head_dim))
         return cudaErrorInvalidValue;
-    const cudaError_t e = cudaMemsetAsync(p.work_counter, 0, sizeof(int), s);
+    const cudaError_t e = cudaMemsetAsync(p.work_counter, 0, sizeof(int) * p.zero_words, s);
     if (e != cudaSuccess) return e;
     return act == kBF16 ? launch_ext<kBF16>(p, km, vm, qm, head_dim, BS, G, s)
                         : launch_ext<kF16>(p, km, vm, qm, head_dim, BS, G, s);

@@ -54,9 +54,9 @@ int sm_count() {
     return counts[dev];
 }
 
-__global__ void zero_counter_kernel(int* counter) {
+__global__ void zero_counter_kernel(int* counter, int words) {
     asm volatile("griddepcontrol.launch_dependents;");
-    if (threadIdx.x == 0) *counter = 0;
+    if (static_cast<int>(threadIdx.x) < words) counter[threadIdx.x] = 0;
 }
 
 template <int ACT, int CACHE, int BS, int G, int NS, bool PAIR, bool HALF, bool EXT>
@@ -85,14 +85,14 @@ cudaError_t launch(const DecodeParams& p, const CUtensorMap& km, const CUtensorM
     const int grid = static_cast<int>(items < static_cast<long long>(sms) * ctas_per_sm ? items : sms * ctas_per_sm);
     if (grid <= 0) return cudaSuccess;
     if constexpr (CACHE == kE4M3B) {
-        if (items <= grid) {  // an item a block: nothing to claim, nothing to zero
+        if (items <= grid && p.failed == nullptr) {  // an item a block: nothing to claim, nothing to zero
             DecodeParams one = p;
             one.work_counter = nullptr;
             kern<<<grid, threads, smem, s>>>(km, vm, qm, one);
             return cudaGetLastError();
         }
         // zero the work counter, and let the decode kernel's prologue run meanwhile
-        zero_counter_kernel<<<1, 32, 0, s>>>(p.work_counter);
+        zero_counter_kernel<<<1, 32, 0, s>>>(p.work_counter, EXT ? p.zero_words : 1);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
         cudaLaunchConfig_t cfg = {};

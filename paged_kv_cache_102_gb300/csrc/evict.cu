@@ -215,7 +215,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(const EvictPar
 // head) a block: scores += sum over the group's heads of 2^(logit - M) / l, one
 // thread for every two tokens, (M, l) the statistics of the head's partitions joined; and a
 // share of the output's elements, where there are partitions to join (as the
-// merge kernel would: sum_i w_i o_i / l with w_i = l_i 2^(m_i - M)).  Bound by
+// merge kernel would: sum_i w_i o_i / l with w_i = l_i 2^(m_i - M)).  Rows with a
+// partition that went wrong, statistics (0, 0), leave their scores as they are, all
+// do where a block of the tensor-core kernel gave up a wait.  Bound by
 // the chain of loads of a block; 1, 2 or 4 tokens a thread: 122.5, 119.5 and
 // 120.9 us for the call over 64 sequences of up to 4096 tokens, 64 / 8 heads (the
 // decode before it 108 by itself, its K and V 80 at the copy's rate).
@@ -257,11 +259,17 @@ __global__ void __launch_bounds__(kAddThreads) scored_finish_kernel(const AddWei
         }
     }
     const float2* stats = reinterpret_cast<const float2*>(p.ws_ml) + row * p.group * p.max_parts;
+    bool wrong = threadIdx.x == 0 && p.failed != nullptr && *p.failed != 0;
+    auto is_wrong = [](float2 x) { return x.x == 0.f && x.y == 0.f; };  // (a sum has a term of 1 at least, or 2^-inf ones alone)
     if (warp < p.group) {
         const float2* ml = stats + warp * p.max_parts;
         const float2 mine = lane < parts ? ml[lane] : make_float2(-INFINITY, 0.f);
+        wrong = wrong || (lane < parts && is_wrong(mine));
         float M = mine.x;
-        for (int i = 32 + lane; i < parts; i += 32) M = fmaxf(M, ml[i].x);
+        for (int i = 32 + lane; i < parts; i += 32) {
+            wrong = wrong || is_wrong(ml[i]);
+            M = fmaxf(M, ml[i].x);
+        }
         M = warp_max(M);
         float l = lane < parts ? mine.y * fast_exp2(mine.x - M) : 0.f;
         for (int i = 32 + lane; i < parts; i += 32) l += ml[i].y * fast_exp2(ml[i].x - M);
@@ -272,11 +280,11 @@ __global__ void __launch_bounds__(kAddThreads) scored_finish_kernel(const AddWei
             s_inv[warp] = 1.f / l;
         }
     }
-    __syncthreads();
+    wrong = __syncthreads_or(wrong);
 #pragma unroll
     for (int y = 0; y < kAddEach; ++y) {
         const int64_t t = first + y * kAddThreads + threadIdx.x;
-        if (t >= L) break;
+        if (t >= L || wrong) break;
         float sum = 0.f;
 #pragma unroll
         for (int g = 0; g < 8; ++g)

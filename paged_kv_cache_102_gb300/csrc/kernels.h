@@ -154,6 +154,8 @@ struct DecodeParams {
     int window;      // the last `window` tokens and the first `sinks` are seen; 0: all
     int sinks;
     bool one_scale;  // block-scaled kernels: k_scale and v_scale hold one value, every block's
+    int* failed;     // tensor cores, kept logits: set to 1 where a block gave up a wait; the word behind work_counter
+    int zero_words;  // words at work_counter to zero ahead of the launch
     float* logits;   // [num_seqs][num_kv_heads][logit_tokens][G], in log2 units; null: not kept
     int64_t logit_tokens;
 };
@@ -197,8 +199,9 @@ struct MergeParams {
 // scores[seq][kvh][token] += sum over the group's heads of their weights.
 struct AddWeightsParams {
     const float* logits;  // [num_seqs][num_kv_heads][logit_tokens][group], log2 units
-    const float* ws_ml;   // [num_seqs][num_kv_heads * group][max_parts][2]
+    const float* ws_ml;   // [num_seqs][num_kv_heads * group][max_parts][2]; (0, 0): the partition went wrong
     const int32_t* context_lens;
+    const int* failed;    // not null and not 0: nothing is added
     float* scores;        // [num_seqs][num_kv_heads][score_tokens]
     const float* ws_o;    // [num_seqs][num_kv_heads * group][max_parts][head_dim], where there are several
     void* out;

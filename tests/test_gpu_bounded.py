@@ -83,3 +83,31 @@ def test_nothing_to_do_is_done_in_order(pkv):
         starts.copy_(valid)
         torch.cuda.synchronize()
         assert torch.all(out[:200] == 3.0)
+
+
+@pytest.mark.parametrize("cache,group,dim", [("act", 1, 64), ("act", 2, 128), ("act", 4, 64), ("act", 8, 128),
+                                             ("e4m3", 1, 128), ("e4m3", 4, 128), ("e4m3", 8, 64), ("e4m3", 8, 128)])
+def test_scores_of_a_bad_table_stay(pkv, cache, group, dim):
+    """A step over a table with an entry outside the pool leaves that sequence's scores as they are, the others' are right,
+    and the next step with the table put right adds as ever."""
+    lens, hkv = [700, 1300, 90, 1300, 40], 2
+    paged = ref.Paged(lens, hkv, 16, dim, F16, cache, seed=group)
+    (k, v, tables, n), scales = paged.cuda()
+    one = dict(k_scale=scales["k_scale"], v_scale=scales["v_scale"])
+    q = torch.randn(len(lens), hkv * group, dim, generator=torch.Generator().manual_seed(3)).to(F16).cuda()
+    base = torch.rand(len(lens), hkv, tables.shape[1] * 16).cuda()
+    right = base.clone()
+    out = pkv.paged_attention_decode_scored(q, k, v, tables, n, 0.1, right, **one)
+    for b, i, entry in ((1, 0, -1), (1, 81, k.shape[0]), (3, 40, 2 ** 30), (2, 5, -2 ** 31), (4, 2, k.shape[0])):
+        for part in (-1, 0, 64):
+            broken, scores = tables.clone(), base.clone()
+            broken[b, i] = entry
+            got = pkv.paged_attention_decode_scored(q, k, v, broken, n, 0.1, scores, partition_size=part, **one)
+            assert pkv.device_error() == 1
+            assert torch.equal(scores[b], base[b]), (b, i, part)
+            rest = [x for x in range(len(lens)) if x != b]
+            if part == -1:
+                assert torch.equal(scores[rest], right[rest]) and torch.equal(got[rest], out[rest])
+            assert torch.all((scores[rest] - right[rest]).abs() < 1e-4)
+            pkv.paged_attention_decode_scored(q, k, v, tables, n, 0.1, scores, partition_size=part, **one)
+            assert torch.all((scores[b] - right[b]).abs() < 1e-4)
