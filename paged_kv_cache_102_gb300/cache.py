@@ -55,6 +55,7 @@ class PagedKVCache:
             v_scales = v_scales if v_scales is not None else zeros()
         self.k_scales, self.v_scales = k_scales, v_scales
         self.blocks = BlockManager(num_blocks, block_size, free_list=free_list)
+        self._moves = []  # (stream, event) of evictions that may still read blocks they freed
 
     # -- host-side bookkeeping -------------------------------------------------
     def add_sequence(self, seq_id: int, num_tokens: int) -> None:
@@ -77,6 +78,19 @@ class PagedKVCache:
         if stream is not None:
             t.record_stream(_torch_stream(stream, self.device))
         return t
+
+    def _step_stream(self, stream):
+        return torch.cuda.current_stream(self.device) if stream is None else _torch_stream(stream, self.device)
+
+    def _await_moves(self, stream) -> None:
+        """The step on the stream may write blocks that evictions on other streams freed: behind their moves."""
+        if not self._moves:
+            return
+        s = self._step_stream(stream)
+        for other, event in self._moves:
+            if other != s.cuda_stream:
+                s.wait_event(event)
+        self._moves = [m for m in self._moves if not m[1].query()]
 
     # -- device steps ------------------------------------------------------------
     def append(self, seq_ids, k: torch.Tensor, v: torch.Tensor, stream=None):
@@ -104,6 +118,7 @@ class PagedKVCache:
     def _reserve(self, seq_ids, stream):
         """Slots of one new token per sequence; the copy-on-write copies run on the stream."""
         slots, pairs = self.blocks.append_slots(seq_ids)
+        self._await_moves(stream)
         if len(pairs):
             paged_block_copy(self.k_cache, self.v_cache, self._upload(pairs, stream), stream=stream,
                              k_scales=self.k_scales, v_scales=self.v_scales)
@@ -155,7 +170,10 @@ class PagedKVCache:
     def evict(self, seq_ids, new_ids, scores: torch.Tensor, budget: int, recent: int, sinks=0, stream=None):
         """Replace each sequence by one of at most budget tokens under a new id: those that paged_kv_evict keeps, whose
         result this returns.  The old sequences are freed (blocks that they share with others stay).  Positions go on
-        from the old sequence's; a window counts the tokens that are held, not the ones between them that went."""
+        from the old sequence's; a window counts the tokens that are held, not the ones between them that went.
+        The pool has to have free blocks for the new sequences before the old ones go.  Later appends and evictions of
+        this cache wait for the move whatever their stream; other calls that write into blocks taken after it, on
+        another stream, are the caller's to order."""
         if self.k_scales is not None:
             raise ValueError("PagedKVCache.evict: not for a block-scaled cache")
         seq_ids, new_ids = [int(s) for s in np.asarray(seq_ids)], [int(s) for s in np.asarray(new_ids)]
@@ -173,12 +191,16 @@ class PagedKVCache:
                 self.blocks.set_dropped(s, self.blocks.num_dropped(old) + n - min(n, int(budget)))
             src, length = (self._upload(a, stream) for a in self.blocks.tables(seq_ids))
             dst = self._upload(self.blocks.tables(new_ids)[0], stream)
+            self._await_moves(stream)
             got = paged_kv_evict(self.k_cache, self.v_cache, scores, src, length, dst, budget, recent, sinks=sinks,
                                  stream=stream)
         except Exception:
             for s in added:  # as before
                 self.blocks.free_sequence(s)
             raise
+        if self.device.type == "cuda":
+            s = self._step_stream(stream)
+            self._moves.append((s.cuda_stream, s.record_event()))
         for s in seq_ids:
             self.blocks.free_sequence(s)
         return got

@@ -60,3 +60,60 @@ def test_positions_go_on_after_an_eviction(host_cache):
     cache.free(31)
     cache.add_sequence(31, 4)
     assert positions(31) == [4]
+
+
+class Recorder:
+    """A stream that notes what is put on it."""
+
+    def __init__(self, handle, log):
+        self.cuda_stream, self.log = handle, log
+
+    def record_event(self):
+        self.log.append(("record", self.cuda_stream))
+        return Event(self.cuda_stream)
+
+    def wait_event(self, event):
+        self.log.append(("wait", self.cuda_stream, event.handle))
+
+
+class Event:
+    def __init__(self, handle):
+        self.handle, self.done = handle, False
+
+    def query(self):
+        return self.done
+
+
+def test_blocks_of_an_eviction_are_written_behind_its_move(host_cache, monkeypatch):
+    """Appends and evictions on other streams than an eviction's wait for its move: they may write the blocks it freed."""
+    cache, log = host_cache
+    monkeypatch.setattr(cache_module, "_torch_stream", lambda s, device: s)
+    monkeypatch.setattr(cache, "_upload", lambda array, stream: torch.from_numpy(array))
+    monkeypatch.setattr(cache, "device", torch.device("cuda"))
+    one, two = Recorder(1, log), Recorder(2, log)
+    cache.add_sequence(1, 100)
+    cache.add_sequence(2, 30)
+
+    def steps(call):
+        log.clear()
+        call()
+        return [x if x[0] in ("record", "wait") else x[0] for x in log]
+
+    def append(stream):
+        return steps(lambda: cache.append([2], None, None, stream=stream))
+
+    def evict(old, new, budget, stream):
+        return steps(lambda: cache.evict([old], [new], torch.zeros(1, 1, 128), budget, 8, stream=stream))
+
+    assert append(two) == ["paged_kv_append"]
+    assert evict(1, 3, 40, one) == ["paged_kv_evict", ("record", 1)]
+    assert append(one) == ["paged_kv_append"]
+    assert append(two) == [("wait", 2, 1), "paged_kv_append"]
+    assert steps(lambda: cache.rope_append([2], None, None, None, None, stream=two)) == [("wait", 2, 1), "paged_rope_append"]
+    assert evict(3, 4, 20, two) == [("wait", 2, 1), "paged_kv_evict", ("record", 2)]
+    cache._moves[0][1].done = True
+    assert append(one) == [("wait", 1, 2), "paged_kv_append"]
+    assert len(cache._moves) == 1  # the finished one is forgotten
+    cache._moves[0][1].done = True
+    append(one)
+    assert append(one) == ["paged_kv_append"] and not cache._moves

@@ -111,3 +111,31 @@ def test_scores_of_a_bad_table_stay(pkv, cache, group, dim):
             assert torch.all((scores[rest] - right[rest]).abs() < 1e-4)
             pkv.paged_attention_decode_scored(q, k, v, tables, n, 0.1, scores, partition_size=part, **one)
             assert torch.all((scores[b] - right[b]).abs() < 1e-4)
+
+
+def test_an_eviction_on_a_stream_that_is_behind(pkv):
+    """Appends on the current stream, into blocks that an eviction on a busy stream has freed, come after its move."""
+    from paged_kv_cache_102_gb300.cache import PagedKVCache
+    hkv, dim, n = 2, 64, 64
+    g = torch.Generator().manual_seed(2)
+    k, v, q = (torch.randn(n, h, dim, generator=g).to(F16).cuda() for h in (hkv, hkv, 4))
+    scores = torch.rand(1, hkv, 64, generator=g).cuda()
+    outs = []
+    for busy in (False, True):
+        cache = PagedKVCache(6, hkv, 16, dim, dtype=F16)
+        cache.add_sequence(1, 0)
+        for i in range(n):
+            cache.append([1], k[i:i + 1], v[i:i + 1])
+        side = torch.cuda.Stream()
+        side.wait_stream(torch.cuda.current_stream())
+        if busy:
+            with torch.cuda.stream(side):
+                torch.cuda._sleep(100_000_000)
+        cache.evict([1], [2], scores, 32, 4, stream=side)
+        cache.add_sequence(3, 0)
+        for i in range(n):  # every other block
+            cache.append([3], v[i:i + 1], k[i:i + 1])
+        assert cache.blocks.num_free == 0
+        torch.cuda.current_stream().wait_stream(side)
+        outs.append(cache.decode([2, 3], q[:2], 0.125))
+    assert torch.equal(outs[0], outs[1])
