@@ -259,6 +259,10 @@ int paged_block_swap(void* k_cache, void* v_cache, const int32_t* block_ids, int
 
 }  // extern "C"
 
+static size_t pool_bytes(int num_blocks, int num_kv_heads, int block_size, int head_dim, int cache_dtype) {
+    return static_cast<size_t>(num_blocks) * num_kv_heads * block_size * head_dim * (cache_dtype == PKV_E4M3 ? 1 : 2);
+}
+
 // What the calls with a window or with accumulated weights add to a decode.
 struct DecodeExt {
     int window = 0;  // 0: none
@@ -394,9 +398,11 @@ static int decode_impl(const char* fn, const void* q, const void* k_cache, const
     if (scored) {  // written, the scores read and written by different blocks
         const auto at = reinterpret_cast<uintptr_t>(ext->scores);
         const size_t B = num_seqs, rows = 2 * B * num_q_heads * head_dim;
+        const size_t pool = pool_bytes(num_blocks, num_kv_heads, block_size, head_dim, cache_dtype);
         const uintptr_t end = at + sizeof(float) * B * num_kv_heads * ext->score_tokens;
         const struct { const void* at; size_t bytes; } others[] = {
-            {q, rows}, {out, rows}, {context_lens, 4 * B}, {block_tables, 4 * B * max_blocks_per_seq}, {workspace, need}};
+            {q, rows}, {out, rows}, {context_lens, 4 * B}, {block_tables, 4 * B * max_blocks_per_seq}, {workspace, need},
+            {k_cache, pool}, {v_cache, pool}, {k_scale, k_scale ? 4u : 0u}, {v_scale, v_scale ? 4u : 0u}};
         for (const auto& o : others) {
             const auto x = reinterpret_cast<uintptr_t>(o.at);
             if (x < end && at < x + o.bytes) return fail(PKV_ERR_INVALID, F + ": " + "scores must be a buffer of its own");
@@ -682,17 +688,19 @@ int paged_kv_evict(void* k_cache, void* v_cache, int num_blocks, int num_kv_head
         !aligned(context_lens, 4) || !aligned(dst_tables, 4) || !aligned(scores_out, 4) || !aligned(context_lens_out, 4) ||
         !aligned(kept, 4))
         return fail(PKV_ERR_INVALID, F + "caches must be 16-byte aligned (others 4)");
-    // what is written (first) and read: buffers of their own
+    // what is written (first; the pools too) and read: buffers of their own
     const size_t B = num_seqs, BH = B * num_kv_heads;
+    const size_t pool = pool_bytes(num_blocks, num_kv_heads, block_size, head_dim, cache_dtype);
     const struct { const void* at; size_t bytes; } buffers[] = {
         {scores_out, 4 * BH * score_tokens_out}, {context_lens_out, 4 * B}, {kept, 4 * BH * budget},
-        {scores, 4 * BH * score_tokens}, {context_lens, 4 * B}, {block_tables, 4 * B * max_blocks_per_seq},
+        {k_cache, pool}, {v_cache, pool}, {scores, 4 * BH * score_tokens}, {context_lens, 4 * B}, {block_tables, 4 * B * max_blocks_per_seq},
         {dst_tables, 4 * B * max_dst_blocks}};
-    for (int i = 0; i < 3; ++i)
-        for (int j = i + 1; j < 7; ++j) {
+    for (int i = 0; i < 5; ++i)
+        for (int j = i + 1; j < 9; ++j) {
+            if (i == 3 && j == 4) continue;  // K and V: the caller's pools
             const auto a = reinterpret_cast<uintptr_t>(buffers[i].at), b = reinterpret_cast<uintptr_t>(buffers[j].at);
             if (a < b + buffers[j].bytes && b < a + buffers[i].bytes)
-                return fail(PKV_ERR_INVALID, F + "scores_out, context_lens_out and kept must be buffers of their own");
+                return fail(PKV_ERR_INVALID, F + "scores_out, context_lens_out, kept and the caches must be buffers of their own");
         }
     int* err = device_error_word();
     if (!err) return fail(PKV_ERR_CUDA, F + "cannot resolve the device error word");

@@ -117,3 +117,32 @@ def test_blocks_of_an_eviction_are_written_behind_its_move(host_cache, monkeypat
     cache._moves[0][1].done = True
     append(one)
     assert append(one) == ["paged_kv_append"] and not cache._moves
+
+
+def test_buffers_over_the_pools_are_refused(pkv_lib):
+    """Scores inside a pool or a scale, and what an eviction reads or writes inside a pool: refused on the host."""
+    lib = pkv_lib._native.lib()
+    M = 1 << 24  # buffers of their own; the pools are 512 KB
+    at = dict(q=1, k=2, v=3, tables=4, lens=5, scores=6, out=7, k1=8, v1=9, ws=10)
+
+    def scored(**kw):
+        a = {n: i * M for n, i in at.items()} | kw
+        return lib.paged_attention_decode_scored(
+            a["q"], a["k"], a["v"], a["tables"], 4, a["lens"], 2, 8, 8, 16, 128, 16, 0.1, a["scores"], 64, a["out"], 1, 2,
+            a["k1"], a["v1"], -1, a["ws"], 1 << 22, None)
+
+    for name, inside in (("k", 2048), ("v", 16 * 8 * 16 * 128 - 4), ("k1", 0), ("v1", 0)):
+        assert scored(scores=at[name] * M + inside) == 1
+        assert "buffer of its own" in lib.pkv_last_error().decode(), name
+
+    where = dict(k=1, v=2, scores=3, tables=4, lens=5, dst=6, so=7, lo=8, kept=9)
+
+    def evict(**kw):
+        a = {n: i * M for n, i in where.items()} | kw
+        return lib.paged_kv_evict(a["k"], a["v"], 16, 2, 16, 64, 1, a["scores"], 64, a["tables"], 4, a["lens"], 2, a["dst"], 2,
+                                  32, 4, 0, a["so"], 64, a["lo"], a["kept"], None)
+
+    for name in ("scores", "tables", "lens", "dst", "so", "lo", "kept"):
+        for pool in (1, 2):
+            assert evict(**{name: pool * M + 16 * 2 * 16 * 64 * 2 - 4}) == 1
+            assert "buffers of their own" in lib.pkv_last_error().decode(), (name, pool)
