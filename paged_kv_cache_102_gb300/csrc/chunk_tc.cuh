@@ -1062,7 +1062,8 @@ __global__ void __launch_bounds__(chunk_threads(CACHE), 1)
             const int lo = p.window ? max(0, pos - p.window + 1) : 0;
             for (int i = it.i0; i < it.i1; ++i) {
                 const int start = chunk_tile_start(it, i);
-                for (int j = start; j < start + kChunkTile && j <= pos; ++j) {
+                for (int y = 0; y < kChunkTile && y <= pos - start; ++y) {
+                    const int j = start + y;
                     if (j < lo && j >= p.sinks) continue;
                     const int blk = table[j / p.block_size];
                     if (blk < 0 || blk >= p.num_blocks) continue;

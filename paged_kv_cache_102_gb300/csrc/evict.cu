@@ -101,21 +101,23 @@ __device__ __forceinline__ int evict_select(const EvictParams& p, int h, int b, 
         L = m = 0;
     }
     if (h == 0 && tid == 0) p.lens_out[b] = m;
-    for (int i = m + tid; i < p.budget; i += kSelectThreads) kept[i] = -1;
+    // (unsigned: a step of the block's threads may pass 2^31 - 1)
+    const unsigned budget = p.budget, len = L;
+    for (unsigned i = m + tid; i < budget; i += kSelectThreads) kept[i] = -1;
     for (int64_t i = m + tid; i < p.score_tokens_out; i += kSelectThreads) out[i] = 0.f;
     if (L <= p.budget) {
-        for (int i = tid; i < L; i += kSelectThreads) {
+        for (unsigned i = tid; i < len; i += kSelectThreads) {
             kept[i] = i;
             out[i] = scores[i];
         }
         return m;
     }
     // the others compete: [sinks, L - recent)
-    const int first = p.sinks, last = L - p.recent;
+    const unsigned first = p.sinks, last = L - p.recent;
     const bool cached = L <= kKeyTokens;
-    auto key_at = [&](int i) { return cached ? keys[i] : score_key(scores[i]); };
+    auto key_at = [&](unsigned i) { return cached ? keys[i] : score_key(scores[i]); };
     if (cached)
-        for (int i = tid; i < L; i += kSelectThreads) keys[i] = score_key(scores[i]);
+        for (unsigned i = tid; i < len; i += kSelectThreads) keys[i] = score_key(scores[i]);
     uint32_t rest = p.budget - p.sinks - p.recent;  // of them this many stay
     uint32_t found = 0, mask = 0;
     if (rest == 0) {
@@ -125,7 +127,7 @@ __device__ __forceinline__ int evict_select(const EvictParams& p, int h, int b, 
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bins = pass == 2 ? 1024 : kBins;
             for (int i = tid; i < kBins; i += kSelectThreads) hist[i] = 0;
             __syncthreads();
-            for (int i = first + tid; i < last; i += kSelectThreads) {
+            for (unsigned i = first + tid; i < last; i += kSelectThreads) {
                 const uint32_t k = key_at(i);
                 if ((k & mask) == found) atomicAdd(&hist[(k >> shift) & (bins - 1)], 1u);
             }
@@ -149,13 +151,13 @@ __device__ __forceinline__ int evict_select(const EvictParams& p, int h, int b, 
     __syncthreads();
     // keys above `found` stay, and the first `rest` equal to it
     uint32_t above = 0, equal = 0;
-    for (int base = 0, turn = 0; base < L; base += 4 * kSelectThreads, ++turn) {
+    for (unsigned base = 0, turn = 0; base < len; base += 4 * kSelectThreads, ++turn) {
         uint32_t flags = 0;  // 2 bits a token: 1 above, 2 equal
-        const int i0 = base + 4 * tid;
+        const unsigned i0 = base + 4 * tid;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            const int i = i0 + j;
-            if (i >= L) continue;
+            const unsigned i = i0 + j;
+            if (i >= len) continue;
             const bool must = i < first || i >= last;
             const uint32_t k = must ? 0 : key_at(i);
             if (must || k > found) flags |= 1u << (2 * j);
@@ -234,7 +236,7 @@ __global__ void __launch_bounds__(kAddThreads) scored_finish_kernel(const AddWei
         if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
         return;
     }
-    const int parts = (L + p.partition_size - 1) / p.partition_size;
+    const int parts = (L - 1) / p.partition_size + 1;
     const int64_t row = static_cast<int64_t>(seq) * p.num_kv_heads + kvh;
     float before[kAddEach], logit[kAddEach][8];
 #pragma unroll
@@ -292,7 +294,7 @@ __global__ void __launch_bounds__(kAddThreads) scored_finish_kernel(const AddWei
         p.scores[row * p.score_tokens + t] = before[y] + sum;
     }
     if (parts == 1) return;
-    const int blocks = (L + kAddTokens - 1) / kAddTokens, each = (p.group * D + blocks - 1) / blocks;
+    const int blocks = (L - 1) / kAddTokens + 1, each = (p.group * D + blocks - 1) / blocks;
     const int end = min(p.group * D, static_cast<int>(blockIdx.x + 1) * each);
     for (int e = blockIdx.x * each + threadIdx.x; e < end; e += kAddThreads) {
         const int g = e / D, d = e % D;
@@ -351,7 +353,7 @@ cudaError_t launch_evict(const EvictParams& p, cudaStream_t stream) {
 }
 
 cudaError_t launch_scored_finish(const AddWeightsParams& p, int act, int head_dim, cudaStream_t stream) {
-    const dim3 grid((p.max_context + kAddTokens - 1) / kAddTokens, p.num_kv_heads, p.num_seqs);
+    const dim3 grid((p.max_context - 1) / kAddTokens + 1, p.num_kv_heads, p.num_seqs);
     auto kernel = head_dim == 64 ? (act == kBF16 ? scored_finish_kernel<kBF16, 64> : scored_finish_kernel<kF16, 64>)
                                  : (act == kBF16 ? scored_finish_kernel<kBF16, 128> : scored_finish_kernel<kF16, 128>);
     return launch_after(kernel, p, grid, kAddThreads, stream);

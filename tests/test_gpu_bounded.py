@@ -139,3 +139,20 @@ def test_an_eviction_on_a_stream_that_is_behind(pkv):
         torch.cuda.current_stream().wait_stream(side)
         outs.append(cache.decode([2, 3], q[:2], 0.125))
     assert torch.equal(outs[0], outs[1])
+
+
+def test_eviction_without_a_limit(pkv):
+    """The largest budget there is: everything stays, and the list of it is -1 behind that to its end."""
+    n, most = 40, 2 ** 31 - 1
+    paged = ref.Paged([n], 1, 16, 64, F16, seed=4, extra_blocks=4)
+    (k, v, tables, lens), _ = paged.cuda()
+    scores, dst = torch.rand(1, 1, 48).cuda(), paged.free[:3].view(1, 3).to(torch.int32).cuda()
+    kept = torch.zeros(1, 1, most, dtype=torch.int32, device="cuda")
+    got = pkv.paged_kv_evict(k, v, scores, tables, lens, dst, most, 8, kept=kept)
+    assert got.context_lens.tolist() == [n] and torch.equal(got.scores[0, 0, :n], scores[0, 0, :n])
+    assert kept[0, 0, :n].tolist() == list(range(n))
+    rest = kept.view(-1)[n:]
+    assert all(bool(torch.all(part == -1)) for part in rest.split(1 << 28))
+    for j in range(n):
+        a, b = (int(t[0, j // 16]) for t in (tables, dst))
+        assert torch.equal(k[a, 0, j % 16], k[b, 0, j % 16]) and torch.equal(v[a, 0, j % 16], v[b, 0, j % 16])
