@@ -241,7 +241,7 @@ struct EvictParams {
     int sinks;
 };
 
-// Attention of each sequence's new tokens over the cache (chunk.cu).
+// Attention of each sequence's new tokens over the cache (chunk_tc.cuh, chunk_tc.cu).
 struct ChunkParams {
     const void* q;
     int64_t q_stride;  // elements from one token's row to the next
