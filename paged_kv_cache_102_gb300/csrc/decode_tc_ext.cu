@@ -2,8 +2,8 @@
 // instantiations and their launch (E4M3 caches: decode_tc_ext_e4m3b.cu).  One ring depth each, two CTAs per SM: the API calls
 // with at most decode_tc_ext_max_rows sequences, whose tables leave room for it.
 // Measured: a window of 1024 and 4 first tokens, 128 sequences of up to 8192, 64 / 8
-// heads of 128, bfloat16: 80 us with the merge (8), its K and V 58 at the copy's rate;
-// block scales, 64 sequences of 40 heads, each its own: 61 us of 50.  Ramp and tail of
+// heads of 128, bfloat16: 82 us with the merge (8), its K and V 58 at the copy's rate;
+// block scales, 64 sequences of 40 heads, each its own: 62 us of 50.  Ramp and tail of
 // one launch, as without a window.
 #include "decode_tc_host.cuh"
 

@@ -15,8 +15,8 @@
 // packed scan.
 // A small budget's rows move in the same kernel, by the block that chose them.
 // Measured: 4 sequences of 270 tokens, 8 heads of 64, to 256: 8.0 us, a launch and a
-// dozen dependent passes over shared memory (a call 11.8, with two launches 15.8); 16 of 4096 to
-// 8192 tokens, 8 heads of 128, to 2048: selection 13 us, bound by its passes too (a
+// dozen dependent passes over shared memory (a call 12.5, 11 to 13 with the host; two launches
+// took 4 more); 16 of 4096 to 8192 tokens, 8 heads of 128, to 2048: selection 13 us, bound by its passes too (a
 // block an SM, 128 blocks), the move 43, 268 MB at 6.2 TB/s.
 // evict_move_kernel: 16 bytes a thread, kept rows of K and V to their new
 // blocks; source and destination blocks differ, so that rows are independent.
