@@ -829,6 +829,8 @@ int pkv_bm_num_seq_blocks(const pkv_block_manager* bm, int64_t seq_id); /* -1 if
  * appended since.  PagedKVCache sets it; tables and lengths do not change. */
 int pkv_bm_set_dropped(pkv_block_manager* bm, int64_t seq_id, int num_dropped);
 int pkv_bm_num_dropped(const pkv_block_manager* bm, int64_t seq_id);
+/* Positions of the newest tokens of n sequences: length + dropped - 1 (host int32 [n]). */
+int pkv_bm_get_positions(const pkv_block_manager* bm, const int64_t* seq_ids, int n, int32_t* positions_out);
 /* Copy the free list, in pop order, into out (capacity cap); returns its length. */
 int pkv_bm_free_list(const pkv_block_manager* bm, int32_t* out, int cap);
 

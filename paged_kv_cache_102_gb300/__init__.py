@@ -1151,6 +1151,14 @@ class BlockManager:
         """Tokens before the sequence's that are no longer held: its next token's position is context_len + num_dropped."""
         return int(_native.lib().pkv_bm_num_dropped(self._h, int(seq_id)))
 
+    def positions(self, seq_ids) -> np.ndarray:
+        """Positions of the sequences' newest tokens, int32 [n]: context_len + num_dropped - 1."""
+        ids = np.ascontiguousarray(seq_ids, dtype=np.int64)
+        out = np.empty(len(ids), np.int32)
+        self._check("pkv_bm_get_positions", _native.lib().pkv_bm_get_positions(
+            self._h, ids.ctypes.data_as(ctypes.c_void_p), len(ids), out.ctypes.data_as(ctypes.c_void_p)))
+        return out
+
     def free_list(self) -> np.ndarray:
         n = int(_native.lib().pkv_bm_free_list(self._h, None, 0))
         out = np.empty(n, np.int32)

@@ -86,6 +86,7 @@ SIGNATURES = {
     "pkv_bm_num_seq_blocks": (I32, [P, I64]),
     "pkv_bm_set_dropped": (I32, [P, I64, I32]),
     "pkv_bm_num_dropped": (I32, [P, I64]),
+    "pkv_bm_get_positions": (I32, [P, P, I32, P]),
     "pkv_bm_free_list": (I32, [P, P, I32]),
 }
 

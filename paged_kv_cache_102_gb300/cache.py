@@ -108,8 +108,7 @@ class PagedKVCache:
         """append with rotary positions: rotate q [n, Hq, D] and k at each sequence's newest position (evicted tokens
         counted) and write k, v; returns the rotated queries."""
         slots, _ = self._reserve(seq_ids, stream)
-        positions = np.asarray([self.blocks.context_len(s) + self.blocks.num_dropped(s) - 1 for s in np.asarray(seq_ids)],
-                               np.int32)
+        positions = self.blocks.positions(seq_ids)
         return paged_rope_append(q, k, v, self._upload(positions, stream), self._upload(slots, stream), inv_freq,
                                  self.k_cache, self.v_cache, interleaved=interleaved,
                                  attention_factor=attention_factor, q_out=q_out, k_scale=self.k_scale,

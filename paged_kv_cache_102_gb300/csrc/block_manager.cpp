@@ -518,6 +518,17 @@ int pkv_bm_num_dropped(const pkv_block_manager* bm, int64_t seq_id) {
     return it == bm->seqs.end() ? -1 : static_cast<int>(it->second.dropped);
 }
 
+int pkv_bm_get_positions(const pkv_block_manager* bm, const int64_t* seq_ids, int n, int32_t* positions_out) {
+    if (!bm || n < 0 || (n > 0 && (!seq_ids || !positions_out)))
+        return pkv::fail(PKV_ERR_INVALID, "pkv_bm_get_positions: bad arguments");
+    for (int i = 0; i < n; ++i) {
+        auto it = bm->seqs.find(seq_ids[i]);
+        if (it == bm->seqs.end()) return pkv::fail(PKV_ERR_NOT_FOUND, "pkv_bm_get_positions: unknown id");
+        positions_out[i] = static_cast<int32_t>(it->second.len + it->second.dropped - 1);
+    }
+    return PKV_OK;
+}
+
 int pkv_bm_num_seq_blocks(const pkv_block_manager* bm, int64_t seq_id) {
     if (!bm) return -1;
     auto it = bm->seqs.find(seq_id);

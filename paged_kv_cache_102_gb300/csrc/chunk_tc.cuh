@@ -54,16 +54,17 @@
 //                  multiplied by its block's K scale, and a weight, for the product
 //                  alone, by vs 2^(m - R), R the running maximum of a row's logits
 //                  plus log2 |vs|: O is a sum in units of 2^R whose largest term
-//                  is about 1, however far apart the scales are.
+//                  is about 1 (binary16: 2^7), however far apart the scales are.
 // Measured, head_dim 128: four prompts of up to 4096 tokens, 64 / 8 heads, bfloat16, 499 us, 1.02 PFLOP/s (52 % of a large
 // library product's); 509 new tokens behind 32K, 32 / 8 heads, binary16, 244 us, 1.11 PFLOP/s; head_dim 64 a third of that
 // (the same exponentials for half the products).  Of each pair of row tiles' 128-token step, 3300 cycles, the products
 // are 2048 at the tensor rate, and their operands and the copies take 256 KB of shared memory's 128 bytes a cycle, as long;
 // with the exponentials, maxima and sums left out it is 10 % shorter, and no pipe is busy for half of it.  What fills the
 // other 1250 cycles was not traced: likely a row tile's chain of scores, weights, O and the next scores, which have one
-// buffer.  Products add in float32, so that weights below 2^-24 of an O's size are lost to it.  Single tokens over 16-bit caches are bound by
-// HBM (1.5 us a tile an SM), over E4M3 ones (1.7 us; block scales 2.0) by shared memory, which the products' operands,
-// the conversion and the copies of codes share (224 KB a tile).  A block's start and end are some 6 tiles' time.
+// buffer.  Products add in float32, so that weights below 2^-24 of an O's size are lost to it.
+// Single tokens over 16-bit caches are bound by HBM (1.5 us a tile an SM), over E4M3 ones (1.7 us; block scales 2.0) by
+// shared memory, which the products' operands, the conversion and the copies of codes share (224 KB a tile).  A block's
+// start and end are some 6 tiles' time.
 // Every barrier wait is bounded (kWaitLimitNs); on a timeout the block stops,
 // drains its copies and products, frees tensor memory and reports kErrTimeout.
 #pragma once

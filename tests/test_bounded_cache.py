@@ -23,6 +23,9 @@ def test_manager_counts_dropped_tokens(pkv_lib):
     bm.set_dropped(1, 5)
     bm.fork(1, 2)
     assert bm.num_dropped(2) == 5 and bm.context_len(2) == 20
+    assert bm.positions([2, 1]).tolist() == [24, 24] and bm.positions([]).tolist() == []
+    with pytest.raises(pkv_lib.PagedKVError):
+        bm.positions([1, 9])
     bm.append_slots([1])
     assert bm.num_dropped(1) == 5 and bm.context_len(1) == 21
     bm.swap_out(1)
