@@ -55,7 +55,7 @@ class PagedKVCache:
             v_scales = v_scales if v_scales is not None else zeros()
         self.k_scales, self.v_scales = k_scales, v_scales
         self.blocks = BlockManager(num_blocks, block_size, free_list=free_list)
-        self._moves = []  # (stream, event) of evictions that may still read blocks they freed
+        self._moves = []  # events of evictions that may still read blocks they freed
 
     # -- host-side bookkeeping -------------------------------------------------
     def add_sequence(self, seq_id: int, num_tokens: int) -> None:
@@ -83,14 +83,10 @@ class PagedKVCache:
         return torch.cuda.current_stream(self.device) if stream is None else _torch_stream(stream, self.device)
 
     def _await_moves(self, stream) -> None:
-        """The step on the stream may write blocks that evictions on other streams freed: behind their moves."""
-        if not self._moves:
-            return
-        s = self._step_stream(stream)
-        for other, event in self._moves:
-            if other != s.cuda_stream:
-                s.wait_event(event)
-        self._moves = [m for m in self._moves if not m[1].query()]
+        """The step on the stream may write blocks that evictions, maybe on other streams, freed: behind their moves."""
+        self._moves = [event for event in self._moves if not event.query()]
+        for event in self._moves:
+            self._step_stream(stream).wait_event(event)
 
     # -- device steps ------------------------------------------------------------
     def append(self, seq_ids, k: torch.Tensor, v: torch.Tensor, stream=None):
@@ -198,8 +194,7 @@ class PagedKVCache:
                 self.blocks.free_sequence(s)
             raise
         if self.device.type == "cuda":
-            s = self._step_stream(stream)
-            self._moves.append((s.cuda_stream, s.record_event()))
+            self._moves.append(self._step_stream(stream).record_event())
         for s in seq_ids:
             self.blocks.free_sequence(s)
         return got

@@ -110,15 +110,13 @@ def test_blocks_of_an_eviction_are_written_behind_its_move(host_cache, monkeypat
 
     assert append(two) == ["paged_kv_append"]
     assert evict(1, 3, 40, one) == ["paged_kv_evict", ("record", 1)]
-    assert append(one) == ["paged_kv_append"]
     assert append(two) == [("wait", 2, 1), "paged_kv_append"]
+    assert append(one) == [("wait", 1, 1), "paged_kv_append"]  # (in order already)
     assert steps(lambda: cache.rope_append([2], None, None, None, None, stream=two)) == [("wait", 2, 1), "paged_rope_append"]
     assert evict(3, 4, 20, two) == [("wait", 2, 1), "paged_kv_evict", ("record", 2)]
-    cache._moves[0][1].done = True
+    cache._moves[0].done = True  # the finished one is forgotten
     assert append(one) == [("wait", 1, 2), "paged_kv_append"]
-    assert len(cache._moves) == 1  # the finished one is forgotten
-    cache._moves[0][1].done = True
-    append(one)
+    cache._moves[0].done = True
     assert append(one) == ["paged_kv_append"] and not cache._moves
 
 
